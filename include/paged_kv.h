@@ -82,6 +82,8 @@ enum {
 
 enum { PKV_DTYPE_FP16 = 0, PKV_DTYPE_BF16 = 1 };
 
+enum { PKV_ELEM_INT4 = 0 }; /* paged_kv_copy_blocks' element size of a 4-bit pool */
+
 typedef struct pkv_dims {
   int32_t num_seqs;            /* batch size B (also num_tokens for the append) */
   int32_t num_q_heads;         /* Hq */
@@ -312,6 +314,69 @@ int paged_decode_step_fp8(const void* q, const void* k_new, const void* v_new, v
                           const pkv_dims* dims, void* stream);
 
 /* ------------------------------------------------------------------------
+ * 4-bit KV cache.  The quantisation section of youngju.dev "LLM サービング最適化
+ * 完全ガイド" and design.babushkai.com "GPU推論の内部構造", section "KVキャッシュの
+ * 台帳": fewer bits per value, fewer bytes per token.  The pages fix no format;
+ * here each row (one token of one KV head) has its own scale and minimum, so
+ * that nothing has to be calibrated: value = scale * code + minimum, code 0..15.
+ *
+ * Layout: k_cache, v_cache : uint8[num_blocks][num_kv_heads][16 * (D/2 + 4)]
+ *   One (block, KV head) tile: 16 * D/2 bytes of codes, then 16 pairs of float16
+ *   (scale, minimum), pair t for the token at offset t.  Low four bits first:
+ *   K codes: dims d, d + 1 (d even) of token t in byte t * D/2 + d/2;
+ *   V codes: with G = D/8, in byte (t/8) 4D + (d/G) 4G + (t/2 % 4) G +
+ *   (d%G)/4 * 4 + (t%2) 2 + (d%4)/2 (integer divisions).
+ *   q, out, k_new, v_new : T as above (pkv_dims.dtype is their type).
+ * Quantisation of a row x (append), every step in IEEE float32: x limited to
+ *   +-65504; minimum = float16(min x); scale = float16((max x - minimum) / 15);
+ *   code = round_half_even((x - minimum) * (1 / scale)) limited to 0..15 (0
+ *   where the scale is not above 0).  The codes of NaN inputs are outside the
+ *   contract.
+ * Attention: the plain attention of the dequantised cache.  The products run
+ *   as fp16 mma (codes are exact in fp16); a bf16 query is converted to fp16: an
+ *   entry beyond +-65504 sets the error word (PKV_ERR_OUT_OF_RANGE from
+ *   paged_kv_check_status).  A scale in the pool must be finite; slots past a
+ *   sequence's length may hold anything.  A block id outside the pool reads as
+ *   zeros and is flagged.
+ * Limits: head_dim 64 or 128; at most 2048 sequences per call; only the
+ *   automatic persistent path (workspace: paged_decode_workspace_bytes(dims, 0)
+ *   bytes, zero-filled once, as above).  Bad shapes and pointers return
+ *   PKV_ERR_INVALID_ARG / PKV_ERR_UNSUPPORTED.
+ * paged_kv_copy_blocks copies blocks of a 4-bit pool with cache_elem_bytes =
+ *   PKV_ELEM_INT4.
+ * ---------------------------------------------------------------------- */
+
+/* Slot-mapped quantising append of num_tokens tokens into a 4-bit pool
+ * (device).  Same slot rule and error behaviour as paged_kv_append; all value
+ * and cache pointers 16-byte aligned.  The other rows of the blocks that are
+ * written into keep their bytes.  Two tokens of one call must not share a
+ * slot. */
+int paged_kv_append_int4(const void* k_new, const void* v_new, const int32_t* slot_mapping,
+                         int32_t num_tokens, void* k_cache, void* v_cache, const pkv_dims* dims, void* stream);
+
+/* The reverse (device): the values of the rows at slot_mapping[0..num_tokens)
+ * as T, rounded once, into k_out / v_out T[num_tokens][num_kv_heads][head_dim]
+ * (for a prefix that another kernel attends to, or that moves to another
+ * pool).  A negative slot gives a zero row; one >= num_blocks * 16 too, and is
+ * flagged (PKV_ERR_OUT_OF_RANGE from paged_kv_check_status). */
+int paged_kv_read_int4(const int32_t* slot_mapping, int32_t num_tokens, const void* k_cache, const void* v_cache,
+                       void* k_out, void* v_out, const pkv_dims* dims, void* stream);
+
+/* Decode attention over a 4-bit pool (device); arguments as
+ * paged_decode_attention with the automatic path. */
+int paged_decode_attention_int4(const void* q, const void* k_cache, const void* v_cache,
+                                const int32_t* block_tables, const int32_t* context_lens, float scale,
+                                void* out, void* workspace, size_t workspace_bytes,
+                                const pkv_dims* dims, void* stream);
+
+/* One decode step over a 4-bit pool (device): quantise and append each
+ * sequence's token at position context_lens[b] - 1, then attend, in one fused
+ * launch; arguments as paged_decode_step with the automatic path. */
+int paged_decode_step_int4(const void* q, const void* k_new, const void* v_new, void* k_cache, void* v_cache,
+                           const int32_t* block_tables, const int32_t* context_lens, float scale, void* out,
+                           void* workspace, size_t workspace_bytes, const pkv_dims* dims, void* stream);
+
+/* ------------------------------------------------------------------------
  * Several new tokens per sequence (speculative verification, chunked decode):
  * youngju.dev "LLM サービング最適化完全ガイド", speculative decoding section (the
  * target model checks several draft tokens in one pass) and
@@ -382,8 +447,8 @@ int paged_kv_slot_mapping_multi(const int32_t* block_tables, const int32_t* cont
  * block_pairs[i] = {src, dst} (int32[num_pairs][2], device), physical block
  * dst of k_cache and of v_cache becomes a copy of block src.  Destinations
  * must be distinct and not among the sources (the allocator's are fresh
- * blocks).  cache_elem_bytes: 2 for fp16/bf16 pools, 1 for E4M3 pools
- * (dims.dtype is not used).  Enqueue it before the append that writes into the
+ * blocks).  cache_elem_bytes: 2 for fp16/bf16 pools, 1 for E4M3 pools,
+ * PKV_ELEM_INT4 for 4-bit pools (dims.dtype is not used).  Enqueue it before the append that writes into the
  * copies.  A pair outside [0, num_blocks) is skipped and flagged
  * (PKV_ERR_OUT_OF_RANGE from paged_kv_check_status).
  * ---------------------------------------------------------------------- */
@@ -572,6 +637,12 @@ int decode_engine_admit(pkv_decode_engine* e, int32_t prompt_tokens, int32_t gen
  * with paged_kv_append_fp8, steps run paged_decode_step_fp8, and
  * copy-on-write copies 1-byte elements.  NULL for both: fp16/bf16 pools. */
 int decode_engine_set_kv_scales(pkv_decode_engine* e, const float* k_scale, const float* v_scale);
+
+/* 4-bit pools: with enabled != 0 the engine's pools are 4-bit: admission
+ * appends with paged_kv_append_int4, steps run paged_decode_step_int4, and
+ * copy-on-write copies 4-bit blocks.  PKV_ERR_INVALID_ARG together with E4M3
+ * scales.  Set it before the first admission. */
+int decode_engine_set_int4(pkv_decode_engine* e, int32_t enabled);
 
 /* Parallel sampling: a new sequence in a free batch slot that shares every
  * block of the sequence in src_slot (its whole context so far; reference

@@ -459,11 +459,145 @@ def paged_decode_step_fp8(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Ten
     return out
 
 
+# ---------------------------------------------------------------- 4-bit cache
+
+def int4_row_bytes(head_dim: int) -> int:
+    """Bytes of one token's K (or V) row of one KV head in a 4-bit pool: the
+    codes and the float16 (scale, minimum) pair."""
+    return head_dim // 2 + 4
+
+
+def _int4_head_dim(k_cache: torch.Tensor, v_cache: torch.Tensor) -> int:
+    for n, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        _need_cuda(n, t, torch.uint8)
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape:
+        raise ValueError("4-bit caches must both be uint8 [num_blocks][num_kv_heads][16][head_dim/2 + 4]")
+    return 2 * (k_cache.shape[3] - 4)
+
+
+def make_dims_int4(q_or_new: torch.Tensor, k_cache: torch.Tensor, block_tables: Optional[torch.Tensor] = None,
+                   num_q_heads: Optional[int] = None) -> PkvDims:
+    """Dims of a call over a 4-bit pool: dtype is that of q / out / k_new / v_new."""
+    nb, hkv, bs, row = k_cache.shape
+    if q_or_new.dtype not in _DTYPE_CODE:
+        raise ValueError("q / k_new / v_new must be float16 or bfloat16")
+    return PkvDims(num_seqs=q_or_new.shape[0],
+                   num_q_heads=num_q_heads if num_q_heads is not None else q_or_new.shape[1],
+                   num_kv_heads=hkv, head_dim=2 * (row - 4), block_size=bs, num_blocks=nb,
+                   max_blocks_per_seq=block_tables.shape[1] if block_tables is not None else 0,
+                   dtype=_DTYPE_CODE[q_or_new.dtype])
+
+
+def make_workspace_int4(q: torch.Tensor, k_cache: torch.Tensor, block_tables: torch.Tensor) -> torch.Tensor:
+    """A zero-filled workspace for the 4-bit calls on these shapes."""
+    dims = make_dims_int4(q, k_cache, block_tables)
+    need = int(lib().paged_decode_workspace_bytes(ctypes.byref(dims), 0))
+    return torch.zeros(need, dtype=torch.uint8, device=q.device)
+
+
+def paged_kv_append_int4(k_new: torch.Tensor, v_new: torch.Tensor, slot_mapping: torch.Tensor,
+                         k_cache: torch.Tensor, v_cache: torch.Tensor, stream=None) -> None:
+    """paged_kv_append into 4-bit caches (uint8 [num_blocks][Hkv][16][D/2 + 4]):
+    each row is quantised with a scale and a minimum of its own."""
+    d = _int4_head_dim(k_cache, v_cache)
+    _need_cuda("k_new", k_new)
+    _need_cuda("v_new", v_new, k_new.dtype)
+    _need_cuda("slot_mapping", slot_mapping, torch.int32)
+    if k_new.dim() != 3 or k_new.shape != v_new.shape or k_new.shape[1:] != (k_cache.shape[1], d):
+        raise ValueError("k_new / v_new must be [num_tokens][num_kv_heads][head_dim] matching the cache")
+    if slot_mapping.shape != (k_new.shape[0],):
+        raise ValueError("slot_mapping must be [num_tokens]")
+    dims = make_dims_int4(k_new, k_cache, num_q_heads=k_cache.shape[1])
+    _check(lib().paged_kv_append_int4(_ptr(k_new), _ptr(v_new), _ptr(slot_mapping), k_new.shape[0], _ptr(k_cache),
+                                      _ptr(v_cache), ctypes.byref(dims), _stream(stream)),
+           "paged_kv_append_int4")
+
+
+def paged_kv_read_int4(slot_mapping: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                       dtype: Optional[torch.dtype] = None, k_out: Optional[torch.Tensor] = None,
+                       v_out: Optional[torch.Tensor] = None, stream=None):
+    """The rows at these slots as values: (k, v), each [num_tokens][Hkv][D] of
+    ``dtype`` (float16 or bfloat16; or that of k_out / v_out).  A negative slot
+    gives a zero row."""
+    d = _int4_head_dim(k_cache, v_cache)
+    _need_cuda("slot_mapping", slot_mapping, torch.int32)
+    if slot_mapping.dim() != 1:
+        raise ValueError("slot_mapping must be [num_tokens]")
+    shape = (slot_mapping.shape[0], k_cache.shape[1], d)
+    if k_out is None and v_out is None:
+        if dtype not in _DTYPE_CODE:
+            raise ValueError("dtype must be float16 or bfloat16")
+        k_out, v_out = (torch.empty(shape, dtype=dtype, device=k_cache.device) for _ in range(2))
+    elif k_out is None or v_out is None:
+        raise ValueError("give both k_out and v_out, or neither")
+    _need_cuda("k_out", k_out, dtype)
+    _need_cuda("v_out", v_out, k_out.dtype)
+    if k_out.shape != shape or v_out.shape != shape:
+        raise ValueError("k_out / v_out must be [num_tokens][num_kv_heads][head_dim] matching the cache")
+    dims = make_dims_int4(k_out, k_cache, num_q_heads=k_cache.shape[1])
+    _check(lib().paged_kv_read_int4(_ptr(slot_mapping), shape[0], _ptr(k_cache), _ptr(v_cache), _ptr(k_out),
+                                    _ptr(v_out), ctypes.byref(dims), _stream(stream)),
+           "paged_kv_read_int4")
+    return k_out, v_out
+
+
+def _int4_call_checks(q, k_cache, v_cache, block_tables, context_lens, out):
+    _need_cuda("q", q)
+    d = _int4_head_dim(k_cache, v_cache)
+    _need_cuda("block_tables", block_tables, torch.int32)
+    _need_cuda("context_lens", context_lens, torch.int32)
+    _need_cuda("out", out, q.dtype)
+    if out.shape != q.shape or q.dim() != 3 or q.shape[2] != d:
+        raise ValueError("q / out must be [num_seqs][num_q_heads][head_dim] matching the caches")
+    if block_tables.dim() != 2 or block_tables.shape[0] != q.shape[0] or context_lens.shape != (q.shape[0],):
+        raise ValueError("block_tables must be [num_seqs][max_blocks], context_lens [num_seqs]")
+
+
+def paged_decode_attention_int4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                                block_tables: torch.Tensor, context_lens: torch.Tensor, scale: float,
+                                out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                                stream=None) -> torch.Tensor:
+    """paged_decode_attention over 4-bit caches.  Returns out."""
+    if out is None:
+        out = torch.empty_like(q)
+    _int4_call_checks(q, k_cache, v_cache, block_tables, context_lens, out)
+    dims = make_dims_int4(q, k_cache, block_tables)
+    workspace, ws_bytes = _fp8_workspace(dims, q, workspace)
+    _check(lib().paged_decode_attention_int4(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
+                                             _ptr(context_lens), float(scale), _ptr(out), _ptr(workspace), ws_bytes,
+                                             ctypes.byref(dims), _stream(stream)),
+           "paged_decode_attention_int4")
+    return out
+
+
+def paged_decode_step_int4(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, k_cache: torch.Tensor,
+                           v_cache: torch.Tensor, block_tables: torch.Tensor, context_lens: torch.Tensor,
+                           scale: float, out: Optional[torch.Tensor] = None,
+                           workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """paged_decode_step over 4-bit caches: the new token is quantised and
+    appended, then attended, in one fused launch.  Returns out."""
+    if out is None:
+        out = torch.empty_like(q)
+    _int4_call_checks(q, k_cache, v_cache, block_tables, context_lens, out)
+    _need_cuda("k_new", k_new, q.dtype)
+    _need_cuda("v_new", v_new, q.dtype)
+    if k_new.shape != (q.shape[0], k_cache.shape[1], q.shape[2]) or v_new.shape != k_new.shape:
+        raise ValueError("k_new / v_new must be [num_seqs][num_kv_heads][head_dim]")
+    dims = make_dims_int4(q, k_cache, block_tables)
+    workspace, ws_bytes = _fp8_workspace(dims, q, workspace)
+    _check(lib().paged_decode_step_int4(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache),
+                                        _ptr(block_tables), _ptr(context_lens), float(scale), _ptr(out),
+                                        _ptr(workspace), ws_bytes, ctypes.byref(dims), _stream(stream)),
+           "paged_decode_step_int4")
+    return out
+
+
 def paged_kv_copy_blocks(k_cache: torch.Tensor, v_cache: torch.Tensor, block_pairs: torch.Tensor,
                          stream=None) -> None:
     """Copy-on-write: for each row (src, dst) of block_pairs (int32 [n][2] on
     the device), physical block dst of both caches becomes a copy of block src.
-    Caches: fp16/bf16 [NB][Hkv][16][D] or E4M3 codes (uint8 / float8_e4m3fn)."""
+    Caches: fp16/bf16 [NB][Hkv][16][D], E4M3 codes (uint8 / float8_e4m3fn) or
+    4-bit tiles (uint8 [NB][Hkv][16][D/2 + 4], D = 64 or 128)."""
     _need_cuda("k_cache", k_cache)
     _need_cuda("v_cache", v_cache, k_cache.dtype)
     _need_cuda("block_pairs", block_pairs, torch.int32)
@@ -472,10 +606,13 @@ def paged_kv_copy_blocks(k_cache: torch.Tensor, v_cache: torch.Tensor, block_pai
     if k_cache.shape != v_cache.shape or k_cache.dim() != 4:
         raise ValueError("caches must both be [num_blocks][num_kv_heads][16][head_dim]")
     nb, hkv, bs, d = k_cache.shape
+    elem = k_cache.element_size()
+    if k_cache.dtype == torch.uint8 and d in (int4_row_bytes(64), int4_row_bytes(128)):  # no E4M3 row is that wide
+        d, elem = 2 * (d - 4), 0
     dims = PkvDims(num_seqs=0, num_q_heads=hkv, num_kv_heads=hkv, head_dim=d, block_size=bs, num_blocks=nb,
                    max_blocks_per_seq=0, dtype=_DTYPE_CODE.get(k_cache.dtype, 0))
     _check(lib().paged_kv_copy_blocks(_ptr(k_cache), _ptr(v_cache), _ptr(block_pairs), block_pairs.shape[0],
-                                      ctypes.byref(dims), k_cache.element_size(), _stream(stream)),
+                                      ctypes.byref(dims), elem, _stream(stream)),
            "paged_kv_copy_blocks")
 
 

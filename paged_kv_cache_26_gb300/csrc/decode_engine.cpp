@@ -72,6 +72,7 @@ struct pkv_decode_engine {
   int adm_i = 0;
   const float* k_scale = nullptr;        // set: the pools hold E4M3 codes with these per-KV-head scales
   const float* v_scale = nullptr;
+  bool int4 = false;                     // the pools hold 4-bit tiles
   std::vector<int32_t> row;
   pkv_engine_stats stats = {};
 
@@ -157,10 +158,12 @@ int decode_engine_admit(pkv_decode_engine* e, int32_t prompt_tokens, int32_t gen
     if (e->adm_pending[i]) cudaEventSynchronize(e->adm_ev[i]);  // the append that last read this buffer is done
     int32_t* host = e->slots[i].h;
     for (int32_t p = 0; p < prompt_tokens; ++p) host[p] = e->row[p / kBlockSize] * kBlockSize + p % kBlockSize;
-    rc = e->k_scale ? paged_kv_append_fp8(prompt_k, prompt_v, e->slots[i].d, prompt_tokens, k_cache, v_cache,
-                                          e->k_scale, e->v_scale, dims, stream)
-                    : paged_kv_append(prompt_k, prompt_v, e->slots[i].d, prompt_tokens, k_cache, v_cache, dims,
-                                      stream);
+    rc = e->int4      ? paged_kv_append_int4(prompt_k, prompt_v, e->slots[i].d, prompt_tokens, k_cache, v_cache, dims,
+                                             stream)
+         : e->k_scale ? paged_kv_append_fp8(prompt_k, prompt_v, e->slots[i].d, prompt_tokens, k_cache, v_cache,
+                                            e->k_scale, e->v_scale, dims, stream)
+                      : paged_kv_append(prompt_k, prompt_v, e->slots[i].d, prompt_tokens, k_cache, v_cache, dims,
+                                        stream);
     if (rc != PKV_OK) {
       block_allocator_free_seq(e->alloc, sid);
       return rc;
@@ -214,13 +217,14 @@ int decode_engine_step(pkv_decode_engine* e, const void* q, const void* k_new, c
   e->last = i;
   e->step_i = (i + 1) % kStepRing;
   if (ncopy > 0) {
-    rc = paged_kv_copy_blocks(k_cache, v_cache, e->pairs(i, true), ncopy, dims, e->k_scale ? 1 : 2, stream);
+    rc = paged_kv_copy_blocks(k_cache, v_cache, e->pairs(i, true), ncopy, dims,
+                              e->int4 ? PKV_ELEM_INT4 : e->k_scale ? 1 : 2, stream);
     if (rc != PKV_OK) return rc;
   }
   // The tables and lengths were written by the host above and no kernel writes
   // them: the kernels may trust what they read before their grid wait.
-  rc = decode_step_host_written(q, k_new, v_new, k_cache, v_cache, e->k_scale, e->v_scale, e->tables(i, true),
-                                e->lens(i, true), scale, out, workspace, workspace_bytes, dims, stream);
+  rc = decode_step_host_written(q, k_new, v_new, k_cache, v_cache, e->k_scale, e->v_scale, e->int4,
+                                e->tables(i, true), e->lens(i, true), scale, out, workspace, workspace_bytes, dims, stream);
   // Recorded even after a failed launch, so that the entry is never reused
   // while an earlier kernel (the block copy) may still read it.
   const cudaError_t ce = cudaEventRecord(e->step_ev[i], static_cast<cudaStream_t>(stream));
@@ -265,8 +269,17 @@ int decode_engine_reset_stats(pkv_decode_engine* e) {
 int decode_engine_set_kv_scales(pkv_decode_engine* e, const float* k_scale, const float* v_scale) {
   if (!e || (k_scale == nullptr) != (v_scale == nullptr))
     return pkv_fail(PKV_ERR_INVALID_ARG, "decode_engine_set_kv_scales: give both scales or neither");
+  if (k_scale && e->int4)
+    return pkv_fail(PKV_ERR_INVALID_ARG, "decode_engine_set_kv_scales: the engine's pools are 4-bit");
   e->k_scale = k_scale;
   e->v_scale = v_scale;
+  return PKV_OK;
+}
+
+int decode_engine_set_int4(pkv_decode_engine* e, int32_t enabled) {
+  if (!e || (enabled && e->k_scale))
+    return pkv_fail(PKV_ERR_INVALID_ARG, "decode_engine_set_int4: NULL engine, or one with E4M3 scales set");
+  e->int4 = enabled != 0;
   return PKV_OK;
 }
 

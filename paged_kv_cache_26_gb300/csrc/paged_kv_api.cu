@@ -11,6 +11,7 @@
 #include <cstring>
 #include <mutex>
 #include <string>
+#include <type_traits>
 
 #include "paged_kv.h"
 #include "block_copy.cuh"
@@ -160,13 +161,16 @@ struct SplitPlan {
 
 // Largest batch of the persistent kernel: its prefix sums live in shared
 // memory beside the ring (2048 sequences for every pool format built).
-int max_persistent_seqs(const pkv_dims* d, bool f8) {
-  if (f8) return pkv::persistent_max_seqs<128, true>() / 256 * 256;
+int max_persistent_seqs(const pkv_dims* d, int format) {
+  if (format == pkv::kPoolE4M3) return pkv::persistent_max_seqs<128, pkv::kPoolE4M3>() / 256 * 256;
+  if (format == pkv::kPoolInt4)
+    return d->head_dim == 128 ? pkv::persistent_max_seqs<128, pkv::kPoolInt4>()
+                              : pkv::persistent_max_seqs<64, pkv::kPoolInt4>();
   return d->head_dim == 128 ? pkv::persistent_max_seqs<128>() : pkv::persistent_max_seqs<64>();
 }
 
-bool persistent_eligible(const pkv_dims* d, bool f8 = false) {
-  return d->num_seqs <= max_persistent_seqs(d, f8) &&
+bool persistent_eligible(const pkv_dims* d, int format = pkv::kPool16) {
+  return d->num_seqs <= max_persistent_seqs(d, format) &&
          static_cast<int64_t>(d->num_seqs) * d->num_kv_heads * d->max_blocks_per_seq < (int64_t(1) << 31);
 }
 
@@ -240,12 +244,12 @@ cudaError_t configure_smem(int bytes) {
 // Persistent decode + merge.  Both are programmatic dependent launches: each
 // may start while the kernel before it in the stream finishes, and waits
 // in-kernel (griddepcontrol.wait) before touching anything that kernel writes.
-template <typename T, int D, bool F8>
+template <typename T, int D, int F>
 int launch_persistent(const CUtensorMap& mk, const CUtensorMap& mv, const pkv::DecodeArgs& args,
                       const pkv_dims* d, int max_seqs, cudaStream_t stream, bool pdl = true) {
-  using PS = pkv::PersistentShape<D, F8>;
-  constexpr auto kern = pkv::decode_persistent_kernel<T, D, F8>;
-  cudaError_t e = configure_smem<kern>(static_cast<int>(pkv::persistent_smem_bytes<D, F8>(max_seqs)));
+  using PS = pkv::PersistentShape<D, F>;
+  constexpr auto kern = pkv::decode_persistent_kernel<T, D, F>;
+  cudaError_t e = configure_smem<kern>(static_cast<int>(pkv::persistent_smem_bytes<D, F>(max_seqs)));
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(decode_persistent_kernel)");
   const int64_t upper_blocks = static_cast<int64_t>(d->num_seqs) * d->num_kv_heads * d->max_blocks_per_seq;
   int64_t grid = (upper_blocks + PS::kWarps - 1) / PS::kWarps;
@@ -257,7 +261,7 @@ int launch_persistent(const CUtensorMap& mk, const CUtensorMap& mv, const pkv::D
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
   cfg.blockDim = dim3(PS::kWarps * 32);
-  cfg.dynamicSmemBytes = pkv::persistent_smem_bytes<D, F8>(d->num_seqs);
+  cfg.dynamicSmemBytes = pkv::persistent_smem_bytes<D, F>(d->num_seqs);
   cfg.stream = stream;
   cfg.attrs = attr;
   // !pdl: the kernel before this one wrote its inputs (block tables, lengths,
@@ -278,7 +282,7 @@ int launch_persistent(const CUtensorMap& mk, const CUtensorMap& mv, const pkv::D
   // fold up to 16 per round trip (fewer registers leave room for more merge
   // CTAs beside the decode grid, which pays when rows are many and short).
   const bool wide = !coop && nwarps >= 2 * units;
-  const int merge_smem = static_cast<int>((2 * static_cast<size_t>(max_persistent_seqs(d, false)) + 1) * 4);
+  const int merge_smem = static_cast<int>((2 * static_cast<size_t>(max_persistent_seqs(d, pkv::kPool16)) + 1) * 4);
   const int rows = d->num_seqs * d->num_q_heads;
   const int rows_per_cta = coop ? 1 : pkv::kMergeWarps;
   cfg.gridDim = dim3(static_cast<unsigned>((rows + rows_per_cta - 1) / rows_per_cta));
@@ -306,7 +310,7 @@ int launch_decode(const CUtensorMap& mk, const CUtensorMap& mv, const pkv::Decod
                   const pkv_dims* d, cudaStream_t stream, bool pdl) {
   using Shape = pkv::TileShape<D>;
   if (plan.persistent)
-    return launch_persistent<T, D, false>(mk, mv, args, d, max_persistent_seqs(d, false), stream, pdl);
+    return launch_persistent<T, D, pkv::kPool16>(mk, mv, args, d, max_persistent_seqs(d, pkv::kPool16), stream, pdl);
   constexpr int kSmem = kStages * Shape::kStageBytes + 1024;
   constexpr auto kern = pkv::decode_split_kernel<T, D, kConsumerWarps, kStages>;
   cudaError_t e = configure_smem<kern>(kSmem);
@@ -334,20 +338,24 @@ int append_at_end_impl(const void* k_new, const void* v_new, const int32_t* bloc
 // position context_lens[b] - 1 (k_new / v_new non-null): fused into the
 // persistent kernel when that path runs, else a separate append launch.
 //
-// f8: the pool holds E4M3 codes with per-KV-head scales k_scale / v_scale
-// (head_dim 128, persistent path only).
+// format: what the pool holds; kPoolE4M3 (with per-KV-head scales k_scale /
+// v_scale, head_dim 128) and kPoolInt4 run on the persistent path only.
 int decode_impl(const void* q, const void* k_new, const void* v_new, void* k_cache, void* v_cache,
                 const int32_t* block_tables, const int32_t* context_lens, float scale, void* out,
                 int32_t num_splits, void* workspace, size_t workspace_bytes, const pkv_dims* d,
-                cudaStream_t stream, bool f8 = false, const float* k_scale = nullptr,
+                cudaStream_t stream, int format = pkv::kPool16, const float* k_scale = nullptr,
                 const float* v_scale = nullptr, bool pdl = true, const int32_t* pre_lens = nullptr,
                 const int32_t* pre_tables = nullptr, bool recheck = true, bool publish = true) {
   int rc = check_dims(d, true);
   if (rc != PKV_OK) return rc;
+  if (format == pkv::kPoolInt4 && !persistent_eligible(d, format))
+    return pkv_fail(PKV_ERR_UNSUPPORTED, "4-bit cache: at most " + std::to_string(max_persistent_seqs(d, format)) +
+                                             " sequences per call");
+  const bool f8 = format == pkv::kPoolE4M3;
   if (f8) {
     if (d->head_dim != 128) return pkv_fail(PKV_ERR_UNSUPPORTED, "fp8 cache: head_dim must be 128");
-    if (!persistent_eligible(d, true))
-      return pkv_fail(PKV_ERR_UNSUPPORTED, "fp8 cache: at most " + std::to_string(max_persistent_seqs(d, true)) +
+    if (!persistent_eligible(d, format))
+      return pkv_fail(PKV_ERR_UNSUPPORTED, "fp8 cache: at most " + std::to_string(max_persistent_seqs(d, format)) +
                                                " sequences per call");
     if (!k_scale || !v_scale || !aligned(k_scale, 4) || !aligned(v_scale, 4))
       return pkv_fail(PKV_ERR_INVALID_ARG, "fp8 cache: k_scale / v_scale missing or misaligned");
@@ -378,9 +386,11 @@ int decode_impl(const void* q, const void* k_new, const void* v_new, void* k_cac
     rc = append_at_end_impl(k_new, v_new, block_tables, context_lens, k_cache, v_cache, d, stream);
     if (rc != PKV_OK) return rc;
   }
-  CUtensorMap mk, mv;
-  if ((rc = g_maps.get(k_cache, d, f8, &mk)) != PKV_OK) return rc;
-  if ((rc = g_maps.get(v_cache, d, f8, &mv)) != PKV_OK) return rc;
+  CUtensorMap mk = {}, mv = {};  // 4-bit tiles are loaded by untiled bulk copies
+  if (format != pkv::kPoolInt4) {
+    if ((rc = g_maps.get(k_cache, d, f8, &mk)) != PKV_OK) return rc;
+    if ((rc = g_maps.get(v_cache, d, f8, &mv)) != PKV_OK) return rc;
+  }
 
   pkv::DecodeArgs args;
   args.k_new = append && plan.persistent ? k_new : nullptr;
@@ -426,10 +436,16 @@ int decode_impl(const void* q, const void* k_new, const void* v_new, void* k_cac
   args.split_blocks = plan.split_blocks;
 
   const bool bf16 = d->dtype == PKV_DTYPE_BF16;
-  if (f8) {
-    const int mx = max_persistent_seqs(d, true);
-    return bf16 ? launch_persistent<__nv_bfloat16, 128, true>(mk, mv, args, d, mx, stream, pdl)
-                : launch_persistent<__half, 128, true>(mk, mv, args, d, mx, stream, pdl);
+  const int mx = max_persistent_seqs(d, format);
+  if (f8)
+    return bf16 ? launch_persistent<__nv_bfloat16, 128, pkv::kPoolE4M3>(mk, mv, args, d, mx, stream, pdl)
+                : launch_persistent<__half, 128, pkv::kPoolE4M3>(mk, mv, args, d, mx, stream, pdl);
+  if (format == pkv::kPoolInt4) {
+    if (d->head_dim == 128)
+      return bf16 ? launch_persistent<__nv_bfloat16, 128, pkv::kPoolInt4>(mk, mv, args, d, mx, stream, pdl)
+                  : launch_persistent<__half, 128, pkv::kPoolInt4>(mk, mv, args, d, mx, stream, pdl);
+    return bf16 ? launch_persistent<__nv_bfloat16, 64, pkv::kPoolInt4>(mk, mv, args, d, mx, stream, pdl)
+                : launch_persistent<__half, 64, pkv::kPoolInt4>(mk, mv, args, d, mx, stream, pdl);
   }
   if (d->head_dim == 128)
     return bf16 ? launch_decode<__nv_bfloat16, 128>(mk, mv, args, plan, d, stream, pdl)
@@ -513,6 +529,66 @@ int append_fp8_impl(const void* k_new, const void* v_new, const int32_t* slot_ma
     kv(pkv::append_fp8_kernel<__half>);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "append_fp8_kernel launch");
+  return PKV_OK;
+}
+
+// Slot-mapped append into, and read-back from, a 4-bit pool.
+int check_int4_rows(const void* k, const void* v, const int32_t* slot_mapping, int32_t num_tokens, const void* k_cache,
+                    const void* v_cache, const pkv_dims* d, const char* what) {
+  int rc = check_dims(d, false);
+  if (rc != PKV_OK) return rc;
+  if (num_tokens < 0) return pkv_fail(PKV_ERR_INVALID_ARG, std::string(what) + ": num_tokens < 0");
+  if (num_tokens == 0) return PKV_OK;
+  if (!k || !v || !slot_mapping || !k_cache || !v_cache)
+    return pkv_fail(PKV_ERR_INVALID_ARG, std::string(what) + ": NULL pointer");
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(slot_mapping, 4))
+    return pkv_fail(PKV_ERR_INVALID_ARG, std::string(what) + ": misaligned pointer (values and caches need 16 bytes)");
+  return PKV_OK;
+}
+
+// f(T, D) for the value type and head_dim of d.
+template <typename F>
+void with_type_and_dim(const pkv_dims* d, F&& f) {
+  const bool bf16 = d->dtype == PKV_DTYPE_BF16;
+  if (d->head_dim == 128)
+    bf16 ? f(__nv_bfloat16{}, std::integral_constant<int, 128>{}) : f(__half{}, std::integral_constant<int, 128>{});
+  else
+    bf16 ? f(__nv_bfloat16{}, std::integral_constant<int, 64>{}) : f(__half{}, std::integral_constant<int, 64>{});
+}
+
+int append_int4_impl(const void* k_new, const void* v_new, const int32_t* slot_mapping, int32_t num_tokens,
+                     void* k_cache, void* v_cache, const pkv_dims* d, cudaStream_t stream) {
+  const int rc = check_int4_rows(k_new, v_new, slot_mapping, num_tokens, k_cache, v_cache, d, "append_int4");
+  if (rc != PKV_OK || num_tokens == 0) return rc;
+  const int64_t rows = static_cast<int64_t>(num_tokens) * d->num_kv_heads;
+  const int64_t blocks64 = (rows + 7) / 8;
+  const int blocks = static_cast<int>(blocks64 < 65536 ? blocks64 : 65536);
+  const int64_t slots = static_cast<int64_t>(d->num_blocks) * pkv::kBlockSize;
+  with_type_and_dim(d, [&](auto t, auto dim) {
+    pkv::append_int4_kernel<decltype(t), decltype(dim)::value><<<blocks, 256, 0, stream>>>(
+        static_cast<const uint2*>(k_new), static_cast<const uint2*>(v_new), slot_mapping, num_tokens, d->num_kv_heads,
+        slots, static_cast<uint8_t*>(k_cache), static_cast<uint8_t*>(v_cache));
+  });
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(e, "append_int4_kernel launch");
+  return PKV_OK;
+}
+
+int read_int4_impl(const int32_t* slot_mapping, int32_t num_tokens, const void* k_cache, const void* v_cache,
+                   void* k_out, void* v_out, const pkv_dims* d, cudaStream_t stream) {
+  const int rc = check_int4_rows(k_out, v_out, slot_mapping, num_tokens, k_cache, v_cache, d, "read_int4");
+  if (rc != PKV_OK || num_tokens == 0) return rc;
+  const int64_t total = static_cast<int64_t>(num_tokens) * d->num_kv_heads * (d->head_dim / 8);
+  const int64_t blocks64 = (total + 255) / 256;
+  const int blocks = static_cast<int>(blocks64 < 65536 ? blocks64 : 65536);
+  const int64_t slots = static_cast<int64_t>(d->num_blocks) * pkv::kBlockSize;
+  with_type_and_dim(d, [&](auto t, auto dim) {
+    pkv::read_int4_kernel<decltype(t), decltype(dim)::value><<<blocks, 256, 0, stream>>>(
+        slot_mapping, num_tokens, d->num_kv_heads, slots, static_cast<const uint8_t*>(k_cache),
+        static_cast<const uint8_t*>(v_cache), static_cast<uint4*>(k_out), static_cast<uint4*>(v_out));
+  });
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(e, "read_int4_kernel launch");
   return PKV_OK;
 }
 
@@ -874,12 +950,11 @@ int step_from_host(const pkv_step_buffers* s, int32_t q_len, void* k_cache, void
       early = true;
     else
       pre_lens = pre_tables = nullptr;
-    const bool f8 = k_scale != nullptr;
     // The host buffers hold their final values before this call (the caller
     // wrote them), so the early reads need no re-check after the grid wait.
     rc = decode_impl(s->q_dev, s->k_new_dev, s->v_new_dev, k_cache, v_cache, s->block_tables_dev,
-                     s->context_lens_dev, scale, s->out_dev, num_splits, workspace, workspace_bytes, d, stream, f8,
-                     k_scale, v_scale, early, reinterpret_cast<const int32_t*>(pre_lens),
+                     s->context_lens_dev, scale, s->out_dev, num_splits, workspace, workspace_bytes, d, stream,
+                     k_scale ? pkv::kPoolE4M3 : pkv::kPool16, k_scale, v_scale, early, reinterpret_cast<const int32_t*>(pre_lens),
                      reinterpret_cast<const int32_t*>(pre_tables), pre_lens == nullptr);
   }
   if (rc != PKV_OK) return rc;
@@ -890,13 +965,13 @@ int step_from_host(const pkv_step_buffers* s, int32_t q_len, void* k_cache, void
 }  // namespace
 
 int decode_step_host_written(const void* q, const void* k_new, const void* v_new, void* k_cache, void* v_cache,
-                             const float* k_scale, const float* v_scale, const int32_t* block_tables,
+                             const float* k_scale, const float* v_scale, bool int4, const int32_t* block_tables,
                              const int32_t* context_lens, float scale, void* out, void* workspace,
                              size_t workspace_bytes, const pkv_dims* dims, void* stream) {
   if (!k_new || !v_new) return pkv_fail(PKV_ERR_INVALID_ARG, "decode_step: NULL k_new / v_new");
   return decode_impl(q, k_new, v_new, k_cache, v_cache, block_tables, context_lens, scale, out, 0, workspace,
-                     workspace_bytes, dims, static_cast<cudaStream_t>(stream), k_scale != nullptr, k_scale, v_scale,
-                     true, nullptr, nullptr, false);
+                     workspace_bytes, dims, static_cast<cudaStream_t>(stream),
+                     int4 ? pkv::kPoolInt4 : k_scale ? pkv::kPoolE4M3 : pkv::kPool16, k_scale, v_scale, true, nullptr, nullptr, false);
 }
 
 extern "C" {
@@ -948,15 +1023,17 @@ int paged_kv_copy_blocks(void* k_cache, void* v_cache, const int32_t* block_pair
   if (!d) return pkv_fail(PKV_ERR_INVALID_ARG, "copy_blocks: dims is NULL");
   if (num_pairs < 0) return pkv_fail(PKV_ERR_INVALID_ARG, "copy_blocks: num_pairs < 0");
   if (num_pairs == 0) return PKV_OK;
-  if (cache_elem_bytes != 1 && cache_elem_bytes != 2)
-    return pkv_fail(PKV_ERR_INVALID_ARG, "copy_blocks: cache_elem_bytes must be 1 (E4M3) or 2 (fp16/bf16)");
+  if (cache_elem_bytes != PKV_ELEM_INT4 && cache_elem_bytes != 1 && cache_elem_bytes != 2)
+    return pkv_fail(PKV_ERR_INVALID_ARG,
+                    "copy_blocks: cache_elem_bytes must be PKV_ELEM_INT4, 1 (E4M3) or 2 (fp16/bf16)");
   if (d->num_kv_heads <= 0 || d->num_blocks <= 0 || d->head_dim <= 0 || d->head_dim % 16 != 0 ||
       d->block_size != pkv::kBlockSize)
     return pkv_fail(PKV_ERR_INVALID_ARG, "copy_blocks: bad dims");
   if (!k_cache || !v_cache || !block_pairs) return pkv_fail(PKV_ERR_INVALID_ARG, "copy_blocks: NULL pointer");
   if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(block_pairs, 4))
     return pkv_fail(PKV_ERR_INVALID_ARG, "copy_blocks: misaligned pointer (caches need 16 bytes)");
-  const int64_t chunks = static_cast<int64_t>(d->num_kv_heads) * pkv::kBlockSize * d->head_dim * cache_elem_bytes / 16;
+  const int64_t row_bytes = cache_elem_bytes == PKV_ELEM_INT4 ? d->head_dim / 2 + 4 : d->head_dim * cache_elem_bytes;
+  const int64_t chunks = d->num_kv_heads * row_bytes;  // of 16 bytes: a block has 16 rows per KV head
   const int64_t total = chunks * num_pairs;
   const int64_t blocks64 = (total + 255) / 256;
   const int cap = 8 * device_sms();
@@ -985,7 +1062,7 @@ int paged_kv_selftest_stale_prologue(const void* q, const void* k_new, const voi
       !aligned(stale_context_lens, 4))
     return pkv_fail(PKV_ERR_INVALID_ARG, "selftest_stale_prologue: stale inputs missing or misaligned");
   return decode_impl(q, k_new, v_new, k_cache, v_cache, block_tables, context_lens, scale, out, 0, workspace,
-                     workspace_bytes, dims, static_cast<cudaStream_t>(stream), false, nullptr, nullptr, true,
+                     workspace_bytes, dims, static_cast<cudaStream_t>(stream), pkv::kPool16, nullptr, nullptr, true,
                      stale_context_lens, stale_block_tables, true, publish != 0);
 }
 
@@ -1002,7 +1079,7 @@ int paged_decode_attention_fp8(const void* q, const void* k_cache, const void* v
                                const pkv_dims* dims, void* stream) {
   return decode_impl(q, nullptr, nullptr, const_cast<void*>(k_cache), const_cast<void*>(v_cache), block_tables,
                      context_lens, scale, out, 0, workspace, workspace_bytes, dims,
-                     static_cast<cudaStream_t>(stream), true, k_scale, v_scale);
+                     static_cast<cudaStream_t>(stream), pkv::kPoolE4M3, k_scale, v_scale);
 }
 
 int paged_decode_step_fp8(const void* q, const void* k_new, const void* v_new, void* k_cache, void* v_cache,
@@ -1011,7 +1088,35 @@ int paged_decode_step_fp8(const void* q, const void* k_new, const void* v_new, v
                           size_t workspace_bytes, const pkv_dims* dims, void* stream) {
   if (!k_new || !v_new) return pkv_fail(PKV_ERR_INVALID_ARG, "decode_step_fp8: NULL k_new / v_new");
   return decode_impl(q, k_new, v_new, k_cache, v_cache, block_tables, context_lens, scale, out, 0, workspace,
-                     workspace_bytes, dims, static_cast<cudaStream_t>(stream), true, k_scale, v_scale);
+                     workspace_bytes, dims, static_cast<cudaStream_t>(stream), pkv::kPoolE4M3, k_scale, v_scale);
+}
+
+int paged_kv_append_int4(const void* k_new, const void* v_new, const int32_t* slot_mapping, int32_t num_tokens,
+                         void* k_cache, void* v_cache, const pkv_dims* dims, void* stream) {
+  return append_int4_impl(k_new, v_new, slot_mapping, num_tokens, k_cache, v_cache, dims,
+                          static_cast<cudaStream_t>(stream));
+}
+
+int paged_kv_read_int4(const int32_t* slot_mapping, int32_t num_tokens, const void* k_cache, const void* v_cache,
+                       void* k_out, void* v_out, const pkv_dims* dims, void* stream) {
+  return read_int4_impl(slot_mapping, num_tokens, k_cache, v_cache, k_out, v_out, dims,
+                        static_cast<cudaStream_t>(stream));
+}
+
+int paged_decode_attention_int4(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
+                                const int32_t* context_lens, float scale, void* out, void* workspace,
+                                size_t workspace_bytes, const pkv_dims* dims, void* stream) {
+  return decode_impl(q, nullptr, nullptr, const_cast<void*>(k_cache), const_cast<void*>(v_cache), block_tables,
+                     context_lens, scale, out, 0, workspace, workspace_bytes, dims,
+                     static_cast<cudaStream_t>(stream), pkv::kPoolInt4);
+}
+
+int paged_decode_step_int4(const void* q, const void* k_new, const void* v_new, void* k_cache, void* v_cache,
+                           const int32_t* block_tables, const int32_t* context_lens, float scale, void* out,
+                           void* workspace, size_t workspace_bytes, const pkv_dims* dims, void* stream) {
+  if (!k_new || !v_new) return pkv_fail(PKV_ERR_INVALID_ARG, "decode_step_int4: NULL k_new / v_new");
+  return decode_impl(q, k_new, v_new, k_cache, v_cache, block_tables, context_lens, scale, out, 0, workspace,
+                     workspace_bytes, dims, static_cast<cudaStream_t>(stream), pkv::kPoolInt4);
 }
 
 int paged_kv_append(const void* k_new, const void* v_new, const int32_t* slot_mapping, int32_t num_tokens,
@@ -1090,7 +1195,7 @@ int paged_kv_check_status(void* stream_v) {
   if (word & pkv::kErrSlot) msg += " append slot out of range;";
   if (word & pkv::kErrContext) msg += " context length out of range;";
   if (word & pkv::kErrTimeout) msg += " a bounded wait gave up;";
-  if (word & pkv::kErrQuery) msg += " a query value exceeds the fp16 range (fp8 cache path);";
+  if (word & pkv::kErrQuery) msg += " a query value exceeds the fp16 range (fp8 or 4-bit cache path);";
   return pkv_fail((word & pkv::kErrTimeout) ? PKV_ERR_TIMEOUT : PKV_ERR_OUT_OF_RANGE, msg);
 }
 

@@ -15,7 +15,7 @@ enum : unsigned {
   kErrSlot = 2u,      // an append slot outside the pool
   kErrContext = 4u,   // a context length < 0 or longer than its block table
   kErrTimeout = 8u,   // a bounded wait gave up
-  kErrQuery = 16u,    // E4M3 path: a query value beyond the fp16 range
+  kErrQuery = 16u,    // E4M3 and 4-bit pools: a query value beyond the fp16 range
 };
 
 // A wait that has not finished after this long is treated as lost.
@@ -124,6 +124,16 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
                : "memory");
+}
+
+// The same with an L2 cache policy.
+__device__ __forceinline__ void bulk_load_hint(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar,
+                                               uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar), "l"(policy)
+      : "memory");
 }
 
 // ------------------------------------------------------------------ mma.sync

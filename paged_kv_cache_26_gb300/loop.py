@@ -25,7 +25,8 @@ Empty batch slots have context length 0 (zero output, nothing appended).
 With ``k_scale`` / ``v_scale`` (float32[num_kv_heads]) the pools hold E4M3
 codes (design.babushkai.com "GPU推論の内部構造", section "KVキャッシュの台帳":
 an FP8 cache halves the bytes per token); prompts and new tokens stay
-fp16/bf16 and are quantised as they are appended.
+fp16/bf16 and are quantised as they are appended.  With ``int4`` the pools are
+4-bit: each row carries its own scale and minimum, so nothing else is given.
 """
 from __future__ import annotations
 
@@ -45,7 +46,8 @@ BLOCK_SIZE = 16
 class DecodeLoop:
     def __init__(self, num_blocks: int, num_q_heads: int, num_kv_heads: int, head_dim: int, max_batch: int,
                  max_context: int, dtype=torch.bfloat16, device="cuda", seed: int = 0,
-                 k_scale: Optional[torch.Tensor] = None, v_scale: Optional[torch.Tensor] = None):
+                 k_scale: Optional[torch.Tensor] = None, v_scale: Optional[torch.Tensor] = None,
+                 int4: bool = False):
         self.device = torch.device(device)
         self.dtype = dtype
         self.H, self.Hk, self.D = num_q_heads, num_kv_heads, head_dim
@@ -54,8 +56,12 @@ class DecodeLoop:
         self.fp8 = k_scale is not None
         if self.fp8 != (v_scale is not None):
             raise ValueError("give both k_scale and v_scale, or neither")
-        cache_dtype = torch.uint8 if self.fp8 else dtype
-        self.k_cache = torch.zeros(num_blocks, num_kv_heads, BLOCK_SIZE, head_dim, dtype=cache_dtype,
+        self.int4 = int4
+        if int4 and self.fp8:
+            raise ValueError("a 4-bit pool takes no scales: give int4 or k_scale / v_scale")
+        cache_dtype = torch.uint8 if self.fp8 or int4 else dtype
+        row = api.int4_row_bytes(head_dim) if int4 else head_dim
+        self.k_cache = torch.zeros(num_blocks, num_kv_heads, BLOCK_SIZE, row, dtype=cache_dtype,
                                    device=self.device)
         self.v_cache = torch.zeros_like(self.k_cache)
         if self.fp8:
@@ -74,6 +80,9 @@ class DecodeLoop:
             api._check(lib().decode_engine_set_kv_scales(self._eng, ctypes.c_void_p(k_scale.data_ptr()),
                                                          ctypes.c_void_p(v_scale.data_ptr())), "set_kv_scales")
             self._dims = api.make_dims_fp8(probe_q, self.k_cache)
+        elif int4:
+            api._check(lib().decode_engine_set_int4(self._eng, 1), "set_int4")
+            self._dims = api.make_dims_int4(probe_q, self.k_cache)
         else:
             self._dims = api.make_dims(probe_q, self.k_cache)
         self._dims.max_blocks_per_seq = self.max_blocks

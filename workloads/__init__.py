@@ -321,3 +321,32 @@ def generate_multi(spec: WorkloadSpec, q_len: int, seed: int = 0, device="cpu",
         m.k_new.append(torch.randn((B, q_len, Hk, D), generator=gen, device=device, dtype=torch.float32).to(dt))
         m.v_new.append(torch.randn((B, q_len, Hk, D), generator=gen, device=device, dtype=torch.float32).to(dt))
     return w, m
+
+
+# ---------------------------------------------------------------- 4-bit pools
+
+@dataclass
+class Int4Caches:
+    """4-bit stand-ins of a workload's caches (before the append)."""
+
+    k_cache: List[torch.Tensor]   # per layer: uint8[NB][Hkv][BS][D/2 + 4]
+    v_cache: List[torch.Tensor]
+
+
+def int4_caches(w: Workload, store) -> Int4Caches:
+    """A 4-bit pool for workload ``w``: the workload's own cache values of every
+    token slot, put into a pool of 0xFF bytes (whose pairs are NaN) by
+    ``store(k_rows, v_rows, slots, k_pool, v_pool)``, the caller's quantising
+    append.  The new token's K/V stay fp16/bf16: the step quantises them."""
+    s = w.spec
+    out = Int4Caches([], [])
+    for layer in range(len(w.k_cache)):
+        kc, vc = w.k_cache[layer], w.v_cache[layer]
+        live = torch.nonzero(~torch.isnan(kc[:, 0, :, 0].float()).flatten())[:, 0]
+        rows = [c.transpose(1, 2).reshape(-1, s.num_kv_heads, s.head_dim)[live].contiguous() for c in (kc, vc)]
+        pools = [torch.full((w.num_blocks, s.num_kv_heads, s.block_size, s.head_dim // 2 + 4), 0xFF,
+                            dtype=torch.uint8, device=kc.device) for _ in range(2)]
+        pools = store(rows[0], rows[1], live.int(), *pools) or pools
+        out.k_cache.append(pools[0])
+        out.v_cache.append(pools[1])
+    return out
