@@ -80,7 +80,7 @@ enum {
   PKV_ERR_SHARED_BLOCK = -7   /* a write would land in a block other sequences share */
 };
 
-enum { PKV_DTYPE_FP16 = 0, PKV_DTYPE_BF16 = 1 };
+enum { PKV_DTYPE_FP16 = 0, PKV_DTYPE_BF16 = 1, PKV_DTYPE_FP32 = 2 /* paged_verify_draft only */ };
 
 enum { PKV_ELEM_INT4 = 0 }; /* paged_kv_copy_blocks' element size of a 4-bit pool */
 
@@ -438,6 +438,90 @@ int paged_kv_slot_mapping_multi(const int32_t* block_tables, const int32_t* cont
                                 int32_t q_len, int32_t* slot_mapping);
 
 /* ------------------------------------------------------------------------
+ * Verification of drafted tokens (device): youngju.dev "LLM サービング最適化完全
+ * ガイド", speculative decoding section (the target model checks several draft
+ * tokens in one pass; accepted ones are kept, the first rejected one is
+ * sampled again).  It follows a paged_decode_step_multi of q_len = num_draft + 1
+ * tokens per sequence (the last known token and the drafts).
+ *
+ * target_probs : T[num_seqs][num_draft + 1][vocab], row i the target's
+ *                distribution after draft i - 1 (row 0: after the last known token)
+ * draft_probs  : T[num_seqs][num_draft][vocab], what draft i was drawn from; NULL:
+ *                drafts given without probabilities (looked up in the prompt),
+ *                as if each had been certain
+ * draft_tokens : int32[num_seqs][num_draft]
+ * draft_lens   : int32[num_seqs], drafts of each sequence, 0..num_draft; NULL: all
+ * accept_u     : float[num_seqs][num_draft], sample_u: float[num_seqs], uniform
+ *                random numbers in [0, 1) of the caller's
+ * T = fp16, bf16 or fp32 (dims->dtype); rows have unit stride, sequences and
+ * rows the strides in dims (in elements; a padded vocabulary needs no copy).
+ *
+ * Draft i is accepted if accept_u * q(x) < p(x) (exact products) and all before
+ * it were.  After a accepted drafts of n, one token is drawn by the inverse CDF
+ * at sample_u: from max(p - q, 0) of row a if a < n (from p if that is 0
+ * everywhere), else from p of row n.  Probabilities count as whole numbers of
+ * 2^-40 (rounded to nearest, half to even; limited to 0..1, NaN as 0), w(v);
+ * with total W = sum w and U = min(floor(sample_u * 2^30), 2^30 - 1), limited
+ * below to 0, the token is the lowest v with sum of w(0..v) > floor(W U / 2^30):
+ * the sums are exact and the result the same in every run.
+ * num_accepted int32[num_seqs] = a; out_tokens int32[num_seqs][num_draft + 1] =
+ * the accepted drafts, the drawn token (-1 if the row has no probability at
+ * all), then -1.  new_lens (NULL, or int32[num_seqs] with context_lens given) =
+ * context_lens[b] - (num_draft - a): the length without the rejected drafts, for
+ * paged_kv_resize_tables.  A sequence with context_lens[b] <= 0 (an empty batch
+ * slot) gets 0 accepted, tokens -1 and length 0; its rows are not read.
+ * Limits: num_draft 0..31, vocab 1..2^22.  A token outside the vocabulary is
+ * rejected, a draft length outside 0..num_draft is limited; both are flagged
+ * (PKV_ERR_OUT_OF_RANGE from paged_kv_check_status).
+ * ---------------------------------------------------------------------- */
+typedef struct pkv_verify_dims {
+  int32_t num_seqs, num_draft, vocab, dtype;
+  int64_t target_seq_stride, target_row_stride, draft_seq_stride, draft_row_stride;
+} pkv_verify_dims;
+
+int paged_verify_draft(const void* target_probs, const void* draft_probs, const int32_t* draft_tokens,
+                       const int32_t* draft_lens, const float* accept_u, const float* sample_u,
+                       const int32_t* context_lens, const pkv_verify_dims* dims, int32_t* num_accepted,
+                       int32_t* out_tokens, int32_t* new_lens, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Block tables and slot maps built on the GPU from the sequences' lengths
+ * (device; nothing is copied from or to the host, so a captured loop can grow):
+ * kasblo.com "vLLMとは？", section "blockはrequestの成長に合わせて割り当てる" (blocks come
+ * from a pool, one more when the current block fills, and go back to it), and
+ * youngju.dev's PagedAttention layout figure (position -> table -> slot).
+ *
+ * Sequence b goes from context_lens[b] to new_lens[b] tokens.  With n(L) =
+ * ceil(L / 16), a sequence that needs more blocks takes n(new) - n(old) from the
+ * free list into entries n(old).. of its table row; one that needs fewer gives
+ * entries n(new)..n(old) - 1 back (they keep their old contents; entries past
+ * the length are never read).
+ * free_blocks : int32[num_blocks], of which the first num_free[0] are free
+ *   blocks, a stack.  Blocks given are put on it first, in descending order of
+ *   (sequence, block); blocks taken then come off its top in ascending order.
+ *   So a growth that is taken back leaves the list as it was.
+ * slot_mapping : int32[num_slots] or NULL (num_slots 0): the slots of the tokens
+ *   gained, positions old..new - 1 of each sequence that grows, packed by
+ *   sequence; -1 behind them, which every append skips.  num_slots must hold
+ *   them all.
+ * token_offsets : int32[num_seqs + 1] or NULL: where each sequence's slots begin.
+ * On success context_lens becomes new_lens and num_free the new count.
+ * All or nothing: with too few blocks (PKV_ERR_NO_BLOCKS from
+ * paged_kv_check_status), a length outside 0..max_blocks * 16, more tokens than
+ * num_slots or a count outside the list (PKV_ERR_OUT_OF_RANGE), nothing changes
+ * but slot_mapping (all -1) and token_offsets (all 0).  A block id outside
+ * 0..num_blocks - 1 met on the list or in a table gives slot -1 and is flagged.
+ * Every block belongs to one sequence: shared blocks (reference counts) are the
+ * host allocator's.  Calls on the same pool must not run concurrently; the
+ * arrays must not overlap.  Limits: block_size 16, num_seqs 0..8192,
+ * num_blocks * 16, max_blocks * 16 and num_seqs * max_blocks below 2^31.
+ * ---------------------------------------------------------------------- */
+int paged_kv_resize_tables(int32_t* context_lens, const int32_t* new_lens, int32_t num_seqs, int32_t max_blocks,
+                           int32_t block_size, int32_t* block_tables, int32_t* free_blocks, int32_t* num_free,
+                           int32_t num_blocks, int32_t* slot_mapping, int32_t num_slots, int32_t* token_offsets,
+                           void* stream);
+
+/* ------------------------------------------------------------------------
  * Copy-on-write of shared blocks: kasblo.com "vLLMとは？", section
  * "block共有とAutomatic Prefix Caching" (a block carries a reference count, is
  * shared by several sequences, and is duplicated only when one of them must
@@ -485,7 +569,8 @@ int paged_kv_selftest_stale_prologue(const void* q, const void* k_new, const voi
                                      int32_t publish, const pkv_dims* dims, void* stream);
 
 /* Synchronises `stream`, then reads and clears this device's error word.
- * Returns PKV_OK, PKV_ERR_OUT_OF_RANGE, PKV_ERR_TIMEOUT or PKV_ERR_CUDA. */
+ * Returns PKV_OK, PKV_ERR_OUT_OF_RANGE, PKV_ERR_NO_BLOCKS (nothing but a table
+ * resize that wanted too many blocks), PKV_ERR_TIMEOUT or PKV_ERR_CUDA. */
 int paged_kv_check_status(void* stream);
 
 /* Message for the calling thread's last non-OK return (never NULL). */

@@ -21,6 +21,12 @@ class PkvStepBuffers(ctypes.Structure):
         "q_dev", "k_new_dev", "v_new_dev", "block_tables_dev", "context_lens_dev", "out_dev")]
 
 
+class PkvVerifyDims(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_int32) for name in ("num_seqs", "num_draft", "vocab", "dtype")] + \
+               [(name, ctypes.c_int64) for name in ("target_seq_stride", "target_row_stride", "draft_seq_stride",
+                                                    "draft_row_stride")]
+
+
 class PkvEngineStats(ctypes.Structure):
     _fields_ = [(name, ctypes.c_int64) for name in (
         "steps", "sequence_steps", "context_tokens", "unused_tail_slots", "copied_blocks")]
@@ -80,6 +86,14 @@ _SIGNATURES = {
                                               ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_float,
                                               ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t,
                                               ctypes.POINTER(PkvDims), ctypes.c_void_p]),
+    "paged_kv_resize_tables": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32,
+                                              ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                              ctypes.c_int32, ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p,
+                                              ctypes.c_void_p]),
+    "paged_verify_draft": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                          ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                          ctypes.POINTER(PkvVerifyDims), ctypes.c_void_p, ctypes.c_void_p,
+                                          ctypes.c_void_p, ctypes.c_void_p]),
     "paged_decode_attention_multi": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                                                     ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_float,
                                                     ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p,

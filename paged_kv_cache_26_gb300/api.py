@@ -10,7 +10,7 @@ from typing import Optional, Sequence
 import numpy as np
 import torch
 
-from ._native import PkvDims, PkvStepBuffers, c_int32_p, lib
+from ._native import PkvDims, PkvStepBuffers, PkvVerifyDims, c_int32_p, lib
 
 PKV_OK = 0
 ERROR_NAMES = {
@@ -590,6 +590,101 @@ def paged_decode_step_int4(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Te
                                         _ptr(workspace), ws_bytes, ctypes.byref(dims), _stream(stream)),
            "paged_decode_step_int4")
     return out
+
+
+# ---------------------------------------------------------------- speculative serving on the GPU
+
+def paged_kv_resize_tables(context_lens: torch.Tensor, new_lens: torch.Tensor, block_tables: torch.Tensor,
+                           free_blocks: torch.Tensor, num_free: torch.Tensor,
+                           slot_mapping: Optional[torch.Tensor] = None,
+                           token_offsets: Optional[torch.Tensor] = None, stream=None):
+    """Take every sequence from context_lens[b] to new_lens[b] tokens, on the
+    GPU: blocks it needs come off the stack free_blocks[:num_free[0]] into its
+    table row, blocks it no longer needs go back.  slot_mapping (int32, at least
+    as long as the tokens gained) receives the slots of positions old..new - 1,
+    packed by sequence and -1 behind them; token_offsets (int32 [num_seqs + 1])
+    where each sequence's begin.  context_lens, block_tables, free_blocks
+    (int32 [num_blocks]) and num_free (int32 [1]) are updated in place, all or
+    nothing (paged_kv_check_status tells).  Returns (slot_mapping,
+    token_offsets)."""
+    for n, t in (("context_lens", context_lens), ("new_lens", new_lens), ("block_tables", block_tables),
+                 ("free_blocks", free_blocks), ("num_free", num_free)):
+        _need_cuda(n, t, torch.int32)
+    for n, t in (("slot_mapping", slot_mapping), ("token_offsets", token_offsets)):
+        if t is not None:
+            _need_cuda(n, t, torch.int32)
+    B = context_lens.shape[0] if context_lens.dim() == 1 else -1
+    if new_lens.shape != (B,) or block_tables.dim() != 2 or block_tables.shape[0] != B:
+        raise ValueError("context_lens / new_lens must be [num_seqs], block_tables [num_seqs][max_blocks]")
+    if free_blocks.dim() != 1 or num_free.numel() != 1:
+        raise ValueError("free_blocks must be [num_blocks], num_free one number")
+    if slot_mapping is not None and slot_mapping.dim() != 1:
+        raise ValueError("slot_mapping must be [num_slots]")
+    if token_offsets is not None and token_offsets.shape != (B + 1,):
+        raise ValueError("token_offsets must be [num_seqs + 1]")
+    _check(lib().paged_kv_resize_tables(
+        _ptr(context_lens), _ptr(new_lens), B, block_tables.shape[1], 16, _ptr(block_tables), _ptr(free_blocks),
+        _ptr(num_free), free_blocks.shape[0], _ptr(slot_mapping),
+        slot_mapping.shape[0] if slot_mapping is not None else 0, _ptr(token_offsets), _stream(stream)),
+        "paged_kv_resize_tables")
+    return slot_mapping, token_offsets
+
+
+_PROB_CODE = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
+
+
+def _need_rows(name: str, t: torch.Tensor, shape, dtype):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 3 or tuple(t.shape) != tuple(shape) or (t.shape[2] > 1 and t.stride(2) != 1):
+        raise ValueError(f"{name} must be {list(shape)} with a unit stride along the vocabulary")
+
+
+def paged_verify_draft(target_probs: torch.Tensor, draft_probs: Optional[torch.Tensor], draft_tokens: torch.Tensor,
+                       accept_u: torch.Tensor, sample_u: torch.Tensor, draft_lens: Optional[torch.Tensor] = None,
+                       context_lens: Optional[torch.Tensor] = None, stream=None):
+    """Accept or reject drafted tokens against the target's probabilities.
+
+    target_probs [B][K + 1][V] (float32, float16 or bfloat16; rows may be views
+    into a padded vocabulary), draft_probs [B][K][V] of the same type or None
+    (drafts without probabilities), draft_tokens int32 [B][K], accept_u float32
+    [B][K] and sample_u float32 [B] uniform in [0, 1), draft_lens int32 [B] (how
+    many of the K are drafts), context_lens int32 [B] (lengths with the K + 1
+    tokens of the multi-token step).  Returns (num_accepted int32 [B], tokens
+    int32 [B][K + 1]: the accepted drafts, the token drawn after them, then -1,
+    new_lens int32 [B]: context_lens without the rejected drafts, or None)."""
+    if target_probs.dtype not in _PROB_CODE:
+        raise ValueError("target_probs must be float32, float16 or bfloat16")
+    _need_cuda("draft_tokens", draft_tokens, torch.int32)
+    _need_cuda("accept_u", accept_u, torch.float32)
+    _need_cuda("sample_u", sample_u, torch.float32)
+    if draft_tokens.dim() != 2 or accept_u.shape != draft_tokens.shape:
+        raise ValueError("draft_tokens / accept_u must be [num_seqs][num_draft]")
+    B, K = draft_tokens.shape
+    V = target_probs.shape[2] if target_probs.dim() == 3 else 0
+    _need_rows("target_probs", target_probs, (B, K + 1, V), target_probs.dtype)
+    if draft_probs is not None:
+        _need_rows("draft_probs", draft_probs, (B, K, V), target_probs.dtype)
+    if sample_u.shape != (B,):
+        raise ValueError("sample_u must be [num_seqs]")
+    for n, t in (("draft_lens", draft_lens), ("context_lens", context_lens)):
+        if t is not None:
+            _need_cuda(n, t, torch.int32)
+            if t.shape != (B,):
+                raise ValueError(f"{n} must be [num_seqs]")
+    new = lambda *shape: torch.empty(shape, dtype=torch.int32, device=target_probs.device)  # noqa: E731
+    accepted, tokens = new(B), new(B, K + 1)
+    lens = new(B) if context_lens is not None else None
+    dims = PkvVerifyDims(B, K, V, _PROB_CODE[target_probs.dtype], target_probs.stride(0), target_probs.stride(1),
+                         draft_probs.stride(0) if draft_probs is not None else 0,
+                         draft_probs.stride(1) if draft_probs is not None else 0)
+    _check(lib().paged_verify_draft(_ptr(target_probs), _ptr(draft_probs), _ptr(draft_tokens), _ptr(draft_lens),
+                                    _ptr(accept_u), _ptr(sample_u), _ptr(context_lens), ctypes.byref(dims),
+                                    _ptr(accepted), _ptr(tokens), _ptr(lens), _stream(stream)),
+           "paged_verify_draft")
+    return accepted, tokens, lens
 
 
 def paged_kv_copy_blocks(k_cache: torch.Tensor, v_cache: torch.Tensor, block_pairs: torch.Tensor,

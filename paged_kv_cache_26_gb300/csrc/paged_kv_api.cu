@@ -21,6 +21,8 @@
 #include "paged_kv_kernels.cuh"
 #include "pkv_errors.h"
 #include "pkv_internal.h"
+#include "table_resize.cuh"
+#include "verify_draft.cuh"
 
 namespace {
 
@@ -592,6 +594,94 @@ int read_int4_impl(const int32_t* slot_mapping, int32_t num_tokens, const void* 
   return PKV_OK;
 }
 
+// ------------------------------------------------------------------ block tables from lengths
+
+// A launch of `grid` CTAs in clusters of `cluster`.
+template <typename... Params, typename... Args>
+cudaError_t launch_clusters(void (*kern)(Params...), unsigned grid, unsigned cluster, unsigned threads, size_t smem,
+                            cudaStream_t stream, Args... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cluster;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+int resize_tables_impl(const pkv::ResizeArgs& a, int32_t block_size, cudaStream_t stream) {
+  if (a.num_seqs < 0 || a.max_blocks < 0 || a.num_blocks <= 0 || a.num_slots < 0)
+    return pkv_fail(PKV_ERR_INVALID_ARG, "resize_tables: negative or zero size");
+  if (block_size != pkv::kBlockSize) return pkv_fail(PKV_ERR_UNSUPPORTED, "resize_tables: block_size must be 16");
+  if (a.num_seqs > pkv::kMaxResizeSeqs)
+    return pkv_fail(PKV_ERR_UNSUPPORTED,
+                    "resize_tables: at most " + std::to_string(pkv::kMaxResizeSeqs) + " sequences per call");
+  if (static_cast<int64_t>(a.num_blocks) * pkv::kBlockSize >= (int64_t(1) << 31) ||
+      static_cast<int64_t>(a.max_blocks) * pkv::kBlockSize >= (int64_t(1) << 31) ||
+      static_cast<int64_t>(a.num_seqs) * a.max_blocks >= (int64_t(1) << 31))
+    return pkv_fail(PKV_ERR_UNSUPPORTED, "resize_tables: num_blocks * 16, max_blocks * 16 and num_seqs * max_blocks "
+                                         "must be < 2^31");
+  if (a.num_seqs > 0 && (!a.context_lens || !a.new_lens || (!a.block_tables && a.max_blocks > 0)))
+    return pkv_fail(PKV_ERR_INVALID_ARG, "resize_tables: NULL pointer");
+  if (!a.free_blocks || !a.num_free) return pkv_fail(PKV_ERR_INVALID_ARG, "resize_tables: NULL free list");
+  if (!a.slot_mapping && a.num_slots > 0) return pkv_fail(PKV_ERR_INVALID_ARG, "resize_tables: NULL slot_mapping");
+  for (const void* p : {static_cast<const void*>(a.context_lens), static_cast<const void*>(a.new_lens),
+                        static_cast<const void*>(a.block_tables), static_cast<const void*>(a.free_blocks),
+                        static_cast<const void*>(a.num_free), static_cast<const void*>(a.slot_mapping),
+                        static_cast<const void*>(a.token_offsets)})
+    if (!aligned(p, 4)) return pkv_fail(PKV_ERR_INVALID_ARG, "resize_tables: misaligned pointer");
+  const size_t smem = pkv::resize_smem_bytes(a.num_seqs);
+  cudaError_t e = configure_smem<pkv::resize_tables_kernel>(
+      static_cast<int>(pkv::resize_smem_bytes(pkv::kMaxResizeSeqs)));
+  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(resize_tables_kernel)");
+  // One CTA for what it writes in one pass, eight for prompts.
+  const unsigned cluster = a.num_slots > 4 * pkv::kResizeThreads ? 8 : 1;
+  e = launch_clusters(pkv::resize_tables_kernel, cluster, cluster, pkv::kResizeThreads, smem, stream, a);
+  if (e != cudaSuccess) return cuda_fail(e, "resize_tables_kernel launch");
+  return PKV_OK;
+}
+
+// ------------------------------------------------------------------ draft verification
+
+int verify_draft_impl(const pkv::VerifyArgs& a, int32_t num_seqs, int32_t dtype, cudaStream_t stream) {
+  if (num_seqs < 0 || a.num_draft < 0 || a.vocab < 1)
+    return pkv_fail(PKV_ERR_INVALID_ARG, "verify_draft: negative or zero size");
+  if (dtype != PKV_DTYPE_FP16 && dtype != PKV_DTYPE_BF16 && dtype != PKV_DTYPE_FP32)
+    return pkv_fail(PKV_ERR_UNSUPPORTED, "verify_draft: probabilities must be fp16, bf16 or fp32");
+  if (a.num_draft > pkv::kMaxDrafts || a.vocab > pkv::kMaxVocab)
+    return pkv_fail(PKV_ERR_UNSUPPORTED, "verify_draft: at most " + std::to_string(pkv::kMaxDrafts) +
+                                             " drafts and a vocabulary of " + std::to_string(pkv::kMaxVocab));
+  if (num_seqs > (1 << 27)) return pkv_fail(PKV_ERR_UNSUPPORTED, "verify_draft: too many sequences");
+  if (num_seqs == 0) return PKV_OK;
+  if (!a.target || !a.sample_u || !a.num_accepted || !a.out_tokens || (a.num_draft > 0 && (!a.tokens || !a.accept_u)) ||
+      (a.new_lens && !a.context_lens))
+    return pkv_fail(PKV_ERR_INVALID_ARG, "verify_draft: NULL pointer");
+  if (a.target_seq < 0 || a.target_row < 0 || a.draft_seq < 0 || a.draft_row < 0)
+    return pkv_fail(PKV_ERR_INVALID_ARG, "verify_draft: negative stride");
+  const uintptr_t elem = dtype == PKV_DTYPE_FP32 ? 4 : 2;
+  if (!aligned(a.target, elem) || !aligned(a.draft, elem) || !aligned(a.tokens, 4) || !aligned(a.draft_lens, 4) ||
+      !aligned(a.accept_u, 4) || !aligned(a.sample_u, 4) || !aligned(a.context_lens, 4) ||
+      !aligned(a.num_accepted, 4) || !aligned(a.out_tokens, 4) || !aligned(a.new_lens, 4))
+    return pkv_fail(PKV_ERR_INVALID_ARG, "verify_draft: misaligned pointer");
+  // As many CTAs per row as have a step of 128 entries for each of their warps.
+  unsigned cluster = 1;
+  while (cluster < pkv::kMaxVerifyCluster && a.vocab > static_cast<int>(cluster) * pkv::kVerifyWarps * 128) cluster *= 2;
+  auto launch = [&](auto kern) {
+    return launch_clusters(kern, static_cast<unsigned>(num_seqs) * cluster, cluster, pkv::kVerifyWarps * 32, 0, stream,
+                           a);
+  };
+  const cudaError_t e = dtype == PKV_DTYPE_FP32   ? launch(pkv::verify_draft_kernel<float>)
+                        : dtype == PKV_DTYPE_BF16 ? launch(pkv::verify_draft_kernel<__nv_bfloat16>)
+                                                  : launch(pkv::verify_draft_kernel<__half>);
+  if (e != cudaSuccess) return cuda_fail(e, "verify_draft_kernel launch");
+  return PKV_OK;
+}
+
 // ------------------------------------------------------------------ several new tokens per sequence
 
 // Splits of the multi-token kernels: 512-token splits, at least 2 blocks per
@@ -1046,6 +1136,39 @@ int paged_kv_copy_blocks(void* k_cache, void* v_cache, const int32_t* block_pair
   return PKV_OK;
 }
 
+int paged_kv_resize_tables(int32_t* context_lens, const int32_t* new_lens, int32_t num_seqs, int32_t max_blocks,
+                           int32_t block_size, int32_t* block_tables, int32_t* free_blocks, int32_t* num_free,
+                           int32_t num_blocks, int32_t* slot_mapping, int32_t num_slots, int32_t* token_offsets,
+                           void* stream) {
+  const pkv::ResizeArgs a = {context_lens, new_lens,   block_tables, free_blocks, num_free, slot_mapping,
+                             token_offsets, num_seqs, max_blocks,   num_blocks,  num_slots};
+  return resize_tables_impl(a, block_size, static_cast<cudaStream_t>(stream));
+}
+
+int paged_verify_draft(const void* target_probs, const void* draft_probs, const int32_t* draft_tokens,
+                       const int32_t* draft_lens, const float* accept_u, const float* sample_u,
+                       const int32_t* context_lens, const pkv_verify_dims* dims, int32_t* num_accepted,
+                       int32_t* out_tokens, int32_t* new_lens, void* stream) {
+  if (!dims) return pkv_fail(PKV_ERR_INVALID_ARG, "verify_draft: dims is NULL");
+  const pkv::VerifyArgs a = {target_probs,
+                             draft_probs,
+                             draft_tokens,
+                             draft_lens,
+                             accept_u,
+                             sample_u,
+                             context_lens,
+                             num_accepted,
+                             out_tokens,
+                             new_lens,
+                             dims->target_seq_stride,
+                             dims->target_row_stride,
+                             dims->draft_seq_stride,
+                             dims->draft_row_stride,
+                             dims->num_draft,
+                             dims->vocab};
+  return verify_draft_impl(a, dims->num_seqs, dims->dtype, static_cast<cudaStream_t>(stream));
+}
+
 int paged_kv_selftest_wait(void* stream) {
   pkv::wait_selftest_kernel<<<1, 32, 0, static_cast<cudaStream_t>(stream)>>>();
   cudaError_t e = cudaGetLastError();
@@ -1195,8 +1318,14 @@ int paged_kv_check_status(void* stream_v) {
   if (word & pkv::kErrSlot) msg += " append slot out of range;";
   if (word & pkv::kErrContext) msg += " context length out of range;";
   if (word & pkv::kErrTimeout) msg += " a bounded wait gave up;";
+  if (word & pkv::kErrNoBlocks) msg += " the free list is too short;";
+  if (word & pkv::kErrFreeList) msg += " the free list's count is out of range;";
+  if (word & pkv::kErrDraft) msg += " a draft token or draft length out of range;";
   if (word & pkv::kErrQuery) msg += " a query value exceeds the fp16 range (fp8 or 4-bit cache path);";
-  return pkv_fail((word & pkv::kErrTimeout) ? PKV_ERR_TIMEOUT : PKV_ERR_OUT_OF_RANGE, msg);
+  return pkv_fail((word & pkv::kErrTimeout)         ? PKV_ERR_TIMEOUT
+                  : word == unsigned(pkv::kErrNoBlocks) ? PKV_ERR_NO_BLOCKS
+                                                        : PKV_ERR_OUT_OF_RANGE,
+                  msg);
 }
 
 const char* paged_kv_last_error(void) { return pkv_error_slot().c_str(); }

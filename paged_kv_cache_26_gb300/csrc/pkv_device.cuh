@@ -16,6 +16,9 @@ enum : unsigned {
   kErrContext = 4u,   // a context length < 0 or longer than its block table
   kErrTimeout = 8u,   // a bounded wait gave up
   kErrQuery = 16u,    // E4M3 and 4-bit pools: a query value beyond the fp16 range
+  kErrNoBlocks = 32u, // table resize: more blocks wanted than the free list holds
+  kErrFreeList = 64u, // table resize: the free list's count is outside the list
+  kErrDraft = 128u,   // draft verification: a token or a draft length out of range
 };
 
 // A wait that has not finished after this long is treated as lost.
