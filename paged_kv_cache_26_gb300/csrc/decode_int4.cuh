@@ -1,0 +1,776 @@
+// Decode attention over a 4-bit pool (sm_103a): one persistent CTA per SM on the
+// partition of the (sequence, KV head, block) space that decode_persistent_kernel
+// uses, the same early reads before the grid wait, and the same pieces for
+// merge_persistent_kernel.
+//
+// A token is a quarter of a bf16 pool's bytes, so at the same bandwidth a warp
+// has a quarter of the instructions per token.  What the kernel does about it:
+//   * a stage is up to four blocks of one unit, described when a window of 32
+//     table entries is read (all lanes at once);
+//   * codes are multiplied without a conversion (WarpAttnInt4);
+//   * the softmax step covers a stage and mostly needs no cross-lane work.
+#pragma once
+
+#include "int4_cache.cuh"
+#include "paged_kv_kernels.cuh"
+
+namespace pkv {
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// d += A * B and d = A * B in fp16 with fp32 accumulation.  Not volatile: the
+// compiler may interleave the independent chains.
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// ===================================================================== warp math
+
+// One warp's attention state for one (sequence, KV head) unit over 4-bit tiles.
+//
+// Codes go to the tensor cores without a conversion: a code masked out of its
+// word in place, c or 16 c in the low bits of a 16-bit half, is the float16
+// subnormal c * 2^-24 or c * 2^-20, which mma.sync multiplies exactly.  Eight
+// codes cost one shift and four ANDs.
+//   scores:  q . K_t = s_t (q . c_t) + m_t sum(q)            (float32, per token)
+//   output:  sum_t p_t V_t = R sum_t P_t c_t + sum_t p_t m_t,  P_t = p_t s_t / R
+// P is rounded to float16; R is a power of two near the largest scale met so
+// far, so that small scales keep their bits.  The rounding must act on c - 7.5
+// and not on c, whose common part is several times the value: with a = sum of
+// the rounded P (one more mma, against ones),
+//   R sum P_t c_t + sum p_t m_t = R [sum P_t c_t - 7.5 a] + sum p_t (m_t + 7.5 s_t).
+// The bracket is formed every kFlushBlocks blocks (flush), which also keeps
+// the accumulators at the output's size: an accumulator that carried 7.5 a
+// over a long context would lose the output's low bits to it.
+//
+// Neither the softmax reference m nor R need be the maximum: m moves only when
+// a score exceeds it by more than kSlack, R when a scale exceeds 2^kScaleSlack R.
+// P then stays below 2^(kSlack + kScaleSlack + 1), within float16's 65504, and
+// float32 sums do not mind, so most steps take one vote and no shuffles or
+// rescaling.
+//
+// Lane (gid = lane/4, c = lane%4): scores of tokens gid, gid + 8 and heads 2c,
+// 2c + 1 as in WarpAttn; O^T entries of dims [G gid, G gid + G), G = D/8.
+template <typename T, int D>
+struct WarpAttnInt4 {
+  using Tile = Int4Tile<D>;
+  static constexpr int kWords = D / 32;  // 32-bit words of codes per lane and row
+  static constexpr int kFlushBlocks = 64;
+  static constexpr float kSlack = 8.f;
+  static constexpr float kScaleSlack = 6.f;
+  static constexpr float kTiny = 5.9604644775390625e-8f;  // 2^-24, the smallest float16 scale
+  uint32_t qf[4 * kWords];
+  float acc[D / 16][4];
+  float ones[4];         // sum of rounded P since the last flush (heads 2c, 2c + 1; twice)
+  float m0, m1, l0, l1;  // softmax reference (log2 units) and sum of p
+  float b0, b1;          // sum of p (m + 7.5 s)
+  float qs0, qs1;        // scale_log2 * sum(q)
+  float ref, inv_ref;    // R and 1 / R
+  int since_flush;       // blocks; -1 before the first step
+
+  __device__ __forceinline__ void reset() {
+    m0 = m1 = l0 = l1 = b0 = b1 = 0.f;
+    ref = kTiny;
+    inv_ref = 16777216.f;
+    since_flush = -1;
+    ones[0] = ones[1] = ones[2] = ones[3] = 0.f;
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+  }
+
+  // Entries [(D/4) c, (D/4) (c + 1)) of query row gid as float16 in the order
+  // the masked K words pair them; a bf16 query beyond the float16 range is
+  // flagged (kErrQuery).  Word w holds dims d0..d7: registers (d0,d4), (d2,d6)
+  // meet the masks of factor 1, (d1,d5), (d3,d7) those of factor 16.
+  __device__ __forceinline__ void load_q(const T* q_group, int group, float scale_log2, int lane) {
+    const int gid = lane >> 2, c = lane & 3;
+    bool big = false;
+    float sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWords; ++w) {
+      const uint4 raw = gid < group ? __ldg(reinterpret_cast<const uint4*>(q_group + gid * D + (D / 4) * c) + w)
+                                    : make_uint4(0, 0, 0, 0);
+      uint32_t h[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 f = unpack2<T>(word_of(raw, i));
+        if constexpr (MmaKind<T>::kBf16) {
+          big |= fabsf(f.x) > kF16Max || fabsf(f.y) > kF16Max;
+          h[i] = pack2<__half>(f.x, f.y);
+          const float2 g = unpack2<__half>(h[i]);
+          sum += g.x + g.y;
+        } else {
+          h[i] = word_of(raw, i);
+          sum += f.x + f.y;
+        }
+      }
+      qf[4 * w] = __byte_perm(h[0], h[2], 0x5410);
+      qf[4 * w + 1] = __byte_perm(h[1], h[3], 0x5410);
+      qf[4 * w + 2] = __byte_perm(h[0], h[2], 0x7632);
+      qf[4 * w + 3] = __byte_perm(h[1], h[3], 0x7632);
+    }
+    if (__any_sync(0xffffffffu, big) && lane == 0) flag_error(kErrQuery);
+    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+    qs0 = scale_log2 * __shfl_sync(0xffffffffu, sum, 8 * c);
+    qs1 = scale_log2 * __shfl_sync(0xffffffffu, sum, 8 * c + 4);
+  }
+
+  __device__ __forceinline__ static void load_words(const uint8_t* p, uint32_t (&w)[kWords]) {
+    if constexpr (kWords == 4) {
+      const uint4 v = *reinterpret_cast<const uint4*>(p);
+      w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    } else {
+      const uint2 v = *reinterpret_cast<const uint2*>(p);
+      w[0] = v.x, w[1] = v.y;
+    }
+  }
+
+  static constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
+
+  // 2^-24 (q . c) of tokens gid (x[.][0..1]) and gid + 8 (x[.][2..3]), heads 2c
+  // and 2c + 1, of NB blocks' K tiles (2 * kBytes apart): 2 NB independent mma
+  // chains, interleaved.
+  template <int NB>
+  __device__ __forceinline__ void dots(const uint8_t* ks, int lane, float (&x)[NB][4]) const {
+    float t[NB][4];
+    uint32_t wa[NB][kWords], wb[NB][kWords];
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      load_words(ks + i * 2 * Tile::kBytes + lane * (D / 8), wa[i]);                         // row gid, quarter c
+      load_words(ks + i * 2 * Tile::kBytes + Tile::kCodeBytes / 2 + lane * (D / 8), wb[i]);  // row gid + 8
+    }
+#pragma unroll
+    for (int w = 0; w < kWords; ++w) {
+#pragma unroll
+      for (int i = 0; i < NB; ++i) {
+        const uint32_t a = wa[i][w], b = wb[i][w], a8 = a >> 8, b8 = b >> 8;
+        if (w == 0) {
+          mma_f16_first(x[i], a & kLow, b & kLow, a8 & kLow, b8 & kLow, qf[0], qf[1]);
+          mma_f16_first(t[i], a & kHigh, b & kHigh, a8 & kHigh, b8 & kHigh, qf[2], qf[3]);
+        } else {
+          mma_f16(x[i], a & kLow, b & kLow, a8 & kLow, b8 & kLow, qf[4 * w], qf[4 * w + 1]);
+          mma_f16(t[i], a & kHigh, b & kHigh, a8 & kHigh, b8 & kHigh, qf[4 * w + 2], qf[4 * w + 3]);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NB; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[i][k] = fmaf(t[i][k], 0.0625f, x[i][k]);
+  }
+
+  // acc += V^T P^T for one tile: m-tile 2w + h holds dims 4w + h (rows gid) and
+  // 4w + h + 2 (rows gid + 8) of the lane's G, times 2^-24 (h = 0) or 2^-20.
+  __device__ __forceinline__ void pv(const uint8_t* vs, uint32_t p0, uint32_t p1, int lane) {
+    uint32_t x[kWords], y[kWords];
+    load_words(vs + lane * (D / 8), x);                         // tokens 2c, 2c + 1
+    load_words(vs + Tile::kCodeBytes / 2 + lane * (D / 8), y);  // tokens 2c + 8, 2c + 9
+#pragma unroll
+    for (int w = 0; w < kWords; ++w) {
+      const uint32_t x8 = x[w] >> 8, y8 = y[w] >> 8;
+      mma_f16(acc[2 * w], x[w] & kLow, x8 & kLow, y[w] & kLow, y8 & kLow, p0, p1);
+      mma_f16(acc[2 * w + 1], x[w] & kHigh, x8 & kHigh, y[w] & kHigh, y8 & kHigh, p0, p1);
+    }
+  }
+
+  // Sum over the lanes that share c.
+  __device__ __forceinline__ static float sum_gid(float v) {
+#pragma unroll
+    for (int o = 4; o <= 16; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+  }
+
+  __device__ __forceinline__ void flush() {
+    const float f0 = ones[0] * (7.5f * kTiny), f1 = ones[1] * (7.5f * kTiny);
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {
+      const float u = i & 1 ? -16.f : -1.f;
+      acc[i][0] = fmaf(u, f0, acc[i][0]);
+      acc[i][1] = fmaf(u, f1, acc[i][1]);
+      acc[i][2] = fmaf(u, f0, acc[i][2]);
+      acc[i][3] = fmaf(u, f1, acc[i][3]);
+    }
+    ones[0] = ones[1] = ones[2] = ones[3] = 0.f;
+    since_flush = 0;
+  }
+
+  // Move the softmax reference by what covers d0, d1 (this lane's largest
+  // scores less the reference) and R to cover smax; returns in d0, d1 how far
+  // the reference went up.  What was summed so far is rescaled.
+  __device__ __forceinline__ void rescale(float& d0, float& d1, float smax) {
+#pragma unroll
+    for (int o = 4; o <= 16; o <<= 1) {
+      d0 = fmaxf(d0, __shfl_xor_sync(0xffffffffu, d0, o));
+      d1 = fmaxf(d1, __shfl_xor_sync(0xffffffffu, d1, o));
+    }
+    // The largest scale's exponent (the bits of floats >= 0 order as they do).
+    const float r_new = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(smax)) & 0x7f800000u);
+    if (since_flush >= 0) {  // else: the first step, nothing summed yet, any reference will do
+      d0 = fmaxf(d0, 0.f);
+      d1 = fmaxf(d1, 0.f);
+    }
+    m0 += d0;
+    m1 += d1;
+    const float al0 = exp2_approx(-d0), al1 = exp2_approx(-d1);
+    float f = 1.f;
+    if (r_new > ref) {
+      f = ref / r_new;
+      ref = r_new;
+      inv_ref = 1.f / r_new;  // exact: powers of two
+    }
+    if (since_flush >= 0) {
+      const float g0 = al0 * f, g1 = al1 * f;
+      l0 *= al0;
+      l1 *= al1;
+      b0 *= al0;
+      b1 *= al1;
+      ones[0] *= g0;
+      ones[1] *= g1;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        acc[i][0] *= g0;
+        acc[i][1] *= g1;
+        acc[i][2] *= g0;
+        acc[i][3] *= g1;
+      }
+    } else {
+      since_flush = 0;
+    }
+  }
+
+  // One softmax step over NB consecutive blocks of one unit, whose (K tile, V
+  // tile) pairs lie back to back at `stage`.  MASK: only the first `valid` (1..16
+  // NB) tokens belong to the context; pairs and codes of the slots behind them
+  // may hold anything, their scores and scales are replaced.
+  template <int NB, bool MASK>
+  __device__ __forceinline__ void step(const uint8_t* stage, int valid, float scale_log2, int lane) {
+    const int gid = lane >> 2;
+    const float k_mul = scale_log2 * 16777216.f;  // 2^24
+    float x[NB][4], sv[NB][2], mv[NB][2];         // scores less the reference; V's scales and minima
+    float d0 = -INFINITY, d1 = -INFINITY, smax = 0.f;
+    if constexpr (NB % 2 == 0) {
+#pragma unroll
+      for (int i = 0; i < NB; i += 2) dots<2>(stage + i * 2 * Tile::kBytes, lane, reinterpret_cast<float(&)[2][4]>(x[i]));
+    } else {
+      dots<NB>(stage, lane, x);
+    }
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      const uint8_t* ks = stage + i * 2 * Tile::kBytes;
+      const uint32_t* km = reinterpret_cast<const uint32_t*>(ks + Tile::kCodeBytes) + gid;
+      const uint32_t* vm = reinterpret_cast<const uint32_t*>(ks + Tile::kBytes + Tile::kCodeBytes) + gid;
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const float2 k = unpack2<__half>(km[8 * r]), v = unpack2<__half>(vm[8 * r]);
+        const float sk = k.x * k_mul;
+        x[i][2 * r] = fmaf(sk, x[i][2 * r], fmaf(k.y, qs0, -m0));
+        x[i][2 * r + 1] = fmaf(sk, x[i][2 * r + 1], fmaf(k.y, qs1, -m1));
+        sv[i][r] = v.x;
+        mv[i][r] = v.y;
+        if (MASK && 16 * i + 8 * r + gid >= valid) {
+          x[i][2 * r] = x[i][2 * r + 1] = -INFINITY;
+          sv[i][r] = mv[i][r] = 0.f;
+        }
+        d0 = fmaxf(d0, x[i][2 * r]);
+        d1 = fmaxf(d1, x[i][2 * r + 1]);
+        smax = fmaxf(smax, fabsf(sv[i][r]));
+      }
+    }
+    constexpr float kScaleLimit = 64.f;  // 2^kScaleSlack
+    if (__any_sync(0xffffffffu, fmaxf(d0, d1) > kSlack || smax > kScaleLimit * ref || since_flush < 0)) {
+      rescale(d0, d1, smax);
+#pragma unroll
+      for (int i = 0; i < NB; ++i) {
+        x[i][0] -= d0;
+        x[i][1] -= d1;
+        x[i][2] -= d0;
+        x[i][3] -= d1;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      uint32_t p[2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const float e0 = exp2_approx(x[i][2 * r]), e1 = exp2_approx(x[i][2 * r + 1]);
+        const float s = sv[i][r] * inv_ref, mid = fmaf(7.5f, sv[i][r], mv[i][r]);
+        l0 += e0;
+        l1 += e1;
+        b0 = fmaf(e0, mid, b0);
+        b1 = fmaf(e1, mid, b1);
+        p[r] = pack2<__half>(e0 * s, e1 * s);
+      }
+      p[0] = movmatrix_trans(p[0]);
+      p[1] = movmatrix_trans(p[1]);
+      mma_f16(ones, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u, p[0], p[1]);
+      pv(stage + (2 * i + 1) * Tile::kBytes, p[0], p[1], lane);
+    }
+    since_flush += NB;
+    if (since_flush >= kFlushBlocks) flush();
+  }
+
+  // n (1..NB) consecutive blocks of a stage: whole stages as one step, a unit's
+  // or segment's last blocks one by one.
+  template <int NB, int STEP>
+  __device__ __forceinline__ void blocks(const uint8_t* stage, int n, int valid, float scale_log2, int lane) {
+    if (valid == 16 * NB) {
+#pragma unroll
+      for (int i = 0; i < NB; i += STEP) step<STEP, false>(stage + i * 2 * Tile::kBytes, valid, scale_log2, lane);
+    } else {
+#pragma unroll 1
+      for (int i = 0; i < n; ++i) step<1, true>(stage + i * 2 * Tile::kBytes, valid - 16 * i, scale_log2, lane);
+    }
+  }
+
+  __device__ __forceinline__ void finish_sums() {
+    flush();
+    l0 = sum_gid(l0);
+    l1 = sum_gid(l1);
+    b0 = sum_gid(b0);
+    b1 = sum_gid(b1);
+  }
+
+  // Entries chunk_dim(lane, k) .. + 7 of head 2c + e, scaled by `mul`.
+  __device__ __forceinline__ void chunk_values(int e, int k, float mul, float (&v)[8]) const {
+    const float f = ref * 16777216.f, b = e ? b1 : b0;
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      const float(&even)[4] = acc[4 * k + 2 * w];
+      const float(&odd)[4] = acc[4 * k + 2 * w + 1];
+      v[4 * w] = fmaf(even[e], f, b) * mul;
+      v[4 * w + 1] = fmaf(odd[e], 0.0625f * f, b) * mul;
+      v[4 * w + 2] = fmaf(even[2 + e], f, b) * mul;
+      v[4 * w + 3] = fmaf(odd[2 + e], 0.0625f * f, b) * mul;
+    }
+  }
+  __device__ __forceinline__ static int chunk_dim(int lane, int k) { return (D / 8) * (lane >> 2) + 8 * k; }
+  static constexpr int kChunks = D / 64;
+};
+
+// ===================================================================== kernel
+
+// A ring of kStages stages of up to kBlocksPerStage blocks per warp.  With the
+// fused append, a unit's last stage holds a block less at most, and the
+// appended token's K and V rows (fp16/bf16) take the last block's place.
+template <int D>
+struct Int4Shape {
+  static constexpr int kWarps = 12;
+  static constexpr int kBlocksPerStage = 4;
+  static constexpr int kStepBlocks = 4;  // per softmax step
+  static constexpr int kStages = 2;
+  static constexpr int kBlockBytes = 2 * Int4Tile<D>::kBytes;  // K and V tile
+  static constexpr int kStageBytes = kBlocksPerStage * kBlockBytes;
+  static constexpr int kRingBytes = kWarps * kStages * kStageBytes;
+};
+
+// Dynamic shared memory: [ring][prefix P[B+1]][context ctx[B]].
+template <int D>
+constexpr size_t int4_smem_bytes(int num_seqs) {
+  return Int4Shape<D>::kRingBytes + (2 * static_cast<size_t>(num_seqs) + 1) * 4 + 128;
+}
+constexpr int kInt4MaxSeqs = 2048;
+// A 4-bit block counts as a quarter of one in the partition's thresholds: a
+// share's tail is handed out dynamically from 192 blocks on.  (8 x 32768 tokens,
+// 72 blocks a share: 68.7 us with thresholds in blocks, 58.2 us so; 256
+// sequences with a long tail of lengths, 112 blocks: 114 and 109 us.)
+constexpr int kInt4ShareUnit = 4;
+static_assert(int4_smem_bytes<128>(kInt4MaxSeqs) + 1536 <= 232448, "227 KB of shared memory, 1.5 KB kept for static");
+
+// What a stage holds (written when it is issued, read when it is consumed).
+struct StageInfo {
+  static constexpr int kValidBits = 127;      // tokens of the context in it, 1..64
+  static constexpr int kUnitStart = 1 << 7;   // its first block is the unit's first
+  static constexpr int kUnitEnd = 1 << 8;     // its last block is the unit's last
+  static constexpr int kSegStart = 1 << 9;    // the same for the segment
+  static constexpr int kSegEnd = 1 << 10;
+  static constexpr int kCountShift = 11;      // blocks
+};
+
+template <typename T, int D>
+__global__ void __maxnreg__(168) decode_int4_kernel(const DecodeArgs a) {
+  using Tile = Int4Tile<D>;
+  using Shape = Int4Shape<D>;
+  using Attn = WarpAttnInt4<T, D>;
+  constexpr int NW = Shape::kWarps, SW = Shape::kStages, NB = Shape::kBlocksPerStage;
+  constexpr int kNewRowBytes = D * 2;  // one appended token's K (or V) row for one KV head (fp16/bf16)
+  constexpr int kNewRows = (NB - 1) * Shape::kBlockBytes;  // where they lie in a unit's last stage
+  static_assert(2 * kNewRowBytes <= Shape::kBlockBytes, "the appended rows fit one block");
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t full_bar[NW][SW];
+  __shared__ int4 s_desc[NW][SW];  // per stage: sequence, KV head, StageInfo, segment id
+  __shared__ int s_prow[NW][SW];   // per stage: pool row of its last block (the fused append's target)
+  __shared__ int s_warp_sum[NW];
+
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
+  int* s_P = reinterpret_cast<int*>(ring + Shape::kRingBytes);
+  int* s_ctx = s_P + a.num_seqs + 1;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int B = a.num_seqs, Hkv = a.num_kv_heads, g = a.group;
+  const bool fused_append = a.k_new != nullptr;
+
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (lane == 0) {
+    for (int s = 0; s < SW; ++s) mbar_init(smem_u32(&full_bar[warp][s]), 1);
+    fence_mbar_init();
+  }
+  // Lengths and tables read before the grid wait are a guess that is checked
+  // after it, as in decode_persistent_kernel.
+  context_prefix(a, a.pre_context_lens ? a.pre_context_lens : a.context_lens, s_P, s_ctx, s_warp_sum, NW * 32,
+                 !a.recheck && blockIdx.x == 0);
+
+  Partition part(Hkv * s_P[B], gridDim.x * NW, a.share_unit);
+  const int gw = blockIdx.x * NW + warp;
+
+  // Sequence b, KV head kvh and block j of flattened block f: units are
+  // ordered (b, kvh) and unit (b, kvh) holds blocks [Hkv*P[b] + kvh*nb, +nb).
+  auto locate = [&](int f, int& b, int& kvh, int& j, int& nb) {
+    int lo = 0, hi = B - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (Hkv * s_P[mid] <= f) lo = mid; else hi = mid - 1;
+    }
+    b = lo;
+    nb = (s_ctx[b] + kBlockSize - 1) / kBlockSize;
+    const int rem = f - Hkv * s_P[b];
+    kvh = rem / nb;
+    j = rem - kvh * nb;
+  };
+
+  uint8_t* wring = ring + warp * SW * Shape::kStageBytes;
+  const uint64_t policy = l2_evict_first_policy();
+
+  const int32_t* tables = a.pre_block_tables ? a.pre_block_tables : a.block_tables;
+  bool after_wait = !a.recheck;  // block ids are flagged only from values known to be final
+
+  // ---- issue side: current segment [seg_s, seg_e) and a 32-block window of it,
+  // lane i describing block win_s + i.  The window is cut into stages at the
+  // unit borders and every NB blocks (and before a unit's last block where the
+  // appended rows would find no room): lane i's block belongs to stage
+  // wstage, and the first lane of a stage holds its description.
+  int seg, seg_s, seg_e;
+  int win_s, win_e, ip;              // window, and the first block not yet issued
+  int stage_i = 0, stages = 0;       // next stage of the window to issue, and how many it has
+  int wb = -1, wkvh = 0, wj = 0, wphys = -1, wrow = -kBlockSize, wstage = -1, wslot = 0, winfo = 0;
+  bool bad_window = false;           // some block of the window is outside the pool
+  bool more = true;
+  auto fill_window = [&]() {
+    win_s = ip;
+    win_e = min(seg_e, ip + 32);
+    stage_i = 0;
+    wb = -1; wkvh = 0; wj = 0; wphys = -1; wrow = -kBlockSize; wstage = -1; wslot = 0; winfo = 0;
+    const int n = win_e - win_s;
+    const bool in = lane < n;
+    int nb = 0;
+    if (in) {
+      locate(win_s + lane, wb, wkvh, wj, nb);
+      const int32_t* entry = tables + static_cast<int64_t>(wb) * a.max_blocks + wj;
+      wphys = __ldcg(entry);
+      if (wj == 0 || lane == 0)  // a unit starts here: bring its query rows into L2
+        prefetch_l2_bulk(static_cast<const T*>(a.q) + (static_cast<int64_t>(wb) * Hkv + wkvh) * g * D,
+                         static_cast<uint32_t>(g * D * sizeof(T)));
+    }
+    const unsigned upto = 0xffffffffu >> (31 - lane);
+    const unsigned runs = __ballot_sync(0xffffffffu, in && (lane == 0 || wj == 0));
+    const int pos = lane - (31 - __clz(runs & upto));  // lane 0 starts a run
+    const unsigned firsts = __ballot_sync(
+        0xffffffffu, in && (pos % NB == 0 || (fused_append && wj == nb - 1 && pos % NB == NB - 1)));
+    stages = __popc(firsts);
+    if (in) {
+      wrow = tile_row(wphys, wkvh, a, after_wait);
+      wstage = __popc(firsts & upto) - 1;
+      wslot = lane - (31 - __clz(firsts & upto));
+      const unsigned later = firsts & ~upto;
+      const int count = (later ? __ffs(later) - 1 : n) - lane;  // blocks of the stage from this one on
+      const int valid = min(count * kBlockSize, s_ctx[wb] - wj * kBlockSize);
+      winfo = valid | (wj == 0 ? StageInfo::kUnitStart : 0) | (wj + count == nb ? StageInfo::kUnitEnd : 0) |
+              (win_s + lane == seg_s ? StageInfo::kSegStart : 0) |
+              (win_s + lane + count == seg_e ? StageInfo::kSegEnd : 0) | count << StageInfo::kCountShift;
+    }
+    bad_window = __any_sync(0xffffffffu, in && wrow < 0);
+  };
+  // Start on this warp's static head segment.
+  auto start_head = [&]() {
+    part.head(gw, seg_s, seg_e);
+    seg = gw;
+    ip = win_s = win_e = seg_s;
+    stage_i = stages = 0;
+    more = true;
+    if (ip < seg_e) fill_window();
+  };
+  // Next window: the rest of this segment, else the next claimed chunk.
+  auto advance = [&]() {
+    ip = win_e;
+    if (ip < seg_e) {
+      fill_window();
+      return;
+    }
+    if (part.nchunks == 0) {  // all head: nothing to claim, the counters stay untouched
+      more = false;
+      return;
+    }
+    while (true) {
+      int q = 0;
+      if (lane == 0) q = atomicAdd(a.sched, 1);
+      q = __shfl_sync(0xffffffffu, q, 0);
+      if (q >= part.num_chunks()) {
+        more = false;
+        // The last warp to run out of chunks resets the counters for the next call.
+        if (lane == 0 && atomicAdd(a.sched + 1, 1) == part.nwarps - 1) {
+          a.sched[0] = 0;
+          a.sched[1] = 0;
+        }
+        return;
+      }
+      int s, e;
+      part.chunk(q / part.nwarps, q % part.nwarps, s, e);
+      if (e > s) {
+        seg = part.nwarps + q;
+        seg_s = s;
+        seg_e = e;
+        ip = s;
+        fill_window();
+        return;
+      }
+    }
+  };
+
+  int issued = 0, consumed = 0;
+  int st_i = 0;            // stage slot the next issue fills
+  int st_c = 0, ph_c = 0;  // stage slot the next consume reads, and its phase parity
+  // Fill free stage slots.  With may_advance false the issue stops at the end
+  // of the current window: no chunk is claimed from the counter.
+  auto issue_stages = [&](bool may_advance) {
+    while (more && issued - consumed < SW) {
+      if (stage_i == stages) {
+        if (!may_advance) break;
+        advance();
+        if (!more) break;
+      }
+      const bool mine = wstage == stage_i;
+      const uint32_t bar = smem_u32(&full_bar[warp][st_i]);
+      uint8_t* stage = wring + st_i * Shape::kStageBytes;
+      uint32_t bytes = (winfo >> StageInfo::kCountShift) * Shape::kBlockBytes;  // of the stage's first lane
+      if (bad_window) {  // blocks outside the pool are not copied: they read as zeros
+        const unsigned missing = __ballot_sync(0xffffffffu, mine && wrow < 0);
+        bytes -= __popc(missing) * Shape::kBlockBytes;
+        for (unsigned left = missing; left; left &= left - 1) {
+          const int slot = __shfl_sync(0xffffffffu, wslot, __ffs(left) - 1);
+          for (int o = lane * 16; o < Shape::kBlockBytes; o += 512)
+            *reinterpret_cast<uint4*>(stage + slot * Shape::kBlockBytes + o) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();  // these writes come before the copies that refill the slot later
+      }
+      __syncwarp();  // every lane is done with this slot's last contents
+      if (mine && wslot == 0) {
+        s_desc[warp][st_i] = make_int4(wb, wkvh, winfo, seg);
+        if (fused_append && (winfo & StageInfo::kUnitEnd)) {
+          // A unit's last stage: the appended token's K and V rows too.
+          const int64_t unit = static_cast<int64_t>(wb) * Hkv + wkvh;
+          mbar_arrive_expect_tx(bar, bytes + 2 * kNewRowBytes);
+          const uint32_t sd = smem_u32(stage + kNewRows);
+          bulk_load(sd, static_cast<const T*>(a.k_new) + unit * D, kNewRowBytes, bar);
+          bulk_load(sd + kNewRowBytes, static_cast<const T*>(a.v_new) + unit * D, kNewRowBytes, bar);
+        } else {
+          mbar_arrive_expect_tx(bar, bytes);
+        }
+      }
+      if (fused_append && mine && winfo >> StageInfo::kCountShift == 1) s_prow[warp][st_i] = wrow;
+      __syncwarp();  // the transaction count is set before the copies that complete it
+      if (mine && wrow >= 0) {
+        const uint32_t dst = smem_u32(stage) + wslot * Shape::kBlockBytes;
+        const int64_t off = static_cast<int64_t>(wrow) * Tile::kRowBytes;
+        bulk_load_hint(dst, static_cast<const uint8_t*>(a.k_cache_w) + off, Tile::kBytes, bar, policy);
+        bulk_load_hint(dst + Tile::kBytes, static_cast<const uint8_t*>(a.v_cache_w) + off, Tile::kBytes, bar, policy);
+      }
+      ++issued;
+      ++stage_i;
+      st_i = st_i + 1 == SW ? 0 : st_i + 1;
+    }
+  };
+  // Wait for the oldest stage in flight (bounded; false on a timeout).
+  auto wait_oldest = [&]() -> bool { return mbar_wait(smem_u32(&full_bar[warp][st_c]), ph_c); };
+  auto next_oldest = [&]() {
+    ++consumed;
+    if (++st_c == SW) {
+      st_c = 0;
+      ph_c ^= 1;
+    }
+  };
+
+  // The head's first window (inputs only), its first stages' tiles prefetched
+  // into L2, then the wait for the previous kernels in the stream.
+  start_head();
+  if (lane < SW * NB && win_s + lane < win_e && wrow >= 0) {
+    const int64_t off = static_cast<int64_t>(wrow) * Tile::kRowBytes;
+    prefetch_l2_bulk(static_cast<const uint8_t*>(a.k_cache_w) + off, Tile::kBytes);
+    prefetch_l2_bulk(static_cast<const uint8_t*>(a.v_cache_w) + off, Tile::kBytes);
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  tables = a.block_tables;
+  after_wait = true;
+
+  // The first stages go out on the prologue's reading of the inputs; then the
+  // lengths and this warp's first window of table entries are read again, and
+  // if either changed the stages are dropped and everything is rebuilt from the
+  // values read now.  With at most kWarpChecked sequences every warp compares
+  // all the lengths itself once its first stage has landed; larger batches
+  // compare at once with a CTA vote.  (decode_persistent_kernel has the reasons.)
+  issue_stages(false);
+  bool ok = true;
+  if (a.recheck) {
+    constexpr int kHeld = 4;
+    constexpr int kWarpChecked = 32 * kHeld;
+    const bool warp_check = B <= kWarpChecked;
+    int held[kHeld];
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k)
+      held[k] = warp_check && lane + 32 * k < B ? __ldcg(a.context_lens + lane + 32 * k) : 0;
+    const bool in_window = win_s + lane < win_e;
+    const int tv = in_window ? __ldcg(tables + static_cast<int64_t>(wb) * a.max_blocks + wj) : wphys;
+    if (warp_check && issued > consumed) ok = wait_oldest();
+    bool lens_changed;
+    if (warp_check) {
+      bool d = false;
+      const bool flag = blockIdx.x == 0 && warp == 0;
+#pragma unroll
+      for (int k = 0; k < kHeld; ++k)
+        if (lane + 32 * k < B) d |= clamp_context(held[k], a.max_blocks, flag) != s_ctx[lane + 32 * k];
+      lens_changed = __any_sync(0xffffffffu, d);
+    } else {
+      lens_changed = context_changed(a, s_ctx, NW * 32, blockIdx.x == 0);
+    }
+    const bool table_changed = __any_sync(0xffffffffu, !lens_changed && in_window && tv != wphys);
+    if (lens_changed || table_changed) {
+      for (; ok && consumed < issued; next_oldest()) ok = wait_oldest();  // dropped, once they have landed
+      if (lens_changed) {
+        // CTA-uniform: every warp takes this branch.  The barrier keeps the
+        // rebuild from changing s_ctx while another warp still compares.
+        __syncthreads();
+        context_prefix_again(a, s_P, s_ctx, s_warp_sum, NW * 32);
+        part = Partition(Hkv * s_P[B], gridDim.x * NW, a.share_unit);
+      }
+      start_head();
+    } else if (in_window) {
+      tile_row(wphys, wkvh, a, true);
+    }
+  }
+
+  // The lengths and block prefix this grid partitioned go to the merge of the
+  // same call, under its tag.
+  if (a.epoch != 0 && blockIdx.x == gridDim.x - 1 && warp == NW - 1) {
+    for (int b = lane; b < B; b += 32) a.pub[1 + b] = s_ctx[b];
+    for (int b = lane; b <= B; b += 32) a.pub[1 + B + b] = s_P[b];
+    __syncwarp();  // the lanes' stores come before lane 0's (cumulative) release
+    if (lane == 0) st_release_gpu(a.pub, static_cast<int32_t>(a.epoch));
+  }
+
+  // ---- consume side
+  Attn at;
+  bool from_start = false;       // the unit's blocks in this segment begin with its first
+  bool seg_first_flush = true;
+  while (ok) {
+    issue_stages(true);
+    if (consumed == issued) break;
+    __syncwarp();  // the descriptions written at issue are visible to the warp
+
+    const int4 dsc = s_desc[warp][st_c];
+    const int b = dsc.x, kvh = dsc.y, info = dsc.z, sid = dsc.w;
+    if (info & (StageInfo::kUnitStart | StageInfo::kSegStart)) {
+      // While the tiles are under way: the query rows (L2), and a fresh state.
+      if (info & StageInfo::kSegStart) seg_first_flush = true;
+      from_start = info & StageInfo::kUnitStart;
+      at.load_q(static_cast<const T*>(a.q) + (static_cast<int64_t>(b) * a.num_q_heads + kvh * g) * D, g, a.scale_log2,
+                lane);
+      at.reset();
+    }
+    if (!wait_oldest()) {  // timed out: flagged
+      ok = false;
+      break;
+    }
+    const int n = info >> StageInfo::kCountShift, valid = info & StageInfo::kValidBits;
+    uint8_t* stage = wring + st_c * Shape::kStageBytes;
+    if (fused_append && (info & StageInfo::kUnitEnd)) {
+      // Append: the context's last token goes into its row of the stage's last
+      // block, in the staged tiles (for this step's attention) and in the pool.
+      // D / 4 lanes quantise a row, four entries each (D = 64: both rows at once).
+      const int r = (valid - 1) % kBlockSize;
+      const int prow = s_prow[warp][st_c];
+      uint8_t* tile = stage + (n - 1) * Shape::kBlockBytes;
+      const uint8_t* sd = stage + kNewRows;
+      constexpr int W = D / 4;
+      const int l = lane % W;
+#pragma unroll
+      for (int i = 0; i < W / 16; ++i) {
+        const bool is_v = W == 32 ? i == 1 : lane >= 16;
+        uint32_t pair;
+        const uint32_t codes =
+            int4_quantise4<T, W>(*reinterpret_cast<const uint2*>(sd + (is_v ? kNewRowBytes : 0) + 8 * l), pair);
+        int4_store4<D>(tile + (is_v ? Tile::kBytes : 0), is_v, r, l, codes, pair);
+        if (prow >= 0)
+          int4_store4<D>(static_cast<uint8_t*>(is_v ? a.v_cache_w : a.k_cache_w) +
+                             static_cast<int64_t>(prow) * Tile::kRowBytes,
+                         is_v, r, l, codes, pair);
+      }
+      fence_proxy_async_smem();  // the patch comes before the copies that refill the slot
+      __syncwarp();
+    }
+    at.template blocks<NB, Shape::kStepBlocks>(stage, n, valid, a.scale_log2, lane);
+    next_oldest();
+
+    if (info & (StageInfo::kUnitEnd | StageInfo::kSegEnd)) {
+      // ---- the unit ends here or the segment does: write it out, or leave a piece for the merge
+      at.finish_sums();
+      const int gid = lane >> 2, c = lane & 3;
+      const bool complete = from_start && (info & StageInfo::kUnitEnd);
+      const int64_t pbase = (static_cast<int64_t>(sid) * 2 + (seg_first_flush ? 0 : 1)) * kMaxGroup;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int h = 2 * c + e;
+        if (h >= g) continue;
+        const float l = e ? at.l1 : at.l0;
+        if (complete) {
+          T* orow = static_cast<T*>(a.out) + (static_cast<int64_t>(b) * a.num_q_heads + kvh * g + h) * D;
+#pragma unroll
+          for (int kk = 0; kk < Attn::kChunks; ++kk) {
+            float v[8];
+            at.chunk_values(e, kk, 1.f / l, v);
+            *reinterpret_cast<uint4*>(orow + Attn::chunk_dim(lane, kk)) = pack8<T>(v);
+          }
+        } else {
+          float* prow = a.part_o + (pbase + h) * D;
+#pragma unroll
+          for (int kk = 0; kk < Attn::kChunks; ++kk) {
+            float v[8];
+            at.chunk_values(e, kk, 1.f / l, v);
+            float4* dst = reinterpret_cast<float4*>(prow + Attn::chunk_dim(lane, kk));
+            dst[0] = make_float4(v[0], v[1], v[2], v[3]);
+            dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+          }
+          if (gid == 0) a.part_lse[pbase + h] = (e ? at.m1 : at.m0) + log2f(l);
+        }
+      }
+      seg_first_flush = false;
+    }
+  }
+  if (!ok && lane == 0) {
+    // A wait gave up: let this warp's copies in flight land before the CTA exits.
+    for (; consumed < issued; next_oldest()) wait_oldest();
+  }
+}
+
+}  // namespace pkv

@@ -15,6 +15,7 @@
 
 #include "paged_kv.h"
 #include "block_copy.cuh"
+#include "decode_int4.cuh"
 #include "host_copy.cuh"
 #include "multi_query.cuh"
 #include "multi_query_tc.cuh"
@@ -161,17 +162,18 @@ struct SplitPlan {
   int32_t split_blocks;   // split kernel: blocks per split
 };
 
+// What a pool holds.
+enum PoolFormat : int { kPool16, kPoolE4M3, kPoolInt4 };
+
 // Largest batch of the persistent kernel: its prefix sums live in shared
 // memory beside the ring (2048 sequences for every pool format built).
 int max_persistent_seqs(const pkv_dims* d, int format) {
-  if (format == pkv::kPoolE4M3) return pkv::persistent_max_seqs<128, pkv::kPoolE4M3>() / 256 * 256;
-  if (format == pkv::kPoolInt4)
-    return d->head_dim == 128 ? pkv::persistent_max_seqs<128, pkv::kPoolInt4>()
-                              : pkv::persistent_max_seqs<64, pkv::kPoolInt4>();
+  if (format == kPoolE4M3) return pkv::persistent_max_seqs<128, true>() / 256 * 256;
+  if (format == kPoolInt4) return pkv::kInt4MaxSeqs;
   return d->head_dim == 128 ? pkv::persistent_max_seqs<128>() : pkv::persistent_max_seqs<64>();
 }
 
-bool persistent_eligible(const pkv_dims* d, int format = pkv::kPool16) {
+bool persistent_eligible(const pkv_dims* d, int format = kPool16) {
   return d->num_seqs <= max_persistent_seqs(d, format) &&
          static_cast<int64_t>(d->num_seqs) * d->num_kv_heads * d->max_blocks_per_seq < (int64_t(1) << 31);
 }
@@ -243,18 +245,27 @@ cudaError_t configure_smem(int bytes) {
   return e;
 }
 
-// Persistent decode + merge.  Both are programmatic dependent launches: each
+// f(T, D) for the value type and head_dim of d.
+template <typename F>
+void with_type_and_dim(const pkv_dims* d, F&& f) {
+  const bool bf16 = d->dtype == PKV_DTYPE_BF16;
+  if (d->head_dim == 128)
+    bf16 ? f(__nv_bfloat16{}, std::integral_constant<int, 128>{}) : f(__half{}, std::integral_constant<int, 128>{});
+  else
+    bf16 ? f(__nv_bfloat16{}, std::integral_constant<int, 64>{}) : f(__half{}, std::integral_constant<int, 64>{});
+}
+
+// Persistent decode (`kern`, of `warps` warps a CTA and smem(B) bytes of dynamic
+// shared memory) + merge.  Both are programmatic dependent launches: each
 // may start while the kernel before it in the stream finishes, and waits
 // in-kernel (griddepcontrol.wait) before touching anything that kernel writes.
-template <typename T, int D, int F>
-int launch_persistent(const CUtensorMap& mk, const CUtensorMap& mv, const pkv::DecodeArgs& args,
-                      const pkv_dims* d, int max_seqs, cudaStream_t stream, bool pdl = true) {
-  using PS = pkv::PersistentShape<D, F>;
-  constexpr auto kern = pkv::decode_persistent_kernel<T, D, F>;
-  cudaError_t e = configure_smem<kern>(static_cast<int>(pkv::persistent_smem_bytes<D, F>(max_seqs)));
-  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(decode_persistent_kernel)");
+template <typename T, int D, auto kern, typename... KernArgs>
+int launch_persistent(int warps, size_t (*smem)(int), const pkv::DecodeArgs& args, const pkv_dims* d, int max_seqs,
+                      cudaStream_t stream, bool pdl, const KernArgs&... kern_args) {
+  cudaError_t e = configure_smem<kern>(static_cast<int>(smem(max_seqs)));
+  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(persistent decode kernel)");
   const int64_t upper_blocks = static_cast<int64_t>(d->num_seqs) * d->num_kv_heads * d->max_blocks_per_seq;
-  int64_t grid = (upper_blocks + PS::kWarps - 1) / PS::kWarps;
+  int64_t grid = (upper_blocks + warps - 1) / warps;
   if (grid > device_sms()) grid = device_sms();
   if (grid < 1) grid = 1;
   cudaLaunchAttribute attr[1];
@@ -262,29 +273,29 @@ int launch_persistent(const CUtensorMap& mk, const CUtensorMap& mv, const pkv::D
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  cfg.blockDim = dim3(PS::kWarps * 32);
-  cfg.dynamicSmemBytes = pkv::persistent_smem_bytes<D, F>(d->num_seqs);
+  cfg.blockDim = dim3(warps * 32);
+  cfg.dynamicSmemBytes = smem(d->num_seqs);
   cfg.stream = stream;
   cfg.attrs = attr;
   // !pdl: the kernel before this one wrote its inputs (block tables, lengths,
   // query), which it reads before griddepcontrol.wait: no early launch.
   cfg.numAttrs = pdl ? 1 : 0;
-  e = cudaLaunchKernelEx(&cfg, kern, mk, mv, args);
-  if (e != cudaSuccess) return cuda_fail(e, "decode_persistent_kernel launch");
+  e = cudaLaunchKernelEx(&cfg, kern, kern_args...);
+  if (e != cudaSuccess) return cuda_fail(e, "persistent decode kernel launch");
   cfg.numAttrs = 1;
   // Long units cut into many pieces (on average 8 or more warp shares per
   // unit): a CTA per row, its warps splitting the row's pieces; otherwise a
   // warp per row (measured: at 7.1 shares, the E4M3 pool at B=32, a warp per
   // row 0.741 against 0.703; at 9.5, bf16 at B=16, a CTA per row 0.784
   // against 0.770).
-  const int32_t nwarps = static_cast<int32_t>(grid) * PS::kWarps;
+  const int32_t nwarps = static_cast<int32_t>(grid) * warps;
   const int64_t units = static_cast<int64_t>(d->num_seqs) * d->num_kv_heads;
   const bool coop = nwarps >= 8 * units;
   // Two or more warp shares per unit on average: rows have many pieces, so
   // fold up to 16 per round trip (fewer registers leave room for more merge
   // CTAs beside the decode grid, which pays when rows are many and short).
   const bool wide = !coop && nwarps >= 2 * units;
-  const int merge_smem = static_cast<int>((2 * static_cast<size_t>(max_persistent_seqs(d, pkv::kPool16)) + 1) * 4);
+  const int merge_smem = static_cast<int>((2 * static_cast<size_t>(max_persistent_seqs(d, kPool16)) + 1) * 4);
   const int rows = d->num_seqs * d->num_q_heads;
   const int rows_per_cta = coop ? 1 : pkv::kMergeWarps;
   cfg.gridDim = dim3(static_cast<unsigned>((rows + rows_per_cta - 1) / rows_per_cta));
@@ -312,7 +323,9 @@ int launch_decode(const CUtensorMap& mk, const CUtensorMap& mv, const pkv::Decod
                   const pkv_dims* d, cudaStream_t stream, bool pdl) {
   using Shape = pkv::TileShape<D>;
   if (plan.persistent)
-    return launch_persistent<T, D, pkv::kPool16>(mk, mv, args, d, max_persistent_seqs(d, pkv::kPool16), stream, pdl);
+    return launch_persistent<T, D, pkv::decode_persistent_kernel<T, D>>(
+        pkv::PersistentShape<D>::kWarps, pkv::persistent_smem_bytes<D>, args, d, max_persistent_seqs(d, kPool16), stream,
+        pdl, mk, mv, args);
   constexpr int kSmem = kStages * Shape::kStageBytes + 1024;
   constexpr auto kern = pkv::decode_split_kernel<T, D, kConsumerWarps, kStages>;
   cudaError_t e = configure_smem<kern>(kSmem);
@@ -345,15 +358,15 @@ int append_at_end_impl(const void* k_new, const void* v_new, const int32_t* bloc
 int decode_impl(const void* q, const void* k_new, const void* v_new, void* k_cache, void* v_cache,
                 const int32_t* block_tables, const int32_t* context_lens, float scale, void* out,
                 int32_t num_splits, void* workspace, size_t workspace_bytes, const pkv_dims* d,
-                cudaStream_t stream, int format = pkv::kPool16, const float* k_scale = nullptr,
+                cudaStream_t stream, int format = kPool16, const float* k_scale = nullptr,
                 const float* v_scale = nullptr, bool pdl = true, const int32_t* pre_lens = nullptr,
                 const int32_t* pre_tables = nullptr, bool recheck = true, bool publish = true) {
   int rc = check_dims(d, true);
   if (rc != PKV_OK) return rc;
-  if (format == pkv::kPoolInt4 && !persistent_eligible(d, format))
+  if (format == kPoolInt4 && !persistent_eligible(d, format))
     return pkv_fail(PKV_ERR_UNSUPPORTED, "4-bit cache: at most " + std::to_string(max_persistent_seqs(d, format)) +
                                              " sequences per call");
-  const bool f8 = format == pkv::kPoolE4M3;
+  const bool f8 = format == kPoolE4M3;
   if (f8) {
     if (d->head_dim != 128) return pkv_fail(PKV_ERR_UNSUPPORTED, "fp8 cache: head_dim must be 128");
     if (!persistent_eligible(d, format))
@@ -389,7 +402,7 @@ int decode_impl(const void* q, const void* k_new, const void* v_new, void* k_cac
     if (rc != PKV_OK) return rc;
   }
   CUtensorMap mk = {}, mv = {};  // 4-bit tiles are loaded by untiled bulk copies
-  if (format != pkv::kPoolInt4) {
+  if (format != kPoolInt4) {
     if ((rc = g_maps.get(k_cache, d, f8, &mk)) != PKV_OK) return rc;
     if ((rc = g_maps.get(v_cache, d, f8, &mv)) != PKV_OK) return rc;
   }
@@ -436,18 +449,27 @@ int decode_impl(const void* q, const void* k_new, const void* v_new, void* k_cac
   args.num_blocks = d->num_blocks;
   args.num_splits = plan.num_splits;
   args.split_blocks = plan.split_blocks;
+  args.share_unit = format == kPoolInt4 ? pkv::kInt4ShareUnit : 1;
 
   const bool bf16 = d->dtype == PKV_DTYPE_BF16;
   const int mx = max_persistent_seqs(d, format);
-  if (f8)
-    return bf16 ? launch_persistent<__nv_bfloat16, 128, pkv::kPoolE4M3>(mk, mv, args, d, mx, stream, pdl)
-                : launch_persistent<__half, 128, pkv::kPoolE4M3>(mk, mv, args, d, mx, stream, pdl);
-  if (format == pkv::kPoolInt4) {
-    if (d->head_dim == 128)
-      return bf16 ? launch_persistent<__nv_bfloat16, 128, pkv::kPoolInt4>(mk, mv, args, d, mx, stream, pdl)
-                  : launch_persistent<__half, 128, pkv::kPoolInt4>(mk, mv, args, d, mx, stream, pdl);
-    return bf16 ? launch_persistent<__nv_bfloat16, 64, pkv::kPoolInt4>(mk, mv, args, d, mx, stream, pdl)
-                : launch_persistent<__half, 64, pkv::kPoolInt4>(mk, mv, args, d, mx, stream, pdl);
+  if (f8) {
+    using PS = pkv::PersistentShape<128, true>;
+    constexpr auto smem = pkv::persistent_smem_bytes<128, true>;
+    return bf16 ? launch_persistent<__nv_bfloat16, 128, pkv::decode_persistent_kernel<__nv_bfloat16, 128, true>>(
+                      PS::kWarps, smem, args, d, mx, stream, pdl, mk, mv, args)
+                : launch_persistent<__half, 128, pkv::decode_persistent_kernel<__half, 128, true>>(
+                      PS::kWarps, smem, args, d, mx, stream, pdl, mk, mv, args);
+  }
+  if (format == kPoolInt4) {
+    int rc4 = PKV_OK;
+    with_type_and_dim(d, [&](auto t, auto dim) {
+      using U = decltype(t);
+      constexpr int D = decltype(dim)::value;
+      rc4 = launch_persistent<U, D, pkv::decode_int4_kernel<U, D>>(pkv::Int4Shape<D>::kWarps, pkv::int4_smem_bytes<D>,
+                                                                  args, d, mx, stream, pdl, args);
+    });
+    return rc4;
   }
   if (d->head_dim == 128)
     return bf16 ? launch_decode<__nv_bfloat16, 128>(mk, mv, args, plan, d, stream, pdl)
@@ -546,16 +568,6 @@ int check_int4_rows(const void* k, const void* v, const int32_t* slot_mapping, i
   if (!aligned(k, 16) || !aligned(v, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(slot_mapping, 4))
     return pkv_fail(PKV_ERR_INVALID_ARG, std::string(what) + ": misaligned pointer (values and caches need 16 bytes)");
   return PKV_OK;
-}
-
-// f(T, D) for the value type and head_dim of d.
-template <typename F>
-void with_type_and_dim(const pkv_dims* d, F&& f) {
-  const bool bf16 = d->dtype == PKV_DTYPE_BF16;
-  if (d->head_dim == 128)
-    bf16 ? f(__nv_bfloat16{}, std::integral_constant<int, 128>{}) : f(__half{}, std::integral_constant<int, 128>{});
-  else
-    bf16 ? f(__nv_bfloat16{}, std::integral_constant<int, 64>{}) : f(__half{}, std::integral_constant<int, 64>{});
 }
 
 int append_int4_impl(const void* k_new, const void* v_new, const int32_t* slot_mapping, int32_t num_tokens,
@@ -1044,7 +1056,7 @@ int step_from_host(const pkv_step_buffers* s, int32_t q_len, void* k_cache, void
     // wrote them), so the early reads need no re-check after the grid wait.
     rc = decode_impl(s->q_dev, s->k_new_dev, s->v_new_dev, k_cache, v_cache, s->block_tables_dev,
                      s->context_lens_dev, scale, s->out_dev, num_splits, workspace, workspace_bytes, d, stream,
-                     k_scale ? pkv::kPoolE4M3 : pkv::kPool16, k_scale, v_scale, early, reinterpret_cast<const int32_t*>(pre_lens),
+                     k_scale ? kPoolE4M3 : kPool16, k_scale, v_scale, early, reinterpret_cast<const int32_t*>(pre_lens),
                      reinterpret_cast<const int32_t*>(pre_tables), pre_lens == nullptr);
   }
   if (rc != PKV_OK) return rc;
@@ -1061,7 +1073,7 @@ int decode_step_host_written(const void* q, const void* k_new, const void* v_new
   if (!k_new || !v_new) return pkv_fail(PKV_ERR_INVALID_ARG, "decode_step: NULL k_new / v_new");
   return decode_impl(q, k_new, v_new, k_cache, v_cache, block_tables, context_lens, scale, out, 0, workspace,
                      workspace_bytes, dims, static_cast<cudaStream_t>(stream),
-                     int4 ? pkv::kPoolInt4 : k_scale ? pkv::kPoolE4M3 : pkv::kPool16, k_scale, v_scale, true, nullptr, nullptr, false);
+                     int4 ? kPoolInt4 : k_scale ? kPoolE4M3 : kPool16, k_scale, v_scale, true, nullptr, nullptr, false);
 }
 
 extern "C" {
@@ -1185,7 +1197,7 @@ int paged_kv_selftest_stale_prologue(const void* q, const void* k_new, const voi
       !aligned(stale_context_lens, 4))
     return pkv_fail(PKV_ERR_INVALID_ARG, "selftest_stale_prologue: stale inputs missing or misaligned");
   return decode_impl(q, k_new, v_new, k_cache, v_cache, block_tables, context_lens, scale, out, 0, workspace,
-                     workspace_bytes, dims, static_cast<cudaStream_t>(stream), pkv::kPool16, nullptr, nullptr, true,
+                     workspace_bytes, dims, static_cast<cudaStream_t>(stream), kPool16, nullptr, nullptr, true,
                      stale_context_lens, stale_block_tables, true, publish != 0);
 }
 
@@ -1202,7 +1214,7 @@ int paged_decode_attention_fp8(const void* q, const void* k_cache, const void* v
                                const pkv_dims* dims, void* stream) {
   return decode_impl(q, nullptr, nullptr, const_cast<void*>(k_cache), const_cast<void*>(v_cache), block_tables,
                      context_lens, scale, out, 0, workspace, workspace_bytes, dims,
-                     static_cast<cudaStream_t>(stream), pkv::kPoolE4M3, k_scale, v_scale);
+                     static_cast<cudaStream_t>(stream), kPoolE4M3, k_scale, v_scale);
 }
 
 int paged_decode_step_fp8(const void* q, const void* k_new, const void* v_new, void* k_cache, void* v_cache,
@@ -1211,7 +1223,7 @@ int paged_decode_step_fp8(const void* q, const void* k_new, const void* v_new, v
                           size_t workspace_bytes, const pkv_dims* dims, void* stream) {
   if (!k_new || !v_new) return pkv_fail(PKV_ERR_INVALID_ARG, "decode_step_fp8: NULL k_new / v_new");
   return decode_impl(q, k_new, v_new, k_cache, v_cache, block_tables, context_lens, scale, out, 0, workspace,
-                     workspace_bytes, dims, static_cast<cudaStream_t>(stream), pkv::kPoolE4M3, k_scale, v_scale);
+                     workspace_bytes, dims, static_cast<cudaStream_t>(stream), kPoolE4M3, k_scale, v_scale);
 }
 
 int paged_kv_append_int4(const void* k_new, const void* v_new, const int32_t* slot_mapping, int32_t num_tokens,
@@ -1231,7 +1243,7 @@ int paged_decode_attention_int4(const void* q, const void* k_cache, const void* 
                                 size_t workspace_bytes, const pkv_dims* dims, void* stream) {
   return decode_impl(q, nullptr, nullptr, const_cast<void*>(k_cache), const_cast<void*>(v_cache), block_tables,
                      context_lens, scale, out, 0, workspace, workspace_bytes, dims,
-                     static_cast<cudaStream_t>(stream), pkv::kPoolInt4);
+                     static_cast<cudaStream_t>(stream), kPoolInt4);
 }
 
 int paged_decode_step_int4(const void* q, const void* k_new, const void* v_new, void* k_cache, void* v_cache,
@@ -1239,7 +1251,7 @@ int paged_decode_step_int4(const void* q, const void* k_new, const void* v_new, 
                            void* workspace, size_t workspace_bytes, const pkv_dims* dims, void* stream) {
   if (!k_new || !v_new) return pkv_fail(PKV_ERR_INVALID_ARG, "decode_step_int4: NULL k_new / v_new");
   return decode_impl(q, k_new, v_new, k_cache, v_cache, block_tables, context_lens, scale, out, 0, workspace,
-                     workspace_bytes, dims, static_cast<cudaStream_t>(stream), pkv::kPoolInt4);
+                     workspace_bytes, dims, static_cast<cudaStream_t>(stream), kPoolInt4);
 }
 
 int paged_kv_append(const void* k_new, const void* v_new, const int32_t* slot_mapping, int32_t num_tokens,

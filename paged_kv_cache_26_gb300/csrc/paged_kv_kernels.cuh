@@ -35,21 +35,13 @@
 // code * scale; design.babushkai.com "GPU推論の内部構造", section "KVキャッシュの
 // 台帳": an FP8 cache halves the bytes per token).  A tile row is then 128
 // bytes for D = 128 and a tile one 2 KB box.
-//
-// 4-bit cache: the same kernels over tiles of 16 * (D/2 + 4) bytes (codes and
-// float16 (scale, minimum) pairs; int4_cache.cuh), each brought in by one
-// untiled bulk copy.
 #pragma once
 
 #include <type_traits>
 
-#include "int4_cache.cuh"
 #include "pkv_device.cuh"
 
 namespace pkv {
-
-// What a pool holds.
-enum PoolFormat : int { kPool16 = 0, kPoolE4M3 = 1, kPoolInt4 = 2 };
 
 constexpr int kBlockSize = 16;
 constexpr int kMaxGroup = 8;  // query heads per KV head served by one mma tile
@@ -598,6 +590,7 @@ struct DecodeArgs {
   int32_t group;              // Hq / Hkv, 1..8
   int32_t max_blocks;
   int32_t num_blocks;
+  int32_t share_unit;         // persistent: blocks that the partition's thresholds count as one
   int32_t num_splits;         // split path only
   int32_t split_blocks;       // split path only
 };
@@ -628,23 +621,22 @@ __device__ __forceinline__ int tile_row(int phys, int kvh, const DecodeArgs& a, 
 
 // Byte geometry of one (block, KV head) K or V tile: 16 rows of D elements
 // (2 bytes for fp16 / bf16, 1 for E4M3), loaded as 128-byte-wide TMA boxes of
-// 16 rows (2 KB each) with the 128-byte swizzle; or a 4-bit tile (D/2 + 4
-// bytes a row), loaded by one bulk copy.
-template <int D, int F>
+// 16 rows (2 KB each) with the 128-byte swizzle.
+template <int D, bool F8>
 struct KvTile {
-  static constexpr int kRowBytes = F == kPoolInt4 ? Int4Tile<D>::kRowBytes : F == kPoolE4M3 ? D : 2 * D;
+  static constexpr int kRowBytes = F8 ? D : 2 * D;
   static constexpr int kBoxes = kRowBytes / 128;
-  static constexpr int kBoxElems = F == kPoolE4M3 ? 128 : 64;
+  static constexpr int kBoxElems = F8 ? 128 : 64;
   static constexpr int kTileBytes = kBlockSize * kRowBytes;
   static constexpr int kStageBytes = 2 * kTileBytes;
 };
 
 // TMA loads of one block's K and V tiles into a stage, completing on `bar`
 // (whose transaction count the caller has set).
-template <int D, int F = kPool16>
+template <int D, bool F8 = false>
 __device__ __forceinline__ void issue_tiles(uint32_t stage, uint32_t bar, const CUtensorMap* mk,
                                             const CUtensorMap* mv, int row, uint64_t policy) {
-  using Tile = KvTile<D, F>;
+  using Tile = KvTile<D, F8>;
 #pragma unroll
   for (int bx = 0; bx < Tile::kBoxes; ++bx) {
     tma_load_2d(stage + bx * 2048, mk, bx * Tile::kBoxElems, row, bar, policy);
@@ -652,11 +644,11 @@ __device__ __forceinline__ void issue_tiles(uint32_t stage, uint32_t bar, const 
   }
 }
 
-template <int D, int F = kPool16>
+template <int D, bool F8 = false>
 __device__ __forceinline__ void issue_block(uint32_t stage, uint32_t bar, const CUtensorMap* mk,
                                             const CUtensorMap* mv, int row, uint64_t policy) {
-  mbar_arrive_expect_tx(bar, KvTile<D, F>::kStageBytes);
-  issue_tiles<D, F>(stage, bar, mk, mv, row, policy);
+  mbar_arrive_expect_tx(bar, KvTile<D, F8>::kStageBytes);
+  issue_tiles<D, F8>(stage, bar, mk, mv, row, policy);
 }
 
 // ===================================================================== persistent kernel
@@ -665,33 +657,31 @@ __device__ __forceinline__ void issue_block(uint32_t stage, uint32_t bar, const 
 // stages of 8 KB for D = 128, 6 of 4 KB for D = 64) or, for E4M3, two
 // consecutive blocks of one unit (3 stages of 2 x 4 KB): 32 tokens per softmax
 // step halve the per-block bookkeeping and give each warp two independent
-// score chains.  4-bit pools: stages of two blocks too (2 x 2176 bytes for
-// D = 128), three per warp.
-template <int D, int F = kPool16>
+// score chains.
+template <int D, bool F8 = false>
 struct PersistentShape {
-  static constexpr int kWarps = F != kPool16 ? 12 : 8;
-  static constexpr int kBlocksPerStage = F != kPool16 ? 2 : 1;
-  static constexpr int kStageBytes = kBlocksPerStage * KvTile<D, F>::kStageBytes;
-  static constexpr int kStages =  // per warp
-      F == kPoolInt4 ? 3 : (F == kPoolE4M3 ? 16384 : 24576) / kStageBytes;
+  static constexpr int kWarps = F8 ? 12 : 8;
+  static constexpr int kBlocksPerStage = F8 ? 2 : 1;
+  static constexpr int kStageBytes = kBlocksPerStage * KvTile<D, F8>::kStageBytes;
+  static constexpr int kStages = (F8 ? 16384 : 24576) / kStageBytes;  // per warp
   static constexpr int kRingBytes = kWarps * kStages * kStageBytes;
 };
 constexpr int kMaxPersistentWarps = 12;  // sizes the workspace
 
 // Dynamic shared memory: [ring][appended-token rows (fp16/bf16, K and V)]
 // [prefix P[B+1]][context ctx[B]] (+1 KB alignment slack).
-template <int D, int F = kPool16>
+template <int D, bool F8 = false>
 constexpr size_t persistent_smem_bytes(int num_seqs) {
-  return PersistentShape<D, F>::kRingBytes +
-         PersistentShape<D, F>::kWarps * PersistentShape<D, F>::kStages * 4 * D +
+  return PersistentShape<D, F8>::kRingBytes +
+         PersistentShape<D, F8>::kWarps * PersistentShape<D, F8>::kStages * 4 * D +
          (2 * static_cast<size_t>(num_seqs) + 1) * 4 + 1024;
 }
 
 // Largest batch whose prefix arrays fit beside the ring in 227 KB of shared
 // memory (1.5 KB kept for the static arrays, which take 1.2 KB), at most 2048.
-template <int D, int F = kPool16>
+template <int D, bool F8 = false>
 constexpr int persistent_max_seqs() {
-  constexpr long long room = 232448LL - 1536 - static_cast<long long>(persistent_smem_bytes<D, F>(0));
+  constexpr long long room = 232448LL - 1536 - static_cast<long long>(persistent_smem_bytes<D, F8>(0));
   return room / 8 < 2048 ? static_cast<int>(room / 8) : 2048;
 }
 
@@ -706,10 +696,11 @@ constexpr int persistent_max_seqs() {
 // boundary inside a unit leaves a piece for the merge, and fewer, larger
 // chunks keep those few where a share is short.  Shares under
 // kMinDynamicShare blocks are all head, with nothing to claim (the chunks
-// would be too small to pay for their hand-over).  Chunk k of share w is
-// segment nwarps + k * nwarps + w.  Every segment is a contiguous block
+// would be too small to pay for their hand-over).  The thresholds are in units
+// of `share_unit` blocks: a block of a pool with fewer bits is less work.
+// Chunk k of share w is segment nwarps + k * nwarps + w.  Every segment is a contiguous block
 // range; the decode and merge kernels derive all boundaries from
-// (total, nwarps) alone.
+// (total, nwarps, share_unit) alone.
 struct Partition {
   static constexpr int kMaxTailChunks = 4;
   static constexpr int kMinDynamicShare = 48;
@@ -717,9 +708,12 @@ struct Partition {
   static constexpr int kFourChunkShare = 200;
   int total, nwarps, R, nchunks;
 
-  __device__ __forceinline__ Partition(int total_, int nwarps_)
+  __device__ __forceinline__ Partition(int total_, int nwarps_, int share_unit)
       : total(total_), nwarps(nwarps_), R(total_ > 0 ? (total_ + nwarps_ - 1) / nwarps_ : 1),
-        nchunks(R < kMinDynamicShare ? 0 : R < kThreeChunkShare ? 2 : R < kFourChunkShare ? 3 : 4) {}
+        nchunks(R < kMinDynamicShare * share_unit   ? 0
+                : R < kThreeChunkShare * share_unit ? 2
+                : R < kFourChunkShare * share_unit  ? 3
+                                                    : 4) {}
   // Cumulative tenths of the tail before chunk k.
   __device__ __forceinline__ int cum(int k) const {
     if (nchunks == 2) return k == 0 ? 0 : k == 1 ? 8 : 10;
@@ -808,20 +802,18 @@ __device__ __forceinline__ bool context_changed(const DecodeArgs& a, const int* 
   return __syncthreads_or(diff) != 0;
 }
 
-// F: what the pool holds (kPoolE4M3: D = 128 only).  With codes the query,
-// output and the appended token's K/V stay fp16/bf16 and the append quantises
-// in-kernel.  Registers are capped so that two 4-warp merge CTAs (64 registers
-// a thread) fit beside a decode CTA (8 warps x 192 registers) on an SM.
-template <typename T, int D, int F = kPool16>
-__global__ void __maxnreg__(F != kPool16 ? 168 : 192)
+// F8: the pool holds E4M3 codes (D = 128 only); the query, output and the
+// appended token's K/V stay fp16/bf16 and the append quantises in-kernel.
+// Registers are capped so that two 4-warp merge CTAs (64 registers a thread)
+// fit beside a decode CTA (8 warps x 192 registers) on an SM.
+template <typename T, int D, bool F8 = false>
+__global__ void __maxnreg__(F8 ? 168 : 192)
     decode_persistent_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                              const DecodeArgs a) {
-  static_assert(F != kPoolE4M3 || D == 128, "the E4M3 path is built for head_dim 128");
-  constexpr bool F8 = F == kPoolE4M3;
-  constexpr bool I4 = F == kPoolInt4;
-  using Tile = KvTile<D, F>;
-  using Shape = PersistentShape<D, F>;
-  using Attn = std::conditional_t<I4, WarpAttnInt4<T, D>, std::conditional_t<F8, WarpAttnE4M3<T>, WarpAttn<T, D>>>;
+  static_assert(!F8 || D == 128, "the E4M3 path is built for head_dim 128");
+  using Tile = KvTile<D, F8>;
+  using Shape = PersistentShape<D, F8>;
+  using Attn = std::conditional_t<F8, WarpAttnE4M3<T>, WarpAttn<T, D>>;
   constexpr int NW = Shape::kWarps;
   constexpr int SW = Shape::kStages;
   constexpr int NPS = Shape::kBlocksPerStage;
@@ -858,7 +850,7 @@ __global__ void __maxnreg__(F != kPool16 ? 168 : 192)
   context_prefix(a, a.pre_context_lens ? a.pre_context_lens : a.context_lens, s_P, s_ctx, s_warp_sum, NW * 32,
                  !a.recheck && blockIdx.x == 0);
 
-  Partition part(Hkv * s_P[B], gridDim.x * NW);
+  Partition part(Hkv * s_P[B], gridDim.x * NW, a.share_unit);
   const int gw = blockIdx.x * NW + warp;
 
   // Sequence b, KV head kvh and block j of flattened block f: units are
@@ -879,7 +871,7 @@ __global__ void __maxnreg__(F != kPool16 ? 168 : 192)
   uint8_t* wring = ring + warp * SW * Shape::kStageBytes;
   uint8_t* wside = side + warp * SW * 2 * kRowBytes;
   const uint64_t policy = l2_evict_first_policy();
-  if (!I4 && lane == 0) {
+  if (lane == 0) {
     prefetch_tensormap(&tmap_k);
     prefetch_tensormap(&tmap_v);
   }
@@ -975,52 +967,7 @@ __global__ void __maxnreg__(F != kPool16 ? 168 : 192)
       const int j = __shfl_sync(0xffffffffu, wj, src);
       const int row = __shfl_sync(0xffffffffu, wrow, src);
       int n = 1, row2 = row;
-      if constexpr (I4) {
-        // As many blocks as the stage holds, while they are in this window (so
-        // in this segment) and belong to the same unit.  Lanes src .. src+n-1
-        // each load their own block's two tiles.
-        const unsigned same = __ballot_sync(0xffffffffu, wb == b && wkvh == kvh && win_s + lane < win_e) >> src;
-        n = __ffs(~(same & ((1u << NPS) - 1))) - 1;
-        const bool mine = lane >= src && lane < src + n;
-        const int have = __popc(__ballot_sync(0xffffffffu, mine && wrow >= 0));
-        const uint32_t bar = smem_u32(&full_bar[warp][st_i]);
-        uint8_t* stage = wring + st_i * Shape::kStageBytes;
-        fence_proxy_async_smem();  // each lane's earlier accesses of this stage come before the refill
-        if (mine && lane == src + n - 1) s_prow[warp][st_i] = wrow;
-        __syncwarp();
-        if (lane == 0) {
-          const bool unit_last = j + n == (s_ctx[b] + kBlockSize - 1) / kBlockSize;
-          const int flags = (ip == seg_s ? 1 : 0) | (ip + n == seg_e ? 2 : 0) | ((n - 1) << 2);
-          s_desc[warp][st_i] = make_int4(b, kvh, j, seg | (flags << 28));
-          if (fused_append && unit_last) {
-            const int64_t unit = static_cast<int64_t>(b) * Hkv + kvh;
-            mbar_arrive_expect_tx(bar, have * Tile::kStageBytes + 2 * kRowBytes);
-            const uint32_t sd = smem_u32(wside + st_i * 2 * kRowBytes);
-            bulk_load(sd, static_cast<const T*>(a.k_new) + unit * D, kRowBytes, bar);
-            bulk_load(sd + kRowBytes, static_cast<const T*>(a.v_new) + unit * D, kRowBytes, bar);
-          } else {
-            mbar_arrive_expect_tx(bar, have * Tile::kStageBytes);
-          }
-        }
-        __syncwarp();  // the transaction count is set before the copies that complete it
-        if (mine && wrow >= 0) {
-          const uint32_t dst = smem_u32(stage + (lane - src) * Tile::kStageBytes);
-          const int64_t off = static_cast<int64_t>(wrow) * Tile::kRowBytes;
-          bulk_load_hint(dst, static_cast<const uint8_t*>(a.k_cache_w) + off, Tile::kTileBytes, bar, policy);
-          bulk_load_hint(dst + Tile::kTileBytes, static_cast<const uint8_t*>(a.v_cache_w) + off, Tile::kTileBytes, bar,
-                         policy);
-        }
-        if (have < n) {  // blocks outside the pool read as zeros
-          for (int i = 0; i < n; ++i)
-            if (__shfl_sync(0xffffffffu, wrow, src + i) < 0)
-              for (int o = lane * 16; o < Tile::kStageBytes; o += 512)
-                *reinterpret_cast<uint4*>(stage + i * Tile::kStageBytes + o) = make_uint4(0, 0, 0, 0);
-        }
-        ++issued;
-        ip += n;
-        st_i = st_i + 1 == SW ? 0 : st_i + 1;
-        continue;
-      } else if constexpr (NPS == 2) {
+      if constexpr (NPS == 2) {
         // Take the next block too when it is in this window (so in this
         // segment) and belongs to the same unit.
         const int src2 = src + 1 < 32 ? src + 1 : src;
@@ -1050,8 +997,8 @@ __global__ void __maxnreg__(F != kPool16 ? 168 : 192)
         } else {
           mbar_arrive_expect_tx(bar, n * Tile::kStageBytes);
         }
-        issue_tiles<D, F>(stage, bar, &tmap_k, &tmap_v, row, policy);
-        if (NPS == 2 && n == 2) issue_tiles<D, F>(stage + Tile::kStageBytes, bar, &tmap_k, &tmap_v, row2, policy);
+        issue_tiles<D, F8>(stage, bar, &tmap_k, &tmap_v, row, policy);
+        if (NPS == 2 && n == 2) issue_tiles<D, F8>(stage + Tile::kStageBytes, bar, &tmap_k, &tmap_v, row2, policy);
       }
       ++issued;
       ip += n;
@@ -1078,7 +1025,8 @@ __global__ void __maxnreg__(F != kPool16 ? 168 : 192)
   // wait see every earlier write, so they just find the lines in L2.
   start_head();
   if (lane < SW * NPS && win_s + lane < win_e && wrow >= 0) {
-    const int64_t off = static_cast<int64_t>(wrow) * Tile::kRowBytes;
+    constexpr int kCacheRowBytes = F8 ? D : 2 * D;
+    const int64_t off = static_cast<int64_t>(wrow) * kCacheRowBytes;
     prefetch_l2_bulk(static_cast<const uint8_t*>(a.k_cache_w) + off, Tile::kTileBytes);
     prefetch_l2_bulk(static_cast<const uint8_t*>(a.v_cache_w) + off, Tile::kTileBytes);
   }
@@ -1130,7 +1078,7 @@ __global__ void __maxnreg__(F != kPool16 ? 168 : 192)
         // rebuild from changing s_ctx while another warp still compares.
         __syncthreads();
         context_prefix_again(a, s_P, s_ctx, s_warp_sum, NW * 32);
-        part = Partition(Hkv * s_P[B], gridDim.x * NW);
+        part = Partition(Hkv * s_P[B], gridDim.x * NW, a.share_unit);
       }
       start_head();
     } else if (in_window) {
@@ -1168,7 +1116,7 @@ __global__ void __maxnreg__(F != kPool16 ? 168 : 192)
     const int b = dsc.x, kvh = dsc.y, j = dsc.z, sid = dsc.w & 0x0FFFFFFF;
     const int flags = dsc.w >> 28;
     const bool first_of_seg = flags & 1, last_of_seg = flags & 2;
-    const int n = 1 + (I4 ? (flags >> 2) & 3 : (flags >> 2) & 1);
+    const int n = 1 + ((flags >> 2) & 1);
     const int ctx = s_ctx[b];
     const int nb = (ctx + kBlockSize - 1) / kBlockSize;
     const int jl = j + n - 1;  // the stage's last block
@@ -1181,23 +1129,7 @@ __global__ void __maxnreg__(F != kPool16 ? 168 : 192)
       uint8_t* lt = ks + (n - 1) * Tile::kStageBytes;  // K tile of block jl; its V tile follows
       const uint8_t* sd = wside + st_c * 2 * kRowBytes;
       constexpr int kChunksPerRow = D / 8;
-      if constexpr (I4) {
-        // D / 4 lanes quantise a row, four entries each (D = 64: both rows at once).
-        constexpr int W = D / 4;
-        const int l = lane % W;
-#pragma unroll
-        for (int i = 0; i < W / 16; ++i) {
-          const bool is_v = W == 32 ? i == 1 : lane >= 16;
-          uint32_t pair;
-          const uint32_t codes =
-              int4_quantise4<T, W>(*reinterpret_cast<const uint2*>(sd + (is_v ? kRowBytes : 0) + 8 * l), pair);
-          int4_store4<D>(lt + (is_v ? Tile::kTileBytes : 0), is_v, r, l, codes, pair);
-          if (prow >= 0)
-            int4_store4<D>(static_cast<uint8_t*>(is_v ? a.v_cache_w : a.k_cache_w) +
-                               static_cast<int64_t>(prow) * Tile::kRowBytes,
-                           is_v, r, l, codes, pair);
-        }
-      } else if constexpr (F8) {
+      if constexpr (F8) {
         // Lanes 0-15 quantise 8 entries each of the K row, lanes 16-31 of the V row.
         const int v = lane >> 4, c8 = lane & 15;
         const uint4 val = *reinterpret_cast<const uint4*>(sd + v * kRowBytes + c8 * 16);
@@ -1223,11 +1155,7 @@ __global__ void __maxnreg__(F != kPool16 ? 168 : 192)
     if (first_of_seg || j == 0) {
       if (first_of_seg) seg_first_flush = true;
       unit_first_j = j;
-      const T* q_group = static_cast<const T*>(a.q) + (static_cast<int64_t>(b) * a.num_q_heads + kvh * g) * D;
-      if constexpr (I4)
-        at.load_q(q_group, g, a.scale_log2, lane);
-      else
-        at.load_q(q_group, g, lane);
+      at.load_q(static_cast<const T*>(a.q) + (static_cast<int64_t>(b) * a.num_q_heads + kvh * g) * D, g, lane);
       at.reset();
       if constexpr (F8) {
         unit_sl2 = a.scale_log2 * __ldg(a.k_scale + kvh);
@@ -1235,9 +1163,7 @@ __global__ void __maxnreg__(F != kPool16 ? 168 : 192)
       }
     }
     const int valid = min(n * kBlockSize, ctx - j * kBlockSize);
-    if constexpr (I4)
-      at.template blocks<NPS>(ks, n, valid, a.scale_log2, lane);
-    else if constexpr (NPS == 2)
+    if constexpr (NPS == 2)
       at.block2(ks, ks + Tile::kTileBytes, ks + Tile::kStageBytes, ks + Tile::kStageBytes + Tile::kTileBytes, valid,
                 unit_sl2, lane);
     else
@@ -1445,7 +1371,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32, COOP ? 6 : WIDE ? 4 : 8)
   RowPlan r{};
   unsigned valid0 = 0;
   auto plan_first = [&]() {
-    const Partition part(Hkv * s_P[a.num_seqs], nwarps);
+    const Partition part(Hkv * s_P[a.num_seqs], nwarps, a.share_unit);
     r = plan_row(part, first_base + warp / wpr);
     valid0 = r.work && sub < r.ncand ? gather(part, r, 0) : 0u;
   };
@@ -1461,7 +1387,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32, COOP ? 6 : WIDE ? 4 : 8)
   for (int base_row = first_base; base_row < rows; base_row += gridDim.x * rows_per_cta) {
     const int row = base_row + warp / wpr;
     const bool first = base_row == first_base;
-    const Partition part(Hkv * s_P[a.num_seqs], nwarps);
+    const Partition part(Hkv * s_P[a.num_seqs], nwarps, a.share_unit);
     if (!first) r = plan_row(part, row);
     const bool work = r.work, zero_row = r.zero_row;
     T* dst = static_cast<T*>(a.out) + static_cast<int64_t>(row) * D + lane * kPer;
