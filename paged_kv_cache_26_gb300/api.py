@@ -460,6 +460,45 @@ def paged_decode_step_fp8(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Ten
 
 
 # ---------------------------------------------------------------- 4-bit cache
+#
+# These calls and those of the next section check everything in one expression
+# (their calls take microseconds on the GPU, so microseconds of checking count)
+# and look for the message only when it fails.  They run on the device of their
+# tensors, whichever is current.
+
+_i32, _u8, _f32 = torch.int32, torch.uint8, torch.float32
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else None
+
+
+def _stream_of(stream, dev: int) -> int:
+    """The stream's handle; None: the current one of device dev."""
+    if stream is None:
+        return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream(dev).cuda_stream
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _call(name: str, dev: int, stream, args: tuple) -> None:
+    """Calls the library function on device dev with the stream's handle last."""
+    if dev == _current_device():
+        rc = getattr(lib(), name)(*args, _stream_of(stream, dev))
+    else:
+        with torch.cuda.device(dev):
+            rc = getattr(lib(), name)(*args, _stream_of(stream, dev))
+    if rc < 0:
+        raise PagedKVError(rc, name)
+
+
+def _explain(dev: int, *tensors) -> None:
+    """Raises the message for the first (name, tensor, dtype) that is not a
+    contiguous CUDA tensor of that dtype on device dev."""
+    for name, t, dtype in tensors:
+        if t is None:
+            continue
+        _need_cuda(name, t, dtype)
+        if t.get_device() != dev:
+            raise ValueError(f"{name} must be on device {dev} like the other tensors")
+
 
 def int4_row_bytes(head_dim: int) -> int:
     """Bytes of one token's K (or V) row of one KV head in a 4-bit pool: the
@@ -467,25 +506,16 @@ def int4_row_bytes(head_dim: int) -> int:
     return head_dim // 2 + 4
 
 
-def _int4_head_dim(k_cache: torch.Tensor, v_cache: torch.Tensor) -> int:
-    for n, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        _need_cuda(n, t, torch.uint8)
-    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape:
-        raise ValueError("4-bit caches must both be uint8 [num_blocks][num_kv_heads][16][head_dim/2 + 4]")
-    return 2 * (k_cache.shape[3] - 4)
-
-
 def make_dims_int4(q_or_new: torch.Tensor, k_cache: torch.Tensor, block_tables: Optional[torch.Tensor] = None,
                    num_q_heads: Optional[int] = None) -> PkvDims:
     """Dims of a call over a 4-bit pool: dtype is that of q / out / k_new / v_new."""
     nb, hkv, bs, row = k_cache.shape
-    if q_or_new.dtype not in _DTYPE_CODE:
+    code = _DTYPE_CODE.get(q_or_new.dtype)
+    if code is None:
         raise ValueError("q / k_new / v_new must be float16 or bfloat16")
-    return PkvDims(num_seqs=q_or_new.shape[0],
-                   num_q_heads=num_q_heads if num_q_heads is not None else q_or_new.shape[1],
-                   num_kv_heads=hkv, head_dim=2 * (row - 4), block_size=bs, num_blocks=nb,
-                   max_blocks_per_seq=block_tables.shape[1] if block_tables is not None else 0,
-                   dtype=_DTYPE_CODE[q_or_new.dtype])
+    n = q_or_new.shape
+    return PkvDims(n[0], num_q_heads if num_q_heads is not None else n[1], hkv, 2 * (row - 4), bs, nb,
+                   block_tables.shape[1] if block_tables is not None else 0, code)
 
 
 def make_workspace_int4(q: torch.Tensor, k_cache: torch.Tensor, block_tables: torch.Tensor) -> torch.Tensor:
@@ -495,22 +525,33 @@ def make_workspace_int4(q: torch.Tensor, k_cache: torch.Tensor, block_tables: to
     return torch.zeros(need, dtype=torch.uint8, device=q.device)
 
 
+def _int4_rows(what: str, k: torch.Tensor, v: torch.Tensor, slot_mapping: torch.Tensor, k_cache: torch.Tensor,
+               v_cache: torch.Tensor):
+    """Checks rows k / v [num_tokens][Hkv][D] against slots and 4-bit caches; (device, dims)."""
+    dev = k.get_device()
+    cs = k_cache.shape
+    if not (dev >= 0 and v.get_device() == dev and slot_mapping.get_device() == dev and k_cache.get_device() == dev and
+            v_cache.get_device() == dev and v.dtype == k.dtype and slot_mapping.dtype == _i32 and
+            k_cache.dtype == _u8 and v_cache.dtype == _u8 and k.is_contiguous() and v.is_contiguous() and
+            slot_mapping.is_contiguous() and k_cache.is_contiguous() and v_cache.is_contiguous() and len(cs) == 4 and
+            v_cache.shape == cs and k.shape == (slot_mapping.numel(), cs[1], 2 * (cs[3] - 4)) and v.shape == k.shape and
+            slot_mapping.dim() == 1):
+        _need_cuda(f"k_{what}", k)
+        _explain(dev, (f"v_{what}", v, k.dtype), ("slot_mapping", slot_mapping, _i32), ("k_cache", k_cache, _u8),
+                 ("v_cache", v_cache, _u8))
+        raise ValueError(f"k_{what} / v_{what} must be [num_tokens][num_kv_heads][head_dim], slot_mapping [num_tokens] "
+                         "and the 4-bit caches both uint8 [num_blocks][num_kv_heads][16][head_dim/2 + 4]")
+    return dev, make_dims_int4(k, k_cache, num_q_heads=cs[1])
+
+
 def paged_kv_append_int4(k_new: torch.Tensor, v_new: torch.Tensor, slot_mapping: torch.Tensor,
                          k_cache: torch.Tensor, v_cache: torch.Tensor, stream=None) -> None:
     """paged_kv_append into 4-bit caches (uint8 [num_blocks][Hkv][16][D/2 + 4]):
     each row is quantised with a scale and a minimum of its own."""
-    d = _int4_head_dim(k_cache, v_cache)
-    _need_cuda("k_new", k_new)
-    _need_cuda("v_new", v_new, k_new.dtype)
-    _need_cuda("slot_mapping", slot_mapping, torch.int32)
-    if k_new.dim() != 3 or k_new.shape != v_new.shape or k_new.shape[1:] != (k_cache.shape[1], d):
-        raise ValueError("k_new / v_new must be [num_tokens][num_kv_heads][head_dim] matching the cache")
-    if slot_mapping.shape != (k_new.shape[0],):
-        raise ValueError("slot_mapping must be [num_tokens]")
-    dims = make_dims_int4(k_new, k_cache, num_q_heads=k_cache.shape[1])
-    _check(lib().paged_kv_append_int4(_ptr(k_new), _ptr(v_new), _ptr(slot_mapping), k_new.shape[0], _ptr(k_cache),
-                                      _ptr(v_cache), ctypes.byref(dims), _stream(stream)),
-           "paged_kv_append_int4")
+    dev, dims = _int4_rows("new", k_new, v_new, slot_mapping, k_cache, v_cache)
+    _call("paged_kv_append_int4", dev, stream,
+          (k_new.data_ptr(), v_new.data_ptr(), slot_mapping.data_ptr(), dims.num_seqs, k_cache.data_ptr(),
+           v_cache.data_ptr(), ctypes.byref(dims)))
 
 
 def paged_kv_read_int4(slot_mapping: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -519,38 +560,48 @@ def paged_kv_read_int4(slot_mapping: torch.Tensor, k_cache: torch.Tensor, v_cach
     """The rows at these slots as values: (k, v), each [num_tokens][Hkv][D] of
     ``dtype`` (float16 or bfloat16; or that of k_out / v_out).  A negative slot
     gives a zero row."""
-    d = _int4_head_dim(k_cache, v_cache)
-    _need_cuda("slot_mapping", slot_mapping, torch.int32)
-    if slot_mapping.dim() != 1:
-        raise ValueError("slot_mapping must be [num_tokens]")
-    shape = (slot_mapping.shape[0], k_cache.shape[1], d)
     if k_out is None and v_out is None:
         if dtype not in _DTYPE_CODE:
             raise ValueError("dtype must be float16 or bfloat16")
+        if k_cache.dim() != 4 or slot_mapping.dim() != 1:
+            raise ValueError("caches must be uint8 [num_blocks][num_kv_heads][16][head_dim/2 + 4], slot_mapping "
+                             "[num_tokens]")
+        shape = (slot_mapping.shape[0], k_cache.shape[1], 2 * (k_cache.shape[3] - 4))
         k_out, v_out = (torch.empty(shape, dtype=dtype, device=k_cache.device) for _ in range(2))
     elif k_out is None or v_out is None:
         raise ValueError("give both k_out and v_out, or neither")
-    _need_cuda("k_out", k_out, dtype)
-    _need_cuda("v_out", v_out, k_out.dtype)
-    if k_out.shape != shape or v_out.shape != shape:
-        raise ValueError("k_out / v_out must be [num_tokens][num_kv_heads][head_dim] matching the cache")
-    dims = make_dims_int4(k_out, k_cache, num_q_heads=k_cache.shape[1])
-    _check(lib().paged_kv_read_int4(_ptr(slot_mapping), shape[0], _ptr(k_cache), _ptr(v_cache), _ptr(k_out),
-                                    _ptr(v_out), ctypes.byref(dims), _stream(stream)),
-           "paged_kv_read_int4")
+    elif dtype is not None and dtype != k_out.dtype:
+        raise ValueError(f"k_out must be {dtype}, got {k_out.dtype}")
+    dev, dims = _int4_rows("out", k_out, v_out, slot_mapping, k_cache, v_cache)
+    _call("paged_kv_read_int4", dev, stream,
+          (slot_mapping.data_ptr(), dims.num_seqs, k_cache.data_ptr(), v_cache.data_ptr(), k_out.data_ptr(),
+           v_out.data_ptr(), ctypes.byref(dims)))
     return k_out, v_out
 
 
-def _int4_call_checks(q, k_cache, v_cache, block_tables, context_lens, out):
-    _need_cuda("q", q)
-    d = _int4_head_dim(k_cache, v_cache)
-    _need_cuda("block_tables", block_tables, torch.int32)
-    _need_cuda("context_lens", context_lens, torch.int32)
-    _need_cuda("out", out, q.dtype)
-    if out.shape != q.shape or q.dim() != 3 or q.shape[2] != d:
-        raise ValueError("q / out must be [num_seqs][num_q_heads][head_dim] matching the caches")
-    if block_tables.dim() != 2 or block_tables.shape[0] != q.shape[0] or context_lens.shape != (q.shape[0],):
-        raise ValueError("block_tables must be [num_seqs][max_blocks], context_lens [num_seqs]")
+def _int4_decode(q, k_cache, v_cache, block_tables, context_lens, out, workspace):
+    """Checks of the 4-bit attention calls; (device, dims, workspace and its bytes)."""
+    dev = q.get_device()
+    qs, cs, bt = q.shape, k_cache.shape, block_tables.shape
+    if not (dev >= 0 and k_cache.get_device() == dev and v_cache.get_device() == dev and
+            block_tables.get_device() == dev and context_lens.get_device() == dev and out.get_device() == dev and
+            k_cache.dtype == _u8 and v_cache.dtype == _u8 and block_tables.dtype == _i32 and
+            context_lens.dtype == _i32 and out.dtype == q.dtype and q.is_contiguous() and k_cache.is_contiguous() and
+            v_cache.is_contiguous() and block_tables.is_contiguous() and context_lens.is_contiguous() and
+            out.is_contiguous() and len(qs) == 3 and len(cs) == 4 and len(bt) == 2 and v_cache.shape == cs and
+            out.shape == qs and qs[2] == 2 * (cs[3] - 4) and bt[0] == qs[0] and context_lens.shape == (qs[0],)):
+        _need_cuda("q", q)
+        _explain(dev, ("k_cache", k_cache, _u8), ("v_cache", v_cache, _u8), ("block_tables", block_tables, _i32),
+                 ("context_lens", context_lens, _i32), ("out", out, q.dtype))
+        raise ValueError("q / out must be [num_seqs][num_q_heads][head_dim], the 4-bit caches both uint8 "
+                         "[num_blocks][num_kv_heads][16][head_dim/2 + 4], block_tables [num_seqs][max_blocks], "
+                         "context_lens [num_seqs]")
+    dims = make_dims_int4(q, k_cache, block_tables)
+    if workspace is None:
+        workspace = make_workspace_int4(q, k_cache, block_tables)
+    elif workspace.get_device() != dev:
+        raise ValueError(f"workspace must be on device {dev} like the other tensors")
+    return dev, dims, workspace, workspace.numel() * workspace.element_size()
 
 
 def paged_decode_attention_int4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -560,13 +611,10 @@ def paged_decode_attention_int4(q: torch.Tensor, k_cache: torch.Tensor, v_cache:
     """paged_decode_attention over 4-bit caches.  Returns out."""
     if out is None:
         out = torch.empty_like(q)
-    _int4_call_checks(q, k_cache, v_cache, block_tables, context_lens, out)
-    dims = make_dims_int4(q, k_cache, block_tables)
-    workspace, ws_bytes = _fp8_workspace(dims, q, workspace)
-    _check(lib().paged_decode_attention_int4(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
-                                             _ptr(context_lens), float(scale), _ptr(out), _ptr(workspace), ws_bytes,
-                                             ctypes.byref(dims), _stream(stream)),
-           "paged_decode_attention_int4")
+    dev, dims, workspace, ws_bytes = _int4_decode(q, k_cache, v_cache, block_tables, context_lens, out, workspace)
+    _call("paged_decode_attention_int4", dev, stream,
+          (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), scale,
+           out.data_ptr(), workspace.data_ptr(), ws_bytes, ctypes.byref(dims)))
     return out
 
 
@@ -578,17 +626,16 @@ def paged_decode_step_int4(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Te
     appended, then attended, in one fused launch.  Returns out."""
     if out is None:
         out = torch.empty_like(q)
-    _int4_call_checks(q, k_cache, v_cache, block_tables, context_lens, out)
-    _need_cuda("k_new", k_new, q.dtype)
-    _need_cuda("v_new", v_new, q.dtype)
-    if k_new.shape != (q.shape[0], k_cache.shape[1], q.shape[2]) or v_new.shape != k_new.shape:
+    dev, dims, workspace, ws_bytes = _int4_decode(q, k_cache, v_cache, block_tables, context_lens, out, workspace)
+    if not (k_new.get_device() == dev and v_new.get_device() == dev and k_new.dtype == q.dtype and
+            v_new.dtype == q.dtype and k_new.is_contiguous() and v_new.is_contiguous() and
+            k_new.shape == (dims.num_seqs, dims.num_kv_heads, dims.head_dim) and v_new.shape == k_new.shape):
+        _explain(dev, ("k_new", k_new, q.dtype), ("v_new", v_new, q.dtype))
         raise ValueError("k_new / v_new must be [num_seqs][num_kv_heads][head_dim]")
-    dims = make_dims_int4(q, k_cache, block_tables)
-    workspace, ws_bytes = _fp8_workspace(dims, q, workspace)
-    _check(lib().paged_decode_step_int4(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache),
-                                        _ptr(block_tables), _ptr(context_lens), float(scale), _ptr(out),
-                                        _ptr(workspace), ws_bytes, ctypes.byref(dims), _stream(stream)),
-           "paged_decode_step_int4")
+    _call("paged_decode_step_int4", dev, stream,
+          (q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+           block_tables.data_ptr(), context_lens.data_ptr(), scale, out.data_ptr(), workspace.data_ptr(), ws_bytes,
+           ctypes.byref(dims)))
     return out
 
 
@@ -607,35 +654,44 @@ def paged_kv_resize_tables(context_lens: torch.Tensor, new_lens: torch.Tensor, b
     (int32 [num_blocks]) and num_free (int32 [1]) are updated in place, all or
     nothing (paged_kv_check_status tells).  Returns (slot_mapping,
     token_offsets)."""
-    for n, t in (("context_lens", context_lens), ("new_lens", new_lens), ("block_tables", block_tables),
-                 ("free_blocks", free_blocks), ("num_free", num_free)):
-        _need_cuda(n, t, torch.int32)
-    for n, t in (("slot_mapping", slot_mapping), ("token_offsets", token_offsets)):
-        if t is not None:
-            _need_cuda(n, t, torch.int32)
-    B = context_lens.shape[0] if context_lens.dim() == 1 else -1
-    if new_lens.shape != (B,) or block_tables.dim() != 2 or block_tables.shape[0] != B:
-        raise ValueError("context_lens / new_lens must be [num_seqs], block_tables [num_seqs][max_blocks]")
-    if free_blocks.dim() != 1 or num_free.numel() != 1:
-        raise ValueError("free_blocks must be [num_blocks], num_free one number")
-    if slot_mapping is not None and slot_mapping.dim() != 1:
-        raise ValueError("slot_mapping must be [num_slots]")
-    if token_offsets is not None and token_offsets.shape != (B + 1,):
-        raise ValueError("token_offsets must be [num_seqs + 1]")
-    _check(lib().paged_kv_resize_tables(
-        _ptr(context_lens), _ptr(new_lens), B, block_tables.shape[1], 16, _ptr(block_tables), _ptr(free_blocks),
-        _ptr(num_free), free_blocks.shape[0], _ptr(slot_mapping),
-        slot_mapping.shape[0] if slot_mapping is not None else 0, _ptr(token_offsets), _stream(stream)),
-        "paged_kv_resize_tables")
+    dev, bt = context_lens.get_device(), block_tables.shape
+    if not (dev >= 0 and new_lens.get_device() == dev and block_tables.get_device() == dev and
+            free_blocks.get_device() == dev and num_free.get_device() == dev and context_lens.dtype == _i32 and
+            new_lens.dtype == _i32 and block_tables.dtype == _i32 and free_blocks.dtype == _i32 and
+            num_free.dtype == _i32 and context_lens.is_contiguous() and new_lens.is_contiguous() and
+            block_tables.is_contiguous() and free_blocks.is_contiguous() and len(bt) == 2 and
+            context_lens.shape == bt[:1] and new_lens.shape == bt[:1] and free_blocks.dim() == 1 and
+            num_free.numel() == 1):
+        _need_cuda("context_lens", context_lens, _i32)
+        _explain(dev, ("new_lens", new_lens, _i32), ("block_tables", block_tables, _i32),
+                 ("free_blocks", free_blocks, _i32), ("num_free", num_free, _i32))
+        raise ValueError("context_lens / new_lens must be [num_seqs], block_tables [num_seqs][max_blocks], free_blocks "
+                         "[num_blocks], num_free one number")
+    slots, num_slots, offsets = 0, 0, 0
+    if slot_mapping is not None:
+        if not (slot_mapping.get_device() == dev and slot_mapping.dtype == _i32 and slot_mapping.dim() == 1 and
+                slot_mapping.is_contiguous()):
+            _explain(dev, ("slot_mapping", slot_mapping, _i32))
+            raise ValueError("slot_mapping must be [num_slots]")
+        slots, num_slots = slot_mapping.data_ptr(), slot_mapping.numel()
+    if token_offsets is not None:
+        if not (token_offsets.get_device() == dev and token_offsets.dtype == _i32 and
+                token_offsets.shape == (bt[0] + 1,) and token_offsets.is_contiguous()):
+            _explain(dev, ("token_offsets", token_offsets, _i32))
+            raise ValueError("token_offsets must be [num_seqs + 1]")
+        offsets = token_offsets.data_ptr()
+    _call("paged_kv_resize_tables", dev, stream,
+          (context_lens.data_ptr(), new_lens.data_ptr(), bt[0], bt[1], 16, block_tables.data_ptr(),
+           free_blocks.data_ptr(), num_free.data_ptr(), free_blocks.numel(), slots, num_slots, offsets))
     return slot_mapping, token_offsets
 
 
 _PROB_CODE = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
 
 
-def _need_rows(name: str, t: torch.Tensor, shape, dtype):
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
+def _need_rows(name: str, t: torch.Tensor, dev: int, shape, dtype):
+    if t.get_device() != dev or dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor on the device of the others")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if t.dim() != 3 or tuple(t.shape) != tuple(shape) or (t.shape[2] > 1 and t.stride(2) != 1):
@@ -655,35 +711,49 @@ def paged_verify_draft(target_probs: torch.Tensor, draft_probs: Optional[torch.T
     tokens of the multi-token step).  Returns (num_accepted int32 [B], tokens
     int32 [B][K + 1]: the accepted drafts, the token drawn after them, then -1,
     new_lens int32 [B]: context_lens without the rejected drafts, or None)."""
-    if target_probs.dtype not in _PROB_CODE:
-        raise ValueError("target_probs must be float32, float16 or bfloat16")
-    _need_cuda("draft_tokens", draft_tokens, torch.int32)
-    _need_cuda("accept_u", accept_u, torch.float32)
-    _need_cuda("sample_u", sample_u, torch.float32)
-    if draft_tokens.dim() != 2 or accept_u.shape != draft_tokens.shape:
-        raise ValueError("draft_tokens / accept_u must be [num_seqs][num_draft]")
-    B, K = draft_tokens.shape
-    V = target_probs.shape[2] if target_probs.dim() == 3 else 0
-    _need_rows("target_probs", target_probs, (B, K + 1, V), target_probs.dtype)
+    dev, dtype = target_probs.get_device(), target_probs.dtype
+    code, xs, ts = _PROB_CODE.get(dtype), draft_tokens.shape, target_probs.shape
+    if not (dev >= 0 and code is not None and draft_tokens.get_device() == dev and accept_u.get_device() == dev and
+            sample_u.get_device() == dev and draft_tokens.dtype == _i32 and accept_u.dtype == _f32 and
+            sample_u.dtype == _f32 and draft_tokens.is_contiguous() and accept_u.is_contiguous() and
+            sample_u.is_contiguous() and len(xs) == 2 and accept_u.shape == xs and sample_u.shape == xs[:1] and
+            len(ts) == 3 and ts[:2] == (xs[0], xs[1] + 1)):
+        if code is None:
+            raise ValueError("target_probs must be float32, float16 or bfloat16")
+        _explain(dev, ("draft_tokens", draft_tokens, _i32), ("accept_u", accept_u, _f32), ("sample_u", sample_u, _f32))
+        raise ValueError("draft_tokens / accept_u must be [num_seqs][num_draft], sample_u [num_seqs], target_probs "
+                         "[num_seqs][num_draft + 1][vocab] on their device")
+    B, K = xs
+    V = ts[2]
+    t_stride = target_probs.stride()
+    if t_stride[2] != 1:
+        _need_rows("target_probs", target_probs, dev, (B, K + 1, V), dtype)
+    q, d_stride = 0, (0, 0)
     if draft_probs is not None:
-        _need_rows("draft_probs", draft_probs, (B, K, V), target_probs.dtype)
-    if sample_u.shape != (B,):
-        raise ValueError("sample_u must be [num_seqs]")
-    for n, t in (("draft_lens", draft_lens), ("context_lens", context_lens)):
-        if t is not None:
-            _need_cuda(n, t, torch.int32)
-            if t.shape != (B,):
-                raise ValueError(f"{n} must be [num_seqs]")
-    new = lambda *shape: torch.empty(shape, dtype=torch.int32, device=target_probs.device)  # noqa: E731
-    accepted, tokens = new(B), new(B, K + 1)
-    lens = new(B) if context_lens is not None else None
-    dims = PkvVerifyDims(B, K, V, _PROB_CODE[target_probs.dtype], target_probs.stride(0), target_probs.stride(1),
-                         draft_probs.stride(0) if draft_probs is not None else 0,
-                         draft_probs.stride(1) if draft_probs is not None else 0)
-    _check(lib().paged_verify_draft(_ptr(target_probs), _ptr(draft_probs), _ptr(draft_tokens), _ptr(draft_lens),
-                                    _ptr(accept_u), _ptr(sample_u), _ptr(context_lens), ctypes.byref(dims),
-                                    _ptr(accepted), _ptr(tokens), _ptr(lens), _stream(stream)),
-           "paged_verify_draft")
+        _need_rows("draft_probs", draft_probs, dev, (B, K, V), dtype)
+        q, d_stride = draft_probs.data_ptr(), draft_probs.stride()
+    n = ctx = 0
+    if draft_lens is not None:
+        if not (draft_lens.get_device() == dev and draft_lens.dtype == _i32 and draft_lens.shape == (B,) and
+                draft_lens.is_contiguous()):
+            _explain(dev, ("draft_lens", draft_lens, _i32))
+            raise ValueError("draft_lens must be [num_seqs]")
+        n = draft_lens.data_ptr()
+    if context_lens is not None:
+        if not (context_lens.get_device() == dev and context_lens.dtype == _i32 and context_lens.shape == (B,) and
+                context_lens.is_contiguous()):
+            _explain(dev, ("context_lens", context_lens, _i32))
+            raise ValueError("context_lens must be [num_seqs]")
+        ctx = context_lens.data_ptr()
+    # One allocation for the three results.
+    accepted, lens, tokens = torch.empty((B * (K + 3),), dtype=_i32, device=dev).split_with_sizes((B, B, B * (K + 1)))
+    tokens = tokens.view(B, K + 1)
+    if context_lens is None:
+        lens = None
+    dims = PkvVerifyDims(B, K, V, code, t_stride[0], t_stride[1], d_stride[0], d_stride[1])
+    _call("paged_verify_draft", dev, stream,
+          (target_probs.data_ptr(), q, draft_tokens.data_ptr(), n, accept_u.data_ptr(), sample_u.data_ptr(), ctx,
+           ctypes.byref(dims), accepted.data_ptr(), tokens.data_ptr(), lens.data_ptr() if lens is not None else 0))
     return accepted, tokens, lens
 
 

@@ -400,7 +400,31 @@ struct StageInfo {
   static constexpr int kCountShift = 11;      // blocks
 };
 
+// The fused append's patch of a unit's last stage: row r of the staged K and V
+// tiles (at `tile`) and of the pool's (tile bytes at `off`) gets the new rows at
+// `rows`, quantised.  D / 4 lanes take a row, four entries each (D = 64: both
+// rows at once).
 template <typename T, int D>
+__device__ __forceinline__ void append_patch(uint8_t* tile, const uint8_t* rows, int r, uint8_t* k_pool, uint8_t* v_pool,
+                                          int64_t off) {
+  constexpr int W = D / 4;
+  const int lane = threadIdx.x & 31, l = lane % W;
+#pragma unroll
+  for (int i = 0; i < W / 16; ++i) {
+    const bool is_v = W == 32 ? i == 1 : lane >= 16;
+    uint32_t pair;
+    const uint32_t codes =
+        int4_quantise4<T, W>(*reinterpret_cast<const uint2*>(rows + (is_v ? 2 * D : 0) + 8 * l), pair);
+    int4_store4<D>(tile + (is_v ? Int4Tile<D>::kBytes : 0), is_v, r, l, codes, pair);
+    if (off >= 0) int4_store4<D>((is_v ? v_pool : k_pool) + off, is_v, r, l, codes, pair);
+  }
+  fence_proxy_async_smem();  // the patch comes before the copies that refill the slot
+  __syncwarp();
+}
+
+// APPEND: the step, with k_new / v_new; else attention alone.  (One kernel for
+// both cost attention 3.5 us of 39 at 8 x 16384 tokens.)
+template <typename T, int D, bool APPEND>
 __global__ void __maxnreg__(168) decode_int4_kernel(const DecodeArgs a) {
   using Tile = Int4Tile<D>;
   using Shape = Int4Shape<D>;
@@ -421,7 +445,6 @@ __global__ void __maxnreg__(168) decode_int4_kernel(const DecodeArgs a) {
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int B = a.num_seqs, Hkv = a.num_kv_heads, g = a.group;
-  const bool fused_append = a.k_new != nullptr;
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (lane == 0) {
@@ -488,7 +511,7 @@ __global__ void __maxnreg__(168) decode_int4_kernel(const DecodeArgs a) {
     const unsigned runs = __ballot_sync(0xffffffffu, in && (lane == 0 || wj == 0));
     const int pos = lane - (31 - __clz(runs & upto));  // lane 0 starts a run
     const unsigned firsts = __ballot_sync(
-        0xffffffffu, in && (pos % NB == 0 || (fused_append && wj == nb - 1 && pos % NB == NB - 1)));
+        0xffffffffu, in && (pos % NB == 0 || (APPEND && wj == nb - 1 && pos % NB == NB - 1)));
     stages = __popc(firsts);
     if (in) {
       wrow = tile_row(wphys, wkvh, a, after_wait);
@@ -578,7 +601,7 @@ __global__ void __maxnreg__(168) decode_int4_kernel(const DecodeArgs a) {
       __syncwarp();  // every lane is done with this slot's last contents
       if (mine && wslot == 0) {
         s_desc[warp][st_i] = make_int4(wb, wkvh, winfo, seg);
-        if (fused_append && (winfo & StageInfo::kUnitEnd)) {
+        if (APPEND && (winfo & StageInfo::kUnitEnd)) {
           // A unit's last stage: the appended token's K and V rows too.
           const int64_t unit = static_cast<int64_t>(wb) * Hkv + wkvh;
           mbar_arrive_expect_tx(bar, bytes + 2 * kNewRowBytes);
@@ -589,7 +612,7 @@ __global__ void __maxnreg__(168) decode_int4_kernel(const DecodeArgs a) {
           mbar_arrive_expect_tx(bar, bytes);
         }
       }
-      if (fused_append && mine && winfo >> StageInfo::kCountShift == 1) s_prow[warp][st_i] = wrow;
+      if (APPEND && mine && winfo >> StageInfo::kCountShift == 1) s_prow[warp][st_i] = wrow;
       __syncwarp();  // the transaction count is set before the copies that complete it
       if (mine && wrow >= 0) {
         const uint32_t dst = smem_u32(stage) + wslot * Shape::kBlockBytes;
@@ -704,30 +727,13 @@ __global__ void __maxnreg__(168) decode_int4_kernel(const DecodeArgs a) {
     }
     const int n = info >> StageInfo::kCountShift, valid = info & StageInfo::kValidBits;
     uint8_t* stage = wring + st_c * Shape::kStageBytes;
-    if (fused_append && (info & StageInfo::kUnitEnd)) {
+    if (APPEND && (info & StageInfo::kUnitEnd)) {
       // Append: the context's last token goes into its row of the stage's last
       // block, in the staged tiles (for this step's attention) and in the pool.
-      // D / 4 lanes quantise a row, four entries each (D = 64: both rows at once).
-      const int r = (valid - 1) % kBlockSize;
       const int prow = s_prow[warp][st_c];
-      uint8_t* tile = stage + (n - 1) * Shape::kBlockBytes;
-      const uint8_t* sd = stage + kNewRows;
-      constexpr int W = D / 4;
-      const int l = lane % W;
-#pragma unroll
-      for (int i = 0; i < W / 16; ++i) {
-        const bool is_v = W == 32 ? i == 1 : lane >= 16;
-        uint32_t pair;
-        const uint32_t codes =
-            int4_quantise4<T, W>(*reinterpret_cast<const uint2*>(sd + (is_v ? kNewRowBytes : 0) + 8 * l), pair);
-        int4_store4<D>(tile + (is_v ? Tile::kBytes : 0), is_v, r, l, codes, pair);
-        if (prow >= 0)
-          int4_store4<D>(static_cast<uint8_t*>(is_v ? a.v_cache_w : a.k_cache_w) +
-                             static_cast<int64_t>(prow) * Tile::kRowBytes,
-                         is_v, r, l, codes, pair);
-      }
-      fence_proxy_async_smem();  // the patch comes before the copies that refill the slot
-      __syncwarp();
+      append_patch<T, D>(stage + (n - 1) * Shape::kBlockBytes, stage + kNewRows, (valid - 1) % kBlockSize,
+                         static_cast<uint8_t*>(a.k_cache_w), static_cast<uint8_t*>(a.v_cache_w),
+                         prow >= 0 ? static_cast<int64_t>(prow) * Tile::kRowBytes : -1);
     }
     at.template blocks<NB, Shape::kStepBlocks>(stage, n, valid, a.scale_log2, lane);
     next_oldest();
@@ -770,6 +776,195 @@ __global__ void __maxnreg__(168) decode_int4_kernel(const DecodeArgs a) {
   if (!ok && lane == 0) {
     // A wait gave up: let this warp's copies in flight land before the CTA exits.
     for (; consumed < issued; next_oldest()) wait_oldest();
+  }
+}
+
+// ===================================================================== merge
+
+// Merge of the pieces the decode kernel left, one warp per unit (sequence, KV
+// head): what merge_persistent_kernel does for one query head at a time, with
+// the unit's pieces found once for all heads of its group and the heads' loads
+// in flight together.  For many rows: a warp per row spends its time finding the
+// pieces, the same ones for every head of a unit.
+constexpr int kUnitMergeWarps = 4;
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kUnitMergeWarps * 32) merge_units_kernel(const DecodeArgs a, int32_t nwarps) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  constexpr int kPer = D / 32;
+  extern __shared__ int merge_smem[];
+  __shared__ int s_warp_sum[kUnitMergeWarps];
+  __shared__ int s_row[kUnitMergeWarps][32];
+  int* s_P = merge_smem;
+  int* s_ctx = s_P + a.num_seqs + 1;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int kThreads = kUnitMergeWarps * 32;
+  const int B = a.num_seqs, Hkv = a.num_kv_heads, g = a.group;
+  const int unit = blockIdx.x * kUnitMergeWarps + warp;
+  const bool live = unit < B * Hkv;
+  const int b = live ? unit / Hkv : 0, kvh = unit - b * Hkv;
+
+  // The lengths the decode grid partitioned: published by it under the call's
+  // tag, or read here (and, if they may be stale, checked after the wait), as
+  // in merge_persistent_kernel.
+  bool published = false;
+  if (a.recheck && a.epoch != 0) {
+    const int32_t tag = static_cast<int32_t>(a.epoch);
+    __shared__ int s_got;
+    if (threadIdx.x == 0) {
+      const unsigned long long t0 = global_ns();
+      bool got = ld_acquire_gpu(a.pub) == tag;
+      while (!got && global_ns() - t0 < kWaitLimitNs) {
+        __nanosleep(256);
+        got = ld_acquire_gpu(a.pub) == tag;
+      }
+      s_got = got;
+    }
+    __syncthreads();
+    published = s_got != 0;
+  }
+  if (!published)
+    context_prefix(a, a.pre_context_lens ? a.pre_context_lens : a.context_lens, s_P, s_ctx, s_warp_sum, kThreads,
+                   false);
+
+  // The unit's blocks [U, Uend) and its candidate segments, those of shares
+  // w0 .. ; ncand = 0: one segment holds it all, and the decode kernel wrote it.
+  int nb = 0, U = 0, w0 = 0, ncand = 0;
+  Partition part(0, nwarps, a.share_unit);
+  auto plan = [&]() {
+    const int ctx = published ? __ldcg(a.pub + 1 + b) : s_ctx[b];
+    const int before = published ? __ldcg(a.pub + 1 + B + b) : s_P[b];
+    const int blocks = published ? __ldcg(a.pub + 1 + B + B) : s_P[B];
+    part = Partition(Hkv * blocks, nwarps, a.share_unit);
+    nb = (ctx + kBlockSize - 1) / kBlockSize;
+    ncand = 0;
+    if (!live || nb == 0) return;
+    U = Hkv * before + kvh * nb;
+    w0 = U / part.R;
+    const int w1 = (U + nb - 1) / part.R;
+    if (part.nchunks == 0) {  // a share is one segment
+      if (w1 > w0) ncand = w1 - w0 + 1;
+      return;
+    }
+    int s, e;
+    part.segment_of(U, s, e);
+    if (e < U + nb) ncand = (w1 - w0 + 1) * part.seg_per_share();
+  };
+  // Row of the piece (its first head's) that candidate c left, or -1 where that
+  // segment does not overlap the unit.
+  auto piece = [&](int c) -> int {
+    int w, s, e, sid;
+    if (part.nchunks == 0) {
+      sid = w = w0 + c;
+      part.head(w, s, e);
+    } else {
+      const int per = part.seg_per_share(), k = c % per;
+      w = w0 + c / per;
+      if (k == 0) {
+        part.head(w, s, e);
+        sid = w;
+      } else {
+        part.chunk(k - 1, w, s, e);
+        sid = part.nwarps + (k - 1) * part.nwarps + w;
+      }
+    }
+    if (e <= s || e <= U || s >= U + nb) return -1;
+    return (sid * 2 + (U > s ? 1 : 0)) * kMaxGroup;
+  };
+  // Candidates 32 k + lane, compacted: how many overlap.
+  auto gather = [&](int k) -> int {
+    const int c = 32 * k + lane;
+    const int row = c < ncand ? piece(c) : -1;
+    const unsigned valid = __ballot_sync(0xffffffffu, row >= 0);
+    __syncwarp();  // the last batch's rows have been read
+    if (row >= 0) s_row[warp][__popc(valid & ((1u << lane) - 1))] = row;
+    __syncwarp();
+    return __popc(valid);
+  };
+  plan();
+  int count = ncand > 0 ? gather(0) : 0;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (!published && a.recheck && context_changed(a, s_ctx, kThreads, false)) {
+    context_prefix(a, a.context_lens, s_P, s_ctx, s_warp_sum, kThreads, false);
+    plan();
+    count = ncand > 0 ? gather(0) : 0;
+  }
+  if (!live) return;
+  T* out = static_cast<T*>(a.out) + (static_cast<int64_t>(b) * a.num_q_heads + kvh * g) * D + lane * kPer;
+  if (nb == 0) {  // an empty context: zero rows
+    for (int h = 0; h < g; ++h)
+#pragma unroll
+      for (int k = 0; k < kPer; k += 2) *reinterpret_cast<uint32_t*>(out + h * D + k) = 0;
+    return;
+  }
+  if (ncand == 0) return;
+
+  float m[kMaxGroup], L[kMaxGroup], o[kMaxGroup][kPer];
+#pragma unroll
+  for (int h = 0; h < kMaxGroup; ++h) {
+    m[h] = -INFINITY;
+    L[h] = 0.f;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) o[h][k] = 0.f;
+  }
+  for (int k = 0; 32 * k < ncand; ++k) {
+    if (k > 0) count = gather(k);
+    if (count == 0) continue;
+    const float* lse = a.part_lse + s_row[warp][min(lane, count - 1)];
+    float w[kMaxGroup];
+#pragma unroll
+    for (int h = 0; h < kMaxGroup; ++h) w[h] = h < g && lane < count ? __ldcg(lse + h) : -INFINITY;
+#pragma unroll
+    for (int h = 0; h < kMaxGroup; ++h) {
+      if (h < g) {
+        float mx = w[h];
+#pragma unroll
+        for (int s = 16; s > 0; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
+        mx = fmaxf(mx, m[h]);
+        const float sc = exp2f(m[h] - mx);
+        m[h] = mx;
+        w[h] = exp2f(w[h] - mx);
+        float sum = w[h];
+#pragma unroll
+        for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
+        L[h] = L[h] * sc + sum;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) o[h][i] *= sc;
+      }
+    }
+    for (int i = 0; i < count; ++i) {
+      const float* src = a.part_o + static_cast<int64_t>(s_row[warp][i]) * D + lane * kPer;
+      float v[kMaxGroup][kPer];
+#pragma unroll
+      for (int h = 0; h < kMaxGroup; ++h) {
+        if (h < g) {
+          if constexpr (kPer == 4) {
+            const float4 f = __ldcg(reinterpret_cast<const float4*>(src + h * D));
+            v[h][0] = f.x, v[h][1] = f.y, v[h][2] = f.z, v[h][3] = f.w;
+          } else {
+            const float2 f = __ldcg(reinterpret_cast<const float2*>(src + h * D));
+            v[h][0] = f.x, v[h][1] = f.y;
+          }
+        }
+      }
+#pragma unroll
+      for (int h = 0; h < kMaxGroup; ++h) {
+        if (h < g) {
+          const float wi = __shfl_sync(0xffffffffu, w[h], i);
+#pragma unroll
+          for (int k2 = 0; k2 < kPer; ++k2) o[h][k2] = fmaf(wi, v[h][k2], o[h][k2]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int h = 0; h < kMaxGroup; ++h) {
+    if (h < g) {
+      const float inv = 1.f / L[h];
+#pragma unroll
+      for (int k = 0; k < kPer; k += 2)
+        *reinterpret_cast<uint32_t*>(out + h * D + k) = pack2<T>(o[h][k] * inv, o[h][k + 1] * inv);
+    }
   }
 }
 

@@ -89,84 +89,191 @@ __device__ __forceinline__ void int4_store4(uint8_t* tile, bool is_v, int t, int
 
 // ===================================================================== append
 
-// Slot-mapped append into a 4-bit pool: a warp quantises one token's K and V
-// rows of one KV head (D = 64: one half-warp each).
-template <typename T, int D>
-__global__ void append_int4_kernel(const uint2* __restrict__ k_new, const uint2* __restrict__ v_new,
-                                   const int32_t* __restrict__ slots, int32_t num_tokens, int32_t num_kv_heads,
-                                   int64_t num_slots, uint8_t* __restrict__ k_cache, uint8_t* __restrict__ v_cache) {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  constexpr int W = D / 4;
-  const int lane = threadIdx.x & 31;
-  const int64_t rows = static_cast<int64_t>(num_tokens) * num_kv_heads;
-  const int64_t warps = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
-  for (int64_t row = blockIdx.x * static_cast<int64_t>(blockDim.x >> 5) + (threadIdx.x >> 5); row < rows;
-       row += warps) {
-    const int64_t token = row / num_kv_heads;
-    const int head = static_cast<int>(row - token * num_kv_heads);
-    const int32_t slot = slots[token];
-    if (slot < 0) continue;
-    if (slot >= num_slots) {
-      if (lane == 0) flag_error(kErrSlot);
-      continue;
-    }
-    const int t = slot & 15;
-    const int64_t tile = (static_cast<int64_t>(slot >> 4) * num_kv_heads + head) * Int4Tile<D>::kBytes;
-    const int l = lane % W;
+// The larger / smaller of two packed pairs of T, half by half.
+template <typename T>
+__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  if constexpr (MmaKind<T>::kBf16)
+    asm("min.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else
+    asm("min.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  if constexpr (MmaKind<T>::kBf16)
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else
+    asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// 16 consecutive values of one row (packed), the row spread over L = D/16
+// neighbouring lanes: their codes as four 16-bit quads (quad i = dims 4i..4i+3)
+// and the row's pair.  Extremes are found on the packed values (exact).  A code
+// needs no lower limit: x - minimum is at least minus half a float16 step of
+// the minimum, and the scale, if above 0, at least such a step, so the quotient
+// is -0.5 or more and rounds to 0.  Rounding is by adding 1.5 * 2^23.
+template <typename T, int L>
+__device__ __forceinline__ uint2 int4_quantise16(const uint4 (&raw)[2], uint32_t& pair) {
+  uint32_t lo = word_of(raw[0], 0), hi = lo;
 #pragma unroll
-    for (int h = 0; h < W / 16; ++h) {
-      const bool is_v = W == 32 ? h == 1 : lane >= 16;
-      const uint2 raw = (is_v ? v_new : k_new)[row * W + l];
-      uint32_t pair;
-      const uint32_t codes = int4_quantise4<T, W>(raw, pair);
-      int4_store4<D>((is_v ? v_cache : k_cache) + tile, is_v, t, l, codes, pair);
+  for (int i = 1; i < 8; ++i) {
+    lo = min2<T>(lo, word_of(raw[i >> 2], i & 3));
+    hi = max2<T>(hi, word_of(raw[i >> 2], i & 3));
+  }
+  // One word holds (smallest, -largest): min2 reduces both at once.
+  lo = min2<T>(lo, __byte_perm(lo, 0, 0x1032));
+  hi = max2<T>(hi, __byte_perm(hi, 0, 0x1032)) ^ 0x80008000u;
+  uint32_t ext = __byte_perm(lo, hi, 0x5410);
+#pragma unroll
+  for (int o = 1; o < L; o <<= 1) ext = min2<T>(ext, __shfl_xor_sync(0xffffffffu, ext, o));
+  const float2 e = unpack2<T>(ext);
+  const float mn = limit_f16(e.x), mx = limit_f16(-e.y);
+  const bool wide = !(e.x >= -kF16Max && -e.y <= kF16Max);  // some value is past the float16 range
+  const Int4Row r = int4_row(mn, mx);
+  pair = r.pair;
+  uint32_t out[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float q[2];  // two quads as whole numbers below 2^16
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      q[k] = 0.f;
+#pragma unroll
+      for (int i = 1; i >= 0; --i) {
+        float2 x = unpack2<T>(word_of(raw[h], 2 * k + i));
+        if (wide) x = make_float2(limit_f16(x.x), limit_f16(x.y));
+        const float c0 = fminf(__fmul_rn(__fsub_rn(x.x, r.low), r.inv), 15.f);
+        const float c1 = fminf(__fmul_rn(__fsub_rn(x.y, r.low), r.inv), 15.f);
+        const float r0 = __fsub_rn(__fadd_rn(c0, 12582912.f), 12582912.f);
+        const float r1 = __fsub_rn(__fadd_rn(c1, 12582912.f), 12582912.f);
+        q[k] = fmaf(q[k], 256.f, fmaf(r1, 16.f, r0));
+      }
+    }
+    out[h] = __byte_perm(__float_as_uint(q[0] + 8388608.f), __float_as_uint(q[1] + 8388608.f), 0x5410);
+  }
+  return make_uint2(out[0], out[1]);
+}
+
+constexpr int kAppendThreads = 256;
+
+// Slot-mapped append into a 4-bit pool.  A CTA takes kAppendThreads / L
+// neighbouring tokens of one KV head, L = D/16 lanes a row with 16 values each.
+// V's codes of an even token and of the odd one after it share 32-bit words, so
+// the lanes of an even token whose neighbour in the pool is the next token of
+// the CTA (a prompt's tokens) take its codes through shared memory and store
+// for both, whole words; other tokens store their 16-bit halves.
+// Bound by the values read (2 bytes each) where tokens are many; 16 values a
+// lane because the row's parameters (two divisions) and reductions are paid per
+// lane.
+template <typename T, int D>
+__global__ void __launch_bounds__(kAppendThreads)
+    append_int4_kernel(const uint4* __restrict__ k_new, const uint4* __restrict__ v_new,
+                       const int32_t* __restrict__ slots, int32_t num_tokens, int32_t num_kv_heads, int64_t num_slots,
+                       uint8_t* __restrict__ k_cache, uint8_t* __restrict__ v_cache) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  constexpr int L = D / 16, kTokens = kAppendThreads / L;
+  __shared__ int s_slot[kTokens + 1];
+  __shared__ uint2 s_codes[kAppendThreads];
+  const int tid = threadIdx.x, t = tid / L, l = tid % L;
+  const int head = blockIdx.y;
+  const int64_t token = static_cast<int64_t>(blockIdx.x) * kTokens + t;
+  const bool in = token < num_tokens;
+  int slot = in ? slots[token] : -1;
+  uint4 kr[2] = {}, vr[2] = {};
+  if (slot >= 0) {
+    const int64_t at = ((token * num_kv_heads + head) * L + l) * 2;
+    kr[0] = k_new[at], kr[1] = k_new[at + 1];
+    vr[0] = v_new[at], vr[1] = v_new[at + 1];
+  }
+  if (slot >= num_slots) {
+    if (l == 0) flag_error(kErrSlot);
+    slot = -1;
+  }
+  uint32_t kp, vp;
+  const uint2 kc = int4_quantise16<T, L>(kr, kp), vc = int4_quantise16<T, L>(vr, vp);
+  if (l == 0) s_slot[t] = slot;
+  if (tid == 0) s_slot[kTokens] = -1;
+  s_codes[tid] = vc;
+  __syncthreads();
+  if (slot >= 0) {
+    const int r = slot & 15;
+    const int64_t tile = (static_cast<int64_t>(slot >> 4) * num_kv_heads + head) * Int4Tile<D>::kBytes;
+    uint8_t* kt = k_cache + tile;
+    uint8_t* vt = v_cache + tile;
+    // K: quads in order, 8 bytes.
+    *reinterpret_cast<uint2*>(kt + r * (D / 2) + 8 * l) = kc;
+    if (l == 0) {
+      *reinterpret_cast<uint32_t*>(kt + Int4Tile<D>::kCodeBytes + 4 * r) = kp;
+      *reinterpret_cast<uint32_t*>(vt + Int4Tile<D>::kCodeBytes + 4 * r) = vp;
+    }
+    const bool leads = !(r & 1) && s_slot[t + 1] == slot + 1;
+    const bool follows = (r & 1) && t > 0 && s_slot[t - 1] == slot - 1;
+    if (leads) {
+      const uint2 oc = s_codes[tid + L];
+      const uint32_t w[4] = {__byte_perm(vc.x, oc.x, 0x5410), __byte_perm(vc.x, oc.x, 0x7632),
+                             __byte_perm(vc.y, oc.y, 0x5410), __byte_perm(vc.y, oc.y, 0x7632)};
+      if constexpr (D == 128) {
+        *reinterpret_cast<uint4*>(vt + Int4Tile<D>::v_offset(r, 16 * l)) = make_uint4(w[0], w[1], w[2], w[3]);
+      } else {
+        *reinterpret_cast<uint2*>(vt + Int4Tile<D>::v_offset(r, 16 * l)) = make_uint2(w[0], w[1]);
+        *reinterpret_cast<uint2*>(vt + Int4Tile<D>::v_offset(r, 16 * l + 8)) = make_uint2(w[2], w[3]);
+      }
+    } else if (!follows) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<uint16_t*>(vt + Int4Tile<D>::v_offset(r, 16 * l + 4 * i)) =
+            static_cast<uint16_t>((i < 2 ? vc.x : vc.y) >> (16 * (i & 1)));
     }
   }
 }
 
 // Values of the rows at these slots, rounded to T: one thread reads eight dims
-// of a K row and of its V row.  A negative slot gives a zero row.
+// of a K row and of its V row (V's come with the neighbouring token's, in whole
+// words).  A negative slot gives a zero row.  Bound by the values written.
 template <typename T, int D>
-__global__ void read_int4_kernel(const int32_t* __restrict__ slots, int32_t num_tokens, int32_t num_kv_heads,
-                                 int64_t num_slots, const uint8_t* __restrict__ k_cache,
-                                 const uint8_t* __restrict__ v_cache, uint4* __restrict__ k_out,
-                                 uint4* __restrict__ v_out) {
+__global__ void __launch_bounds__(256)
+    read_int4_kernel(const int32_t* __restrict__ slots, int32_t num_tokens, int32_t num_kv_heads, int64_t num_slots,
+                     const uint8_t* __restrict__ k_cache, const uint8_t* __restrict__ v_cache,
+                     uint4* __restrict__ k_out, uint4* __restrict__ v_out) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   constexpr int C = D / 8;
-  const int64_t total = static_cast<int64_t>(num_tokens) * num_kv_heads * C;
-  for (int64_t idx = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; idx < total;
-       idx += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-    const int64_t row = idx / C;
-    const int d = static_cast<int>(idx - row * C) * 8;
-    const int64_t token = row / num_kv_heads;
-    const int head = static_cast<int>(row - token * num_kv_heads);
+  const int64_t rows = static_cast<int64_t>(num_tokens) * num_kv_heads;
+  const int c = threadIdx.x % C, d = 8 * c;
+  for (int64_t row = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) / C; row < rows;
+       row += static_cast<int64_t>(gridDim.x) * blockDim.x / C) {
+    const uint32_t token = static_cast<uint32_t>(row / num_kv_heads);
+    const int head = static_cast<int>(row - static_cast<int64_t>(token) * num_kv_heads);
     const int32_t slot = slots[token];
-    if (slot < 0 || slot >= num_slots) {
-      if (slot >= num_slots) flag_error(kErrSlot);
-      k_out[idx] = v_out[idx] = make_uint4(0, 0, 0, 0);
-      continue;
-    }
-    const int t = slot & 15;
-    const int64_t tile = (static_cast<int64_t>(slot >> 4) * num_kv_heads + head) * Int4Tile<D>::kBytes;
+    uint4 kv[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+    if (slot >= num_slots) {
+      if (c == 0) flag_error(kErrSlot);
+    } else if (slot >= 0) {
+      const int t = slot & 15;
+      const int64_t tile = (static_cast<int64_t>(slot >> 4) * num_kv_heads + head) * Int4Tile<D>::kBytes;
+      const uint8_t* kt = k_cache + tile;
+      const uint8_t* vt = v_cache + tile;
+      const uint32_t kc = *reinterpret_cast<const uint32_t*>(kt + t * (D / 2) + d / 2);
+      const uint2 vw = *reinterpret_cast<const uint2*>(vt + Int4Tile<D>::v_offset(t & ~1, d));
+      const uint32_t vc = __byte_perm(vw.x, vw.y, t & 1 ? 0x7632 : 0x5410);
+      const float2 ks = unpack2<__half>(*reinterpret_cast<const uint32_t*>(kt + Int4Tile<D>::kCodeBytes + 4 * t));
+      const float2 vs = unpack2<__half>(*reinterpret_cast<const uint32_t*>(vt + Int4Tile<D>::kCodeBytes + 4 * t));
 #pragma unroll
-    for (int is_v = 0; is_v < 2; ++is_v) {
-      const uint8_t* p = (is_v ? v_cache : k_cache) + tile;
-      uint32_t codes;
-      if (is_v) {
-        const uint32_t lo = *reinterpret_cast<const uint16_t*>(p + Int4Tile<D>::v_offset(t, d));
-        const uint32_t hi = *reinterpret_cast<const uint16_t*>(p + Int4Tile<D>::v_offset(t, d + 4));
-        codes = lo | hi << 16;
-      } else {
-        codes = *reinterpret_cast<const uint32_t*>(p + t * (D / 2) + d / 2);
+      for (int v = 0; v < 2; ++v) {
+        const uint32_t codes = v ? vc : kc;
+        const float2 sm = v ? vs : ks;
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)  // s * c is exact in float32 (11 + 4 bits): fused or not, one rounding
+          w[i] = pack2<T>(fmaf(static_cast<float>(codes >> (8 * i) & 15u), sm.x, sm.y),
+                          fmaf(static_cast<float>(codes >> (8 * i + 4) & 15u), sm.x, sm.y));
+        kv[v] = make_uint4(w[0], w[1], w[2], w[3]);
       }
-      const float2 sm = unpack2<__half>(*reinterpret_cast<const uint32_t*>(p + Int4Tile<D>::kCodeBytes + 4 * t));
-      uint32_t w[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)  // s * c is exact in float32 (11 + 4 bits): fused or not, one rounding
-        w[i] = pack2<T>(fmaf(static_cast<float>(codes >> (8 * i) & 15u), sm.x, sm.y),
-                        fmaf(static_cast<float>(codes >> (8 * i + 4) & 15u), sm.x, sm.y));
-      (is_v ? v_out : k_out)[idx] = make_uint4(w[0], w[1], w[2], w[3]);
     }
+    k_out[row * C + c] = kv[0];
+    v_out[row * C + c] = kv[1];
   }
 }
 

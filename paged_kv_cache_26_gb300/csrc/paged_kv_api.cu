@@ -259,7 +259,9 @@ void with_type_and_dim(const pkv_dims* d, F&& f) {
 // shared memory) + merge.  Both are programmatic dependent launches: each
 // may start while the kernel before it in the stream finishes, and waits
 // in-kernel (griddepcontrol.wait) before touching anything that kernel writes.
-template <typename T, int D, auto kern, typename... KernArgs>
+// MERGE_UNITS: where units are many, merge by unit (merge_units_kernel) and not
+// by row.
+template <typename T, int D, auto kern, bool MERGE_UNITS = false, typename... KernArgs>
 int launch_persistent(int warps, size_t (*smem)(int), const pkv::DecodeArgs& args, const pkv_dims* d, int max_seqs,
                       cudaStream_t stream, bool pdl, const KernArgs&... kern_args) {
   cudaError_t e = configure_smem<kern>(static_cast<int>(smem(max_seqs)));
@@ -301,7 +303,17 @@ int launch_persistent(int warps, size_t (*smem)(int), const pkv::DecodeArgs& arg
   cfg.gridDim = dim3(static_cast<unsigned>((rows + rows_per_cta - 1) / rows_per_cta));
   cfg.blockDim = dim3(pkv::kMergeWarps * 32);
   cfg.dynamicSmemBytes = (2 * static_cast<size_t>(d->num_seqs) + 1) * 4;
-  if (coop) {
+  // A warp per unit where rows are many and share their unit's plan (us, a warp
+  // per row and per unit, 4-bit pools: 1024 x 256 tokens, 8 x 4 heads 173 and 91;
+  // 512 x 512 80 and 66; 128 x 2048 57.1 and 57.0; but 64 x 2048 35.1 and 36.1,
+  // and 1024 x 256 with one head a unit 85 and 88).
+  if (MERGE_UNITS && !coop && rows >= 4096 && args.group > 1) {
+    constexpr auto merge = pkv::merge_units_kernel<T, D>;
+    cfg.gridDim = dim3(static_cast<unsigned>((units + pkv::kUnitMergeWarps - 1) / pkv::kUnitMergeWarps));
+    cfg.blockDim = dim3(pkv::kUnitMergeWarps * 32);
+    e = configure_smem<merge>(merge_smem);
+    if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, merge, args, nwarps);
+  } else if (coop) {
     constexpr auto merge = pkv::merge_persistent_kernel<T, D, true>;
     e = configure_smem<merge>(merge_smem);
     if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, merge, args, nwarps);
@@ -466,8 +478,11 @@ int decode_impl(const void* q, const void* k_new, const void* v_new, void* k_cac
     with_type_and_dim(d, [&](auto t, auto dim) {
       using U = decltype(t);
       constexpr int D = decltype(dim)::value;
-      rc4 = launch_persistent<U, D, pkv::decode_int4_kernel<U, D>>(pkv::Int4Shape<D>::kWarps, pkv::int4_smem_bytes<D>,
-                                                                  args, d, mx, stream, pdl, args);
+      constexpr int warps = pkv::Int4Shape<D>::kWarps;
+      rc4 = append ? launch_persistent<U, D, pkv::decode_int4_kernel<U, D, true>, true>(
+                         warps, pkv::int4_smem_bytes<D>, args, d, mx, stream, pdl, args)
+                   : launch_persistent<U, D, pkv::decode_int4_kernel<U, D, false>, true>(
+                         warps, pkv::int4_smem_bytes<D>, args, d, mx, stream, pdl, args);
     });
     return rc4;
   }
@@ -574,13 +589,13 @@ int append_int4_impl(const void* k_new, const void* v_new, const int32_t* slot_m
                      void* k_cache, void* v_cache, const pkv_dims* d, cudaStream_t stream) {
   const int rc = check_int4_rows(k_new, v_new, slot_mapping, num_tokens, k_cache, v_cache, d, "append_int4");
   if (rc != PKV_OK || num_tokens == 0) return rc;
-  const int64_t rows = static_cast<int64_t>(num_tokens) * d->num_kv_heads;
-  const int64_t blocks64 = (rows + 7) / 8;
-  const int blocks = static_cast<int>(blocks64 < 65536 ? blocks64 : 65536);
+  if (d->num_kv_heads > 65535) return pkv_fail(PKV_ERR_UNSUPPORTED, "append_int4: more than 65535 KV heads");
+  const int tokens_per_cta = pkv::kAppendThreads / (d->head_dim / 16);
+  const dim3 grid((num_tokens + tokens_per_cta - 1) / tokens_per_cta, d->num_kv_heads);
   const int64_t slots = static_cast<int64_t>(d->num_blocks) * pkv::kBlockSize;
   with_type_and_dim(d, [&](auto t, auto dim) {
-    pkv::append_int4_kernel<decltype(t), decltype(dim)::value><<<blocks, 256, 0, stream>>>(
-        static_cast<const uint2*>(k_new), static_cast<const uint2*>(v_new), slot_mapping, num_tokens, d->num_kv_heads,
+    pkv::append_int4_kernel<decltype(t), decltype(dim)::value><<<grid, pkv::kAppendThreads, 0, stream>>>(
+        static_cast<const uint4*>(k_new), static_cast<const uint4*>(v_new), slot_mapping, num_tokens, d->num_kv_heads,
         slots, static_cast<uint8_t*>(k_cache), static_cast<uint8_t*>(v_cache));
   });
   const cudaError_t e = cudaGetLastError();
@@ -651,9 +666,17 @@ int resize_tables_impl(const pkv::ResizeArgs& a, int32_t block_size, cudaStream_
   cudaError_t e = configure_smem<pkv::resize_tables_kernel>(
       static_cast<int>(pkv::resize_smem_bytes(pkv::kMaxResizeSeqs)));
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(resize_tables_kernel)");
-  // One CTA for what it writes in one pass, eight for prompts.
-  const unsigned cluster = a.num_slots > 4 * pkv::kResizeThreads ? 8 : 1;
-  e = launch_clusters(pkv::resize_tables_kernel, cluster, cluster, pkv::kResizeThreads, smem, stream, a);
+  // A decode step's growth is one CTA's work (64 sequences by 5 tokens and back:
+  // 8.4 us for both calls with 512 threads, 12.3 with 1024).  Prompts are a
+  // cluster's, and so may be what a call without slots gives back (256 prompts,
+  // 380,000 tokens, and back: 18.9 us with 16 CTAs, 25.8 with 8, 160 with one).
+  const bool many = a.num_slots > 4096 ||
+                    (a.num_slots == 0 && static_cast<int64_t>(a.num_seqs) * a.max_blocks > 4096);
+  const unsigned cluster = many ? pkv::kResizeCluster : 1;
+  const unsigned threads = a.num_seqs > 1024 || a.num_slots > 32768 ? pkv::kResizeThreads : 512;
+  e = cudaFuncSetAttribute(pkv::resize_tables_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(resize_tables_kernel)");
+  e = launch_clusters(pkv::resize_tables_kernel, cluster, cluster, threads, smem, stream, a);
   if (e != cudaSuccess) return cuda_fail(e, "resize_tables_kernel launch");
   return PKV_OK;
 }
@@ -680,9 +703,13 @@ int verify_draft_impl(const pkv::VerifyArgs& a, int32_t num_seqs, int32_t dtype,
       !aligned(a.accept_u, 4) || !aligned(a.sample_u, 4) || !aligned(a.context_lens, 4) ||
       !aligned(a.num_accepted, 4) || !aligned(a.out_tokens, 4) || !aligned(a.new_lens, 4))
     return pkv_fail(PKV_ERR_INVALID_ARG, "verify_draft: misaligned pointer");
-  // As many CTAs per row as have a step of 128 entries for each of their warps.
+  // As many CTAs per row as have a step of 128 entries for each of their warps,
+  // and as fit the GPU at once with the other rows' (four CTAs per SM; 64 rows of
+  // 131072 entries: 19.6 us, and 27.0 with 16 warps a CTA and as many CTAs).
   unsigned cluster = 1;
-  while (cluster < pkv::kMaxVerifyCluster && a.vocab > static_cast<int>(cluster) * pkv::kVerifyWarps * 128) cluster *= 2;
+  while (cluster < pkv::kMaxVerifyCluster && a.vocab > static_cast<int>(cluster) * pkv::kVerifyWarps * 128 &&
+         2 * cluster * static_cast<int64_t>(num_seqs) <= 4 * static_cast<int64_t>(device_sms()))
+    cluster *= 2;
   auto launch = [&](auto kern) {
     return launch_clusters(kern, static_cast<unsigned>(num_seqs) * cluster, cluster, pkv::kVerifyWarps * 32, 0, stream,
                            a);

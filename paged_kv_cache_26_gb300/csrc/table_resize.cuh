@@ -27,7 +27,9 @@
 
 namespace pkv {
 
-constexpr int kResizeThreads = 1024;
+constexpr int kResizeThreads = 1024;  // at most
+constexpr int kResizeCluster = 16;    // CTAs for prompts
+constexpr int kSlotRun = 16;          // slots a thread writes at a time, at most
 constexpr int kMaxResizeSeqs = 8192;  // four int32 arrays in shared memory
 
 struct ResizeArgs {
@@ -81,10 +83,11 @@ __global__ void __launch_bounds__(kResizeThreads, 1) resize_tables_kernel(const 
   int* s_give = s_take + B + 1;  // [B + 1] blocks given
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = cluster_rank();
-  const int nthreads = cluster_size() * kResizeThreads, gtid = rank * kResizeThreads + tid;
+  const int cta = blockDim.x, warps = cta / 32;
+  const int nthreads = cluster_size() * cta, gtid = rank * cta + tid;
 
   // ---- prefix sums: each thread takes `per` consecutive sequences
-  const int per = (B + kResizeThreads - 1) / kResizeThreads;
+  const int per = (B + cta - 1) / cta;
   const int lo = min(B, tid * per), hi = min(B, lo + per);
   const int count = *a.num_free;
   long long tok = 0;
@@ -113,8 +116,8 @@ __global__ void __launch_bounds__(kResizeThreads, 1) resize_tables_kernel(const 
   bad = __syncthreads_or(bad);
   long long btok = itok - tok, total_tok = 0;
   int btake = itake - take, bgive = igive - give, T = 0, R = 0;
-#pragma unroll 8
-  for (int w = 0; w < 32; ++w) {
+#pragma unroll 4
+  for (int w = 0; w < warps; ++w) {
     if (w < warp) btok += s_wtok[w], btake += s_wtake[w], bgive += s_wgive[w];
     total_tok += s_wtok[w], T += s_wtake[w], R += s_wgive[w];
   }
@@ -159,56 +162,87 @@ __global__ void __launch_bounds__(kResizeThreads, 1) resize_tables_kernel(const 
     return id;
   };
 
-  // ---- the slots of the gained tokens, four at a time
+  // ---- the slots of the gained tokens: each thread a run of them, for which one
+  // search, and mostly one or two blocks, will do; single slots while they are
+  // few, since then the time is one thread's chain of loads
   if (a.slot_mapping) {
     const int total = static_cast<int>(total_tok);
     const bool wide = (reinterpret_cast<uintptr_t>(a.slot_mapping) & 15) == 0;
-    for (int64_t i0 = static_cast<int64_t>(gtid) * 4; i0 < a.num_slots; i0 += static_cast<int64_t>(nthreads) * 4) {
-      int v[4] = {-1, -1, -1, -1};
-      const int i = static_cast<int>(i0);
-      if (i < total) {
-        int b = holder(s_tok, B, i), id = -1, held = -1;
+    const int run = a.num_slots <= nthreads ? 1 : a.num_slots <= 4 * nthreads ? 4 : kSlotRun;
+    for (int64_t i0 = static_cast<int64_t>(gtid) * run; i0 < a.num_slots; i0 += static_cast<int64_t>(nthreads) * run) {
+      const int begin = static_cast<int>(i0), end = static_cast<int>(min(i0 + run, static_cast<int64_t>(a.num_slots)));
+      int b = begin < total ? holder(s_tok, B, begin) : 0, held = -1, base = -1;
+      // First slot of block j of sequence b, or -1.
+      auto find = [&](int j) {
+        if (j == held) return;
+        const int nb_old = (s_old[b] + kBlockSize - 1) / kBlockSize;
+        const int id = j < nb_old ? *table(b, j) : at_position(top - 1 - (s_take[b] + j - nb_old));
+        if (id < 0 || id >= a.num_blocks) flag_error(kErrBlockId);
+        base = id < 0 || id >= a.num_blocks ? -1 : id * kBlockSize;
+        held = j;
+      };
+      for (int i = begin; i < end; i += 4) {
+        int v[4] = {-1, -1, -1, -1};
+        const int pos = s_old[b] + (i - s_tok[b]);
+        if (i + 4 <= min(end, s_tok[b + 1]) && pos % kBlockSize <= kBlockSize - 4) {  // four of one block
+          find(pos / kBlockSize);
+          if (base >= 0)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if (i + k >= total) break;
-          if (i + k >= s_tok[b + 1]) {
-            do ++b;
-            while (i + k >= s_tok[b + 1]);
-            held = -1;
-          }
-          const int pos = s_old[b] + (i + k - s_tok[b]), j = pos / kBlockSize;
-          if (j != held) {
-            const int nb_old = (s_old[b] + kBlockSize - 1) / kBlockSize;
-            id = j < nb_old ? *table(b, j) : at_position(top - 1 - (s_take[b] + j - nb_old));
-            if (id < 0 || id >= a.num_blocks) {
-              flag_error(kErrBlockId);
-              id = -1;
+            for (int k = 0; k < 4; ++k) v[k] = base + pos % kBlockSize + k;
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if (i + k >= min(end, total)) break;
+            if (i + k >= s_tok[b + 1]) {
+              do ++b;
+              while (i + k >= s_tok[b + 1]);
+              held = -1;
             }
-            held = j;
+            const int at = s_old[b] + (i + k - s_tok[b]);
+            find(at / kBlockSize);
+            v[k] = base < 0 ? -1 : base + at % kBlockSize;
           }
-          v[k] = id < 0 ? -1 : id * kBlockSize + pos % kBlockSize;
         }
-      }
-      if (wide && i + 3 < a.num_slots) {
-        *reinterpret_cast<int4*>(a.slot_mapping + i) = make_int4(v[0], v[1], v[2], v[3]);
-      } else {
-        for (int k = 0; k < 4 && i + k < a.num_slots; ++k) a.slot_mapping[i + k] = v[k];
+        if (wide && i + 4 <= end && run > 1) {
+          *reinterpret_cast<int4*>(a.slot_mapping + i) = make_int4(v[0], v[1], v[2], v[3]);
+        } else {
+          for (int k = 0; k < 4 && i + k < end; ++k) a.slot_mapping[i + k] = v[k];
+        }
       }
     }
   }
 
   // ---- table entries of the taken blocks, and the given blocks that stay on the list
-  for (int i = gtid; i < T; i += nthreads) {
-    const int b = holder(s_take, B, i);
-    const int nb_old = (s_old[b] + kBlockSize - 1) / kBlockSize;
-    const int id = at_position(top - 1 - i);
-    if (id < 0 || id >= a.num_blocks) flag_error(kErrBlockId);
-    *table(b, nb_old + i - s_take[b]) = id;
+  // (four at a time: their searches and loads overlap)
+  constexpr int kIlp = 4;
+  for (int i0 = gtid; i0 < T; i0 += kIlp * nthreads) {
+    int id[kIlp], b[kIlp];
+#pragma unroll
+    for (int k = 0; k < kIlp; ++k) {
+      const int i = i0 + k * nthreads;
+      b[k] = i < T ? holder(s_take, B, i) : 0;
+      id[k] = i < T ? at_position(top - 1 - i) : 0;
+    }
+#pragma unroll
+    for (int k = 0; k < kIlp; ++k) {
+      const int i = i0 + k * nthreads;
+      if (id[k] < 0 || id[k] >= a.num_blocks) flag_error(kErrBlockId);
+      if (i < T) *table(b[k], (s_old[b[k]] + kBlockSize - 1) / kBlockSize + i - s_take[b[k]]) = id[k];
+    }
   }
-  for (int r = T + gtid; r < R; r += nthreads) {
-    const int id = at_position(top - 1 - r);
-    if (id < 0 || id >= a.num_blocks) flag_error(kErrBlockId);
-    a.free_blocks[top - 1 - r] = id;
+  for (int r0 = T + gtid; r0 < R; r0 += kIlp * nthreads) {
+    int id[kIlp];
+#pragma unroll
+    for (int k = 0; k < kIlp; ++k) {
+      const int r = r0 + k * nthreads;
+      id[k] = r < R ? at_position(top - 1 - r) : 0;
+    }
+#pragma unroll
+    for (int k = 0; k < kIlp; ++k) {
+      const int r = r0 + k * nthreads;
+      if (id[k] < 0 || id[k] >= a.num_blocks) flag_error(kErrBlockId);
+      if (r < R) a.free_blocks[top - 1 - r] = id[k];
+    }
   }
   if (a.token_offsets)
     for (int i = gtid; i <= B; i += nthreads) a.token_offsets[i] = s_tok[i];

@@ -16,8 +16,8 @@
 // Bound by reading one row of p and, where a draft was rejected, one of q.  A
 // cluster of CTAs shares a sequence's row, each warp a contiguous piece of it:
 // 64-bit sums per warp, then per CTA, exchanged through distributed shared
-// memory; the warp whose piece holds the draw reads it again (from L2) to find
-// the token.
+// memory; the CTA that holds the draw reads the one piece it lies in again (from
+// L2), all its warps together, to find the token.
 #pragma once
 
 #include "pkv_device.cuh"
@@ -25,7 +25,7 @@
 
 namespace pkv {
 
-constexpr int kVerifyWarps = 16;
+constexpr int kVerifyWarps = 8;
 constexpr int kMaxVerifyCluster = 8;
 constexpr int kMaxDrafts = 31;
 constexpr int kProbBits = 40;    // weights are whole numbers of 2^-40
@@ -51,9 +51,23 @@ __device__ __forceinline__ float prob_value(float v) { return v; }
 __device__ __forceinline__ float prob_value(__half v) { return __half2float(v); }
 __device__ __forceinline__ float prob_value(__nv_bfloat16 v) { return __bfloat162float(v); }
 
-// A probability as a whole number of 2^-40; below 0 and NaN count as 0, above 1 as 1.
+// A probability p in [0, 1] as a whole number w of 2^-40 (to nearest, half to
+// even), in float32 operations and without a 64-bit conversion: adding 64
+// rounds p to a multiple of 2^-17, h; p - h is exact, at most 2^-18, and its
+// product with 2^40 is rounded by adding 1.5 * 2^23.  w = 2^23 (2^17 h) + low,
+// the two whole numbers left in the sums' low bits, on top of constants.
+constexpr uint32_t kHighBias = 0x42800000u;  // bits of 64
+constexpr uint32_t kLowBias = 0x4b400000u;   // bits of 1.5 * 2^23
+__device__ __forceinline__ void weight_parts(float p, uint32_t& high, uint32_t& low) {
+  const float t = __fadd_rn(p, 64.f);
+  const float r = __fsub_rn(p, __fsub_rn(t, 64.f));
+  high = __float_as_uint(t);
+  low = __float_as_uint(fmaf(r, 1099511627776.f, 12582912.f));
+}
 __device__ __forceinline__ unsigned long long prob_weight(float p) {
-  return p > 0.f ? __float2ull_rn(fminf(p, 1.f) * 1099511627776.f) : 0ull;
+  uint32_t h, l;
+  weight_parts(p, h, l);
+  return (static_cast<unsigned long long>(h - kHighBias) << 23) + static_cast<long long>(static_cast<int32_t>(l - kLowBias));
 }
 
 // Four consecutive values from i on (those at or past V as 0).
@@ -86,6 +100,7 @@ __global__ void __launch_bounds__(kVerifyWarps * 32) verify_draft_kernel(const V
   __shared__ int s_accepted, s_drafts;
   __shared__ unsigned long long s_warp[2][kVerifyWarps];  // [residual, p] sums of each warp's piece
   __shared__ unsigned long long s_total[2];               // of this CTA's, read by the cluster
+  __shared__ unsigned long long s_scan[kVerifyWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int C = cluster_size(), rank = cluster_rank();
   const int b = blockIdx.x / C, K = a.num_draft, V = a.vocab;
@@ -139,31 +154,49 @@ __global__ void __launch_bounds__(kVerifyWarps * 32) verify_draft_kernel(const V
   const int first = (rank * kVerifyWarps + warp) * steps * 128;
   constexpr uintptr_t kAlign = 4 * sizeof(T) - 1;
   const bool wide = ((reinterpret_cast<uintptr_t>(prow) | reinterpret_cast<uintptr_t>(qrow)) & kAlign) == 0;
-  auto weights = [&](int i, unsigned long long (&w)[4], unsigned long long (&wp)[4]) {
-    float p[4], q[4] = {0.f, 0.f, 0.f, 0.f};
-    load4<T>(prow, i, V, wide, p);
-    if (qrow) load4<T>(qrow, i, V, wide, q);
+  // Entries i..i+3 of p and of m = min(p, q), limited to [0, 1] (a NaN counts as
+  // 0).  Weights are monotone, so max(w(p) - w(q), 0) = w(p) - w(m).
+  const bool residual = rejected;
+  auto load = [&](int i, float (&p)[4], float (&m)[4]) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) p[k] = m[k] = 0.f;
+    if (i < V) {
+      load4<T>(prow, i, V, wide, p);
+      if (qrow) load4<T>(qrow, i, V, wide, m);
+    }
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      wp[k] = prob_weight(p[k]);
-      const unsigned long long off = i + k == gone ? 1ull << kProbBits : prob_weight(q[k]);
-      w[k] = wp[k] > off ? wp[k] - off : 0ull;
+      p[k] = __saturatef(p[k]);
+      m[k] = fminf(p[k], i + k == gone ? 1.f : __saturatef(m[k]));
     }
   };
-  unsigned long long sum = 0, sum_p = 0;
-#pragma unroll 4
-  for (int s = 0; s < steps; ++s) {
-    const int i = first + s * 128 + lane * 4;
-    if (i < V) {
-      unsigned long long w[4], wp[4];
-      weights(i, w, wp);
-      sum += (w[0] + w[1]) + (w[2] + w[3]);
-      sum_p += (wp[0] + wp[1]) + (wp[2] + wp[3]);
-    }
+  long long sum_p = 0, sum_m = 0;
+  constexpr int kUnroll = 4;  // 16 entries a lane: the low parts' sum stays below 2^26
+  for (int s0 = 0; s0 < steps; s0 += kUnroll) {
+    float p[kUnroll][4], m[kUnroll][4];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) load(s0 + u < steps ? first + (s0 + u) * 128 + lane * 4 : V, p[u], m[u]);
+    auto add = [&](const float (&v)[kUnroll][4], long long& sum) {
+      uint32_t high = 0, low = 0;
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint32_t h, l;
+          weight_parts(v[u][k], h, l);
+          high += h;
+          low += l;
+        }
+      constexpr uint32_t n = 4 * kUnroll;
+      sum += (static_cast<long long>(high - n * kHighBias) << 23) + static_cast<int32_t>(low - n * kLowBias);
+    };
+    add(p, sum_p);
+    if (residual) add(m, sum_m);
   }
+  unsigned long long sum = sum_p - sum_m;
   sum = warp_sum(sum);
-  sum_p = warp_sum(sum_p);
-  if (lane == 0) s_warp[0][warp] = sum, s_warp[1][warp] = sum_p;
+  const unsigned long long whole = warp_sum(sum_p);
+  if (lane == 0) s_warp[0][warp] = sum, s_warp[1][warp] = whole;
   __syncthreads();
   if (tid < 2) {
     unsigned long long t = 0;
@@ -191,16 +224,19 @@ __global__ void __launch_bounds__(kVerifyWarps * 32) verify_draft_kernel(const V
   const unsigned long long all = which ? total[1] : total[0];
   const unsigned long long goal = __umul64hi(all, u << (64 - kDrawBits));
   unsigned long long before = warp_sum(lane >= rank ? 0ull : which ? part[1] : part[0]);
-  for (int w = 0; w < warp; ++w) before += s_warp[which][w];
-  const unsigned long long mine = s_warp[which][warp];
-  if (goal >= before && goal - before < mine) {  // one warp of the cluster (none if the total is 0)
+  if (goal >= before && goal - before < s_total[which]) {  // one CTA of the cluster (none if the total is 0)
+    int piece = 0;
     unsigned long long left = goal - before;
-    for (int s = 0; s < steps; ++s) {
-      const int i = first + s * 128 + lane * 4;
-      unsigned long long w[4] = {0, 0, 0, 0}, wp[4] = {0, 0, 0, 0};
-      if (i < V) weights(i, w, wp);
+    for (; left >= s_warp[which][piece]; ++piece) left -= s_warp[which][piece];
+    const int begin = (rank * kVerifyWarps + piece) * steps * 128;
+    for (int i0 = 0; i0 < steps * 128; i0 += kVerifyWarps * 128) {
+      const bool here = i0 + tid * 4 < steps * 128;
+      const int i = begin + i0 + tid * 4;
+      float p[4], m[4];
+      unsigned long long w[4];
+      load(here ? i : V, p, m);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) w[k] = which ? wp[k] : w[k];
+      for (int k = 0; k < 4; ++k) w[k] = prob_weight(p[k]) - (residual && !which ? prob_weight(m[k]) : 0ull);
       const unsigned long long own = (w[0] + w[1]) + (w[2] + w[3]);
       unsigned long long incl = own;
 #pragma unroll
@@ -208,15 +244,21 @@ __global__ void __launch_bounds__(kVerifyWarps * 32) verify_draft_kernel(const V
         const unsigned long long t = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += t;
       }
-      const unsigned hit = __ballot_sync(0xffffffffu, left < incl);
-      if (hit) {
-        if (lane == __ffs(hit) - 1) {
-          const unsigned long long r1 = incl - own + w[0], r2 = r1 + w[1], r3 = r2 + w[2];
-          a.out_tokens[static_cast<int64_t>(b) * (K + 1) + acc] = i + (left >= r1) + (left >= r2) + (left >= r3);
-        }
-        break;
+      __syncthreads();  // the previous pass's sums (and the first time s_warp's) have been read
+      if (lane == 31) s_scan[warp] = incl;
+      __syncthreads();
+      unsigned long long run = incl - own, all_here = 0;
+      for (int v = 0; v < kVerifyWarps; ++v) {
+        const unsigned long long t = s_scan[v];
+        if (v < warp) run += t;
+        all_here += t;
       }
-      left -= __shfl_sync(0xffffffffu, incl, 31);
+      if (left >= run && left - run < own) {
+        const unsigned long long r1 = run + w[0], r2 = r1 + w[1], r3 = r2 + w[2];
+        a.out_tokens[static_cast<int64_t>(b) * (K + 1) + acc] = i + (left >= r1) + (left >= r2) + (left >= r3);
+      }
+      if (left < all_here) break;  // the same in every thread
+      left -= all_here;
     }
   }
   if (rank == 0) {

@@ -290,6 +290,32 @@ def test_verify_borders_of_the_draw():
         assert a.item() == want and out.tolist() == ([[0, 1]] if want else [[1, -1]])
 
 
+def test_verify_weights_around_the_small_entries_border():
+    """Entries around 2^-17, 2^-40 and ties of the rounding: the draw counts them as the oracle does."""
+    small = np.float32(2.0 ** -17)
+    vals = [np.nextafter(small, np.float32(0)), small, np.nextafter(small, np.float32(1)), 2.0 ** -41, 1.5 * 2.0 ** -40,
+            2.5 * 2.0 ** -40, 3.5 * 2.0 ** -40, 2.0 ** -40, 2.0 ** -126, 1e-45, 0.0, 1.0, np.nextafter(np.float32(1), np.float32(0))]
+    g = np.random.default_rng(0)
+    p = np.array([vals[i] for i in g.integers(0, len(vals) - 3, 700)], np.float32)   # small ones only
+    p[::97] = 2.0 ** -20
+    w = [serving.weight(float(v)) for v in p]
+    total = sum(w)
+    us = np.concatenate([g.random(200), [0.0, 1 - 2.0 ** -24]]).astype(np.float32)
+    t = torch.from_numpy(p).to(DEV).expand(len(us), 1, 700)
+    _, out, _ = pkv.paged_verify_draft(t, None, torch.empty(len(us), 0, dtype=torch.int32, device=DEV),
+                                       torch.empty(len(us), 0, device=DEV), torch.from_numpy(us).to(DEV))
+    assert out[:, 0].tolist() == [serving.draw(w, float(u)) for u in us]
+    for v in vals:                                             # one entry alone, another of the same weight after it
+        q = np.array([v, v, 0.0], np.float32)
+        w = [serving.weight(float(x)) for x in q]
+        us = np.array([0.49999, 0.5, 0.75], np.float32)
+        t = torch.from_numpy(q).to(DEV).expand(3, 1, 3)
+        _, out, _ = pkv.paged_verify_draft(t, None, torch.empty(3, 0, dtype=torch.int32, device=DEV),
+                                           torch.empty(3, 0, device=DEV), torch.from_numpy(us).to(DEV))
+        assert out[:, 0].tolist() == [serving.draw(w, float(u)) for u in us], v
+    assert total > 0
+
+
 def test_verify_rows_without_a_residual_and_without_mass():
     V = 300
     t = torch.full((3, 2, V), 0.0)
