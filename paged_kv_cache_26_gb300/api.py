@@ -739,17 +739,16 @@ def paged_verify_draft(target_probs: torch.Tensor, draft_probs: Optional[torch.T
             _explain(dev, ("draft_lens", draft_lens, _i32))
             raise ValueError("draft_lens must be [num_seqs]")
         n = draft_lens.data_ptr()
+    lens = None
     if context_lens is not None:
         if not (context_lens.get_device() == dev and context_lens.dtype == _i32 and context_lens.shape == (B,) and
                 context_lens.is_contiguous()):
             _explain(dev, ("context_lens", context_lens, _i32))
             raise ValueError("context_lens must be [num_seqs]")
         ctx = context_lens.data_ptr()
-    # One allocation for the three results.
-    accepted, lens, tokens = torch.empty((B * (K + 3),), dtype=_i32, device=dev).split_with_sizes((B, B, B * (K + 1)))
-    tokens = tokens.view(B, K + 1)
-    if context_lens is None:
-        lens = None
+        lens = torch.empty_like(context_lens)
+    accepted = torch.empty((B,), dtype=_i32, device=dev)
+    tokens = torch.empty((B, K + 1), dtype=_i32, device=dev)
     dims = PkvVerifyDims(B, K, V, code, t_stride[0], t_stride[1], d_stride[0], d_stride[1])
     _call("paged_verify_draft", dev, stream,
           (target_probs.data_ptr(), q, draft_tokens.data_ptr(), n, accept_u.data_ptr(), sample_u.data_ptr(), ctx,

@@ -110,11 +110,13 @@ __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
 }
 
 // 16 consecutive values of one row (packed), the row spread over L = D/16
-// neighbouring lanes: their codes as four 16-bit quads (quad i = dims 4i..4i+3)
-// and the row's pair.  Extremes are found on the packed values (exact).  A code
-// needs no lower limit: x - minimum is at least minus half a float16 step of
+// neighbouring lanes: their codes in order, eight to a word, and the row's pair.
+// Extremes are found on the packed values (exact).  Codes need no limits, apart
+// from rows told by `odd`: x - minimum is at least minus half a float16 step of
 // the minimum, and the scale, if above 0, at least such a step, so the quotient
-// is -0.5 or more and rounds to 0.  Rounding is by adding 1.5 * 2^23.
+// is -0.5 or more and rounds to 0; the largest is checked once for the row.
+// Rounding is by adding 1.5 * 2^23, which leaves the code in the low bits: a
+// word is the sum of bits * 16^k, less what the upper bits add up to (mod 2^32).
 template <typename T, int L>
 __device__ __forceinline__ uint2 int4_quantise16(const uint4 (&raw)[2], uint32_t& pair) {
   uint32_t lo = word_of(raw[0], 0), hi = lo;
@@ -131,33 +133,42 @@ __device__ __forceinline__ uint2 int4_quantise16(const uint4 (&raw)[2], uint32_t
   for (int o = 1; o < L; o <<= 1) ext = min2<T>(ext, __shfl_xor_sync(0xffffffffu, ext, o));
   const float2 e = unpack2<T>(ext);
   const float mn = limit_f16(e.x), mx = limit_f16(-e.y);
-  const bool wide = !(e.x >= -kF16Max && -e.y <= kF16Max);  // some value is past the float16 range
   const Int4Row r = int4_row(mn, mx);
   pair = r.pair;
+  constexpr float kMagic = 12582912.f;           // 1.5 * 2^23
+  constexpr uint32_t kExcess = 0x4b400000u * 0x11111111u;  // its bits times 1 + 16 + .. + 16^7
   uint32_t out[2];
+  // Values past the float16 range, a quotient that rounds above 15 (a scale in
+  // float16's subnormal range), or a NaN: limited one by one.
+  const bool odd = !(e.x >= -kF16Max && -e.y <= kF16Max && __fmul_rn(__fsub_rn(mx, r.low), r.inv) < 15.5f);
+  if (odd) {
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    float q[2];  // two quads as whole numbers below 2^16
+    for (int h = 0; h < 2; ++h) {
+      out[h] = 0;
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      q[k] = 0.f;
-#pragma unroll
-      for (int i = 1; i >= 0; --i) {
-        float2 x = unpack2<T>(word_of(raw[h], 2 * k + i));
-        if (wide) x = make_float2(limit_f16(x.x), limit_f16(x.y));
-        const float c0 = fminf(__fmul_rn(__fsub_rn(x.x, r.low), r.inv), 15.f);
-        const float c1 = fminf(__fmul_rn(__fsub_rn(x.y, r.low), r.inv), 15.f);
-        const float r0 = __fsub_rn(__fadd_rn(c0, 12582912.f), 12582912.f);
-        const float r1 = __fsub_rn(__fadd_rn(c1, 12582912.f), 12582912.f);
-        q[k] = fmaf(q[k], 256.f, fmaf(r1, 16.f, r0));
+      for (int i = 3; i >= 0; --i) {
+        const float2 x = unpack2<T>(word_of(raw[h], i));
+        out[h] = out[h] << 8 | int4_code(limit_f16(x.y), r) << 4 | int4_code(limit_f16(x.x), r);
       }
     }
-    out[h] = __byte_perm(__float_as_uint(q[0] + 8388608.f), __float_as_uint(q[1] + 8388608.f), 0x5410);
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t w = 0;
+#pragma unroll
+      for (int i = 3; i >= 0; --i) {
+        const float2 x = unpack2<T>(word_of(raw[h], i));
+        w = w * 16 + __float_as_uint(__fadd_rn(__fmul_rn(__fsub_rn(x.y, r.low), r.inv), kMagic));
+        w = w * 16 + __float_as_uint(__fadd_rn(__fmul_rn(__fsub_rn(x.x, r.low), r.inv), kMagic));
+      }
+      out[h] = w - kExcess;
+    }
   }
   return make_uint2(out[0], out[1]);
 }
 
 constexpr int kAppendThreads = 256;
+constexpr int kReadThreads = 256;
 
 // Slot-mapped append into a 4-bit pool.  A CTA takes kAppendThreads / L
 // neighbouring tokens of one KV head, L = D/16 lanes a row with 16 values each.
@@ -234,47 +245,49 @@ __global__ void __launch_bounds__(kAppendThreads)
 // of a K row and of its V row (V's come with the neighbouring token's, in whole
 // words).  A negative slot gives a zero row.  Bound by the values written.
 template <typename T, int D>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kReadThreads)
     read_int4_kernel(const int32_t* __restrict__ slots, int32_t num_tokens, int32_t num_kv_heads, int64_t num_slots,
                      const uint8_t* __restrict__ k_cache, const uint8_t* __restrict__ v_cache,
                      uint4* __restrict__ k_out, uint4* __restrict__ v_out) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  constexpr int C = D / 8;
-  const int64_t rows = static_cast<int64_t>(num_tokens) * num_kv_heads;
-  const int c = threadIdx.x % C, d = 8 * c;
-  for (int64_t row = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) / C; row < rows;
-       row += static_cast<int64_t>(gridDim.x) * blockDim.x / C) {
-    const uint32_t token = static_cast<uint32_t>(row / num_kv_heads);
-    const int head = static_cast<int>(row - static_cast<int64_t>(token) * num_kv_heads);
-    const int32_t slot = slots[token];
-    uint4 kv[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-    if (slot >= num_slots) {
-      if (c == 0) flag_error(kErrSlot);
-    } else if (slot >= 0) {
-      const int t = slot & 15;
-      const int64_t tile = (static_cast<int64_t>(slot >> 4) * num_kv_heads + head) * Int4Tile<D>::kBytes;
-      const uint8_t* kt = k_cache + tile;
-      const uint8_t* vt = v_cache + tile;
-      const uint32_t kc = *reinterpret_cast<const uint32_t*>(kt + t * (D / 2) + d / 2);
-      const uint2 vw = *reinterpret_cast<const uint2*>(vt + Int4Tile<D>::v_offset(t & ~1, d));
-      const uint32_t vc = __byte_perm(vw.x, vw.y, t & 1 ? 0x7632 : 0x5410);
-      const float2 ks = unpack2<__half>(*reinterpret_cast<const uint32_t*>(kt + Int4Tile<D>::kCodeBytes + 4 * t));
-      const float2 vs = unpack2<__half>(*reinterpret_cast<const uint32_t*>(vt + Int4Tile<D>::kCodeBytes + 4 * t));
+  constexpr int C = D / 8, kTokens = kReadThreads / C;
+  const int c = threadIdx.x % C, d = 8 * c, head = blockIdx.y;
+  const int64_t token = static_cast<int64_t>(blockIdx.x) * kTokens + threadIdx.x / C;
+  if (token >= num_tokens) return;
+  const int32_t slot = slots[token];
+  uint4 kv[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+  if (slot >= num_slots) {
+    if (c == 0) flag_error(kErrSlot);
+  } else if (slot >= 0) {
+    const int t = slot & 15;
+    const int64_t tile = (static_cast<int64_t>(slot >> 4) * num_kv_heads + head) * Int4Tile<D>::kBytes;
+    const uint8_t* kt = k_cache + tile;
+    const uint8_t* vt = v_cache + tile;
+    const uint32_t kc = *reinterpret_cast<const uint32_t*>(kt + t * (D / 2) + d / 2);
+    const uint2 vw = *reinterpret_cast<const uint2*>(vt + Int4Tile<D>::v_offset(t & ~1, d));
+    const uint32_t vc = __byte_perm(vw.x, vw.y, t & 1 ? 0x7632 : 0x5410);
+    const float2 ks = unpack2<__half>(*reinterpret_cast<const uint32_t*>(kt + Int4Tile<D>::kCodeBytes + 4 * t));
+    const float2 vs = unpack2<__half>(*reinterpret_cast<const uint32_t*>(vt + Int4Tile<D>::kCodeBytes + 4 * t));
 #pragma unroll
-      for (int v = 0; v < 2; ++v) {
-        const uint32_t codes = v ? vc : kc;
-        const float2 sm = v ? vs : ks;
-        uint32_t w[4];
+    for (int v = 0; v < 2; ++v) {
+      const uint32_t codes = v ? vc : kc;
+      const float2 sm = v ? vs : ks;
+      const uint32_t even = codes & 0x0f0f0f0fu, odd = codes >> 4 & 0x0f0f0f0fu;
+      uint32_t w[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)  // s * c is exact in float32 (11 + 4 bits): fused or not, one rounding
-          w[i] = pack2<T>(fmaf(static_cast<float>(codes >> (8 * i) & 15u), sm.x, sm.y),
-                          fmaf(static_cast<float>(codes >> (8 * i + 4) & 15u), sm.x, sm.y));
-        kv[v] = make_uint4(w[0], w[1], w[2], w[3]);
+      for (int i = 0; i < 4; ++i) {
+        // The code as the low byte of 2^23's bits; s * c is exact in float32
+        // (11 + 4 bits): fused or not, one rounding.
+        const float c0 = __uint_as_float(__byte_perm(even, 0x4b000000u, 0x7650 + i)) - 8388608.f;
+        const float c1 = __uint_as_float(__byte_perm(odd, 0x4b000000u, 0x7650 + i)) - 8388608.f;
+        w[i] = pack2<T>(fmaf(c0, sm.x, sm.y), fmaf(c1, sm.x, sm.y));
       }
+      kv[v] = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    k_out[row * C + c] = kv[0];
-    v_out[row * C + c] = kv[1];
   }
+  const int64_t at = (token * num_kv_heads + head) * C + c;
+  k_out[at] = kv[0];
+  v_out[at] = kv[1];
 }
 
 }  // namespace pkv

@@ -580,6 +580,7 @@ int check_int4_rows(const void* k, const void* v, const int32_t* slot_mapping, i
   if (num_tokens == 0) return PKV_OK;
   if (!k || !v || !slot_mapping || !k_cache || !v_cache)
     return pkv_fail(PKV_ERR_INVALID_ARG, std::string(what) + ": NULL pointer");
+  if (d->num_kv_heads > 65535) return pkv_fail(PKV_ERR_UNSUPPORTED, std::string(what) + ": more than 65535 KV heads");
   if (!aligned(k, 16) || !aligned(v, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(slot_mapping, 4))
     return pkv_fail(PKV_ERR_INVALID_ARG, std::string(what) + ": misaligned pointer (values and caches need 16 bytes)");
   return PKV_OK;
@@ -589,9 +590,9 @@ int append_int4_impl(const void* k_new, const void* v_new, const int32_t* slot_m
                      void* k_cache, void* v_cache, const pkv_dims* d, cudaStream_t stream) {
   const int rc = check_int4_rows(k_new, v_new, slot_mapping, num_tokens, k_cache, v_cache, d, "append_int4");
   if (rc != PKV_OK || num_tokens == 0) return rc;
-  if (d->num_kv_heads > 65535) return pkv_fail(PKV_ERR_UNSUPPORTED, "append_int4: more than 65535 KV heads");
   const int tokens_per_cta = pkv::kAppendThreads / (d->head_dim / 16);
-  const dim3 grid((num_tokens + tokens_per_cta - 1) / tokens_per_cta, d->num_kv_heads);
+  const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(num_tokens) + tokens_per_cta - 1) / tokens_per_cta),
+                  d->num_kv_heads);
   const int64_t slots = static_cast<int64_t>(d->num_blocks) * pkv::kBlockSize;
   with_type_and_dim(d, [&](auto t, auto dim) {
     pkv::append_int4_kernel<decltype(t), decltype(dim)::value><<<grid, pkv::kAppendThreads, 0, stream>>>(
@@ -607,12 +608,12 @@ int read_int4_impl(const int32_t* slot_mapping, int32_t num_tokens, const void* 
                    void* k_out, void* v_out, const pkv_dims* d, cudaStream_t stream) {
   const int rc = check_int4_rows(k_out, v_out, slot_mapping, num_tokens, k_cache, v_cache, d, "read_int4");
   if (rc != PKV_OK || num_tokens == 0) return rc;
-  const int64_t total = static_cast<int64_t>(num_tokens) * d->num_kv_heads * (d->head_dim / 8);
-  const int64_t blocks64 = (total + 255) / 256;
-  const int blocks = static_cast<int>(blocks64 < 65536 ? blocks64 : 65536);
+  const int tokens_per_cta = pkv::kReadThreads / (d->head_dim / 8);
+  const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(num_tokens) + tokens_per_cta - 1) / tokens_per_cta),
+                  d->num_kv_heads);
   const int64_t slots = static_cast<int64_t>(d->num_blocks) * pkv::kBlockSize;
   with_type_and_dim(d, [&](auto t, auto dim) {
-    pkv::read_int4_kernel<decltype(t), decltype(dim)::value><<<blocks, 256, 0, stream>>>(
+    pkv::read_int4_kernel<decltype(t), decltype(dim)::value><<<grid, pkv::kReadThreads, 0, stream>>>(
         slot_mapping, num_tokens, d->num_kv_heads, slots, static_cast<const uint8_t*>(k_cache),
         static_cast<const uint8_t*>(v_cache), static_cast<uint4*>(k_out), static_cast<uint4*>(v_out));
   });
