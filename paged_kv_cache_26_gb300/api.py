@@ -689,15 +689,6 @@ def paged_kv_resize_tables(context_lens: torch.Tensor, new_lens: torch.Tensor, b
 _PROB_CODE = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
 
 
-def _need_rows(name: str, t: torch.Tensor, dev: int, shape, dtype):
-    if t.get_device() != dev or dev < 0:
-        raise ValueError(f"{name} must be a CUDA tensor on the device of the others")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 3 or tuple(t.shape) != tuple(shape) or (t.shape[2] > 1 and t.stride(2) != 1):
-        raise ValueError(f"{name} must be {list(shape)} with a unit stride along the vocabulary")
-
-
 def paged_verify_draft(target_probs: torch.Tensor, draft_probs: Optional[torch.Tensor], draft_tokens: torch.Tensor,
                        accept_u: torch.Tensor, sample_u: torch.Tensor, draft_lens: Optional[torch.Tensor] = None,
                        context_lens: Optional[torch.Tensor] = None, stream=None):
@@ -713,46 +704,49 @@ def paged_verify_draft(target_probs: torch.Tensor, draft_probs: Optional[torch.T
     new_lens int32 [B]: context_lens without the rejected drafts, or None)."""
     dev, dtype = target_probs.get_device(), target_probs.dtype
     code, xs, ts = _PROB_CODE.get(dtype), draft_tokens.shape, target_probs.shape
+    t_stride = target_probs.stride()
     if not (dev >= 0 and code is not None and draft_tokens.get_device() == dev and accept_u.get_device() == dev and
-            sample_u.get_device() == dev and draft_tokens.dtype == _i32 and accept_u.dtype == _f32 and
-            sample_u.dtype == _f32 and draft_tokens.is_contiguous() and accept_u.is_contiguous() and
-            sample_u.is_contiguous() and len(xs) == 2 and accept_u.shape == xs and sample_u.shape == xs[:1] and
-            len(ts) == 3 and ts[:2] == (xs[0], xs[1] + 1)):
+            sample_u.get_device() == dev and draft_tokens.dtype is _i32 and accept_u.dtype is _f32 and
+            sample_u.dtype is _f32 and draft_tokens.is_contiguous() and accept_u.is_contiguous() and
+            sample_u.is_contiguous() and len(xs) == 2 and accept_u.shape == xs and len(ts) == 3 and
+            ts[0] == xs[0] and ts[1] == xs[1] + 1 and sample_u.dim() == 1 and sample_u.numel() == xs[0] and
+            (t_stride[2] == 1 or ts[2] <= 1)):
         if code is None:
             raise ValueError("target_probs must be float32, float16 or bfloat16")
         _explain(dev, ("draft_tokens", draft_tokens, _i32), ("accept_u", accept_u, _f32), ("sample_u", sample_u, _f32))
         raise ValueError("draft_tokens / accept_u must be [num_seqs][num_draft], sample_u [num_seqs], target_probs "
-                         "[num_seqs][num_draft + 1][vocab] on their device")
+                         "[num_seqs][num_draft + 1][vocab] on their device, with a unit stride along the vocabulary")
     B, K = xs
     V = ts[2]
-    t_stride = target_probs.stride()
-    if t_stride[2] != 1:
-        _need_rows("target_probs", target_probs, dev, (B, K + 1, V), dtype)
-    q, d_stride = 0, (0, 0)
+    q = d_seq = d_row = n = ctx = 0
     if draft_probs is not None:
-        _need_rows("draft_probs", draft_probs, dev, (B, K, V), dtype)
-        q, d_stride = draft_probs.data_ptr(), draft_probs.stride()
-    n = ctx = 0
+        ds, d_stride = draft_probs.shape, draft_probs.stride()
+        if not (draft_probs.get_device() == dev and draft_probs.dtype is dtype and len(ds) == 3 and ds[0] == B and
+                ds[1] == K and ds[2] == V and (d_stride[2] == 1 or V <= 1)):
+            raise ValueError("draft_probs must be [num_seqs][num_draft][vocab] of target_probs' type and on its device, "
+                             "with a unit stride along the vocabulary")
+        q, (d_seq, d_row, _) = draft_probs.data_ptr(), d_stride
     if draft_lens is not None:
-        if not (draft_lens.get_device() == dev and draft_lens.dtype == _i32 and draft_lens.shape == (B,) and
-                draft_lens.is_contiguous()):
+        if not (draft_lens.get_device() == dev and draft_lens.dtype is _i32 and draft_lens.dim() == 1 and
+                draft_lens.numel() == B and draft_lens.is_contiguous()):
             _explain(dev, ("draft_lens", draft_lens, _i32))
             raise ValueError("draft_lens must be [num_seqs]")
         n = draft_lens.data_ptr()
-    lens = None
+    lens, lens_ptr = None, 0
     if context_lens is not None:
-        if not (context_lens.get_device() == dev and context_lens.dtype == _i32 and context_lens.shape == (B,) and
-                context_lens.is_contiguous()):
+        if not (context_lens.get_device() == dev and context_lens.dtype is _i32 and context_lens.dim() == 1 and
+                context_lens.numel() == B and context_lens.is_contiguous()):
             _explain(dev, ("context_lens", context_lens, _i32))
             raise ValueError("context_lens must be [num_seqs]")
         ctx = context_lens.data_ptr()
         lens = torch.empty_like(context_lens)
+        lens_ptr = lens.data_ptr()
     accepted = torch.empty((B,), dtype=_i32, device=dev)
     tokens = torch.empty((B, K + 1), dtype=_i32, device=dev)
-    dims = PkvVerifyDims(B, K, V, code, t_stride[0], t_stride[1], d_stride[0], d_stride[1])
+    dims = PkvVerifyDims(B, K, V, code, t_stride[0], t_stride[1], d_seq, d_row)
     _call("paged_verify_draft", dev, stream,
           (target_probs.data_ptr(), q, draft_tokens.data_ptr(), n, accept_u.data_ptr(), sample_u.data_ptr(), ctx,
-           ctypes.byref(dims), accepted.data_ptr(), tokens.data_ptr(), lens.data_ptr() if lens is not None else 0))
+           ctypes.byref(dims), accepted.data_ptr(), tokens.data_ptr(), lens_ptr))
     return accepted, tokens, lens
 
 

@@ -296,9 +296,13 @@ int launch_persistent(int warps, size_t (*smem)(int), const pkv::DecodeArgs& arg
   // Two or more warp shares per unit on average: rows have many pieces, so
   // fold up to 16 per round trip (fewer registers leave room for more merge
   // CTAs beside the decode grid, which pays when rows are many and short).
-  const bool wide = !coop && nwarps >= 2 * units;
-  const int merge_smem = static_cast<int>((2 * static_cast<size_t>(max_persistent_seqs(d, kPool16)) + 1) * 4);
   const int rows = d->num_seqs * d->num_q_heads;
+  // Beside 4-bit decode CTAs no merge CTA fits whatever its registers, so there
+  // the small ones are better as soon as rows are many (us, small and wide: 64 x
+  // 2048 tokens, 32 heads 33.6 and 35.2; 48 sequences 28.9 and 29.4; 32 23.9 and
+  // 22.6).
+  const bool wide = !coop && nwarps >= 2 * units && !(MERGE_UNITS && rows > 8 * device_sms());
+  const int merge_smem = static_cast<int>((2 * static_cast<size_t>(max_persistent_seqs(d, kPool16)) + 1) * 4);
   const int rows_per_cta = coop ? 1 : pkv::kMergeWarps;
   cfg.gridDim = dim3(static_cast<unsigned>((rows + rows_per_cta - 1) / rows_per_cta));
   cfg.blockDim = dim3(pkv::kMergeWarps * 32);
