@@ -22,6 +22,27 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return r;
 }
 
+// The largest of three, and two float32 additions / fused multiply-adds in one
+// instruction each.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ void add2(float& x, float& y, float a, float b) {
+  asm("{\n\t.reg .b64 u, v;\n\tmov.b64 u, {%0, %1};\n\tmov.b64 v, {%2, %3};\n\tadd.rn.f32x2 u, u, v;\n\t"
+      "mov.b64 {%0, %1}, u;\n\t}"
+      : "+f"(x), "+f"(y)
+      : "f"(a), "f"(b));
+}
+// (x, y) += k (a, b)
+__device__ __forceinline__ void fma2(float& x, float& y, float a, float b, float k) {
+  asm("{\n\t.reg .b64 u, v, w;\n\tmov.b64 u, {%0, %1};\n\tmov.b64 v, {%2, %3};\n\tmov.b64 w, {%4, %4};\n\t"
+      "fma.rn.f32x2 u, v, w, u;\n\tmov.b64 {%0, %1}, u;\n\t}"
+      : "+f"(x), "+f"(y)
+      : "f"(a), "f"(b), "f"(k));
+}
+
 // d += A * B and d = A * B in fp16 with fp32 accumulation.  Not volatile: the
 // compiler may interleave the independent chains.
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -46,21 +67,22 @@ __device__ __forceinline__ void mma_f16_first(float (&d)[4], uint32_t a0, uint32
 // subnormal c * 2^-24 or c * 2^-20, which mma.sync multiplies exactly.  Eight
 // codes cost one shift and four ANDs.
 //   scores:  q . K_t = s_t (q . c_t) + m_t sum(q)            (float32, per token)
-//   output:  sum_t p_t V_t = R sum_t P_t c_t + sum_t p_t m_t,  P_t = p_t s_t / R
-// P is rounded to float16; R is a power of two near the largest scale met so
-// far, so that small scales keep their bits.  The rounding must act on c - 7.5
-// and not on c, whose common part is several times the value: with a = sum of
-// the rounded P (one more mma, against ones),
-//   R sum P_t c_t + sum p_t m_t = R [sum P_t c_t - 7.5 a] + sum p_t (m_t + 7.5 s_t).
+//   output:  sum_t p_t V_t = sum_t P_t c_t + sum_t p_t m_t,  P_t = p_t s_t
+// P is rounded to float16, and the rounding must act on c - 7.5 and not on c,
+// whose common part is several times the value: with a = sum of the rounded P
+// (one more mma, against ones),
+//   sum P_t c_t + sum p_t m_t = [sum P_t c_t - 7.5 a] + sum p_t (m_t + 7.5 s_t).
 // The bracket is formed every kFlushBlocks blocks (flush), which also keeps
 // the accumulators at the output's size: an accumulator that carried 7.5 a
 // over a long context would lose the output's low bits to it.
 //
-// Neither the softmax reference m nor R need be the maximum: m moves only when
-// a score exceeds it by more than kSlack, R when a scale exceeds 2^kScaleSlack R.
-// P then stays below 2^(kSlack + kScaleSlack + 1), within float16's 65504, and
-// float32 sums do not mind, so most steps take one vote and no shuffles or
-// rescaling.
+// The softmax reference M (p_t = 2^(x_t - M)) is not the maximum but what keeps
+// P within float16: with a cap C on the scales met, scores may exceed M by up to
+// `limit` = kTop - log2 C, so P stays below 2^kTop.  When a score or a scale goes
+// beyond, M is set so that the largest score lies kSlack below that limit (its P
+// then is about 2^(kTop - kSlack - kScaleSlack), far above float16's subnormals)
+// and C to 2^kScaleSlack times the largest scale.  Most steps then take one vote
+// and no shuffles or rescaling; float32 sums do not mind the common factor.
 //
 // Lane (gid = lane/4, c = lane%4): scores of tokens gid, gid + 8 and heads 2c,
 // 2c + 1 as in WarpAttn; O^T entries of dims [G gid, G gid + G), G = D/8.
@@ -69,23 +91,24 @@ struct WarpAttnInt4 {
   using Tile = Int4Tile<D>;
   static constexpr int kWords = D / 32;  // 32-bit words of codes per lane and row
   static constexpr int kFlushBlocks = 64;
-  static constexpr float kSlack = 8.f;
-  static constexpr float kScaleSlack = 6.f;
-  static constexpr float kTiny = 5.9604644775390625e-8f;  // 2^-24, the smallest float16 scale
+  static constexpr float kTop = 14.f;    // log2; float16's largest is 65504
+  static constexpr float kSlack = 8.f;   // log2, for later scores
+  static constexpr int kScaleSlack = 6;  // log2, for later scales
+  static constexpr float kTiny = 5.9604644775390625e-8f;  // 2^-24
   uint32_t qf[4 * kWords];
   float acc[D / 16][4];
   float ones[4];         // sum of rounded P since the last flush (heads 2c, 2c + 1; twice)
   float m0, m1, l0, l1;  // softmax reference (log2 units) and sum of p
   float b0, b1;          // sum of p (m + 7.5 s)
   float qs0, qs1;        // scale_log2 * sum(q)
-  float ref, inv_ref;    // R and 1 / R
-  int since_flush;       // blocks; -1 before the first step
+  float cap, limit;      // C, and how far a score may exceed the reference; cap < 0 before the first step
+  int since_flush;       // blocks
 
   __device__ __forceinline__ void reset() {
     m0 = m1 = l0 = l1 = b0 = b1 = 0.f;
-    ref = kTiny;
-    inv_ref = 16777216.f;
-    since_flush = -1;
+    cap = -1.f;
+    limit = 0.f;
+    since_flush = 0;
     ones[0] = ones[1] = ones[2] = ones[3] = 0.f;
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
@@ -168,9 +191,10 @@ struct WarpAttnInt4 {
       }
     }
 #pragma unroll
-    for (int i = 0; i < NB; ++i)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) x[i][k] = fmaf(t[i][k], 0.0625f, x[i][k]);
+    for (int i = 0; i < NB; ++i) {
+      fma2(x[i][0], x[i][1], t[i][0], t[i][1], 0.0625f);
+      fma2(x[i][2], x[i][3], t[i][2], t[i][3], 0.0625f);
+    }
   }
 
   // acc += V^T P^T for one tile: m-tile 2w + h holds dims 4w + h (rows gid) and
@@ -208,49 +232,49 @@ struct WarpAttnInt4 {
     since_flush = 0;
   }
 
-  // Move the softmax reference by what covers d0, d1 (this lane's largest
-  // scores less the reference) and R to cover smax; returns in d0, d1 how far
-  // the reference went up.  What was summed so far is rescaled.
+  // Raise the cap to cover smax and the references to leave kSlack above d0, d1
+  // (this lane's largest scores less the reference); returns in d0, d1 how far
+  // the references went up.  What was summed so far is rescaled.
   __device__ __forceinline__ void rescale(float& d0, float& d1, float smax) {
 #pragma unroll
     for (int o = 4; o <= 16; o <<= 1) {
       d0 = fmaxf(d0, __shfl_xor_sync(0xffffffffu, d0, o));
       d1 = fmaxf(d1, __shfl_xor_sync(0xffffffffu, d1, o));
     }
-    // The largest scale's exponent (the bits of floats >= 0 order as they do).
-    const float r_new = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(smax)) & 0x7f800000u);
-    if (since_flush >= 0) {  // else: the first step, nothing summed yet, any reference will do
+    const bool first = cap < 0.f;  // nothing is summed yet: the references may also go down
+    // The bits of floats >= 0 order as they do; the exponent is all that counts.
+    const uint32_t e = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(smax, kTiny))) >> 23;
+    if (first || smax_exceeds(e)) {
+      cap = __uint_as_float((e + kScaleSlack) << 23);
+      limit = kTop - static_cast<float>(static_cast<int>(e) + kScaleSlack - 127);
+    }
+    d0 -= limit - kSlack;
+    d1 -= limit - kSlack;
+    if (!first) {
       d0 = fmaxf(d0, 0.f);
       d1 = fmaxf(d1, 0.f);
     }
     m0 += d0;
     m1 += d1;
-    const float al0 = exp2_approx(-d0), al1 = exp2_approx(-d1);
-    float f = 1.f;
-    if (r_new > ref) {
-      f = ref / r_new;
-      ref = r_new;
-      inv_ref = 1.f / r_new;  // exact: powers of two
-    }
-    if (since_flush >= 0) {
-      const float g0 = al0 * f, g1 = al1 * f;
+    if (!first) {
+      const float al0 = exp2_approx(-d0), al1 = exp2_approx(-d1);
       l0 *= al0;
       l1 *= al1;
       b0 *= al0;
       b1 *= al1;
-      ones[0] *= g0;
-      ones[1] *= g1;
+      ones[0] *= al0;
+      ones[1] *= al1;
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) {
-        acc[i][0] *= g0;
-        acc[i][1] *= g1;
-        acc[i][2] *= g0;
-        acc[i][3] *= g1;
+        acc[i][0] *= al0;
+        acc[i][1] *= al1;
+        acc[i][2] *= al0;
+        acc[i][3] *= al1;
       }
-    } else {
-      since_flush = 0;
     }
   }
+  // Whether a scale with this exponent (biased) can be above the cap, a power of two.
+  __device__ __forceinline__ bool smax_exceeds(uint32_t e) const { return e >= __float_as_uint(cap) >> 23; }
 
   // One softmax step over NB consecutive blocks of one unit, whose (K tile, V
   // tile) pairs lie back to back at `stage`.  MASK: only the first `valid` (1..16
@@ -285,13 +309,12 @@ struct WarpAttnInt4 {
           x[i][2 * r] = x[i][2 * r + 1] = -INFINITY;
           sv[i][r] = mv[i][r] = 0.f;
         }
-        d0 = fmaxf(d0, x[i][2 * r]);
-        d1 = fmaxf(d1, x[i][2 * r + 1]);
-        smax = fmaxf(smax, fabsf(sv[i][r]));
       }
+      d0 = max3(d0, x[i][0], x[i][2]);
+      d1 = max3(d1, x[i][1], x[i][3]);
+      smax = max3(smax, fabsf(sv[i][0]), fabsf(sv[i][1]));
     }
-    constexpr float kScaleLimit = 64.f;  // 2^kScaleSlack
-    if (__any_sync(0xffffffffu, fmaxf(d0, d1) > kSlack || smax > kScaleLimit * ref || since_flush < 0)) {
+    if (__any_sync(0xffffffffu, fmaxf(d0, d1) > limit || smax > cap)) {  // and before anything is summed: cap < 0
       rescale(d0, d1, smax);
 #pragma unroll
       for (int i = 0; i < NB; ++i) {
@@ -307,12 +330,10 @@ struct WarpAttnInt4 {
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const float e0 = exp2_approx(x[i][2 * r]), e1 = exp2_approx(x[i][2 * r + 1]);
-        const float s = sv[i][r] * inv_ref, mid = fmaf(7.5f, sv[i][r], mv[i][r]);
-        l0 += e0;
-        l1 += e1;
-        b0 = fmaf(e0, mid, b0);
-        b1 = fmaf(e1, mid, b1);
-        p[r] = pack2<__half>(e0 * s, e1 * s);
+        const float mid = fmaf(7.5f, sv[i][r], mv[i][r]);
+        add2(l0, l1, e0, e1);
+        fma2(b0, b1, e0, e1, mid);
+        p[r] = pack2<__half>(e0 * sv[i][r], e1 * sv[i][r]);
       }
       p[0] = movmatrix_trans(p[0]);
       p[1] = movmatrix_trans(p[1]);
@@ -346,7 +367,7 @@ struct WarpAttnInt4 {
 
   // Entries chunk_dim(lane, k) .. + 7 of head 2c + e, scaled by `mul`.
   __device__ __forceinline__ void chunk_values(int e, int k, float mul, float (&v)[8]) const {
-    const float f = ref * 16777216.f, b = e ? b1 : b0;
+    const float f = 16777216.f, b = e ? b1 : b0;  // 2^24
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
       const float(&even)[4] = acc[4 * k + 2 * w];
