@@ -514,7 +514,8 @@ int paged_verify_draft(const void* target_probs, const void* draft_probs, const 
  * Every block belongs to one sequence: shared blocks (reference counts) are the
  * host allocator's.  Calls on the same pool must not run concurrently; the
  * arrays must not overlap.  Limits: block_size 16, num_seqs 0..8192,
- * num_blocks * 16, max_blocks * 16 and num_seqs * max_blocks below 2^31.
+ * num_blocks * 16, max_blocks * 16 and num_seqs * max_blocks below 2^31,
+ * num_slots below 2^31 - 64.
  * ---------------------------------------------------------------------- */
 int paged_kv_resize_tables(int32_t* context_lens, const int32_t* new_lens, int32_t num_seqs, int32_t max_blocks,
                            int32_t block_size, int32_t* block_tables, int32_t* free_blocks, int32_t* num_free,
@@ -567,6 +568,14 @@ int paged_kv_selftest_stale_prologue(const void* q, const void* k_new, const voi
                                      const int32_t* stale_block_tables, const int32_t* stale_context_lens,
                                      float scale, void* out, void* workspace, size_t workspace_bytes,
                                      int32_t publish, const pkv_dims* dims, void* stream);
+
+/* The same self-test of paged_decode_step_int4 (4-bit pools, with or without
+ * k_new / v_new). */
+int paged_kv_selftest_stale_prologue_int4(const void* q, const void* k_new, const void* v_new, void* k_cache,
+                                          void* v_cache, const int32_t* block_tables, const int32_t* context_lens,
+                                          const int32_t* stale_block_tables, const int32_t* stale_context_lens,
+                                          float scale, void* out, void* workspace, size_t workspace_bytes,
+                                          int32_t publish, const pkv_dims* dims, void* stream);
 
 /* Synchronises `stream`, then reads and clears this device's error word.
  * Returns PKV_OK, PKV_ERR_OUT_OF_RANGE, PKV_ERR_NO_BLOCKS (nothing but a table

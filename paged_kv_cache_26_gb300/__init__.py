@@ -11,7 +11,7 @@ from .api import (BlockAllocator, PagedKVError, make_workspace, paged_decode_att
                   paged_decode_attention_multi, paged_decode_step_multi,
                   paged_decode_multi_workspace_bytes, paged_decode_multi_resolve_splits, paged_kv_slot_mapping_multi,
                   paged_kv_copy_blocks, paged_kv_selftest_wait, paged_kv_selftest_stale_prologue,
-                  paged_decode_resolve_splits, paged_decode_step, paged_decode_step_from_host,
+                  paged_kv_selftest_stale_prologue_int4, paged_decode_resolve_splits, paged_decode_step, paged_decode_step_from_host,
                   paged_decode_step_fp8_from_host, paged_decode_step_multi_from_host,
                   paged_decode_workspace_bytes,
                   paged_kv_append, paged_kv_check_status, paged_kv_slot_mapping)
@@ -28,5 +28,5 @@ __all__ = [
     "make_workspace_int4", "paged_kv_resize_tables", "paged_verify_draft",
     "paged_decode_attention_multi", "paged_decode_step_multi", "paged_decode_multi_workspace_bytes",
     "paged_decode_multi_resolve_splits", "paged_kv_slot_mapping_multi", "paged_kv_copy_blocks",
-    "paged_kv_selftest_wait", "paged_kv_selftest_stale_prologue",
+    "paged_kv_selftest_wait", "paged_kv_selftest_stale_prologue", "paged_kv_selftest_stale_prologue_int4",
 ]

@@ -817,6 +817,36 @@ def paged_kv_selftest_stale_prologue(q: torch.Tensor, k_new: torch.Tensor, v_new
     return out
 
 
+def paged_kv_selftest_stale_prologue_int4(q: torch.Tensor, k_new: Optional[torch.Tensor],
+                                          v_new: Optional[torch.Tensor], k_cache: torch.Tensor,
+                                          v_cache: torch.Tensor, block_tables: torch.Tensor,
+                                          context_lens: torch.Tensor, stale_block_tables: torch.Tensor,
+                                          stale_context_lens: torch.Tensor, scale: float,
+                                          out: Optional[torch.Tensor] = None,
+                                          workspace: Optional[torch.Tensor] = None, stream=None,
+                                          publish: bool = True) -> torch.Tensor:
+    """paged_kv_selftest_stale_prologue over 4-bit caches (attention alone when
+    k_new / v_new are None).  Returns out."""
+    if out is None:
+        out = torch.empty_like(q)
+    dev, dims, workspace, ws_bytes = _int4_decode(q, k_cache, v_cache, block_tables, context_lens, out, workspace)
+    for n, t in (("stale_block_tables", stale_block_tables), ("stale_context_lens", stale_context_lens)):
+        _need_cuda(n, t, _i32)
+    if stale_block_tables.shape != block_tables.shape or stale_context_lens.shape != context_lens.shape:
+        raise ValueError("stale inputs must have the shapes of the real ones")
+    for n, t in (("k_new", k_new), ("v_new", v_new)):
+        if t is not None:
+            _need_cuda(n, t, q.dtype)
+            if t.shape != (dims.num_seqs, dims.num_kv_heads, dims.head_dim):
+                raise ValueError("k_new / v_new must be [num_seqs][num_kv_heads][head_dim]")
+    _call("paged_kv_selftest_stale_prologue_int4", dev, stream,
+          (q.data_ptr(), k_new.data_ptr() if k_new is not None else 0, v_new.data_ptr() if v_new is not None else 0,
+           k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(),
+           stale_block_tables.data_ptr(), stale_context_lens.data_ptr(), scale, out.data_ptr(), workspace.data_ptr(),
+           ws_bytes, 1 if publish else 0, ctypes.byref(dims)))
+    return out
+
+
 def paged_kv_check_status(stream=None) -> None:
     """Synchronise the stream and raise if a kernel flagged an error."""
     _check(lib().paged_kv_check_status(_stream(stream)), "paged_kv_check_status")

@@ -649,6 +649,7 @@ cudaError_t launch_clusters(void (*kern)(Params...), unsigned grid, unsigned clu
 int resize_tables_impl(const pkv::ResizeArgs& a, int32_t block_size, cudaStream_t stream) {
   if (a.num_seqs < 0 || a.max_blocks < 0 || a.num_blocks <= 0 || a.num_slots < 0)
     return pkv_fail(PKV_ERR_INVALID_ARG, "resize_tables: negative or zero size");
+  if (a.num_slots > INT32_MAX - 64) return pkv_fail(PKV_ERR_UNSUPPORTED, "resize_tables: too many slots");
   if (block_size != pkv::kBlockSize) return pkv_fail(PKV_ERR_UNSUPPORTED, "resize_tables: block_size must be 16");
   if (a.num_seqs > pkv::kMaxResizeSeqs)
     return pkv_fail(PKV_ERR_UNSUPPORTED,
@@ -1230,6 +1231,19 @@ int paged_kv_selftest_stale_prologue(const void* q, const void* k_new, const voi
     return pkv_fail(PKV_ERR_INVALID_ARG, "selftest_stale_prologue: stale inputs missing or misaligned");
   return decode_impl(q, k_new, v_new, k_cache, v_cache, block_tables, context_lens, scale, out, 0, workspace,
                      workspace_bytes, dims, static_cast<cudaStream_t>(stream), kPool16, nullptr, nullptr, true,
+                     stale_context_lens, stale_block_tables, true, publish != 0);
+}
+
+int paged_kv_selftest_stale_prologue_int4(const void* q, const void* k_new, const void* v_new, void* k_cache,
+                                          void* v_cache, const int32_t* block_tables, const int32_t* context_lens,
+                                          const int32_t* stale_block_tables, const int32_t* stale_context_lens,
+                                          float scale, void* out, void* workspace, size_t workspace_bytes,
+                                          int32_t publish, const pkv_dims* dims, void* stream) {
+  if (!stale_block_tables || !stale_context_lens || !aligned(stale_block_tables, 4) ||
+      !aligned(stale_context_lens, 4))
+    return pkv_fail(PKV_ERR_INVALID_ARG, "selftest_stale_prologue_int4: stale inputs missing or misaligned");
+  return decode_impl(q, k_new, v_new, k_cache, v_cache, block_tables, context_lens, scale, out, 0, workspace,
+                     workspace_bytes, dims, static_cast<cudaStream_t>(stream), kPoolInt4, nullptr, nullptr, true,
                      stale_context_lens, stale_block_tables, true, publish != 0);
 }
 

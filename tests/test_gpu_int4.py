@@ -361,6 +361,77 @@ def test_inputs_written_on_the_stream_right_before_the_step():
     assert np.array_equal(kp.cpu().numpy(), rk) and np.array_equal(vp.cpu().numpy(), rv)
 
 
+@pytest.mark.parametrize("publish", [True, False])
+@pytest.mark.parametrize("batch", [6, 40, 200])
+@pytest.mark.parametrize("kind", ["lengths", "tables", "garbage", "zeros"])
+def test_stale_inputs_before_the_grid_wait_are_rebuilt(kind, batch, publish):
+    """The prologue is handed other lengths and tables than the real ones: outputs and pools are the normal step's."""
+    spec = wl.LLAMA3_8B.replace(name="stale", batch=batch, lengths=("uniform", 1, 900), num_q_heads=8, num_kv_heads=2)
+    w = wl.generate(spec, seed=batch)
+    c = wl.int4_caches(w, oracle_store)
+    q, kn, vn = (t[0].to(DEV) for t in (w.q, w.k_new, w.v_new))
+    bt, cl = torch.from_numpy(w.block_tables).to(DEV), torch.from_numpy(w.context_lens).to(DEV)
+    g = torch.Generator().manual_seed(1)
+    sl, st = cl.clone(), bt.clone()
+    if kind == "lengths":
+        sl = (cl - 1).clamp(min=0)
+    elif kind == "tables":
+        st[:, 0] = st[:, 0].roll(1)
+    elif kind == "garbage":
+        sl = torch.randint(-50, 4 * 900, cl.shape, generator=g, dtype=torch.int32).to(DEV)
+        st = torch.randint(-5, w.num_blocks + 5, bt.shape, generator=g, dtype=torch.int32).to(DEV)
+    else:
+        sl.zero_()
+    for append in (True, False):
+        kc, vc = c.k_cache[0].to(DEV, copy=True), c.v_cache[0].to(DEV, copy=True)
+        if not append:
+            pkv.paged_kv_append_int4(kn, vn, torch.from_numpy(pkv.paged_kv_slot_mapping(w.block_tables, w.context_lens)
+                                                              ).to(DEV), kc, vc)
+        k2, v2 = kc.clone(), vc.clone()
+        if append:
+            want = pkv.paged_decode_step_int4(q, kn, vn, kc, vc, bt, cl, w.scale)
+        else:
+            want = pkv.paged_decode_attention_int4(q, kc, vc, bt, cl, w.scale)
+        got = pkv.paged_kv_selftest_stale_prologue_int4(q, kn if append else None, vn if append else None, k2, v2, bt,
+                                                        cl, st, sl, w.scale, publish=publish)
+        pkv.paged_kv_check_status()
+        assert torch.equal(got.view(torch.int16), want.view(torch.int16))
+        assert torch.equal(kc, k2) and torch.equal(vc, v2)
+
+
+def test_offsets_past_32_bits():
+    """Pools of more than 4 GB: blocks near their end, through every call that addresses them."""
+    hk, d, nb = 8, 128, 520_000                    # 4.5 GB each
+    kc, vc = (torch.empty(nb, hk, 16, 68, dtype=torch.uint8, device=DEV) for _ in range(2))
+    assert kc.numel() > 1 << 32
+    lens = [100, 33]
+    ids = torch.tensor([[nb - 1, 3, nb - 7, nb - 2, nb - 3, nb - 4, 9], [nb - 5, nb - 6, nb - 9, -1, -1, -1, -1]],
+                       dtype=torch.int32)
+    ks, vs = (torch.zeros(10, hk, 16, 68, dtype=torch.uint8, device=DEV) for _ in range(2))
+    ids_s = torch.tensor([[0, 1, 2, 3, 4, 5, 6], [7, 8, 9, -1, -1, -1, -1]], dtype=torch.int32)  # a small pool
+    g = torch.Generator().manual_seed(0)
+    for b, n in enumerate(lens):
+        k, v = (torch.randn(n, hk, d, generator=g).bfloat16().to(DEV) for _ in range(2))
+        pos = torch.arange(n)
+        for t, kp, vp in ((ids, kc, vc), (ids_s, ks, vs)):
+            slots = (t[b, pos // 16] * 16 + pos % 16).int().to(DEV)
+            pkv.paged_kv_append_int4(k, v, slots, kp, vp)
+            ko, vo = pkv.paged_kv_read_int4(slots, kp, vp, torch.bfloat16)
+            if kp is kc:
+                far = (ko, vo)
+        assert torch.equal(ko, far[0]) and torch.equal(vo, far[1])
+    q = torch.randn(2, 16, d, generator=g).bfloat16().to(DEV)
+    kn, vn = (torch.randn(2, hk, d, generator=g).bfloat16().to(DEV) for _ in range(2))
+    cl = torch.tensor(lens, dtype=torch.int32, device=DEV) + 1
+    outs = [pkv.paged_decode_step_int4(q, kn, vn, kp, vp, t.to(DEV), cl, d ** -0.5)
+            for t, kp, vp in ((ids, kc, vc), (ids_s, ks, vs))]
+    pkv.paged_kv_check_status()
+    assert torch.equal(outs[0], outs[1])
+    pkv.paged_kv_copy_blocks(kc, vc, torch.tensor([[nb - 1, nb - 8]], dtype=torch.int32, device=DEV))
+    pkv.paged_kv_check_status()
+    assert torch.equal(kc[nb - 8], ks[0]) and torch.equal(vc[nb - 8], vs[0])
+
+
 def test_another_stream_and_captured_graphs():
     w = wl.generate(REDUCED[3], seed=4)
     c = wl.int4_caches(w, oracle_store)

@@ -241,6 +241,20 @@ def test_verify_large_vocabularies(V):
     check_verify(*(v.to(DEV) for v in (t, d, tok, au, su)))
 
 
+def test_verify_the_largest_vocabulary():
+    V = 1 << 22
+    p = torch.zeros(1, 1, V)
+    at = [0, 5, 127, 128, 1 << 20, V - 129, V - 1]
+    p[0, 0, at] = torch.tensor([0.1, 0.2, 0.05, 0.25, 0.1, 0.2, 0.1])
+    w = [serving.weight(float(v)) for v in p[0, 0, at]]
+    us = [0.0, 0.05, 0.2, 0.31, 0.349, 0.5, 0.65, 0.8, 0.95, 0.999999]
+    t = p.to(DEV).expand(len(us), 1, V)
+    _, out, _ = pkv.paged_verify_draft(t, None, torch.empty(len(us), 0, dtype=torch.int32, device=DEV),
+                                       torch.empty(len(us), 0, device=DEV), torch.tensor(us, device=DEV))
+    u32 = np.array(us, np.float32)
+    assert out[:, 0].tolist() == [at[serving.draw(w, float(u))] for u in u32]
+
+
 def test_verify_many_drafts_and_none():
     g = torch.Generator().manual_seed(0)
     for K in (0, 1, 7, 31):
