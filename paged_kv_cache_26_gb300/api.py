@@ -4,6 +4,7 @@ path runs in the library's CUDA kernels (or, for the allocator and slot
 mapping, its host C++)."""
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from typing import Optional, Sequence
 
@@ -489,6 +490,18 @@ def _call(name: str, dev: int, stream, args: tuple) -> None:
         raise PagedKVError(rc, name)
 
 
+def _allocating_on(stream, dev: int):
+    """Context in which new tensors belong to the stream of the call: memory that
+    kernels still queued on the current stream may be using is not handed out,
+    and a fill comes before the call's kernels."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream_of(stream, dev)
+        stream = torch.cuda.ExternalStream(handle, device=dev) if handle else torch.cuda.default_stream(dev)
+    return torch.cuda.stream(stream)
+
+
 def _explain(dev: int, *tensors) -> None:
     """Raises the message for the first (name, tensor, dtype) that is not a
     contiguous CUDA tensor of that dtype on device dev."""
@@ -567,7 +580,8 @@ def paged_kv_read_int4(slot_mapping: torch.Tensor, k_cache: torch.Tensor, v_cach
             raise ValueError("caches must be uint8 [num_blocks][num_kv_heads][16][head_dim/2 + 4], slot_mapping "
                              "[num_tokens]")
         shape = (slot_mapping.shape[0], k_cache.shape[1], 2 * (k_cache.shape[3] - 4))
-        k_out, v_out = (torch.empty(shape, dtype=dtype, device=k_cache.device) for _ in range(2))
+        with _allocating_on(stream, k_cache.get_device()):
+            k_out, v_out = (torch.empty(shape, dtype=dtype, device=k_cache.device) for _ in range(2))
     elif k_out is None or v_out is None:
         raise ValueError("give both k_out and v_out, or neither")
     elif dtype is not None and dtype != k_out.dtype:
@@ -579,9 +593,15 @@ def paged_kv_read_int4(slot_mapping: torch.Tensor, k_cache: torch.Tensor, v_cach
     return k_out, v_out
 
 
-def _int4_decode(q, k_cache, v_cache, block_tables, context_lens, out, workspace):
-    """Checks of the 4-bit attention calls; (device, dims, workspace and its bytes)."""
+def _int4_decode(q, k_cache, v_cache, block_tables, context_lens, out, workspace, stream):
+    """Checks of the 4-bit attention calls; (device, dims, out, workspace and its bytes)."""
     dev = q.get_device()
+    if out is None:
+        if stream is None:
+            out = torch.empty_like(q)
+        else:
+            with _allocating_on(stream, dev):
+                out = torch.empty_like(q)
     qs, cs, bt = q.shape, k_cache.shape, block_tables.shape
     if not (dev >= 0 and k_cache.get_device() == dev and v_cache.get_device() == dev and
             block_tables.get_device() == dev and context_lens.get_device() == dev and out.get_device() == dev and
@@ -598,10 +618,11 @@ def _int4_decode(q, k_cache, v_cache, block_tables, context_lens, out, workspace
                          "context_lens [num_seqs]")
     dims = make_dims_int4(q, k_cache, block_tables)
     if workspace is None:
-        workspace = make_workspace_int4(q, k_cache, block_tables)
-    elif workspace.get_device() != dev:
-        raise ValueError(f"workspace must be on device {dev} like the other tensors")
-    return dev, dims, workspace, workspace.numel() * workspace.element_size()
+        with _allocating_on(stream, dev):
+            workspace = make_workspace_int4(q, k_cache, block_tables)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on device {dev} like the other tensors")
+    return dev, dims, out, workspace, workspace.numel() * workspace.element_size()
 
 
 def paged_decode_attention_int4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -609,9 +630,8 @@ def paged_decode_attention_int4(q: torch.Tensor, k_cache: torch.Tensor, v_cache:
                                 out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
                                 stream=None) -> torch.Tensor:
     """paged_decode_attention over 4-bit caches.  Returns out."""
-    if out is None:
-        out = torch.empty_like(q)
-    dev, dims, workspace, ws_bytes = _int4_decode(q, k_cache, v_cache, block_tables, context_lens, out, workspace)
+    dev, dims, out, workspace, ws_bytes = _int4_decode(q, k_cache, v_cache, block_tables, context_lens, out, workspace,
+                                                       stream)
     _call("paged_decode_attention_int4", dev, stream,
           (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), scale,
            out.data_ptr(), workspace.data_ptr(), ws_bytes, ctypes.byref(dims)))
@@ -624,9 +644,8 @@ def paged_decode_step_int4(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Te
                            workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """paged_decode_step over 4-bit caches: the new token is quantised and
     appended, then attended, in one fused launch.  Returns out."""
-    if out is None:
-        out = torch.empty_like(q)
-    dev, dims, workspace, ws_bytes = _int4_decode(q, k_cache, v_cache, block_tables, context_lens, out, workspace)
+    dev, dims, out, workspace, ws_bytes = _int4_decode(q, k_cache, v_cache, block_tables, context_lens, out, workspace,
+                                                       stream)
     if not (k_new.get_device() == dev and v_new.get_device() == dev and k_new.dtype == q.dtype and
             v_new.dtype == q.dtype and k_new.is_contiguous() and v_new.is_contiguous() and
             k_new.shape == (dims.num_seqs, dims.num_kv_heads, dims.head_dim) and v_new.shape == k_new.shape):
@@ -732,17 +751,21 @@ def paged_verify_draft(target_probs: torch.Tensor, draft_probs: Optional[torch.T
             _explain(dev, ("draft_lens", draft_lens, _i32))
             raise ValueError("draft_lens must be [num_seqs]")
         n = draft_lens.data_ptr()
-    lens, lens_ptr = None, 0
     if context_lens is not None:
         if not (context_lens.get_device() == dev and context_lens.dtype is _i32 and context_lens.dim() == 1 and
                 context_lens.numel() == B and context_lens.is_contiguous()):
             _explain(dev, ("context_lens", context_lens, _i32))
             raise ValueError("context_lens must be [num_seqs]")
         ctx = context_lens.data_ptr()
-        lens = torch.empty_like(context_lens)
-        lens_ptr = lens.data_ptr()
-    accepted = torch.empty((B,), dtype=_i32, device=dev)
-    tokens = torch.empty((B, K + 1), dtype=_i32, device=dev)
+    if stream is None:
+        accepted, tokens = torch.empty((B,), dtype=_i32, device=dev), torch.empty((B, K + 1), dtype=_i32, device=dev)
+        lens = torch.empty_like(context_lens) if ctx else None
+    else:
+        with _allocating_on(stream, dev):
+            accepted = torch.empty((B,), dtype=_i32, device=dev)
+            tokens = torch.empty((B, K + 1), dtype=_i32, device=dev)
+            lens = torch.empty_like(context_lens) if ctx else None
+    lens_ptr = lens.data_ptr() if ctx else 0
     dims = PkvVerifyDims(B, K, V, code, t_stride[0], t_stride[1], d_seq, d_row)
     _call("paged_verify_draft", dev, stream,
           (target_probs.data_ptr(), q, draft_tokens.data_ptr(), n, accept_u.data_ptr(), sample_u.data_ptr(), ctx,
@@ -827,9 +850,8 @@ def paged_kv_selftest_stale_prologue_int4(q: torch.Tensor, k_new: Optional[torch
                                           publish: bool = True) -> torch.Tensor:
     """paged_kv_selftest_stale_prologue over 4-bit caches (attention alone when
     k_new / v_new are None).  Returns out."""
-    if out is None:
-        out = torch.empty_like(q)
-    dev, dims, workspace, ws_bytes = _int4_decode(q, k_cache, v_cache, block_tables, context_lens, out, workspace)
+    dev, dims, out, workspace, ws_bytes = _int4_decode(q, k_cache, v_cache, block_tables, context_lens, out, workspace,
+                                                       stream)
     for n, t in (("stale_block_tables", stale_block_tables), ("stale_context_lens", stale_context_lens)):
         _need_cuda(n, t, _i32)
     if stale_block_tables.shape != block_tables.shape or stale_context_lens.shape != context_lens.shape:

@@ -542,3 +542,12 @@ def test_wrong_shapes_are_refused():
     with pytest.raises(pkv.PagedKVError) as e:
         pkv.paged_decode_attention_int4(**{**ok, "q": torch.zeros(2, 18, 128, dtype=torch.bfloat16, device=DEV)})
     assert e.value.code == -2
+
+
+def test_a_strided_workspace_is_refused():
+    kc, vc, q = (torch.zeros(4, 2, 16, 68, dtype=torch.uint8, device=DEV), torch.zeros(4, 2, 16, 68, dtype=torch.uint8,
+                 device=DEV), torch.zeros(1, 8, 128, dtype=torch.half, device=DEV))
+    bt, cl = torch.zeros(1, 2, dtype=torch.int32, device=DEV), torch.zeros(1, dtype=torch.int32, device=DEV)
+    ws = torch.zeros(2 * pkv.make_workspace_int4(q, kc, bt).numel(), dtype=torch.uint8, device=DEV)
+    with pytest.raises(ValueError):
+        pkv.paged_decode_attention_int4(q, kc, vc, bt, cl, 0.1, workspace=ws[::2])

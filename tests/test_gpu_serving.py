@@ -454,3 +454,36 @@ def test_4bit_steps_over_tables_built_on_the_gpu():
         assert_attention(out.cpu(), ref, torch.bfloat16, rv, t, [i + 1] * B, f"step {i}")
     pkv.paged_kv_check_status()
     assert np.array_equal(kp.cpu().numpy(), rk) and np.array_equal(vp.cpu().numpy(), rv)
+
+
+@pytest.mark.parametrize("by_handle", [False, True])
+def test_new_tensors_belong_to_the_calls_stream(by_handle):
+    """Tensors a call makes when it is given a stream: not memory that work still
+    queued on the current stream writes to."""
+    rng = np.random.default_rng(6)
+    gen = torch.Generator(DEV).manual_seed(6)
+    kc, vc = (torch.zeros(24, 2, 16, 68, dtype=torch.uint8, device=DEV) for _ in range(2))
+    k, v = (torch.randn(90, 2, 128, generator=gen, device=DEV).half() for _ in range(2))
+    pkv.paged_kv_append_int4(k, v, i32(np.arange(90)), kc, vc)
+    q = torch.randn(3, 8, 128, generator=gen, device=DEV).half()
+    bt, cl = i32([[0, 1], [2, 3], [4, 5]]), i32([30, 9, 20])
+    slots = i32(rng.permutation(90)[:33])
+    p = torch.softmax(torch.randn(3, 4, 500, generator=gen, device=DEV), -1)
+    d = torch.softmax(torch.randn(3, 3, 500, generator=gen, device=DEV), -1)
+    tokens, u, su = i32(rng.integers(0, 500, (3, 3))), torch.full((3, 3), 0.2, device=DEV), torch.full((3,), 0.5, device=DEV)
+    calls = [lambda s: pkv.paged_kv_read_int4(slots, kc, vc, torch.float16, stream=s),
+             lambda s: (pkv.paged_decode_attention_int4(q, kc, vc, bt, cl, 0.1, stream=s),),
+             lambda s: pkv.paged_verify_draft(p, d, tokens, u, su, context_lens=cl, stream=s)]
+    side = torch.cuda.Stream()
+    for call in calls:
+        want = [t.clone() for t in call(None)]
+        stale = [torch.empty_like(t) for t in want]
+        torch.cuda.synchronize()
+        torch.cuda._sleep(40_000_000)
+        for t in stale:
+            t.fill_(7)
+        del stale
+        got = call(side.cuda_stream if by_handle else side)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    pkv.paged_kv_check_status()
