@@ -22,27 +22,12 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return r;
 }
 
-// The largest of three, and two float32 additions / fused multiply-adds in one
-// instruction each.
+// The largest of three.
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-__device__ __forceinline__ void add2(float& x, float& y, float a, float b) {
-  asm("{\n\t.reg .b64 u, v;\n\tmov.b64 u, {%0, %1};\n\tmov.b64 v, {%2, %3};\n\tadd.rn.f32x2 u, u, v;\n\t"
-      "mov.b64 {%0, %1}, u;\n\t}"
-      : "+f"(x), "+f"(y)
-      : "f"(a), "f"(b));
-}
-// (x, y) += k (a, b)
-__device__ __forceinline__ void fma2(float& x, float& y, float a, float b, float k) {
-  asm("{\n\t.reg .b64 u, v, w;\n\tmov.b64 u, {%0, %1};\n\tmov.b64 v, {%2, %3};\n\tmov.b64 w, {%4, %4};\n\t"
-      "fma.rn.f32x2 u, v, w, u;\n\tmov.b64 {%0, %1}, u;\n\t}"
-      : "+f"(x), "+f"(y)
-      : "f"(a), "f"(b), "f"(k));
-}
-
 // d += A * B and d = A * B in fp16 with fp32 accumulation.  Not volatile: the
 // compiler may interleave the independent chains.
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -162,7 +147,7 @@ struct WarpAttnInt4 {
     }
   }
 
-  static constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
+  static constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u, kBoth = 0x00ff00ffu;
 
   // 2^-24 (q . c) of tokens gid (x[.][0..1]) and gid + 8 (x[.][2..3]), heads 2c
   // and 2c + 1, of NB blocks' K tiles (2 * kBytes apart): 2 NB independent mma
@@ -192,22 +177,25 @@ struct WarpAttnInt4 {
     }
 #pragma unroll
     for (int i = 0; i < NB; ++i) {
-      fma2(x[i][0], x[i][1], t[i][0], t[i][1], 0.0625f);
-      fma2(x[i][2], x[i][3], t[i][2], t[i][3], 0.0625f);
+      fma2(x[i][0], x[i][1], t[i][0], t[i][1], 0.0625f, x[i][0], x[i][1]);
+      fma2(x[i][2], x[i][3], t[i][2], t[i][3], 0.0625f, x[i][2], x[i][3]);
     }
   }
 
-  // acc += V^T P^T for one tile: m-tile 2w + h holds dims 4w + h (rows gid) and
-  // 4w + h + 2 (rows gid + 8) of the lane's G, times 2^-24 (h = 0) or 2^-20.
+  // acc += V^T P^T for one tile, times 2^-24: m-tile 2w holds dims 4w (rows gid)
+  // and 4w + 2 (rows gid + 8) of the lane's G, m-tile 2w + 1 those plus 16 times
+  // dims 4w + 1 and 4w + 3.  A byte with both its codes c + 16 c' is a float16
+  // subnormal too, and takes one operation less to cut out than c' alone; the
+  // two are told apart at the end (chunk_values).
   __device__ __forceinline__ void pv(const uint8_t* vs, uint32_t p0, uint32_t p1, int lane) {
     uint32_t x[kWords], y[kWords];
     load_words(vs + lane * (D / 8), x);                         // tokens 2c, 2c + 1
     load_words(vs + Tile::kCodeBytes / 2 + lane * (D / 8), y);  // tokens 2c + 8, 2c + 9
 #pragma unroll
     for (int w = 0; w < kWords; ++w) {
-      const uint32_t x8 = x[w] >> 8, y8 = y[w] >> 8;
+      const uint32_t x8 = __byte_perm(x[w], 0, 0x4341), y8 = __byte_perm(y[w], 0, 0x4341);  // bytes 1 and 3
       mma_f16(acc[2 * w], x[w] & kLow, x8 & kLow, y[w] & kLow, y8 & kLow, p0, p1);
-      mma_f16(acc[2 * w + 1], x[w] & kHigh, x8 & kHigh, y[w] & kHigh, y8 & kHigh, p0, p1);
+      mma_f16(acc[2 * w + 1], x[w] & kBoth, x8, y[w] & kBoth, y8, p0, p1);
     }
   }
 
@@ -222,7 +210,7 @@ struct WarpAttnInt4 {
     const float f0 = ones[0] * (7.5f * kTiny), f1 = ones[1] * (7.5f * kTiny);
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) {
-      const float u = i & 1 ? -16.f : -1.f;
+      const float u = i & 1 ? -17.f : -1.f;
       acc[i][0] = fmaf(u, f0, acc[i][0]);
       acc[i][1] = fmaf(u, f1, acc[i][1]);
       acc[i][2] = fmaf(u, f0, acc[i][2]);
@@ -332,7 +320,7 @@ struct WarpAttnInt4 {
         const float e0 = exp2_approx(x[i][2 * r]), e1 = exp2_approx(x[i][2 * r + 1]);
         const float mid = fmaf(7.5f, sv[i][r], mv[i][r]);
         add2(l0, l1, e0, e1);
-        fma2(b0, b1, e0, e1, mid);
+        fma2(b0, b1, e0, e1, mid, b0, b1);
         p[r] = pack2<__half>(e0 * sv[i][r], e1 * sv[i][r]);
       }
       p[0] = movmatrix_trans(p[0]);
@@ -367,15 +355,15 @@ struct WarpAttnInt4 {
 
   // Entries chunk_dim(lane, k) .. + 7 of head 2c + e, scaled by `mul`.
   __device__ __forceinline__ void chunk_values(int e, int k, float mul, float (&v)[8]) const {
-    const float f = 16777216.f, b = e ? b1 : b0;  // 2^24
+    const float f = 16777216.f, h = 0.0625f * f, b = e ? b1 : b0;  // 2^24
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
       const float(&even)[4] = acc[4 * k + 2 * w];
       const float(&odd)[4] = acc[4 * k + 2 * w + 1];
       v[4 * w] = fmaf(even[e], f, b) * mul;
-      v[4 * w + 1] = fmaf(odd[e], 0.0625f * f, b) * mul;
+      v[4 * w + 1] = fmaf(odd[e] - even[e], h, b) * mul;
       v[4 * w + 2] = fmaf(even[2 + e], f, b) * mul;
-      v[4 * w + 3] = fmaf(odd[2 + e], 0.0625f * f, b) * mul;
+      v[4 * w + 3] = fmaf(odd[2 + e] - even[2 + e], h, b) * mul;
     }
   }
   __device__ __forceinline__ static int chunk_dim(int lane, int k) { return (D / 8) * (lane >> 2) + 8 * k; }

@@ -37,6 +37,21 @@ struct Int4Tile {
 
 constexpr float kF16Max = 65504.f;
 
+// Two float32 operations (each rounded to nearest even) in one instruction.
+__device__ __forceinline__ void add2(float& x, float& y, float a, float b) {  // (x, y) += (a, b)
+  asm("{\n\t.reg .b64 u, v;\n\tmov.b64 u, {%0, %1};\n\tmov.b64 v, {%2, %3};\n\tadd.rn.f32x2 u, u, v;\n\t"
+      "mov.b64 {%0, %1}, u;\n\t}"
+      : "+f"(x), "+f"(y)
+      : "f"(a), "f"(b));
+}
+// (x, y) = k (a, b) + (c, d)
+__device__ __forceinline__ void fma2(float& x, float& y, float a, float b, float k, float c, float d) {
+  asm("{\n\t.reg .b64 u, v, w;\n\tmov.b64 u, {%5, %6};\n\tmov.b64 v, {%2, %3};\n\tmov.b64 w, {%4, %4};\n\t"
+      "fma.rn.f32x2 u, v, w, u;\n\tmov.b64 {%0, %1}, u;\n\t}"
+      : "=f"(x), "=f"(y)
+      : "f"(a), "f"(b), "f"(k), "f"(c), "f"(d));
+}
+
 // The stored pair of a row with these extremes (of values limited to the
 // float16 range): m = f16(min), s = f16((max - m) / 15), all IEEE float32, so
 // that the codes are the same wherever the formula is evaluated in float32.
@@ -49,9 +64,15 @@ __device__ __forceinline__ Int4Row int4_row(float mn, float mx) {
   Int4Row r;
   const __half lo = __float2half_rn(mn);
   r.low = __half2float(lo);
-  const __half sc = __float2half_rn(__fdiv_rn(__fsub_rn(mx, r.low), 15.f));
+  // The correctly rounded quotient by 15 from the product with the rounded 1/15
+  // and one correction by the (exact) remainder (P. Markstein, "Computation of
+  // elementary functions on the IBM RISC System/6000 processor", 1990); where a
+  // step could underflow the quotient rounds to a float16 zero all the same.
+  constexpr float kFifteenth = 1.f / 15.f;
+  const float x = __fsub_rn(mx, r.low), y = __fmul_rn(x, kFifteenth);
+  const __half sc = __float2half_rn(__fmaf_rn(__fmaf_rn(-15.f, y, x), kFifteenth, y));
   const float s = __half2float(sc);
-  r.inv = s > 0.f ? __fdiv_rn(1.f, s) : 0.f;
+  r.inv = s > 0.f ? __frcp_rn(s) : 0.f;
   r.pair = static_cast<uint32_t>(__half_as_ushort(sc)) | static_cast<uint32_t>(__half_as_ushort(lo)) << 16;
   return r;
 }
@@ -157,9 +178,13 @@ __device__ __forceinline__ uint2 int4_quantise16(const uint4 (&raw)[2], uint32_t
       uint32_t w = 0;
 #pragma unroll
       for (int i = 3; i >= 0; --i) {
-        const float2 x = unpack2<T>(word_of(raw[h], i));
-        w = w * 16 + __float_as_uint(__fadd_rn(__fmul_rn(__fsub_rn(x.y, r.low), r.inv), kMagic));
-        w = w * 16 + __float_as_uint(__fadd_rn(__fmul_rn(__fsub_rn(x.x, r.low), r.inv), kMagic));
+        float2 x = unpack2<T>(word_of(raw[h], i));
+        add2(x.x, x.y, -r.low, -r.low);
+        x.x = __fmul_rn(x.x, r.inv);  // (a packed product and sum would be fused to one rounding)
+        x.y = __fmul_rn(x.y, r.inv);
+        add2(x.x, x.y, kMagic, kMagic);
+        w = w * 16 + __float_as_uint(x.y);
+        w = w * 16 + __float_as_uint(x.x);
       }
       out[h] = w - kExcess;
     }
@@ -241,21 +266,24 @@ __global__ void __launch_bounds__(kAppendThreads)
   }
 }
 
-// Values of the rows at these slots, rounded to T: one thread reads eight dims
-// of a K row and of its V row (V's come with the neighbouring token's, in whole
-// words).  A negative slot gives a zero row.  Bound by the values written.
+// Values of the rows at these slots, rounded to T: one thread reads dims 8c ..
+// 8c + 7 of either half of a K row and of its V row (V's come with the
+// neighbouring token's, in whole words).  A negative slot gives a zero row.
+// Bound by the values written: so few lanes a row, as finding the tile and the
+// pairs is paid per lane, and halves, as neighbouring lanes then store
+// neighbouring 16 bytes.
 template <typename T, int D>
 __global__ void __launch_bounds__(kReadThreads)
     read_int4_kernel(const int32_t* __restrict__ slots, int32_t num_tokens, int32_t num_kv_heads, int64_t num_slots,
                      const uint8_t* __restrict__ k_cache, const uint8_t* __restrict__ v_cache,
                      uint4* __restrict__ k_out, uint4* __restrict__ v_out) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  constexpr int C = D / 8, kTokens = kReadThreads / C;
-  const int c = threadIdx.x % C, d = 8 * c, head = blockIdx.y;
+  constexpr int C = D / 16, kTokens = kReadThreads / C;
+  const int c = threadIdx.x % C, head = blockIdx.y;
   const int64_t token = static_cast<int64_t>(blockIdx.x) * kTokens + threadIdx.x / C;
   if (token >= num_tokens) return;
   const int32_t slot = slots[token];
-  uint4 kv[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+  uint4 kv[2][2] = {};
   if (slot >= num_slots) {
     if (c == 0) flag_error(kErrSlot);
   } else if (slot >= 0) {
@@ -263,31 +291,45 @@ __global__ void __launch_bounds__(kReadThreads)
     const int64_t tile = (static_cast<int64_t>(slot >> 4) * num_kv_heads + head) * Int4Tile<D>::kBytes;
     const uint8_t* kt = k_cache + tile;
     const uint8_t* vt = v_cache + tile;
-    const uint32_t kc = *reinterpret_cast<const uint32_t*>(kt + t * (D / 2) + d / 2);
-    const uint2 vw = *reinterpret_cast<const uint2*>(vt + Int4Tile<D>::v_offset(t & ~1, d));
-    const uint32_t vc = __byte_perm(vw.x, vw.y, t & 1 ? 0x7632 : 0x5410);
+    uint32_t kc[2];
+    uint2 vw[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int d = 8 * c + j * (D / 2);
+      kc[j] = *reinterpret_cast<const uint32_t*>(kt + t * (D / 2) + d / 2);
+      vw[j] = *reinterpret_cast<const uint2*>(vt + Int4Tile<D>::v_offset(t & ~1, d));
+    }
     const float2 ks = unpack2<__half>(*reinterpret_cast<const uint32_t*>(kt + Int4Tile<D>::kCodeBytes + 4 * t));
     const float2 vs = unpack2<__half>(*reinterpret_cast<const uint32_t*>(vt + Int4Tile<D>::kCodeBytes + 4 * t));
+    const uint32_t pick = t & 1 ? 0x7632 : 0x5410;
 #pragma unroll
-    for (int v = 0; v < 2; ++v) {
-      const uint32_t codes = v ? vc : kc;
-      const float2 sm = v ? vs : ks;
-      const uint32_t even = codes & 0x0f0f0f0fu, odd = codes >> 4 & 0x0f0f0f0fu;
-      uint32_t w[4];
+    for (int j = 0; j < 2; ++j) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        // The code as the low byte of 2^23's bits; s * c is exact in float32
-        // (11 + 4 bits): fused or not, one rounding.
-        const float c0 = __uint_as_float(__byte_perm(even, 0x4b000000u, 0x7650 + i)) - 8388608.f;
-        const float c1 = __uint_as_float(__byte_perm(odd, 0x4b000000u, 0x7650 + i)) - 8388608.f;
-        w[i] = pack2<T>(fmaf(c0, sm.x, sm.y), fmaf(c1, sm.x, sm.y));
+      for (int v = 0; v < 2; ++v) {
+        const uint32_t codes = v ? __byte_perm(vw[j].x, vw[j].y, pick) : kc[j];
+        const float2 sm = v ? vs : ks;
+        const uint32_t even = codes & 0x0f0f0f0fu, odd = codes >> 4 & 0x0f0f0f0fu;
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          // The code as the low byte of 2^23's bits; s * c is exact in float32
+          // (11 + 4 bits): fused or not, one rounding.
+          float x = __uint_as_float(__byte_perm(even, 0x4b000000u, 0x7650 + i));
+          float y = __uint_as_float(__byte_perm(odd, 0x4b000000u, 0x7650 + i));
+          add2(x, y, -8388608.f, -8388608.f);
+          fma2(x, y, x, y, sm.x, sm.y, sm.y);
+          w[i] = pack2<T>(x, y);
+        }
+        kv[v][j] = make_uint4(w[0], w[1], w[2], w[3]);
       }
-      kv[v] = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
-  const int64_t at = (token * num_kv_heads + head) * C + c;
-  k_out[at] = kv[0];
-  v_out[at] = kv[1];
+  const int64_t at = (token * num_kv_heads + head) * (2 * C) + c;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    k_out[at + j * C] = kv[0][j];
+    v_out[at + j * C] = kv[1][j];
+  }
 }
 
 }  // namespace pkv

@@ -612,7 +612,7 @@ int read_int4_impl(const int32_t* slot_mapping, int32_t num_tokens, const void* 
                    void* k_out, void* v_out, const pkv_dims* d, cudaStream_t stream) {
   const int rc = check_int4_rows(k_out, v_out, slot_mapping, num_tokens, k_cache, v_cache, d, "read_int4");
   if (rc != PKV_OK || num_tokens == 0) return rc;
-  const int tokens_per_cta = pkv::kReadThreads / (d->head_dim / 8);
+  const int tokens_per_cta = pkv::kReadThreads / (d->head_dim / 16);
   const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(num_tokens) + tokens_per_cta - 1) / tokens_per_cta),
                   d->num_kv_heads);
   const int64_t slots = static_cast<int64_t>(d->num_blocks) * pkv::kBlockSize;
