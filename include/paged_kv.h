@@ -575,7 +575,7 @@ int paged_kv_selftest_stale_prologue_int4(const void* q, const void* k_new, cons
                                           void* v_cache, const int32_t* block_tables, const int32_t* context_lens,
                                           const int32_t* stale_block_tables, const int32_t* stale_context_lens,
                                           float scale, void* out, void* workspace, size_t workspace_bytes,
-                                          int32_t publish, const pkv_dims* dims, void* stream);
+                                          const pkv_dims* dims, void* stream);
 
 /* Synchronises `stream`, then reads and clears this device's error word.
  * Returns PKV_OK, PKV_ERR_OUT_OF_RANGE, PKV_ERR_NO_BLOCKS (nothing but a table

@@ -122,7 +122,7 @@ _SIGNATURES = {
                                                              ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                                                              ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                                                              ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p,
-                                                             ctypes.c_size_t, ctypes.c_int32,
+                                                             ctypes.c_size_t,
                                                              ctypes.POINTER(PkvDims), ctypes.c_void_p]),
     "paged_kv_check_status": (ctypes.c_int, [ctypes.c_void_p]),
     "paged_kv_last_error": (ctypes.c_char_p, []),

@@ -846,8 +846,7 @@ def paged_kv_selftest_stale_prologue_int4(q: torch.Tensor, k_new: Optional[torch
                                           context_lens: torch.Tensor, stale_block_tables: torch.Tensor,
                                           stale_context_lens: torch.Tensor, scale: float,
                                           out: Optional[torch.Tensor] = None,
-                                          workspace: Optional[torch.Tensor] = None, stream=None,
-                                          publish: bool = True) -> torch.Tensor:
+                                          workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """paged_kv_selftest_stale_prologue over 4-bit caches (attention alone when
     k_new / v_new are None).  Returns out."""
     dev, dims, out, workspace, ws_bytes = _int4_decode(q, k_cache, v_cache, block_tables, context_lens, out, workspace,
@@ -865,7 +864,7 @@ def paged_kv_selftest_stale_prologue_int4(q: torch.Tensor, k_new: Optional[torch
           (q.data_ptr(), k_new.data_ptr() if k_new is not None else 0, v_new.data_ptr() if v_new is not None else 0,
            k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(),
            stale_block_tables.data_ptr(), stale_context_lens.data_ptr(), scale, out.data_ptr(), workspace.data_ptr(),
-           ws_bytes, 1 if publish else 0, ctypes.byref(dims)))
+           ws_bytes, ctypes.byref(dims)))
     return out
 
 

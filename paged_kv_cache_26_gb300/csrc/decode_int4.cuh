@@ -1,7 +1,7 @@
-// Decode attention over a 4-bit pool (sm_103a): one persistent CTA per SM on the
-// partition of the (sequence, KV head, block) space that decode_persistent_kernel
-// uses, the same early reads before the grid wait, and the same pieces for
-// merge_persistent_kernel.
+// Decode attention over a 4-bit pool (sm_103a): one persistent CTA per SM, the
+// (sequence, KV head, block) space in equal shares, one per warp, and the early
+// reads before the grid wait of decode_persistent_kernel; then a merge of the
+// units that shares cut (merge_int4_kernel).
 //
 // A token is a quarter of a bf16 pool's bytes, so at the same bandwidth a warp
 // has a quarter of the instructions per token.  What the kernel does about it:
@@ -391,11 +391,6 @@ constexpr size_t int4_smem_bytes(int num_seqs) {
   return Int4Shape<D>::kRingBytes + (2 * static_cast<size_t>(num_seqs) + 1) * 4 + 128;
 }
 constexpr int kInt4MaxSeqs = 2048;
-// A 4-bit block counts as a quarter of one in the partition's thresholds: a
-// share's tail is handed out dynamically from 192 blocks on.  (8 x 32768 tokens,
-// 72 blocks a share: 68.7 us with thresholds in blocks, 58.2 us so; 256
-// sequences with a long tail of lengths, 112 blocks: 114 and 109 us.)
-constexpr int kInt4ShareUnit = 4;
 static_assert(int4_smem_bytes<128>(kInt4MaxSeqs) + 1536 <= 232448, "227 KB of shared memory, 1.5 KB kept for static");
 
 // What a stage holds (written when it is issued, read when it is consumed).
@@ -430,6 +425,31 @@ __device__ __forceinline__ void append_patch(uint8_t* tile, const uint8_t* rows,
   __syncwarp();
 }
 
+// Where the merge finds a unit's pieces.
+struct UnitPieces {
+  int32_t first;  // the share that it begins in, times two, + 1 if the piece is the share's second
+  int32_t count;  // pieces, of that share and the next ones; 0: one share wrote it whole
+};
+
+// The shares: share w is blocks [w R, (w + 1) R) of the flattened space (cut off
+// at `total`).  All of them are static.  (Handing out a share's tail dynamically
+// costs pieces, and a merge that runs after the grid: 64 x 16384 tokens 192.5 us
+// with dynamic tails and 184.7 without, 256 x 4096 205.8 and 200.4, 512 x 4096
+// 380.7 and 383.1.)  A few blocks are a short step of work and pieces cost
+// more than the warps they keep busy: a share is at least a 32nd of the average
+// unit, up to kFew blocks, and never between half of kFew and kFew.  (1 x 2048
+// tokens 10.7 us without this rule and 9.3 with it, 1 x 8192 20.7 and 14.8.)
+struct Int4Shares {
+  static constexpr int kFew = 8;
+  int total, R;
+  __device__ __forceinline__ Int4Shares(int total_, int nwarps, int units) : total(total_), R(1) {
+    if (total <= 0) return;
+    R = max((total + nwarps - 1) / nwarps, min(kFew, total / units / 32));
+    if (R > kFew / 2 && R < kFew) R = kFew;
+  }
+  __device__ __forceinline__ int start(int w) const { return min(total, w * R); }
+};
+
 // APPEND: the step, with k_new / v_new; else attention alone.  (One kernel for
 // both cost attention 3.5 us of 39 at 8 x 16384 tokens.)
 template <typename T, int D, bool APPEND>
@@ -443,7 +463,7 @@ __global__ void __maxnreg__(168) decode_int4_kernel(const DecodeArgs a) {
   static_assert(2 * kNewRowBytes <= Shape::kBlockBytes, "the appended rows fit one block");
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full_bar[NW][SW];
-  __shared__ int4 s_desc[NW][SW];  // per stage: sequence, KV head, StageInfo, segment id
+  __shared__ int4 s_desc[NW][SW];  // per stage: sequence, KV head, StageInfo, share (kept here, it costs no register)
   __shared__ int s_prow[NW][SW];   // per stage: pool row of its last block (the fused append's target)
   __shared__ int s_warp_sum[NW];
 
@@ -464,7 +484,7 @@ __global__ void __maxnreg__(168) decode_int4_kernel(const DecodeArgs a) {
   context_prefix(a, a.pre_context_lens ? a.pre_context_lens : a.context_lens, s_P, s_ctx, s_warp_sum, NW * 32,
                  !a.recheck && blockIdx.x == 0);
 
-  Partition part(Hkv * s_P[B], gridDim.x * NW, a.share_unit, B * Hkv);
+  Int4Shares part(Hkv * s_P[B], gridDim.x * NW, B * Hkv);
   const int gw = blockIdx.x * NW + warp;
 
   // Sequence b, KV head kvh and block j of flattened block f: units are
@@ -488,20 +508,19 @@ __global__ void __maxnreg__(168) decode_int4_kernel(const DecodeArgs a) {
   const int32_t* tables = a.pre_block_tables ? a.pre_block_tables : a.block_tables;
   bool after_wait = !a.recheck;  // block ids are flagged only from values known to be final
 
-  // ---- issue side: current segment [seg_s, seg_e) and a 32-block window of it,
+  // ---- issue side: the share [seg_s, seg_e) and a 32-block window of it,
   // lane i describing block win_s + i.  The window is cut into stages at the
   // unit borders and every NB blocks (and before a unit's last block where the
   // appended rows would find no room): lane i's block belongs to stage
   // wstage, and the first lane of a stage holds its description.
-  int seg, seg_s, seg_e;
-  int win_s, win_e, ip;              // window, and the first block not yet issued
+  int seg_s, seg_e;
+  int win_s, win_e;                  // window
   int stage_i = 0, stages = 0;       // next stage of the window to issue, and how many it has
   int wb = -1, wkvh = 0, wj = 0, wphys = -1, wrow = -kBlockSize, wstage = -1, wslot = 0, winfo = 0;
   bool bad_window = false;           // some block of the window is outside the pool
-  bool more = true;
   auto fill_window = [&]() {
-    win_s = ip;
-    win_e = min(seg_e, ip + 32);
+    win_s = win_e;
+    win_e = min(seg_e, win_s + 32);
     stage_i = 0;
     wb = -1; wkvh = 0; wj = 0; wphys = -1; wrow = -kBlockSize; wstage = -1; wslot = 0; winfo = 0;
     const int n = win_e - win_s;
@@ -534,63 +553,23 @@ __global__ void __maxnreg__(168) decode_int4_kernel(const DecodeArgs a) {
     }
     bad_window = __any_sync(0xffffffffu, in && wrow < 0);
   };
-  // Start on this warp's static head segment.
-  auto start_head = [&]() {
-    part.head(gw, seg_s, seg_e);
-    seg = gw;
-    ip = win_s = win_e = seg_s;
+  auto start_share = [&]() {
+    seg_s = part.start(gw);
+    seg_e = part.start(gw + 1);
+    win_s = win_e = seg_s;
     stage_i = stages = 0;
-    more = true;
-    if (ip < seg_e) fill_window();
-  };
-  // Next window: the rest of this segment, else the next claimed chunk.
-  auto advance = [&]() {
-    ip = win_e;
-    if (ip < seg_e) {
-      fill_window();
-      return;
-    }
-    if (part.nchunks == 0) {  // all head: nothing to claim, the counters stay untouched
-      more = false;
-      return;
-    }
-    while (true) {
-      int q = 0;
-      if (lane == 0) q = atomicAdd(a.sched, 1);
-      q = __shfl_sync(0xffffffffu, q, 0);
-      if (q >= part.num_chunks()) {
-        more = false;
-        // The last warp to run out of chunks resets the counters for the next call.
-        if (lane == 0 && atomicAdd(a.sched + 1, 1) == part.nwarps - 1) {
-          a.sched[0] = 0;
-          a.sched[1] = 0;
-        }
-        return;
-      }
-      int s, e;
-      part.chunk(q / part.nwarps, q % part.nwarps, s, e);
-      if (e > s) {
-        seg = part.nwarps + q;
-        seg_s = s;
-        seg_e = e;
-        ip = s;
-        fill_window();
-        return;
-      }
-    }
+    if (win_e < seg_e) fill_window();
   };
 
   int issued = 0, consumed = 0;
   int st_i = 0;            // stage slot the next issue fills
   int st_c = 0, ph_c = 0;  // stage slot the next consume reads, and its phase parity
-  // Fill free stage slots.  With may_advance false the issue stops at the end
-  // of the current window: no chunk is claimed from the counter.
+  // Fill free stage slots; with may_advance false, up to the end of the window.
   auto issue_stages = [&](bool may_advance) {
-    while (more && issued - consumed < SW) {
+    while (issued - consumed < SW) {
       if (stage_i == stages) {
-        if (!may_advance) break;
-        advance();
-        if (!more) break;
+        if (!may_advance || win_e >= seg_e) break;
+        fill_window();
       }
       const bool mine = wstage == stage_i;
       const uint32_t bar = smem_u32(&full_bar[warp][st_i]);
@@ -608,7 +587,7 @@ __global__ void __maxnreg__(168) decode_int4_kernel(const DecodeArgs a) {
       }
       __syncwarp();  // every lane is done with this slot's last contents
       if (mine && wslot == 0) {
-        s_desc[warp][st_i] = make_int4(wb, wkvh, winfo, seg);
+        s_desc[warp][st_i] = make_int4(wb, wkvh, winfo, gw);
         if (APPEND && (winfo & StageInfo::kUnitEnd)) {
           // A unit's last stage: the appended token's K and V rows too.
           const int64_t unit = static_cast<int64_t>(wb) * Hkv + wkvh;
@@ -645,7 +624,7 @@ __global__ void __maxnreg__(168) decode_int4_kernel(const DecodeArgs a) {
 
   // The head's first window (inputs only), its first stages' tiles prefetched
   // into L2, then the wait for the previous kernels in the stream.
-  start_head();
+  start_share();
   if (lane < SW * NB && win_s + lane < win_e && wrow >= 0) {
     const int64_t off = static_cast<int64_t>(wrow) * Tile::kRowBytes;
     prefetch_l2_bulk(static_cast<const uint8_t*>(a.k_cache_w) + off, Tile::kBytes);
@@ -693,22 +672,25 @@ __global__ void __maxnreg__(168) decode_int4_kernel(const DecodeArgs a) {
         // rebuild from changing s_ctx while another warp still compares.
         __syncthreads();
         context_prefix_again(a, s_P, s_ctx, s_warp_sum, NW * 32);
-        part = Partition(Hkv * s_P[B], gridDim.x * NW, a.share_unit, B * Hkv);
+        part = Int4Shares(Hkv * s_P[B], gridDim.x * NW, B * Hkv);
       }
-      start_head();
+      start_share();
     } else if (in_window) {
       tile_row(wphys, wkvh, a, true);
     }
   }
 
-  // The lengths and block prefix this grid partitioned go to the merge of the
-  // same call, under its tag.
-  if (a.epoch != 0 && blockIdx.x == gridDim.x - 1 && warp == NW - 1) {
-    for (int b = lane; b < B; b += 32) a.pub[1 + b] = s_ctx[b];
-    for (int b = lane; b <= B; b += 32) a.pub[1 + B + b] = s_P[b];
-    __syncwarp();  // the lanes' stores come before lane 0's (cumulative) release
-    if (lane == 0) st_release_gpu(a.pub, static_cast<int32_t>(a.epoch));
+  // What the merge will find of each unit, and zero rows for empty contexts.
+  const int spread = warp * gridDim.x + blockIdx.x;  // a few warps of all CTAs
+  for (int u = spread * 32 + lane; u < B * Hkv; u += gridDim.x * NW * 32) {
+    const int b = u / Hkv, nb = (s_ctx[b] + kBlockSize - 1) / kBlockSize, U = Hkv * s_P[b] + (u - b * Hkv) * nb;
+    const int w = U / part.R, n = nb > 0 ? (U + nb - 1) / part.R - w + 1 : 1;
+    reinterpret_cast<UnitPieces*>(a.sched)[u] = {2 * w + (U > w * part.R ? 1 : 0), n > 1 ? n : 0};
   }
+  for (int b = spread; b < B; b += gridDim.x * NW)
+    if (s_ctx[b] == 0)
+      for (int i = lane; i < a.num_q_heads * (D / 8); i += 32)
+        reinterpret_cast<uint4*>(a.out)[static_cast<int64_t>(b) * a.num_q_heads * (D / 8) + i] = make_uint4(0, 0, 0, 0);
 
   // ---- consume side
   Attn at;
@@ -720,7 +702,7 @@ __global__ void __maxnreg__(168) decode_int4_kernel(const DecodeArgs a) {
     __syncwarp();  // the descriptions written at issue are visible to the warp
 
     const int4 dsc = s_desc[warp][st_c];
-    const int b = dsc.x, kvh = dsc.y, info = dsc.z, sid = dsc.w;
+    const int b = dsc.x, kvh = dsc.y, info = dsc.z, share = dsc.w;
     if (info & (StageInfo::kUnitStart | StageInfo::kSegStart)) {
       // While the tiles are under way: the query rows (L2), and a fresh state.
       if (info & StageInfo::kSegStart) seg_first_flush = true;
@@ -747,11 +729,11 @@ __global__ void __maxnreg__(168) decode_int4_kernel(const DecodeArgs a) {
     next_oldest();
 
     if (info & (StageInfo::kUnitEnd | StageInfo::kSegEnd)) {
-      // ---- the unit ends here or the segment does: write it out, or leave a piece for the merge
+      // ---- the unit ends here or the share does: write it out, or leave a piece for the merge
       at.finish_sums();
       const int gid = lane >> 2, c = lane & 3;
       const bool complete = from_start && (info & StageInfo::kUnitEnd);
-      const int64_t pbase = (static_cast<int64_t>(sid) * 2 + (seg_first_flush ? 0 : 1)) * kMaxGroup;
+      const int64_t pbase = (static_cast<int64_t>(share) * 2 + (seg_first_flush ? 0 : 1)) * kMaxGroup;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int h = 2 * c + e;
@@ -789,185 +771,121 @@ __global__ void __maxnreg__(168) decode_int4_kernel(const DecodeArgs a) {
 
 // ===================================================================== merge
 
-// Merge of the pieces the decode kernel left, one warp per unit (sequence, KV
-// head): what merge_persistent_kernel does for one query head at a time, with
-// the unit's pieces found once for all heads of its group and the heads' loads
-// in flight together.  For many rows: a warp per row spends its time finding the
-// pieces, the same ones for every head of a unit.
-constexpr int kUnitMergeWarps = 4;
-
-template <typename T, int D>
-__global__ void __launch_bounds__(kUnitMergeWarps * 32) merge_units_kernel(const DecodeArgs a, int32_t nwarps) {
+// Merge of the units that shares cut.  S = 1: a warp per HN heads of a unit; S =
+// kMergeWarps: a CTA per head, its warps every S-th piece.  A chain of two round
+// trips to L2 after the decode grid's end (the description of the unit's pieces;
+// the log-sum-exps together with the first pieces), where merge_persistent_kernel,
+// which works the plan out from the lengths, takes four: no CTA of it fits beside
+// a decode CTA (registers), so that nothing of it can be done before.
+template <typename T, int D, int HN, int S>
+__global__ void __launch_bounds__(kMergeWarps * 32, HN == 4 ? 4 : 8) merge_int4_kernel(const DecodeArgs a) {
+  static_assert(S == 1 || (S == kMergeWarps && HN == 1), "several warps take one head");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  constexpr int kPer = D / 32;
-  extern __shared__ int merge_smem[];
-  __shared__ int s_warp_sum[kUnitMergeWarps];
-  __shared__ int s_row[kUnitMergeWarps][32];
-  int* s_P = merge_smem;
-  int* s_ctx = s_P + a.num_seqs + 1;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr int kThreads = kUnitMergeWarps * 32;
-  const int B = a.num_seqs, Hkv = a.num_kv_heads, g = a.group;
-  const int unit = blockIdx.x * kUnitMergeWarps + warp;
-  const bool live = unit < B * Hkv;
-  const int b = live ? unit / Hkv : 0, kvh = unit - b * Hkv;
-
-  // The lengths the decode grid partitioned: published by it under the call's
-  // tag, or read here (and, if they may be stale, checked after the wait), as
-  // in merge_persistent_kernel.
-  bool published = false;
-  if (a.recheck && a.epoch != 0) {
-    const int32_t tag = static_cast<int32_t>(a.epoch);
-    __shared__ int s_got;
-    if (threadIdx.x == 0) {
-      const unsigned long long t0 = global_ns();
-      bool got = ld_acquire_gpu(a.pub) == tag;
-      while (!got && global_ns() - t0 < kWaitLimitNs) {
-        __nanosleep(256);
-        got = ld_acquire_gpu(a.pub) == tag;
-      }
-      s_got = got;
-    }
-    __syncthreads();
-    published = s_got != 0;
-  }
-  if (!published)
-    context_prefix(a, a.pre_context_lens ? a.pre_context_lens : a.context_lens, s_P, s_ctx, s_warp_sum, kThreads,
-                   false);
-
-  // The unit's blocks [U, Uend) and its candidate segments, those of shares
-  // w0 .. ; ncand = 0: one segment holds it all, and the decode kernel wrote it.
-  int nb = 0, U = 0, w0 = 0, ncand = 0;
-  Partition part(0, nwarps, a.share_unit, B * Hkv);
-  auto plan = [&]() {
-    const int ctx = published ? __ldcg(a.pub + 1 + b) : s_ctx[b];
-    const int before = published ? __ldcg(a.pub + 1 + B + b) : s_P[b];
-    const int blocks = published ? __ldcg(a.pub + 1 + B + B) : s_P[B];
-    part = Partition(Hkv * blocks, nwarps, a.share_unit, B * Hkv);
-    nb = (ctx + kBlockSize - 1) / kBlockSize;
-    ncand = 0;
-    if (!live || nb == 0) return;
-    U = Hkv * before + kvh * nb;
-    w0 = U / part.R;
-    const int w1 = (U + nb - 1) / part.R;
-    if (part.nchunks == 0) {  // a share is one segment
-      if (w1 > w0) ncand = w1 - w0 + 1;
-      return;
-    }
-    int s, e;
-    part.segment_of(U, s, e);
-    if (e < U + nb) ncand = (w1 - w0 + 1) * part.seg_per_share();
-  };
-  // Row of the piece (its first head's) that candidate c left, or -1 where that
-  // segment does not overlap the unit.
-  auto piece = [&](int c) -> int {
-    int w, s, e, sid;
-    if (part.nchunks == 0) {
-      sid = w = w0 + c;
-      part.head(w, s, e);
-    } else {
-      const int per = part.seg_per_share(), k = c % per;
-      w = w0 + c / per;
-      if (k == 0) {
-        part.head(w, s, e);
-        sid = w;
-      } else {
-        part.chunk(k - 1, w, s, e);
-        sid = part.nwarps + (k - 1) * part.nwarps + w;
-      }
-    }
-    if (e <= s || e <= U || s >= U + nb) return -1;
-    return (sid * 2 + (U > s ? 1 : 0)) * kMaxGroup;
-  };
-  // Candidates 32 k + lane, compacted: how many overlap.
-  auto gather = [&](int k) -> int {
-    const int c = 32 * k + lane;
-    const int row = c < ncand ? piece(c) : -1;
-    const unsigned valid = __ballot_sync(0xffffffffu, row >= 0);
-    __syncwarp();  // the last batch's rows have been read
-    if (row >= 0) s_row[warp][__popc(valid & ((1u << lane) - 1))] = row;
-    __syncwarp();
-    return __popc(valid);
-  };
-  plan();
-  int count = ncand > 0 ? gather(0) : 0;
+  constexpr int kPer = D / 32, kFly = 8 / HN;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = S == 1 ? 0 : warp;
+  const int task = S == 1 ? blockIdx.x * kMergeWarps + warp : blockIdx.x;
+  const int per = (a.group + HN - 1) / HN, unit = task / per, h0 = (task - unit * per) * HN;
+  const int heads = HN == 1 ? 1 : min(HN, a.group - h0);
+  const bool live = S > 1 || unit < a.num_seqs * a.num_kv_heads;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (!published && a.recheck && context_changed(a, s_ctx, kThreads, false)) {
-    context_prefix(a, a.context_lens, s_P, s_ctx, s_warp_sum, kThreads, false);
-    plan();
-    count = ncand > 0 ? gather(0) : 0;
-  }
-  if (!live) return;
-  T* out = static_cast<T*>(a.out) + (static_cast<int64_t>(b) * a.num_q_heads + kvh * g) * D + lane * kPer;
-  if (nb == 0) {  // an empty context: zero rows
-    for (int h = 0; h < g; ++h)
+  const int2 c = live ? __ldcg(reinterpret_cast<const int2*>(a.sched) + unit) : make_int2(0, 0);  // UnitPieces
+  const int pieces = c.y;
+  if (pieces == 0) return;
+  const int n = (pieces - sub + S - 1) / S;  // this warp's
+  auto row = [&](int i) {
+    const int p = sub + S * i;
+    return (p == 0 ? c.x : (c.x & ~1) + 2 * p) * kMaxGroup + h0;
+  };
+  float m[HN], L[HN], o[HN][kPer];
 #pragma unroll
-      for (int k = 0; k < kPer; k += 2) *reinterpret_cast<uint32_t*>(out + h * D + k) = 0;
-    return;
-  }
-  if (ncand == 0) return;
-
-  float m[kMaxGroup], L[kMaxGroup], o[kMaxGroup][kPer];
-#pragma unroll
-  for (int h = 0; h < kMaxGroup; ++h) {
+  for (int h = 0; h < HN; ++h) {
     m[h] = -INFINITY;
     L[h] = 0.f;
 #pragma unroll
     for (int k = 0; k < kPer; ++k) o[h][k] = 0.f;
   }
-  for (int k = 0; 32 * k < ncand; ++k) {
-    if (k > 0) count = gather(k);
-    if (count == 0) continue;
-    const float* lse = a.part_lse + s_row[warp][min(lane, count - 1)];
-    float w[kMaxGroup];
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    const int count = min(32, n - i0);
+    float w[HN];
 #pragma unroll
-    for (int h = 0; h < kMaxGroup; ++h) w[h] = h < g && lane < count ? __ldcg(lse + h) : -INFINITY;
+    for (int h = 0; h < HN; ++h)
+      w[h] = lane < count && h < heads ? __ldcg(a.part_lse + row(i0 + lane) + h) : -INFINITY;
+    for (int i = 0; i < count; i += kFly) {
+      float v[kFly][HN][kPer];
 #pragma unroll
-    for (int h = 0; h < kMaxGroup; ++h) {
-      if (h < g) {
-        float mx = w[h];
+      for (int u = 0; u < kFly; ++u) {
+        if (i + u >= count) break;
+        const float* src = a.part_o + static_cast<int64_t>(row(i0 + i + u)) * D + lane * kPer;
 #pragma unroll
-        for (int s = 16; s > 0; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
-        mx = fmaxf(mx, m[h]);
-        const float sc = exp2f(m[h] - mx);
-        m[h] = mx;
-        w[h] = exp2f(w[h] - mx);
-        float sum = w[h];
-#pragma unroll
-        for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
-        L[h] = L[h] * sc + sum;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) o[h][i] *= sc;
-      }
-    }
-    for (int i = 0; i < count; ++i) {
-      const float* src = a.part_o + static_cast<int64_t>(s_row[warp][i]) * D + lane * kPer;
-      float v[kMaxGroup][kPer];
-#pragma unroll
-      for (int h = 0; h < kMaxGroup; ++h) {
-        if (h < g) {
+        for (int h = 0; h < HN; ++h) {  // (rows past the group's heads exist and are not used)
           if constexpr (kPer == 4) {
             const float4 f = __ldcg(reinterpret_cast<const float4*>(src + h * D));
-            v[h][0] = f.x, v[h][1] = f.y, v[h][2] = f.z, v[h][3] = f.w;
+            v[u][h][0] = f.x, v[u][h][1] = f.y, v[u][h][2] = f.z, v[u][h][3] = f.w;
           } else {
             const float2 f = __ldcg(reinterpret_cast<const float2*>(src + h * D));
-            v[h][0] = f.x, v[h][1] = f.y;
+            v[u][h][0] = f.x, v[u][h][1] = f.y;
           }
         }
       }
+      if (i == 0) {  // the weights, with the first rows on their way
 #pragma unroll
-      for (int h = 0; h < kMaxGroup; ++h) {
-        if (h < g) {
-          const float wi = __shfl_sync(0xffffffffu, w[h], i);
+        for (int h = 0; h < HN; ++h) {
+          float mx = w[h];
 #pragma unroll
-          for (int k2 = 0; k2 < kPer; ++k2) o[h][k2] = fmaf(wi, v[h][k2], o[h][k2]);
+          for (int s = 16; s > 0; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
+          mx = fmaxf(mx, m[h]);
+          const float sc = exp2f(m[h] - mx);
+          m[h] = mx;
+          w[h] = exp2f(w[h] - mx);
+          float sum = w[h];
+#pragma unroll
+          for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
+          L[h] = L[h] * sc + sum;
+#pragma unroll
+          for (int k = 0; k < kPer; ++k) o[h][k] *= sc;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kFly; ++u) {
+        if (i + u >= count) break;
+#pragma unroll
+        for (int h = 0; h < HN; ++h) {
+          const float wi = __shfl_sync(0xffffffffu, w[h], i + u);
+#pragma unroll
+          for (int k = 0; k < kPer; ++k) o[h][k] = fmaf(wi, v[u][h][k], o[h][k]);
         }
       }
     }
   }
+  if constexpr (S > 1) {
+    __shared__ float s_ml[S][2];
+    __shared__ __align__(16) float s_o[S][D];
+    if (lane == 0) {
+      s_ml[sub][0] = m[0];
+      s_ml[sub][1] = L[0];
+    }
 #pragma unroll
-  for (int h = 0; h < kMaxGroup; ++h) {
-    if (h < g) {
+    for (int k = 0; k < kPer; ++k) s_o[sub][lane * kPer + k] = o[0][k];
+    __syncthreads();
+    if (sub > 0) return;
+    float mx = m[0];
+#pragma unroll
+    for (int s = 1; s < S; ++s) mx = fmaxf(mx, s_ml[s][0]);
+    L[0] = 0.f;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) o[0][k] = 0.f;
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      const float sc = exp2f(s_ml[s][0] - mx);  // 0 for a warp without pieces
+      L[0] = fmaf(s_ml[s][1], sc, L[0]);
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) o[0][k] = fmaf(s_o[s][lane * kPer + k], sc, o[0][k]);
+    }
+  }
+  T* out = static_cast<T*>(a.out) + (static_cast<int64_t>(unit) * a.group + h0) * D + lane * kPer;
+#pragma unroll
+  for (int h = 0; h < HN; ++h) {
+    if (h < heads) {
       const float inv = 1.f / L[h];
 #pragma unroll
       for (int k = 0; k < kPer; k += 2)

@@ -198,10 +198,11 @@ int plan_splits(const pkv_dims* d, int32_t requested, SplitPlan* plan) {
 }
 
 // Workspace regions: [partial outputs][partial log-sum-exps][publication of
-// the decode grid's lengths to its merge][scheduler counters].
+// the decode grid's lengths to its merge][scheduler counters][4-bit pools: each unit's
+// pieces].
 struct WorkspaceLayout {
-  size_t o_bytes = 0, lse_bytes = 0, sched_bytes = 0, pub_bytes = 0;
-  size_t total() const { return o_bytes + lse_bytes + sched_bytes + pub_bytes; }
+  size_t o_bytes = 0, lse_bytes = 0, sched_bytes = 0, pub_bytes = 0, unit_bytes = 0;
+  size_t total() const { return o_bytes + lse_bytes + sched_bytes + pub_bytes + unit_bytes; }
 };
 
 // Segments of the persistent partition for the largest grid (one CTA per SM).
@@ -216,6 +217,7 @@ WorkspaceLayout workspace_layout(const pkv_dims* d, const SplitPlan& p) {
     w.o_bytes = align256(seg * 2 * pkv::kMaxGroup * d->head_dim * sizeof(float));
     w.lse_bytes = align256(seg * 2 * pkv::kMaxGroup * sizeof(float));
     w.sched_bytes = 256;
+    w.unit_bytes = align256(static_cast<size_t>(d->num_seqs) * d->num_kv_heads * sizeof(pkv::UnitPieces));
     // The decode grid's validated lengths and block prefix, for the merge:
     // [epoch][context B][prefix B + 1] int32.
     w.pub_bytes = align256((2 * static_cast<size_t>(d->num_seqs) + 2) * sizeof(int32_t));
@@ -255,19 +257,18 @@ void with_type_and_dim(const pkv_dims* d, F&& f) {
     bf16 ? f(__nv_bfloat16{}, std::integral_constant<int, 64>{}) : f(__half{}, std::integral_constant<int, 64>{});
 }
 
-// Persistent decode (`kern`, of `warps` warps a CTA and smem(B) bytes of dynamic
-// shared memory) + merge.  Both are programmatic dependent launches: each
+// Persistent decode + merge.  Both are programmatic dependent launches: each
 // may start while the kernel before it in the stream finishes, and waits
 // in-kernel (griddepcontrol.wait) before touching anything that kernel writes.
-// MERGE_UNITS: where units are many, merge by unit (merge_units_kernel) and not
-// by row.
-template <typename T, int D, auto kern, bool MERGE_UNITS = false, typename... KernArgs>
-int launch_persistent(int warps, size_t (*smem)(int), const pkv::DecodeArgs& args, const pkv_dims* d, int max_seqs,
-                      cudaStream_t stream, bool pdl, const KernArgs&... kern_args) {
-  cudaError_t e = configure_smem<kern>(static_cast<int>(smem(max_seqs)));
-  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(persistent decode kernel)");
+template <typename T, int D, bool F8>
+int launch_persistent(const CUtensorMap& mk, const CUtensorMap& mv, const pkv::DecodeArgs& args,
+                      const pkv_dims* d, int max_seqs, cudaStream_t stream, bool pdl = true) {
+  using PS = pkv::PersistentShape<D, F8>;
+  constexpr auto kern = pkv::decode_persistent_kernel<T, D, F8>;
+  cudaError_t e = configure_smem<kern>(static_cast<int>(pkv::persistent_smem_bytes<D, F8>(max_seqs)));
+  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(decode_persistent_kernel)");
   const int64_t upper_blocks = static_cast<int64_t>(d->num_seqs) * d->num_kv_heads * d->max_blocks_per_seq;
-  int64_t grid = (upper_blocks + warps - 1) / warps;
+  int64_t grid = (upper_blocks + PS::kWarps - 1) / PS::kWarps;
   if (grid > device_sms()) grid = device_sms();
   if (grid < 1) grid = 1;
   cudaLaunchAttribute attr[1];
@@ -275,49 +276,35 @@ int launch_persistent(int warps, size_t (*smem)(int), const pkv::DecodeArgs& arg
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  cfg.blockDim = dim3(warps * 32);
-  cfg.dynamicSmemBytes = smem(d->num_seqs);
+  cfg.blockDim = dim3(PS::kWarps * 32);
+  cfg.dynamicSmemBytes = pkv::persistent_smem_bytes<D, F8>(d->num_seqs);
   cfg.stream = stream;
   cfg.attrs = attr;
   // !pdl: the kernel before this one wrote its inputs (block tables, lengths,
   // query), which it reads before griddepcontrol.wait: no early launch.
   cfg.numAttrs = pdl ? 1 : 0;
-  e = cudaLaunchKernelEx(&cfg, kern, kern_args...);
-  if (e != cudaSuccess) return cuda_fail(e, "persistent decode kernel launch");
+  e = cudaLaunchKernelEx(&cfg, kern, mk, mv, args);
+  if (e != cudaSuccess) return cuda_fail(e, "decode_persistent_kernel launch");
   cfg.numAttrs = 1;
   // Long units cut into many pieces (on average 8 or more warp shares per
   // unit): a CTA per row, its warps splitting the row's pieces; otherwise a
   // warp per row (measured: at 7.1 shares, the E4M3 pool at B=32, a warp per
   // row 0.741 against 0.703; at 9.5, bf16 at B=16, a CTA per row 0.784
   // against 0.770).
-  const int32_t nwarps = static_cast<int32_t>(grid) * warps;
+  const int32_t nwarps = static_cast<int32_t>(grid) * PS::kWarps;
   const int64_t units = static_cast<int64_t>(d->num_seqs) * d->num_kv_heads;
   const bool coop = nwarps >= 8 * units;
   // Two or more warp shares per unit on average: rows have many pieces, so
   // fold up to 16 per round trip (fewer registers leave room for more merge
   // CTAs beside the decode grid, which pays when rows are many and short).
-  const int rows = d->num_seqs * d->num_q_heads;
-  // Beside 4-bit decode CTAs no merge CTA fits whatever its registers, so there
-  // the small ones are better as soon as rows are many (us, small and wide: 64 x
-  // 2048 tokens, 32 heads 33.6 and 35.2; 48 sequences 28.9 and 29.4; 32 23.9 and
-  // 22.6).
-  const bool wide = !coop && nwarps >= 2 * units && !(MERGE_UNITS && rows > 8 * device_sms());
+  const bool wide = !coop && nwarps >= 2 * units;
   const int merge_smem = static_cast<int>((2 * static_cast<size_t>(max_persistent_seqs(d, kPool16)) + 1) * 4);
+  const int rows = d->num_seqs * d->num_q_heads;
   const int rows_per_cta = coop ? 1 : pkv::kMergeWarps;
   cfg.gridDim = dim3(static_cast<unsigned>((rows + rows_per_cta - 1) / rows_per_cta));
   cfg.blockDim = dim3(pkv::kMergeWarps * 32);
   cfg.dynamicSmemBytes = (2 * static_cast<size_t>(d->num_seqs) + 1) * 4;
-  // A warp per unit where rows are many and share their unit's plan (us, a warp
-  // per row and per unit, 4-bit pools: 1024 x 256 tokens, 8 x 4 heads 173 and 91;
-  // 512 x 512 80 and 66; 128 x 2048 57.1 and 57.0; but 64 x 2048 35.1 and 36.1,
-  // and 1024 x 256 with one head a unit 85 and 88).
-  if (MERGE_UNITS && !coop && rows >= 4096 && args.group > 1) {
-    constexpr auto merge = pkv::merge_units_kernel<T, D>;
-    cfg.gridDim = dim3(static_cast<unsigned>((units + pkv::kUnitMergeWarps - 1) / pkv::kUnitMergeWarps));
-    cfg.blockDim = dim3(pkv::kUnitMergeWarps * 32);
-    e = configure_smem<merge>(merge_smem);
-    if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, merge, args, nwarps);
-  } else if (coop) {
+  if (coop) {
     constexpr auto merge = pkv::merge_persistent_kernel<T, D, true>;
     e = configure_smem<merge>(merge_smem);
     if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, merge, args, nwarps);
@@ -334,14 +321,59 @@ int launch_persistent(int warps, size_t (*smem)(int), const pkv::DecodeArgs& arg
   return PKV_OK;
 }
 
+// Decode over a 4-bit pool and its merge, with the same programmatic dependence.
+int launch_int4(const pkv::DecodeArgs& args, const pkv_dims* d, bool append, cudaStream_t stream, bool pdl) {
+  cudaError_t e = cudaSuccess;
+  with_type_and_dim(d, [&](auto t, auto dim) {
+    using T = decltype(t);
+    constexpr int D = decltype(dim)::value;
+    const int64_t upper_blocks = static_cast<int64_t>(d->num_seqs) * d->num_kv_heads * d->max_blocks_per_seq;
+    const int64_t ctas = (upper_blocks + pkv::Int4Shape<D>::kWarps - 1) / pkv::Int4Shape<D>::kWarps;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(ctas, device_sms()))));
+    cfg.blockDim = dim3(pkv::Int4Shape<D>::kWarps * 32);
+    cfg.dynamicSmemBytes = pkv::int4_smem_bytes<D>(d->num_seqs);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl ? 1 : 0;
+    auto launch = [&](auto kern) {
+      e = configure_smem<decltype(kern)::value>(static_cast<int>(pkv::int4_smem_bytes<D>(pkv::kInt4MaxSeqs)));
+      if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, decltype(kern)::value, args);
+    };
+    if (append)
+      launch(std::integral_constant<decltype(&pkv::decode_int4_kernel<T, D, true>), pkv::decode_int4_kernel<T, D, true>>{});
+    else
+      launch(
+          std::integral_constant<decltype(&pkv::decode_int4_kernel<T, D, false>), pkv::decode_int4_kernel<T, D, false>>{});
+    if (e != cudaSuccess) return;
+    // Units of eight or more shares on average have many pieces: a CTA per head.
+    // Else a warp per head, or, with more heads than the GPU holds such warps at
+    // once, per four heads of a unit.
+    const int64_t units = static_cast<int64_t>(d->num_seqs) * d->num_kv_heads, rows = units * args.group;
+    const bool many = static_cast<int64_t>(cfg.gridDim.x) * pkv::Int4Shape<D>::kWarps >= 8 * units;
+    const bool fours = !many && rows > 32 * static_cast<int64_t>(device_sms());
+    const int64_t warps = fours ? units * ((args.group + 3) / 4) : rows;
+    cfg.gridDim = dim3(static_cast<unsigned>(many ? rows : (warps + pkv::kMergeWarps - 1) / pkv::kMergeWarps));
+    cfg.blockDim = dim3(pkv::kMergeWarps * 32);
+    cfg.dynamicSmemBytes = 0;
+    cfg.numAttrs = 1;
+    e = many    ? cudaLaunchKernelEx(&cfg, pkv::merge_int4_kernel<T, D, 1, pkv::kMergeWarps>, args)
+        : fours ? cudaLaunchKernelEx(&cfg, pkv::merge_int4_kernel<T, D, 4, 1>, args)
+                : cudaLaunchKernelEx(&cfg, pkv::merge_int4_kernel<T, D, 1, 1>, args);
+  });
+  if (e != cudaSuccess) return cuda_fail(e, "decode_int4_kernel launch");
+  return PKV_OK;
+}
+
 template <typename T, int D>
 int launch_decode(const CUtensorMap& mk, const CUtensorMap& mv, const pkv::DecodeArgs& args, const SplitPlan& plan,
                   const pkv_dims* d, cudaStream_t stream, bool pdl) {
   using Shape = pkv::TileShape<D>;
   if (plan.persistent)
-    return launch_persistent<T, D, pkv::decode_persistent_kernel<T, D>>(
-        pkv::PersistentShape<D>::kWarps, pkv::persistent_smem_bytes<D>, args, d, max_persistent_seqs(d, kPool16), stream,
-        pdl, mk, mv, args);
+    return launch_persistent<T, D, false>(mk, mv, args, d, max_persistent_seqs(d, kPool16), stream, pdl);
   constexpr int kSmem = kStages * Shape::kStageBytes + 1024;
   constexpr auto kern = pkv::decode_split_kernel<T, D, kConsumerWarps, kStages>;
   cudaError_t e = configure_smem<kern>(kSmem);
@@ -435,11 +467,12 @@ int decode_impl(const void* q, const void* k_new, const void* v_new, void* k_cac
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   args.part_o = need ? reinterpret_cast<float*>(ws) : nullptr;
   args.part_lse = need ? reinterpret_cast<float*>(ws + wl.o_bytes) : nullptr;
-  // [partials][log-sum-exps][publication][scheduler counters]
+  // [partials][log-sum-exps][publication][scheduler counters][units' pieces]
   args.pub = wl.pub_bytes ? reinterpret_cast<int32_t*>(ws + wl.o_bytes + wl.lse_bytes) : nullptr;
   args.sched = wl.sched_bytes ? reinterpret_cast<int32_t*>(ws + wl.o_bytes + wl.lse_bytes + wl.pub_bytes) : nullptr;
+  if (format == kPoolInt4) args.sched = reinterpret_cast<int32_t*>(ws + wl.total() - wl.unit_bytes);
   args.epoch = 0;
-  if (recheck && publish && plan.persistent && args.pub) {
+  if (recheck && publish && plan.persistent && args.pub && format != kPoolInt4) {
     // A new tag per call, so that a merge never takes an earlier call's
     // publication for its own; 0 (no publication: the merge re-reads the
     // lengths itself) while the stream is being captured, since a graph
@@ -465,30 +498,12 @@ int decode_impl(const void* q, const void* k_new, const void* v_new, void* k_cac
   args.num_blocks = d->num_blocks;
   args.num_splits = plan.num_splits;
   args.split_blocks = plan.split_blocks;
-  args.share_unit = format == kPoolInt4 ? pkv::kInt4ShareUnit : 1;
-
   const bool bf16 = d->dtype == PKV_DTYPE_BF16;
-  const int mx = max_persistent_seqs(d, format);
+  if (format == kPoolInt4) return launch_int4(args, d, append, stream, pdl);
   if (f8) {
-    using PS = pkv::PersistentShape<128, true>;
-    constexpr auto smem = pkv::persistent_smem_bytes<128, true>;
-    return bf16 ? launch_persistent<__nv_bfloat16, 128, pkv::decode_persistent_kernel<__nv_bfloat16, 128, true>>(
-                      PS::kWarps, smem, args, d, mx, stream, pdl, mk, mv, args)
-                : launch_persistent<__half, 128, pkv::decode_persistent_kernel<__half, 128, true>>(
-                      PS::kWarps, smem, args, d, mx, stream, pdl, mk, mv, args);
-  }
-  if (format == kPoolInt4) {
-    int rc4 = PKV_OK;
-    with_type_and_dim(d, [&](auto t, auto dim) {
-      using U = decltype(t);
-      constexpr int D = decltype(dim)::value;
-      constexpr int warps = pkv::Int4Shape<D>::kWarps;
-      rc4 = append ? launch_persistent<U, D, pkv::decode_int4_kernel<U, D, true>, true>(
-                         warps, pkv::int4_smem_bytes<D>, args, d, mx, stream, pdl, args)
-                   : launch_persistent<U, D, pkv::decode_int4_kernel<U, D, false>, true>(
-                         warps, pkv::int4_smem_bytes<D>, args, d, mx, stream, pdl, args);
-    });
-    return rc4;
+    const int mx = max_persistent_seqs(d, format);
+    return bf16 ? launch_persistent<__nv_bfloat16, 128, true>(mk, mv, args, d, mx, stream, pdl)
+                : launch_persistent<__half, 128, true>(mk, mv, args, d, mx, stream, pdl);
   }
   if (d->head_dim == 128)
     return bf16 ? launch_decode<__nv_bfloat16, 128>(mk, mv, args, plan, d, stream, pdl)
@@ -1238,13 +1253,13 @@ int paged_kv_selftest_stale_prologue_int4(const void* q, const void* k_new, cons
                                           void* v_cache, const int32_t* block_tables, const int32_t* context_lens,
                                           const int32_t* stale_block_tables, const int32_t* stale_context_lens,
                                           float scale, void* out, void* workspace, size_t workspace_bytes,
-                                          int32_t publish, const pkv_dims* dims, void* stream) {
+                                          const pkv_dims* dims, void* stream) {
   if (!stale_block_tables || !stale_context_lens || !aligned(stale_block_tables, 4) ||
       !aligned(stale_context_lens, 4))
     return pkv_fail(PKV_ERR_INVALID_ARG, "selftest_stale_prologue_int4: stale inputs missing or misaligned");
   return decode_impl(q, k_new, v_new, k_cache, v_cache, block_tables, context_lens, scale, out, 0, workspace,
                      workspace_bytes, dims, static_cast<cudaStream_t>(stream), kPoolInt4, nullptr, nullptr, true,
-                     stale_context_lens, stale_block_tables, true, publish != 0);
+                     stale_context_lens, stale_block_tables, true);
 }
 
 int paged_kv_append_fp8(const void* k_new, const void* v_new, const int32_t* slot_mapping, int32_t num_tokens,

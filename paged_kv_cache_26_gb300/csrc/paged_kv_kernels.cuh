@@ -590,7 +590,6 @@ struct DecodeArgs {
   int32_t group;              // Hq / Hkv, 1..8
   int32_t max_blocks;
   int32_t num_blocks;
-  int32_t share_unit;         // persistent: blocks that the partition's thresholds count as one
   int32_t num_splits;         // split path only
   int32_t split_blocks;       // split path only
 };
@@ -696,11 +695,10 @@ constexpr int persistent_max_seqs() {
 // boundary inside a unit leaves a piece for the merge, and fewer, larger
 // chunks keep those few where a share is short.  Shares under
 // kMinDynamicShare blocks are all head, with nothing to claim (the chunks
-// would be too small to pay for their hand-over).  The thresholds are in units
-// of `share_unit` blocks: a block of a pool with fewer bits is less work.
-// Chunk k of share w is segment nwarps + k * nwarps + w.  Every segment is a contiguous block
+// would be too small to pay for their hand-over).  Chunk k of share w is
+// segment nwarps + k * nwarps + w.  Every segment is a contiguous block
 // range; the decode and merge kernels derive all boundaries from
-// (total, nwarps, share_unit) alone.
+// (total, nwarps) alone.
 struct Partition {
   static constexpr int kMaxTailChunks = 4;
   static constexpr int kMinDynamicShare = 48;
@@ -708,26 +706,9 @@ struct Partition {
   static constexpr int kFourChunkShare = 200;
   int total, nwarps, R, nchunks;
 
-  __device__ __forceinline__ Partition(int total_, int nwarps_, int share_unit, int units)
-      : total(total_), nwarps(nwarps_), R(share(total_, nwarps_, share_unit, units)),
-        nchunks(R < kMinDynamicShare * share_unit   ? 0
-                : R < kThreeChunkShare * share_unit ? 2
-                : R < kFourChunkShare * share_unit  ? 3
-                                                    : 4) {}
-  // Blocks per share.  With share_unit > 1 a few blocks are a short step of work,
-  // and the pieces to merge cost more than the warps they keep busy: a share is
-  // then at least a 32nd of the average unit, up to two such units, and whole
-  // units up to there.  (4-bit pools, us before and after: 1 x 2048 tokens 10.7
-  // and 9.3, 1 x 8192 20.7 and 14.8, 8 x 2048 13.6 and 12.6.)
-  __device__ __forceinline__ static int share(int total, int nwarps, int share_unit, int units) {
-    if (total <= 0) return 1;
-    int r = (total + nwarps - 1) / nwarps;
-    if (share_unit > 1) {
-      r = max(r, min(2 * share_unit, total / units / 32));
-      if (r > share_unit && r < 2 * share_unit) r = 2 * share_unit;
-    }
-    return r;
-  }
+  __device__ __forceinline__ Partition(int total_, int nwarps_)
+      : total(total_), nwarps(nwarps_), R(total_ > 0 ? (total_ + nwarps_ - 1) / nwarps_ : 1),
+        nchunks(R < kMinDynamicShare ? 0 : R < kThreeChunkShare ? 2 : R < kFourChunkShare ? 3 : 4) {}
   // Cumulative tenths of the tail before chunk k.
   __device__ __forceinline__ int cum(int k) const {
     if (nchunks == 2) return k == 0 ? 0 : k == 1 ? 8 : 10;
@@ -864,7 +845,7 @@ __global__ void __maxnreg__(F8 ? 168 : 192)
   context_prefix(a, a.pre_context_lens ? a.pre_context_lens : a.context_lens, s_P, s_ctx, s_warp_sum, NW * 32,
                  !a.recheck && blockIdx.x == 0);
 
-  Partition part(Hkv * s_P[B], gridDim.x * NW, a.share_unit, B * Hkv);
+  Partition part(Hkv * s_P[B], gridDim.x * NW);
   const int gw = blockIdx.x * NW + warp;
 
   // Sequence b, KV head kvh and block j of flattened block f: units are
@@ -1092,7 +1073,7 @@ __global__ void __maxnreg__(F8 ? 168 : 192)
         // rebuild from changing s_ctx while another warp still compares.
         __syncthreads();
         context_prefix_again(a, s_P, s_ctx, s_warp_sum, NW * 32);
-        part = Partition(Hkv * s_P[B], gridDim.x * NW, a.share_unit, B * Hkv);
+        part = Partition(Hkv * s_P[B], gridDim.x * NW);
       }
       start_head();
     } else if (in_window) {
@@ -1385,7 +1366,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32, COOP ? 6 : WIDE ? 4 : 8)
   RowPlan r{};
   unsigned valid0 = 0;
   auto plan_first = [&]() {
-    const Partition part(Hkv * s_P[a.num_seqs], nwarps, a.share_unit, a.num_seqs * Hkv);
+    const Partition part(Hkv * s_P[a.num_seqs], nwarps);
     r = plan_row(part, first_base + warp / wpr);
     valid0 = r.work && sub < r.ncand ? gather(part, r, 0) : 0u;
   };
@@ -1401,7 +1382,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32, COOP ? 6 : WIDE ? 4 : 8)
   for (int base_row = first_base; base_row < rows; base_row += gridDim.x * rows_per_cta) {
     const int row = base_row + warp / wpr;
     const bool first = base_row == first_base;
-    const Partition part(Hkv * s_P[a.num_seqs], nwarps, a.share_unit, a.num_seqs * Hkv);
+    const Partition part(Hkv * s_P[a.num_seqs], nwarps);
     if (!first) r = plan_row(part, row);
     const bool work = r.work, zero_row = r.zero_row;
     T* dst = static_cast<T*>(a.out) + static_cast<int64_t>(row) * D + lane * kPer;

@@ -361,10 +361,9 @@ def test_inputs_written_on_the_stream_right_before_the_step():
     assert np.array_equal(kp.cpu().numpy(), rk) and np.array_equal(vp.cpu().numpy(), rv)
 
 
-@pytest.mark.parametrize("publish", [True, False])
 @pytest.mark.parametrize("batch", [6, 40, 200])
 @pytest.mark.parametrize("kind", ["lengths", "tables", "garbage", "zeros"])
-def test_stale_inputs_before_the_grid_wait_are_rebuilt(kind, batch, publish):
+def test_stale_inputs_before_the_grid_wait_are_rebuilt(kind, batch):
     """The prologue is handed other lengths and tables than the real ones: outputs and pools are the normal step's."""
     spec = wl.LLAMA3_8B.replace(name="stale", batch=batch, lengths=("uniform", 1, 900), num_q_heads=8, num_kv_heads=2)
     w = wl.generate(spec, seed=batch)
@@ -393,7 +392,7 @@ def test_stale_inputs_before_the_grid_wait_are_rebuilt(kind, batch, publish):
         else:
             want = pkv.paged_decode_attention_int4(q, kc, vc, bt, cl, w.scale)
         got = pkv.paged_kv_selftest_stale_prologue_int4(q, kn if append else None, vn if append else None, k2, v2, bt,
-                                                        cl, st, sl, w.scale, publish=publish)
+                                                        cl, st, sl, w.scale)
         pkv.paged_kv_check_status()
         assert torch.equal(got.view(torch.int16), want.view(torch.int16))
         assert torch.equal(kc, k2) and torch.equal(vc, v2)

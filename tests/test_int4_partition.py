@@ -1,6 +1,6 @@
-"""CPU model of the 4-bit decode kernel's index arithmetic: the partition with
-its share rule, the cutting of windows into stages, and the merges' search for
-the pieces the decode kernel leaves (constants read from the kernel sources)."""
+"""CPU model of the 4-bit decode kernel's index arithmetic: the shares, the
+cutting of windows into stages, and where the merge finds the pieces that the
+decode kernel leaves (constants read from the kernel source)."""
 import os
 import re
 
@@ -8,7 +8,6 @@ import numpy as np
 import pytest
 
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "paged_kv_cache_26_gb300", "csrc")
-KERNELS = open(os.path.join(CSRC, "paged_kv_kernels.cuh")).read()
 INT4 = open(os.path.join(CSRC, "decode_int4.cuh")).read()
 
 
@@ -16,47 +15,19 @@ def const(text, name):
     return int(re.search(rf"constexpr int {name} = (\d+);", text).group(1))
 
 
-UNIT, NB, WARPS = const(INT4, "kInt4ShareUnit"), const(INT4, "kBlocksPerStage"), const(INT4, "kWarps")
-MIN2, MIN3, MIN4 = (const(KERNELS, n) for n in ("kMinDynamicShare", "kThreeChunkShare", "kFourChunkShare"))
+FEW, NB, WARPS = const(INT4, "kFew"), const(INT4, "kBlocksPerStage"), const(INT4, "kWarps")
 
 
-class Partition:
-    def __init__(self, total, nwarps, units, unit=UNIT):
-        self.total, self.nwarps = total, nwarps
-        r = -(-total // nwarps) if total > 0 else 1
-        if total > 0 and unit > 1:
-            r = max(r, min(2 * unit, total // units // 32))
-            if unit < r < 2 * unit:
-                r = 2 * unit
-        self.R = r
-        self.n = 0 if r < MIN2 * unit else 2 if r < MIN3 * unit else 3 if r < MIN4 * unit else 4
-        self.cum = {0: [0], 2: [0, 8, 10], 3: [0, 7, 9, 10], 4: [0, 4, 7, 9, 10]}[self.n]
+class Shares:
+    def __init__(self, total, nwarps, units):
+        self.total, self.R = total, 1
+        if total > 0:
+            self.R = max(-(-total // nwarps), min(FEW, total // units // 32))
+            if FEW // 2 < self.R < FEW:
+                self.R = FEW
 
-    def head(self, w):
-        s = min(self.total, w * self.R)
-        n = min(self.total, (w + 1) * self.R) - s
-        return s, s + (n if self.n == 0 else n * 17 // 20 if self.n == 2 else n * 4 // 5)
-
-    def chunk(self, k, w):
-        he = self.head(w)[1]
-        tail = min(self.total, (w + 1) * self.R) - he
-        return he + tail * self.cum[k] // 10, he + tail * self.cum[k + 1] // 10
-
-    def segments(self):
-        out = [(w, *self.head(w)) for w in range(self.nwarps)]
-        return out + [(self.nwarps + k * self.nwarps + w, *self.chunk(k, w)) for k in range(self.n)
-                      for w in range(self.nwarps)]
-
-    def segment_of(self, p):
-        w = p // self.R
-        s, e = self.head(w)
-        if p < e:
-            return s, e
-        for k in range(self.n):
-            s, e = self.chunk(k, w)
-            if p < e:
-                return s, e
-        raise AssertionError
+    def start(self, w):
+        return min(self.total, w * self.R)
 
 
 def batches():
@@ -69,7 +40,7 @@ def batches():
     yield list(rng.integers(32, 257, 64)), 8, 152
     yield [5000, 1, 0, 3, 700], 3, 152
     yield list(rng.integers(0, 40, 300)), 5, 152
-    yield list(rng.integers(500, 2500, 12)), 8, 20          # shares with dynamic tails
+    yield list(rng.integers(500, 2500, 12)), 8, 20
     yield list(rng.integers(500, 2500, 40)), 8, 12
     yield list(rng.integers(2000, 9000, 40)), 8, 30
 
@@ -77,17 +48,18 @@ def batches():
 @pytest.mark.parametrize("case", range(11))
 def test_every_block_once_and_every_piece_found(case):
     nbs, hkv, sms = list(batches())[case]
-    B = len(nbs)
+    B, nwarps = len(nbs), sms * WARPS
     P = np.concatenate([[0], np.cumsum(nbs)]).astype(int)
-    part = Partition(hkv * int(P[-1]), sms * WARPS, B * hkv)
+    part = Shares(hkv * int(P[-1]), nwarps, B * hkv)
     seen = np.zeros(part.total, int)
     units = [(hkv * int(P[b]) + k * nbs[b], nbs[b]) for b in range(B) for k in range(hkv)]
     starts = np.array([u for u, _ in units])
     wrote, direct = {}, set()
-    for sid, s, e in part.segments():
+    for w in range(nwarps):
+        s, e = part.start(w), part.start(w + 1)
         seen[s:e] += 1
         p, first = s, True
-        while p < e:                                        # the units of this segment, in order
+        while p < e:                                        # the units of this share, in order
             i = int(np.searchsorted(starts, p, side="right")) - 1
             while units[i][1] == 0:
                 i -= 1
@@ -96,28 +68,15 @@ def test_every_block_once_and_every_piece_found(case):
             if p == U and q == U + nb:
                 direct.add(i)
             else:
-                wrote.setdefault(i, set()).add(sid * 2 + (0 if first else 1))
+                wrote.setdefault(i, []).append(w * 2 + (0 if first else 1))
             p, first = q, False
     assert (seen == 1).all()
-    per = 1 + part.n
-    for i, (U, nb) in enumerate(units):                     # merge_units_kernel's plan and gather
-        if nb == 0:
-            continue
-        w0, w1 = U // part.R, (U + nb - 1) // part.R
-        if part.n == 0:
-            ncand = w1 - w0 + 1 if w1 > w0 else 0
-        else:
-            ncand = (w1 - w0 + 1) * per if part.segment_of(U)[1] < U + nb else 0
-        found = set()
-        for c in range(ncand):
-            w, k = (w0 + c, 0) if part.n == 0 else (w0 + c // per, c % per)
-            s, e = part.head(w) if k == 0 else part.chunk(k - 1, w)
-            sid = w if k == 0 else part.nwarps + (k - 1) * part.nwarps + w
-            if e <= s or e <= U or s >= U + nb:
-                continue
-            found.add(sid * 2 + (1 if U > s else 0))
-        assert found == wrote.get(i, set()), (i, U, nb)
-        assert (ncand == 0) == (i in direct)
+    for i, (U, nb) in enumerate(units):                     # UnitPieces and merge_int4_kernel's row()
+        w = U // part.R
+        n = (U + nb - 1) // part.R - w + 1 if nb > 0 else 1
+        first, count = 2 * w + (U > w * part.R), n if n > 1 else 0
+        assert [first if p == 0 else first // 2 * 2 + 2 * p for p in range(count)] == wrote.get(i, [])
+        assert (count == 0) == (nb == 0 or i in direct)
 
 
 @pytest.mark.parametrize("append", [False, True])
