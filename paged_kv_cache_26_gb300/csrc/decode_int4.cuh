@@ -444,7 +444,8 @@ struct Int4Shares {
   int total, R;
   __device__ __forceinline__ Int4Shares(int total_, int nwarps, int units) : total(total_), R(1) {
     if (total <= 0) return;
-    R = max((total + nwarps - 1) / nwarps, min(kFew, total / units / 32));
+    const int average = total / units;
+    R = max(max((total + nwarps - 1) / nwarps, min(kFew, average / 32)), average / 256);
     if (R > kFew / 2 && R < kFew) R = kFew;
   }
   __device__ __forceinline__ int start(int w) const { return min(total, w * R); }

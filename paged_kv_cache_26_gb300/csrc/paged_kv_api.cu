@@ -726,7 +726,7 @@ int verify_draft_impl(const pkv::VerifyArgs& a, int32_t num_seqs, int32_t dtype,
     return pkv_fail(PKV_ERR_INVALID_ARG, "verify_draft: misaligned pointer");
   // As many CTAs per row as have a step of 128 entries for each of their warps,
   // and as fit the GPU at once with the other rows' (four CTAs per SM; 64 rows of
-  // 131072 entries: 19.6 us, and 27.0 with 16 warps a CTA and as many CTAs).
+  // 131072 entries: 16.9 us, and 42.4 with 16 warps a CTA and as many CTAs).
   unsigned cluster = 1;
   while (cluster < pkv::kMaxVerifyCluster && a.vocab > static_cast<int>(cluster) * pkv::kVerifyWarps * 128 &&
          2 * cluster * static_cast<int64_t>(num_seqs) <= 4 * static_cast<int64_t>(device_sms()))

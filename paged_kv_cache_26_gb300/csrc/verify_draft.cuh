@@ -107,7 +107,18 @@ __global__ void __launch_bounds__(kVerifyWarps * 32) verify_draft_kernel(const V
   const T* target = static_cast<const T*>(a.target) + b * a.target_seq;
   const T* draft = a.draft ? static_cast<const T*>(a.draft) + b * a.draft_seq : nullptr;
 
+  // All that needs no other load first is asked for at once.
   const int ctx = a.context_lens ? a.context_lens[b] : 1;
+  const float uf = a.sample_u[b];
+  int n = K, x = -1;
+  float accept = 0.f;
+  if (warp == 0) {
+    if (a.draft_lens) n = a.draft_lens[b];
+    if (lane < K) {
+      x = a.tokens[static_cast<int64_t>(b) * K + lane];
+      accept = a.accept_u[static_cast<int64_t>(b) * K + lane];
+    }
+  }
   if (ctx <= 0) {  // an empty batch slot: nothing to verify (the same in every CTA of the cluster)
     if (rank == 0) {
       if (tid <= K) a.out_tokens[static_cast<int64_t>(b) * (K + 1) + tid] = -1;
@@ -121,18 +132,16 @@ __global__ void __launch_bounds__(kVerifyWarps * 32) verify_draft_kernel(const V
 
   // ---- acceptance: lane i judges draft i
   if (warp == 0) {
-    int n = a.draft_lens ? a.draft_lens[b] : K;
     bool bad = n < 0 || n > K;
     n = min(max(n, 0), K);
     bool ok = false;
     if (lane < n) {
-      const int x = a.tokens[static_cast<int64_t>(b) * K + lane];
       if (x < 0 || x >= V) {
         bad = true;  // no such token: rejected
       } else {
         const double p = prob_value(target[lane * a.target_row + x]);
         const double q = draft ? prob_value(draft[lane * a.draft_row + x]) : 1.f;
-        ok = static_cast<double>(a.accept_u[static_cast<int64_t>(b) * K + lane]) * q < p;
+        ok = static_cast<double>(accept) * q < p;
       }
     }
     const unsigned accepted = __ballot_sync(0xffffffffu, ok);
@@ -164,6 +173,8 @@ __global__ void __launch_bounds__(kVerifyWarps * 32) verify_draft_kernel(const V
       load4<T>(prow, i, V, wide, p);
       if (qrow) load4<T>(qrow, i, V, wide, m);
     }
+  };
+  auto limit = [&](int i, float (&p)[4], float (&m)[4]) {  // (apart, so that loads can stay under way)
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       p[k] = __saturatef(p[k]);
@@ -171,27 +182,42 @@ __global__ void __launch_bounds__(kVerifyWarps * 32) verify_draft_kernel(const V
     }
   };
   long long sum_p = 0, sum_m = 0;
-  constexpr int kUnroll = 4;  // 16 entries a lane: the low parts' sum stays below 2^26
-  for (int s0 = 0; s0 < steps; s0 += kUnroll) {
-    float p[kUnroll][4], m[kUnroll][4];
+  // 8 entries a lane, and the next 8 on their way: within 64 registers, so that
+  // four CTAs fit an SM (64 rows of 131072 entries 16.9 us; 16 entries without
+  // the next on their way 19.6, with them, in 80 registers, 23.3).
+  constexpr int kUnroll = 2;
+  auto sum_up = [&](const float (&v)[kUnroll][4], long long& sum) {
+    uint32_t high = 0, low = 0;  // the low parts' sum stays below 2^25
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) load(s0 + u < steps ? first + (s0 + u) * 128 + lane * 4 : V, p[u], m[u]);
-    auto add = [&](const float (&v)[kUnroll][4], long long& sum) {
-      uint32_t high = 0, low = 0;
+    for (int u = 0; u < kUnroll; ++u)
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u)
+      for (int k = 0; k < 4; ++k) {
+        uint32_t h, l;
+        weight_parts(v[u][k], h, l);
+        high += h;
+        low += l;
+      }
+    constexpr uint32_t n = 4 * kUnroll;
+    sum += (static_cast<long long>(high - n * kHighBias) << 23) + static_cast<int32_t>(low - n * kLowBias);
+  };
+  auto at = [&](int s0, int u) { return s0 + u < steps ? first + (s0 + u) * 128 + lane * 4 : V; };
+  auto fetch = [&](int s0, float (&p)[kUnroll][4], float (&m)[kUnroll][4]) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uint32_t h, l;
-          weight_parts(v[u][k], h, l);
-          high += h;
-          low += l;
-        }
-      constexpr uint32_t n = 4 * kUnroll;
-      sum += (static_cast<long long>(high - n * kHighBias) << 23) + static_cast<int32_t>(low - n * kLowBias);
-    };
-    add(p, sum_p);
-    if (residual) add(m, sum_m);
+    for (int u = 0; u < kUnroll; ++u) load(at(s0, u), p[u], m[u]);
+  };
+  auto add = [&](int s0, float (&p)[kUnroll][4], float (&m)[kUnroll][4]) {
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) limit(at(s0, u), p[u], m[u]);
+    sum_up(p, sum_p);
+    if (residual) sum_up(m, sum_m);
+  };
+  float pa[kUnroll][4], ma[kUnroll][4], pb[kUnroll][4], mb[kUnroll][4];
+  fetch(0, pa, ma);
+  for (int s0 = 0; s0 < steps; s0 += 2 * kUnroll) {
+    fetch(s0 + kUnroll, pb, mb);
+    add(s0, pa, ma);
+    fetch(s0 + 2 * kUnroll, pa, ma);
+    add(s0 + kUnroll, pb, mb);
   }
   unsigned long long sum = sum_p - sum_m;
   sum = warp_sum(sum);
@@ -217,7 +243,6 @@ __global__ void __launch_bounds__(kVerifyWarps * 32) verify_draft_kernel(const V
     total[k] = warp_sum(part[k]);
   }
   const int which = total[0] > 0 ? 0 : 1;  // nothing left of p - q (p <= q everywhere): from p itself
-  const float uf = a.sample_u[b];
   const unsigned long long u = min(static_cast<unsigned long long>(uf > 0.f ? fminf(uf, 1.f) * 1073741824.f : 0.f),
                                    (1ull << kDrawBits) - 1);
   // floor(total u / 2^30): 62 + 30 bits
@@ -229,12 +254,13 @@ __global__ void __launch_bounds__(kVerifyWarps * 32) verify_draft_kernel(const V
     unsigned long long left = goal - before;
     for (; left >= s_warp[which][piece]; ++piece) left -= s_warp[which][piece];
     const int begin = (rank * kVerifyWarps + piece) * steps * 128;
+    auto entry = [&](int i0) { return i0 + tid * 4 < steps * 128 ? begin + i0 + tid * 4 : V; };
     for (int i0 = 0; i0 < steps * 128; i0 += kVerifyWarps * 128) {
-      const bool here = i0 + tid * 4 < steps * 128;
-      const int i = begin + i0 + tid * 4;
+      const int i = entry(i0);
       float p[4], m[4];
       unsigned long long w[4];
-      load(here ? i : V, p, m);
+      load(i, p, m);
+      limit(i, p, m);
 #pragma unroll
       for (int k = 0; k < 4; ++k) w[k] = prob_weight(p[k]) - (residual && !which ? prob_weight(m[k]) : 0ull);
       const unsigned long long own = (w[0] + w[1]) + (w[2] + w[3]);
@@ -265,7 +291,7 @@ __global__ void __launch_bounds__(kVerifyWarps * 32) verify_draft_kernel(const V
     if (tid <= K) {
       int32_t* out = a.out_tokens + static_cast<int64_t>(b) * (K + 1) + tid;
       if (tid < acc)
-        *out = a.tokens[static_cast<int64_t>(b) * K + tid];
+        *out = x;
       else if (tid > acc || all == 0)
         *out = -1;
     }

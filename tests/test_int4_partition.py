@@ -22,7 +22,7 @@ class Shares:
     def __init__(self, total, nwarps, units):
         self.total, self.R = total, 1
         if total > 0:
-            self.R = max(-(-total // nwarps), min(FEW, total // units // 32))
+            self.R = max(-(-total // nwarps), min(FEW, total // units // 32), total // units // 256)
             if FEW // 2 < self.R < FEW:
                 self.R = FEW
 
@@ -36,6 +36,7 @@ def batches():
     yield [1], 1, 152
     yield [128] * 8, 8, 152
     yield [512], 8, 152
+    yield [8192], 1, 152
     yield [2048] * 8, 8, 152
     yield list(rng.integers(32, 257, 64)), 8, 152
     yield [5000, 1, 0, 3, 700], 3, 152
@@ -45,7 +46,7 @@ def batches():
     yield list(rng.integers(2000, 9000, 40)), 8, 30
 
 
-@pytest.mark.parametrize("case", range(11))
+@pytest.mark.parametrize("case", range(12))
 def test_every_block_once_and_every_piece_found(case):
     nbs, hkv, sms = list(batches())[case]
     B, nwarps = len(nbs), sms * WARPS
