@@ -338,7 +338,8 @@ int paged_decode_step_fp8(const void* q, const void* k_new, const void* v_new, v
  *   paged_kv_check_status).  A scale in the pool must be finite; slots past a
  *   sequence's length may hold anything.  A block id outside the pool reads as
  *   zeros and is flagged.
- * Limits: head_dim 64 or 128; at most 2048 sequences per call; only the
+ * Limits: head_dim 64 or 128; at most 2048 sequences per call, and
+ *   num_seqs * num_kv_heads * max_blocks_per_seq below 2^31 - 65536; only the
  *   automatic persistent path (workspace: paged_decode_workspace_bytes(dims, 0)
  *   bytes, zero-filled once, as above).  Bad shapes and pointers return
  *   PKV_ERR_INVALID_ARG / PKV_ERR_UNSUPPORTED.

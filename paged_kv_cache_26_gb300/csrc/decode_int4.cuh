@@ -333,7 +333,7 @@ struct WarpAttnInt4 {
   }
 
   // n (1..NB) consecutive blocks of a stage: whole stages as one step, a unit's
-  // or segment's last blocks one by one (masking a whole step instead, for the
+  // or share's last blocks one by one (masking a whole step instead, for the
   // sake of fewer steps, was no faster: 64 sequences 42.8 us against 41.8).
   template <int NB>
   __device__ __forceinline__ void blocks(const uint8_t* stage, int n, int valid, float scale_log2, int lane) {
@@ -398,8 +398,8 @@ struct StageInfo {
   static constexpr int kValidBits = 127;      // tokens of the context in it, 1..64
   static constexpr int kUnitStart = 1 << 7;   // its first block is the unit's first
   static constexpr int kUnitEnd = 1 << 8;     // its last block is the unit's last
-  static constexpr int kSegStart = 1 << 9;    // the same for the segment
-  static constexpr int kSegEnd = 1 << 10;
+  static constexpr int kShareStart = 1 << 9;  // the same for the share
+  static constexpr int kShareEnd = 1 << 10;
   static constexpr int kCountShift = 11;      // blocks
 };
 
@@ -408,8 +408,8 @@ struct StageInfo {
 // `rows`, quantised.  D / 4 lanes take a row, four entries each (D = 64: both
 // rows at once).
 template <typename T, int D>
-__device__ __forceinline__ void append_patch(uint8_t* tile, const uint8_t* rows, int r, uint8_t* k_pool, uint8_t* v_pool,
-                                          int64_t off) {
+__device__ __forceinline__ void append_patch(uint8_t* tile, const uint8_t* rows, int r, uint8_t* k_pool,
+                                             uint8_t* v_pool, int64_t off) {
   constexpr int W = D / 4;
   const int lane = threadIdx.x & 31, l = lane % W;
 #pragma unroll
@@ -432,13 +432,15 @@ struct UnitPieces {
 };
 
 // The shares: share w is blocks [w R, (w + 1) R) of the flattened space (cut off
-// at `total`).  All of them are static.  (Handing out a share's tail dynamically
-// costs pieces, and a merge that runs after the grid: 64 x 16384 tokens 192.5 us
-// with dynamic tails and 184.7 without, 256 x 4096 205.8 and 200.4, 512 x 4096
-// 380.7 and 383.1.)  A few blocks are a short step of work and pieces cost
-// more than the warps they keep busy: a share is at least a 32nd of the average
-// unit, up to kFew blocks, and never between half of kFew and kFew.  (1 x 2048
-// tokens 10.7 us without this rule and 9.3 with it, 1 x 8192 20.7 and 14.8.)
+// at `total`).  All of them are static: handing out their tails dynamically
+// costs pieces to merge.  (64 x 16384 tokens 192.5 us with dynamic tails and
+// 184.7 without, 256 x 4096 205.8 and 200.4; only from 2 GB a call on they are
+// level, 512 x 4096 380.6 and 384.0, or better, 256 x 8192 370.7 and 383.)  A few
+// blocks are a short step of work and pieces cost more than the warps they keep
+// busy: a share is at least a 32nd of the average unit, up to kFew blocks, and
+// never between half of kFew and kFew (1 x 8192 tokens 13.1 us, 14.5 with kFew 4
+// and 15.7 with 16; 64 x 256 11.7, 13.4 and 13.4); and a unit has 256 pieces or
+// so at most (one head of 131072 tokens 35.8 us, 55.3 without).
 struct Int4Shares {
   static constexpr int kFew = 8;
   int total, R;
@@ -509,19 +511,19 @@ __global__ void __maxnreg__(168) decode_int4_kernel(const DecodeArgs a) {
   const int32_t* tables = a.pre_block_tables ? a.pre_block_tables : a.block_tables;
   bool after_wait = !a.recheck;  // block ids are flagged only from values known to be final
 
-  // ---- issue side: the share [seg_s, seg_e) and a 32-block window of it,
+  // ---- issue side: the share [share_s, share_e) and a 32-block window of it,
   // lane i describing block win_s + i.  The window is cut into stages at the
   // unit borders and every NB blocks (and before a unit's last block where the
   // appended rows would find no room): lane i's block belongs to stage
   // wstage, and the first lane of a stage holds its description.
-  int seg_s, seg_e;
+  int share_s, share_e;
   int win_s, win_e;                  // window
   int stage_i = 0, stages = 0;       // next stage of the window to issue, and how many it has
   int wb = -1, wkvh = 0, wj = 0, wphys = -1, wrow = -kBlockSize, wstage = -1, wslot = 0, winfo = 0;
   bool bad_window = false;           // some block of the window is outside the pool
   auto fill_window = [&]() {
     win_s = win_e;
-    win_e = min(seg_e, win_s + 32);
+    win_e = min(share_e, win_s + 32);
     stage_i = 0;
     wb = -1; wkvh = 0; wj = 0; wphys = -1; wrow = -kBlockSize; wstage = -1; wslot = 0; winfo = 0;
     const int n = win_e - win_s;
@@ -549,17 +551,17 @@ __global__ void __maxnreg__(168) decode_int4_kernel(const DecodeArgs a) {
       const int count = (later ? __ffs(later) - 1 : n) - lane;  // blocks of the stage from this one on
       const int valid = min(count * kBlockSize, s_ctx[wb] - wj * kBlockSize);
       winfo = valid | (wj == 0 ? StageInfo::kUnitStart : 0) | (wj + count == nb ? StageInfo::kUnitEnd : 0) |
-              (win_s + lane == seg_s ? StageInfo::kSegStart : 0) |
-              (win_s + lane + count == seg_e ? StageInfo::kSegEnd : 0) | count << StageInfo::kCountShift;
+              (win_s + lane == share_s ? StageInfo::kShareStart : 0) |
+              (win_s + lane + count == share_e ? StageInfo::kShareEnd : 0) | count << StageInfo::kCountShift;
     }
     bad_window = __any_sync(0xffffffffu, in && wrow < 0);
   };
   auto start_share = [&]() {
-    seg_s = part.start(gw);
-    seg_e = part.start(gw + 1);
-    win_s = win_e = seg_s;
+    share_s = part.start(gw);
+    share_e = part.start(gw + 1);
+    win_s = win_e = share_s;
     stage_i = stages = 0;
-    if (win_e < seg_e) fill_window();
+    if (win_e < share_e) fill_window();
   };
 
   int issued = 0, consumed = 0;
@@ -569,7 +571,7 @@ __global__ void __maxnreg__(168) decode_int4_kernel(const DecodeArgs a) {
   auto issue_stages = [&](bool may_advance) {
     while (issued - consumed < SW) {
       if (stage_i == stages) {
-        if (!may_advance || win_e >= seg_e) break;
+        if (!may_advance || win_e >= share_e) break;
         fill_window();
       }
       const bool mine = wstage == stage_i;
@@ -623,7 +625,7 @@ __global__ void __maxnreg__(168) decode_int4_kernel(const DecodeArgs a) {
     }
   };
 
-  // The head's first window (inputs only), its first stages' tiles prefetched
+  // The share's first window (inputs only), its first stages' tiles prefetched
   // into L2, then the wait for the previous kernels in the stream.
   start_share();
   if (lane < SW * NB && win_s + lane < win_e && wrow >= 0) {
@@ -695,8 +697,8 @@ __global__ void __maxnreg__(168) decode_int4_kernel(const DecodeArgs a) {
 
   // ---- consume side
   Attn at;
-  bool from_start = false;       // the unit's blocks in this segment begin with its first
-  bool seg_first_flush = true;
+  bool from_start = false;   // the unit's blocks in this share begin with its first
+  bool first_flush = true;   // of this share
   while (ok) {
     issue_stages(true);
     if (consumed == issued) break;
@@ -704,9 +706,9 @@ __global__ void __maxnreg__(168) decode_int4_kernel(const DecodeArgs a) {
 
     const int4 dsc = s_desc[warp][st_c];
     const int b = dsc.x, kvh = dsc.y, info = dsc.z, share = dsc.w;
-    if (info & (StageInfo::kUnitStart | StageInfo::kSegStart)) {
+    if (info & (StageInfo::kUnitStart | StageInfo::kShareStart)) {
       // While the tiles are under way: the query rows (L2), and a fresh state.
-      if (info & StageInfo::kSegStart) seg_first_flush = true;
+      if (info & StageInfo::kShareStart) first_flush = true;
       from_start = info & StageInfo::kUnitStart;
       at.load_q(static_cast<const T*>(a.q) + (static_cast<int64_t>(b) * a.num_q_heads + kvh * g) * D, g, a.scale_log2,
                 lane);
@@ -729,12 +731,12 @@ __global__ void __maxnreg__(168) decode_int4_kernel(const DecodeArgs a) {
     at.template blocks<NB>(stage, n, valid, a.scale_log2, lane);
     next_oldest();
 
-    if (info & (StageInfo::kUnitEnd | StageInfo::kSegEnd)) {
+    if (info & (StageInfo::kUnitEnd | StageInfo::kShareEnd)) {
       // ---- the unit ends here or the share does: write it out, or leave a piece for the merge
       at.finish_sums();
       const int gid = lane >> 2, c = lane & 3;
       const bool complete = from_start && (info & StageInfo::kUnitEnd);
-      const int64_t pbase = (static_cast<int64_t>(share) * 2 + (seg_first_flush ? 0 : 1)) * kMaxGroup;
+      const int64_t pbase = (static_cast<int64_t>(share) * 2 + (first_flush ? 0 : 1)) * kMaxGroup;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int h = 2 * c + e;
@@ -761,7 +763,7 @@ __global__ void __maxnreg__(168) decode_int4_kernel(const DecodeArgs a) {
           if (gid == 0) a.part_lse[pbase + h] = (e ? at.m1 : at.m0) + log2f(l);
         }
       }
-      seg_first_flush = false;
+      first_flush = false;
     }
   }
   if (!ok && lane == 0) {

@@ -175,7 +175,8 @@ int max_persistent_seqs(const pkv_dims* d, int format) {
 
 bool persistent_eligible(const pkv_dims* d, int format = kPool16) {
   return d->num_seqs <= max_persistent_seqs(d, format) &&
-         static_cast<int64_t>(d->num_seqs) * d->num_kv_heads * d->max_blocks_per_seq < (int64_t(1) << 31);
+         static_cast<int64_t>(d->num_seqs) * d->num_kv_heads * d->max_blocks_per_seq <
+             (int64_t(1) << 31) - (format == kPoolInt4 ? 65536 : 0);  // (its shares' ends are 32-bit too)
 }
 
 int plan_splits(const pkv_dims* d, int32_t requested, SplitPlan* plan) {
@@ -198,8 +199,8 @@ int plan_splits(const pkv_dims* d, int32_t requested, SplitPlan* plan) {
 }
 
 // Workspace regions: [partial outputs][partial log-sum-exps][publication of
-// the decode grid's lengths to its merge][scheduler counters][4-bit pools: each unit's
-// pieces].
+// the decode grid's lengths to its merge][scheduler counters][4-bit pools: where
+// the merge finds each unit's pieces].
 struct WorkspaceLayout {
   size_t o_bytes = 0, lse_bytes = 0, sched_bytes = 0, pub_bytes = 0, unit_bytes = 0;
   size_t total() const { return o_bytes + lse_bytes + sched_bytes + pub_bytes + unit_bytes; }
@@ -349,12 +350,15 @@ int launch_int4(const pkv::DecodeArgs& args, const pkv_dims* d, bool append, cud
       launch(
           std::integral_constant<decltype(&pkv::decode_int4_kernel<T, D, false>), pkv::decode_int4_kernel<T, D, false>>{});
     if (e != cudaSuccess) return;
-    // Units of eight or more shares on average have many pieces: a CTA per head.
-    // Else a warp per head, or, with more heads than the GPU holds such warps at
-    // once, per four heads of a unit.
+    // Units of eight or more shares on average have many pieces: a CTA per head
+    // (us with the threshold at 4, 8 and 16: 16 x 2048 tokens, 9.5 shares, 15.8,
+    // 15.8 and 17.7; 32 x 2048, 4.8 shares, 21.9, 21.4 and 21.4).  Else a warp per
+    // head, or, when these are more than can run at once, per four heads of a
+    // unit (16 warps an SM: 128 x 2048 tokens 54.9, and 56.1 with 32; 256 x 256
+    // 23.6, and 25.2 with 64).
     const int64_t units = static_cast<int64_t>(d->num_seqs) * d->num_kv_heads, rows = units * args.group;
     const bool many = static_cast<int64_t>(cfg.gridDim.x) * pkv::Int4Shape<D>::kWarps >= 8 * units;
-    const bool fours = !many && rows > 32 * static_cast<int64_t>(device_sms());
+    const bool fours = !many && rows > 16 * static_cast<int64_t>(device_sms());
     const int64_t warps = fours ? units * ((args.group + 3) / 4) : rows;
     cfg.gridDim = dim3(static_cast<unsigned>(many ? rows : (warps + pkv::kMergeWarps - 1) / pkv::kMergeWarps));
     cfg.blockDim = dim3(pkv::kMergeWarps * 32);
@@ -413,7 +417,8 @@ int decode_impl(const void* q, const void* k_new, const void* v_new, void* k_cac
   if (rc != PKV_OK) return rc;
   if (format == kPoolInt4 && !persistent_eligible(d, format))
     return pkv_fail(PKV_ERR_UNSUPPORTED, "4-bit cache: at most " + std::to_string(max_persistent_seqs(d, format)) +
-                                             " sequences per call");
+                                             " sequences, and num_seqs * num_kv_heads * max_blocks_per_seq below 2^31 - "
+                                             "65536, per call");
   const bool f8 = format == kPoolE4M3;
   if (f8) {
     if (d->head_dim != 128) return pkv_fail(PKV_ERR_UNSUPPORTED, "fp8 cache: head_dim must be 128");

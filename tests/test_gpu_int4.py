@@ -550,3 +550,22 @@ def test_a_strided_workspace_is_refused():
     ws = torch.zeros(2 * pkv.make_workspace_int4(q, kc, bt).numel(), dtype=torch.uint8, device=DEV)
     with pytest.raises(ValueError):
         pkv.paged_decode_attention_int4(q, kc, vc, bt, cl, 0.1, workspace=ws[::2])
+
+
+@pytest.mark.parametrize("group", [3, 4, 5, 8])
+def test_many_units_merged_four_heads_at_a_time(group):
+    """More heads than warps run at once: groups that four does not divide, units cut once or not at all, and one
+    long sequence whose units have many pieces."""
+    lens = np.random.default_rng(group).integers(0, 330, 450)
+    lens[7], lens[100] = 5000, 0
+    spec = wl.LLAMA3_8B.replace(name="many", batch=450, lengths=("fixed", tuple(int(max(n, 1)) for n in lens)),
+                                num_q_heads=2 * group, num_kv_heads=2)
+    w = wl.generate(spec, seed=group)
+    check_step(w, wl.int4_caches(w, oracle_store))
+
+
+@pytest.mark.parametrize("group", [1, 3, 8])
+def test_one_head_in_many_pieces(group):
+    spec = wl.LLAMA3_8B.replace(name="one", batch=2, lengths=("fixed", (20011, 3)), num_q_heads=group, num_kv_heads=1)
+    w = wl.generate(spec, seed=group)
+    check_step(w, wl.int4_caches(w, oracle_store))
