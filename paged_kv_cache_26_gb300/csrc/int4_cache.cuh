@@ -210,6 +210,7 @@ __global__ void __launch_bounds__(kAppendThreads)
                        const int32_t* __restrict__ slots, int32_t num_tokens, int32_t num_kv_heads, int64_t num_slots,
                        uint8_t* __restrict__ k_cache, uint8_t* __restrict__ v_cache) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   constexpr int L = D / 16, kTokens = kAppendThreads / L;
   __shared__ int s_slot[kTokens + 1];
   __shared__ uint2 s_codes[kAppendThreads];
@@ -278,6 +279,7 @@ __global__ void __launch_bounds__(kReadThreads)
                      const uint8_t* __restrict__ k_cache, const uint8_t* __restrict__ v_cache,
                      uint4* __restrict__ k_out, uint4* __restrict__ v_out) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   constexpr int C = D / 16, kTokens = kReadThreads / C;
   const int c = threadIdx.x % C, head = blockIdx.y;
   const int64_t token = static_cast<int64_t>(blockIdx.x) * kTokens + threadIdx.x / C;

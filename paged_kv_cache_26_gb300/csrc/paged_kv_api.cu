@@ -595,6 +595,28 @@ int append_fp8_impl(const void* k_new, const void* v_new, const int32_t* slot_ma
   return PKV_OK;
 }
 
+// A launch of `grid` CTAs in clusters of `cluster`, as a programmatic dependent
+// launch: the kernel may start while the one before it in the stream finishes,
+// and waits for it first (griddepcontrol.wait), so that what overlaps is the start.
+template <typename... Params, typename... Args>
+cudaError_t launch_dependent(void (*kern)(Params...), dim3 grid, unsigned cluster, unsigned threads, size_t smem,
+                             cudaStream_t stream, Args... args) {
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 // Slot-mapped append into, and read-back from, a 4-bit pool.
 int check_int4_rows(const void* k, const void* v, const int32_t* slot_mapping, int32_t num_tokens, const void* k_cache,
                     const void* v_cache, const pkv_dims* d, const char* what) {
@@ -618,12 +640,13 @@ int append_int4_impl(const void* k_new, const void* v_new, const int32_t* slot_m
   const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(num_tokens) + tokens_per_cta - 1) / tokens_per_cta),
                   d->num_kv_heads);
   const int64_t slots = static_cast<int64_t>(d->num_blocks) * pkv::kBlockSize;
+  cudaError_t e = cudaSuccess;
   with_type_and_dim(d, [&](auto t, auto dim) {
-    pkv::append_int4_kernel<decltype(t), decltype(dim)::value><<<grid, pkv::kAppendThreads, 0, stream>>>(
-        static_cast<const uint4*>(k_new), static_cast<const uint4*>(v_new), slot_mapping, num_tokens, d->num_kv_heads,
-        slots, static_cast<uint8_t*>(k_cache), static_cast<uint8_t*>(v_cache));
+    e = launch_dependent(pkv::append_int4_kernel<decltype(t), decltype(dim)::value>, grid, 1, pkv::kAppendThreads, 0,
+                         stream, static_cast<const uint4*>(k_new), static_cast<const uint4*>(v_new), slot_mapping,
+                         num_tokens, d->num_kv_heads, slots, static_cast<uint8_t*>(k_cache),
+                         static_cast<uint8_t*>(v_cache));
   });
-  const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "append_int4_kernel launch");
   return PKV_OK;
 }
@@ -636,35 +659,17 @@ int read_int4_impl(const int32_t* slot_mapping, int32_t num_tokens, const void* 
   const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(num_tokens) + tokens_per_cta - 1) / tokens_per_cta),
                   d->num_kv_heads);
   const int64_t slots = static_cast<int64_t>(d->num_blocks) * pkv::kBlockSize;
+  cudaError_t e = cudaSuccess;
   with_type_and_dim(d, [&](auto t, auto dim) {
-    pkv::read_int4_kernel<decltype(t), decltype(dim)::value><<<grid, pkv::kReadThreads, 0, stream>>>(
-        slot_mapping, num_tokens, d->num_kv_heads, slots, static_cast<const uint8_t*>(k_cache),
-        static_cast<const uint8_t*>(v_cache), static_cast<uint4*>(k_out), static_cast<uint4*>(v_out));
+    e = launch_dependent(pkv::read_int4_kernel<decltype(t), decltype(dim)::value>, grid, 1, pkv::kReadThreads, 0, stream,
+                         slot_mapping, num_tokens, d->num_kv_heads, slots, static_cast<const uint8_t*>(k_cache),
+                         static_cast<const uint8_t*>(v_cache), static_cast<uint4*>(k_out), static_cast<uint4*>(v_out));
   });
-  const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "read_int4_kernel launch");
   return PKV_OK;
 }
 
 // ------------------------------------------------------------------ block tables from lengths
-
-// A launch of `grid` CTAs in clusters of `cluster`.
-template <typename... Params, typename... Args>
-cudaError_t launch_clusters(void (*kern)(Params...), unsigned grid, unsigned cluster, unsigned threads, size_t smem,
-                            cudaStream_t stream, Args... args) {
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = cluster;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, args...);
-}
 
 int resize_tables_impl(const pkv::ResizeArgs& a, int32_t block_size, cudaStream_t stream) {
   if (a.num_seqs < 0 || a.max_blocks < 0 || a.num_blocks <= 0 || a.num_slots < 0)
@@ -702,7 +707,7 @@ int resize_tables_impl(const pkv::ResizeArgs& a, int32_t block_size, cudaStream_
   const unsigned threads = a.num_seqs > 1024 || a.num_slots > 32768 ? pkv::kResizeThreads : 512;
   e = cudaFuncSetAttribute(pkv::resize_tables_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(resize_tables_kernel)");
-  e = launch_clusters(pkv::resize_tables_kernel, cluster, cluster, threads, smem, stream, a);
+  e = launch_dependent(pkv::resize_tables_kernel, dim3(cluster), cluster, threads, smem, stream, a);
   if (e != cudaSuccess) return cuda_fail(e, "resize_tables_kernel launch");
   return PKV_OK;
 }
@@ -737,8 +742,8 @@ int verify_draft_impl(const pkv::VerifyArgs& a, int32_t num_seqs, int32_t dtype,
          2 * cluster * static_cast<int64_t>(num_seqs) <= 4 * static_cast<int64_t>(device_sms()))
     cluster *= 2;
   auto launch = [&](auto kern) {
-    return launch_clusters(kern, static_cast<unsigned>(num_seqs) * cluster, cluster, pkv::kVerifyWarps * 32, 0, stream,
-                           a);
+    return launch_dependent(kern, dim3(static_cast<unsigned>(num_seqs) * cluster), cluster, pkv::kVerifyWarps * 32, 0,
+                            stream, a);
   };
   const cudaError_t e = dtype == PKV_DTYPE_FP32   ? launch(pkv::verify_draft_kernel<float>)
                         : dtype == PKV_DTYPE_BF16 ? launch(pkv::verify_draft_kernel<__nv_bfloat16>)

@@ -73,6 +73,7 @@ __device__ __forceinline__ uint32_t cluster_size() {
 
 __global__ void __launch_bounds__(kResizeThreads, 1) resize_tables_kernel(const ResizeArgs a) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   extern __shared__ int resize_smem[];
   __shared__ long long s_wtok[32];
   __shared__ int s_wtake[32], s_wgive[32];

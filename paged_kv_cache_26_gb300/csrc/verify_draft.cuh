@@ -97,6 +97,7 @@ __device__ __forceinline__ unsigned long long warp_sum(unsigned long long v) {
 template <typename T>
 __global__ void __launch_bounds__(kVerifyWarps * 32) verify_draft_kernel(const VerifyArgs a) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   __shared__ int s_accepted, s_drafts;
   __shared__ unsigned long long s_warp[2][kVerifyWarps];  // [residual, p] sums of each warp's piece
   __shared__ unsigned long long s_total[2];               // of this CTA's, read by the cluster
