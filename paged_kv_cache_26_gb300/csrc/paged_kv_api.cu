@@ -698,9 +698,9 @@ int resize_tables_impl(const pkv::ResizeArgs& a, int32_t block_size, cudaStream_
       static_cast<int>(pkv::resize_smem_bytes(pkv::kMaxResizeSeqs)));
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(resize_tables_kernel)");
   // A decode step's growth is one CTA's work (64 sequences by 5 tokens and back:
-  // 8.4 us for both calls with 512 threads, 12.3 with 1024).  Prompts are a
+  // 7.7 us for both calls with 512 threads, 11.1 with 1024).  Prompts are a
   // cluster's, and so may be what a call without slots gives back (256 prompts,
-  // 380,000 tokens, and back: 18.9 us with 16 CTAs, 25.8 with 8, 160 with one).
+  // 380,000 tokens, and back: 18.3 us with 16 CTAs, 24.9 with 8, 112 with one).
   const bool many = a.num_slots > 4096 ||
                     (a.num_slots == 0 && static_cast<int64_t>(a.num_seqs) * a.max_blocks > 4096);
   const unsigned cluster = many ? pkv::kResizeCluster : 1;
@@ -736,7 +736,7 @@ int verify_draft_impl(const pkv::VerifyArgs& a, int32_t num_seqs, int32_t dtype,
     return pkv_fail(PKV_ERR_INVALID_ARG, "verify_draft: misaligned pointer");
   // As many CTAs per row as have a step of 128 entries for each of their warps,
   // and as fit the GPU at once with the other rows' (four CTAs per SM; 64 rows of
-  // 131072 entries: 16.9 us, and 42.4 with 16 warps a CTA and as many CTAs).
+  // 131072 entries: 16.9 us, and 23.8 with 16 warps a CTA and as many CTAs).
   unsigned cluster = 1;
   while (cluster < pkv::kMaxVerifyCluster && a.vocab > static_cast<int>(cluster) * pkv::kVerifyWarps * 128 &&
          2 * cluster * static_cast<int64_t>(num_seqs) <= 4 * static_cast<int64_t>(device_sms()))

@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(kVerifyWarps * 32) verify_draft_kernel(const V
   long long sum_p = 0, sum_m = 0;
   // 8 entries a lane, and the next 8 on their way: within 64 registers, so that
   // four CTAs fit an SM (64 rows of 131072 entries 16.9 us; 16 entries without
-  // the next on their way 19.6, with them, in 80 registers, 23.3).
+  // the next on their way 19.6, with them, in 80 registers, 22.8).
   constexpr int kUnroll = 2;
   auto sum_up = [&](const float (&v)[kUnroll][4], long long& sum) {
     uint32_t high = 0, low = 0;  // the low parts' sum stays below 2^25
