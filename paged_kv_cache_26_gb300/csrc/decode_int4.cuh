@@ -62,12 +62,17 @@ __device__ __forceinline__ void mma_f16_first(float (&d)[4], uint32_t a0, uint32
 // over a long context would lose the output's low bits to it.
 //
 // The softmax reference M (p_t = 2^(x_t - M)) is not the maximum but what keeps
-// P within float16: with a cap C on the scales met, scores may exceed M by up to
-// `limit` = kTop - log2 C, so P stays below 2^kTop.  When a score or a scale goes
-// beyond, M is set so that the largest score lies kSlack below that limit (its P
-// then is about 2^(kTop - kSlack - kScaleSlack), far above float16's subnormals)
-// and C to 2^kScaleSlack times the largest scale.  Most steps then take one vote
-// and no shuffles or rescaling; float32 sums do not mind the common factor.
+// P within float16 and its largest value well inside: M moves so that the largest
+// product p_t s_t met, and not the largest p_t or s_t, lies at 2^kTarget when it
+// moves and below 2^kTop always.  A row's rounding error is then 2^-11 of its own
+// P, or 2^-25 where the largest is at least 1, whatever the scales of rows that
+// carry no weight.  (A scale of 0 counts as 2^-24, float16's smallest, so that p
+// stays below 2^38.  Scales count by their exponent, which makes the heaviest
+// row's p a power of two: a context of one token returns its row.)
+// Most steps need no look at the products: scores up to `limit` above M and
+// scales up to a cap C, limit = kTop - log2 C, cannot exceed 2^kTop; one vote, no
+// shuffles, no rescaling.  C is 2^kScaleSlack times the largest scale of the last
+// step that failed this; it decides only which steps are looked at.
 //
 // Lane (gid = lane/4, c = lane%4): scores of tokens gid, gid + 8 and heads 2c,
 // 2c + 1 as in WarpAttn; O^T entries of dims [G gid, G gid + G), G = D/8.
@@ -77,7 +82,7 @@ struct WarpAttnInt4 {
   static constexpr int kWords = D / 32;  // 32-bit words of codes per lane and row
   static constexpr int kFlushBlocks = 64;
   static constexpr float kTop = 14.f;    // log2; float16's largest is 65504
-  static constexpr float kSlack = 8.f;   // log2, for later scores
+  static constexpr float kTarget = 0.f;  // log2: room below kTop for later scores (8) and scales (6)
   static constexpr int kScaleSlack = 6;  // log2, for later scales
   static constexpr float kTiny = 5.9604644775390625e-8f;  // 2^-24
   uint32_t qf[4 * kWords];
@@ -86,7 +91,7 @@ struct WarpAttnInt4 {
   float m0, m1, l0, l1;  // softmax reference (log2 units) and sum of p
   float b0, b1;          // sum of p (m + 7.5 s)
   float qs0, qs1;        // scale_log2 * sum(q)
-  float cap, limit;      // C, and how far a score may exceed the reference; cap < 0 before the first step
+  float cap, limit;      // C, and how far a score may exceed the reference untested; cap < 0 before the first step
   int since_flush;       // blocks
 
   __device__ __forceinline__ void reset() {
@@ -220,10 +225,24 @@ struct WarpAttnInt4 {
     since_flush = 0;
   }
 
-  // Raise the cap to cover smax and the references to leave kSlack above d0, d1
-  // (this lane's largest scores less the reference); returns in d0, d1 how far
-  // the references went up.  What was summed so far is rescaled.
-  __device__ __forceinline__ void rescale(float& d0, float& d1, float smax) {
+  // The references for a step that failed the quick test (or the first): up, so
+  // that the largest product lies at 2^kTarget, where it lies above; x (scores
+  // less the reference) and what was summed so far follow.
+  template <int NB>
+  __device__ __forceinline__ void move_reference(float (&x)[NB][4], const float (&sv)[NB][2], float smax) {
+    float d0 = -INFINITY, d1 = -INFINITY;  // log2 of the largest products, less 1 at most
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      // log2 of the scales, rounded down: their exponents as the low bits of 2^23's.
+      float la = __uint_as_float(__funnelshift_r(__float_as_uint(fmaxf(fabsf(sv[i][0]), kTiny)), 0x4b000000u >> 9, 23));
+      float lb = __uint_as_float(__funnelshift_r(__float_as_uint(fmaxf(fabsf(sv[i][1]), kTiny)), 0x4b000000u >> 9, 23));
+      add2(la, lb, -(8388608.f + 127.f), -(8388608.f + 127.f));
+      float y0 = x[i][0], y1 = x[i][1], y2 = x[i][2], y3 = x[i][3];
+      add2(y0, y1, la, la);
+      add2(y2, y3, lb, lb);
+      d0 = max3(d0, y0, y2);
+      d1 = max3(d1, y1, y3);
+    }
 #pragma unroll
     for (int o = 4; o <= 16; o <<= 1) {
       d0 = fmaxf(d0, __shfl_xor_sync(0xffffffffu, d0, o));
@@ -232,15 +251,18 @@ struct WarpAttnInt4 {
     const bool first = cap < 0.f;  // nothing is summed yet: the references may also go down
     // The bits of floats >= 0 order as they do; the exponent is all that counts.
     const uint32_t e = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(smax, kTiny))) >> 23;
-    if (first || smax_exceeds(e)) {
-      cap = __uint_as_float((e + kScaleSlack) << 23);
-      limit = kTop - static_cast<float>(static_cast<int>(e) + kScaleSlack - 127);
-    }
-    d0 -= limit - kSlack;
-    d1 -= limit - kSlack;
+    cap = __uint_as_float((e + kScaleSlack) << 23);
+    limit = kTop - static_cast<float>(static_cast<int>(e) + kScaleSlack - 127);
+    d0 -= kTarget;
+    d1 -= kTarget;
     if (!first) {
       d0 = fmaxf(d0, 0.f);
       d1 = fmaxf(d1, 0.f);
+    }
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      add2(x[i][0], x[i][1], -d0, -d1);
+      add2(x[i][2], x[i][3], -d0, -d1);
     }
     m0 += d0;
     m1 += d1;
@@ -261,8 +283,6 @@ struct WarpAttnInt4 {
       }
     }
   }
-  // Whether a scale with this exponent (biased) can be above the cap, a power of two.
-  __device__ __forceinline__ bool smax_exceeds(uint32_t e) const { return e >= __float_as_uint(cap) >> 23; }
 
   // One softmax step over NB consecutive blocks of one unit, whose (K tile, V
   // tile) pairs lie back to back at `stage`.  MASK: only the first `valid` (1..16
@@ -302,16 +322,8 @@ struct WarpAttnInt4 {
       d1 = max3(d1, x[i][1], x[i][3]);
       smax = max3(smax, fabsf(sv[i][0]), fabsf(sv[i][1]));
     }
-    if (__any_sync(0xffffffffu, fmaxf(d0, d1) > limit || smax > cap)) {  // and before anything is summed: cap < 0
-      rescale(d0, d1, smax);
-#pragma unroll
-      for (int i = 0; i < NB; ++i) {
-        x[i][0] -= d0;
-        x[i][1] -= d1;
-        x[i][2] -= d0;
-        x[i][3] -= d1;
-      }
-    }
+    if (__any_sync(0xffffffffu, fmaxf(d0, d1) > limit || smax > cap))  // and before anything is summed: cap < 0
+      move_reference<NB>(x, sv, smax);
 #pragma unroll
     for (int i = 0; i < NB; ++i) {
       uint32_t p[2];
