@@ -330,8 +330,8 @@ int paged_decode_step_fp8(const void* q, const void* k_new, const void* v_new, v
  * Quantisation of a row x (append), every step in IEEE float32: x limited to
  *   +-65504; minimum = float16(min x); scale = float16((max x - minimum) / 15);
  *   code = round_half_even((x - minimum) * (1 / scale)) limited to 0..15 (0
- *   where the scale is not above 0).  The codes of NaN inputs are outside the
- *   contract.
+ *   where the scale is not above 0).  A row with a NaN is stored with codes 0,
+ *   scale 0 and minimum NaN (0x7FFF): all of it reads as NaN.
  * Attention: the plain attention of the dequantised cache.  The products run
  *   as fp16 mma (codes are exact in fp16); a bf16 query is converted to fp16: an
  *   entry beyond +-65504 sets the error word (PKV_ERR_OUT_OF_RANGE from

@@ -16,14 +16,18 @@ F16_MAX = np.float32(65504.0)
 
 def quantise_rows(x: np.ndarray):
     """Codes uint8 [..., D] and float16 pairs [..., 2] (scale, minimum) of rows
-    of values [..., D]; every step in IEEE float32, as the contract says."""
+    of values [..., D]; every step in IEEE float32, as the contract says.  A row
+    with a NaN: codes 0, scale 0, minimum NaN (0x7FFF)."""
     x = np.clip(np.asarray(x, np.float32), -F16_MAX, F16_MAX)
+    bad = np.isnan(x).any(-1, keepdims=True)
+    x = np.where(bad, np.float32(0), x)
     low = x.min(-1, keepdims=True).astype(np.float16)
     lowf = low.astype(np.float32)
     scale = ((x.max(-1, keepdims=True) - lowf) / np.float32(15)).astype(np.float16)
     sf = scale.astype(np.float32)
     inv = np.divide(np.float32(1), sf, out=np.zeros_like(sf), where=sf > 0)
     codes = np.clip(np.rint((x - lowf) * inv), 0, 15).astype(np.uint8)
+    low = np.where(bad, np.uint16(0x7FFF), low.view(np.uint16)).view(np.float16)
     return codes, np.concatenate([scale, low], -1)
 
 

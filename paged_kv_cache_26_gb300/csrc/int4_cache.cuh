@@ -52,10 +52,24 @@ __device__ __forceinline__ void fma2(float& x, float& y, float a, float b, float
       : "f"(a), "f"(b), "f"(k), "f"(c), "f"(d));
 }
 
+// The smaller / larger of two, NaN if either is.
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // The stored pair of a row with these extremes (of values limited to the
 // float16 range): m = f16(min), s = f16((max - m) / 15), all IEEE float32, so
 // that the codes are the same wherever the formula is evaluated in float32.
 // s rounds to 0 for a row of (nearly) equal values: its codes are then 0.
+// A row with a NaN (both extremes are) has m = NaN, s = 0 and codes 0: it reads
+// as NaN and attention that meets it gives NaN, as with a 16-bit pool.
 struct Int4Row {
   float low, inv;
   uint32_t pair;  // scale in bits 0-15, minimum in bits 16-31
@@ -73,6 +87,12 @@ __device__ __forceinline__ Int4Row int4_row(float mn, float mx) {
   const __half sc = __float2half_rn(__fmaf_rn(__fmaf_rn(-15.f, y, x), kFifteenth, y));
   const float s = __half2float(sc);
   r.inv = s > 0.f ? __frcp_rn(s) : 0.f;
+  if (mn != mn) {  // (x - low) * inv is then 0 or NaN for every x: code 0
+    r.low = 0.f;
+    r.inv = 0.f;
+    r.pair = 0x7fffu << 16;
+    return r;
+  }
   r.pair = static_cast<uint32_t>(__half_as_ushort(sc)) | static_cast<uint32_t>(__half_as_ushort(lo)) << 16;
   return r;
 }
@@ -80,7 +100,7 @@ __device__ __forceinline__ uint32_t int4_code(float x, const Int4Row& r) {
   const float v = rintf(__fmul_rn(__fsub_rn(x, r.low), r.inv));
   return static_cast<uint32_t>(fminf(fmaxf(v, 0.f), 15.f));  // a NaN gives 0
 }
-__device__ __forceinline__ float limit_f16(float x) { return fminf(fmaxf(x, -kF16Max), kF16Max); }
+__device__ __forceinline__ float limit_f16(float x) { return min_nan(max_nan(x, -kF16Max), kF16Max); }
 
 // One row of D values spread over W = D/4 neighbouring lanes, four consecutive
 // values (packed in `raw`) each: the lane's four codes and the row's pair.
@@ -88,11 +108,11 @@ template <typename T, int W>
 __device__ __forceinline__ uint32_t int4_quantise4(const uint2& raw, uint32_t& pair) {
   const float2 a = unpack2<T>(raw.x), b = unpack2<T>(raw.y);
   const float x0 = limit_f16(a.x), x1 = limit_f16(a.y), x2 = limit_f16(b.x), x3 = limit_f16(b.y);
-  float mn = fminf(fminf(x0, x1), fminf(x2, x3)), mx = fmaxf(fmaxf(x0, x1), fmaxf(x2, x3));
+  float mn = min_nan(min_nan(x0, x1), min_nan(x2, x3)), mx = max_nan(max_nan(x0, x1), max_nan(x2, x3));
 #pragma unroll
   for (int o = 1; o < W; o <<= 1) {
-    mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    mn = min_nan(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+    mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
   }
   const Int4Row r = int4_row(mn, mx);
   pair = r.pair;
@@ -110,23 +130,23 @@ __device__ __forceinline__ void int4_store4(uint8_t* tile, bool is_v, int t, int
 
 // ===================================================================== append
 
-// The larger / smaller of two packed pairs of T, half by half.
+// The larger / smaller of two packed pairs of T, half by half; NaN if either is.
 template <typename T>
 __device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
   uint32_t r;
   if constexpr (MmaKind<T>::kBf16)
-    asm("min.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   else
-    asm("min.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    asm("min.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
 template <typename T>
 __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
   uint32_t r;
   if constexpr (MmaKind<T>::kBf16)
-    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   else
-    asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
 
@@ -160,7 +180,7 @@ __device__ __forceinline__ uint2 int4_quantise16(const uint4 (&raw)[2], uint32_t
   constexpr uint32_t kExcess = 0x4b400000u * 0x11111111u;  // its bits times 1 + 16 + .. + 16^7
   uint32_t out[2];
   // Values past the float16 range, a quotient that rounds above 15 (a scale in
-  // float16's subnormal range), or a NaN: limited one by one.
+  // float16's subnormal range), or a NaN (both extremes are): limited one by one.
   const bool odd = !(e.x >= -kF16Max && -e.y <= kF16Max && __fmul_rn(__fsub_rn(mx, r.low), r.inv) < 15.5f);
   if (odd) {
 #pragma unroll

@@ -122,3 +122,54 @@ def test_the_heaviest_rows_are_constant(level, d):
     v[::7] = level
     check_weighted(q, k, v.to(dtype), d ** -0.5)
     check_weighted(q, k, torch.full_like(v, level).to(dtype), d ** -0.5)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16], ids=["fp16", "bf16"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_rows_with_a_nan_are_nan_and_alone(d, dtype):
+    """Both appends store the same bytes for a row with a NaN; it reads and attends as NaN, its neighbours as ever."""
+    hk, g, n, nb = 2, 3, 40, 6
+    gen = torch.Generator().manual_seed(d)
+    k, v = (torch.randn(n, hk, d, generator=gen).to(dtype) for _ in range(2))
+    nan = float("nan")
+    v[5, 1, 7], v[6, 0], k[21, 0, d - 1] = nan, nan, nan
+    v[8, 1, :4] = torch.tensor([nan, float("inf"), -float("inf"), 1.0])
+    v[9, 0, 3], v[10, 0, 5] = float("inf"), -float("inf")           # no NaN: limited, as ever
+    k[22, 1].view(torch.int16)[9] = -1                              # a negative NaN
+    table = np.array([3, 0, 5], np.int32)
+    rk, rv = pools_of(k, v, table, nb)
+    slots = (table[np.arange(n) // 16] * 16 + np.arange(n) % 16).astype(np.int32)
+    kp, vp = (torch.full((nb, hk, 16, d // 2 + 4), 0xFF, dtype=torch.uint8, device=DEV) for _ in range(2))
+    pkv.paged_kv_append_int4(k.to(DEV), v.to(DEV), torch.from_numpy(slots).to(DEV), kp, vp)
+    assert np.array_equal(kp.cpu().numpy(), rk) and np.array_equal(vp.cpu().numpy(), rv)
+    # the same rows one by one through the fused step
+    k2, v2 = (torch.full_like(kp, 0xFF) for _ in range(2))
+    bt = torch.from_numpy(table[None].copy()).to(DEV)
+    q = torch.randn(1, hk * g, d, generator=gen).to(dtype).to(DEV)
+    for i in range(n):
+        cl = torch.tensor([i + 1], dtype=torch.int32, device=DEV)
+        out = pkv.paged_decode_step_int4(q, k[i:i + 1].to(DEV), v[i:i + 1].to(DEV), k2, v2, bt, cl, 0.1)[0].float().cpu()
+        ref = int4.decode_attention(widen_out(q.cpu(), NAMES[dtype]), rk, rv, table[None], [i + 1], 0.1)[0]
+        assert np.array_equal(np.isnan(out.numpy()), np.isnan(ref)), i
+        assert np.isnan(ref[:g]).all() == (i >= 6) and np.isnan(ref[g:]).all() == (i >= 5)
+    assert torch.equal(k2, kp) and torch.equal(v2, vp)
+    ko, vo = pkv.paged_kv_read_int4(torch.from_numpy(slots).to(DEV), kp, vp, dtype)
+    pkv.paged_kv_check_status()
+    assert torch.equal(ko.cpu().isnan().all(-1), k.isnan().any(-1)) and torch.equal(vo.cpu().isnan().any(-1), v.isnan().any(-1))
+    assert torch.equal(ko.cpu().isnan().any(-1), k.isnan().any(-1)) and torch.equal(vo.cpu().isnan().all(-1), v.isnan().any(-1))
+
+
+@pytest.mark.parametrize("at", [0, 9, 70, 299])
+def test_a_nan_key_gives_nan_for_its_kv_head_alone(at):
+    """Anywhere in a context, in the first step or a later one."""
+    n, d, dtype = 300, 128, torch.bfloat16
+    _, _, q, k, v = context(n, d, dtype, 5)
+    k[at, 1, 3] = float("nan")
+    nb = -(-n // 16)
+    table = np.arange(nb, dtype=np.int32)
+    kp, vp = pools_of(k, v.to(dtype), table, nb)
+    out = pkv.paged_decode_attention_int4(q[None].to(DEV), torch.from_numpy(kp).to(DEV), torch.from_numpy(vp).to(DEV),
+                                          torch.from_numpy(table[None].copy()).to(DEV),
+                                          torch.tensor([n], dtype=torch.int32, device=DEV), 0.1)[0]
+    pkv.paged_kv_check_status()
+    assert out[4:].isnan().all() and torch.isfinite(out[:4]).all()

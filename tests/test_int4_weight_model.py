@@ -110,3 +110,14 @@ def test_the_largest_scale_alone_would_not_do():
         p /= p.sum()
         worst = max(worst, abs(got - (p * (mid + dev)).sum()) / (2.0 ** -11 * 7.5 * (p * s).sum()))
     assert worst > 8
+
+
+def test_the_oracle_keeps_a_nan_in_its_row():
+    from oracle import int4
+    x = np.linspace(-1, 1, 3 * 64, dtype=np.float32).reshape(3, 64)
+    clean = int4.quantise_rows(x)
+    x[1, 5] = np.nan
+    codes, pairs = int4.quantise_rows(x)
+    assert not codes[1].any() and list(pairs[1].view(np.uint16)) == [0, 0x7FFF]
+    for i in (0, 2):
+        assert np.array_equal(codes[i], clean[0][i]) and np.array_equal(pairs[i], clean[1][i])
