@@ -140,7 +140,12 @@ int paged_kv_append(const void* k_new, const void* v_new, const int32_t* slot_ma
  * counters in it at zero (on the automatic path it also carries, from the
  * decode kernel to the merge of the same call, the lengths the decode kernel
  * used, under a per-call tag).  It may be NULL when that size is 0.  Calls
- * that share a workspace must not run concurrently.
+ * that share a workspace must not run concurrently; one after the other, calls
+ * of any dims, num_splits, q_len and pool format (16-bit, E4M3, 4-bit) can share
+ * one of the largest size that paged_decode_workspace_bytes and
+ * paged_decode_multi_workspace_bytes give for them: what has to last from call
+ * to call is its first 256 bytes, which no call uses for anything else (a split
+ * or multi-token call does where workspace_bytes leaves no room for them).
  *
  * Requirements: head_dim 64 or 128, block_size 16, 1 <= Hq/Hkv <= 8,
  * caches and q/out 16-byte aligned, num_blocks * num_kv_heads * 16 < 2^31.
@@ -394,7 +399,8 @@ int paged_decode_step_int4(const void* q, const void* k_new, const void* v_new, 
  * automatic (512-token splits, more when the batch alone would not fill the
  * GPU), n >= 1 = n splits.  Workspace: paged_decode_multi_workspace_bytes
  * bytes (0 for one split), 256-byte aligned; its contents need no
- * initialisation.  Errors as paged_decode_attention; q_len outside 1..8 gives
+ * initialisation (for these calls; shared with paged_decode_attention's
+ * automatic path, as there).  Errors as paged_decode_attention; q_len outside 1..8 gives
  * PKV_ERR_UNSUPPORTED.
  * ---------------------------------------------------------------------- */
 int paged_decode_attention_multi(const void* q, const void* k_cache, const void* v_cache,

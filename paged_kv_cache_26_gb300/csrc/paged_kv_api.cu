@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdint>
@@ -198,17 +199,37 @@ int plan_splits(const pkv_dims* d, int32_t requested, SplitPlan* plan) {
   return PKV_OK;
 }
 
-// Workspace regions: [partial outputs][partial log-sum-exps][publication of
-// the decode grid's lengths to its merge][scheduler counters][4-bit pools: where
-// the merge finds each unit's pieces].
+// Workspace regions.  The first kHeaderBytes hold what a call finds there from
+// the calls before it: the scheduler counters of the persistent kernel (zero
+// between calls) and, as their last word, the tag of the publication that
+// follows.  They lie at the front, whatever the dims and the pool's format, and
+// no other region covers them, so that calls of any shapes can share one
+// workspace:
+//   persistent: [header][publication][log-sum-exps][partial outputs];
+//   split and multi-token: [header, if there is room][partial outputs][log-sum-exps].
+// A 4-bit call uses one of the five segments per warp; where its merge finds
+// each unit's pieces lies behind them, in the partials' unused part (and past
+// their end only for more units than fit: 3.7 million at head_dim 64).
+constexpr size_t kHeaderBytes = 256;
 struct WorkspaceLayout {
-  size_t o_bytes = 0, lse_bytes = 0, sched_bytes = 0, pub_bytes = 0, unit_bytes = 0;
-  size_t total() const { return o_bytes + lse_bytes + sched_bytes + pub_bytes + unit_bytes; }
+  size_t o_bytes = 0, lse_bytes = 0, pub_bytes = 0, header_bytes = 0, unit_bytes = 0;
+  size_t total() const { return o_bytes + lse_bytes + pub_bytes + header_bytes; }
+  size_t unit_offset() const { return header_bytes + pub_bytes + lse_bytes + o_bytes / kSegmentsPerWarp; }
+  size_t total_int4() const { return std::max(total(), unit_offset() + unit_bytes); }
+
+  static constexpr size_t kSegmentsPerWarp = 1 + pkv::Partition::kMaxTailChunks;
 };
+static_assert(pkv::Int4Shape<128>::kWarps <= pkv::kMaxPersistentWarps, "a segment per warp");
+
+// Where a call of the split kernels puts its partials: behind the header of the
+// automatic path if the workspace has room for it.
+uint8_t* split_partials(void* workspace, size_t workspace_bytes, size_t need) {
+  return static_cast<uint8_t*>(workspace) + (workspace_bytes - need >= kHeaderBytes ? kHeaderBytes : 0);
+}
 
 // Segments of the persistent partition for the largest grid (one CTA per SM).
 size_t persistent_segments() {
-  return static_cast<size_t>(device_sms()) * pkv::kMaxPersistentWarps * (1 + pkv::Partition::kMaxTailChunks);
+  return static_cast<size_t>(device_sms()) * pkv::kMaxPersistentWarps * WorkspaceLayout::kSegmentsPerWarp;
 }
 
 WorkspaceLayout workspace_layout(const pkv_dims* d, const SplitPlan& p) {
@@ -217,10 +238,10 @@ WorkspaceLayout workspace_layout(const pkv_dims* d, const SplitPlan& p) {
     const size_t seg = persistent_segments();
     w.o_bytes = align256(seg * 2 * pkv::kMaxGroup * d->head_dim * sizeof(float));
     w.lse_bytes = align256(seg * 2 * pkv::kMaxGroup * sizeof(float));
-    w.sched_bytes = 256;
+    w.header_bytes = kHeaderBytes;
     w.unit_bytes = align256(static_cast<size_t>(d->num_seqs) * d->num_kv_heads * sizeof(pkv::UnitPieces));
     // The decode grid's validated lengths and block prefix, for the merge:
-    // [epoch][context B][prefix B + 1] int32.
+    // [tag, the header's last word][context B][prefix B + 1] int32.
     w.pub_bytes = align256((2 * static_cast<size_t>(d->num_seqs) + 2) * sizeof(int32_t));
   } else if (p.num_splits > 1) {
     const size_t rows = static_cast<size_t>(d->num_seqs) * d->num_q_heads * p.num_splits;
@@ -441,7 +462,7 @@ int decode_impl(const void* q, const void* k_new, const void* v_new, void* k_cac
   rc = plan_splits(d, num_splits, &plan);
   if (rc != PKV_OK) return rc;
   const WorkspaceLayout wl = workspace_layout(d, plan);
-  const size_t need = wl.total();
+  const size_t need = format == kPoolInt4 ? wl.total_int4() : wl.total();
   if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256)))
     return pkv_fail(PKV_ERR_INVALID_ARG, "decode_attention: workspace missing, too small (" +
                                              std::to_string(need) + " bytes needed) or not 256-byte aligned");
@@ -470,14 +491,20 @@ int decode_impl(const void* q, const void* k_new, const void* v_new, void* k_cac
   args.q = q;
   args.out = out;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  args.part_o = need ? reinterpret_cast<float*>(ws) : nullptr;
-  args.part_lse = need ? reinterpret_cast<float*>(ws + wl.o_bytes) : nullptr;
-  // [partials][log-sum-exps][publication][scheduler counters][units' pieces]
-  args.pub = wl.pub_bytes ? reinterpret_cast<int32_t*>(ws + wl.o_bytes + wl.lse_bytes) : nullptr;
-  args.sched = wl.sched_bytes ? reinterpret_cast<int32_t*>(ws + wl.o_bytes + wl.lse_bytes + wl.pub_bytes) : nullptr;
-  if (format == kPoolInt4) args.sched = reinterpret_cast<int32_t*>(ws + wl.total() - wl.unit_bytes);
+  args.part_o = args.part_lse = nullptr;
+  args.pub = args.sched = nullptr;
+  if (plan.persistent) {
+    args.sched = reinterpret_cast<int32_t*>(format == kPoolInt4 ? ws + wl.unit_offset() : ws);
+    args.pub = reinterpret_cast<int32_t*>(ws + kHeaderBytes) - 1;
+    args.part_lse = reinterpret_cast<float*>(ws + kHeaderBytes + wl.pub_bytes);
+    args.part_o = reinterpret_cast<float*>(ws + kHeaderBytes + wl.pub_bytes + wl.lse_bytes);
+  } else if (need > 0) {
+    ws = split_partials(workspace, workspace_bytes, need);
+    args.part_o = reinterpret_cast<float*>(ws);
+    args.part_lse = reinterpret_cast<float*>(ws + wl.o_bytes);
+  }
   args.epoch = 0;
-  if (recheck && publish && plan.persistent && args.pub && format != kPoolInt4) {
+  if (recheck && publish && plan.persistent && format != kPoolInt4) {
     // A new tag per call, so that a merge never takes an earlier call's
     // publication for its own; 0 (no publication: the merge re-reads the
     // lengths itself) while the stream is being captured, since a graph
@@ -851,7 +878,7 @@ int decode_multi_impl(const void* q, const void* k_new, const void* v_new, void*
   args.out = out;
   args.block_tables = block_tables;
   args.context_lens = context_lens;
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  uint8_t* ws = need ? split_partials(workspace, workspace_bytes, need) : nullptr;
   const size_t rows = static_cast<size_t>(d->num_seqs) * q_len * d->num_q_heads;
   args.part_o = need ? reinterpret_cast<float*>(ws) : nullptr;
   args.part_lse = need ? reinterpret_cast<float*>(ws + align256(rows * splits * d->head_dim * sizeof(float)))
@@ -1167,7 +1194,8 @@ size_t paged_decode_multi_workspace_bytes(const pkv_dims* dims, int32_t q_len, i
   if (check_multi(dims, q_len, num_splits) != PKV_OK) return 0;
   int32_t splits, split_blocks;
   multi_plan(dims, q_len, num_splits, &splits, &split_blocks);
-  return multi_workspace(dims, q_len, splits);
+  const size_t need = multi_workspace(dims, q_len, splits);
+  return need ? need + kHeaderBytes : 0;
 }
 
 int32_t paged_decode_multi_resolve_splits(const pkv_dims* dims, int32_t q_len, int32_t num_splits) {
@@ -1360,7 +1388,9 @@ size_t paged_decode_workspace_bytes(const pkv_dims* dims, int32_t num_splits) {
   if (check_dims(dims, true) != PKV_OK) return 0;
   SplitPlan p;
   if (plan_splits(dims, num_splits, &p) != PKV_OK) return 0;
-  return workspace_layout(dims, p).total();
+  const WorkspaceLayout w = workspace_layout(dims, p);
+  if (p.persistent) return w.total_int4();
+  return w.total() ? w.total() + kHeaderBytes : 0;
 }
 
 int paged_decode_step_from_host(const pkv_step_buffers* s, void* k_cache, void* v_cache, float scale,

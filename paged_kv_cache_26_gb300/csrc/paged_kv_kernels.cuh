@@ -567,6 +567,7 @@ struct DecodeArgs {
   float* part_o;              // split: f32[B][Hq][splits][D]; persistent: f32[segments][2][8][D]
   float* part_lse;            // split: f32[B][Hq][splits];    persistent: f32[segments][2][8]
   int32_t* sched;             // persistent: int32[2] chunk counter and finished-warp counter, zero between calls
+                              // (4-bit pools: UnitPieces[B][Hkv], written in every call)
   int32_t* pub;               // persistent: [epoch][context B][prefix B + 1]: the decode grid's validated
                               // lengths, published (release) for the merge of the same call
   uint32_t epoch;             // persistent: this call's publication tag; 0 = none (the merge re-reads)
