@@ -510,7 +510,7 @@ int paged_verify_draft(const void* target_probs, const void* draft_probs, const 
  * slot_mapping : int32[num_slots] or NULL (num_slots 0): the slots of the tokens
  *   gained, positions old..new - 1 of each sequence that grows, packed by
  *   sequence; -1 behind them, which every append skips.  num_slots must hold
- *   them all.
+ *   them all (0 with a pointer that is not NULL: no token may be gained).
  * token_offsets : int32[num_seqs + 1] or NULL: where each sequence's slots begin.
  * On success context_lens becomes new_lens and num_free the new count.
  * All or nothing: with too few blocks (PKV_ERR_NO_BLOCKS from

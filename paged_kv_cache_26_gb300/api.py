@@ -692,7 +692,8 @@ def paged_kv_resize_tables(context_lens: torch.Tensor, new_lens: torch.Tensor, b
                 slot_mapping.is_contiguous()):
             _explain(dev, ("slot_mapping", slot_mapping, _i32))
             raise ValueError("slot_mapping must be [num_slots]")
-        slots, num_slots = slot_mapping.data_ptr(), slot_mapping.numel()
+        # An empty map is a map without room; its null pointer would mean that none is wanted.
+        slots, num_slots = slot_mapping.data_ptr() or num_free.data_ptr(), slot_mapping.numel()
     if token_offsets is not None:
         if not (token_offsets.get_device() == dev and token_offsets.dtype == _i32 and
                 token_offsets.shape == (bt[0] + 1,) and token_offsets.is_contiguous()):
