@@ -760,13 +760,13 @@ def paged_verify_draft(target_probs: torch.Tensor, draft_probs: Optional[torch.T
         ctx = context_lens.data_ptr()
     if stream is None:
         accepted, tokens = torch.empty((B,), dtype=_i32, device=dev), torch.empty((B, K + 1), dtype=_i32, device=dev)
-        lens = torch.empty_like(context_lens) if ctx else None
+        lens = torch.empty_like(context_lens) if context_lens is not None else None
     else:
         with _allocating_on(stream, dev):
             accepted = torch.empty((B,), dtype=_i32, device=dev)
             tokens = torch.empty((B, K + 1), dtype=_i32, device=dev)
-            lens = torch.empty_like(context_lens) if ctx else None
-    lens_ptr = lens.data_ptr() if ctx else 0
+            lens = torch.empty_like(context_lens) if context_lens is not None else None
+    lens_ptr = lens.data_ptr() if lens is not None else 0
     dims = PkvVerifyDims(B, K, V, code, t_stride[0], t_stride[1], d_seq, d_row)
     _call("paged_verify_draft", dev, stream,
           (target_probs.data_ptr(), q, draft_tokens.data_ptr(), n, accept_u.data_ptr(), sample_u.data_ptr(), ctx,

@@ -46,3 +46,16 @@ def test_a_slot_map_without_room_takes_no_tokens(width):
     pkv.paged_kv_resize_tables(d[0], i32([18, 20, 0]), d[1], d[2], d[3])
     pkv.paged_kv_check_status()
     assert d[0].tolist() == [18, 20, 0] and d[1][0, 1] == 6
+
+
+@pytest.mark.parametrize("by_stream", [False, True])
+def test_an_empty_batch_has_lengths_when_it_gave_some(by_stream):
+    t, d = torch.zeros(0, 3, 8, device=DEV), torch.zeros(0, 2, 8, device=DEV)
+    x, au, su = torch.zeros(0, 2, dtype=torch.int32, device=DEV), torch.zeros(0, 2, device=DEV), torch.zeros(0, device=DEV)
+    stream = torch.cuda.Stream() if by_stream else None
+    a, out, lens = pkv.paged_verify_draft(t, d, x, au, su, context_lens=i32([]), stream=stream)
+    assert a.shape == (0,) and out.shape == (0, 3) and lens.shape == (0,) and lens.dtype == torch.int32
+    assert pkv.paged_verify_draft(t, d, x, au, su, stream=stream)[2] is None
+    free, num = i32([0, 1]), i32([2])
+    pkv.paged_kv_resize_tables(i32([]), lens, i32(np.zeros((0, 4))), free, num)   # and on to giving back
+    pkv.paged_kv_check_status()
