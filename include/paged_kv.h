@@ -82,7 +82,7 @@ enum {
 
 enum { PKV_DTYPE_FP16 = 0, PKV_DTYPE_BF16 = 1, PKV_DTYPE_FP32 = 2 /* paged_verify_draft only */ };
 
-enum { PKV_ELEM_INT4 = 0 }; /* paged_kv_copy_blocks' element size of a 4-bit pool */
+enum { PKV_ELEM_INT4 = -4 }; /* paged_kv_copy_blocks' element size of a 4-bit pool (not a byte count, and not 0) */
 
 typedef struct pkv_dims {
   int32_t num_seqs;            /* batch size B (also num_tokens for the append) */

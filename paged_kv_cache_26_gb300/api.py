@@ -14,6 +14,7 @@ import torch
 from ._native import PkvDims, PkvStepBuffers, PkvVerifyDims, c_int32_p, lib
 
 PKV_OK = 0
+PKV_ELEM_INT4 = -4  # paged_kv_copy_blocks' element size of a 4-bit pool
 ERROR_NAMES = {
     -1: "PKV_ERR_INVALID_ARG", -2: "PKV_ERR_UNSUPPORTED", -3: "PKV_ERR_CUDA", -4: "PKV_ERR_TIMEOUT",
     -5: "PKV_ERR_NO_BLOCKS", -6: "PKV_ERR_OUT_OF_RANGE", -7: "PKV_ERR_SHARED_BLOCK",
@@ -790,7 +791,7 @@ def paged_kv_copy_blocks(k_cache: torch.Tensor, v_cache: torch.Tensor, block_pai
     nb, hkv, bs, d = k_cache.shape
     elem = k_cache.element_size()
     if k_cache.dtype == torch.uint8 and d in (int4_row_bytes(64), int4_row_bytes(128)):  # no E4M3 row is that wide
-        d, elem = 2 * (d - 4), 0
+        d, elem = 2 * (d - 4), PKV_ELEM_INT4
     dims = PkvDims(num_seqs=0, num_q_heads=hkv, num_kv_heads=hkv, head_dim=d, block_size=bs, num_blocks=nb,
                    max_blocks_per_seq=0, dtype=_DTYPE_CODE.get(k_cache.dtype, 0))
     _check(lib().paged_kv_copy_blocks(_ptr(k_cache), _ptr(v_cache), _ptr(block_pairs), block_pairs.shape[0],
