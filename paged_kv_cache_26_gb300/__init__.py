@@ -6,7 +6,7 @@ The shared library loads lazily on the first call; if it has not been built
 every call raises (there is no fallback implementation)."""
 from .api import (BlockAllocator, PagedKVError, make_workspace, paged_decode_attention,
                   paged_decode_attention_fp8, paged_decode_attention_no_alloc, paged_decode_step_fp8,
-                  paged_kv_append_fp8, make_workspace_int4, paged_decode_attention_int4, paged_decode_step_int4,
+                  paged_kv_append_fp8, int4_row_bytes, make_workspace_int4, paged_decode_attention_int4, paged_decode_step_int4,
                   paged_kv_append_int4, paged_kv_read_int4, paged_kv_resize_tables, paged_verify_draft,
                   paged_decode_attention_multi, paged_decode_step_multi,
                   paged_decode_multi_workspace_bytes, paged_decode_multi_resolve_splits, paged_kv_slot_mapping_multi,
@@ -25,7 +25,7 @@ __all__ = [
     "paged_kv_check_status", "paged_kv_slot_mapping",
     "paged_kv_append_fp8", "paged_decode_attention_fp8", "paged_decode_step_fp8",
     "paged_kv_append_int4", "paged_kv_read_int4", "paged_decode_attention_int4", "paged_decode_step_int4",
-    "make_workspace_int4", "paged_kv_resize_tables", "paged_verify_draft",
+    "int4_row_bytes", "make_workspace_int4", "paged_kv_resize_tables", "paged_verify_draft",
     "paged_decode_attention_multi", "paged_decode_step_multi", "paged_decode_multi_workspace_bytes",
     "paged_decode_multi_resolve_splits", "paged_kv_slot_mapping_multi", "paged_kv_copy_blocks",
     "paged_kv_selftest_wait", "paged_kv_selftest_stale_prologue", "paged_kv_selftest_stale_prologue_int4",

@@ -630,7 +630,8 @@ def paged_decode_attention_int4(q: torch.Tensor, k_cache: torch.Tensor, v_cache:
                                 block_tables: torch.Tensor, context_lens: torch.Tensor, scale: float,
                                 out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
                                 stream=None) -> torch.Tensor:
-    """paged_decode_attention over 4-bit caches.  Returns out."""
+    """paged_decode_attention over 4-bit caches.  Returns out.  Pass a workspace
+    (make_workspace_int4) that lasts: None allocates and fills one in every call."""
     dev, dims, out, workspace, ws_bytes = _int4_decode(q, k_cache, v_cache, block_tables, context_lens, out, workspace,
                                                        stream)
     _call("paged_decode_attention_int4", dev, stream,
@@ -644,7 +645,8 @@ def paged_decode_step_int4(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Te
                            scale: float, out: Optional[torch.Tensor] = None,
                            workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """paged_decode_step over 4-bit caches: the new token is quantised and
-    appended, then attended, in one fused launch.  Returns out."""
+    appended, then attended, in one fused launch.  Returns out.  Workspace as
+    paged_decode_attention_int4."""
     dev, dims, out, workspace, ws_bytes = _int4_decode(q, k_cache, v_cache, block_tables, context_lens, out, workspace,
                                                        stream)
     if not (k_new.get_device() == dev and v_new.get_device() == dev and k_new.dtype == q.dtype and
