@@ -1348,7 +1348,8 @@ int paged_decode_attention_int4(const void* q, const void* k_cache, const void* 
 int paged_decode_step_int4(const void* q, const void* k_new, const void* v_new, void* k_cache, void* v_cache,
                            const int32_t* block_tables, const int32_t* context_lens, float scale, void* out,
                            void* workspace, size_t workspace_bytes, const pkv_dims* dims, void* stream) {
-  if (!k_new || !v_new) return pkv_fail(PKV_ERR_INVALID_ARG, "decode_step_int4: NULL k_new / v_new");
+  const bool empty = dims && dims->num_seqs == 0;  // nothing to append: the rows' pointers may be NULL
+  if (!empty && (!k_new || !v_new)) return pkv_fail(PKV_ERR_INVALID_ARG, "decode_step_int4: NULL k_new / v_new");
   return decode_impl(q, k_new, v_new, k_cache, v_cache, block_tables, context_lens, scale, out, 0, workspace,
                      workspace_bytes, dims, static_cast<cudaStream_t>(stream), kPoolInt4);
 }
