@@ -180,8 +180,10 @@ int paged_decode_step(const void* q, const void* k_new, const void* v_new, void*
  * or a PKV_ERR_* code. */
 int32_t paged_decode_resolve_splits(const pkv_dims* dims, int32_t num_splits);
 
-/* Workspace bytes paged_decode_attention needs for these dims and num_splits
- * (0 when it runs in one pass). */
+/* Workspace bytes for paged_decode_attention with these dims and num_splits (0
+ * when it runs in one pass), enough for the other pool formats' calls with
+ * these dims too.  For splits it is 256 bytes more than the call requires, so
+ * that a shared workspace's first 256 bytes stay free. */
 size_t paged_decode_workspace_bytes(const pkv_dims* dims, int32_t num_splits);
 
 /*
@@ -338,9 +340,12 @@ int paged_decode_step_fp8(const void* q, const void* k_new, const void* v_new, v
  *   where the scale is not above 0).  A row with a NaN is stored with codes 0,
  *   scale 0 and minimum NaN (0x7FFF): all of it reads as NaN.
  * Attention: the plain attention of the dequantised cache.  The products run
- *   as fp16 mma (codes are exact in fp16); a bf16 query is converted to fp16: an
- *   entry beyond +-65504 sets the error word (PKV_ERR_OUT_OF_RANGE from
- *   paged_kv_check_status).  A scale in the pool must be finite; slots past a
+ *   as fp16 mma (codes are exact in fp16); each product of a softmax weight and
+ *   a V scale is rounded to fp16 (2^-11 of it).  A bf16 query is converted to
+ *   fp16: an entry beyond +-65504 sets the error word (PKV_ERR_OUT_OF_RANGE from
+ *   paged_kv_check_status), one below 2^-14 is rounded to a multiple of 2^-24
+ *   (off by 2^-25 at most, which moves a logit by scale * 2^-25 * sum |K_t|).
+ *   A scale in the pool must be finite; slots past a
  *   sequence's length may hold anything.  A block id outside the pool reads as
  *   zeros and is flagged.
  * Limits: head_dim 64 or 128; at most 2048 sequences per call, and

@@ -106,7 +106,7 @@ struct WarpAttnInt4 {
 
   // Entries [(D/4) c, (D/4) (c + 1)) of query row gid as float16 in the order
   // the masked K words pair them; a bf16 query beyond the float16 range is
-  // flagged (kErrQuery).  Word w holds dims d0..d7: registers (d0,d4), (d2,d6)
+  // flagged (kErrQuery), below its normal range (2^-14) it is off by 2^-25 at most.  Word w holds dims d0..d7: registers (d0,d4), (d2,d6)
   // meet the masks of factor 1, (d1,d5), (d3,d7) those of factor 16.
   __device__ __forceinline__ void load_q(const T* q_group, int group, float scale_log2, int lane) {
     const int gid = lane >> 2, c = lane & 3;
