@@ -535,6 +535,146 @@ int paged_kv_resize_tables(int32_t* context_lens, const int32_t* new_lens, int32
                            void* stream);
 
 /* ------------------------------------------------------------------------
+ * Rotary positions (device).  "How to Scale Your Model, Part 7: Inference",
+ * section "Transformer 推論の基礎: Prefill と Generation": keys enter the cache as
+ * attention will read them, so queries and keys are turned to their tokens'
+ * positions before.  The pages give no position encoding; this is the usual one:
+ * frequency f of rot_dim / 2 turns the dims (i, j) of every query and key head
+ * by a = position * inv_freq[f],
+ *   x'_i = factor (x_i cos a - x_j sin a),  x'_j = factor (x_j cos a + x_i sin a),
+ * (i, j) = (f, f + rot_dim/2), or (2f, 2f + 1) when interleaved.  Dims past
+ * rot_dim stay as they are.  A token has num_axes positions (1 for text; time,
+ * height and width for images and video), and frequency f takes that of axis
+ * axes[f].  Positions are int32, negative ones allowed; the angle keeps its
+ * precision at any of them (2^-32 of a turn plus the frequency's own 2^-53).
+ *
+ * pkv_rope is a plain value, made once on the host by paged_kv_rope_init.
+ * positions : int32[num_axes][num_tokens] (device)
+ * q, q_out  : T[num_tokens][Hq][D], k, k_out, v : T[num_tokens][Hkv][D], with the
+ *             token and head strides of pkv_rope_strides in elements (NULL: packed);
+ *             each a multiple of 8, so that the parts of a fused projection need no
+ *             copy.  Outputs may be the inputs (same pointer and strides) but must
+ *             not overlap them otherwise.
+ * Uses dims->num_q_heads (0: no queries, q and q_out may be NULL), num_kv_heads,
+ * head_dim (64 or 128), dtype and, for the append, block_size and num_blocks.
+ * Values are computed in fp32 and rounded once to T.
+ * Limits: rot_dim a multiple of 16 from 16 to head_dim; 1 to 4 axes; Hq + 2 Hkv at
+ * most 8192.
+ * ---------------------------------------------------------------------- */
+typedef struct pkv_rope {
+  int32_t rot_dim, num_axes, interleaved;
+  float factor;
+  uint64_t axis_bits[2];  /* two bits a frequency */
+  uint64_t turns[64];     /* turns per position, in units of 2^-64 */
+} pkv_rope;
+
+typedef struct pkv_rope_strides {
+  int64_t q_token, q_head, k_token, k_head, v_token, v_head;
+  int64_t q_out_token, q_out_head, k_out_token, k_out_head;
+} pkv_rope_strides;
+
+/* Host: fills *rope.  inv_freq: num_freqs = rot_dim / 2 frequencies (radians per
+ * position, finite; 8 to 64, a multiple of 8); axes: the axis of each, NULL for axis
+ * 0; factor multiplies sines and cosines (1 but for some context extensions). */
+int paged_kv_rope_init(pkv_rope* rope, const double* inv_freq, int32_t num_freqs, const int32_t* axes, int32_t num_axes,
+                       int32_t interleaved, double factor);
+
+/* Turns q and k into q_out and k_out: in front of a fused step
+ * (paged_decode_step and the other formats'), which appends k_out itself. */
+int paged_kv_rope(const void* q, const void* k, const int32_t* positions, int32_t num_tokens, const pkv_rope* rope,
+                  void* q_out, void* k_out, const pkv_rope_strides* strides, const pkv_dims* dims, void* stream);
+
+/* Turns q into q_out, and stores the turned k_new and v_new of token i at slot
+ * slot_mapping[i] of the caches: paged_kv_rope followed by paged_kv_append or, with
+ * k_scale and v_scale (E4M3 pools, float32[Hkv]), paged_kv_append_fp8, with the same
+ * results, slot rule and errors.  NULL scales: 16-bit pools of T. */
+int paged_kv_append_rope(const void* q, const void* k_new, const void* v_new, const int32_t* positions,
+                         const int32_t* slot_mapping, int32_t num_tokens, const pkv_rope* rope, void* q_out,
+                         void* k_cache, void* v_cache, const float* k_scale, const float* v_scale,
+                         const pkv_rope_strides* strides, const pkv_dims* dims, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Attention of chunks of new tokens (device): design.babushkai.com "GPU推論の内部構造",
+ * section "KVキャッシュの台帳" (chunked prefill), and its section "カーネル:
+ * FlashAttentionとメモリ階層" (tiled attention with a running softmax).  Whole prompts,
+ * their chunks and single tokens in one ragged batch, over 16-bit pools.
+ *
+ * q, out      : T[num_tokens][Hq][D]; sequence b's n_b = q_offsets[b + 1] -
+ *               q_offsets[b] rows start at q_offsets[b] (int32[num_seqs + 1], device,
+ *               as paged_kv_resize_tables writes token_offsets).
+ * context_lens[b] = L counts the new tokens, which sit at positions L - n_b .. L - 1
+ *               and are in the cache already (paged_kv_append_rope, paged_kv_append).
+ * Row i of sequence b attends to positions [0, L - n_b + i]; a row whose position
+ * would be negative (L < n_b) is zero.  Rows before q_offsets[0] and from
+ * q_offsets[num_seqs] on are left as they are.  Products run in T with fp32
+ * accumulation; softmax weights (below 2^8 times the largest) are rounded to T for
+ * their product with V, their sum is fp32.  Slots past a sequence's length, and for
+ * each row the positions it does not attend to, may hold anything, NaN and
+ * infinities too.
+ * workspace (device): paged_chunk_workspace_bytes(dims) bytes, 256-byte aligned;
+ * its contents need no initialisation.  Calls that share it must not overlap.
+ * Limits: dims as paged_decode_attention; at most 2048 sequences; num_seqs *
+ * num_kv_heads * num_tokens below 2^40.  Offsets that fall or leave [0, num_tokens]
+ * are flagged (PKV_ERR_OUT_OF_RANGE from paged_kv_check_status) and limited.
+ * ---------------------------------------------------------------------- */
+int paged_chunk_attention(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
+                          const int32_t* context_lens, const int32_t* q_offsets, int32_t num_tokens, float scale,
+                          void* out, void* workspace, size_t workspace_bytes, const pkv_dims* dims, void* stream);
+size_t paged_chunk_workspace_bytes(const pkv_dims* dims);
+
+/* ------------------------------------------------------------------------
+ * Block-sparse decode (device): a decode step that reads, of a long context, the
+ * blocks whose keys can give the largest logits.  youngju.dev "LLM サービング最適化
+ * 完全ガイド" and design.babushkai.com "GPU推論の内部構造" state that decode is bound by
+ * the bytes of the cache; the pages give no selection, this is the library's own.
+ *
+ * Bounds: for the n valid keys of a (block, KV head), every step in IEEE float32:
+ *   scale = max |K| * float32(1/127); upper[d] = ceil(max_t K[t][d] / scale), lower[d] =
+ *   floor(min_t K[t][d] / scale), limited to +-127 (0 where scale is 0).  If a
+ *   value is not finite: scale infinity, upper 127, lower -127 for every d.
+ *   bounds : int8[num_blocks][Hkv][2][D] (upper, lower); scales :
+ *   float32[num_blocks][Hkv].  Copies of blocks (copy-on-write) copy these too.
+ * Score of block j for KV head x, each query head h of its group having r =
+ *   max |q_h| * float32(1/127), c[d] = round_half_even(q_h[d] / r) (0 where r is 0, or
+ *   a query value is not finite): max over h of (S * scale) * r, two float32 products
+ *   of the whole number S = sum_d max(c[d] upper[d], c[d] lower[d]); a NaN counts as
+ *   +infinity.  The score does not depend on how it is computed.
+ * ---------------------------------------------------------------------- */
+
+/* Makes the bounds of every block that holds one of the new tokens (positions
+ * L - n .. L - 1 of each sequence) from all its valid keys.  q_offsets as
+ * paged_chunk_attention, with num_tokens an upper limit of q_offsets[num_seqs]; NULL:
+ * one new token each (num_tokens is not used).  Blocks further on keep what they
+ * have.  Two sequences that share a block must agree on its valid keys.  Offsets that
+ * fall or pass num_tokens are flagged (PKV_ERR_OUT_OF_RANGE), their sequence skipped. */
+int paged_kv_update_bounds(const void* k_cache, const int32_t* block_tables, const int32_t* context_lens,
+                           const int32_t* q_offsets, int32_t num_tokens, int8_t* bounds, float* scales,
+                           const pkv_dims* dims, void* stream);
+
+/* selected int32[num_seqs][Hkv][num_selected]: the logical blocks chosen for each
+ * (sequence, KV head), rising, -1 behind them.  The first sink_blocks and the last
+ * recent_blocks (>= 1) of a context are always among them, the others are those of
+ * the largest scores, the lowest block first among equals.  num_selected >= sink_blocks
+ * + recent_blocks; a context of fewer blocks has all of them.  q:
+ * T[num_seqs][Hq][D], one token each.  workspace (device):
+ * paged_select_workspace_bytes(dims) bytes, 256-byte aligned, without
+ * initialisation (NULL where max_blocks_per_seq <= num_selected).  At most 65535
+ * sequences and KV heads. */
+int paged_select_blocks(const void* q, const int8_t* bounds, const float* scales, const int32_t* block_tables,
+                        const int32_t* context_lens, int32_t num_selected, int32_t sink_blocks, int32_t recent_blocks,
+                        int32_t* selected, void* workspace, size_t workspace_bytes, const pkv_dims* dims, void* stream);
+size_t paged_select_workspace_bytes(const pkv_dims* dims);
+
+/* Decode attention as paged_decode_attention over the tokens of the listed blocks
+ * only: selected int32[num_seqs][Hkv][num_selected], logical blocks in any
+ * order; negative entries are passed over, one at or behind ceil(L / 16) too, and
+ * flagged (PKV_ERR_OUT_OF_RANGE).  A block listed twice counts twice.  No block: a zero
+ * row.  16-bit pools; no workspace. */
+int paged_decode_attention_sparse(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
+                                  const int32_t* context_lens, const int32_t* selected, int32_t num_selected, float scale,
+                                  void* out, const pkv_dims* dims, void* stream);
+
+/* ------------------------------------------------------------------------
  * Copy-on-write of shared blocks: kasblo.com "vLLMとは？", section
  * "block共有とAutomatic Prefix Caching" (a block carries a reference count, is
  * shared by several sequences, and is duplicated only when one of them must

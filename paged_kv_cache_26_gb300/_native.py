@@ -27,6 +27,17 @@ class PkvVerifyDims(ctypes.Structure):
                                                     "draft_row_stride")]
 
 
+class PkvRope(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_int32) for name in ("rot_dim", "num_axes", "interleaved")] + \
+               [("factor", ctypes.c_float), ("axis_bits", ctypes.c_uint64 * 2), ("turns", ctypes.c_uint64 * 64)]
+
+
+class PkvRopeStrides(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_int64) for name in (
+        "q_token", "q_head", "k_token", "k_head", "v_token", "v_head",
+        "q_out_token", "q_out_head", "k_out_token", "k_out_head")]
+
+
 class PkvEngineStats(ctypes.Structure):
     _fields_ = [(name, ctypes.c_int64) for name in (
         "steps", "sequence_steps", "context_tokens", "unused_tail_slots", "copied_blocks")]
@@ -94,6 +105,33 @@ _SIGNATURES = {
                                           ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                                           ctypes.POINTER(PkvVerifyDims), ctypes.c_void_p, ctypes.c_void_p,
                                           ctypes.c_void_p, ctypes.c_void_p]),
+    "paged_kv_rope_init": (ctypes.c_int, [ctypes.POINTER(PkvRope), ctypes.POINTER(ctypes.c_double), ctypes.c_int32,
+                                          c_int32_p, ctypes.c_int32, ctypes.c_int32, ctypes.c_double]),
+    "paged_kv_rope": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32,
+                                     ctypes.POINTER(PkvRope), ctypes.c_void_p, ctypes.c_void_p,
+                                     ctypes.POINTER(PkvRopeStrides), ctypes.POINTER(PkvDims), ctypes.c_void_p]),
+    "paged_kv_append_rope": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                            ctypes.c_void_p, ctypes.c_int32, ctypes.POINTER(PkvRope), ctypes.c_void_p,
+                                            ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                            ctypes.POINTER(PkvRopeStrides), ctypes.POINTER(PkvDims),
+                                            ctypes.c_void_p]),
+    "paged_chunk_attention": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                             ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_float,
+                                             ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t,
+                                             ctypes.POINTER(PkvDims), ctypes.c_void_p]),
+    "paged_chunk_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(PkvDims)]),
+    "paged_kv_update_bounds": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                              ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p,
+                                              ctypes.POINTER(PkvDims), ctypes.c_void_p]),
+    "paged_select_blocks": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                           ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
+                                           ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t,
+                                           ctypes.POINTER(PkvDims), ctypes.c_void_p]),
+    "paged_select_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(PkvDims)]),
+    "paged_decode_attention_sparse": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                                     ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                                     ctypes.c_int32, ctypes.c_float, ctypes.c_void_p,
+                                                     ctypes.POINTER(PkvDims), ctypes.c_void_p]),
     "paged_decode_attention_multi": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                                                     ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_float,
                                                     ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p,

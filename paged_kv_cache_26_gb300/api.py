@@ -11,7 +11,7 @@ from typing import Optional, Sequence
 import numpy as np
 import torch
 
-from ._native import PkvDims, PkvStepBuffers, PkvVerifyDims, c_int32_p, lib
+from ._native import PkvDims, PkvRope, PkvRopeStrides, PkvStepBuffers, PkvVerifyDims, c_int32_p, lib
 
 PKV_OK = 0
 PKV_ELEM_INT4 = -4  # paged_kv_copy_blocks' element size of a 4-bit pool
@@ -775,6 +775,349 @@ def paged_verify_draft(target_probs: torch.Tensor, draft_probs: Optional[torch.T
           (target_probs.data_ptr(), q, draft_tokens.data_ptr(), n, accept_u.data_ptr(), sample_u.data_ptr(), ctx,
            ctypes.byref(dims), accepted.data_ptr(), tokens.data_ptr(), lens_ptr))
     return accepted, tokens, lens
+
+
+# ---------------------------------------------------------------- prompts and long contexts
+
+def _empty(shape, dtype, stream, dev: int) -> torch.Tensor:
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with _allocating_on(stream, dev):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+class Rope:
+    """Rotary positions: made by make_rope, used by paged_kv_rope and
+    paged_kv_append_rope.  A plain host value; it holds no device memory."""
+
+    def __init__(self, value: PkvRope, head_dim: int):
+        self._value, self._ref = value, ctypes.byref(value)
+        self.head_dim, self.rot_dim, self.num_axes = head_dim, value.rot_dim, value.num_axes
+
+
+def make_rope(inv_freq: Sequence[float], head_dim: int, axes: Optional[Sequence[int]] = None,
+              interleaved: bool = False, factor: float = 1.0) -> Rope:
+    """Rotary positions of heads of head_dim dims whose first 2 * len(inv_freq) turn:
+    frequency f (radians per position) turns dims f and f + len(inv_freq), or 2f and
+    2f + 1 when interleaved.  axes: the position axis of every frequency (0 where not
+    given), from 0 to at most 3; factor multiplies sines and cosines."""
+    freqs = [float(x) for x in inv_freq]
+    n = len(freqs)
+    if 2 * n > head_dim:
+        raise ValueError(f"{n} frequencies turn {2 * n} dims, a head has {head_dim}")
+    axis = None
+    num_axes = 1
+    if axes is not None:
+        axis = [int(x) for x in axes]
+        if len(axis) != n:
+            raise ValueError("axes must name one axis for every frequency")
+        num_axes = max(axis, default=0) + 1
+    value = PkvRope()
+    _check(lib().paged_kv_rope_init(ctypes.byref(value), (ctypes.c_double * n)(*freqs), n,
+                                    (ctypes.c_int32 * n)(*axis) if axis is not None else None, num_axes,
+                                    1 if interleaved else 0, float(factor)), "paged_kv_rope_init")
+    return Rope(value, head_dim)
+
+
+def _rows(name: str, t: torch.Tensor, dev: int, dtype, tokens: int, d: int):
+    """(address, token stride, head stride) of rows [tokens][heads][d]."""
+    st = t.stride()
+    if not (t.get_device() == dev and t.dtype is dtype and t.dim() == 3 and t.shape[0] == tokens and t.shape[2] == d and
+            (st[2] == 1 or t.numel() == 0)):
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.get_device() != dev:
+            raise ValueError(f"{name} must be on device {dev} like the other tensors")
+        if t.dtype is not dtype:
+            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+        raise ValueError(f"{name} must be [num_tokens][heads][head_dim] with a unit stride along head_dim")
+    return t.data_ptr(), st[0], st[1]
+
+
+def _rope_positions(positions: torch.Tensor, rope: Rope, dev: int, tokens: int) -> None:
+    ps = positions.shape
+    if not (positions.get_device() == dev and positions.dtype is _i32 and positions.is_contiguous() and
+            (ps == (rope.num_axes, tokens) or (rope.num_axes == 1 and ps == (tokens,)))):
+        _explain(dev, ("positions", positions, _i32))
+        raise ValueError("positions must be [num_tokens], or [num_axes][num_tokens] of the rope's axes")
+
+
+def paged_kv_rope(q: Optional[torch.Tensor], k: torch.Tensor, positions: torch.Tensor, rope: Rope,
+                  q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None, stream=None):
+    """Turn q [T][Hq][D] and k [T][Hkv][D] (float16 or bfloat16; tokens and heads
+    may be strided, by multiples of 8) to their positions (int32 [T], or
+    [axes][T]), in front of a step that appends k.  q may be None.  Outputs may be
+    the inputs.  Returns (q_out, k_out)."""
+    dev, dtype = k.get_device(), k.dtype
+    code = _DTYPE_CODE.get(dtype)
+    if dev < 0 or code is None or k.dim() != 3 or k.shape[2] != rope.head_dim:
+        _need_strided("k", k)
+        raise ValueError(f"k must be float16 or bfloat16 [num_tokens][num_kv_heads][{rope.head_dim}]")
+    tokens, hk, d = k.shape
+    _rope_positions(positions, rope, dev, tokens)
+    if k_out is None:
+        k_out = _empty(k.shape, dtype, stream, dev)
+    if q is not None and q_out is None:
+        q_out = _empty(q.shape, dtype, stream, dev)
+    if q is None and q_out is not None:
+        raise ValueError("q_out without q")
+    if k_out.shape != k.shape or (q is not None and q_out.shape != q.shape):
+        raise ValueError("outputs must have the shapes of the inputs")
+    kp, kt, kh = _rows("k", k, dev, dtype, tokens, d)
+    op, ot, oh = _rows("k_out", k_out, dev, dtype, tokens, d)
+    qp = qt = qh = rp = rt = rh = hq = 0
+    if q is not None:
+        qp, qt, qh = _rows("q", q, dev, dtype, tokens, d)
+        rp, rt, rh = _rows("q_out", q_out, dev, dtype, tokens, d)
+        hq = q.shape[1]
+    if hk == 0:
+        raise ValueError("k has no heads")
+    dims = PkvDims(tokens, hq, hk, d, 16, 1, 0, code)
+    strides = PkvRopeStrides(qt, qh, kt, kh, 0, 0, rt, rh, ot, oh)
+    _call("paged_kv_rope", dev, stream, (qp, kp, positions.data_ptr(), tokens, rope._ref, rp, op, ctypes.byref(strides),
+                                         ctypes.byref(dims)))
+    return q_out, k_out
+
+
+def _need_strided(name: str, t: torch.Tensor) -> None:
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+
+
+def paged_kv_append_rope(q: Optional[torch.Tensor], k_new: torch.Tensor, v_new: torch.Tensor, positions: torch.Tensor,
+                         rope: Rope, slot_mapping: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                         k_scale: Optional[torch.Tensor] = None, v_scale: Optional[torch.Tensor] = None,
+                         q_out: Optional[torch.Tensor] = None, stream=None) -> Optional[torch.Tensor]:
+    """paged_kv_rope, then the append of the turned keys and of v_new at
+    slot_mapping, in one pass: into 16-bit caches [NB][Hkv][16][D] of the rows' type,
+    or with k_scale and v_scale (float32 [Hkv]) into E4M3 ones (uint8 or
+    float8_e4m3fn).  Rows may be strided as in paged_kv_rope (the parts of a fused
+    projection).  Returns q_out (None without q)."""
+    dev, dtype = k_new.get_device(), k_new.dtype
+    code, cs = _DTYPE_CODE.get(dtype), k_cache.shape
+    if not (dev >= 0 and code is not None and k_new.dim() == 3 and len(cs) == 4 and v_cache.shape == cs and
+            cs[1] == k_new.shape[1] and cs[3] == k_new.shape[2] == rope.head_dim and k_cache.get_device() == dev and
+            v_cache.get_device() == dev and k_cache.is_contiguous() and v_cache.is_contiguous() and
+            v_cache.dtype is k_cache.dtype and v_new.shape == k_new.shape and slot_mapping.get_device() == dev and
+            slot_mapping.dtype is _i32 and slot_mapping.is_contiguous() and slot_mapping.shape == k_new.shape[:1]):
+        _need_strided("k_new", k_new)
+        _explain(dev, ("k_cache", k_cache, None), ("v_cache", v_cache, k_cache.dtype),
+                 ("slot_mapping", slot_mapping, _i32))
+        raise ValueError("k_new / v_new must be float16 or bfloat16 [num_tokens][num_kv_heads][head_dim] matching the "
+                         "caches and the rope, slot_mapping [num_tokens]")
+    tokens, hk, d = k_new.shape
+    scales = [0, 0]
+    if k_scale is not None or v_scale is not None:
+        if k_cache.dtype not in (_u8, torch.float8_e4m3fn):
+            raise ValueError("scales belong to E4M3 caches (uint8 or float8_e4m3fn)")
+        for i, (n, t) in enumerate((("k_scale", k_scale), ("v_scale", v_scale))):
+            if t is None:
+                raise ValueError("give both k_scale and v_scale, or neither")
+            _explain(dev, (n, t, _f32))
+            if t.shape != (hk,):
+                raise ValueError(f"{n} must be [num_kv_heads]")
+            scales[i] = t.data_ptr()
+    elif k_cache.dtype is not dtype:
+        raise ValueError(f"k_cache must be {dtype} like the rows (or E4M3, with scales), got {k_cache.dtype}")
+    _rope_positions(positions, rope, dev, tokens)
+    kp, kt, kh = _rows("k_new", k_new, dev, dtype, tokens, d)
+    vp, vt, vh = _rows("v_new", v_new, dev, dtype, tokens, d)
+    qp = qt = qh = rp = rt = rh = hq = 0
+    if q is not None:
+        if q_out is None:
+            q_out = _empty(q.shape, dtype, stream, dev)
+        elif q_out.shape != q.shape:
+            raise ValueError("q_out must have q's shape")
+        qp, qt, qh = _rows("q", q, dev, dtype, tokens, d)
+        rp, rt, rh = _rows("q_out", q_out, dev, dtype, tokens, d)
+        hq = q.shape[1]
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    dims = PkvDims(tokens, hq, hk, d, cs[2], cs[0], 0, code)
+    strides = PkvRopeStrides(qt, qh, kt, kh, vt, vh, rt, rh, 0, 0)
+    _call("paged_kv_append_rope", dev, stream,
+          (qp, kp, vp, positions.data_ptr(), slot_mapping.data_ptr(), tokens, rope._ref, rp, k_cache.data_ptr(),
+           v_cache.data_ptr(), scales[0], scales[1], ctypes.byref(strides), ctypes.byref(dims)))
+    return q_out
+
+
+def _context_checks(q, caches, block_tables, context_lens, rows: int) -> int:
+    """Checks shared by the calls below: (q, caches) of one 16-bit type, the tables
+    and lengths of `rows` sequences (None: any), all on one device."""
+    dev, bt = caches[0].get_device(), block_tables.shape
+    dtype, cs = caches[0].dtype, caches[0].shape
+    if not (dev >= 0 and dtype in _DTYPE_CODE and all(c.get_device() == dev and c.dtype is dtype and c.is_contiguous() and
+                                                      c.shape == cs for c in caches) and len(cs) == 4 and
+            block_tables.get_device() == dev and context_lens.get_device() == dev and block_tables.dtype is _i32 and
+            context_lens.dtype is _i32 and block_tables.is_contiguous() and context_lens.is_contiguous() and
+            len(bt) == 2 and context_lens.shape == bt[:1] and (rows is None or rows == bt[0]) and
+            (q is None or (q.get_device() == dev and q.dtype is dtype and q.is_contiguous() and q.dim() == 3 and
+                           q.shape[2] == cs[3]))):
+        _need_cuda("caches", caches[0])
+        _explain(dev, ("caches", caches[-1], dtype), ("block_tables", block_tables, _i32),
+                 ("context_lens", context_lens, _i32), ("q", q, dtype))
+        raise ValueError("q must be [rows][num_q_heads][head_dim], the caches float16 or bfloat16 "
+                         "[num_blocks][num_kv_heads][16][head_dim], block_tables [num_seqs][max_blocks], context_lens "
+                         "[num_seqs]")
+    return dev
+
+
+def _context_dims(num_q_heads: int, k_cache, block_tables) -> PkvDims:
+    nb, hkv, bs, d = k_cache.shape
+    return PkvDims(block_tables.shape[0], num_q_heads, hkv, d, bs, nb, block_tables.shape[1], _DTYPE_CODE[k_cache.dtype])
+
+
+def _own_workspace(workspace, need: int, stream, dev: int):
+    """The caller's workspace, or one for this call; its bytes."""
+    if workspace is None:
+        workspace = _empty((need,), _u8, stream, dev) if need else None
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on device {dev} like the other tensors")
+    return (workspace.data_ptr(), workspace.numel() * workspace.element_size()) if workspace is not None else (0, 0)
+
+
+def _on_device(dev: int, f):
+    """f() with device dev current (sizes of workspaces depend on its SMs)."""
+    if dev == _current_device():
+        return f()
+    with torch.cuda.device(dev):
+        return f()
+
+
+def make_workspace_chunk(q: torch.Tensor, k_cache: torch.Tensor, block_tables: torch.Tensor) -> torch.Tensor:
+    """A workspace for paged_chunk_attention with these heads (any batch and any
+    number of tokens; its contents need no initialisation)."""
+    dims = _context_dims(q.shape[1], k_cache, block_tables)
+    need = _on_device(q.get_device(), lambda: int(lib().paged_chunk_workspace_bytes(ctypes.byref(dims))))
+    return torch.empty(need, dtype=_u8, device=q.device)
+
+
+def paged_chunk_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor,
+                          context_lens: torch.Tensor, q_offsets: torch.Tensor, scale: float,
+                          out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                          stream=None) -> torch.Tensor:
+    """Causal attention of a ragged batch of new tokens over their paged contexts.
+
+    q [T][Hq][D]: the new tokens of sequence b are rows q_offsets[b] ..
+    q_offsets[b + 1] - 1 (int32 [num_seqs + 1] on the device), at positions
+    context_lens[b] - n .. context_lens[b] - 1, and already in the caches.  Row i
+    attends to positions 0 .. its own.  Rows outside the offsets keep what out
+    holds.  Returns out."""
+    dev = _context_checks(q, (k_cache, v_cache), block_tables, context_lens, None)
+    if not (q_offsets.get_device() == dev and q_offsets.dtype is _i32 and q_offsets.is_contiguous() and
+            q_offsets.shape == (block_tables.shape[0] + 1,)):
+        _explain(dev, ("q_offsets", q_offsets, _i32))
+        raise ValueError("q_offsets must be [num_seqs + 1]")
+    if out is None:
+        out = _empty(q.shape, q.dtype, stream, dev)
+    elif not (out.get_device() == dev and out.dtype is q.dtype and out.is_contiguous() and out.shape == q.shape):
+        _explain(dev, ("out", out, q.dtype))
+        raise ValueError("out must have q's shape")
+    dims = _context_dims(q.shape[1], k_cache, block_tables)
+    need = 0
+    if workspace is None:
+        need = _on_device(dev, lambda: int(lib().paged_chunk_workspace_bytes(ctypes.byref(dims))))
+    ws, ws_bytes = _own_workspace(workspace, need, stream, dev)
+    _call("paged_chunk_attention", dev, stream,
+          (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(),
+           q_offsets.data_ptr(), q.shape[0], scale, out.data_ptr(), ws, ws_bytes, ctypes.byref(dims)))
+    return out
+
+
+def _check_bounds(bounds, scales, k_shape, dev: int) -> None:
+    nb, hk, _, d = k_shape
+    if not (bounds.get_device() == dev and bounds.dtype is torch.int8 and bounds.is_contiguous() and
+            bounds.shape == (nb, hk, 2, d) and scales.get_device() == dev and scales.dtype is _f32 and
+            scales.is_contiguous() and scales.shape == (nb, hk)):
+        _explain(dev, ("bounds", bounds, torch.int8), ("bound_scales", scales, _f32))
+        raise ValueError("bounds must be [num_blocks][num_kv_heads][2][head_dim], bound_scales [num_blocks][num_kv_heads]")
+
+
+def paged_kv_update_bounds(k_cache: torch.Tensor, block_tables: torch.Tensor, context_lens: torch.Tensor,
+                           bounds: torch.Tensor, bound_scales: torch.Tensor,
+                           q_offsets: Optional[torch.Tensor] = None, num_tokens: Optional[int] = None,
+                           stream=None) -> None:
+    """Make the bounds (int8 [NB][Hkv][2][D], upper and lower, with float32 scales
+    [NB][Hkv]) of the blocks that hold each sequence's new tokens, from all their
+    valid keys.  One new token each, or those of q_offsets (as paged_chunk_attention),
+    with num_tokens at least q_offsets[-1]."""
+    dev = _context_checks(None, (k_cache,), block_tables, context_lens, None)
+    _check_bounds(bounds, bound_scales, k_cache.shape, dev)
+    offsets = 0
+    if q_offsets is not None:
+        if num_tokens is None:
+            raise ValueError("q_offsets need num_tokens, an upper limit of the last")
+        if not (q_offsets.get_device() == dev and q_offsets.dtype is _i32 and q_offsets.is_contiguous() and
+                q_offsets.shape == (block_tables.shape[0] + 1,)):
+            _explain(dev, ("q_offsets", q_offsets, _i32))
+            raise ValueError("q_offsets must be [num_seqs + 1]")
+        offsets = q_offsets.data_ptr()
+    dims = _context_dims(k_cache.shape[1], k_cache, block_tables)
+    _call("paged_kv_update_bounds", dev, stream,
+          (k_cache.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), offsets, num_tokens or 0,
+           bounds.data_ptr(), bound_scales.data_ptr(), ctypes.byref(dims)))
+
+
+def paged_select_blocks(q: torch.Tensor, bounds: torch.Tensor, bound_scales: torch.Tensor, block_tables: torch.Tensor,
+                        context_lens: torch.Tensor, num_selected: int, sink_blocks: int = 1, recent_blocks: int = 1,
+                        selected: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                        stream=None) -> torch.Tensor:
+    """The logical blocks that a decode step of q [B][Hq][D] should attend to, for
+    every (sequence, KV head): the first sink_blocks, the last recent_blocks and
+    those whose bounds promise the largest logits, num_selected in all, rising,
+    -1 behind them: int32 [B][Hkv][num_selected]."""
+    dev, dtype, qs, bs, bt = q.get_device(), q.dtype, q.shape, bounds.shape, block_tables.shape
+    if not (dev >= 0 and dtype in _DTYPE_CODE and q.is_contiguous() and len(qs) == 3 and len(bs) == 4 and
+            qs[2] == bs[3] and block_tables.get_device() == dev and context_lens.get_device() == dev and
+            block_tables.dtype is _i32 and context_lens.dtype is _i32 and block_tables.is_contiguous() and
+            context_lens.is_contiguous() and len(bt) == 2 and bt[0] == qs[0] and context_lens.shape == (qs[0],)):
+        _need_cuda("q", q)
+        _explain(dev, ("block_tables", block_tables, _i32), ("context_lens", context_lens, _i32))
+        raise ValueError("q must be float16 or bfloat16 [num_seqs][num_q_heads][head_dim], bounds "
+                         "[num_blocks][num_kv_heads][2][head_dim], block_tables [num_seqs][max_blocks], context_lens "
+                         "[num_seqs]")
+    _check_bounds(bounds, bound_scales, (bs[0], bs[1], 16, bs[3]), dev)
+    shape = (qs[0], bs[1], num_selected)
+    if selected is None:
+        if num_selected < 1:
+            raise ValueError("num_selected must be at least 1")
+        selected = _empty(shape, _i32, stream, dev)
+    elif not (selected.get_device() == dev and selected.dtype is _i32 and selected.is_contiguous() and
+              selected.shape == shape):
+        _explain(dev, ("selected", selected, _i32))
+        raise ValueError("selected must be [num_seqs][num_kv_heads][num_selected]")
+    dims = PkvDims(qs[0], qs[1], bs[1], qs[2], 16, bs[0], bt[1], _DTYPE_CODE[dtype])
+    need = 0
+    if workspace is None and bt[1] > num_selected:
+        need = int(lib().paged_select_workspace_bytes(ctypes.byref(dims)))
+    ws, ws_bytes = _own_workspace(workspace, need, stream, dev)
+    _call("paged_select_blocks", dev, stream,
+          (q.data_ptr(), bounds.data_ptr(), bound_scales.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(),
+           num_selected, sink_blocks, recent_blocks, selected.data_ptr(), ws, ws_bytes, ctypes.byref(dims)))
+    return selected
+
+
+def paged_decode_attention_sparse(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                                  block_tables: torch.Tensor, context_lens: torch.Tensor, selected: torch.Tensor,
+                                  scale: float, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """paged_decode_attention over the tokens of the selected logical blocks only
+    (int32 [B][Hkv][n], as paged_select_blocks gives them; negative entries are
+    passed over).  Returns out."""
+    dev = _context_checks(q, (k_cache, v_cache), block_tables, context_lens, q.shape[0])
+    if not (selected.get_device() == dev and selected.dtype is _i32 and selected.is_contiguous() and
+            selected.dim() == 3 and selected.shape[:2] == (q.shape[0], k_cache.shape[1])):
+        _explain(dev, ("selected", selected, _i32))
+        raise ValueError("selected must be [num_seqs][num_kv_heads][num_selected]")
+    if out is None:
+        out = _empty(q.shape, q.dtype, stream, dev)
+    elif not (out.get_device() == dev and out.dtype is q.dtype and out.is_contiguous() and out.shape == q.shape):
+        _explain(dev, ("out", out, q.dtype))
+        raise ValueError("out must have q's shape")
+    dims = _context_dims(q.shape[1], k_cache, block_tables)
+    _call("paged_decode_attention_sparse", dev, stream,
+          (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(),
+           selected.data_ptr(), selected.shape[2], scale, out.data_ptr(), ctypes.byref(dims)))
+    return out
 
 
 def paged_kv_copy_blocks(k_cache: torch.Tensor, v_cache: torch.Tensor, block_pairs: torch.Tensor,

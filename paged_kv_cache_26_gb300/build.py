@@ -1,8 +1,8 @@
 """Builds libpagedkv.so in-tree with nvcc for sm_103a (GB300).
 
-Two translation units (the CUDA kernels + C ABI, and the host block
-allocator) are compiled in parallel and linked into one shared library next
-to this file.  The library is rebuilt only when a source or header is newer.
+The translation units (two of CUDA kernels with their C ABI, the host block
+allocator and the decode engine) are compiled in parallel and linked into one
+shared library next to this file.  The library is rebuilt only when a source or header is newer.
 """
 from __future__ import annotations
 
@@ -18,7 +18,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_PATH = os.path.join(PKG, "libpagedkv.so")
 
-SOURCES = ["paged_kv_api.cu", "block_allocator.cpp", "decode_engine.cpp"]
+SOURCES = ["paged_kv_api.cu", "long_context_api.cu", "block_allocator.cpp", "decode_engine.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 

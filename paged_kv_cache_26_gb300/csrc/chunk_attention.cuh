@@ -1,0 +1,899 @@
+// Attention of chunks of new tokens over a paged cache (sm_103a): causal, ragged,
+// any number of new tokens a sequence, on the fifth-generation tensor cores.
+//
+// A work unit is up to 256 query rows of one (sequence, KV head): the rows of
+// consecutive new tokens with their group of query heads packed (row = token * g +
+// head), as two tiles A and B of 128 rows (128 / g whole tokens each).  It walks its
+// keys in tiles of 128 tokens (eight blocks):
+//   S = Q K^T        M = 128 rows, N = 128 keys, from shared memory into TMEM
+//   P = 2^(S c - m)  in registers, one thread a row; m, the row's reference, moves
+//                    only when a score passes it by 2^8, so O is rarely rescaled
+//   O += P V         P from TMEM (over S's columns), O in TMEM, fp32
+// The tensor pipe alternates between the tiles, PV_A S_A' PV_B S_B', so that the
+// softmax of one tile runs under the products of the other.
+//
+// Work is divided by keys, not by units: the units' keys (plus a fixed amount for
+// a unit's start and end) form one line which is cut into equal parts, one per
+// CTA, one CTA per SM.  A part begins and ends inside units; such pieces leave
+// unnormalised fp32 partial results that merge_chunk_kernel joins in order.  Every
+// cut follows from the lengths alone: each kernel computes them for itself, from
+// closed sums, and nothing is counted or claimed at run time.
+//
+// Values that a row does not attend to may be anything.  Scores there are replaced,
+// not weighted.  A weight of 0 would still meet V in the product (0 * NaN = NaN), so
+// two warps go over V in the tiles where some row attends to less than all: rows
+// past the sequence become zeros, and if a value that later rows attend to is not
+// finite, the tile's P V is summed by the softmax threads instead, each row its own
+// tokens.
+//
+// Warps: 0-3 softmax of tile A, 4-7 of tile B, 8 TMA, 9 MMA, 10-11 V.
+// Every mbarrier wait is on a phase at most one ahead of the last completed one
+// (the V warps wait for a signal of the MMA warp for that reason) and gives up after
+// kWaitLimitNs.
+#pragma once
+
+#include "paged_kv_kernels.cuh"
+#include "tcgen05.cuh"
+
+namespace pkv {
+
+constexpr int kChunkKeys = 128;            // keys of a tile
+constexpr int kChunkRows = 256;            // query rows of a unit
+constexpr int kChunkThreads = 384;
+constexpr int kMaxChunkSeqs = 8192;
+constexpr int kChunkPieces = 4;            // pieces known ahead
+// A unit's start and end (first loads, first softmax, output) in keys, and the least
+// number of keys worth a CTA of its own.
+constexpr int kUnitKeys = 128;
+constexpr int kLeastKeys = 512;
+
+struct ChunkArgs {
+  void* out;
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  const int32_t* q_offsets;
+  float* part;              // [2 grid][256 * D + 512]: O, then m and l of every row
+  float c2;                 // |scale| * log2(e), at least the smallest float
+  int32_t negate;           // scale < 0: S is negated in the product
+  int32_t grid;             // CTAs of the main kernel
+  int32_t num_tokens, num_seqs, num_q_heads, num_kv_heads, group, max_blocks, num_blocks;
+  int32_t tile_tokens;      // tokens of a tile: 128 / group
+};
+
+template <int D>
+struct ChunkShape {
+  static constexpr int kHalfBytes = kChunkKeys * 128;        // 128 rows of 64 dims
+  static constexpr int kTileBytes = kChunkKeys * D * 2;
+  static constexpr int kSlots = D == 128 ? 5 : 10;           // ring of K and V tiles: 160 KB
+  static constexpr int kSmem = (2 + kSlots) * kTileBytes + 1024;
+  static constexpr int kSCol = 0, kOCol = 256;               // TMEM: S (and P) 128 columns a tile, then O
+  static constexpr int kTmemCols = 512;
+  static constexpr int64_t kPart = static_cast<int64_t>(kChunkRows) * (D + 2);  // floats of a partial result
+};
+
+// ------------------------------------------------------------------ the line of work
+
+// One sequence's share of the line.
+struct ChunkSeq {
+  int o0, n, ctx;  // first row, new tokens, context
+  int units;       // per KV head
+  int before;      // max(ctx - n, 0): keys before the chunk
+  int64_t line;    // length per KV head
+
+  // Where unit i starts, from the start of its (sequence, KV head).
+  __device__ __forceinline__ int64_t start(int i, int tt) const {
+    return static_cast<int64_t>(i) * (before + kUnitKeys) + static_cast<int64_t>(tt) * (static_cast<int64_t>(i) * (i + 1) / 2);
+  }
+};
+
+__device__ __forceinline__ ChunkSeq chunk_seq(const ChunkArgs& a, int b, bool flag) {
+  ChunkSeq s;
+  const int r0 = __ldg(a.q_offsets + b), r1 = __ldg(a.q_offsets + b + 1);
+  s.o0 = min(max(r0, 0), a.num_tokens);
+  const int o1 = min(max(r1, 0), a.num_tokens);
+  s.n = max(o1 - s.o0, 0);
+  if (flag && (r0 < 0 || r1 < r0 || r1 > a.num_tokens)) flag_error(kErrOffsets);
+  s.ctx = clamped_context(a.context_lens, b, a.max_blocks, flag);
+  const int tt = 2 * a.tile_tokens;
+  s.units = (s.n + tt - 1) / tt;
+  s.before = max(s.ctx - s.n, 0);
+  s.line = s.n > 0 ? s.start(s.units - 1, tt) + s.before + s.n + kUnitKeys : 0;
+  return s;
+}
+
+// What a CTA does of one unit.
+struct ChunkPiece {
+  int b, kvh;
+  int row0;        // first row of q
+  int tokens;      // of the unit, 1 .. 2 tile_tokens
+  int first;       // position of its first token (negative: the context is shorter than the chunk)
+  int ctx;
+  int t0, t1;      // key tiles of this piece
+  int kt[2];       // key tiles of the unit, for its tiles A and B
+  int slot;        // partial result, or -1: the piece is the whole unit
+  __device__ __forceinline__ int tiles() const { return max(kt[0], kt[1]); }
+  __device__ __forceinline__ int end(int q) const { return min(t1, kt[q]); }
+};
+
+// Position on the line, and a walk along it.
+struct ChunkWalk {
+  ChunkSeq s;
+  int b, kvh, unit;
+  int64_t unit_at;  // where the unit starts on the line
+  int64_t at, stop; // what is left of this CTA's part
+
+  __device__ __forceinline__ int64_t cost(int tt) const {
+    return min(static_cast<int64_t>(unit + 1) * tt, static_cast<int64_t>(s.n)) + s.before + kUnitKeys;
+  }
+  // The unit at `at`, which lies `rest` into sequence b.
+  __device__ __forceinline__ void locate(const ChunkArgs& a, int seq, int64_t rest, bool flag = false) {
+    const int tt = 2 * a.tile_tokens;
+    b = seq;
+    s = chunk_seq(a, b, flag);
+    kvh = static_cast<int>(rest / s.line);
+    rest -= kvh * s.line;
+    // start(i) <= rest: the root of a quadratic, corrected by a step or two.
+    const double p = s.before + kUnitKeys + 0.5 * tt;
+    int i = static_cast<int>((sqrt(p * p + 2.0 * tt * static_cast<double>(rest)) - p) / tt);
+    i = min(max(i, 0), s.units - 1);
+    while (i > 0 && s.start(i, tt) > rest) --i;
+    while (i + 1 < s.units && s.start(i + 1, tt) <= rest) ++i;
+    unit = i;
+    unit_at = at - (rest - s.start(i, tt));
+  }
+  __device__ __forceinline__ ChunkPiece describe(const ChunkArgs& a) const {
+    const int T = a.tile_tokens, tt = 2 * T;
+    ChunkPiece p;
+    p.b = b;
+    p.kvh = kvh;
+    p.row0 = s.o0 + unit * tt;
+    p.tokens = min(tt, s.n - unit * tt);
+    p.first = s.ctx - s.n + unit * tt;
+    p.ctx = s.ctx;
+    p.kt[0] = (max(p.first + min(p.tokens, T), 0) + kChunkKeys - 1) / kChunkKeys;
+    p.kt[1] = p.tokens > T ? (max(p.first + p.tokens, 0) + kChunkKeys - 1) / kChunkKeys : 0;
+    return p;
+  }
+  // The key tile at an offset of the line into the unit.
+  __device__ __forceinline__ static int tile_at(int64_t offset, int64_t cost, int tiles) {
+    return offset >= cost ? tiles : static_cast<int>(min(offset / kChunkKeys, static_cast<int64_t>(tiles)));
+  }
+  __device__ __forceinline__ void step(const ChunkArgs& a, int64_t unit_cost) {
+    unit_at += unit_cost;
+    if (++unit < s.units) return;
+    unit = 0;
+    if (++kvh < a.num_kv_heads) return;
+    kvh = 0;
+    while (++b < a.num_seqs) {
+      s = chunk_seq(a, b, false);
+      if (s.n > 0) return;
+    }
+  }
+  // The next piece of this CTA that has something to do.
+  __device__ __forceinline__ bool next(const ChunkArgs& a, int cta, ChunkPiece& p) {
+    const int tt = 2 * a.tile_tokens;
+    while (at < stop && b < a.num_seqs) {
+      p = describe(a);
+      const int64_t c = cost(tt), from = at - unit_at, to = min(stop - unit_at, c);
+      const int tiles = p.tiles();
+      p.t0 = tile_at(from, c, tiles);
+      p.t1 = tile_at(to, c, tiles);
+      p.slot = p.t0 == 0 && p.t1 == tiles ? -1 : p.t0 == 0 ? 2 * cta + 1 : 2 * cta;
+      at = unit_at + to;
+      if (to == c) step(a, c);
+      if (p.t0 < p.t1 || (tiles == 0 && from == 0)) return true;
+    }
+    return false;
+  }
+};
+
+// CTA c's part of a line of `total` for `parts` CTAs: [line_cut(c), line_cut(c + 1)).
+__device__ __forceinline__ int64_t line_cut(int64_t total, int parts, int c) {
+  return total / parts * c + total % parts * c / parts;
+}
+
+// By all threads of a CTA: the length of the line, and what lies before each
+// thread's run of sequences (in scratch, one int64 per warp).  Then `find` gives
+// the sequence at a place of the line.
+struct ChunkLine {
+  int64_t total;
+  int parts;
+  int64_t mine;    // line before this thread's sequences
+  int b0, b1;
+
+  __device__ __forceinline__ void measure(const ChunkArgs& a, int64_t* scratch, bool flag) {
+    const int nt = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (a.num_seqs + nt - 1) / nt;
+    b0 = min(tid * per, a.num_seqs);
+    b1 = min(b0 + per, a.num_seqs);
+    int64_t sum = 0;
+    for (int b = b0; b < b1; ++b) sum += chunk_seq(a, b, flag).line * a.num_kv_heads;
+    int64_t scan = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, scan, o);
+      if (lane >= o) scan += v;
+    }
+    if (lane == 31) scratch[warp] = scan;
+    __syncthreads();
+    int64_t before = 0;
+    total = 0;
+    for (int w = 0; w < nt / 32; ++w) {
+      const int64_t v = scratch[w];
+      if (w < warp) before += v;
+      total += v;
+    }
+    mine = before + scan - sum;
+    parts = static_cast<int>(max(static_cast<int64_t>(1), min(static_cast<int64_t>(a.grid), total / kLeastKeys)));
+  }
+  // The thread whose sequences hold place x of the line stores (sequence, rest).
+  __device__ __forceinline__ void find(const ChunkArgs& a, int64_t x, int64_t* found) const {
+    if (x < mine) return;
+    int64_t at = mine;
+    for (int b = b0; b < b1; ++b) {
+      const int64_t l = chunk_seq(a, b, false).line * a.num_kv_heads;
+      if (x < at + l) {
+        if (x >= at) {
+          found[0] = b;
+          found[1] = x - at;
+        }
+        return;
+      }
+      at += l;
+    }
+  }
+};
+
+// ------------------------------------------------------------------ small pieces
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// (x, y) = (x, y) * k + (c, c), each rounded once.
+__device__ __forceinline__ void scale2(float& x, float& y, float k, float c) {
+  asm("{\n\t.reg .b64 u, v, w;\n\tmov.b64 u, {%0, %1};\n\tmov.b64 v, {%2, %2};\n\tmov.b64 w, {%3, %3};\n\t"
+      "fma.rn.f32x2 u, u, v, w;\n\tmov.b64 {%0, %1}, u;\n\t}"
+      : "+f"(x), "+f"(y)
+      : "f"(k), "f"(c));
+}
+__device__ __forceinline__ void sum2(float& x, float& y, float a, float b) {
+  asm("{\n\t.reg .b64 u, v;\n\tmov.b64 u, {%0, %1};\n\tmov.b64 v, {%2, %3};\n\tadd.rn.f32x2 u, u, v;\n\t"
+      "mov.b64 {%0, %1}, u;\n\t}"
+      : "+f"(x), "+f"(y)
+      : "f"(a), "f"(b));
+}
+
+// 3-D tiled TMA load (dims, heads, tokens) of a box of queries.
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, int32_t z,
+                                            uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+
+// The same in two dimensions, for blocks of the pools: without a hint for L2,
+// where the CTAs of a (sequence, KV head) find each other's tiles.
+__device__ __forceinline__ void tma_load_rows(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+
+// Pool row of (block, KV head); a block outside the pool reads as zeros.
+__device__ __forceinline__ int chunk_pool_row(const ChunkArgs& a, int phys, int kvh) {
+  if (phys < 0 || phys >= a.num_blocks) {
+    flag_error(kErrBlockId);
+    return -kBlockSize;
+  }
+  return (phys * a.num_kv_heads + kvh) * kBlockSize;
+}
+
+// Whether one of a word's two values is infinite or NaN.
+template <typename T>
+__device__ __forceinline__ uint32_t not_finite2(uint32_t w) {
+  constexpr uint32_t kExp = MmaKind<T>::kBf16 ? 0x7f807f80u : 0x7c007c00u;
+  constexpr uint32_t kOne = MmaKind<T>::kBf16 ? 0x00800080u : 0x04000400u;
+  return ((w & kExp) + kOne) & 0x80008000u;
+}
+
+// The tile's P V of one row, by its thread: P (packed T) lies in TMEM at p, V in
+// shared memory, and only the row's first `vis` keys count.  For tiles with a value
+// that is not finite: out of line, and slow.
+template <typename T, int D>
+__device__ __noinline__ void chunk_row_product(uint32_t p, uint32_t o, const uint8_t* v, int vis, bool fresh) {
+#pragma unroll 1
+  for (int d = 0; d < D; d += 32) {
+    uint32_t acc[32];
+    if (fresh) {
+#pragma unroll
+      for (int k = 0; k < 32; ++k) acc[k] = 0;
+    } else {
+      tc::tmem_ld32(o + d, acc);
+      tc::tmem_wait_ld();
+    }
+#pragma unroll 1
+    for (int t0 = 0; t0 < kChunkKeys; t0 += 64) {
+      uint32_t pk[32];
+      tc::tmem_ld32(p + t0 / 2, pk);
+      tc::tmem_wait_ld();
+#pragma unroll
+      for (int t = 0; t < 64; ++t) {
+        if (t0 + t >= vis) continue;
+        const float2 w2 = unpack2<T>(pk[t >> 1]);
+        const float w = t & 1 ? w2.y : w2.x;
+        const uint8_t* row = v + (d >> 6) * ChunkShape<D>::kHalfBytes + (t0 + t) * 128;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const uint4 x = *reinterpret_cast<const uint4*>(row + ((((d & 63) >> 3) + c) ^ ((t0 + t) & 7)) * 16);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 f = unpack2<T>(word_of(x, i));
+            const int k = 8 * c + 2 * i;
+            acc[k] = __float_as_uint(fmaf(w, f.x, __uint_as_float(acc[k])));
+            acc[k + 1] = __float_as_uint(fmaf(w, f.y, __uint_as_float(acc[k + 1])));
+          }
+        }
+      }
+    }
+    __syncwarp();
+    tc::tmem_st32(o + d, acc);
+  }
+  tc::tmem_wait_st();
+}
+
+// ------------------------------------------------------------------ main kernel
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kChunkThreads, 1)
+    chunk_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
+                           const __grid_constant__ CUtensorMap tmap_v, const ChunkArgs a) {
+  using Shape = ChunkShape<D>;
+  constexpr int NS = Shape::kSlots;
+  constexpr bool kBf16 = MmaKind<T>::kBf16;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t kv_full[NS], kv_empty[NS];
+  __shared__ __align__(8) uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], v_go, v_clean, mma_fin;
+  __shared__ int64_t s_found[2];
+  __shared__ __align__(8) uint64_t piece_full[kChunkPieces], piece_empty[kChunkPieces];
+  __shared__ ChunkPiece s_piece[kChunkPieces];
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort, s_slow;
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* q_smem = base;
+  uint8_t* ring = base + 2 * Shape::kTileBytes;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(smem_u32(&kv_full[s]), 1);
+      mbar_init(smem_u32(&kv_empty[s]), 1);
+    }
+    for (int s = 0; s < kChunkPieces; ++s) {
+      mbar_init(smem_u32(&piece_full[s]), 1);
+      mbar_init(smem_u32(&piece_empty[s]), 1 + 2 + 8);  // the MMA warp, the V warps, the softmax warps
+    }
+    mbar_init(smem_u32(&q_full), 1);
+    mbar_init(smem_u32(&q_empty), 1);
+    for (int q = 0; q < 2; ++q) {
+      mbar_init(smem_u32(&s_full[q]), 1);
+      mbar_init(smem_u32(&p_full[q]), 4);
+      mbar_init(smem_u32(&o_full[q]), 1);
+    }
+    mbar_init(smem_u32(&v_go), 1);
+    mbar_init(smem_u32(&v_clean), 2);
+    mbar_init(smem_u32(&mma_fin), 1);
+    s_abort = 0;
+    s_slow = 0;
+    s_found[0] = -1;
+    fence_mbar_init();
+    prefetch_tensormap(&tmap_q);
+    prefetch_tensormap(&tmap_k);
+    prefetch_tensormap(&tmap_v);
+  }
+  if (warp == 9) {
+    tc::tmem_alloc(smem_u32(&s_tmem), Shape::kTmemCols);
+    tc::tmem_relinquish();
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int cta = blockIdx.x;
+  int64_t at = 0, stop = 0;  // this CTA's part of the line
+  {
+    ChunkLine line;
+    line.measure(a, reinterpret_cast<int64_t*>(ring), cta == 0);  // (the ring is not in use yet)
+    if (cta < line.parts) {
+      at = line_cut(line.total, line.parts, cta);
+      stop = line_cut(line.total, line.parts, cta + 1);
+    }
+    if (at < stop) line.find(a, at, s_found);
+  }
+  tc::fence_before_sync();
+  fence_proxy_async_smem();  // the scratch in the ring, before its first tile
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tbase = s_tmem;
+  volatile int* abort_flag = &s_abort;
+  // The other warps' next piece: where the TMA warp has put it, or null.  The slot
+  // is theirs until they release it.
+  uint32_t pieces = 0;
+  auto take = [&](bool whole_warp) -> const ChunkPiece* {
+    const uint32_t slot = pieces % kChunkPieces;
+    bool ok = mbar_wait(smem_u32(&piece_full[slot]), (pieces / kChunkPieces) & 1) && !*abort_flag;
+    if (whole_warp) ok = __all_sync(0xffffffffu, ok);
+    if (!ok) {
+      *abort_flag = 1;
+      return nullptr;
+    }
+    ++pieces;
+    return s_piece[slot].b >= 0 ? &s_piece[slot] : nullptr;
+  };
+  auto release = [&]() { mbar_arrive(smem_u32(&piece_empty[(pieces - 1) % kChunkPieces])); };
+
+  if (warp == 8) {
+    // ------------------------------------------------------------ TMA
+    ChunkWalk walk;
+    walk.at = at;
+    walk.stop = stop;
+    walk.b = a.num_seqs;
+    if (at < stop) walk.locate(a, static_cast<int>(s_found[0]), s_found[1]);
+    uint32_t it = 0;      // tiles issued
+    int loads = 0;        // of queries
+    bool ok = true;
+    for (bool last = false; ok && !last;) {
+      ChunkPiece p;
+      last = !walk.next(a, cta, p);
+      if (last) p.b = -1;
+      const uint32_t slot = pieces % kChunkPieces;
+      if (pieces >= kChunkPieces) ok = mbar_wait(smem_u32(&piece_empty[slot]), (pieces / kChunkPieces - 1) & 1);
+      ok = __all_sync(0xffffffffu, ok && !*abort_flag);
+      if (!ok) break;
+      if (lane == 0) {
+        s_piece[slot] = p;
+        mbar_arrive(smem_u32(&piece_full[slot]));
+      }
+      __syncwarp();
+      ++pieces;
+      if (last || p.t0 == p.t1) continue;
+      // Queries, once every S of the piece before is done.
+      if (loads > 0) ok = mbar_wait(smem_u32(&q_empty), (loads - 1) & 1);
+      ++loads;
+      ok = __all_sync(0xffffffffu, ok && !*abort_flag);
+      if (!ok) break;
+      if (lane == 0) {
+        const int tiles = p.t0 < p.kt[1] ? 2 : 1;
+        mbar_arrive_expect_tx(smem_u32(&q_full), tiles * (D / 64) * a.tile_tokens * a.group * 128);
+        for (int q = 0; q < tiles; ++q)
+#pragma unroll
+          for (int d = 0; d < D / 64; ++d)
+            tma_load_3d(smem_u32(q_smem) + q * Shape::kTileBytes + d * Shape::kHalfBytes, &tmap_q, 64 * d,
+                        p.kvh * a.group, p.row0 + q * a.tile_tokens, smem_u32(&q_full));
+      }
+      const int32_t* table = a.block_tables + static_cast<int64_t>(p.b) * a.max_blocks;
+      const int nblk = (p.ctx + kBlockSize - 1) / kBlockSize;
+      int win = -32, row = 0;
+      for (int t = p.t0; t < p.t1 && ok; ++t) {
+        const int blk = t * (kChunkKeys / kBlockSize);
+        if (blk >= win + 32) {
+          win = blk;
+          row = win + lane < nblk ? chunk_pool_row(a, __ldg(table + win + lane), p.kvh) : 0;
+        }
+        const int mine = __shfl_sync(0xffffffffu, row, blk - win + (lane & 7));
+        const int here = min(kChunkKeys / kBlockSize, nblk - blk);
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv, ++it) {  // K, then V
+          const int slot = it % NS;
+          if (it >= NS) ok = ok && mbar_wait(smem_u32(&kv_empty[slot]), (it / NS - 1) & 1);
+          ok = __all_sync(0xffffffffu, ok && !*abort_flag);
+          if (!ok) break;
+          const uint32_t bar = smem_u32(&kv_full[slot]);
+          const uint32_t dst = smem_u32(ring) + slot * Shape::kTileBytes;
+          if (lane == 0) mbar_arrive_expect_tx(bar, here * kBlockSize * D * 2);
+          __syncwarp();
+          if (lane < here)
+#pragma unroll
+            for (int d = 0; d < D / 64; ++d)
+              tma_load_rows(dst + d * Shape::kHalfBytes + lane * 2048, kv ? &tmap_v : &tmap_k, 64 * d, mine, bar);
+        }
+      }
+    }
+    if (!ok) {
+      *abort_flag = 1;
+      // No copy may still be landing in shared memory at exit.
+      if (loads > 0) mbar_wait(smem_u32(&q_full), (loads - 1) & 1);
+      for (uint32_t i = it > NS ? it - NS : 0; i < it; ++i) mbar_wait(smem_u32(&kv_full[i % NS]), (i / NS) & 1);
+    }
+  } else if (warp == 9) {
+    // ------------------------------------------------------------ MMA
+    if (lane == 0) {
+      const uint32_t idesc_s = tc::idesc_f16(kBf16, 128, kChunkKeys, false) | (a.negate ? 1u << 13 : 0u);
+      constexpr uint32_t idesc_o = tc::idesc_f16(kBf16, 128, D, true);
+      uint32_t it = 0;       // K and V tiles, as the TMA warp counts them
+      uint32_t np[2] = {0, 0}, nclean = 0;
+      int loads = 0;
+      bool ok = true;
+      auto full = [&](uint32_t i) { return mbar_wait(smem_u32(&kv_full[i % NS]), (i / NS) & 1); };
+      while (const ChunkPiece* next = take(false)) {
+        const ChunkPiece p = *next;
+        release();
+        if (p.t0 == p.t1) continue;
+        ok = mbar_wait(smem_u32(&q_full), loads & 1) && !*abort_flag;
+        ++loads;
+        if (!ok) break;
+        const int masked_from = max(p.first + 1, 0) / kChunkKeys;  // first tile that not every row sees whole
+        auto scores = [&](int q, uint32_t i) {
+          const uint32_t ks = smem_u32(ring) + (i % NS) * Shape::kTileBytes;
+          const uint32_t qs = smem_u32(q_smem) + q * Shape::kTileBytes;
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t off = (k >> 2) * Shape::kHalfBytes + (k & 3) * 32;
+            tc::mma_ss(tbase + Shape::kSCol + 128 * q, tc::smem_desc_sw128(qs + off, 16, 1024),
+                       tc::smem_desc_sw128(ks + off, 16, 1024), idesc_s, k > 0 ? 1u : 0u);
+          }
+          tc::mma_commit(smem_u32(&s_full[q]));
+        };
+        // After S of tile t: its V may be looked over.
+        auto signal = [&](int t, uint32_t i) {
+          if (t < masked_from) return true;
+          if (!full(i)) return false;
+          mbar_arrive(smem_u32(&v_go));
+          return true;
+        };
+        ok = full(it);
+        if (!ok) break;
+        tc::fence_after_sync();
+        for (int q = 0; q < 2; ++q)
+          if (p.t0 < p.kt[q]) scores(q, it);
+        tc::mma_commit(smem_u32(&kv_empty[it % NS]));
+        if (p.t0 + 1 == p.t1) tc::mma_commit(smem_u32(&q_empty));
+        ok = signal(p.t0, it + 1);
+        ++it;
+        for (int t = p.t0; t < p.t1 && ok; ++t) {
+          const uint32_t iv = it, ik = it + 1;  // V of this tile, K of the next
+          const uint32_t vs = smem_u32(ring) + (iv % NS) * Shape::kTileBytes;
+          ok = full(iv);
+          if (!ok) break;
+          bool slow = false;
+          if (t >= masked_from) {
+            ok = mbar_wait(smem_u32(&v_clean), nclean++ & 1);
+            if (!ok) break;
+            slow = *reinterpret_cast<volatile int*>(&s_slow) != 0;
+          }
+          const bool more = t + 1 < p.t1;
+          if (more) ok = full(ik);
+          for (int q = 0; q < 2 && ok; ++q) {
+            if (t < p.kt[q]) {
+              ok = mbar_wait(smem_u32(&p_full[q]), np[q]++ & 1) && !*abort_flag;
+              if (!ok) break;
+              tc::fence_after_sync();
+              if (!slow) {
+#pragma unroll
+                for (int k = 0; k < kChunkKeys / 16; ++k)
+                  tc::mma_ts(tbase + Shape::kOCol + D * q, tbase + Shape::kSCol + 128 * q + 8 * k,
+                             tc::smem_desc_sw128(vs + k * 2048, Shape::kHalfBytes, 1024), idesc_o,
+                             t > p.t0 || k > 0 ? 1u : 0u);
+              }
+              if (t + 1 == p.end(q)) tc::mma_commit(smem_u32(&o_full[q]));
+            }
+            if (more && t + 1 < p.kt[q]) scores(q, ik);
+          }
+          if (!ok) break;
+          tc::mma_commit(smem_u32(&kv_empty[iv % NS]));
+          ++it;
+          if (more) {
+            tc::mma_commit(smem_u32(&kv_empty[ik % NS]));
+            if (t + 2 == p.t1) tc::mma_commit(smem_u32(&q_empty));
+            ok = signal(t + 1, ik + 1);
+            ++it;
+          }
+        }
+        if (!ok) break;
+      }
+      if (!ok) *abort_flag = 1;
+      // No MMA may still be running when the CTA frees its TMEM.
+      tc::mma_commit(smem_u32(&mma_fin));
+      mbar_wait(smem_u32(&mma_fin), 0);
+    }
+    __syncwarp();
+  } else if (warp >= 10) {
+    // ------------------------------------------------------------ V of masked tiles
+    uint32_t it = 0, ngo = 0;
+    bool ok = true;
+    while (const ChunkPiece* next = take(true)) {
+      const int first = next->first, t0 = next->t0, t1 = next->t1, ctx = next->ctx;
+      __syncwarp();
+      if (lane == 0) release();
+      const int seen = max(first + 1, 0);  // keys that every row sees
+      for (int t = t0; t < t1; ++t, it += 2) {
+        if ((t + 1) * kChunkKeys <= seen) continue;
+        const uint32_t iv = it + 1;
+        ok = mbar_wait(smem_u32(&v_go), ngo++ & 1) && mbar_wait(smem_u32(&kv_full[iv % NS]), (iv / NS) & 1);
+        ok = __all_sync(0xffffffffu, ok && !*abort_flag);
+        if (!ok) break;
+        uint8_t* v = ring + (iv % NS) * Shape::kTileBytes;
+        const int from = max(seen - t * kChunkKeys, 0), valid = min(kChunkKeys, ctx - t * kChunkKeys);
+        const int me = (warp - 10) * 32 + lane;
+        uint32_t bad = 0;
+        // 16 bytes a thread, D / 8 threads a row.
+#pragma unroll 4
+        for (int i = from * (D / 8) + me; i < valid * (D / 8); i += 64) {
+          const int r = i / (D / 8), c = i % (D / 8);
+          const uint4 x = *reinterpret_cast<const uint4*>(v + (c >> 3) * Shape::kHalfBytes + r * 128 + (c & 7) * 16);
+          bad |= not_finite2<T>(x.x) | not_finite2<T>(x.y) | not_finite2<T>(x.z) | not_finite2<T>(x.w);
+        }
+        for (int i = valid * (D / 8) + me; i < kChunkKeys * (D / 8); i += 64) {
+          const int r = i / (D / 8), c = i % (D / 8);
+          *reinterpret_cast<uint4*>(v + (c >> 3) * Shape::kHalfBytes + r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+        // s_slow holds a bit for either warp.
+        const bool slow = __any_sync(0xffffffffu, bad != 0);
+        if (lane == 0) {
+          const int bit = 1 << (warp - 10);
+          if (slow)
+            atomicOr(&s_slow, bit);
+          else
+            atomicAnd(&s_slow, ~bit);
+          __threadfence_block();
+          mbar_arrive(smem_u32(&v_clean));
+        }
+        __syncwarp();
+      }
+      if (!ok) break;
+    }
+    if (!ok) *abort_flag = 1;
+  } else {
+    // ------------------------------------------------------------ softmax
+    const int q = warp >> 2;
+    const int r = threadIdx.x & 127;  // row of the tile = TMEM lane
+    const uint32_t lane_base = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+    const uint32_t s_addr = tbase + lane_base + Shape::kSCol + 128 * q;
+    const uint32_t o_addr = tbase + lane_base + Shape::kOCol + D * q;
+    const int tok = q * a.tile_tokens + r / a.group;  // token of the unit
+    const bool whole_row = r < a.tile_tokens * a.group;
+    const float c2 = a.c2;
+    uint32_t ns = 0, no = 0, nclean = 0;
+    uint32_t it = 0;  // K and V tiles before this piece
+    bool ok = true;
+    while (const ChunkPiece* next = take(true)) {
+      const ChunkPiece& p = *next;
+      const bool valid_row = whole_row && tok < p.tokens;
+      const int limit = valid_row ? p.first + tok : -1;  // last position the row attends to
+      const int seen = max(p.first + 1, 0);
+      const int t0 = p.t0, t1 = p.t1, kt = p.kt[q];
+      float m = -INFINITY, l = 0.f;
+      for (int t = t0; t < t1 && ok; ++t) {
+        const bool masked = (t + 1) * kChunkKeys > seen;
+        if (t >= kt) {  // the other tile's
+          if (masked) ++nclean;
+          continue;
+        }
+        ok = mbar_wait(smem_u32(&s_full[q]), ns++ & 1);
+        ok = __all_sync(0xffffffffu, ok && !*abort_flag);
+        if (!ok) break;
+        tc::fence_after_sync();
+        uint32_t x[4][32];  // scores, then weights, as their bits
+#pragma unroll
+        for (int j = 0; j < 4; ++j) tc::tmem_ld32(s_addr + 32 * j, x[j]);
+        tc::tmem_wait_ld();
+        const int vis = limit + 1 - t * kChunkKeys;
+        if (__any_sync(0xffffffffu, vis < kChunkKeys)) {
+#pragma unroll
+          for (int k = 0; k < 128; ++k) x[k >> 5][k & 31] = k < vis ? x[k >> 5][k & 31] : 0xff800000u;
+        }
+        float mx0 = -INFINITY, mx1 = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < 128; k += 4) {
+          const uint32_t* y = &x[k >> 5][k & 31];
+          mx0 = fmaxf(mx0, fmaxf(__uint_as_float(y[0]), __uint_as_float(y[1])));
+          mx1 = fmaxf(mx1, fmaxf(__uint_as_float(y[2]), __uint_as_float(y[3])));
+        }
+        const float mx = fmaxf(mx0, mx1) * c2;
+        // The reference moves when a score passes it by 2^8 (always for a first one).
+        const bool up = mx > m + 8.f;
+        if (__any_sync(0xffffffffu, up)) {
+          const float al = up ? exp2_approx(m - mx) : 1.f;
+          if (t > t0) {
+            // P V of the tiles before is done: S of this tile was issued after it.
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) {
+              uint32_t o[16];
+              tc::tmem_ld16(o_addr + 16 * j, o);
+              tc::tmem_wait_ld();
+#pragma unroll
+              for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * al);
+              tc::tmem_st16(o_addr + 16 * j, o);
+            }
+          }
+          l *= al;
+          if (up) m = mx;
+        }
+        const float nr = m == -INFINITY ? 0.f : -m;
+        float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int k = 0; k < 16; k += 2) {
+            float y[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) y[i] = __uint_as_float(x[j][2 * k + i]);
+            scale2(y[0], y[1], c2, nr);
+            scale2(y[2], y[3], c2, nr);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) y[i] = exp2_approx(y[i]);
+            sum2(l0, l1, y[0], y[1]);
+            sum2(l2, l3, y[2], y[3]);
+            // Weights rounded to T: 2^-9 (bf16) or 2^-12 (fp16) of each at most, beside an
+            // output rounded to T; two terms would double the product's work.
+            pk[k] = pack2<T>(y[0], y[1]);
+            pk[k + 1] = pack2<T>(y[2], y[3]);
+          }
+          tc::tmem_st16(s_addr + 16 * j, pk);
+        }
+        l += (l0 + l1) + (l2 + l3);
+        tc::tmem_wait_st();
+        if (masked) {
+          ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&v_clean), nclean++ & 1));
+          if (!ok) break;
+          if (*reinterpret_cast<volatile int*>(&s_slow) != 0) {
+            const uint32_t iv = it + 2 * (t - t0) + 1;
+            ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&kv_full[iv % NS]), (iv / NS) & 1));
+            if (!ok) break;
+            chunk_row_product<T, D>(s_addr, o_addr, ring + (iv % NS) * Shape::kTileBytes, vis, t == t0);
+          }
+        }
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&p_full[q]));
+      }
+      if (!ok) break;
+      it += 2 * (t1 - t0);
+      const bool any = t0 < kt;
+      if (any) {
+        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&o_full[q]), no++ & 1));
+        if (!ok) break;
+        tc::fence_after_sync();
+      }
+      const int64_t orow = (static_cast<int64_t>(p.row0) + tok) * a.num_q_heads + p.kvh * a.group + r % a.group;
+      const float inv = l == 0.f ? 0.f : 1.0f / l;  // nothing attended to: a zero row (a NaN stays one)
+      float* part = p.slot >= 0 ? a.part + p.slot * Shape::kPart : nullptr;
+#pragma unroll 1
+      for (int j = 0; j < D / 32; ++j) {
+        uint32_t o[32];
+        if (any) {
+          tc::tmem_ld32(o_addr + 32 * j, o);
+          tc::tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] = 0;
+        }
+        if (valid_row && p.slot < 0) {
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + orow * D + 32 * j);
+          float v[32];
+#pragma unroll
+          for (int k = 0; k < 32; ++k) v[k] = l == 0.f ? 0.f : __uint_as_float(o[k]) * inv;
+#pragma unroll
+          for (int k = 0; k < 32; k += 8)
+            dst[k / 8] = make_uint4(pack2<T>(v[k], v[k + 1]), pack2<T>(v[k + 2], v[k + 3]), pack2<T>(v[k + 4], v[k + 5]),
+                                    pack2<T>(v[k + 6], v[k + 7]));
+        } else if (valid_row) {
+          uint4* dst = reinterpret_cast<uint4*>(part + (q * 128 + r) * D + 32 * j);
+#pragma unroll
+          for (int k = 0; k < 32; k += 4) dst[k / 4] = make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+        }
+        __syncwarp();
+      }
+      if (part && valid_row) {
+        part[kChunkRows * D + q * 128 + r] = m;
+        part[kChunkRows * (D + 1) + q * 128 + r] = l;
+      }
+      tc::fence_before_sync();  // O has been read: the next piece's first product, after this row's next P, may write it
+      __syncwarp();
+      if (lane == 0) release();
+    }
+    if (!ok) *abort_flag = 1;
+  }
+
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == 9) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tbase, Shape::kTmemCols);
+  }
+}
+
+// ------------------------------------------------------------------ merge
+
+constexpr int kChunkMergeThreads = 256;
+constexpr int kChunkMergeRows = 32;
+
+// CTA (c, y) joins the pieces of the unit in which CTA c's part begins, if that is
+// the unit's first cut, for 32 of its rows, a warp a row.  The plan needs only the
+// lengths, and they are read before the main kernel is waited for only if it cannot
+// change them: it is its dependent, and the lengths were there before it.
+template <typename T, int D>
+__global__ void __launch_bounds__(kChunkMergeThreads) merge_chunk_kernel(const ChunkArgs a) {
+  using Shape = ChunkShape<D>;
+  __shared__ int64_t s_scratch[kChunkMergeThreads / 32];
+  __shared__ int64_t s_found[2];
+  const int c = blockIdx.x + 1;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  ChunkLine line;
+  line.measure(a, s_scratch, false);
+  if (c >= line.parts) return;
+  ChunkWalk w;
+  w.at = line_cut(line.total, line.parts, c);
+  line.find(a, w.at, s_found);
+  __syncthreads();
+  w.locate(a, static_cast<int>(s_found[0]), s_found[1]);
+  const ChunkPiece p = w.describe(a);
+  const int tiles = p.tiles();
+  const int64_t cost = w.cost(2 * a.tile_tokens);
+  auto cut = [&](int x) { return w.tile_at(line_cut(line.total, line.parts, x) - w.unit_at, cost, tiles); };
+  const int first = cut(c);
+  if (first == 0 || first == tiles) return;
+  const int64_t prev = line_cut(line.total, line.parts, c - 1) - w.unit_at;
+  if (prev > 0 && w.tile_at(prev, cost, tiles) > 0) return;  // an earlier cut's
+  // Pieces: [0, cut(c)) by CTA c - 1, then [cut(x), cut(x + 1)) by CTA x.
+  const int rows = p.tokens * a.group;
+  const int lane = threadIdx.x & 31;
+  const int r0 = blockIdx.y * kChunkMergeRows;
+  for (int i = threadIdx.x >> 5; i < kChunkMergeRows; i += kChunkMergeThreads / 32) {
+    const int rr = r0 + i;                                 // row of the unit, tokens packed
+    if (rr >= rows) break;
+    const int half = a.tile_tokens * a.group;              // rows of tile A
+    const int pr = rr < half ? rr : 128 + rr - half;       // its place in the partial results
+    float M = -INFINITY;
+    float L = 0.f;
+    float o[D / 32];
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k) o[k] = 0.f;
+    int from = 0, to = first;
+    for (int x = c - 1;;) {
+      if (from < to) {
+        const float* src = a.part + (from == 0 ? 2 * x + 1 : 2 * x) * Shape::kPart;
+        const float m = src[kChunkRows * D + pr], l = src[kChunkRows * (D + 1) + pr];
+        if (!(m == -INFINITY && l == 0.f)) {               // (tile A may have no keys in the last piece)
+          const float top = fmaxf(M, m);
+          const float wo = M == -INFINITY && L == 0.f ? 0.f : exp2f(M - top), wn = exp2f(m - top);
+          float v[D / 32];
+          if constexpr (D == 128) {
+            const float4 f = *reinterpret_cast<const float4*>(src + pr * D + 4 * lane);
+            v[0] = f.x;
+            v[1] = f.y;
+            v[2] = f.z;
+            v[3] = f.w;
+          } else {
+            const float2 f = *reinterpret_cast<const float2*>(src + pr * D + 2 * lane);
+            v[0] = f.x;
+            v[1] = f.y;
+          }
+          L = L * wo + l * wn;
+#pragma unroll
+          for (int k = 0; k < D / 32; ++k) o[k] = o[k] * wo + v[k] * wn;
+          M = top;
+        }
+      }
+      if (to == tiles) break;
+      ++x;
+      from = to;
+      to = x + 1 < line.parts ? cut(x + 1) : tiles;
+    }
+    const float inv = 1.0f / L;
+    const int64_t orow = (static_cast<int64_t>(p.row0) + rr / a.group) * a.num_q_heads + p.kvh * a.group + rr % a.group;
+    T* dst = static_cast<T*>(a.out) + orow * D + lane * (D / 32);
+#pragma unroll
+    for (int k = 0; k < D / 32; k += 2)
+      *reinterpret_cast<uint32_t*>(dst + k) = L == 0.f ? 0u : pack2<T>(o[k] * inv, o[k + 1] * inv);
+  }
+}
+
+}  // namespace pkv

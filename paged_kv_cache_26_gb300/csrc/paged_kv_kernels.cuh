@@ -50,7 +50,7 @@ constexpr int kMaxGroup = 8;  // query heads per KV head served by one mma tile
 
 // One thread copies one 16-byte chunk of one token's K row and the same chunk
 // of its V row for one KV head.  C = chunks per row = D * sizeof(T) / 16.
-__global__ void append_kernel(const uint4* __restrict__ k_new, const uint4* __restrict__ v_new,
+static __global__ void append_kernel(const uint4* __restrict__ k_new, const uint4* __restrict__ v_new,
                               const int32_t* __restrict__ slots, int32_t num_tokens, int32_t num_kv_heads,
                               int32_t chunks_per_row, int64_t num_slots, uint4* __restrict__ k_cache,
                               uint4* __restrict__ v_cache) {
@@ -79,7 +79,7 @@ __global__ void append_kernel(const uint4* __restrict__ k_new, const uint4* __re
 
 // The same copy with each sequence's slot derived from its table: token b goes
 // to position context_lens[b] - 1 (nothing when the context is empty).
-__global__ void append_at_end_kernel(const uint4* __restrict__ k_new, const uint4* __restrict__ v_new,
+static __global__ void append_at_end_kernel(const uint4* __restrict__ k_new, const uint4* __restrict__ v_new,
                                      const int32_t* __restrict__ block_tables,
                                      const int32_t* __restrict__ context_lens, int32_t num_seqs,
                                      int32_t max_blocks, int32_t num_kv_heads, int32_t chunks_per_row,
@@ -779,7 +779,7 @@ __device__ __forceinline__ void context_prefix(const DecodeArgs& a, const int32_
 
 // context_prefix from the staged lengths, for the rare rebuild after the grid
 // wait: kept out of line so that it costs the kernels no registers.
-__device__ __noinline__ void context_prefix_again(const DecodeArgs& a, int* s_P, int* s_ctx, int* s_warp_sum,
+static __device__ __noinline__ void context_prefix_again(const DecodeArgs& a, int* s_P, int* s_ctx, int* s_warp_sum,
                                                   int nthreads) {
   context_prefix(a, a.context_lens, s_P, s_ctx, s_warp_sum, nthreads, false);
 }

@@ -19,6 +19,8 @@ enum : unsigned {
   kErrNoBlocks = 32u, // table resize: more blocks wanted than the free list holds
   kErrFreeList = 64u, // table resize: the free list's count is outside the list
   kErrDraft = 128u,   // draft verification: a token or a draft length out of range
+  kErrOffsets = 256u, // ragged batches: offsets that fall, or lie outside the rows
+  kErrSelected = 512u, // block-sparse decode: a listed block behind the context
 };
 
 // A wait that has not finished after this long is treated as lost.
@@ -26,8 +28,8 @@ constexpr unsigned long long kWaitLimitNs = 1500ull * 1000ull * 1000ull;
 
 }  // namespace pkv
 
-// One word per device (module-scope device variable of this library).
-__device__ unsigned int g_pkv_error_word;
+// One word per device and translation unit; paged_kv_check_status reads them all.
+static __device__ unsigned int g_pkv_error_word;
 
 namespace pkv {
 

@@ -15,3 +15,7 @@ int decode_step_host_written(const void* q, const void* k_new, const void* v_new
                              const float* k_scale, const float* v_scale, bool int4, const int32_t* block_tables,
                              const int32_t* context_lens, float scale, void* out, void* workspace,
                              size_t workspace_bytes, const pkv_dims* dims, void* stream);
+
+// Reads and clears the error word of long_context_api.cu's kernels on the
+// current device; a cudaError_t.
+int pkv_long_context_error_word(unsigned* word);

@@ -1,0 +1,195 @@
+"""CPU model of how chunk attention divides its work: the same integer arithmetic
+as chunk_attention.cuh (ChunkSeq, ChunkWalk, ChunkLine, the merge's plan), checked
+for every key tile of every unit being done exactly once, every partial result
+written once and read once, and every cut unit merged exactly once."""
+import math
+import os
+import re
+
+import numpy as np
+import pytest
+
+SRC = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "paged_kv_cache_26_gb300",
+                        "csrc", "chunk_attention.cuh")).read()
+
+
+def constant(name):
+    return int(re.search(rf"constexpr int {name} = (\d+);", SRC).group(1))
+
+
+KEYS, UNIT_KEYS, LEAST = constant("kChunkKeys"), constant("kUnitKeys"), constant("kLeastKeys")
+
+
+class Seq:
+    def __init__(self, n, ctx, T):
+        self.n, self.ctx, self.T, self.tt = n, ctx, T, 2 * T
+        self.units = -(-n // self.tt)
+        self.before = max(ctx - n, 0)
+        self.line = self.start(self.units - 1) + self.before + n + UNIT_KEYS if n > 0 else 0
+
+    def start(self, i):
+        return i * (self.before + UNIT_KEYS) + self.tt * (i * (i + 1) // 2)
+
+    def cost(self, i):
+        return min((i + 1) * self.tt, self.n) + self.before + UNIT_KEYS
+
+    def tiles(self, i):
+        tokens, first = min(self.tt, self.n - i * self.tt), self.ctx - self.n + i * self.tt
+        a = -(-max(first + min(tokens, self.T), 0) // KEYS)
+        b = -(-max(first + tokens, 0) // KEYS) if tokens > self.T else 0
+        return a, b
+
+
+def tile_at(offset, cost, tiles):
+    return tiles if offset >= cost else min(offset // KEYS, tiles)
+
+
+def line_cut(total, parts, c):
+    return total // parts * c + total % parts * c // parts
+
+
+def locate(seqs, heads, x):
+    at = 0
+    for b, s in enumerate(seqs):
+        if x < at + s.line * heads:
+            rest = x - at
+            kvh, rest = divmod(rest, s.line)
+            p = s.before + UNIT_KEYS + 0.5 * s.tt
+            i = int((math.sqrt(p * p + 2.0 * s.tt * rest) - p) / s.tt)
+            i = min(max(i, 0), s.units - 1)
+            steps = 0
+            while i > 0 and s.start(i) > rest:
+                i, steps = i - 1, steps + 1
+            while i + 1 < s.units and s.start(i + 1) <= rest:
+                i, steps = i + 1, steps + 1
+            assert steps <= 2
+            return b, kvh, i, x - (rest - s.start(i))
+        at += s.line * heads
+    raise AssertionError("past the end of the line")
+
+
+def plan(new, ctx, heads, group, grid):
+    T = 128 // group
+    seqs = [Seq(n, c, T) for n, c in zip(new, ctx)]
+    total = sum(s.line * heads for s in seqs)
+    parts = max(1, min(grid, total // LEAST))
+    pieces = []                       # (cta, unit, t0, t1, slot)
+    for cta in range(parts):
+        at, stop = line_cut(total, parts, cta), line_cut(total, parts, cta + 1)
+        if at >= stop:
+            continue
+        b, kvh, i, unit_at = locate(seqs, heads, at)
+        while at < stop and b < len(seqs):
+            s = seqs[b]
+            cost, tiles = s.cost(i), max(s.tiles(i))
+            begin, end = at - unit_at, min(stop - unit_at, cost)
+            t0, t1 = tile_at(begin, cost, tiles), tile_at(end, cost, tiles)
+            slot = -1 if (t0, t1) == (0, tiles) else 2 * cta + 1 if t0 == 0 else 2 * cta
+            if t0 < t1 or (tiles == 0 and begin == 0):
+                pieces.append((cta, (b, kvh, i), t0, t1, slot))
+            at = unit_at + end
+            if end == cost:
+                unit_at += cost
+                i += 1
+                if i == s.units:
+                    i, kvh = 0, kvh + 1
+                    if kvh == heads:
+                        kvh, b = 0, b + 1
+                        while b < len(seqs) and seqs[b].n == 0:
+                            b += 1
+    return seqs, total, parts, pieces
+
+
+def merges(seqs, heads, total, parts):
+    """What every merge CTA reads: (unit, [(slot, t0, t1)])."""
+    for c in range(1, parts):
+        b, kvh, i, unit_at = locate(seqs, heads, line_cut(total, parts, c))
+        s = seqs[b]
+        cost, tiles = s.cost(i), max(s.tiles(i))
+
+        def cut(x):
+            return tile_at(line_cut(total, parts, x) - unit_at, cost, tiles)
+
+        first = cut(c)
+        if first in (0, tiles):
+            continue
+        prev = line_cut(total, parts, c - 1) - unit_at
+        if prev > 0 and tile_at(prev, cost, tiles) > 0:
+            continue
+        got, x, begin, end = [], c - 1, 0, first
+        while True:
+            if begin < end:
+                got.append((2 * x + 1 if begin == 0 else 2 * x, begin, end))
+            if end == tiles:
+                break
+            x += 1
+            begin, end = end, cut(x + 1) if x + 1 < parts else tiles
+        yield (b, kvh, i), got
+
+
+def check(new, ctx, heads, group, grid):
+    seqs, total, parts, pieces = plan(new, ctx, heads, group, grid)
+    done, slots = {}, {}
+    for cta, unit, t0, t1, slot in pieces:
+        done.setdefault(unit, []).append((t0, t1, slot))
+        if slot >= 0:
+            assert 0 <= slot < 2 * grid and slot not in slots
+            slots[slot] = (unit, t0, t1)
+    units = {(b, h, i) for b, s in enumerate(seqs) for h in range(heads) for i in range(s.units)}
+    assert set(done) == units
+    cut = set()
+    for unit, got in done.items():
+        tiles = max(seqs[unit[0]].tiles(unit[2]))
+        got.sort()
+        assert got[0][0] == 0 and got[-1][1] == tiles
+        assert all(x[1] == y[0] for x, y in zip(got, got[1:]))
+        assert (len(got) == 1) == (got[0][2] == -1)
+        if len(got) > 1:
+            cut.add(unit)
+    merged = list(merges(seqs, heads, total, parts))
+    assert {u for u, _ in merged} == cut and len(merged) == len(cut)
+    for unit, got in merged:
+        assert [(slots.pop(s)) for s, _, _ in got] == [(unit, a, b) for _, a, b in got]
+    assert not slots
+    return parts, pieces
+
+
+@pytest.mark.parametrize("group", range(1, 9))
+@pytest.mark.parametrize("grid", [1, 7, 152])
+def test_every_tile_once(group, grid):
+    rng = np.random.default_rng(group * 1000 + grid)
+    for trial in range(25):
+        B = int(rng.integers(1, 9))
+        kind = trial % 5
+        if kind == 0:
+            new, before = rng.integers(0, 4, B), rng.integers(0, 300, B)
+        elif kind == 1:
+            new, before = rng.integers(0, 700, B), np.zeros(B, int)
+        elif kind == 2:
+            new, before = rng.integers(1, 2, B), rng.integers(0, 40000, B)
+        elif kind == 3:
+            new, before = rng.integers(0, 300, B), rng.integers(0, 5000, B)
+        else:
+            new, before = rng.integers(0, 600, B), -rng.integers(0, 900, B)  # contexts shorter than the chunk
+        ctx = np.maximum(new + before, 0)
+        check(new.tolist(), ctx.tolist(), int(rng.integers(1, 9)), group, grid)
+
+
+def test_no_work():
+    for new, ctx in (([0], [0]), ([0, 0], [5, 0]), ([3], [0])):
+        check(new, ctx, 2, 4, 152)
+
+
+def test_far_lengths():
+    # a million keys and a long chunk: the root of the quadratic stays exact enough
+    check([20000, 1, 16384], [1 << 20, 1 << 20, (1 << 20) + 5], 2, 8, 152)
+    check([1 << 18], [1 << 21], 1, 3, 152)
+
+
+def test_balance():
+    """No CTA has more key tiles than its part of the line holds, plus one."""
+    seqs, total, parts, pieces = plan([2048], [65049], 8, 4, 152)
+    tiles = np.zeros(parts)
+    for cta, _, t0, t1, _ in pieces:
+        tiles[cta] += t1 - t0
+    assert tiles.max() <= total / parts / KEYS + 1
