@@ -10,7 +10,10 @@
 //                    only when a score passes it by 2^8, so O is rarely rescaled
 //   O += P V         P from TMEM (over S's columns), O in TMEM, fp32
 // The tensor pipe alternates between the tiles, PV_A S_A' PV_B S_B', so that the
-// softmax of one tile runs under the products of the other.
+// softmax of one tile runs under the products of the other.  Either tile has an
+// issuing warp of its own: an MMA waits in its thread until the tensor pipe can
+// queue it, and a barrier that is ready costs 100 to 200 cycles, which the pipe would
+// spend idle behind a single thread.
 //
 // Work is divided by keys, not by units: the units' keys (plus a fixed amount for
 // a unit's start and end) form one line which is cut into equal parts, one per
@@ -21,15 +24,15 @@
 //
 // Values that a row does not attend to may be anything.  Scores there are replaced,
 // not weighted.  A weight of 0 would still meet V in the product (0 * NaN = NaN), so
-// two warps go over V in the tiles where some row attends to less than all: rows
-// past the sequence become zeros, and if a value that later rows attend to is not
-// finite, the tile's P V is summed by the softmax threads instead, each row its own
-// tokens.
+// a warp between TMA and MMA goes over V in the tiles where some row attends to less
+// than all: rows past the sequence become zeros, and if a value that later rows
+// attend to is not finite, the tile's P V is summed by the softmax threads instead,
+// each row its own tokens.
 //
-// Warps: 0-3 softmax of tile A, 4-7 of tile B, 8 TMA, 9 MMA, 10-11 V.
-// Every mbarrier wait is on a phase at most one ahead of the last completed one
-// (the V warps wait for a signal of the MMA warp for that reason) and gives up after
-// kWaitLimitNs.
+// Warps: 0-3 softmax of tile A, 4-7 of tile B, 8 TMA, 9 and 10 MMA of A and B, 11 V.
+// Every wait is on a phase at most one ahead of the last completed one: the TMA,
+// V and MMA warps go through all tiles in order, a tile that concerns only one of
+// the MMA warps included.  Waits give up after kWaitLimitNs.
 #pragma once
 
 #include "paged_kv_kernels.cuh"
@@ -358,39 +361,37 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   constexpr int NS = Shape::kSlots;
   constexpr bool kBf16 = MmaKind<T>::kBf16;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t kv_full[NS], kv_empty[NS];
-  __shared__ __align__(8) uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], v_go, v_clean, mma_fin;
+  __shared__ __align__(8) uint64_t kv_full[NS], kv_ready[NS], kv_empty[NS];
+  __shared__ __align__(8) uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], mma_fin[2];
   __shared__ int64_t s_found[2];
   __shared__ __align__(8) uint64_t piece_full[kChunkPieces], piece_empty[kChunkPieces];
   __shared__ ChunkPiece s_piece[kChunkPieces];
   __shared__ uint32_t s_tmem;
-  __shared__ int s_abort, s_slow;
+  __shared__ int s_abort, s_slow[NS];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* q_smem = base;
   uint8_t* ring = base + 2 * Shape::kTileBytes;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS; ++s) {
       mbar_init(smem_u32(&kv_full[s]), 1);
-      mbar_init(smem_u32(&kv_empty[s]), 1);
+      mbar_init(smem_u32(&kv_ready[s]), 1);
+      mbar_init(smem_u32(&kv_empty[s]), 2);
     }
     for (int s = 0; s < kChunkPieces; ++s) {
       mbar_init(smem_u32(&piece_full[s]), 1);
-      mbar_init(smem_u32(&piece_empty[s]), 1 + 2 + 8);  // the MMA warp, the V warps, the softmax warps
+      mbar_init(smem_u32(&piece_empty[s]), 2 + 1 + 8);  // the MMA warps, the V warp, the softmax warps
     }
     mbar_init(smem_u32(&q_full), 1);
-    mbar_init(smem_u32(&q_empty), 1);
+    mbar_init(smem_u32(&q_empty), 2);
     for (int q = 0; q < 2; ++q) {
       mbar_init(smem_u32(&s_full[q]), 1);
       mbar_init(smem_u32(&p_full[q]), 4);
       mbar_init(smem_u32(&o_full[q]), 1);
+      mbar_init(smem_u32(&mma_fin[q]), 1);
     }
-    mbar_init(smem_u32(&v_go), 1);
-    mbar_init(smem_u32(&v_clean), 2);
-    mbar_init(smem_u32(&mma_fin), 1);
     s_abort = 0;
-    s_slow = 0;
     s_found[0] = -1;
     fence_mbar_init();
     prefetch_tensormap(&tmap_q);
@@ -436,219 +437,216 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   };
   auto release = [&]() { mbar_arrive(smem_u32(&piece_empty[(pieces - 1) % kChunkPieces])); };
 
-  if (warp == 8) {
-    // ------------------------------------------------------------ TMA
-    ChunkWalk walk;
-    walk.at = at;
-    walk.stop = stop;
-    walk.b = a.num_seqs;
-    if (at < stop) walk.locate(a, static_cast<int>(s_found[0]), s_found[1]);
-    uint32_t it = 0;      // tiles issued
-    int loads = 0;        // of queries
-    bool ok = true;
-    for (bool last = false; ok && !last;) {
-      ChunkPiece p;
-      last = !walk.next(a, cta, p);
-      if (last) p.b = -1;
-      const uint32_t slot = pieces % kChunkPieces;
-      if (pieces >= kChunkPieces) ok = mbar_wait(smem_u32(&piece_empty[slot]), (pieces / kChunkPieces - 1) & 1);
-      ok = __all_sync(0xffffffffu, ok && !*abort_flag);
-      if (!ok) break;
-      if (lane == 0) {
-        s_piece[slot] = p;
-        mbar_arrive(smem_u32(&piece_full[slot]));
-      }
-      __syncwarp();
-      ++pieces;
-      if (last || p.t0 == p.t1) continue;
-      // Queries, once every S of the piece before is done.
-      if (loads > 0) ok = mbar_wait(smem_u32(&q_empty), (loads - 1) & 1);
-      ++loads;
-      ok = __all_sync(0xffffffffu, ok && !*abort_flag);
-      if (!ok) break;
-      if (lane == 0) {
-        const int tiles = p.t0 < p.kt[1] ? 2 : 1;
-        mbar_arrive_expect_tx(smem_u32(&q_full), tiles * (D / 64) * a.tile_tokens * a.group * 128);
-        for (int q = 0; q < tiles; ++q)
-#pragma unroll
-          for (int d = 0; d < D / 64; ++d)
-            tma_load_3d(smem_u32(q_smem) + q * Shape::kTileBytes + d * Shape::kHalfBytes, &tmap_q, 64 * d,
-                        p.kvh * a.group, p.row0 + q * a.tile_tokens, smem_u32(&q_full));
-      }
-      const int32_t* table = a.block_tables + static_cast<int64_t>(p.b) * a.max_blocks;
-      const int nblk = (p.ctx + kBlockSize - 1) / kBlockSize;
-      int win = -32, row = 0;
-      for (int t = p.t0; t < p.t1 && ok; ++t) {
-        const int blk = t * (kChunkKeys / kBlockSize);
-        if (blk >= win + 32) {
-          win = blk;
-          row = win + lane < nblk ? chunk_pool_row(a, __ldg(table + win + lane), p.kvh) : 0;
+  // The launch's 384 x 168 registers are divided anew: 256 x 208 + 128 x 88.
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp == 8) {
+      // ------------------------------------------------------------ TMA
+      ChunkWalk walk;
+      walk.at = at;
+      walk.stop = stop;
+      walk.b = a.num_seqs;
+      if (at < stop) walk.locate(a, static_cast<int>(s_found[0]), s_found[1]);
+      uint32_t it = 0;      // tiles issued
+      int loads = 0;        // of queries
+      bool ok = true;
+      for (bool last = false; ok && !last;) {
+        ChunkPiece p;
+        last = !walk.next(a, cta, p);
+        if (last) p.b = -1;
+        const uint32_t slot = pieces % kChunkPieces;
+        if (pieces >= kChunkPieces) ok = mbar_wait(smem_u32(&piece_empty[slot]), (pieces / kChunkPieces - 1) & 1);
+        ok = __all_sync(0xffffffffu, ok && !*abort_flag);
+        if (!ok) break;
+        if (lane == 0) {
+          s_piece[slot] = p;
+          mbar_arrive(smem_u32(&piece_full[slot]));
         }
-        const int mine = __shfl_sync(0xffffffffu, row, blk - win + (lane & 7));
-        const int here = min(kChunkKeys / kBlockSize, nblk - blk);
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv, ++it) {  // K, then V
-          const int slot = it % NS;
-          if (it >= NS) ok = ok && mbar_wait(smem_u32(&kv_empty[slot]), (it / NS - 1) & 1);
-          ok = __all_sync(0xffffffffu, ok && !*abort_flag);
-          if (!ok) break;
-          const uint32_t bar = smem_u32(&kv_full[slot]);
-          const uint32_t dst = smem_u32(ring) + slot * Shape::kTileBytes;
-          if (lane == 0) mbar_arrive_expect_tx(bar, here * kBlockSize * D * 2);
-          __syncwarp();
-          if (lane < here)
+        __syncwarp();
+        ++pieces;
+        if (last || p.t0 == p.t1) continue;
+        // Queries, once every S of the piece before is done.
+        if (loads > 0) ok = mbar_wait(smem_u32(&q_empty), (loads - 1) & 1);
+        ++loads;
+        ok = __all_sync(0xffffffffu, ok && !*abort_flag);
+        if (!ok) break;
+        if (lane == 0) {
+          const int tiles = p.t0 < p.kt[1] ? 2 : 1;
+          mbar_arrive_expect_tx(smem_u32(&q_full), tiles * (D / 64) * a.tile_tokens * a.group * 128);
+          for (int q = 0; q < tiles; ++q)
 #pragma unroll
             for (int d = 0; d < D / 64; ++d)
-              tma_load_rows(dst + d * Shape::kHalfBytes + lane * 2048, kv ? &tmap_v : &tmap_k, 64 * d, mine, bar);
+              tma_load_3d(smem_u32(q_smem) + q * Shape::kTileBytes + d * Shape::kHalfBytes, &tmap_q, 64 * d,
+                          p.kvh * a.group, p.row0 + q * a.tile_tokens, smem_u32(&q_full));
+        }
+        const int32_t* table = a.block_tables + static_cast<int64_t>(p.b) * a.max_blocks;
+        const int nblk = (p.ctx + kBlockSize - 1) / kBlockSize;
+        int win = -32, row = 0;
+        for (int t = p.t0; t < p.t1 && ok; ++t) {
+          const int blk = t * (kChunkKeys / kBlockSize);
+          if (blk >= win + 32) {
+            win = blk;
+            row = win + lane < nblk ? chunk_pool_row(a, __ldg(table + win + lane), p.kvh) : 0;
+          }
+          const int mine = __shfl_sync(0xffffffffu, row, blk - win + (lane & 7));
+          const int here = min(kChunkKeys / kBlockSize, nblk - blk);
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv, ++it) {  // K, then V
+            const int slot = it % NS;
+            if (it >= NS) ok = ok && mbar_wait(smem_u32(&kv_empty[slot]), (it / NS - 1) & 1);
+            ok = __all_sync(0xffffffffu, ok && !*abort_flag);
+            if (!ok) break;
+            const uint32_t bar = smem_u32(&kv_full[slot]);
+            const uint32_t dst = smem_u32(ring) + slot * Shape::kTileBytes;
+            if (lane == 0) mbar_arrive_expect_tx(bar, here * kBlockSize * D * 2);
+            __syncwarp();
+            if (lane < here)
+#pragma unroll
+              for (int d = 0; d < D / 64; ++d)
+                tma_load_rows(dst + d * Shape::kHalfBytes + lane * 2048, kv ? &tmap_v : &tmap_k, 64 * d, mine, bar);
+          }
         }
       }
-    }
-    if (!ok) {
-      *abort_flag = 1;
-      // No copy may still be landing in shared memory at exit.
-      if (loads > 0) mbar_wait(smem_u32(&q_full), (loads - 1) & 1);
-      for (uint32_t i = it > NS ? it - NS : 0; i < it; ++i) mbar_wait(smem_u32(&kv_full[i % NS]), (i / NS) & 1);
-    }
-  } else if (warp == 9) {
-    // ------------------------------------------------------------ MMA
-    if (lane == 0) {
-      const uint32_t idesc_s = tc::idesc_f16(kBf16, 128, kChunkKeys, false) | (a.negate ? 1u << 13 : 0u);
-      constexpr uint32_t idesc_o = tc::idesc_f16(kBf16, 128, D, true);
-      uint32_t it = 0;       // K and V tiles, as the TMA warp counts them
-      uint32_t np[2] = {0, 0}, nclean = 0;
-      int loads = 0;
-      bool ok = true;
-      auto full = [&](uint32_t i) { return mbar_wait(smem_u32(&kv_full[i % NS]), (i / NS) & 1); };
-      while (const ChunkPiece* next = take(false)) {
-        const ChunkPiece p = *next;
-        release();
-        if (p.t0 == p.t1) continue;
-        ok = mbar_wait(smem_u32(&q_full), loads & 1) && !*abort_flag;
-        ++loads;
-        if (!ok) break;
-        const int masked_from = max(p.first + 1, 0) / kChunkKeys;  // first tile that not every row sees whole
-        auto scores = [&](int q, uint32_t i) {
-          const uint32_t ks = smem_u32(ring) + (i % NS) * Shape::kTileBytes;
-          const uint32_t qs = smem_u32(q_smem) + q * Shape::kTileBytes;
+      if (!ok) {
+        *abort_flag = 1;
+        // No copy may still be landing in shared memory at exit.
+        if (loads > 0) mbar_wait(smem_u32(&q_full), (loads - 1) & 1);
+        for (uint32_t i = it > NS ? it - NS : 0; i < it; ++i) mbar_wait(smem_u32(&kv_full[i % NS]), (i / NS) & 1);
+      }
+    } else if (warp < 11) {
+      // ------------------------------------------------------------ MMA of one tile
+      if (lane == 0) {
+        const int q = warp - 9;
+        const uint32_t idesc_s = tc::idesc_f16(kBf16, 128, kChunkKeys, false) | (a.negate ? 1u << 13 : 0u);
+        constexpr uint32_t idesc_o = tc::idesc_f16(kBf16, 128, D, true);
+        const uint32_t s_col = tbase + Shape::kSCol + 128 * q, o_col = tbase + Shape::kOCol + D * q;
+        const uint64_t q_desc = tc::smem_desc_sw128(smem_u32(q_smem) + q * Shape::kTileBytes, 16, 1024);
+        uint32_t slot = 0, phase = 0;  // of the next K or V tile, as the TMA warp counts them
+        uint32_t np = 0, loads = 0;
+        bool ok = true;
+        auto advance = [&]() {
+          if (++slot == NS) {
+            slot = 0;
+            phase ^= 1;
+          }
+        };
+        auto ready = [&]() { return mbar_wait(smem_u32(&kv_ready[slot]), phase); };
+        while (const ChunkPiece* next = take(false)) {
+          const int t0 = next->t0, t1 = next->t1, kt = next->kt[q];
+          release();
+          if (t0 == t1) continue;
+          ok = mbar_wait(smem_u32(&q_full), loads++ & 1);
+          // S of the tile whose K is in the slot; the slot is done with after it.
+          auto scores = [&](int t) {
+            if (t < kt) {
+              const uint64_t k_desc = tc::smem_desc_sw128(smem_u32(ring) + slot * Shape::kTileBytes, 16, 1024);
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint32_t off = (k >> 2) * Shape::kHalfBytes + (k & 3) * 32;
-            tc::mma_ss(tbase + Shape::kSCol + 128 * q, tc::smem_desc_sw128(qs + off, 16, 1024),
-                       tc::smem_desc_sw128(ks + off, 16, 1024), idesc_s, k > 0 ? 1u : 0u);
-          }
-          tc::mma_commit(smem_u32(&s_full[q]));
-        };
-        // After S of tile t: its V may be looked over.
-        auto signal = [&](int t, uint32_t i) {
-          if (t < masked_from) return true;
-          if (!full(i)) return false;
-          mbar_arrive(smem_u32(&v_go));
-          return true;
-        };
-        ok = full(it);
-        if (!ok) break;
-        tc::fence_after_sync();
-        for (int q = 0; q < 2; ++q)
-          if (p.t0 < p.kt[q]) scores(q, it);
-        tc::mma_commit(smem_u32(&kv_empty[it % NS]));
-        if (p.t0 + 1 == p.t1) tc::mma_commit(smem_u32(&q_empty));
-        ok = signal(p.t0, it + 1);
-        ++it;
-        for (int t = p.t0; t < p.t1 && ok; ++t) {
-          const uint32_t iv = it, ik = it + 1;  // V of this tile, K of the next
-          const uint32_t vs = smem_u32(ring) + (iv % NS) * Shape::kTileBytes;
-          ok = full(iv);
+              for (int k = 0; k < D / 16; ++k) {
+                const uint32_t off = ((k >> 2) * Shape::kHalfBytes + (k & 3) * 32) >> 4;
+                tc::mma_ss(s_col, q_desc + off, k_desc + off, idesc_s, k > 0 ? 1u : 0u);
+              }
+              tc::mma_commit(smem_u32(&s_full[q]));
+              tc::mma_commit(smem_u32(&kv_empty[slot]));
+            } else {
+              mbar_arrive(smem_u32(&kv_empty[slot]));
+            }
+            advance();
+            if (t + 1 == t1) {
+              if (t0 < kt)
+                tc::mma_commit(smem_u32(&q_empty));
+              else
+                mbar_arrive(smem_u32(&q_empty));
+            }
+          };
+          ok = ok && ready();
           if (!ok) break;
-          bool slow = false;
-          if (t >= masked_from) {
-            ok = mbar_wait(smem_u32(&v_clean), nclean++ & 1);
+          tc::fence_after_sync();
+          scores(t0);
+          for (int t = t0; t < t1; ++t) {
+            ok = ready();
             if (!ok) break;
-            slow = *reinterpret_cast<volatile int*>(&s_slow) != 0;
-          }
-          const bool more = t + 1 < p.t1;
-          if (more) ok = full(ik);
-          for (int q = 0; q < 2 && ok; ++q) {
-            if (t < p.kt[q]) {
-              ok = mbar_wait(smem_u32(&p_full[q]), np[q]++ & 1) && !*abort_flag;
+            const uint32_t vslot = slot;
+            const bool slow = *reinterpret_cast<volatile int*>(&s_slow[slot]) != 0;
+            advance();
+            if (t < kt) {
+              ok = mbar_wait(smem_u32(&p_full[q]), np++ & 1);
               if (!ok) break;
               tc::fence_after_sync();
               if (!slow) {
+                const uint64_t v_desc =
+                    tc::smem_desc_sw128(smem_u32(ring) + vslot * Shape::kTileBytes, Shape::kHalfBytes, 1024);
 #pragma unroll
                 for (int k = 0; k < kChunkKeys / 16; ++k)
-                  tc::mma_ts(tbase + Shape::kOCol + D * q, tbase + Shape::kSCol + 128 * q + 8 * k,
-                             tc::smem_desc_sw128(vs + k * 2048, Shape::kHalfBytes, 1024), idesc_o,
-                             t > p.t0 || k > 0 ? 1u : 0u);
+                  tc::mma_ts(o_col, s_col + 8 * k, v_desc + (k * 2048 >> 4), idesc_o, t > t0 || k > 0 ? 1u : 0u);
               }
-              if (t + 1 == p.end(q)) tc::mma_commit(smem_u32(&o_full[q]));
+              if (t + 1 == min(t1, kt)) tc::mma_commit(smem_u32(&o_full[q]));
+              tc::mma_commit(smem_u32(&kv_empty[vslot]));
+            } else {
+              mbar_arrive(smem_u32(&kv_empty[vslot]));
             }
-            if (more && t + 1 < p.kt[q]) scores(q, ik);
+            if (t + 1 < t1) {
+              ok = ready();
+              if (!ok) break;
+              scores(t + 1);
+            }
           }
+          if (!ok || *abort_flag) break;
+        }
+        if (!ok) *abort_flag = 1;
+        // No MMA may still be running when the CTA frees its TMEM.
+        tc::mma_commit(smem_u32(&mma_fin[q]));
+        mbar_wait(smem_u32(&mma_fin[q]), 0);
+      }
+      __syncwarp();
+    } else {
+      // ------------------------------------------------------------ V of masked tiles
+      uint32_t slot = 0, phase = 0;
+      bool ok = true;
+      while (const ChunkPiece* next = take(true)) {
+        const int first = next->first, t0 = next->t0, t1 = next->t1, ctx = next->ctx;
+        __syncwarp();
+        if (lane == 0) release();
+        const int seen = max(first + 1, 0);  // keys that every row sees
+        for (int i = 2 * t0; i < 2 * t1; ++i) {  // K, then V of a tile
+          const int t = i >> 1;
+          ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&kv_full[slot]), phase) && !*abort_flag);
           if (!ok) break;
-          tc::mma_commit(smem_u32(&kv_empty[iv % NS]));
-          ++it;
-          if (more) {
-            tc::mma_commit(smem_u32(&kv_empty[ik % NS]));
-            if (t + 2 == p.t1) tc::mma_commit(smem_u32(&q_empty));
-            ok = signal(t + 1, ik + 1);
-            ++it;
+          bool slow = false;
+          if ((i & 1) && (t + 1) * kChunkKeys > seen) {
+            uint8_t* v = ring + slot * Shape::kTileBytes;
+            const int from = max(seen - t * kChunkKeys, 0), valid = min(kChunkKeys, ctx - t * kChunkKeys);
+            uint32_t bad = 0;
+            // 16 bytes a lane, D / 8 lanes a row.
+#pragma unroll 4
+            for (int x = from * (D / 8) + lane; x < valid * (D / 8); x += 32) {
+              const int r = x / (D / 8), c = x % (D / 8);
+              const uint4 w = *reinterpret_cast<const uint4*>(v + (c >> 3) * Shape::kHalfBytes + r * 128 + (c & 7) * 16);
+              bad |= not_finite2<T>(w.x) | not_finite2<T>(w.y) | not_finite2<T>(w.z) | not_finite2<T>(w.w);
+            }
+            for (int x = valid * (D / 8) + lane; x < kChunkKeys * (D / 8); x += 32) {
+              const int r = x / (D / 8), c = x % (D / 8);
+              *reinterpret_cast<uint4*>(v + (c >> 3) * Shape::kHalfBytes + r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+            slow = __any_sync(0xffffffffu, bad != 0);
+          }
+          __syncwarp();
+          if (lane == 0) {
+            s_slow[slot] = slow;
+            mbar_arrive(smem_u32(&kv_ready[slot]));
+          }
+          __syncwarp();
+          if (++slot == NS) {
+            slot = 0;
+            phase ^= 1;
           }
         }
         if (!ok) break;
       }
       if (!ok) *abort_flag = 1;
-      // No MMA may still be running when the CTA frees its TMEM.
-      tc::mma_commit(smem_u32(&mma_fin));
-      mbar_wait(smem_u32(&mma_fin), 0);
     }
-    __syncwarp();
-  } else if (warp >= 10) {
-    // ------------------------------------------------------------ V of masked tiles
-    uint32_t it = 0, ngo = 0;
-    bool ok = true;
-    while (const ChunkPiece* next = take(true)) {
-      const int first = next->first, t0 = next->t0, t1 = next->t1, ctx = next->ctx;
-      __syncwarp();
-      if (lane == 0) release();
-      const int seen = max(first + 1, 0);  // keys that every row sees
-      for (int t = t0; t < t1; ++t, it += 2) {
-        if ((t + 1) * kChunkKeys <= seen) continue;
-        const uint32_t iv = it + 1;
-        ok = mbar_wait(smem_u32(&v_go), ngo++ & 1) && mbar_wait(smem_u32(&kv_full[iv % NS]), (iv / NS) & 1);
-        ok = __all_sync(0xffffffffu, ok && !*abort_flag);
-        if (!ok) break;
-        uint8_t* v = ring + (iv % NS) * Shape::kTileBytes;
-        const int from = max(seen - t * kChunkKeys, 0), valid = min(kChunkKeys, ctx - t * kChunkKeys);
-        const int me = (warp - 10) * 32 + lane;
-        uint32_t bad = 0;
-        // 16 bytes a thread, D / 8 threads a row.
-#pragma unroll 4
-        for (int i = from * (D / 8) + me; i < valid * (D / 8); i += 64) {
-          const int r = i / (D / 8), c = i % (D / 8);
-          const uint4 x = *reinterpret_cast<const uint4*>(v + (c >> 3) * Shape::kHalfBytes + r * 128 + (c & 7) * 16);
-          bad |= not_finite2<T>(x.x) | not_finite2<T>(x.y) | not_finite2<T>(x.z) | not_finite2<T>(x.w);
-        }
-        for (int i = valid * (D / 8) + me; i < kChunkKeys * (D / 8); i += 64) {
-          const int r = i / (D / 8), c = i % (D / 8);
-          *reinterpret_cast<uint4*>(v + (c >> 3) * Shape::kHalfBytes + r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
-        }
-        fence_proxy_async_smem();
-        // s_slow holds a bit for either warp.
-        const bool slow = __any_sync(0xffffffffu, bad != 0);
-        if (lane == 0) {
-          const int bit = 1 << (warp - 10);
-          if (slow)
-            atomicOr(&s_slow, bit);
-          else
-            atomicAnd(&s_slow, ~bit);
-          __threadfence_block();
-          mbar_arrive(smem_u32(&v_clean));
-        }
-        __syncwarp();
-      }
-      if (!ok) break;
-    }
-    if (!ok) *abort_flag = 1;
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     // ------------------------------------------------------------ softmax
     const int q = warp >> 2;
     const int r = threadIdx.x & 127;  // row of the tile = TMEM lane
@@ -658,7 +656,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     const int tok = q * a.tile_tokens + r / a.group;  // token of the unit
     const bool whole_row = r < a.tile_tokens * a.group;
     const float c2 = a.c2;
-    uint32_t ns = 0, no = 0, nclean = 0;
+    uint32_t ns = 0, no = 0;
     uint32_t it = 0;  // K and V tiles before this piece
     bool ok = true;
     while (const ChunkPiece* next = take(true)) {
@@ -669,11 +667,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       const int t0 = p.t0, t1 = p.t1, kt = p.kt[q];
       float m = -INFINITY, l = 0.f;
       for (int t = t0; t < t1 && ok; ++t) {
-        const bool masked = (t + 1) * kChunkKeys > seen;
-        if (t >= kt) {  // the other tile's
-          if (masked) ++nclean;
-          continue;
-        }
+        if (t >= kt) break;  // the other tile's
         ok = mbar_wait(smem_u32(&s_full[q]), ns++ & 1);
         ok = __all_sync(0xffffffffu, ok && !*abort_flag);
         if (!ok) break;
@@ -739,15 +733,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         }
         l += (l0 + l1) + (l2 + l3);
         tc::tmem_wait_st();
-        if (masked) {
-          ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&v_clean), nclean++ & 1));
+        if ((t + 1) * kChunkKeys > seen) {
+          const uint32_t iv = it + 2 * (t - t0) + 1;
+          ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&kv_ready[iv % NS]), (iv / NS) & 1));
           if (!ok) break;
-          if (*reinterpret_cast<volatile int*>(&s_slow) != 0) {
-            const uint32_t iv = it + 2 * (t - t0) + 1;
-            ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&kv_full[iv % NS]), (iv / NS) & 1));
-            if (!ok) break;
+          if (*reinterpret_cast<volatile int*>(&s_slow[iv % NS]) != 0)
             chunk_row_product<T, D>(s_addr, o_addr, ring + (iv % NS) * Shape::kTileBytes, vis, t == t0);
-          }
         }
         tc::fence_before_sync();
         __syncwarp();
