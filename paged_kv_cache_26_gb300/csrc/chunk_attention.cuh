@@ -362,7 +362,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   constexpr bool kBf16 = MmaKind<T>::kBf16;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t kv_full[NS], kv_ready[NS], kv_empty[NS];
-  __shared__ __align__(8) uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], mma_fin[2];
+  __shared__ __align__(8) uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], turn[2], mma_fin[2];
   __shared__ int64_t s_found[2];
   __shared__ __align__(8) uint64_t piece_full[kChunkPieces], piece_empty[kChunkPieces];
   __shared__ ChunkPiece s_piece[kChunkPieces];
@@ -389,6 +389,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       mbar_init(smem_u32(&s_full[q]), 1);
       mbar_init(smem_u32(&p_full[q]), 4);
       mbar_init(smem_u32(&o_full[q]), 1);
+      mbar_init(smem_u32(&turn[q]), 1);
       mbar_init(smem_u32(&mma_fin[q]), 1);
     }
     s_abort = 0;
@@ -531,63 +532,74 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           }
         };
         auto ready = [&]() { return mbar_wait(smem_u32(&kv_ready[slot]), phase); };
+        // A and B issue in turn.
+        uint32_t turns = 0;
+        auto my_turn = [&]() {
+          const uint32_t n = turns++;
+          return q == 0 ? n == 0 || mbar_wait(smem_u32(&turn[0]), (n - 1) & 1) : mbar_wait(smem_u32(&turn[1]), n & 1);
+        };
+        auto pass_on = [&]() { mbar_arrive(smem_u32(&turn[q ^ 1])); };
         while (const ChunkPiece* next = take(false)) {
           const int t0 = next->t0, t1 = next->t1, kt = next->kt[q];
           release();
           if (t0 == t1) continue;
           ok = mbar_wait(smem_u32(&q_full), loads++ & 1);
-          // S of the tile whose K is in the slot; the slot is done with after it.
-          auto scores = [&](int t) {
-            if (t < kt) {
-              const uint64_t k_desc = tc::smem_desc_sw128(smem_u32(ring) + slot * Shape::kTileBytes, 16, 1024);
+          // Step t issues P V of tile t and S of tile t + 1 (step t0 - 1 only S).
+          for (int t = t0 - 1; t < t1 && ok; ++t) {
+            const bool pv = t >= t0 && t < kt, sc = t + 1 < t1 && t + 1 < kt;
+            uint32_t vslot = 0, kslot = 0;
+            bool slow = false;
+            if (t >= t0) {
+              ok = ready();
+              vslot = slot;
+              slow = *reinterpret_cast<volatile int*>(&s_slow[slot]) != 0;
+              advance();
+            }
+            if (t + 1 < t1) {
+              ok = ok && ready();
+              kslot = slot;
+              advance();
+            }
+            if (pv) ok = ok && mbar_wait(smem_u32(&p_full[q]), np++ & 1);
+            ok = ok && my_turn();
+            if (!ok) break;
+            tc::fence_after_sync();
+            if (pv && !slow) {
+              const uint64_t v_desc =
+                  tc::smem_desc_sw128(smem_u32(ring) + vslot * Shape::kTileBytes, Shape::kHalfBytes, 1024);
+#pragma unroll
+              for (int k = 0; k < kChunkKeys / 16; ++k)
+                tc::mma_ts(o_col, s_col + 8 * k, v_desc + (k * 2048 >> 4), idesc_o, t > t0 || k > 0 ? 1u : 0u);
+            }
+            if (sc) {
+              const uint64_t k_desc = tc::smem_desc_sw128(smem_u32(ring) + kslot * Shape::kTileBytes, 16, 1024);
 #pragma unroll
               for (int k = 0; k < D / 16; ++k) {
                 const uint32_t off = ((k >> 2) * Shape::kHalfBytes + (k & 3) * 32) >> 4;
                 tc::mma_ss(s_col, q_desc + off, k_desc + off, idesc_s, k > 0 ? 1u : 0u);
               }
               tc::mma_commit(smem_u32(&s_full[q]));
-              tc::mma_commit(smem_u32(&kv_empty[slot]));
-            } else {
-              mbar_arrive(smem_u32(&kv_empty[slot]));
             }
-            advance();
-            if (t + 1 == t1) {
+            pass_on();
+            if (pv && t + 1 == min(t1, kt)) tc::mma_commit(smem_u32(&o_full[q]));
+            // The slots are done with once what was issued is.
+            if (t >= t0) {
+              if (pv)
+                tc::mma_commit(smem_u32(&kv_empty[vslot]));
+              else
+                mbar_arrive(smem_u32(&kv_empty[vslot]));
+            }
+            if (t + 1 < t1) {
+              if (sc)
+                tc::mma_commit(smem_u32(&kv_empty[kslot]));
+              else
+                mbar_arrive(smem_u32(&kv_empty[kslot]));
+            }
+            if (t + 2 == t1) {
               if (t0 < kt)
                 tc::mma_commit(smem_u32(&q_empty));
               else
                 mbar_arrive(smem_u32(&q_empty));
-            }
-          };
-          ok = ok && ready();
-          if (!ok) break;
-          tc::fence_after_sync();
-          scores(t0);
-          for (int t = t0; t < t1; ++t) {
-            ok = ready();
-            if (!ok) break;
-            const uint32_t vslot = slot;
-            const bool slow = *reinterpret_cast<volatile int*>(&s_slow[slot]) != 0;
-            advance();
-            if (t < kt) {
-              ok = mbar_wait(smem_u32(&p_full[q]), np++ & 1);
-              if (!ok) break;
-              tc::fence_after_sync();
-              if (!slow) {
-                const uint64_t v_desc =
-                    tc::smem_desc_sw128(smem_u32(ring) + vslot * Shape::kTileBytes, Shape::kHalfBytes, 1024);
-#pragma unroll
-                for (int k = 0; k < kChunkKeys / 16; ++k)
-                  tc::mma_ts(o_col, s_col + 8 * k, v_desc + (k * 2048 >> 4), idesc_o, t > t0 || k > 0 ? 1u : 0u);
-              }
-              if (t + 1 == min(t1, kt)) tc::mma_commit(smem_u32(&o_full[q]));
-              tc::mma_commit(smem_u32(&kv_empty[vslot]));
-            } else {
-              mbar_arrive(smem_u32(&kv_empty[vslot]));
-            }
-            if (t + 1 < t1) {
-              ok = ready();
-              if (!ok) break;
-              scores(t + 1);
             }
           }
           if (!ok || *abort_flag) break;
