@@ -7,7 +7,8 @@
 // keys in tiles of 128 tokens (eight blocks):
 //   S = Q K^T        M = 128 rows, N = 128 keys, from shared memory into TMEM
 //   P = 2^(S c - m)  in registers, one thread a row; m, the row's reference, moves
-//                    only when a score passes it by 2^8, so O is rarely rescaled
+//                    only when a score passes it by 2^8, so O is rarely rescaled, and
+//                    the weights need not wait for the tile's maximum
 //   O += P V         P from TMEM (over S's columns), O in TMEM, fp32
 // The tensor pipe alternates between the tiles, PV_A S_A' PV_B S_B', so that the
 // softmax of one tile runs under the products of the other.  Either tile has an
@@ -45,6 +46,8 @@ constexpr int kChunkRows = 256;            // query rows of a unit
 constexpr int kChunkThreads = 384;
 constexpr int kMaxChunkSeqs = 8192;
 constexpr int kChunkPieces = 4;            // pieces known ahead
+constexpr int kChunkSteps = 16;            // barriers of steps: more than can be under way (a tile of the ring each)
+constexpr int kEarly = 2;                  // quarters of a tile's weights whose product begins before the others are made
 // A unit's start and end (first loads, first softmax, output) in keys, and the least
 // number of keys worth a CTA of its own.
 constexpr int kUnitKeys = 128;
@@ -65,7 +68,14 @@ struct ChunkArgs {
 
 template <int D>
 struct ChunkShape {
-  static constexpr int kHalfBytes = kChunkKeys * 128;        // 128 rows of 64 dims
+  // Tiles lie in swizzled atoms of 8 rows x 64 dims (1 KB).  Queries: the atoms of
+  // the first 64 dims, then of the others.  Keys and values: the atoms of 8 tokens
+  // side by side, so that a block is one run of shared memory and one TMA box
+  // (a box's cost is per instruction: two boxes of 2 KB a block took 32
+  // instructions and 3,200 cycles for a K and a V tile).
+  static constexpr int kQHalf = 128 * 128;
+  static constexpr int kAtom = 1024;
+  static constexpr int kGroup = kAtom * (D / 64);            // 8 tokens
   static constexpr int kTileBytes = kChunkKeys * D * 2;
   static constexpr int kSlots = D == 128 ? 5 : 10;           // ring of K and V tiles: 160 KB
   static constexpr int kSmem = (2 + kSlots) * kTileBytes + 1024;
@@ -279,23 +289,24 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
-// The same in two dimensions, for blocks of the pools: without a hint for L2,
-// where the CTAs of a (sequence, KV head) find each other's tiles.
-__device__ __forceinline__ void tma_load_rows(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, uint32_t bar) {
+// A block of a pool, as (64 dims, 8 tokens, D / 64, groups of 8 tokens): a box of two
+// groups.  Without a hint for L2, where the CTAs of a (sequence, KV head) find each
+// other's tiles.
+__device__ __forceinline__ void tma_load_block(uint32_t dst, const CUtensorMap* map, int32_t group, uint32_t bar) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-          dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %2, %2, %3}], [%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(group), "r"(bar)
       : "memory");
 }
 
-// Pool row of (block, KV head); a block outside the pool reads as zeros.
-__device__ __forceinline__ int chunk_pool_row(const ChunkArgs& a, int phys, int kvh) {
+// First group of 8 tokens of (block, KV head); a block outside the pool reads as zeros.
+__device__ __forceinline__ int chunk_pool_group(const ChunkArgs& a, int phys, int kvh) {
   if (phys < 0 || phys >= a.num_blocks) {
     flag_error(kErrBlockId);
-    return -kBlockSize;
+    return -2;
   }
-  return (phys * a.num_kv_heads + kvh) * kBlockSize;
+  return (phys * a.num_kv_heads + kvh) * 2;
 }
 
 // Whether one of a word's two values is infinite or NaN.
@@ -331,7 +342,7 @@ __device__ __noinline__ void chunk_row_product(uint32_t p, uint32_t o, const uin
         if (t0 + t >= vis) continue;
         const float2 w2 = unpack2<T>(pk[t >> 1]);
         const float w = t & 1 ? w2.y : w2.x;
-        const uint8_t* row = v + (d >> 6) * ChunkShape<D>::kHalfBytes + (t0 + t) * 128;
+        const uint8_t* row = v + ((t0 + t) >> 3) * ChunkShape<D>::kGroup + (d >> 6) * ChunkShape<D>::kAtom + (t & 7) * 128;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const uint4 x = *reinterpret_cast<const uint4*>(row + ((((d & 63) >> 3) + c) ^ ((t0 + t) & 7)) * 16);
@@ -361,13 +372,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   constexpr int NS = Shape::kSlots;
   constexpr bool kBf16 = MmaKind<T>::kBf16;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t kv_full[NS], kv_ready[NS], kv_empty[NS];
-  __shared__ __align__(8) uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], turn[2], mma_fin[2];
+  __shared__ __align__(8) uint64_t kv_full[NS], ready[kChunkSteps], done[kChunkSteps];
+  __shared__ __align__(8) uint64_t q_full, q_empty, s_full[2], p_early[2], p_full[2], o_full[2], turn[2], mma_fin[2];
   __shared__ int64_t s_found[2];
   __shared__ __align__(8) uint64_t piece_full[kChunkPieces], piece_empty[kChunkPieces];
   __shared__ ChunkPiece s_piece[kChunkPieces];
   __shared__ uint32_t s_tmem;
-  __shared__ int s_abort, s_slow[NS];
+  __shared__ int s_abort, s_slow[kChunkSteps];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* q_smem = base;
   uint8_t* ring = base + 2 * Shape::kTileBytes;
@@ -376,8 +387,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS; ++s) {
       mbar_init(smem_u32(&kv_full[s]), 1);
-      mbar_init(smem_u32(&kv_ready[s]), 1);
-      mbar_init(smem_u32(&kv_empty[s]), 2);
+    }
+    for (int s = 0; s < kChunkSteps; ++s) {
+      mbar_init(smem_u32(&ready[s]), 1);
+      mbar_init(smem_u32(&done[s]), 2);
     }
     for (int s = 0; s < kChunkPieces; ++s) {
       mbar_init(smem_u32(&piece_full[s]), 1);
@@ -387,6 +400,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     mbar_init(smem_u32(&q_empty), 2);
     for (int q = 0; q < 2; ++q) {
       mbar_init(smem_u32(&s_full[q]), 1);
+      mbar_init(smem_u32(&p_early[q]), 4);
       mbar_init(smem_u32(&p_full[q]), 4);
       mbar_init(smem_u32(&o_full[q]), 1);
       mbar_init(smem_u32(&turn[q]), 1);
@@ -449,6 +463,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       walk.b = a.num_seqs;
       if (at < stop) walk.locate(a, static_cast<int>(s_found[0]), s_found[1]);
       uint32_t it = 0;      // tiles issued
+      uint32_t steps = 0;   // of the MMA warps before this piece
+      uint32_t seen_done = 0, slot_step = 0;  // lane s: the step of the tile in slot s
       int loads = 0;        // of queries
       bool ok = true;
       for (bool last = false; ok && !last;) {
@@ -477,7 +493,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           for (int q = 0; q < tiles; ++q)
 #pragma unroll
             for (int d = 0; d < D / 64; ++d)
-              tma_load_3d(smem_u32(q_smem) + q * Shape::kTileBytes + d * Shape::kHalfBytes, &tmap_q, 64 * d,
+              tma_load_3d(smem_u32(q_smem) + q * Shape::kTileBytes + d * Shape::kQHalf, &tmap_q, 64 * d,
                           p.kvh * a.group, p.row0 + q * a.tile_tokens, smem_u32(&q_full));
         }
         const int32_t* table = a.block_tables + static_cast<int64_t>(p.b) * a.max_blocks;
@@ -487,26 +503,29 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           const int blk = t * (kChunkKeys / kBlockSize);
           if (blk >= win + 32) {
             win = blk;
-            row = win + lane < nblk ? chunk_pool_row(a, __ldg(table + win + lane), p.kvh) : 0;
+            row = win + lane < nblk ? chunk_pool_group(a, __ldg(table + win + lane), p.kvh) : 0;
           }
           const int mine = __shfl_sync(0xffffffffu, row, blk - win + (lane & 7));
           const int here = min(kChunkKeys / kBlockSize, nblk - blk);
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv, ++it) {  // K, then V
             const int slot = it % NS;
-            if (it >= NS) ok = ok && mbar_wait(smem_u32(&kv_empty[slot]), (it / NS - 1) & 1);
+            // The slot's last tile is done with when its step is (all before it too).
+            const uint32_t last_step = __shfl_sync(0xffffffffu, slot_step, slot);
+            if (it >= NS)
+              for (; ok && seen_done <= last_step; ++seen_done)
+                ok = mbar_wait(smem_u32(&done[seen_done % kChunkSteps]), (seen_done / kChunkSteps) & 1);
+            if (lane == slot) slot_step = steps + (t - p.t0) + kv;  // V of a tile goes with K of the next
             ok = __all_sync(0xffffffffu, ok && !*abort_flag);
             if (!ok) break;
             const uint32_t bar = smem_u32(&kv_full[slot]);
             const uint32_t dst = smem_u32(ring) + slot * Shape::kTileBytes;
             if (lane == 0) mbar_arrive_expect_tx(bar, here * kBlockSize * D * 2);
             __syncwarp();
-            if (lane < here)
-#pragma unroll
-              for (int d = 0; d < D / 64; ++d)
-                tma_load_rows(dst + d * Shape::kHalfBytes + lane * 2048, kv ? &tmap_v : &tmap_k, 64 * d, mine, bar);
+            if (lane < here) tma_load_block(dst + lane * 2 * Shape::kGroup, kv ? &tmap_v : &tmap_k, mine, bar);
           }
         }
+        steps += p.t1 - p.t0 + 1;
       }
       if (!ok) {
         *abort_flag = 1;
@@ -522,16 +541,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         constexpr uint32_t idesc_o = tc::idesc_f16(kBf16, 128, D, true);
         const uint32_t s_col = tbase + Shape::kSCol + 128 * q, o_col = tbase + Shape::kOCol + D * q;
         const uint64_t q_desc = tc::smem_desc_sw128(smem_u32(q_smem) + q * Shape::kTileBytes, 16, 1024);
-        uint32_t slot = 0, phase = 0;  // of the next K or V tile, as the TMA warp counts them
+        uint32_t slot = 0, step = 0;  // the next K or V tile's, as the TMA warp counts them; the next step
         uint32_t np = 0, loads = 0;
         bool ok = true;
-        auto advance = [&]() {
-          if (++slot == NS) {
-            slot = 0;
-            phase ^= 1;
-          }
+        auto next_slot = [&]() {
+          const uint32_t x = slot;
+          slot = slot + 1 == NS ? 0 : slot + 1;
+          return x;
         };
-        auto ready = [&]() { return mbar_wait(smem_u32(&kv_ready[slot]), phase); };
         // A and B issue in turn.
         uint32_t turns = 0;
         auto my_turn = [&]() {
@@ -541,60 +558,53 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         auto pass_on = [&]() { mbar_arrive(smem_u32(&turn[q ^ 1])); };
         while (const ChunkPiece* next = take(false)) {
           const int t0 = next->t0, t1 = next->t1, kt = next->kt[q];
+          const int masked_from = max(next->first + 1, 0) / kChunkKeys;  // first tile that not every row sees whole
           release();
           if (t0 == t1) continue;
           ok = mbar_wait(smem_u32(&q_full), loads++ & 1);
-          // Step t issues P V of tile t and S of tile t + 1 (step t0 - 1 only S).
-          for (int t = t0 - 1; t < t1 && ok; ++t) {
+          // A step issues P V of tile t and S of tile t + 1 (the first one only S).
+          for (int t = t0 - 1; t < t1 && ok; ++t, ++step) {
             const bool pv = t >= t0 && t < kt, sc = t + 1 < t1 && t + 1 < kt;
-            uint32_t vslot = 0, kslot = 0;
-            bool slow = false;
-            if (t >= t0) {
-              ok = ready();
-              vslot = slot;
-              slow = *reinterpret_cast<volatile int*>(&s_slow[slot]) != 0;
-              advance();
-            }
-            if (t + 1 < t1) {
-              ok = ok && ready();
-              kslot = slot;
-              advance();
-            }
-            if (pv) ok = ok && mbar_wait(smem_u32(&p_full[q]), np++ & 1);
+            ok = mbar_wait(smem_u32(&ready[step % kChunkSteps]), (step / kChunkSteps) & 1);
+            const bool slow = t >= masked_from && *reinterpret_cast<volatile int*>(&s_slow[step % kChunkSteps]) != 0;
+            const uint32_t vslot = t >= t0 ? next_slot() : 0, kslot = t + 1 < t1 ? next_slot() : 0;
+            if (pv) ok = ok && mbar_wait(smem_u32(&p_early[q]), np & 1);
             ok = ok && my_turn();
             if (!ok) break;
             tc::fence_after_sync();
-            if (pv && !slow) {
+            if (pv) {
               const uint64_t v_desc =
-                  tc::smem_desc_sw128(smem_u32(ring) + vslot * Shape::kTileBytes, Shape::kHalfBytes, 1024);
+                  tc::smem_desc_sw128(smem_u32(ring) + vslot * Shape::kTileBytes, Shape::kAtom, Shape::kGroup);
+              auto product = [&](int k) {
+                tc::mma_ts(o_col, s_col + 8 * k, v_desc + (k * 2 * Shape::kGroup >> 4), idesc_o, t > t0 || k > 0 ? 1u : 0u);
+              };
+              if (!slow) {
 #pragma unroll
-              for (int k = 0; k < kChunkKeys / 16; ++k)
-                tc::mma_ts(o_col, s_col + 8 * k, v_desc + (k * 2048 >> 4), idesc_o, t > t0 || k > 0 ? 1u : 0u);
+                for (int k = 0; k < 2 * kEarly; ++k) product(k);
+              }
+              ok = mbar_wait(smem_u32(&p_full[q]), np++ & 1);
+              if (!ok) break;
+              tc::fence_after_sync();
+              if (!slow) {
+#pragma unroll
+                for (int k = 2 * kEarly; k < kChunkKeys / 16; ++k) product(k);
+              }
             }
             if (sc) {
-              const uint64_t k_desc = tc::smem_desc_sw128(smem_u32(ring) + kslot * Shape::kTileBytes, 16, 1024);
+              const uint64_t k_desc = tc::smem_desc_sw128(smem_u32(ring) + kslot * Shape::kTileBytes, 16, Shape::kGroup);
 #pragma unroll
-              for (int k = 0; k < D / 16; ++k) {
-                const uint32_t off = ((k >> 2) * Shape::kHalfBytes + (k & 3) * 32) >> 4;
-                tc::mma_ss(s_col, q_desc + off, k_desc + off, idesc_s, k > 0 ? 1u : 0u);
-              }
+              for (int k = 0; k < D / 16; ++k)
+                tc::mma_ss(s_col, q_desc + (((k >> 2) * Shape::kQHalf + (k & 3) * 32) >> 4),
+                           k_desc + (((k >> 2) * Shape::kAtom + (k & 3) * 32) >> 4), idesc_s, k > 0 ? 1u : 0u);
               tc::mma_commit(smem_u32(&s_full[q]));
             }
             pass_on();
             if (pv && t + 1 == min(t1, kt)) tc::mma_commit(smem_u32(&o_full[q]));
-            // The slots are done with once what was issued is.
-            if (t >= t0) {
-              if (pv)
-                tc::mma_commit(smem_u32(&kv_empty[vslot]));
-              else
-                mbar_arrive(smem_u32(&kv_empty[vslot]));
-            }
-            if (t + 1 < t1) {
-              if (sc)
-                tc::mma_commit(smem_u32(&kv_empty[kslot]));
-              else
-                mbar_arrive(smem_u32(&kv_empty[kslot]));
-            }
+            // The step's tiles are done with once what was issued is.
+            if (pv || sc)
+              tc::mma_commit(smem_u32(&done[step % kChunkSteps]));
+            else
+              mbar_arrive(smem_u32(&done[step % kChunkSteps]));
             if (t + 2 == t1) {
               if (t0 < kt)
                 tc::mma_commit(smem_u32(&q_empty));
@@ -612,46 +622,52 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       __syncwarp();
     } else {
       // ------------------------------------------------------------ V of masked tiles
-      uint32_t slot = 0, phase = 0;
+      uint32_t slot = 0, phase = 0, step = 0;
       bool ok = true;
+      auto landed = [&]() {
+        ok = ok && __all_sync(0xffffffffu, mbar_wait(smem_u32(&kv_full[slot]), phase) && !*abort_flag);
+        if (++slot == NS) {
+          slot = 0;
+          phase ^= 1;
+        }
+      };
       while (const ChunkPiece* next = take(true)) {
         const int first = next->first, t0 = next->t0, t1 = next->t1, ctx = next->ctx;
         __syncwarp();
         if (lane == 0) release();
+        if (t0 == t1) continue;
         const int seen = max(first + 1, 0);  // keys that every row sees
-        for (int i = 2 * t0; i < 2 * t1; ++i) {  // K, then V of a tile
-          const int t = i >> 1;
-          ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&kv_full[slot]), phase) && !*abort_flag);
-          if (!ok) break;
+        for (int t = t0 - 1; t < t1; ++t, ++step) {  // V of tile t, K of tile t + 1
           bool slow = false;
-          if ((i & 1) && (t + 1) * kChunkKeys > seen) {
-            uint8_t* v = ring + slot * Shape::kTileBytes;
+          uint8_t* v = ring + slot * Shape::kTileBytes;
+          if (t >= t0) landed();
+          if (!ok) break;
+          if (t >= t0 && (t + 1) * kChunkKeys > seen) {
             const int from = max(seen - t * kChunkKeys, 0), valid = min(kChunkKeys, ctx - t * kChunkKeys);
             uint32_t bad = 0;
             // 16 bytes a lane, D / 8 lanes a row.
 #pragma unroll 4
             for (int x = from * (D / 8) + lane; x < valid * (D / 8); x += 32) {
               const int r = x / (D / 8), c = x % (D / 8);
-              const uint4 w = *reinterpret_cast<const uint4*>(v + (c >> 3) * Shape::kHalfBytes + r * 128 + (c & 7) * 16);
+              const uint4 w = *reinterpret_cast<const uint4*>(v + (r >> 3) * Shape::kGroup + (c >> 3) * Shape::kAtom + (r & 7) * 128 + (c & 7) * 16);
               bad |= not_finite2<T>(w.x) | not_finite2<T>(w.y) | not_finite2<T>(w.z) | not_finite2<T>(w.w);
             }
             for (int x = valid * (D / 8) + lane; x < kChunkKeys * (D / 8); x += 32) {
               const int r = x / (D / 8), c = x % (D / 8);
-              *reinterpret_cast<uint4*>(v + (c >> 3) * Shape::kHalfBytes + r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+              *reinterpret_cast<uint4*>(v + (r >> 3) * Shape::kGroup + (c >> 3) * Shape::kAtom + (r & 7) * 128 + (c & 7) * 16) =
+                  make_uint4(0, 0, 0, 0);
             }
             fence_proxy_async_smem();
             slow = __any_sync(0xffffffffu, bad != 0);
           }
+          if (t + 1 < t1) landed();
+          if (!ok) break;
           __syncwarp();
           if (lane == 0) {
-            s_slow[slot] = slow;
-            mbar_arrive(smem_u32(&kv_ready[slot]));
+            s_slow[step % kChunkSteps] = slow;
+            mbar_arrive(smem_u32(&ready[step % kChunkSteps]));
           }
           __syncwarp();
-          if (++slot == NS) {
-            slot = 0;
-            phase ^= 1;
-          }
         }
         if (!ok) break;
       }
@@ -669,7 +685,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     const bool whole_row = r < a.tile_tokens * a.group;
     const float c2 = a.c2;
     uint32_t ns = 0, no = 0;
-    uint32_t it = 0;  // K and V tiles before this piece
+    uint32_t it = 0, step = 0;  // K and V tiles, and steps, before this piece
     bool ok = true;
     while (const ChunkPiece* next = take(true)) {
       const ChunkPiece& p = *next;
@@ -693,37 +709,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 #pragma unroll
           for (int k = 0; k < 128; ++k) x[k >> 5][k & 31] = k < vis ? x[k >> 5][k & 31] : 0xff800000u;
         }
-        float mx0 = -INFINITY, mx1 = -INFINITY;
-#pragma unroll
-        for (int k = 0; k < 128; k += 4) {
-          const uint32_t* y = &x[k >> 5][k & 31];
-          mx0 = fmaxf(mx0, fmaxf(__uint_as_float(y[0]), __uint_as_float(y[1])));
-          mx1 = fmaxf(mx1, fmaxf(__uint_as_float(y[2]), __uint_as_float(y[3])));
-        }
-        const float mx = fmaxf(mx0, mx1) * c2;
-        // The reference moves when a score passes it by 2^8 (always for a first one).
-        const bool up = mx > m + 8.f;
-        if (__any_sync(0xffffffffu, up)) {
-          const float al = up ? exp2_approx(m - mx) : 1.f;
-          if (t > t0) {
-            // P V of the tiles before is done: S of this tile was issued after it.
-#pragma unroll
-            for (int j = 0; j < D / 16; ++j) {
-              uint32_t o[16];
-              tc::tmem_ld16(o_addr + 16 * j, o);
-              tc::tmem_wait_ld();
-#pragma unroll
-              for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * al);
-              tc::tmem_st16(o_addr + 16 * j, o);
-            }
-          }
-          l *= al;
-          if (up) m = mx;
-        }
-        const float nr = m == -INFINITY ? 0.f : -m;
-        float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        float l0, l1, l2, l3;
+        auto weights = [&](int j, float nr) {  // of 32 keys, into TMEM
           uint32_t pk[16];
 #pragma unroll
           for (int k = 0; k < 16; k += 2) {
@@ -742,14 +729,56 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             pk[k + 1] = pack2<T>(y[2], y[3]);
           }
           tc::tmem_st16(s_addr + 16 * j, pk);
+        };
+        // The first weights are made with the reference there is while the maxima are
+        // found, and made again if it has to move: when a score passes it by 2^8
+        // (always for a first one).
+        l0 = l1 = l2 = l3 = 0.f;
+        float nr = m == -INFINITY ? 0.f : -m;
+#pragma unroll
+        for (int j = 0; j < kEarly; ++j) weights(j, nr);
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int k = 0; k < 128; k += 8)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            mx[i] = fmaxf(mx[i], fmaxf(__uint_as_float(x[k >> 5][(k & 31) + 2 * i]), __uint_as_float(x[k >> 5][(k & 31) + 2 * i + 1])));
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c2;
+        const bool up = top > m + 8.f;
+        if (__any_sync(0xffffffffu, up)) {
+          const float al = up ? exp2_approx(m - top) : 1.f;
+          if (t > t0) {
+            // P V of the tiles before is done: S of this tile was issued after it.
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) {
+              uint32_t o[16];
+              tc::tmem_ld16(o_addr + 16 * j, o);
+              tc::tmem_wait_ld();
+#pragma unroll
+              for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * al);
+              tc::tmem_st16(o_addr + 16 * j, o);
+            }
+          }
+          l *= al;
+          if (up) m = top;
+          nr = m == -INFINITY ? 0.f : -m;
+          l0 = l1 = l2 = l3 = 0.f;
+#pragma unroll
+          for (int j = 0; j < kEarly; ++j) weights(j, nr);
         }
+        tc::tmem_wait_st();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&p_early[q]));  // their part of P V may begin
+#pragma unroll
+        for (int j = kEarly; j < 4; ++j) weights(j, nr);
         l += (l0 + l1) + (l2 + l3);
         tc::tmem_wait_st();
         if ((t + 1) * kChunkKeys > seen) {
-          const uint32_t iv = it + 2 * (t - t0) + 1;
-          ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&kv_ready[iv % NS]), (iv / NS) & 1));
+          const uint32_t sv = step + (t - t0) + 1, iv = it + 2 * (t - t0) + 1;
+          ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&ready[sv % kChunkSteps]), (sv / kChunkSteps) & 1));
           if (!ok) break;
-          if (*reinterpret_cast<volatile int*>(&s_slow[iv % NS]) != 0)
+          if (*reinterpret_cast<volatile int*>(&s_slow[sv % kChunkSteps]) != 0)
             chunk_row_product<T, D>(s_addr, o_addr, ring + (iv % NS) * Shape::kTileBytes, vis, t == t0);
         }
         tc::fence_before_sync();
@@ -758,6 +787,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       }
       if (!ok) break;
       it += 2 * (t1 - t0);
+      if (t0 < t1) step += t1 - t0 + 1;
       const bool any = t0 < kt;
       if (any) {
         ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&o_full[q]), no++ & 1));

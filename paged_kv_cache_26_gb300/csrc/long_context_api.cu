@@ -154,6 +154,24 @@ int make_query_map(CUtensorMap* map, const void* q, int32_t num_tokens, const pk
   return PKV_OK;
 }
 
+// A pool as (64 dims, 8 tokens, D / 64, groups of 8 tokens): the box of a block puts
+// the atoms of its two groups one after the other (beside ChunkShape).
+int make_block_map(CUtensorMap* map, const void* cache, const pkv_dims* d) {
+  auto fn = encode_fn();
+  if (!fn) return pkv_fail(PKV_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  const cuuint64_t row = static_cast<cuuint64_t>(d->head_dim) * 2;
+  const cuuint32_t parts = static_cast<cuuint32_t>(d->head_dim / 64);
+  const cuuint64_t dims[4] = {64, 8, parts, static_cast<cuuint64_t>(d->num_blocks) * d->num_kv_heads * 2};
+  const cuuint64_t strides[3] = {row, 128, 8 * row};
+  const cuuint32_t box[4] = {64, 8, parts, 2};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUresult r = fn(map, d->dtype == PKV_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                        4, const_cast<void*>(cache), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return pkv_fail(PKV_ERR_CUDA, "cuTensorMapEncodeTiled failed (code " + std::to_string(r) + ")");
+  return PKV_OK;
+}
+
 int chunk_attention_impl(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
                          const int32_t* context_lens, const int32_t* q_offsets, int32_t num_tokens, float scale,
                          void* out, void* workspace, size_t workspace_bytes, const pkv_dims* d, cudaStream_t stream) {
@@ -195,8 +213,8 @@ int chunk_attention_impl(const void* q, const void* k_cache, const void* v_cache
   a.tile_tokens = 128 / a.group;
   CUtensorMap mq, mk, mv;
   if ((rc = make_query_map(&mq, q, num_tokens, d, a.group)) != PKV_OK) return rc;
-  if ((rc = g_maps.get(k_cache, d, false, &mk)) != PKV_OK) return rc;
-  if ((rc = g_maps.get(v_cache, d, false, &mv)) != PKV_OK) return rc;
+  if ((rc = make_block_map(&mk, k_cache, d)) != PKV_OK) return rc;
+  if ((rc = make_block_map(&mv, v_cache, d)) != PKV_OK) return rc;
   cudaError_t e = cudaSuccess;
   with_type_and_dim(d, [&](auto t, auto dim) {
     using T = decltype(t);
