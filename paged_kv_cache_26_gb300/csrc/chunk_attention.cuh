@@ -20,8 +20,8 @@
 // a unit's start and end) form one line which is cut into equal parts, one per
 // CTA, one CTA per SM.  A part begins and ends inside units; such pieces leave
 // unnormalised fp32 partial results that merge_chunk_kernel joins in order.  Every
-// cut follows from the lengths alone: each kernel computes them for itself, from
-// closed sums, and nothing is counted or claimed at run time.
+// cut follows from the lengths alone, by closed sums that each CTA computes for
+// itself; nothing is counted or claimed at run time.
 //
 // Values that a row does not attend to may be anything.  Scores there are replaced,
 // not weighted.  A weight of 0 would still meet V in the product (0 * NaN = NaN), so
@@ -53,12 +53,21 @@ constexpr int kEarly = 2;                  // quarters of a tile's weights whose
 constexpr int kUnitKeys = 128;
 constexpr int kLeastKeys = 512;
 
+// How a CTA's part begins, for the merge: inside a unit (its first piece is then
+// partial result 2 cta) and, `open`, ends inside it too.
+struct ChunkCut {
+  int32_t cut, open;
+  int32_t row0, tokens, kvh;  // the unit's
+  int32_t unused[3];
+};
+
 struct ChunkArgs {
   void* out;
   const int32_t* block_tables;
   const int32_t* context_lens;
   const int32_t* q_offsets;
   float* part;              // [2 grid][256 * D + 512]: O, then m and l of every row
+  ChunkCut* cuts;           // [grid]
   float c2;                 // |scale| * log2(e), at least the smallest float
   int32_t negate;           // scale < 0: S is negated in the product
   int32_t grid;             // CTAs of the main kernel
@@ -467,10 +476,17 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       uint32_t seen_done = 0, slot_step = 0;  // lane s: the step of the tile in slot s
       int loads = 0;        // of queries
       bool ok = true;
+      bool first = true;
       for (bool last = false; ok && !last;) {
         ChunkPiece p;
         last = !walk.next(a, cta, p);
         if (last) p.b = -1;
+        if (first && lane == 0) {
+          ChunkCut c = {};
+          if (!last && p.t0 > 0) c = {1, p.t1 < p.tiles(), p.row0, p.tokens, p.kvh};
+          a.cuts[cta] = c;
+        }
+        first = false;
         const uint32_t slot = pieces % kChunkPieces;
         if (pieces >= kChunkPieces) ok = mbar_wait(smem_u32(&piece_empty[slot]), (pieces / kChunkPieces - 1) & 1);
         ok = __all_sync(0xffffffffu, ok && !*abort_flag);
@@ -847,85 +863,87 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 constexpr int kChunkMergeThreads = 256;
 constexpr int kChunkMergeRows = 32;
 
-// CTA (c, y) joins the pieces of the unit in which CTA c's part begins, if that is
-// the unit's first cut, for 32 of its rows, a warp a row.  The plan needs only the
-// lengths, and they are read before the main kernel is waited for only if it cannot
-// change them: it is its dependent, and the lengths were there before it.
+// CTA (c, y) joins the pieces of the unit inside which CTA c's part begins, if that is
+// the unit's first cut, for 32 of its rows, four a warp with all their loads in
+// flight: the last piece of CTA c - 1, the first of CTA c, and those of the CTAs after
+// it as long as their whole part lay in the unit.
 template <typename T, int D>
 __global__ void __launch_bounds__(kChunkMergeThreads) merge_chunk_kernel(const ChunkArgs a) {
   using Shape = ChunkShape<D>;
-  __shared__ int64_t s_scratch[kChunkMergeThreads / 32];
-  __shared__ int64_t s_found[2];
+  constexpr int kPer = D / 32, kRows = kChunkMergeRows / (kChunkMergeThreads / 32);
   const int c = blockIdx.x + 1;
+  const int lane = threadIdx.x & 31;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  ChunkLine line;
-  line.measure(a, s_scratch, false);
-  if (c >= line.parts) return;
-  ChunkWalk w;
-  w.at = line_cut(line.total, line.parts, c);
-  line.find(a, w.at, s_found);
-  __syncthreads();
-  w.locate(a, static_cast<int>(s_found[0]), s_found[1]);
-  const ChunkPiece p = w.describe(a);
-  const int tiles = p.tiles();
-  const int64_t cost = w.cost(2 * a.tile_tokens);
-  auto cut = [&](int x) { return w.tile_at(line_cut(line.total, line.parts, x) - w.unit_at, cost, tiles); };
-  const int first = cut(c);
-  if (first == 0 || first == tiles) return;
-  const int64_t prev = line_cut(line.total, line.parts, c - 1) - w.unit_at;
-  if (prev > 0 && w.tile_at(prev, cost, tiles) > 0) return;  // an earlier cut's
-  // Pieces: [0, cut(c)) by CTA c - 1, then [cut(x), cut(x + 1)) by CTA x.
-  const int rows = p.tokens * a.group;
-  const int lane = threadIdx.x & 31;
-  const int r0 = blockIdx.y * kChunkMergeRows;
-  for (int i = threadIdx.x >> 5; i < kChunkMergeRows; i += kChunkMergeThreads / 32) {
-    const int rr = r0 + i;                                 // row of the unit, tokens packed
-    if (rr >= rows) break;
-    const int half = a.tile_tokens * a.group;              // rows of tile A
-    const int pr = rr < half ? rr : 128 + rr - half;       // its place in the partial results
-    float M = -INFINITY;
-    float L = 0.f;
-    float o[D / 32];
+  auto cut_of = [&](int x) {
+    const int4* p = reinterpret_cast<const int4*>(a.cuts + x);
+    const int4 u = __ldcg(p), v = __ldcg(p + 1);
+    return ChunkCut{u.x, u.y, u.z, u.w, v.x};
+  };
+  const ChunkCut here = cut_of(c), prev = cut_of(c - 1);
+  if (!here.cut || (prev.cut && prev.open)) return;
+  const int rows = here.tokens * a.group, half = a.tile_tokens * a.group;  // half: rows of tile A
+  const int r0 = blockIdx.y * kChunkMergeRows + (threadIdx.x >> 5) * kRows;  // rows of the unit, tokens packed
+  if (r0 >= rows) return;
+  float M[kRows], L[kRows], o[kRows][kPer];
 #pragma unroll
-    for (int k = 0; k < D / 32; ++k) o[k] = 0.f;
-    int from = 0, to = first;
-    for (int x = c - 1;;) {
-      if (from < to) {
-        const float* src = a.part + (from == 0 ? 2 * x + 1 : 2 * x) * Shape::kPart;
-        const float m = src[kChunkRows * D + pr], l = src[kChunkRows * (D + 1) + pr];
-        if (!(m == -INFINITY && l == 0.f)) {               // (tile A may have no keys in the last piece)
-          const float top = fmaxf(M, m);
-          const float wo = M == -INFINITY && L == 0.f ? 0.f : exp2f(M - top), wn = exp2f(m - top);
-          float v[D / 32];
-          if constexpr (D == 128) {
-            const float4 f = *reinterpret_cast<const float4*>(src + pr * D + 4 * lane);
-            v[0] = f.x;
-            v[1] = f.y;
-            v[2] = f.z;
-            v[3] = f.w;
-          } else {
-            const float2 f = *reinterpret_cast<const float2*>(src + pr * D + 2 * lane);
-            v[0] = f.x;
-            v[1] = f.y;
-          }
-          L = L * wo + l * wn;
+  for (int i = 0; i < kRows; ++i) {
+    M[i] = -INFINITY;
+    L[i] = 0.f;
 #pragma unroll
-          for (int k = 0; k < D / 32; ++k) o[k] = o[k] * wo + v[k] * wn;
-          M = top;
-        }
+    for (int k = 0; k < kPer; ++k) o[i][k] = 0.f;
+  }
+  int slot = 2 * c - 1;
+  bool open = here.open;
+  for (int x = c;; ++x) {
+    const float* src = a.part + slot * Shape::kPart;
+    float m[kRows], l[kRows], v[kRows][kPer];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const int rr = min(r0 + i, rows - 1), pr = rr < half ? rr : 128 + rr - half;  // its place in the partial result
+      m[i] = __ldcg(src + kChunkRows * D + pr);
+      l[i] = __ldcg(src + kChunkRows * (D + 1) + pr);
+      if constexpr (D == 128) {
+        const float4 f = __ldcg(reinterpret_cast<const float4*>(src + pr * D) + lane);
+        v[i][0] = f.x;
+        v[i][1] = f.y;
+        v[i][2] = f.z;
+        v[i][3] = f.w;
+      } else {
+        const float2 f = __ldcg(reinterpret_cast<const float2*>(src + pr * D) + lane);
+        v[i][0] = f.x;
+        v[i][1] = f.y;
       }
-      if (to == tiles) break;
-      ++x;
-      from = to;
-      to = x + 1 < line.parts ? cut(x + 1) : tiles;
     }
-    const float inv = 1.0f / L;
-    const int64_t orow = (static_cast<int64_t>(p.row0) + rr / a.group) * a.num_q_heads + p.kvh * a.group + rr % a.group;
-    T* dst = static_cast<T*>(a.out) + orow * D + lane * (D / 32);
 #pragma unroll
-    for (int k = 0; k < D / 32; k += 2)
-      *reinterpret_cast<uint32_t*>(dst + k) = L == 0.f ? 0u : pack2<T>(o[k] * inv, o[k + 1] * inv);
+    for (int i = 0; i < kRows; ++i) {
+      if (m[i] == -INFINITY && l[i] == 0.f) continue;  // (tile A may have no keys in the last piece)
+      const float top = fmaxf(M[i], m[i]);
+      const float wo = M[i] == -INFINITY && L[i] == 0.f ? 0.f : exp2f(M[i] - top), wn = exp2f(m[i] - top);
+      L[i] = L[i] * wo + l[i] * wn;
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) o[i][k] = o[i][k] * wo + v[i][k] * wn;
+      M[i] = top;
+    }
+    if (slot & 1) {
+      slot = 2 * c;  // after the first piece, CTA c's
+      --x;
+      continue;
+    }
+    if (!open || x + 1 >= a.grid) break;
+    slot = 2 * (x + 1);
+    open = cut_of(x + 1).open;
+  }
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    const int rr = r0 + i;
+    if (rr >= rows) break;
+    const float inv = 1.0f / L[i];
+    const int64_t orow = (static_cast<int64_t>(here.row0) + rr / a.group) * a.num_q_heads + here.kvh * a.group + rr % a.group;
+    T* dst = static_cast<T*>(a.out) + orow * D + lane * kPer;
+#pragma unroll
+    for (int k = 0; k < kPer; k += 2)
+      *reinterpret_cast<uint32_t*>(dst + k) = L[i] == 0.f ? 0u : pack2<T>(o[i][k] * inv, o[i][k + 1] * inv);
   }
 }
 

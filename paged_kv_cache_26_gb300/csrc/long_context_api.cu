@@ -130,9 +130,12 @@ int check_tables(const pkv_dims* d, const void* block_tables, const void* contex
 
 // ------------------------------------------------------------------ chunks of new tokens
 
-// Two partial results for each CTA of the largest grid.
-size_t chunk_workspace(const pkv_dims* d) {
+// Two partial results for each CTA of the grid, then how each CTA's part begins.
+size_t chunk_partials(const pkv_dims* d) {
   return align256(static_cast<size_t>(2) * device_sms() * pkv::kChunkRows * (d->head_dim + 2) * sizeof(float));
+}
+size_t chunk_workspace(const pkv_dims* d) {
+  return chunk_partials(d) + align256(device_sms() * sizeof(pkv::ChunkCut));
 }
 
 // Queries as (dims, heads, tokens): a box is 64 dims of the group's heads of a
@@ -200,6 +203,7 @@ int chunk_attention_impl(const void* q, const void* k_cache, const void* v_cache
   a.context_lens = context_lens;
   a.q_offsets = q_offsets;
   a.part = static_cast<float*>(workspace);
+  a.cuts = reinterpret_cast<pkv::ChunkCut*>(static_cast<uint8_t*>(workspace) + chunk_partials(d));
   a.c2 = std::max(std::fabs(scale) * 1.4426950408889634f, std::numeric_limits<float>::denorm_min());
   a.negate = scale < 0.f;
   a.grid = device_sms();

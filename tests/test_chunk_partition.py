@@ -100,31 +100,25 @@ def plan(new, ctx, heads, group, grid):
     return seqs, total, parts, pieces
 
 
-def merges(seqs, heads, total, parts):
-    """What every merge CTA reads: (unit, [(slot, t0, t1)])."""
-    for c in range(1, parts):
-        b, kvh, i, unit_at = locate(seqs, heads, line_cut(total, parts, c))
-        s = seqs[b]
-        cost, tiles = s.cost(i), max(s.tiles(i))
-
-        def cut(x):
-            return tile_at(line_cut(total, parts, x) - unit_at, cost, tiles)
-
-        first = cut(c)
-        if first in (0, tiles):
+def merges(grid, pieces):
+    """What every merge CTA reads: (unit, [slots]), from how each CTA's part begins."""
+    cuts = [None] * grid
+    for cta, unit, t0, t1, slot in reversed(pieces):
+        cuts[cta] = (unit, t0 > 0, slot)
+    first = {}
+    for cta, unit, t0, t1, slot in pieces:
+        first.setdefault(cta, (unit, t0, t1))
+    opened = {}
+    for cta, (unit, t0, t1) in first.items():
+        opened[cta] = t0 > 0 and t1 < max(p[3] for p in pieces if p[1] == unit)
+    for c in range(1, grid):
+        if not cuts[c] or not cuts[c][1] or (cuts[c - 1] and cuts[c - 1][1] and opened[c - 1]):
             continue
-        prev = line_cut(total, parts, c - 1) - unit_at
-        if prev > 0 and tile_at(prev, cost, tiles) > 0:
-            continue
-        got, x, begin, end = [], c - 1, 0, first
-        while True:
-            if begin < end:
-                got.append((2 * x + 1 if begin == 0 else 2 * x, begin, end))
-            if end == tiles:
-                break
+        got, x = [2 * c - 1, 2 * c], c
+        while opened[x] and x + 1 < grid:
             x += 1
-            begin, end = end, cut(x + 1) if x + 1 < parts else tiles
-        yield (b, kvh, i), got
+            got.append(2 * x)
+        yield cuts[c][0], got
 
 
 def check(new, ctx, heads, group, grid):
@@ -146,10 +140,12 @@ def check(new, ctx, heads, group, grid):
         assert (len(got) == 1) == (got[0][2] == -1)
         if len(got) > 1:
             cut.add(unit)
-    merged = list(merges(seqs, heads, total, parts))
+    merged = list(merges(grid, pieces))
     assert {u for u, _ in merged} == cut and len(merged) == len(cut)
     for unit, got in merged:
-        assert [(slots.pop(s)) for s, _, _ in got] == [(unit, a, b) for _, a, b in got]
+        ranges = [slots.pop(s) for s in got]
+        assert all(u == unit for u, _, _ in ranges) and ranges[0][1] == 0
+        assert all(a[2] == b[1] for a, b in zip(ranges, ranges[1:])) and ranges[-1][2] == max(seqs[unit[0]].tiles(unit[2]))
     assert not slots
     return parts, pieces
 
