@@ -36,6 +36,8 @@
 // the MMA warps included.  Waits give up after kWaitLimitNs.
 #pragma once
 
+#include <climits>
+
 #include "paged_kv_kernels.cuh"
 #include "tcgen05.cuh"
 
@@ -66,7 +68,7 @@ struct ChunkArgs {
   const int32_t* block_tables;
   const int32_t* context_lens;
   const int32_t* q_offsets;
-  float* part;              // [2 grid][256 * D + 512]: O, then m and l of every row
+  float* part;              // [2 grid][256 * (D + 2)]: O as [D / 4][256 rows] of four dims, then m and l of every row
   ChunkCut* cuts;           // [grid]
   float c2;                 // |scale| * log2(e), at least the smallest float
   int32_t negate;           // scale < 0: S is negated in the product
@@ -152,11 +154,14 @@ struct ChunkWalk {
     const int tt = 2 * a.tile_tokens;
     b = seq;
     s = chunk_seq(a, b, flag);
-    kvh = static_cast<int>(rest / s.line);
+    // Quotient and root in float32, corrected by a step or two.
+    kvh = min(static_cast<int>(static_cast<float>(rest) / static_cast<float>(s.line)), a.num_kv_heads - 1);
+    while (kvh > 0 && kvh * s.line > rest) --kvh;
+    while ((kvh + 1) * s.line <= rest) ++kvh;
     rest -= kvh * s.line;
-    // start(i) <= rest: the root of a quadratic, corrected by a step or two.
-    const double p = s.before + kUnitKeys + 0.5 * tt;
-    int i = static_cast<int>((sqrt(p * p + 2.0 * tt * static_cast<double>(rest)) - p) / tt);
+    // start(i) <= rest, i the positive root: 2 rest / (p + sqrt(p^2 + 2 tt rest)).
+    const float p = static_cast<float>(s.before + kUnitKeys) + 0.5f * tt, x = static_cast<float>(rest);
+    int i = static_cast<int>(2.f * x / (p + sqrtf(p * p + 2.f * tt * x)));
     i = min(max(i, 0), s.units - 1);
     while (i > 0 && s.start(i, tt) > rest) --i;
     while (i + 1 < s.units && s.start(i + 1, tt) <= rest) ++i;
@@ -211,6 +216,10 @@ struct ChunkWalk {
 
 // CTA c's part of a line of `total` for `parts` CTAs: [line_cut(c), line_cut(c + 1)).
 __device__ __forceinline__ int64_t line_cut(int64_t total, int parts, int c) {
+  if (total >> 32 == 0) {  // (a 64-bit quotient is some hundred instructions)
+    const uint32_t t = static_cast<uint32_t>(total), p = static_cast<uint32_t>(parts);
+    return static_cast<int64_t>(t / p) * c + t % p * c / p;
+  }
   return total / parts * c + total % parts * c / parts;
 }
 
@@ -246,6 +255,7 @@ struct ChunkLine {
       total += v;
     }
     mine = before + scan - sum;
+    static_assert((kLeastKeys & (kLeastKeys - 1)) == 0, "a shift");
     parts = static_cast<int>(max(static_cast<int64_t>(1), min(static_cast<int64_t>(a.grid), total / kLeastKeys)));
   }
   // The thread whose sequences hold place x of the line stores (sequence, rest).
@@ -706,7 +716,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     while (const ChunkPiece* next = take(true)) {
       const ChunkPiece& p = *next;
       const bool valid_row = whole_row && tok < p.tokens;
-      const int limit = valid_row ? p.first + tok : -1;  // last position the row attends to
+      // Last position the row attends to.  Rows without a token may come out as anything;
+      // a warp of them leaves its weights alone.
+      const int limit = valid_row ? p.first + tok : INT_MAX / 2;
+      const bool idle = !__any_sync(0xffffffffu, valid_row);
       const int seen = max(p.first + 1, 0);
       const int t0 = p.t0, t1 = p.t1, kt = p.kt[q];
       float m = -INFINITY, l = 0.f;
@@ -715,8 +728,16 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         ok = mbar_wait(smem_u32(&s_full[q]), ns++ & 1);
         ok = __all_sync(0xffffffffu, ok && !*abort_flag);
         if (!ok) break;
+        if (idle) {
+          if (lane == 0) {
+            mbar_arrive(smem_u32(&p_early[q]));
+            mbar_arrive(smem_u32(&p_full[q]));
+          }
+          __syncwarp();
+          continue;
+        }
         tc::fence_after_sync();
-        uint32_t x[4][32];  // scores, then weights, as their bits
+        uint32_t x[4][32];  // scores as their bits
 #pragma unroll
         for (int j = 0; j < 4; ++j) tc::tmem_ld32(s_addr + 32 * j, x[j]);
         tc::tmem_wait_ld();
@@ -747,12 +768,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           tc::tmem_st16(s_addr + 16 * j, pk);
         };
         // The first weights are made with the reference there is while the maxima are
-        // found, and made again if it has to move: when a score passes it by 2^8
-        // (always for a first one).
+        // found, and made again if it has to move: when a score passes it by 2^8.
         l0 = l1 = l2 = l3 = 0.f;
         float nr = m == -INFINITY ? 0.f : -m;
+        if (t > t0) {
 #pragma unroll
-        for (int j = 0; j < kEarly; ++j) weights(j, nr);
+          for (int j = 0; j < kEarly; ++j) weights(j, nr);
+        }
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
         for (int k = 0; k < 128; k += 8)
@@ -761,7 +783,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             mx[i] = fmaxf(mx[i], fmaxf(__uint_as_float(x[k >> 5][(k & 31) + 2 * i]), __uint_as_float(x[k >> 5][(k & 31) + 2 * i + 1])));
         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c2;
         const bool up = top > m + 8.f;
-        if (__any_sync(0xffffffffu, up)) {
+        if (t == t0 || __any_sync(0xffffffffu, up)) {
           const float al = up ? exp2_approx(m - top) : 1.f;
           if (t > t0) {
             // P V of the tiles before is done: S of this tile was issued after it.
@@ -813,8 +835,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       const int64_t orow = (static_cast<int64_t>(p.row0) + tok) * a.num_q_heads + p.kvh * a.group + r % a.group;
       const float inv = l == 0.f ? 0.f : 1.0f / l;  // nothing attended to: a zero row (a NaN stays one)
       float* part = p.slot >= 0 ? a.part + p.slot * Shape::kPart : nullptr;
+      // A lane holds a row, and 32 stores of 16 bytes to 32 rows are 32 accesses.  So the
+      // output goes through exchanges within four lanes, after which each has the same
+      // 16 bytes of every 64 of their four rows; partial results lie as they are held.
+      int64_t rows[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) rows[i] = __shfl_sync(0xffffffffu, valid_row ? orow : -1, (lane & ~3) + i);
 #pragma unroll 1
-      for (int j = 0; j < D / 32; ++j) {
+      for (int j = 0; j < (idle ? 0 : D / 32); ++j) {
         uint32_t o[32];
         if (any) {
           tc::tmem_ld32(o_addr + 32 * j, o);
@@ -823,19 +851,38 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 #pragma unroll
           for (int k = 0; k < 32; ++k) o[k] = 0;
         }
-        if (valid_row && p.slot < 0) {
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + orow * D + 32 * j);
-          float v[32];
+        if (part) {
+          uint4* dst = reinterpret_cast<uint4*>(part) + (8 * j) * kChunkRows + q * 128 + r;
 #pragma unroll
-          for (int k = 0; k < 32; ++k) v[k] = l == 0.f ? 0.f : __uint_as_float(o[k]) * inv;
+          for (int k = 0; k < 8; ++k) dst[k * kChunkRows] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+        } else {
+          uint32_t v[16];
 #pragma unroll
-          for (int k = 0; k < 32; k += 8)
-            dst[k / 8] = make_uint4(pack2<T>(v[k], v[k + 1]), pack2<T>(v[k + 2], v[k + 3]), pack2<T>(v[k + 4], v[k + 5]),
-                                    pack2<T>(v[k + 6], v[k + 7]));
-        } else if (valid_row) {
-          uint4* dst = reinterpret_cast<uint4*>(part + (q * 128 + r) * D + 32 * j);
+          for (int k = 0; k < 16; ++k)
+            v[k] = l == 0.f ? 0u : pack2<T>(__uint_as_float(o[2 * k]) * inv, __uint_as_float(o[2 * k + 1]) * inv);
+          // v[4 c + w]: word w of the row's 16 bytes c; then of row c of the four, 16 bytes (lane % 4).
 #pragma unroll
-          for (int k = 0; k < 32; k += 4) dst[k / 4] = make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+          for (int h = 1; h <= 2; h *= 2) {
+            const bool odd = lane & h;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              if (c & h) continue;
+#pragma unroll
+              for (int w = 0; w < 4; ++w) {
+                const uint32_t give = odd ? v[4 * c + w] : v[4 * (c + h) + w];
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, give, h);
+                if (odd)
+                  v[4 * c + w] = got;
+                else
+                  v[4 * (c + h) + w] = got;
+              }
+            }
+          }
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (rows[c] >= 0)
+              reinterpret_cast<uint4*>(static_cast<T*>(a.out) + rows[c] * D + 32 * j)[lane & 3] =
+                  make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
         }
         __syncwarp();
       }
@@ -864,13 +911,13 @@ constexpr int kChunkMergeThreads = 256;
 constexpr int kChunkMergeRows = 32;
 
 // CTA (c, y) joins the pieces of the unit inside which CTA c's part begins, if that is
-// the unit's first cut, for 32 of its rows, four a warp with all their loads in
-// flight: the last piece of CTA c - 1, the first of CTA c, and those of the CTAs after
+// the unit's first cut, for 32 of its rows, four a warp: the last piece of CTA c - 1, the first of CTA c, and those of the CTAs after
 // it as long as their whole part lay in the unit.
 template <typename T, int D>
 __global__ void __launch_bounds__(kChunkMergeThreads) merge_chunk_kernel(const ChunkArgs a) {
   using Shape = ChunkShape<D>;
   constexpr int kPer = D / 32, kRows = kChunkMergeRows / (kChunkMergeThreads / 32);
+  static_assert(kRows == 4, "four rows a warp");
   const int c = blockIdx.x + 1;
   const int lane = threadIdx.x & 31;
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -885,66 +932,48 @@ __global__ void __launch_bounds__(kChunkMergeThreads) merge_chunk_kernel(const C
   const int rows = here.tokens * a.group, half = a.tile_tokens * a.group;  // half: rows of tile A
   const int r0 = blockIdx.y * kChunkMergeRows + (threadIdx.x >> 5) * kRows;  // rows of the unit, tokens packed
   if (r0 >= rows) return;
-  float M[kRows], L[kRows], o[kRows][kPer];
+  // Lane: row r0 + lane % 4, dims 4 (lane / 4) + 32 k.
+  const int rr = r0 + (lane & 3);
+  const int pr = min(rr, rows - 1) < half ? min(rr, rows - 1) : 128 + min(rr, rows - 1) - half;  // its place in a partial result
+  float M = -INFINITY, L = 0.f;
+  float4 o[kPer];
 #pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    M[i] = -INFINITY;
-    L[i] = 0.f;
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) o[i][k] = 0.f;
-  }
+  for (int k = 0; k < kPer; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
   int slot = 2 * c - 1;
   bool open = here.open;
-  for (int x = c;; ++x) {
+  for (int x = c;;) {
     const float* src = a.part + slot * Shape::kPart;
-    float m[kRows], l[kRows], v[kRows][kPer];
+    const float m = __ldcg(src + kChunkRows * D + pr), l = __ldcg(src + kChunkRows * (D + 1) + pr);
+    float4 v[kPer];
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      const int rr = min(r0 + i, rows - 1), pr = rr < half ? rr : 128 + rr - half;  // its place in the partial result
-      m[i] = __ldcg(src + kChunkRows * D + pr);
-      l[i] = __ldcg(src + kChunkRows * (D + 1) + pr);
-      if constexpr (D == 128) {
-        const float4 f = __ldcg(reinterpret_cast<const float4*>(src + pr * D) + lane);
-        v[i][0] = f.x;
-        v[i][1] = f.y;
-        v[i][2] = f.z;
-        v[i][3] = f.w;
-      } else {
-        const float2 f = __ldcg(reinterpret_cast<const float2*>(src + pr * D) + lane);
-        v[i][0] = f.x;
-        v[i][1] = f.y;
-      }
-    }
+    for (int k = 0; k < kPer; ++k) v[k] = __ldcg(reinterpret_cast<const float4*>(src) + ((lane >> 2) + 8 * k) * kChunkRows + pr);
+    if (!(m == -INFINITY && l == 0.f)) {  // (tile A may have no keys in the last piece)
+      const float top = fmaxf(M, m);
+      const float wo = M == -INFINITY && L == 0.f ? 0.f : exp2f(M - top), wn = exp2f(m - top);
+      L = L * wo + l * wn;
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      if (m[i] == -INFINITY && l[i] == 0.f) continue;  // (tile A may have no keys in the last piece)
-      const float top = fmaxf(M[i], m[i]);
-      const float wo = M[i] == -INFINITY && L[i] == 0.f ? 0.f : exp2f(M[i] - top), wn = exp2f(m[i] - top);
-      L[i] = L[i] * wo + l[i] * wn;
-#pragma unroll
-      for (int k = 0; k < kPer; ++k) o[i][k] = o[i][k] * wo + v[i][k] * wn;
-      M[i] = top;
+      for (int k = 0; k < kPer; ++k)
+        o[k] = make_float4(o[k].x * wo + v[k].x * wn, o[k].y * wo + v[k].y * wn, o[k].z * wo + v[k].z * wn,
+                           o[k].w * wo + v[k].w * wn);
+      M = top;
     }
     if (slot & 1) {
       slot = 2 * c;  // after the first piece, CTA c's
-      --x;
-      continue;
+    } else {
+      if (!open || x + 1 >= a.grid) break;
+      slot = 2 * ++x;
+      open = cut_of(x).open;
     }
-    if (!open || x + 1 >= a.grid) break;
-    slot = 2 * (x + 1);
-    open = cut_of(x + 1).open;
   }
+  if (rr >= rows) return;
+  const float inv = 1.0f / L;
+  const int64_t orow = (static_cast<int64_t>(here.row0) + rr / a.group) * a.num_q_heads + here.kvh * a.group + rr % a.group;
+  T* dst = static_cast<T*>(a.out) + orow * D + 4 * (lane >> 2);
 #pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    const int rr = r0 + i;
-    if (rr >= rows) break;
-    const float inv = 1.0f / L[i];
-    const int64_t orow = (static_cast<int64_t>(here.row0) + rr / a.group) * a.num_q_heads + here.kvh * a.group + rr % a.group;
-    T* dst = static_cast<T*>(a.out) + orow * D + lane * kPer;
-#pragma unroll
-    for (int k = 0; k < kPer; k += 2)
-      *reinterpret_cast<uint32_t*>(dst + k) = L[i] == 0.f ? 0u : pack2<T>(o[i][k] * inv, o[i][k + 1] * inv);
-  }
+  for (int k = 0; k < kPer; ++k)
+    *reinterpret_cast<uint2*>(dst + 32 * k) =
+        L == 0.f ? make_uint2(0u, 0u)
+                 : make_uint2(pack2<T>(o[k].x * inv, o[k].y * inv), pack2<T>(o[k].z * inv, o[k].w * inv));
 }
 
 }  // namespace pkv

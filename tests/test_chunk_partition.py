@@ -2,7 +2,6 @@
 as chunk_attention.cuh (ChunkSeq, ChunkWalk, ChunkLine, the merge's plan), checked
 for every key tile of every unit being done exactly once, every partial result
 written once and read once, and every cut unit merged exactly once."""
-import math
 import os
 import re
 
@@ -53,9 +52,16 @@ def locate(seqs, heads, x):
     for b, s in enumerate(seqs):
         if x < at + s.line * heads:
             rest = x - at
-            kvh, rest = divmod(rest, s.line)
-            p = s.before + UNIT_KEYS + 0.5 * s.tt
-            i = int((math.sqrt(p * p + 2.0 * s.tt * rest) - p) / s.tt)
+            f = np.float32
+            kvh, steps = min(int(f(rest) / f(s.line)), heads - 1), 0
+            while kvh > 0 and kvh * s.line > rest:
+                kvh, steps = kvh - 1, steps + 1
+            while (kvh + 1) * s.line <= rest:
+                kvh, steps = kvh + 1, steps + 1
+            assert steps <= 1
+            rest -= kvh * s.line
+            p, y = f(s.before + UNIT_KEYS) + f(0.5) * f(s.tt), f(rest)
+            i = int(f(2) * y / (p + np.sqrt(p * p + f(2) * f(s.tt) * y)))
             i = min(max(i, 0), s.units - 1)
             steps = 0
             while i > 0 and s.start(i) > rest:
