@@ -49,7 +49,7 @@ constexpr int kChunkThreads = 384;
 constexpr int kMaxChunkSeqs = 8192;
 constexpr int kChunkPieces = 4;            // pieces known ahead
 constexpr int kChunkSteps = 16;            // barriers of steps: more than can be under way (a tile of the ring each)
-constexpr int kEarly = 2;                  // quarters of a tile's weights whose product begins before the others are made
+constexpr int kEarly = 1;                  // quarters of a tile's weights whose product begins before the others are made
 // A unit's start and end (first loads, first softmax, output) in keys, and the least
 // number of keys worth a CTA of its own.
 constexpr int kUnitKeys = 128;
@@ -859,7 +859,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           uint32_t v[16];
 #pragma unroll
           for (int k = 0; k < 16; ++k)
-            v[k] = l == 0.f ? 0u : pack2<T>(__uint_as_float(o[2 * k]) * inv, __uint_as_float(o[2 * k + 1]) * inv);
+            v[k] = pack2<T>(__uint_as_float(o[2 * k]) * inv, __uint_as_float(o[2 * k + 1]) * inv);
           // v[4 c + w]: word w of the row's 16 bytes c; then of row c of the four, 16 bytes (lane % 4).
 #pragma unroll
           for (int h = 1; h <= 2; h *= 2) {
