@@ -610,7 +610,8 @@ int paged_kv_append_rope(const void* q, const void* k_new, const void* v_new, co
  * accumulation; softmax weights (below 2^8 times the largest) are rounded to T for
  * their product with V, their sum is fp32.  Slots past a sequence's length, and for
  * each row the positions it does not attend to, may hold anything, NaN and
- * infinities too.
+ * infinities too; an infinite V that a row does attend to gives it an infinity, or
+ * NaN in fp16 where the weight, below 2^-25, rounds to 0.
  * workspace (device): paged_chunk_workspace_bytes(dims) bytes, 256-byte aligned;
  * its contents need no initialisation.  Calls that share it must not overlap.
  * Limits: dims as paged_decode_attention; at most 2048 sequences; num_seqs *

@@ -28,7 +28,7 @@ struct BoundArgs {
   const int32_t* q_offsets;  // [B + 1], or null: one new token of each sequence
   int8_t* bounds;            // [num_blocks][Hkv][2][D]
   float* scales;             // [num_blocks][Hkv]
-  int32_t num_seqs, num_kv_heads, num_blocks, max_blocks;
+  int32_t num_seqs, num_kv_heads, num_blocks, max_blocks, num_tokens;
   int64_t num_items;         // upper limit of the (sequence, block) pairs
 };
 
@@ -74,12 +74,15 @@ __global__ void __launch_bounds__(kBoundWarps * 32) update_bounds_kernel(const B
     b = warp_search(a.num_seqs, item, lane, [&](int s) {
       return static_cast<int64_t>(__ldg(a.q_offsets + s)) / kBlockSize + 2 * static_cast<int64_t>(s);
     });
-    const int o0 = __ldg(a.q_offsets + b), n = __ldg(a.q_offsets + b + 1) - o0;
+    const int o0 = __ldg(a.q_offsets + b), o1 = __ldg(a.q_offsets + b + 1), n = o1 - o0;
     ctx = clamped_context(a.context_lens, b, a.max_blocks, lane == 0 && h == 0);
-    if (n <= 0 || o0 < 0) {
-      if (n < 0 || o0 < 0) flag_error(kErrOffsets);
+    // (The last offset tells of sequences that have no items for lack of room.)
+    if (unit == 0 && lane == 0 && __ldg(a.q_offsets + a.num_seqs) > a.num_tokens) flag_error(kErrOffsets);
+    if (o0 < 0 || o1 < o0 || o1 > a.num_tokens) {
+      if (lane == 0) flag_error(kErrOffsets);
       return;
     }
+    if (n == 0 || item < o0 / kBlockSize + 2 * static_cast<int64_t>(b)) return;
     const int64_t first = max(ctx - n, 0) / kBlockSize;
     const int64_t at = first + (item - (o0 / kBlockSize + 2 * static_cast<int64_t>(b)));
     if (at >= (ctx + kBlockSize - 1) / kBlockSize) return;

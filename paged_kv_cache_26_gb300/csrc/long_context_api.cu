@@ -248,9 +248,8 @@ int update_bounds_impl(const void* k_cache, const int32_t* block_tables, const i
   if (!k_cache || !bounds || !scales) return pkv_fail(PKV_ERR_INVALID_ARG, "update_bounds: NULL pointer");
   if (!aligned(k_cache, 16) || !aligned(bounds, 16) || !aligned(scales, 4) || !aligned(q_offsets, 4))
     return pkv_fail(PKV_ERR_INVALID_ARG, "update_bounds: misaligned pointer (cache and bounds need 16 bytes)");
-  pkv::BoundArgs a = {k_cache,          block_tables, context_lens,  q_offsets,
-                      bounds,           scales,       d->num_seqs,   d->num_kv_heads,
-                      d->num_blocks,    d->max_blocks_per_seq, 0};
+  pkv::BoundArgs a = {k_cache,      block_tables,        context_lens,  q_offsets, bounds, scales, d->num_seqs, d->num_kv_heads,
+                      d->num_blocks, d->max_blocks_per_seq, num_tokens, 0};
   // Where sequence b's items start, plus what the last can have (beside the kernel).
   a.num_items = q_offsets ? static_cast<int64_t>(num_tokens) / pkv::kBlockSize + 2 * static_cast<int64_t>(d->num_seqs)
                           : d->num_seqs;

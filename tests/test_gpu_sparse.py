@@ -49,7 +49,7 @@ def test_bounds(dtype, d, hk):
     off = np.concatenate([[0], np.cumsum(new)])
     rng = np.random.default_rng(0)
     b0, s0 = rng.integers(-127, 128, (nb, hk, 2, d)).astype(np.int8), rng.random((nb, hk)).astype(np.float32)
-    for offsets, many in ((off, int(off[-1])), (off, int(off[-1]) + 1000), (None, None)):
+    for offsets, many in ((off, int(off[-1])), (off, int(off[-1]) + 1000), (off + 37, int(off[-1]) + 37), (None, None)):
         bounds, scales = torch.from_numpy(b0).to(DEV, copy=True), torch.from_numpy(s0).to(DEV, copy=True)
         pkv.paged_kv_update_bounds(kp.to(DEV), i32(tables), i32(lens), bounds, scales,
                                    q_offsets=None if offsets is None else i32(offsets), num_tokens=many)
