@@ -941,20 +941,21 @@ def paged_kv_append_rope(q: Optional[torch.Tensor], k_new: torch.Tensor, v_new: 
     return q_out
 
 
-def _context_checks(q, caches, block_tables, context_lens, rows: int) -> int:
-    """Checks shared by the calls below: (q, caches) of one 16-bit type, the tables
-    and lengths of `rows` sequences (None: any), all on one device."""
-    dev, bt = caches[0].get_device(), block_tables.shape
-    dtype, cs = caches[0].dtype, caches[0].shape
-    if not (dev >= 0 and dtype in _DTYPE_CODE and all(c.get_device() == dev and c.dtype is dtype and c.is_contiguous() and
-                                                      c.shape == cs for c in caches) and len(cs) == 4 and
+def _context_checks(q, k_cache, v_cache, block_tables, context_lens, rows) -> int:
+    """Checks shared by the calls below: q (or None) and the caches of one 16-bit type,
+    the tables and lengths of `rows` sequences (None: any), all on one device."""
+    dev, bt, cs, dtype = k_cache.get_device(), block_tables.shape, k_cache.shape, k_cache.dtype
+    if not (dev >= 0 and dtype in _DTYPE_CODE and k_cache.is_contiguous() and len(cs) == 4 and
+            (v_cache is k_cache or (v_cache.get_device() == dev and v_cache.dtype is dtype and v_cache.is_contiguous() and
+                                    v_cache.shape == cs)) and
             block_tables.get_device() == dev and context_lens.get_device() == dev and block_tables.dtype is _i32 and
             context_lens.dtype is _i32 and block_tables.is_contiguous() and context_lens.is_contiguous() and
-            len(bt) == 2 and context_lens.shape == bt[:1] and (rows is None or rows == bt[0]) and
+            len(bt) == 2 and context_lens.dim() == 1 and context_lens.numel() == bt[0] and
+            (rows is None or rows == bt[0]) and
             (q is None or (q.get_device() == dev and q.dtype is dtype and q.is_contiguous() and q.dim() == 3 and
                            q.shape[2] == cs[3]))):
-        _need_cuda("caches", caches[0])
-        _explain(dev, ("caches", caches[-1], dtype), ("block_tables", block_tables, _i32),
+        _need_cuda("caches", k_cache)
+        _explain(dev, ("caches", v_cache, dtype), ("block_tables", block_tables, _i32),
                  ("context_lens", context_lens, _i32), ("q", q, dtype))
         raise ValueError("q must be [rows][num_q_heads][head_dim], the caches float16 or bfloat16 "
                          "[num_blocks][num_kv_heads][16][head_dim], block_tables [num_seqs][max_blocks], context_lens "
@@ -1003,7 +1004,7 @@ def paged_chunk_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
     context_lens[b] - n .. context_lens[b] - 1, and already in the caches.  Row i
     attends to positions 0 .. its own.  Rows outside the offsets keep what out
     holds.  Returns out."""
-    dev = _context_checks(q, (k_cache, v_cache), block_tables, context_lens, None)
+    dev = _context_checks(q, k_cache, v_cache, block_tables, context_lens, None)
     if not (q_offsets.get_device() == dev and q_offsets.dtype is _i32 and q_offsets.is_contiguous() and
             q_offsets.shape == (block_tables.shape[0] + 1,)):
         _explain(dev, ("q_offsets", q_offsets, _i32))
@@ -1041,7 +1042,7 @@ def paged_kv_update_bounds(k_cache: torch.Tensor, block_tables: torch.Tensor, co
     [NB][Hkv]) of the blocks that hold each sequence's new tokens, from all their
     valid keys.  One new token each, or those of q_offsets (as paged_chunk_attention),
     with num_tokens at least q_offsets[-1]."""
-    dev = _context_checks(None, (k_cache,), block_tables, context_lens, None)
+    dev = _context_checks(None, k_cache, k_cache, block_tables, context_lens, None)
     _check_bounds(bounds, bound_scales, k_cache.shape, dev)
     offsets = 0
     if q_offsets is not None:
@@ -1103,7 +1104,7 @@ def paged_decode_attention_sparse(q: torch.Tensor, k_cache: torch.Tensor, v_cach
     """paged_decode_attention over the tokens of the selected logical blocks only
     (int32 [B][Hkv][n], as paged_select_blocks gives them; negative entries are
     passed over).  Returns out."""
-    dev = _context_checks(q, (k_cache, v_cache), block_tables, context_lens, q.shape[0])
+    dev = _context_checks(q, k_cache, v_cache, block_tables, context_lens, q.shape[0])
     if not (selected.get_device() == dev and selected.dtype is _i32 and selected.is_contiguous() and
             selected.dim() == 3 and selected.shape[:2] == (q.shape[0], k_cache.shape[1])):
         _explain(dev, ("selected", selected, _i32))

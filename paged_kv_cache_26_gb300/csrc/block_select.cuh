@@ -320,7 +320,10 @@ __global__ void __launch_bounds__(kScoreThreads) score_blocks_kernel(const Selec
 // ===================================================================== choice
 
 constexpr int kSelectThreads = 1024;
-constexpr int kSelectCached = 32768;  // keys kept in shared memory (128 KB); more are read again
+constexpr int kSelectCached = 32768;  // keys kept in shared memory (132 KB); more are read again
+// A word in 33 is left out, so that threads on runs of neighbouring keys meet different
+// banks.
+__host__ __device__ constexpr int select_place(int i) { return i + (i >> 5); }
 
 // One CTA per (sequence, KV head): a radix selection finds the smallest chosen key
 // and how many of its equals are chosen, then one pass writes the chosen blocks in
@@ -349,8 +352,9 @@ __global__ void __launch_bounds__(kSelectThreads) select_blocks_kernel(const Sel
   // The blocks always kept rank above every score.
   auto fresh = [&](int i) { return i < a.sink || i >= nb - a.recent ? 0xffffffffu : __ldcg(keys + i); };
   if (cached)
-    for (int i = tid; i < nb; i += kSelectThreads) s_key[i] = fresh(i);
-  auto key_of = [&](int i) { return cached ? s_key[i] : fresh(i); };
+#pragma unroll 8
+    for (int i = tid; i < nb; i += kSelectThreads) s_key[select_place(i)] = fresh(i);
+  auto key_of = [&](int i) { return cached ? s_key[select_place(i)] : fresh(i); };
   if (tid == 0) {
     s_state[0] = 0;
     s_state[1] = static_cast<uint32_t>(want);

@@ -310,10 +310,10 @@ int select_blocks_impl(const pkv::SelectArgs& args, void* workspace, size_t work
     });
     if (e != cudaSuccess) return cuda_fail(e, "score_blocks_kernel launch");
   }
-  const int most = pkv::kSelectCached * 4;
+  const int most = pkv::select_place(pkv::kSelectCached) * 4 + 4;
   e = configure_smem<pkv::select_blocks_kernel>(most);
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(select_blocks_kernel)");
-  const size_t smem = scored ? std::min<size_t>(static_cast<size_t>(a.max_blocks) * 4, most) : 0;
+  const size_t smem = scored ? pkv::select_place(std::min(a.max_blocks, pkv::kSelectCached)) * 4 + 4 : 0;
   e = launch_dependent(pkv::select_blocks_kernel, dim3(d->num_kv_heads, d->num_seqs), 1, pkv::kSelectThreads, smem, stream,
                        a);
   if (e != cudaSuccess) return cuda_fail(e, "select_blocks_kernel launch");
@@ -361,8 +361,7 @@ int decode_sparse_impl(const void* q, const void* k_cache, const void* v_cache, 
   with_type_and_dim(d, [&](auto t, auto dim) {
     constexpr int D = decltype(dim)::value;
     constexpr auto kern = pkv::decode_sparse_kernel<decltype(t), D>;
-    e = configure_smem<kern>(pkv::SparseShape<D>::kSmem);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    e = configure_smem<kern>(pkv::SparseShape<D>::kSmem, true);
     if (e == cudaSuccess)
       e = launch_dependent(kern, dim3(cluster, d->num_kv_heads, d->num_seqs), cluster, pkv::kSparseWarps * 32,
                            pkv::SparseShape<D>::kSmem, stream, mk, mv, a, selected, num_selected,

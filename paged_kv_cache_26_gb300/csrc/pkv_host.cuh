@@ -146,9 +146,10 @@ MapCache g_maps;
 
 // Raise a kernel's dynamic shared-memory limit once per device (and ask for
 // the largest shared-memory carveout).  The kernel is a template argument so
-// that every kernel instantiation keeps its own flags.
+// that every kernel instantiation keeps its own flags.  wide_clusters: of more than
+// eight CTAs.
 template <auto kern>
-cudaError_t configure_smem(int bytes) {
+cudaError_t configure_smem(int bytes, bool wide_clusters = false) {
   static bool done[kMaxDevices] = {};
   int dev = 0;
   cudaGetDevice(&dev);
@@ -156,6 +157,7 @@ cudaError_t configure_smem(int bytes) {
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+  if (e == cudaSuccess && wide_clusters) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e == cudaSuccess && dev < kMaxDevices) done[dev] = true;
   return e;
 }
