@@ -16,10 +16,12 @@
 // half turns in [-1, 1) for sincospif.  Three integer multiplications instead of
 // float64 arithmetic.
 //
-// Bound by the bytes of the rows.  A CTA takes up to kRopeTokens tokens, makes
-// their sines and cosines once in shared memory (they are shared by every head)
-// and then treats all rows alike, two 16-byte vectors a thread and step: the
-// eight pairs of eight neighbouring frequencies.
+// Bound by the bytes of the rows: 16,384 tokens of 32 + 8 + 8 heads, D = 128, bf16 (403
+// MB in and out) take 68 us, 5.9 TB/s.  A CTA takes up to four tokens, makes their sines
+// and cosines once in shared memory (every head shares them), its first rows already
+// on their way, and then treats all rows alike, two 16-byte vectors a thread and step:
+// the eight pairs of eight neighbouring frequencies.  (Eight tokens a CTA 70 us, sixteen
+// 75, the next step's loads ahead of this one's stores 75: fewer threads fit.)
 #pragma once
 
 #include "paged_kv_kernels.cuh"
@@ -27,7 +29,7 @@
 namespace pkv {
 
 constexpr int kRopeThreads = 256;
-constexpr int kRopeTokens = 8;   // tokens of a CTA, at most
+constexpr int kRopeTokens = 4;   // tokens of a CTA, at most
 constexpr int kMaxFreqs = 64;
 
 struct RopeArgs {
@@ -98,25 +100,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
   const int t0 = blockIdx.x * a.tokens_per_cta;
   const int nt = min(a.tokens_per_cta, a.num_tokens - t0);
   asm volatile("griddepcontrol.wait;" ::: "memory");
-
-  for (int i = threadIdx.x; i < nt * a.freqs; i += kRopeThreads) {
-    const int t = i / a.freqs, f = i - t * a.freqs;
-    const int axis = static_cast<int>(a.axis_bits[f >> 5] >> (2 * (f & 31))) & 3;
-    const int64_t pos = a.positions[static_cast<int64_t>(axis) * a.num_tokens + t0 + t];
-    const uint64_t turn = static_cast<uint64_t>(pos) * a.turns[f];
-    float s, c;
-    sincospif(static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f, &s, &c);
-    s_cs[t * a.freqs + f] = make_float2(c * a.factor, s * a.factor);
-  }
-  if (DST != kRopeRows && threadIdx.x < static_cast<unsigned>(nt)) {
-    int64_t slot = a.slots[t0 + threadIdx.x];
-    if (slot >= a.num_slots) {
-      flag_error(kErrSlot);
-      slot = -1;
-    }
-    s_slot[threadIdx.x] = slot;
-  }
-  __syncthreads();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   const int pairs = a.head_vecs >> 1;                 // steps of two vectors in a row: 4 or 8
   const int shift = pairs == 8 ? 3 : 2;
@@ -125,7 +109,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
   const int total = nt * rows << shift;
 
   struct Step {
-    int t, h, kind, j;  // kind 0: query, 1: key, 2: value; j < 0: skipped
+    int t, h, kind, j;  // kind 0: query, 1: key, 2: value
     int64_t lo, hi;     // the two vectors, from the row's start
   };
   auto locate = [&](int i) {
@@ -160,6 +144,29 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
     x = p[s.lo];
     y = p[s.hi];
   };
+  Step s0 = locate(min(static_cast<int>(threadIdx.x), total - 1)), s1 = locate(min(static_cast<int>(threadIdx.x) + kRopeThreads, total - 1));
+  uint4 x0, y0, x1, y1;
+  load(s0, x0, y0);
+  load(s1, x1, y1);
+  for (int i = threadIdx.x; i < nt * a.freqs; i += kRopeThreads) {
+    const int t = i / a.freqs, f = i - t * a.freqs;
+    const int axis = static_cast<int>(a.axis_bits[f >> 5] >> (2 * (f & 31))) & 3;
+    const int64_t pos = a.positions[static_cast<int64_t>(axis) * a.num_tokens + t0 + t];
+    const uint64_t turn = static_cast<uint64_t>(pos) * a.turns[f];
+    float s, c;
+    sincospif(static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f, &s, &c);
+    s_cs[t * a.freqs + f] = make_float2(c * a.factor, s * a.factor);
+  }
+  if (DST != kRopeRows && threadIdx.x < static_cast<unsigned>(nt)) {
+    int64_t slot = a.slots[t0 + threadIdx.x];
+    if (slot >= a.num_slots) {
+      flag_error(kErrSlot);
+      slot = -1;
+    }
+    s_slot[threadIdx.x] = slot;
+  }
+  __syncthreads();
+
   auto store = [&](const Step& s, uint4 x, uint4 y) {
     if (s.kind != 2 && s.j < rot) rotate8<T>(x, y, s_cs + s.t * a.freqs + 8 * s.j, a.interleaved);
     if (s.kind == 0 || DST == kRopeRows) {
@@ -184,15 +191,15 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
       p[s.hi] = quantize8<T>(y, scale);
     }
   };
-  // Two steps' loads in flight.
-  for (int i = threadIdx.x; i < total; i += 2 * kRopeThreads) {
-    const bool two = i + kRopeThreads < total;
-    const Step s0 = locate(i), s1 = locate(two ? i + kRopeThreads : i);
-    uint4 x0, y0, x1, y1;
+  for (int i = threadIdx.x; i < total;) {
+    store(s0, x0, y0);
+    if (i + kRopeThreads < total) store(s1, x1, y1);
+    i += 2 * kRopeThreads;
+    if (i >= total) break;
+    s0 = locate(i);
+    s1 = locate(min(i + kRopeThreads, total - 1));
     load(s0, x0, y0);
     load(s1, x1, y1);
-    store(s0, x0, y0);
-    if (two) store(s1, x1, y1);
   }
 }
 
