@@ -614,9 +614,10 @@ int paged_kv_append_rope(const void* q, const void* k_new, const void* v_new, co
  * NaN in fp16 where the weight, below 2^-25, rounds to 0.
  * workspace (device): paged_chunk_workspace_bytes(dims) bytes, 256-byte aligned;
  * its contents need no initialisation.  Calls that share it must not overlap.
- * Limits: dims as paged_decode_attention; at most 2048 sequences; num_seqs *
- * num_kv_heads * num_tokens below 2^40.  Offsets that fall or leave [0, num_tokens]
- * are flagged (PKV_ERR_OUT_OF_RANGE from paged_kv_check_status) and limited.
+ * Limits: dims as paged_decode_attention; at most 8192 sequences, 2^26 blocks a table
+ * and (num_tokens / 32 + num_seqs) (16 max_blocks + num_tokens + 256) Hkv below
+ * 4 * 10^18.  Offsets that fall or leave [0, num_tokens] are flagged
+ * (PKV_ERR_OUT_OF_RANGE from paged_kv_check_status) and limited.
  * ---------------------------------------------------------------------- */
 int paged_chunk_attention(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
                           const int32_t* context_lens, const int32_t* q_offsets, int32_t num_tokens, float scale,

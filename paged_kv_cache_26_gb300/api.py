@@ -831,7 +831,8 @@ def _rows(name: str, t: torch.Tensor, dev: int, dtype, tokens: int, d: int):
         if t.dtype is not dtype:
             raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
         raise ValueError(f"{name} must be [num_tokens][heads][head_dim] with a unit stride along head_dim")
-    return t.data_ptr(), st[0], st[1]
+    # (a dim of one element has whatever stride)
+    return t.data_ptr(), st[0] if tokens > 1 else 0, st[1] if t.shape[1] > 1 else 0
 
 
 def _rope_positions(positions: torch.Tensor, rope: Rope, dev: int, tokens: int) -> None:

@@ -194,6 +194,8 @@ int chunk_attention_impl(const void* q, const void* k_cache, const void* v_cache
   if (!workspace || workspace_bytes < need || !aligned(workspace, 256))
     return pkv_fail(PKV_ERR_INVALID_ARG, "chunk_attention: workspace missing, too small (" + std::to_string(need) +
                                              " bytes needed) or not 256-byte aligned");
+  if (d->max_blocks_per_seq > (1 << 26))
+    return pkv_fail(PKV_ERR_UNSUPPORTED, "chunk_attention: at most 2^26 blocks a table");
   // The line of work is counted in 64 bits.
   const double keys = (num_tokens / 32.0 + d->num_seqs) * (16.0 * d->max_blocks_per_seq + num_tokens + 256.0) * d->num_kv_heads;
   if (keys > 4e18) return pkv_fail(PKV_ERR_UNSUPPORTED, "chunk_attention: too many tokens, heads and keys");

@@ -152,6 +152,17 @@ def test_slots_outside_the_pool_are_flagged():
     pkv.paged_kv_check_status()
 
 
+def test_dims_of_one_element_have_any_stride():
+    rope = pkv.make_rope(freqs(32), 64)
+    x = rand((7, 3, 64), torch.float16, 0).to(DEV)
+    want = pkv.paged_kv_rope(x, x[:, :1].contiguous(), i32(range(7)), rope)
+    odd = torch.as_strided(x, (7, 1, 64), (192, 5, 1))
+    got = pkv.paged_kv_rope(x, odd, i32(range(7)), rope)
+    assert torch.equal(got[1], want[1])
+    one = torch.as_strided(x, (1, 3, 64), (3, 64, 1))
+    assert torch.equal(pkv.paged_kv_rope(one, one, i32([0]), rope)[0], x[:1])
+
+
 def test_no_tokens_other_stream_and_capture():
     rope = pkv.make_rope(freqs(64), 128)
     empty = torch.empty(0, 2, 128, dtype=torch.float16, device=DEV)
