@@ -635,7 +635,9 @@ size_t paged_chunk_workspace_bytes(const pkv_dims* dims);
  *   floor(min_t K[t][d] / scale), limited to +-127 (0 where scale is 0).  If a
  *   value is not finite: scale infinity, upper 127, lower -127 for every d.
  *   bounds : int8[num_blocks][Hkv][2][D] (upper, lower); scales :
- *   float32[num_blocks][Hkv].  Copies of blocks (copy-on-write) copy these too.
+ *   float32[num_blocks][Hkv].  They belong to the physical block: paged_kv_copy_blocks
+ *   leaves them alone, so a copied block has none until the caller copies them or an
+ *   update covers the block (that of the token appended to the copy does).
  * Score of block j for KV head x, each query head h of its group having r =
  *   max |q_h| * float32(1/127), c[d] = round_half_even(q_h[d] / r) (0 where r is 0, or
  *   a query value is not finite): max over h of (S * scale) * r, two float32 products

@@ -14,7 +14,14 @@
 // softmax of one tile runs under the products of the other.  Either tile has an
 // issuing warp of its own: an MMA waits in its thread until the tensor pipe can
 // queue it, and a barrier that is ready costs 100 to 200 cycles, which the pipe would
-// spend idle behind a single thread.
+// spend idle behind a single thread (438 us against 361, at the size below).
+//
+// Bound by the tensor pipe and the exponentials beside it.  2,048 new tokens after
+// 14,000, 32 query and 8 KV heads, bf16: D = 128 315 us (1.60 PFLOP/s of the measured
+// 1.92; the tensor pipe is busy for 75 % of the main kernel's 294 us), D = 64 258 us,
+// where a key costs half the products and the same exponentials.  2,048 tokens after
+// 63,001: 1.51 ms (1.43 PFLOP/s).  A step of 64 single tokens of 2,000 to 4,000 tokens
+// each 134 us: two of a tile's 128 rows hold a token's group, and K and V bound it.
 //
 // Work is divided by keys, not by units: the units' keys (plus a fixed amount for
 // a unit's start and end) form one line which is cut into equal parts, one per
@@ -49,7 +56,9 @@ constexpr int kChunkThreads = 384;
 constexpr int kMaxChunkSeqs = 8192;
 constexpr int kChunkPieces = 4;            // pieces known ahead
 constexpr int kChunkSteps = 16;            // barriers of steps: more than can be under way (a tile of the ring each)
-constexpr int kEarly = 1;                  // quarters of a tile's weights whose product begins before the others are made
+// Quarters of a tile's weights whose product begins before the others are made: 1 315 us,
+// 2 339, 3 361, all at once 348; an arrival for every quarter 346, half a quarter 329.
+constexpr int kEarly = 1;
 // A unit's start and end (first loads, first softmax, output) in keys, and the least
 // number of keys worth a CTA of its own.
 constexpr int kUnitKeys = 128;
@@ -575,7 +584,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           slot = slot + 1 == NS ? 0 : slot + 1;
           return x;
         };
-        // A and B issue in turn.
+        // A and B issue in turn: left to themselves they fall into phase, both tiles'
+        // products queued at once and then both softmaxes (461 us against 361).
         uint32_t turns = 0;
         auto my_turn = [&]() {
           const uint32_t n = turns++;
@@ -760,7 +770,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             for (int i = 0; i < 4; ++i) y[i] = exp2_approx(y[i]);
             sum2(l0, l1, y[0], y[1]);
             sum2(l2, l3, y[2], y[3]);
-            // Weights rounded to T: 2^-9 (bf16) or 2^-12 (fp16) of each at most, beside an
+            // Weights rounded to T: 2^-8 (bf16) or 2^-11 (fp16) of each at most, beside an
             // output rounded to T; two terms would double the product's work.
             pk[k] = pack2<T>(y[0], y[1]);
             pk[k + 1] = pack2<T>(y[2], y[3]);
@@ -911,8 +921,10 @@ constexpr int kChunkMergeThreads = 256;
 constexpr int kChunkMergeRows = 32;
 
 // CTA (c, y) joins the pieces of the unit inside which CTA c's part begins, if that is
-// the unit's first cut, for 32 of its rows, four a warp: the last piece of CTA c - 1, the first of CTA c, and those of the CTAs after
-// it as long as their whole part lay in the unit.
+// the unit's first cut, for 32 of its rows, four a warp: the last piece of CTA c - 1,
+// the first of CTA c, and those of the CTAs after it as long as their whole part lay in
+// the unit.  40 MB of partial results at most; 9 to 12 us, a chain of cut, pieces, row.
+// (Finding the cuts from the lengths again instead of reading them: 34 us.)
 template <typename T, int D>
 __global__ void __launch_bounds__(kChunkMergeThreads) merge_chunk_kernel(const ChunkArgs a) {
   using Shape = ChunkShape<D>;
