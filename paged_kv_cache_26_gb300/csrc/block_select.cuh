@@ -51,8 +51,9 @@ __device__ __forceinline__ int warp_search(int n, int64_t x, int lane, F&& start
 // One warp per (block, KV head): 16 lanes (8 at D = 64) across a row, 16 bytes
 // each, the rows split over the rest of the warp, so a tile is read whole in
 // 4 (D = 64) or 8 loads a lane, all in flight.  Extremes are exact on packed pairs.
-// Bound by the bytes of the tiles where they are many (1,134 blocks of 8 heads,
-// D = 128), by the chain table, tile, result where they are few.
+// Bound by the bytes of the tiles where they are many (the blocks of 8 prompts, 18,000
+// tokens, 8 heads, D = 128: 39.5 MB in 8.4 us, 4.7 TB/s with launch and ramp), by the
+// chain offsets, table, tile, result where they are few (61 sequences: 3.4 us).
 template <typename T, int D>
 __global__ void __launch_bounds__(kBoundWarps * 32) update_bounds_kernel(const BoundArgs a) {
   constexpr int kLanes = D / 8;             // lanes of a row
@@ -175,8 +176,8 @@ struct SelectArgs {
   int32_t num_selected, sink, recent;
 };
 
-constexpr int kScoreThreads = 256;
-constexpr int kScoreBlocks = 256;  // blocks of a CTA
+constexpr int kScoreThreads = 128;
+constexpr int kScoreBlocks = 128;  // blocks of a CTA: a lane's each
 
 // Unsigned numbers in the order of the floats (there is no -0 among them); NaN as
 // +infinity.
@@ -185,53 +186,84 @@ __device__ __forceinline__ uint32_t ordered_key(float x) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// A CTA scores 256 blocks of one (sequence, KV head) for its G >= group heads.
-// A row of bounds is 2 D bytes: 16 lanes (8 at D = 64) read it whole, 16 bytes
-// each, upper bounds in the first half of them; they keep the query's codes for
-// their bytes in registers, the positive ones against the upper bounds, the
-// negative ones against the lower, as four-way byte products.  The G sums are then
-// folded over the lanes, half of the sums going either way in each exchange.
-// Bound by the bytes of the bounds, for G = 8 by the byte products.
+__device__ __forceinline__ void copy_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// A CTA scores 128 blocks of one (sequence, KV head) for its G >= group heads, a warp 32.
+// The warp starts the copies of all its rows of bounds (2 D bytes each) at once, 8 KB at
+// D = 128, without a register for them; the query's codes are made while they come.
+// max(4, G) lanes share a row, 16 bytes at a time, upper bounds in its first half; they
+// keep the codes for their bytes in registers, the positive ones against the upper
+// bounds, the negative ones against the lower, as four-way byte products.  The G sums are
+// then folded over the lanes, half of the sums going either way in each exchange, after
+// which a lane holds one head's.
+// Bound by the latency of table, bounds and their bytes: with the choice after it, 32
+// sequences of 8,192 to 32,768 tokens, 8 KV heads, G = 4, D = 128 (85 MB) take 25.6 us,
+// 131,072 tokens of one sequence, G = 8 (17 MB) 13.3.  (Loads through registers, eight a
+// lane under way, 16 lanes a row: 37.7 and 21.8 with the choice of that time; four lanes
+// a row and loads through registers: 6 us slower than copies at G = 4, as fewer CTAs fit.
+// The products as s8 tensor products: no gain over byte products.)
 template <typename T, int D, int G>
 __global__ void __launch_bounds__(kScoreThreads) score_blocks_kernel(const SelectArgs a) {
-  constexpr int kLanes = D / 8;
-  constexpr int kRows = 32 / kLanes;                 // blocks of a warp's load
+  constexpr int kLanes = G == 8 ? 8 : 4;
+  constexpr int kPieces = 2 * D / 16;                // 16-byte pieces of a row
+  constexpr int kTurns = kPieces / kLanes;
+  constexpr int kRows = 32 / kLanes;                 // blocks of a warp's step
   constexpr int kWarps = kScoreThreads / 32;
-  constexpr int kPer = kScoreBlocks / kWarps / kRows;  // steps of a warp
-  constexpr int kBatch = G == 8 ? 4 : 8;             // loads in flight
-  static_assert(kPer % kBatch == 0, "whole batches");
+  static_assert(kScoreBlocks == kScoreThreads, "a block a lane");
+  __shared__ __align__(128) uint4 s_rows[kScoreBlocks * kPieces];
   __shared__ __align__(16) int32_t s_code[G][D / 4];
   __shared__ float s_scale[G];
-  __shared__ int32_t s_phys[kScoreBlocks];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int h = blockIdx.y, b = blockIdx.z, first = blockIdx.x * kScoreBlocks;
+  // The heads of a range side by side, so that their pieces of a block, neighbours in
+  // memory, are read at about the same time.
+  const int h = blockIdx.x % a.num_kv_heads, b = blockIdx.y, first = blockIdx.x / a.num_kv_heads * kScoreBlocks;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int ctx = clamped_context(a.context_lens, b, a.max_blocks, threadIdx.x == 0 && blockIdx.x == 0 && h == 0);
+  const int block = first + threadIdx.x;             // this lane's
+  int phys = block < a.max_blocks ? __ldg(a.block_tables + static_cast<int64_t>(b) * a.max_blocks + block) : -1;
+  constexpr int kVals = D / 32, kHeads = (G + kWarps - 1) / kWarps;  // values of a lane, heads of a warp
+  float x[kHeads][kVals];
+#pragma unroll
+  for (int n = 0; n < kHeads; ++n) {
+    const int g = warp + n * kWarps;
+    const T* q = static_cast<const T*>(a.q) + (static_cast<int64_t>(b) * a.num_q_heads + h * a.group + g) * D;
+#pragma unroll
+    for (int i = 0; i < kVals; ++i) x[n][i] = g < a.group ? static_cast<float>(q[lane * kVals + i]) : 0.f;
+  }
+  const int ctx = clamped_context(a.context_lens, b, a.max_blocks, threadIdx.x == 0 && blockIdx.x == 0);
   const int nb = (ctx + kBlockSize - 1) / kBlockSize;
   if (first >= nb || nb <= a.num_selected) return;   // none, or all chosen without scores
-  {
-    const int j = first + threadIdx.x;
-    int phys = -1;
-    if (j < nb) {
-      phys = __ldg(a.block_tables + static_cast<int64_t>(b) * a.max_blocks + j);
-      if (phys < 0 || phys >= a.num_blocks) {
-        if (h == 0) flag_error(kErrBlockId);
-        phys = -1;
-      }
-    }
-    s_phys[threadIdx.x] = phys;
+  if (block >= nb) {
+    phys = -1;
+  } else if (phys < 0 || phys >= a.num_blocks) {
+    if (h == 0) flag_error(kErrBlockId);
+    phys = -1;
   }
-  if (warp < G) {
-    constexpr int kVals = D / 32;
-    float x[kVals], top = 0.f;
-    const T* q = static_cast<const T*>(a.q) + (static_cast<int64_t>(b) * a.num_q_heads + h * a.group + warp) * D;
+  // Without a block: a scale of 0, whatever lies in the row.
+  const float my_step = phys >= 0 ? __ldg(a.scales + static_cast<int64_t>(phys) * a.num_kv_heads + h) : 0.f;
+  uint4* rows = s_rows + warp * 32 * kPieces;
+  // In odd rows the halves of 64 bytes change places: four lanes a row meet all banks.
+  auto place = [](int r, int piece) { return r * kPieces + (piece ^ ((r & 1) << 2)); };
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i) {
+    const int r = i * (32 / kPieces) + lane / kPieces, piece = lane % kPieces;
+    const int p = __shfl_sync(0xffffffffu, phys, r);
+    if (p >= 0)
+      copy_async16(smem_u32(rows + place(r, piece)),
+                   a.bounds + (static_cast<int64_t>(p) * a.num_kv_heads + h) * (2 * D) + 16 * piece);
+  }
+#pragma unroll
+  for (int n = 0; n < kHeads; ++n) {
+    const int g = warp + n * kWarps;
+    if (g >= G) break;
+    float top = 0.f;
     bool finite = true;
 #pragma unroll
     for (int i = 0; i < kVals; ++i) {
-      x[i] = warp < a.group ? static_cast<float>(q[lane * kVals + i]) : 0.f;
-      finite = finite && fabsf(x[i]) < INFINITY;
-      top = fmaxf(top, fabsf(x[i]));
+      finite = finite && fabsf(x[n][i]) < INFINITY;
+      top = fmaxf(top, fabsf(x[n][i]));
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -239,88 +271,87 @@ __global__ void __launch_bounds__(kScoreThreads) score_blocks_kernel(const Selec
     const float s = finite ? __fmul_rn(top, 1.f / 127.f) : 0.f;
 #pragma unroll
     for (int i = 0; i < kVals; ++i)
-      reinterpret_cast<int8_t*>(s_code[warp])[lane * kVals + i] =
-          static_cast<int8_t>(s > 0.f ? static_cast<int>(rintf(__fdiv_rn(x[i], s))) : 0);
-    if (lane == 0) s_scale[warp] = s;
+      reinterpret_cast<int8_t*>(s_code[g])[lane * kVals + i] =
+          static_cast<int8_t>(s > 0.f ? static_cast<int>(rintf(__fdiv_rn(x[n][i], s))) : 0);
+    if (lane == 0) s_scale[g] = s;
   }
   __syncthreads();
   const int sub = lane % kLanes, grp = lane / kLanes;
-  const bool upper = sub < kLanes / 2;
-  int32_t code[G][4];
+  int32_t code[G][kTurns][4];
 #pragma unroll
-  for (int g = 0; g < G; ++g) {
-    const int4 c = *reinterpret_cast<const int4*>(&s_code[g][4 * (sub % (kLanes / 2))]);
-    const int32_t w[4] = {c.x, c.y, c.z, c.w};
+  for (int g = 0; g < G; ++g)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      // Bytes of the other sign are cleared: all ones in the negative bytes.
-      const uint32_t neg = __vcmplts4(static_cast<uint32_t>(w[i]), 0u);
-      code[g][i] = static_cast<int32_t>(upper ? w[i] & ~neg : w[i] & neg);
+    for (int t = 0; t < kTurns; ++t) {
+      const int piece = t * kLanes + sub;
+      const int4 c = *reinterpret_cast<const int4*>(&s_code[g][4 * (piece % (kPieces / 2))]);
+      const int32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        // Bytes of the other sign are cleared: all ones in the negative bytes.
+        const uint32_t neg = __vcmplts4(static_cast<uint32_t>(w[i]), 0u);
+        code[g][t][i] = static_cast<int32_t>(piece < kPieces / 2 ? w[i] & ~neg : w[i] & neg);
+      }
     }
-  }
-  const int base = warp * (kScoreBlocks / kWarps);
-  uint32_t* keys = a.keys + (static_cast<int64_t>(b) * a.num_kv_heads + h) * a.max_blocks + first;
-  for (int i0 = 0; i0 < kPer; i0 += kBatch) {
-    if (first + base + i0 * kRows >= nb) break;
-    uint4 e[kBatch];
-    float step[kBatch];
+  // After the exchanges below, a lane's sum is of this head.
+  int head = 0;
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      const int phys = s_phys[base + (i0 + k) * kRows + grp];
-      const int64_t tile = static_cast<int64_t>(max(phys, 0)) * a.num_kv_heads + h;
-      e[k] = phys >= 0 ? __ldg(reinterpret_cast<const uint4*>(a.bounds + tile * (2 * D)) + sub) : make_uint4(0, 0, 0, 0);
-      step[k] = phys >= 0 ? __ldg(a.scales + tile) : 0.f;
-    }
+  for (int n = G / 2, o = 1; n > 0; n /= 2, o *= 2)
+    if (lane & o) head += n;
+  const float head_scale = s_scale[head];
+  uint32_t* keys = a.keys + (static_cast<int64_t>(b) * a.num_kv_heads + h) * a.max_blocks + first + warp * 32;
+  const int mine = nb - first - warp * 32;           // blocks of this warp, or more
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncwarp();
+  if (mine <= 0) return;
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      int32_t dot[G];
+  for (int r0 = 0; r0 < 32; r0 += kRows) {
+    const int r = r0 + grp;
+    int32_t dot[G];
+#pragma unroll
+    for (int g = 0; g < G; ++g) dot[g] = 0;
+#pragma unroll
+    for (int t = 0; t < kTurns; ++t) {
+      const uint4 e = rows[place(r, t * kLanes + sub)];
 #pragma unroll
       for (int g = 0; g < G; ++g) {
-        dot[g] = __dp4a(code[g][0], static_cast<int32_t>(e[k].x), 0);
-        dot[g] = __dp4a(code[g][1], static_cast<int32_t>(e[k].y), dot[g]);
-        dot[g] = __dp4a(code[g][2], static_cast<int32_t>(e[k].z), dot[g]);
-        dot[g] = __dp4a(code[g][3], static_cast<int32_t>(e[k].w), dot[g]);
-      }
-      // Exchange halves: after it a lane holds the heads whose bits match its own.
-      int n = G, o = 1;
-      int head = 0;
-#pragma unroll
-      for (int r = 0; (1 << r) < kLanes; ++r) {
-        if (n > 1) {
-          const bool odd = lane & o;
-#pragma unroll
-          for (int g = 0; g < G / 2; ++g) {
-            if (g >= n / 2) break;
-            const int32_t give = odd ? dot[g] : dot[g + n / 2];
-            const int32_t keep = odd ? dot[g + n / 2] : dot[g];
-            dot[g] = keep + __shfl_xor_sync(0xffffffffu, give, o);
-          }
-          if (odd) head += n / 2;
-          n /= 2;
-        } else {
-          dot[0] += __shfl_xor_sync(0xffffffffu, dot[0], o);
-        }
-        o *= 2;
-      }
-      // A NaN (0 times an infinite scale) is +infinity, as in ordered_key.
-      // Adding 0 makes a product that underflowed to -0 the equal of +0.
-      float score = __fadd_rn(__fmul_rn(__fmul_rn(static_cast<float>(dot[0]), step[k]), s_scale[head]), 0.f);
-      if (head >= a.group) score = -INFINITY;
-      uint32_t key = ordered_key(score);
-#pragma unroll
-      for (int m = 1; m < G; m *= 2) key = max(key, __shfl_xor_sync(0xffffffffu, key, m));
-      if (sub == 0) {
-        const int j = base + (i0 + k) * kRows + grp;
-        if (first + j < nb) keys[j] = key;
+        dot[g] = __dp4a(code[g][t][0], static_cast<int32_t>(e.x), dot[g]);
+        dot[g] = __dp4a(code[g][t][1], static_cast<int32_t>(e.y), dot[g]);
+        dot[g] = __dp4a(code[g][t][2], static_cast<int32_t>(e.z), dot[g]);
+        dot[g] = __dp4a(code[g][t][3], static_cast<int32_t>(e.w), dot[g]);
       }
     }
+    // Exchange halves while there are several sums, then add.
+#pragma unroll
+    for (int o = 1, n = G; o < kLanes; o *= 2, n = n > 1 ? n / 2 : 1) {
+      if (n > 1) {
+        const bool odd = lane & o;
+#pragma unroll
+        for (int g = 0; g < n / 2; ++g) {
+          const int32_t give = odd ? dot[g] : dot[g + n / 2];
+          const int32_t keep = odd ? dot[g + n / 2] : dot[g];
+          dot[g] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+        }
+      } else {
+        dot[0] += __shfl_xor_sync(0xffffffffu, dot[0], o);
+      }
+    }
+    // A NaN (0 times an infinite scale) is +infinity, as in ordered_key.
+    // Adding 0 makes a product that underflowed to -0 the equal of +0.
+    const float step = __shfl_sync(0xffffffffu, my_step, r);
+    float score = __fadd_rn(__fmul_rn(__fmul_rn(static_cast<float>(dot[0]), step), head_scale), 0.f);
+    if (head >= a.group) score = -INFINITY;
+    uint32_t key = ordered_key(score);
+#pragma unroll
+    for (int m = 1; m < G; m *= 2) key = max(key, __shfl_xor_sync(0xffffffffu, key, m));
+    if (sub == 0 && r < mine) keys[r] = key;
   }
 }
 
 // ===================================================================== choice
 
-constexpr int kSelectThreads = 1024;
-constexpr int kSelectCached = 32768;  // keys kept in shared memory (132 KB); more are read again
+constexpr int kSelectThreads = 1024;  // of a CTA; 256 for tables of up to 2,048 blocks (below)
+constexpr int kSelectRun = 8;         // keys that a thread holds in registers, at most
+constexpr int kSelectCached = 32768;  // keys of longer contexts held in shared memory (132 KB); past it they are read again
 // A word in 33 is left out, so that threads on runs of neighbouring keys meet different
 // banks.
 __host__ __device__ constexpr int select_place(int i) { return i + (i >> 5); }
@@ -328,53 +359,64 @@ __host__ __device__ constexpr int select_place(int i) { return i + (i >> 5); }
 // One CTA per (sequence, KV head): a radix selection finds the smallest chosen key
 // and how many of its equals are chosen, then one pass writes the chosen blocks in
 // rising order: a thread takes a run of neighbouring blocks and learns from one
-// scan how many lie before it.  Bound by that chain (loads, four rounds of counting
-// and three barriers each, the scan); the keys are few bytes.
-__global__ void __launch_bounds__(kSelectThreads) select_blocks_kernel(const SelectArgs a) {
+// scan how many lie before it.  Runs of up to kSelectRun blocks stay in registers; a
+// thread holds so many, so the CTA is as small as the table allows, 256 threads up to
+// 2,048 blocks (its barriers cost less, and 1,024 threads of 64 registers are alone on
+// their SM: 32 x 8 choices were then 2.5 us slower than with keys in shared memory).  Bound by the chain of loads, up to four rounds of counting with two
+// barriers each, and the scan: about 6 us for 8,192 blocks (keys in shared memory 9); the
+// keys are few bytes.  (Scores and choice in one kernel, a cluster a (sequence, KV head):
+// 40 us against 28, as both then were, for the whole step of 131,072 tokens.)
+template <int kThreads, bool kRegs, typename Fresh>
+__device__ __forceinline__ void choose_blocks(const Fresh& fresh, int nb, uint32_t left, int32_t* out) {
   extern __shared__ uint32_t s_key[];
-  __shared__ uint32_t s_hist[256];
-  __shared__ uint32_t s_state[2];        // prefix found so far, how many still to choose among it
+  __shared__ __align__(16) uint32_t s_hist[4][256];
+  __shared__ uint32_t s_state[3];        // prefix found so far, how many still to choose among its bin, all of it
   __shared__ uint32_t s_warp[2][33];
-  const int h = blockIdx.x, b = blockIdx.y;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int ctx = clamped_context(a.context_lens, b, a.max_blocks, false);
-  const int nb = (ctx + kBlockSize - 1) / kBlockSize;
-  const int64_t unit = static_cast<int64_t>(b) * a.num_kv_heads + h;
-  int32_t* out = a.selected + unit * a.num_selected;
-  const int want = min(nb, a.num_selected);
-  for (int i = (nb <= a.num_selected ? 0 : want) + tid; i < a.num_selected; i += kSelectThreads) out[i] = i < nb ? i : -1;
-  if (nb <= a.num_selected) return;
-
-  const uint32_t* keys = a.keys + unit * a.max_blocks;
+  const int per = (nb + kThreads - 1) / kThreads;
+  const int i0 = min(tid * per, nb), i1 = min(i0 + per, nb);
   const bool cached = nb <= kSelectCached;
-  // The blocks always kept rank above every score.
-  auto fresh = [&](int i) { return i < a.sink || i >= nb - a.recent ? 0xffffffffu : __ldcg(keys + i); };
-  if (cached)
+  uint32_t run[kSelectRun];
+  if (kRegs) {
+#pragma unroll
+    for (int j = 0; j < kSelectRun; ++j) run[j] = i0 + j < i1 ? fresh(i0 + j) : 0;
+  } else if (cached) {
 #pragma unroll 8
-    for (int i = tid; i < nb; i += kSelectThreads) s_key[select_place(i)] = fresh(i);
-  auto key_of = [&](int i) { return cached ? s_key[select_place(i)] : fresh(i); };
-  if (tid == 0) {
-    s_state[0] = 0;
-    s_state[1] = static_cast<uint32_t>(want);
+    for (int i = tid; i < nb; i += kThreads) s_key[select_place(i)] = fresh(i);
   }
+#pragma unroll
+  for (int i = tid; i < 1024; i += kThreads) s_hist[i >> 8][i & 255] = 0;
   __syncthreads();
-  uint32_t prefix = 0, left = static_cast<uint32_t>(want);
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    if (tid < 256) s_hist[tid] = 0;
-    __syncthreads();
-    for (int i = tid; i < nb; i += kSelectThreads) {
-      const uint32_t k = key_of(i);
-      if (shift == 24 || (k >> (shift + 8)) == prefix) atomicAdd(&s_hist[(k >> shift) & 255u], 1u);
+  // f(block, key) for this thread's run, and for any share of the blocks.
+  auto each_in_run = [&](auto&& f) {
+    if (kRegs) {
+#pragma unroll
+      for (int j = 0; j < kSelectRun; ++j)
+        if (i0 + j < i1) f(i0 + j, run[j]);
+    } else {
+      for (int i = i0; i < i1; ++i) f(i, cached ? s_key[select_place(i)] : fresh(i));
     }
+  };
+  auto each = [&](auto&& f) {
+    if (kRegs)
+      each_in_run(f);
+    else
+      for (int i = tid; i < nb; i += kThreads) f(i, cached ? s_key[select_place(i)] : fresh(i));
+  };
+  uint32_t prefix = 0;
+  int shift = 24;
+  for (;; shift -= 8) {
+    uint32_t* hist = s_hist[shift >> 3];
+    each([&](int, uint32_t k) {
+      if (shift == 24 || (k >> (shift + 8)) == prefix) atomicAdd(&hist[(k >> shift) & 255u], 1u);
+    });
     __syncthreads();
     if (warp == 0) {
       // Lane l counts bins 255 - 8 l downwards; the bin where the count reaches `left`.
       uint32_t c[8], sum = 0;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        c[i] = s_hist[255 - 8 * lane - i];
+        c[i] = hist[255 - 8 * lane - i];
         sum += c[i];
       }
       uint32_t before = sum;
@@ -386,29 +428,31 @@ __global__ void __launch_bounds__(kSelectThreads) select_blocks_kernel(const Sel
       before -= sum;
       if (before < left && before + sum >= left) {
         int bin = 255 - 8 * lane;
+        uint32_t in_bin = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
+          in_bin = c[i];
           if (before + c[i] >= left) break;
           before += c[i];
           --bin;
         }
         s_state[0] = prefix << 8 | static_cast<uint32_t>(bin);
         s_state[1] = left - before;
+        s_state[2] = in_bin == left - before;
       }
     }
     __syncthreads();
     prefix = s_state[0];
     left = s_state[1];
+    if (shift == 0 || s_state[2]) break;  // (a bin chosen whole needs no further digits)
   }
-  // All keys above `prefix`, and the first `left` of those equal to it.
-  const int per = (nb + kSelectThreads - 1) / kSelectThreads;
-  const int i0 = min(tid * per, nb), i1 = min(i0 + per, nb);
+  // By their digits down to `shift`: all keys above `prefix`, and the first `left` of
+  // those equal to it.
   uint32_t above = 0, equal = 0;
-  for (int i = i0; i < i1; ++i) {
-    const uint32_t k = key_of(i);
-    above += k > prefix;
-    equal += k == prefix;
-  }
+  each_in_run([&](int, uint32_t k) {
+    above += (k >> shift) > prefix;
+    equal += (k >> shift) == prefix;
+  });
   uint32_t sa = above, se = equal;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -423,34 +467,42 @@ __global__ void __launch_bounds__(kSelectThreads) select_blocks_kernel(const Sel
     s_warp[1][warp] = se;
   }
   __syncthreads();
-  if (warp == 0) {
-    uint32_t wa = s_warp[0][lane], we = s_warp[1][lane];
-    const uint32_t ma = wa, me = we;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t va = __shfl_up_sync(0xffffffffu, wa, o), ve = __shfl_up_sync(0xffffffffu, we, o);
-      if (lane >= o) {
-        wa += va;
-        we += ve;
-      }
-    }
-    s_warp[0][lane] = wa - ma;
-    s_warp[1][lane] = we - me;
-  }
-  __syncthreads();
-  sa += s_warp[0][warp] - above;  // keys above / equal before this thread's run
-  se += s_warp[1][warp] - equal;
-  for (int i = i0; i < i1; ++i) {
-    const uint32_t k = key_of(i);
+  // Every warp sums the warps before it.
+  const uint32_t wa = lane < warp ? s_warp[0][lane] : 0, we = lane < warp ? s_warp[1][lane] : 0;
+  sa += __reduce_add_sync(0xffffffffu, wa) - above;  // keys above / equal before this thread's run
+  se += __reduce_add_sync(0xffffffffu, we) - equal;
+  each_in_run([&](int i, uint32_t k) {
     const uint32_t at = sa + min(se, left);
-    if (k > prefix) {
+    if ((k >> shift) > prefix) {
       out[at] = i;
       ++sa;
-    } else if (k == prefix) {
+    } else if ((k >> shift) == prefix) {
       if (se < left) out[at] = i;
       ++se;
     }
+  });
+}
+
+template <int kThreads>
+__global__ void __launch_bounds__(kThreads) select_blocks_kernel(const SelectArgs a) {
+  const int h = blockIdx.x, b = blockIdx.y;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int ctx = clamped_context(a.context_lens, b, a.max_blocks, false);
+  const int nb = (ctx + kBlockSize - 1) / kBlockSize;
+  const int64_t unit = static_cast<int64_t>(b) * a.num_kv_heads + h;
+  int32_t* out = a.selected + unit * a.num_selected;
+  if (nb <= a.num_selected) {
+    for (int i = threadIdx.x; i < a.num_selected; i += kThreads) out[i] = i < nb ? i : -1;
+    return;
   }
+  const uint32_t* keys = a.keys + unit * a.max_blocks;
+  // The blocks always kept rank above every score.
+  auto fresh = [&](int i) { return i < a.sink || i >= nb - a.recent ? 0xffffffffu : __ldcg(keys + i); };
+  if (kThreads < kSelectThreads || nb <= kSelectRun * kThreads)
+    choose_blocks<kThreads, true>(fresh, nb, static_cast<uint32_t>(a.num_selected), out);
+  else
+    choose_blocks<kThreads, false>(fresh, nb, static_cast<uint32_t>(a.num_selected), out);
 }
 
 // ===================================================================== attention over chosen blocks
@@ -472,8 +524,8 @@ struct SparseShape {
 // w, w + W, ... of the list, one 16-token block a step with the math of the decode
 // kernels; the warps' partial results meet in shared memory, the CTAs' in
 // distributed shared memory, so that there is neither workspace nor second launch.
-// Bound by the K and V bytes for large batches, by the chain list, table, tiles,
-// merge for small ones.
+// Bound by the K and V bytes for large batches (32 sequences x 8 KV heads x 128 blocks:
+// 268 MB in 48 us, 5.6 TB/s), by the chain list, table, tiles, merge for small ones.
 template <typename T, int D>
 __global__ void __launch_bounds__(kSparseWarps * 32, 2)
     decode_sparse_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,

@@ -300,7 +300,9 @@ int select_blocks_impl(const pkv::SelectArgs& args, void* workspace, size_t work
   a.max_blocks = d->max_blocks_per_seq;
   cudaError_t e = cudaSuccess;
   if (scored) {
-    const dim3 grid((a.max_blocks + pkv::kScoreBlocks - 1) / pkv::kScoreBlocks, d->num_kv_heads, d->num_seqs);
+    const int64_t ctas = static_cast<int64_t>((a.max_blocks + pkv::kScoreBlocks - 1) / pkv::kScoreBlocks) * d->num_kv_heads;
+    if (ctas > INT32_MAX) return pkv_fail(PKV_ERR_UNSUPPORTED, "select_blocks: too many blocks x KV heads");
+    const dim3 grid(static_cast<unsigned>(ctas), d->num_seqs);
     with_type_and_dim(d, [&](auto t, auto dim) {
       using T = decltype(t);
       constexpr int D = decltype(dim)::value;
@@ -312,12 +314,17 @@ int select_blocks_impl(const pkv::SelectArgs& args, void* workspace, size_t work
     });
     if (e != cudaSuccess) return cuda_fail(e, "score_blocks_kernel launch");
   }
-  const int most = pkv::select_place(pkv::kSelectCached) * 4 + 4;
-  e = configure_smem<pkv::select_blocks_kernel>(most);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(select_blocks_kernel)");
-  const size_t smem = scored ? pkv::select_place(std::min(a.max_blocks, pkv::kSelectCached)) * 4 + 4 : 0;
-  e = launch_dependent(pkv::select_blocks_kernel, dim3(d->num_kv_heads, d->num_seqs), 1, pkv::kSelectThreads, smem, stream,
-                       a);
+  const dim3 grid(d->num_kv_heads, d->num_seqs);
+  if (!scored || a.max_blocks <= 256 * pkv::kSelectRun) {
+    e = launch_dependent(pkv::select_blocks_kernel<256>, grid, 1, 256, 0, stream, a);
+  } else {
+    const int most = pkv::select_place(pkv::kSelectCached) * 4 + 4;
+    e = configure_smem<pkv::select_blocks_kernel<pkv::kSelectThreads>>(most);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(select_blocks_kernel)");
+    const size_t smem = a.max_blocks <= pkv::kSelectThreads * pkv::kSelectRun
+                            ? 0 : pkv::select_place(std::min(a.max_blocks, pkv::kSelectCached)) * 4 + 4;
+    e = launch_dependent(pkv::select_blocks_kernel<pkv::kSelectThreads>, grid, 1, pkv::kSelectThreads, smem, stream, a);
+  }
   if (e != cudaSuccess) return cuda_fail(e, "select_blocks_kernel launch");
   return PKV_OK;
 }

@@ -135,6 +135,33 @@ def test_selection_of_very_long_contexts(blocks):
     assert np.array_equal(got.cpu().numpy()[0, 0], want)
 
 
+@pytest.mark.parametrize("width,blocks", [(2048, 2048), (2049, 2049), (2048, 129), (8192, 8192), (8193, 8192),
+                                          (8193, 8193), (9000, 1500), (40000, 700)])
+@pytest.mark.parametrize("pool", [400, 12000])
+def test_selection_at_the_borders_of_its_forms(width, blocks, pool):
+    """Tables and contexts on either side of what one form of the choice holds, with many
+    equal scores (few blocks in the pool) and with hardly any."""
+    rng = np.random.default_rng(width + blocks)
+    tables = np.full((2, width), -1, np.int32)
+    lens = [blocks * 16, blocks * 16 - 17]
+    bounds = np.sort(rng.integers(-127, 128, (pool, 2, 2, 64)).astype(np.int8), axis=2)[:, :, ::-1].copy()
+    scales = rng.random((pool, 2)).astype(np.float32)
+    for b, n in enumerate(lens):
+        tables[b, :-(-n // 16)] = rng.permutation(max(pool, blocks))[:-(-n // 16)] % pool
+    q = rand((2, 10, 64), torch.bfloat16, 1)
+    for num in (1, 60, 128):
+        got = pkv.paged_select_blocks(q.to(DEV), torch.from_numpy(bounds).to(DEV), torch.from_numpy(scales).to(DEV),
+                                      i32(tables), i32(lens), num, 0, 1)
+        pkv.paged_kv_check_status()
+        for b, n in enumerate(lens):
+            n = -(-n // 16)
+            for h in range(2):
+                score = lc.block_scores(q[b, 5 * h:5 * h + 5].float().numpy(), bounds[:, h], scales[:, h])[tables[b, :n]]
+                best = np.lexsort((np.arange(n - 1), -score[:n - 1]))[:num - 1]
+                want = np.sort(np.append(best, n - 1))
+                assert np.array_equal(got[b, h, :min(num, n)].cpu().numpy(), want[:n]), (b, h, num)
+
+
 def test_selection_flags_and_buffers():
     lens = [400, 30]
     tables, nb = paged(lens, 0)
