@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(kScoreThreads) score_blocks_kernel(const Selec
   constexpr int kWarps = kScoreThreads / 32;
   static_assert(kScoreBlocks == kScoreThreads, "a block a lane");
   __shared__ __align__(128) uint4 s_rows[kScoreBlocks * kPieces];
-  __shared__ __align__(16) int32_t s_code[G][D / 4];
+  __shared__ __align__(16) int8_t s_code[G][2 * D];  // the positive codes, against upper bounds; the negative ones
   __shared__ float s_scale[G];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // The heads of a range side by side, so that their pieces of a block, neighbours in
@@ -270,9 +270,11 @@ __global__ void __launch_bounds__(kScoreThreads) score_blocks_kernel(const Selec
     finite = __all_sync(0xffffffffu, finite);
     const float s = finite ? __fmul_rn(top, 1.f / 127.f) : 0.f;
 #pragma unroll
-    for (int i = 0; i < kVals; ++i)
-      reinterpret_cast<int8_t*>(s_code[g])[lane * kVals + i] =
-          static_cast<int8_t>(s > 0.f ? static_cast<int>(rintf(__fdiv_rn(x[n][i], s))) : 0);
+    for (int i = 0; i < kVals; ++i) {
+      const int c = s > 0.f ? static_cast<int>(rintf(__fdiv_rn(x[n][i], s))) : 0;
+      s_code[g][lane * kVals + i] = static_cast<int8_t>(max(c, 0));
+      s_code[g][D + lane * kVals + i] = static_cast<int8_t>(min(c, 0));
+    }
     if (lane == 0) s_scale[g] = s;
   }
   __syncthreads();
@@ -282,15 +284,11 @@ __global__ void __launch_bounds__(kScoreThreads) score_blocks_kernel(const Selec
   for (int g = 0; g < G; ++g)
 #pragma unroll
     for (int t = 0; t < kTurns; ++t) {
-      const int piece = t * kLanes + sub;
-      const int4 c = *reinterpret_cast<const int4*>(&s_code[g][4 * (piece % (kPieces / 2))]);
-      const int32_t w[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        // Bytes of the other sign are cleared: all ones in the negative bytes.
-        const uint32_t neg = __vcmplts4(static_cast<uint32_t>(w[i]), 0u);
-        code[g][t][i] = static_cast<int32_t>(piece < kPieces / 2 ? w[i] & ~neg : w[i] & neg);
-      }
+      const int4 c = *reinterpret_cast<const int4*>(&s_code[g][16 * (t * kLanes + sub)]);
+      code[g][t][0] = c.x;
+      code[g][t][1] = c.y;
+      code[g][t][2] = c.z;
+      code[g][t][3] = c.w;
     }
   // After the exchanges below, a lane's sum is of this head.
   int head = 0;
