@@ -662,8 +662,9 @@ int paged_kv_update_bounds(const void* k_cache, const int32_t* block_tables, con
  * + recent_blocks; a context of fewer blocks has all of them.  q:
  * T[num_seqs][Hq][D], one token each.  workspace (device):
  * paged_select_workspace_bytes(dims) bytes, 256-byte aligned, without
- * initialisation (NULL where max_blocks_per_seq <= num_selected).  At most 65535
- * sequences and KV heads. */
+ * initialisation (NULL where that is 0, as for few sequences with tables of up to 256
+ * blocks, or where max_blocks_per_seq <= num_selected).  At most 65535 sequences and
+ * KV heads. */
 int paged_select_blocks(const void* q, const int8_t* bounds, const float* scales, const int32_t* block_tables,
                         const int32_t* context_lens, int32_t num_selected, int32_t sink_blocks, int32_t recent_blocks,
                         int32_t* selected, void* workspace, size_t workspace_bytes, const pkv_dims* dims, void* stream);

@@ -176,8 +176,9 @@ struct SelectArgs {
   int32_t num_selected, sink, recent;
 };
 
-constexpr int kScoreThreads = 128;
-constexpr int kScoreBlocks = 128;  // blocks of a CTA: a lane's each
+constexpr int kScoreThreads = 128;  // of a CTA, a block each; of one that chooses too:
+constexpr int kWholeThreads = 256;
+constexpr int kWholeUnits = 2 * 152;  // two on each SM (64 KB of rows, at most 108 registers)
 
 // Unsigned numbers in the order of the floats (there is no -0 among them); NaN as
 // +infinity.
@@ -186,166 +187,7 @@ __device__ __forceinline__ uint32_t ordered_key(float x) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-__device__ __forceinline__ void copy_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-
-// A CTA scores 128 blocks of one (sequence, KV head) for its G >= group heads, a warp 32.
-// The warp starts the copies of all its rows of bounds (2 D bytes each) at once, 8 KB at
-// D = 128, without a register for them; the query's codes are made while they come.
-// max(4, G) lanes share a row, 16 bytes at a time, upper bounds in its first half; they
-// keep the codes for their bytes in registers, the positive ones against the upper
-// bounds, the negative ones against the lower, as four-way byte products.  The G sums are
-// then folded over the lanes, half of the sums going either way in each exchange, after
-// which a lane holds one head's.
-// Bound by the latency of table, bounds and their bytes: with the choice after it, 32
-// sequences of 8,192 to 32,768 tokens, 8 KV heads, G = 4, D = 128 (85 MB) take 25.6 us,
-// 131,072 tokens of one sequence, G = 8 (17 MB) 13.3.  (Loads through registers, eight a
-// lane under way, 16 lanes a row: 37.7 and 21.8 with the choice of that time; four lanes
-// a row and loads through registers: 6 us slower than copies at G = 4, as fewer CTAs fit.
-// The products as s8 tensor products: no gain over byte products.)
-template <typename T, int D, int G>
-__global__ void __launch_bounds__(kScoreThreads) score_blocks_kernel(const SelectArgs a) {
-  constexpr int kLanes = G == 8 ? 8 : 4;
-  constexpr int kPieces = 2 * D / 16;                // 16-byte pieces of a row
-  constexpr int kTurns = kPieces / kLanes;
-  constexpr int kRows = 32 / kLanes;                 // blocks of a warp's step
-  constexpr int kWarps = kScoreThreads / 32;
-  static_assert(kScoreBlocks == kScoreThreads, "a block a lane");
-  __shared__ __align__(128) uint4 s_rows[kScoreBlocks * kPieces];
-  __shared__ __align__(16) int8_t s_code[G][2 * D];  // the positive codes, against upper bounds; the negative ones
-  __shared__ float s_scale[G];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // The heads of a range side by side, so that their pieces of a block, neighbours in
-  // memory, are read at about the same time.
-  const int h = blockIdx.x % a.num_kv_heads, b = blockIdx.y, first = blockIdx.x / a.num_kv_heads * kScoreBlocks;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int block = first + threadIdx.x;             // this lane's
-  int phys = block < a.max_blocks ? __ldg(a.block_tables + static_cast<int64_t>(b) * a.max_blocks + block) : -1;
-  constexpr int kVals = D / 32, kHeads = (G + kWarps - 1) / kWarps;  // values of a lane, heads of a warp
-  float x[kHeads][kVals];
-#pragma unroll
-  for (int n = 0; n < kHeads; ++n) {
-    const int g = warp + n * kWarps;
-    const T* q = static_cast<const T*>(a.q) + (static_cast<int64_t>(b) * a.num_q_heads + h * a.group + g) * D;
-#pragma unroll
-    for (int i = 0; i < kVals; ++i) x[n][i] = g < a.group ? static_cast<float>(q[lane * kVals + i]) : 0.f;
-  }
-  const int ctx = clamped_context(a.context_lens, b, a.max_blocks, threadIdx.x == 0 && blockIdx.x == 0);
-  const int nb = (ctx + kBlockSize - 1) / kBlockSize;
-  if (first >= nb || nb <= a.num_selected) return;   // none, or all chosen without scores
-  if (block >= nb) {
-    phys = -1;
-  } else if (phys < 0 || phys >= a.num_blocks) {
-    if (h == 0) flag_error(kErrBlockId);
-    phys = -1;
-  }
-  // Without a block: a scale of 0, whatever lies in the row.
-  const float my_step = phys >= 0 ? __ldg(a.scales + static_cast<int64_t>(phys) * a.num_kv_heads + h) : 0.f;
-  uint4* rows = s_rows + warp * 32 * kPieces;
-  // In odd rows the halves of 64 bytes change places: four lanes a row meet all banks.
-  auto place = [](int r, int piece) { return r * kPieces + (piece ^ ((r & 1) << 2)); };
-#pragma unroll
-  for (int i = 0; i < kPieces; ++i) {
-    const int r = i * (32 / kPieces) + lane / kPieces, piece = lane % kPieces;
-    const int p = __shfl_sync(0xffffffffu, phys, r);
-    if (p >= 0)
-      copy_async16(smem_u32(rows + place(r, piece)),
-                   a.bounds + (static_cast<int64_t>(p) * a.num_kv_heads + h) * (2 * D) + 16 * piece);
-  }
-#pragma unroll
-  for (int n = 0; n < kHeads; ++n) {
-    const int g = warp + n * kWarps;
-    if (g >= G) break;
-    float top = 0.f;
-    bool finite = true;
-#pragma unroll
-    for (int i = 0; i < kVals; ++i) {
-      finite = finite && fabsf(x[n][i]) < INFINITY;
-      top = fmaxf(top, fabsf(x[n][i]));
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    finite = __all_sync(0xffffffffu, finite);
-    const float s = finite ? __fmul_rn(top, 1.f / 127.f) : 0.f;
-#pragma unroll
-    for (int i = 0; i < kVals; ++i) {
-      const int c = s > 0.f ? static_cast<int>(rintf(__fdiv_rn(x[n][i], s))) : 0;
-      s_code[g][lane * kVals + i] = static_cast<int8_t>(max(c, 0));
-      s_code[g][D + lane * kVals + i] = static_cast<int8_t>(min(c, 0));
-    }
-    if (lane == 0) s_scale[g] = s;
-  }
-  __syncthreads();
-  const int sub = lane % kLanes, grp = lane / kLanes;
-  int32_t code[G][kTurns][4];
-#pragma unroll
-  for (int g = 0; g < G; ++g)
-#pragma unroll
-    for (int t = 0; t < kTurns; ++t) {
-      const int4 c = *reinterpret_cast<const int4*>(&s_code[g][16 * (t * kLanes + sub)]);
-      code[g][t][0] = c.x;
-      code[g][t][1] = c.y;
-      code[g][t][2] = c.z;
-      code[g][t][3] = c.w;
-    }
-  // After the exchanges below, a lane's sum is of this head.
-  int head = 0;
-#pragma unroll
-  for (int n = G / 2, o = 1; n > 0; n /= 2, o *= 2)
-    if (lane & o) head += n;
-  const float head_scale = s_scale[head];
-  uint32_t* keys = a.keys + (static_cast<int64_t>(b) * a.num_kv_heads + h) * a.max_blocks + first + warp * 32;
-  const int mine = nb - first - warp * 32;           // blocks of this warp, or more
-  asm volatile("cp.async.wait_all;" ::: "memory");
-  __syncwarp();
-  if (mine <= 0) return;
-#pragma unroll
-  for (int r0 = 0; r0 < 32; r0 += kRows) {
-    const int r = r0 + grp;
-    int32_t dot[G];
-#pragma unroll
-    for (int g = 0; g < G; ++g) dot[g] = 0;
-#pragma unroll
-    for (int t = 0; t < kTurns; ++t) {
-      const uint4 e = rows[place(r, t * kLanes + sub)];
-#pragma unroll
-      for (int g = 0; g < G; ++g) {
-        dot[g] = __dp4a(code[g][t][0], static_cast<int32_t>(e.x), dot[g]);
-        dot[g] = __dp4a(code[g][t][1], static_cast<int32_t>(e.y), dot[g]);
-        dot[g] = __dp4a(code[g][t][2], static_cast<int32_t>(e.z), dot[g]);
-        dot[g] = __dp4a(code[g][t][3], static_cast<int32_t>(e.w), dot[g]);
-      }
-    }
-    // Exchange halves while there are several sums, then add.
-#pragma unroll
-    for (int o = 1, n = G; o < kLanes; o *= 2, n = n > 1 ? n / 2 : 1) {
-      if (n > 1) {
-        const bool odd = lane & o;
-#pragma unroll
-        for (int g = 0; g < n / 2; ++g) {
-          const int32_t give = odd ? dot[g] : dot[g + n / 2];
-          const int32_t keep = odd ? dot[g + n / 2] : dot[g];
-          dot[g] = keep + __shfl_xor_sync(0xffffffffu, give, o);
-        }
-      } else {
-        dot[0] += __shfl_xor_sync(0xffffffffu, dot[0], o);
-      }
-    }
-    // A NaN (0 times an infinite scale) is +infinity, as in ordered_key.
-    // Adding 0 makes a product that underflowed to -0 the equal of +0.
-    const float step = __shfl_sync(0xffffffffu, my_step, r);
-    float score = __fadd_rn(__fmul_rn(__fmul_rn(static_cast<float>(dot[0]), step), head_scale), 0.f);
-    if (head >= a.group) score = -INFINITY;
-    uint32_t key = ordered_key(score);
-#pragma unroll
-    for (int m = 1; m < G; m *= 2) key = max(key, __shfl_xor_sync(0xffffffffu, key, m));
-    if (sub == 0 && r < mine) keys[r] = key;
-  }
-}
-
-// ===================================================================== choice
+// --------------------------------------------------------------------- choice among keys
 
 constexpr int kSelectThreads = 1024;  // of a CTA; 256 for tables of up to 2,048 blocks (below)
 constexpr int kSelectRun = 8;         // keys that a thread holds in registers, at most
@@ -480,6 +322,185 @@ __device__ __forceinline__ void choose_blocks(const Fresh& fresh, int nb, uint32
     }
   });
 }
+
+// --------------------------------------------------------------------- scores
+
+__device__ __forceinline__ void copy_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// A CTA scores 128 blocks of one (sequence, KV head) for its G >= group heads, a warp 32.
+// The warp starts the copies of all its rows of bounds (2 D bytes each) at once, 8 KB at
+// D = 128, without a register for them; the query's codes are made while they come.
+// max(4, G) lanes share a row, 16 bytes at a time, upper bounds in its first half; they
+// keep the codes for their bytes in registers, the positive ones against the upper
+// bounds, the negative ones against the lower, as four-way byte products.  The G sums are
+// then folded over the lanes, half of the sums going either way in each exchange, after
+// which a lane holds one head's.
+// Bound by the latency of table, bounds and their bytes: with the choice after it, 32
+// sequences of 8,192 to 32,768 tokens, 8 KV heads, G = 4, D = 128 (85 MB) take 25.6 us,
+// 131,072 tokens of one sequence, G = 8 (17 MB) 13.3.  (Loads through registers, eight a
+// lane under way, 16 lanes a row: 37.7 and 21.8 with the choice of that time; four lanes
+// a row and loads through registers: 6 us slower than copies at G = 4, as fewer CTAs fit.
+// The products as s8 tensor products: no gain over byte products.)
+//
+// kWhole: the table has no more blocks than the CTA threads, and the CTA chooses as well.
+template <typename T, int D, int G, bool kWhole>
+__global__ void __launch_bounds__(kWhole ? kWholeThreads : kScoreThreads) score_blocks_kernel(const SelectArgs a) {
+  constexpr int kLanes = G == 8 ? 8 : 4;
+  constexpr int kPieces = 2 * D / 16;                // 16-byte pieces of a row
+  constexpr int kTurns = kPieces / kLanes;
+  constexpr int kRows = 32 / kLanes;                 // blocks of a warp's step
+  constexpr int kThreads = kWhole ? kWholeThreads : kScoreThreads;
+  constexpr int kWarps = kThreads / 32;
+  extern __shared__ __align__(128) uint4 s_rows[];   // [kThreads][kPieces]
+  __shared__ uint32_t s_keys[kWhole ? kThreads : 1];
+  __shared__ __align__(16) int8_t s_code[G][2 * D];  // the positive codes, against upper bounds; the negative ones
+  __shared__ float s_scale[G];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // The heads of a range side by side, so that their pieces of a block, neighbours in
+  // memory, are read at about the same time.
+  const int h = blockIdx.x % a.num_kv_heads, b = blockIdx.y, first = blockIdx.x / a.num_kv_heads * kThreads;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int block = first + threadIdx.x;             // this lane's
+  int phys = block < a.max_blocks ? __ldg(a.block_tables + static_cast<int64_t>(b) * a.max_blocks + block) : -1;
+  constexpr int kVals = D / 32, kHeads = (G + kWarps - 1) / kWarps;  // values of a lane, heads of a warp
+  float x[kHeads][kVals];
+#pragma unroll
+  for (int n = 0; n < kHeads; ++n) {
+    const int g = warp + n * kWarps;
+    const T* q = static_cast<const T*>(a.q) + (static_cast<int64_t>(b) * a.num_q_heads + h * a.group + g) * D;
+#pragma unroll
+    for (int i = 0; i < kVals; ++i) x[n][i] = g < a.group ? static_cast<float>(q[lane * kVals + i]) : 0.f;
+  }
+  const int ctx = clamped_context(a.context_lens, b, a.max_blocks, threadIdx.x == 0 && blockIdx.x == 0);
+  const int nb = (ctx + kBlockSize - 1) / kBlockSize;
+  int32_t* out = a.selected + (static_cast<int64_t>(b) * a.num_kv_heads + h) * a.num_selected;
+  if (nb <= a.num_selected) {                        // all are chosen, without scores
+    if (kWhole)
+      for (int i = threadIdx.x; i < a.num_selected; i += kThreads) out[i] = i < nb ? i : -1;
+    return;
+  }
+  if (first >= nb) return;
+  if (block >= nb) {
+    phys = -1;
+  } else if (phys < 0 || phys >= a.num_blocks) {
+    if (h == 0) flag_error(kErrBlockId);
+    phys = -1;
+  }
+  // Without a block: a scale of 0, whatever lies in the row.
+  const float my_step = phys >= 0 ? __ldg(a.scales + static_cast<int64_t>(phys) * a.num_kv_heads + h) : 0.f;
+  uint4* rows = s_rows + warp * 32 * kPieces;
+  // In odd rows the halves of 64 bytes change places: four lanes a row meet all banks.
+  auto place = [](int r, int piece) { return r * kPieces + (piece ^ ((r & 1) << 2)); };
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i) {
+    const int r = i * (32 / kPieces) + lane / kPieces, piece = lane % kPieces;
+    const int p = __shfl_sync(0xffffffffu, phys, r);
+    if (p >= 0)
+      copy_async16(smem_u32(rows + place(r, piece)),
+                   a.bounds + (static_cast<int64_t>(p) * a.num_kv_heads + h) * (2 * D) + 16 * piece);
+  }
+#pragma unroll
+  for (int n = 0; n < kHeads; ++n) {
+    const int g = warp + n * kWarps;
+    if (g >= G) break;
+    float top = 0.f;
+    bool finite = true;
+#pragma unroll
+    for (int i = 0; i < kVals; ++i) {
+      finite = finite && fabsf(x[n][i]) < INFINITY;
+      top = fmaxf(top, fabsf(x[n][i]));
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    finite = __all_sync(0xffffffffu, finite);
+    const float s = finite ? __fmul_rn(top, 1.f / 127.f) : 0.f;
+#pragma unroll
+    for (int i = 0; i < kVals; ++i) {
+      const int c = s > 0.f ? static_cast<int>(rintf(__fdiv_rn(x[n][i], s))) : 0;
+      s_code[g][lane * kVals + i] = static_cast<int8_t>(max(c, 0));
+      s_code[g][D + lane * kVals + i] = static_cast<int8_t>(min(c, 0));
+    }
+    if (lane == 0) s_scale[g] = s;
+  }
+  __syncthreads();
+  const int sub = lane % kLanes, grp = lane / kLanes;
+  int32_t code[G][kTurns][4];
+#pragma unroll
+  for (int g = 0; g < G; ++g)
+#pragma unroll
+    for (int t = 0; t < kTurns; ++t) {
+      const int4 c = *reinterpret_cast<const int4*>(&s_code[g][16 * (t * kLanes + sub)]);
+      code[g][t][0] = c.x;
+      code[g][t][1] = c.y;
+      code[g][t][2] = c.z;
+      code[g][t][3] = c.w;
+    }
+  // After the exchanges below, a lane's sum is of this head.
+  int head = 0;
+#pragma unroll
+  for (int n = G / 2, o = 1; n > 0; n /= 2, o *= 2)
+    if (lane & o) head += n;
+  const float head_scale = s_scale[head];
+  uint32_t* keys = kWhole ? s_keys + warp * 32
+                          : a.keys + (static_cast<int64_t>(b) * a.num_kv_heads + h) * a.max_blocks + first + warp * 32;
+  const int mine = nb - first - warp * 32;           // blocks of this warp, or more
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncwarp();
+  if (mine > 0) {
+#pragma unroll
+    for (int r0 = 0; r0 < 32; r0 += kRows) {
+      const int r = r0 + grp;
+      int32_t dot[G];
+#pragma unroll
+      for (int g = 0; g < G; ++g) dot[g] = 0;
+#pragma unroll
+      for (int t = 0; t < kTurns; ++t) {
+        const uint4 e = rows[place(r, t * kLanes + sub)];
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          dot[g] = __dp4a(code[g][t][0], static_cast<int32_t>(e.x), dot[g]);
+          dot[g] = __dp4a(code[g][t][1], static_cast<int32_t>(e.y), dot[g]);
+          dot[g] = __dp4a(code[g][t][2], static_cast<int32_t>(e.z), dot[g]);
+          dot[g] = __dp4a(code[g][t][3], static_cast<int32_t>(e.w), dot[g]);
+        }
+      }
+      // Exchange halves while there are several sums, then add.
+#pragma unroll
+      for (int o = 1, n = G; o < kLanes; o *= 2, n = n > 1 ? n / 2 : 1) {
+        if (n > 1) {
+          const bool odd = lane & o;
+#pragma unroll
+          for (int g = 0; g < n / 2; ++g) {
+            const int32_t give = odd ? dot[g] : dot[g + n / 2];
+            const int32_t keep = odd ? dot[g + n / 2] : dot[g];
+            dot[g] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+          }
+        } else {
+          dot[0] += __shfl_xor_sync(0xffffffffu, dot[0], o);
+        }
+      }
+      // A NaN (0 times an infinite scale) is +infinity, as in ordered_key.
+      // Adding 0 makes a product that underflowed to -0 the equal of +0.
+      const float step = __shfl_sync(0xffffffffu, my_step, r);
+      float score = __fadd_rn(__fmul_rn(__fmul_rn(static_cast<float>(dot[0]), step), head_scale), 0.f);
+      if (head >= a.group) score = -INFINITY;
+      uint32_t key = ordered_key(score);
+#pragma unroll
+      for (int m = 1; m < G; m *= 2) key = max(key, __shfl_xor_sync(0xffffffffu, key, m));
+      if (sub == 0 && r < mine) keys[r] = key;
+    }
+  }
+  if constexpr (kWhole) {
+    __syncthreads();
+    auto fresh = [&](int i) { return i < a.sink || i >= nb - a.recent ? 0xffffffffu : s_keys[i]; };
+    choose_blocks<kThreads, true>(fresh, nb, static_cast<uint32_t>(a.num_selected), out);
+  }
+}
+
+// ===================================================================== choice
 
 template <int kThreads>
 __global__ void __launch_bounds__(kThreads) select_blocks_kernel(const SelectArgs a) {

@@ -266,7 +266,19 @@ int update_bounds_impl(const void* k_cache, const int32_t* block_tables, const i
   return PKV_OK;
 }
 
+// Scores and choice in one launch, without a workspace: tables of at most kWholeThreads
+// blocks, as many (sequence, KV head) pairs as CTAs are on the SMs at once.  Up to 256
+// blocks each, 8 KV heads: 32 sequences 7.5 us against 9.2 with two launches, 64 13.1
+// against 11.9 (its CTAs are twice as large and wait for their rows as a whole), 256 45
+// against 37.  With 5 sequences the binding's time counts, 27 us against 36 with the
+// attention after it.
+bool select_whole(const pkv_dims* d) {
+  return d->max_blocks_per_seq <= pkv::kWholeThreads &&
+         static_cast<int64_t>(d->num_seqs) * d->num_kv_heads <= pkv::kWholeUnits;
+}
+
 size_t select_workspace(const pkv_dims* d) {
+  if (select_whole(d)) return 0;
   return align256(static_cast<size_t>(d->num_seqs) * d->num_kv_heads * d->max_blocks_per_seq * sizeof(uint32_t));
 }
 
@@ -299,21 +311,38 @@ int select_blocks_impl(const pkv::SelectArgs& args, void* workspace, size_t work
   a.num_blocks = d->num_blocks;
   a.max_blocks = d->max_blocks_per_seq;
   cudaError_t e = cudaSuccess;
+  const bool whole = scored && select_whole(d);
   if (scored) {
-    const int64_t ctas = static_cast<int64_t>((a.max_blocks + pkv::kScoreBlocks - 1) / pkv::kScoreBlocks) * d->num_kv_heads;
+    const int threads = whole ? pkv::kWholeThreads : pkv::kScoreThreads;
+    const int64_t ctas = static_cast<int64_t>((a.max_blocks + threads - 1) / threads) * d->num_kv_heads;
     if (ctas > INT32_MAX) return pkv_fail(PKV_ERR_UNSUPPORTED, "select_blocks: too many blocks x KV heads");
     const dim3 grid(static_cast<unsigned>(ctas), d->num_seqs);
     with_type_and_dim(d, [&](auto t, auto dim) {
       using T = decltype(t);
       constexpr int D = decltype(dim)::value;
-      auto kern = a.group == 1   ? pkv::score_blocks_kernel<T, D, 1>
-                  : a.group == 2 ? pkv::score_blocks_kernel<T, D, 2>
-                  : a.group <= 4 ? pkv::score_blocks_kernel<T, D, 4>
-                                 : pkv::score_blocks_kernel<T, D, 8>;
-      e = launch_dependent(kern, grid, 1, pkv::kScoreThreads, 0, stream, a);
+      auto launch = [&](auto group) {
+        constexpr int G = decltype(group)::value;
+        const int smem = threads * 2 * D;
+        if (whole) {
+          e = configure_smem<pkv::score_blocks_kernel<T, D, G, true>>(smem);
+          if (e == cudaSuccess)
+            e = launch_dependent(pkv::score_blocks_kernel<T, D, G, true>, grid, 1, threads, smem, stream, a);
+        } else {
+          e = launch_dependent(pkv::score_blocks_kernel<T, D, G, false>, grid, 1, threads, smem, stream, a);
+        }
+      };
+      if (a.group == 1)
+        launch(std::integral_constant<int, 1>{});
+      else if (a.group == 2)
+        launch(std::integral_constant<int, 2>{});
+      else if (a.group <= 4)
+        launch(std::integral_constant<int, 4>{});
+      else
+        launch(std::integral_constant<int, 8>{});
     });
     if (e != cudaSuccess) return cuda_fail(e, "score_blocks_kernel launch");
   }
+  if (whole) return PKV_OK;
   const dim3 grid(d->num_kv_heads, d->num_seqs);
   if (!scored || a.max_blocks <= 256 * pkv::kSelectRun) {
     e = launch_dependent(pkv::select_blocks_kernel<256>, grid, 1, 256, 0, stream, a);

@@ -135,7 +135,7 @@ def test_selection_of_very_long_contexts(blocks):
     assert np.array_equal(got.cpu().numpy()[0, 0], want)
 
 
-@pytest.mark.parametrize("width,blocks", [(2048, 2048), (2049, 2049), (2048, 129), (8192, 8192), (8193, 8192),
+@pytest.mark.parametrize("width,blocks", [(256, 256), (256, 33), (257, 257), (2048, 2048), (2049, 2049), (2048, 129), (8192, 8192), (8193, 8192),
                                           (8193, 8193), (9000, 1500), (40000, 700)])
 @pytest.mark.parametrize("pool", [400, 12000])
 def test_selection_at_the_borders_of_its_forms(width, blocks, pool):
@@ -160,6 +160,27 @@ def test_selection_at_the_borders_of_its_forms(width, blocks, pool):
                 best = np.lexsort((np.arange(n - 1), -score[:n - 1]))[:num - 1]
                 want = np.sort(np.append(best, n - 1))
                 assert np.array_equal(got[b, h, :min(num, n)].cpu().numpy(), want[:n]), (b, h, num)
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hq,hk,seqs", [(1, 1, 304), (1, 1, 305), (6, 2, 152), (8, 2, 153), (16, 2, 150), (40, 8, 60), (5, 5, 3)])
+def test_selection_in_one_and_two_launches(dtype, d, hq, hk, seqs):
+    """Short tables of few and of more sequences, all lengths up to the table's."""
+    rng = np.random.default_rng(seqs)
+    lens = rng.integers(0, 256 * 16 + 1, seqs)
+    lens[:3] = (256 * 16, 0, 255 * 16 + 1)
+    nb = 300
+    tables = rng.integers(0, nb, (seqs, 256)).astype(np.int32)
+    bounds = np.sort(rng.integers(-127, 128, (nb, hk, 2, d)).astype(np.int8), axis=2)[:, :, ::-1].copy()
+    scales = rng.random((nb, hk)).astype(np.float32)
+    q = rand((seqs, hq, d), DT[dtype], 6)
+    for num, sink, recent in ((20, 1, 2), (255, 0, 1)):
+        got = pkv.paged_select_blocks(q.to(DEV), torch.from_numpy(bounds).to(DEV), torch.from_numpy(scales).to(DEV),
+                                      i32(tables), i32(lens), num, sink, recent)
+        pkv.paged_kv_check_status()
+        ref = lc.select_blocks(q.float().numpy(), bounds, scales, tables, lens, num, sink, recent)
+        assert np.array_equal(got.cpu().numpy(), ref), (num, sink, recent)
 
 
 def test_selection_flags_and_buffers():

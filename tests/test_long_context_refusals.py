@@ -100,12 +100,18 @@ def test_sparse_calls():
     def select(q=P, b=P, s=P, t=P, l=P, num=3, sink=1, recent=1, sel=P, ws=P, nws=1 << 40, d=None):
         return lib().paged_select_blocks(q, b, s, t, l, num, sink, recent, sel, ws, nws, d or dims(), 0)
 
-    for kw in (dict(q=0), dict(b=0), dict(s=0), dict(t=0), dict(l=0), dict(sel=0), dict(ws=0), dict(nws=10), dict(ws=P + 64),
+    for kw in (dict(q=0), dict(b=0), dict(s=0), dict(t=0), dict(l=0), dict(sel=0),
+               dict(ws=0, d=dims(max_blocks_per_seq=257)), dict(nws=10, d=dims(max_blocks_per_seq=257)),
+               dict(ws=P + 64, d=dims(max_blocks_per_seq=257)), dict(ws=0, d=dims(num_seqs=305)),
                dict(num=0), dict(sink=-1), dict(recent=0), dict(sink=3), dict(sink=2 ** 31 - 1, recent=5), dict(q=P + 4), dict(b=P + 4)):
         assert select(**kw) == INVALID, kw
     for kw in (dict(d=dims(num_seqs=70000)), dict(d=dims(num_q_heads=20)), dict(d=dims(head_dim=32))):
         assert select(**kw) == UNSUPPORTED, kw
     assert select(d=dims(num_seqs=0)) == 0
+    # few sequences with tables of up to 256 blocks need no workspace
+    need = lib().paged_select_workspace_bytes
+    assert need(dims(max_blocks_per_seq=256)) == 0 and need(dims(max_blocks_per_seq=257)) > 0
+    assert need(dims(num_seqs=304, num_kv_heads=1, num_q_heads=1)) == 0 < need(dims(num_seqs=305, num_kv_heads=1, num_q_heads=1))
 
     def sparse(q=P, k=P, v=P, t=P, l=P, sel=P, num=3, scale=1.0, out=P, d=None):
         return lib().paged_decode_attention_sparse(q, k, v, t, l, sel, num, scale, out, d or dims(), 0)
