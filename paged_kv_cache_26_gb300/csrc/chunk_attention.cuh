@@ -28,7 +28,9 @@
 // CTA, one CTA per SM.  A part begins and ends inside units; such pieces leave
 // unnormalised fp32 partial results that merge_chunk_kernel joins in order.  Every
 // cut follows from the lengths alone, by closed sums that each CTA computes for
-// itself; nothing is counted or claimed at run time.
+// itself; nothing is counted or claimed at run time.  Where there are CTAs enough for
+// one unit each and all contexts are short, the line counts units and nothing is cut;
+// if the tables are too narrow for long contexts, the merge is not launched either.
 //
 // Values that a row does not attend to may be anything.  Scores there are replaced,
 // not weighted.  A weight of 0 would still meet V in the product (0 * NaN = NaN), so
@@ -63,6 +65,13 @@ constexpr int kEarly = 1;
 // number of keys worth a CTA of its own.
 constexpr int kUnitKeys = 128;
 constexpr int kLeastKeys = 512;
+// Units of at most so many keys are not cut where there are CTAs enough for one each:
+// partial results and their merge cost more than what they share out.  32/8 heads, D =
+// 128: 3 sequences of up to 260 tokens 12.1 us against 23.2, 512 new tokens from 0 14.6
+// against 23.2, 16 single tokens of 500 to 1,000 18.3 against 20.9; 2 of 1,000 17.0 against
+// 16.5, 2 of 2,000 26.5 against 17.9.  (About 2 us more where only the GPU knows that they
+// are short.)
+constexpr int kWholeKeys = 1024;
 
 // How a CTA's part begins, for the merge: inside a unit (its first piece is then
 // partial result 2 cta) and, `open`, ends inside it too.
@@ -84,6 +93,9 @@ struct ChunkArgs {
   int32_t grid;             // CTAs of the main kernel
   int32_t num_tokens, num_seqs, num_q_heads, num_kv_heads, group, max_blocks, num_blocks;
   int32_t tile_tokens;      // tokens of a tile: 128 / group
+  // The line may count units instead of keys, so that no cut lies inside one: there are
+  // CTAs enough, and the contexts are known to be short (2) or may turn out so (1).
+  int32_t whole_units;
 };
 
 template <int D>
@@ -111,15 +123,17 @@ struct ChunkSeq {
   int o0, n, ctx;  // first row, new tokens, context
   int units;       // per KV head
   int before;      // max(ctx - n, 0): keys before the chunk
+  bool whole;      // the line counts units
   int64_t line;    // length per KV head
 
   // Where unit i starts, from the start of its (sequence, KV head).
   __device__ __forceinline__ int64_t start(int i, int tt) const {
+    if (whole) return i;
     return static_cast<int64_t>(i) * (before + kUnitKeys) + static_cast<int64_t>(tt) * (static_cast<int64_t>(i) * (i + 1) / 2);
   }
 };
 
-__device__ __forceinline__ ChunkSeq chunk_seq(const ChunkArgs& a, int b, bool flag) {
+__device__ __forceinline__ ChunkSeq chunk_seq(const ChunkArgs& a, int b, bool flag, bool whole) {
   ChunkSeq s;
   const int r0 = __ldg(a.q_offsets + b), r1 = __ldg(a.q_offsets + b + 1);
   s.o0 = min(max(r0, 0), a.num_tokens);
@@ -130,7 +144,8 @@ __device__ __forceinline__ ChunkSeq chunk_seq(const ChunkArgs& a, int b, bool fl
   const int tt = 2 * a.tile_tokens;
   s.units = (s.n + tt - 1) / tt;
   s.before = max(s.ctx - s.n, 0);
-  s.line = s.n > 0 ? s.start(s.units - 1, tt) + s.before + s.n + kUnitKeys : 0;
+  s.whole = whole;
+  s.line = s.whole ? s.units : s.n > 0 ? s.start(s.units - 1, tt) + s.before + s.n + kUnitKeys : 0;
   return s;
 }
 
@@ -156,13 +171,14 @@ struct ChunkWalk {
   int64_t at, stop; // what is left of this CTA's part
 
   __device__ __forceinline__ int64_t cost(int tt) const {
+    if (s.whole) return 1;
     return min(static_cast<int64_t>(unit + 1) * tt, static_cast<int64_t>(s.n)) + s.before + kUnitKeys;
   }
   // The unit at `at`, which lies `rest` into sequence b.
-  __device__ __forceinline__ void locate(const ChunkArgs& a, int seq, int64_t rest, bool flag = false) {
+  __device__ __forceinline__ void locate(const ChunkArgs& a, int seq, int64_t rest, bool whole) {
     const int tt = 2 * a.tile_tokens;
     b = seq;
-    s = chunk_seq(a, b, flag);
+    s = chunk_seq(a, b, false, whole);
     // Quotient and root in float32, corrected by a step or two.
     kvh = min(static_cast<int>(static_cast<float>(rest) / static_cast<float>(s.line)), a.num_kv_heads - 1);
     while (kvh > 0 && kvh * s.line > rest) --kvh;
@@ -170,7 +186,7 @@ struct ChunkWalk {
     rest -= kvh * s.line;
     // start(i) <= rest, i the positive root: 2 rest / (p + sqrt(p^2 + 2 tt rest)).
     const float p = static_cast<float>(s.before + kUnitKeys) + 0.5f * tt, x = static_cast<float>(rest);
-    int i = static_cast<int>(2.f * x / (p + sqrtf(p * p + 2.f * tt * x)));
+    int i = s.whole ? static_cast<int>(rest) : static_cast<int>(2.f * x / (p + sqrtf(p * p + 2.f * tt * x)));
     i = min(max(i, 0), s.units - 1);
     while (i > 0 && s.start(i, tt) > rest) --i;
     while (i + 1 < s.units && s.start(i + 1, tt) <= rest) ++i;
@@ -201,7 +217,7 @@ struct ChunkWalk {
     if (++kvh < a.num_kv_heads) return;
     kvh = 0;
     while (++b < a.num_seqs) {
-      s = chunk_seq(a, b, false);
+      s = chunk_seq(a, b, false, s.whole);
       if (s.n > 0) return;
     }
   }
@@ -240,14 +256,21 @@ struct ChunkLine {
   int parts;
   int64_t mine;    // line before this thread's sequences
   int b0, b1;
+  bool whole;      // the line counts units
 
   __device__ __forceinline__ void measure(const ChunkArgs& a, int64_t* scratch, bool flag) {
     const int nt = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (a.num_seqs + nt - 1) / nt;
     b0 = min(tid * per, a.num_seqs);
     b1 = min(b0 + per, a.num_seqs);
+    whole = a.whole_units == 2;
+    if (a.whole_units == 1) {
+      bool far = false;
+      for (int b = b0; b < b1; ++b) far |= __ldg(a.context_lens + b) > kWholeKeys;
+      whole = !__syncthreads_or(far);
+    }
     int64_t sum = 0;
-    for (int b = b0; b < b1; ++b) sum += chunk_seq(a, b, flag).line * a.num_kv_heads;
+    for (int b = b0; b < b1; ++b) sum += chunk_seq(a, b, flag, whole).line * a.num_kv_heads;
     int64_t scan = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -265,14 +288,15 @@ struct ChunkLine {
     }
     mine = before + scan - sum;
     static_assert((kLeastKeys & (kLeastKeys - 1)) == 0, "a shift");
-    parts = static_cast<int>(max(static_cast<int64_t>(1), min(static_cast<int64_t>(a.grid), total / kLeastKeys)));
+    const int64_t most = whole ? total : total / kLeastKeys;
+    parts = static_cast<int>(max(static_cast<int64_t>(1), min(static_cast<int64_t>(a.grid), most)));
   }
   // The thread whose sequences hold place x of the line stores (sequence, rest).
   __device__ __forceinline__ void find(const ChunkArgs& a, int64_t x, int64_t* found) const {
     if (x < mine) return;
     int64_t at = mine;
     for (int b = b0; b < b1; ++b) {
-      const int64_t l = chunk_seq(a, b, false).line * a.num_kv_heads;
+      const int64_t l = chunk_seq(a, b, false, whole).line * a.num_kv_heads;
       if (x < at + l) {
         if (x >= at) {
           found[0] = b;
@@ -449,6 +473,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int cta = blockIdx.x;
   int64_t at = 0, stop = 0;  // this CTA's part of the line
+  bool whole;
   {
     ChunkLine line;
     line.measure(a, reinterpret_cast<int64_t*>(ring), cta == 0);  // (the ring is not in use yet)
@@ -457,6 +482,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       stop = line_cut(line.total, line.parts, cta + 1);
     }
     if (at < stop) line.find(a, at, s_found);
+    whole = line.whole;
   }
   tc::fence_before_sync();
   fence_proxy_async_smem();  // the scratch in the ring, before its first tile
@@ -489,7 +515,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       walk.at = at;
       walk.stop = stop;
       walk.b = a.num_seqs;
-      if (at < stop) walk.locate(a, static_cast<int>(s_found[0]), s_found[1]);
+      if (at < stop) walk.locate(a, static_cast<int>(s_found[0]), s_found[1], whole);
       uint32_t it = 0;      // tiles issued
       uint32_t steps = 0;   // of the MMA warps before this piece
       uint32_t seen_done = 0, slot_step = 0;  // lane s: the step of the tile in slot s

@@ -217,6 +217,9 @@ int chunk_attention_impl(const void* q, const void* k_cache, const void* v_cache
   a.max_blocks = d->max_blocks_per_seq;
   a.num_blocks = d->num_blocks;
   a.tile_tokens = 128 / a.group;
+  // At most so many units, from the host's view of the lengths.
+  const int64_t units = (static_cast<int64_t>(num_tokens) / (2 * a.tile_tokens) + d->num_seqs) * d->num_kv_heads;
+  a.whole_units = units > a.grid ? 0 : static_cast<int64_t>(a.max_blocks) * pkv::kBlockSize <= pkv::kWholeKeys ? 2 : 1;
   CUtensorMap mq, mk, mv;
   if ((rc = make_query_map(&mq, q, num_tokens, d, a.group)) != PKV_OK) return rc;
   if ((rc = make_block_map(&mk, k_cache, d)) != PKV_OK) return rc;
@@ -229,7 +232,7 @@ int chunk_attention_impl(const void* q, const void* k_cache, const void* v_cache
     e = configure_smem<kern>(pkv::ChunkShape<D>::kSmem);
     if (e == cudaSuccess)
       e = launch_dependent(kern, dim3(a.grid), 1, pkv::kChunkThreads, pkv::ChunkShape<D>::kSmem, stream, mq, mk, mv, a);
-    if (e == cudaSuccess && a.grid > 1)
+    if (e == cudaSuccess && a.grid > 1 && a.whole_units != 2)
       e = launch_dependent(pkv::merge_chunk_kernel<T, D>, dim3(a.grid - 1, pkv::kChunkRows / pkv::kChunkMergeRows), 1,
                            pkv::kChunkMergeThreads, 0, stream, a);
   });

@@ -70,5 +70,6 @@ def tolerance(ref, mag, dtype, q, k, v, scale, keys, weight_bits=None):
 def assert_within(got, ref, tol, what=""):
     assert got.shape == ref.shape
     same = (got == ref) | (np.isnan(got) & np.isnan(ref))           # infinities and NaN where they belong
-    bad = ~same & ~(np.abs(got - ref) <= tol)
+    with np.errstate(invalid="ignore"):                                # (infinity less infinity)
+        bad = ~same & ~(np.abs(got - ref) <= tol)
     assert not bad.any(), (what, int(bad.sum()), got[bad][:3], ref[bad][:3], float(np.nanmax((np.abs(got - ref) / tol)[~same])))

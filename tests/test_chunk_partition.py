@@ -20,16 +20,22 @@ KEYS, UNIT_KEYS, LEAST = constant("kChunkKeys"), constant("kUnitKeys"), constant
 
 
 class Seq:
-    def __init__(self, n, ctx, T):
-        self.n, self.ctx, self.T, self.tt = n, ctx, T, 2 * T
+    def __init__(self, n, ctx, T, whole=False):
+        self.n, self.ctx, self.T, self.tt, self.whole = n, ctx, T, 2 * T, whole
         self.units = -(-n // self.tt)
         self.before = max(ctx - n, 0)
         self.line = self.start(self.units - 1) + self.before + n + UNIT_KEYS if n > 0 else 0
+        if whole:
+            self.line = self.units
 
     def start(self, i):
+        if self.whole:
+            return i
         return i * (self.before + UNIT_KEYS) + self.tt * (i * (i + 1) // 2)
 
     def cost(self, i):
+        if self.whole:
+            return 1
         return min((i + 1) * self.tt, self.n) + self.before + UNIT_KEYS
 
     def tiles(self, i):
@@ -61,7 +67,7 @@ def locate(seqs, heads, x):
             assert steps <= 1
             rest -= kvh * s.line
             p, y = f(s.before + UNIT_KEYS) + f(0.5) * f(s.tt), f(rest)
-            i = int(f(2) * y / (p + np.sqrt(p * p + f(2) * f(s.tt) * y)))
+            i = rest if s.whole else int(f(2) * y / (p + np.sqrt(p * p + f(2) * f(s.tt) * y)))
             i = min(max(i, 0), s.units - 1)
             steps = 0
             while i > 0 and s.start(i) > rest:
@@ -74,11 +80,11 @@ def locate(seqs, heads, x):
     raise AssertionError("past the end of the line")
 
 
-def plan(new, ctx, heads, group, grid):
+def plan(new, ctx, heads, group, grid, whole=False):
     T = 128 // group
-    seqs = [Seq(n, c, T) for n, c in zip(new, ctx)]
+    seqs = [Seq(n, c, T, whole) for n, c in zip(new, ctx)]
     total = sum(s.line * heads for s in seqs)
-    parts = max(1, min(grid, total // LEAST))
+    parts = max(1, min(grid, total if whole else total // LEAST))
     pieces = []                       # (cta, unit, t0, t1, slot)
     for cta in range(parts):
         at, stop = line_cut(total, parts, cta), line_cut(total, parts, cta + 1)
@@ -127,8 +133,8 @@ def merges(grid, pieces):
         yield cuts[c][0], got
 
 
-def check(new, ctx, heads, group, grid):
-    seqs, total, parts, pieces = plan(new, ctx, heads, group, grid)
+def check(new, ctx, heads, group, grid, whole=False):
+    seqs, total, parts, pieces = plan(new, ctx, heads, group, grid, whole)
     done, slots = {}, {}
     for cta, unit, t0, t1, slot in pieces:
         done.setdefault(unit, []).append((t0, t1, slot))
@@ -175,6 +181,23 @@ def test_every_tile_once(group, grid):
             new, before = rng.integers(0, 600, B), -rng.integers(0, 900, B)  # contexts shorter than the chunk
         ctx = np.maximum(new + before, 0)
         check(new.tolist(), ctx.tolist(), int(rng.integers(1, 9)), group, grid)
+
+
+@pytest.mark.parametrize("group", range(1, 9))
+@pytest.mark.parametrize("grid", [1, 7, 152])
+def test_whole_units_are_never_cut(group, grid):
+    """The line of units: no partial results, one unit a CTA where there are enough (more
+    units than CTAs only where the offsets are not what they should be)."""
+    rng = np.random.default_rng(group + grid)
+    for trial in range(20):
+        B = int(rng.integers(1, 9))
+        new = rng.integers(0, 200, B)
+        ctx = np.maximum(new + rng.integers(-100, 800, B), 0)
+        heads = int(rng.integers(1, 9))
+        parts, pieces = check(new.tolist(), ctx.tolist(), heads, group, grid, whole=True)
+        assert all(p[4] == -1 for p in pieces)
+        if len(pieces) <= grid:
+            assert sorted(p[0] for p in pieces) == list(range(len(pieces)))
 
 
 def test_no_work():

@@ -72,6 +72,20 @@ def test_cut_units(dtype, d, hq, hk, new, lens):
     check(out, *a[:4], lens, a[4], d ** -0.5)
 
 
+# (new tokens, contexts) on both sides of the longest context whose units are never cut, and of as many units as CTAs
+@pytest.mark.parametrize("new,lens", [([1, 3, 0, 200], [1024, 1000, 9, 200]), ([1, 3], [1025, 70]), ([1024], [1024]),
+                                      ([600, 1], [1025, 1]), ([1] * 75, [1000] * 74 + [1024]), ([1] * 77, [900] * 77),
+                                      ([1] * 200, list(range(1, 201)))])
+@pytest.mark.parametrize("width", [0, 64, 65, 300])
+def test_units_that_are_not_cut(new, lens, width):
+    """Short contexts in tables that end with them and in wide ones."""
+    d, dtype = (64, "bf16") if width % 2 else (128, "fp16")
+    q, kp, vp, tables, off = inputs(new, lens, 6, 2, d, dtype, seed=width)
+    wide = np.full((len(lens), max(width, tables.shape[1])), -1, np.int32)
+    wide[:, :tables.shape[1]] = tables
+    check(run(q, kp, vp, wide, lens, off, d ** -0.5), q, kp, vp, wide, lens, off, d ** -0.5, (new, lens, width))
+
+
 def test_many_sequences():
     rng = np.random.default_rng(5)
     new = rng.integers(0, 6, 900)
@@ -83,8 +97,9 @@ def test_many_sequences():
 
 @pytest.mark.parametrize("dtype", ["fp16", "bf16"])
 @pytest.mark.parametrize("scale", [0.0, -0.2, 3e-6, 1.7])
-def test_scales(dtype, scale):
-    new, lens = [30, 200], [150, 200]
+@pytest.mark.parametrize("far", [[], [2500]])       # with a long context units are cut
+def test_scales(dtype, scale, far):
+    new, lens = [30, 200] + [2] * len(far), [150, 200] + far
     a = inputs(new, lens, 4, 2, 128, dtype, seed=7, spread=0.5)
     out = run(*a[:4], lens, a[4], scale)
     check(out, *a[:4], lens, a[4], scale)
@@ -106,9 +121,10 @@ def test_references_that_move(dtype, d):
 
 @pytest.mark.parametrize("dtype", ["fp16", "bf16"])
 @pytest.mark.parametrize("d,hq,hk", [(64, 4, 2), (128, 8, 1)])
-def test_values_that_are_not_finite(dtype, d, hq, hk):
+@pytest.mark.parametrize("far", [[], [3000]])       # with a long context units are cut
+def test_values_that_are_not_finite(dtype, d, hq, hk, far):
     """NaN and infinities of later tokens do not reach earlier rows; of visible ones they do."""
-    new, lens = [150, 20], [230, 20]
+    new, lens = [150, 20] + [1] * len(far), [230, 20] + far
     q, kp, vp, tables, off = inputs(new, lens, hq, hk, d, dtype, seed=4)
 
     def put(pool, b, pos, h, dim, value):
@@ -123,10 +139,10 @@ def test_values_that_are_not_finite(dtype, d, hq, hk):
     ref, mag = lc.chunk_attention(f64(q), f64(kp), f64(vp), tables, lens, off, 0.3)
     got = f64(out)
     g = hq // hk
-    assert np.isnan(got[150 + 12:, :g]).all() and np.isnan(ref[150 + 12:, :g]).all()
-    tol = tolerance(np.nan_to_num(ref, posinf=0, neginf=0), mag, q.dtype, f64(q), f64(kp), f64(vp), 0.3, 230)
+    assert np.isnan(got[150 + 12:170, :g]).all() and np.isnan(ref[150 + 12:170, :g]).all()
+    tol = tolerance(np.nan_to_num(ref, posinf=0, neginf=0), mag, q.dtype, f64(q), f64(kp), f64(vp), 0.3, max(lens))
     keep = np.ones_like(ref, bool)
-    keep[150 + 12:, :g] = False
+    keep[150 + 12:170, :g] = False
     if dtype == "fp16":
         # A weight below 2^-25 beside a largest one of 1 rounds to 0 in fp16, and 0 times infinity is NaN:
         # 64 bits keep the weight and give the infinity.
