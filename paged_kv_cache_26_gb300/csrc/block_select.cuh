@@ -19,7 +19,7 @@ namespace pkv {
 
 // ===================================================================== bounds of keys
 
-constexpr int kBoundWarps = 8;
+constexpr int kBoundWarps = 4;
 
 struct BoundArgs {
   const void* k_cache;
@@ -52,10 +52,12 @@ __device__ __forceinline__ int warp_search(int n, int64_t x, int lane, F&& start
 // each, the rows split over the rest of the warp, so a tile is read whole in
 // 4 (D = 64) or 8 loads a lane, all in flight.  Extremes are exact on packed pairs.
 // Bound by the bytes of the tiles where they are many (the blocks of 8 prompts, 18,000
-// tokens, 8 heads, D = 128: 39.5 MB in 8.4 us, 4.7 TB/s with launch and ramp), by the
-// chain offsets, table, tile, result where they are few (61 sequences: 3.4 us).
+// tokens, 8 heads, D = 128: 39.5 MB in 10.0 us, 3.9 TB/s with launch and ramp; 7.8 from
+// L2), by the chain offsets, table, tile, result where they are few (61 sequences: 3.1
+// us).  With eight CTAs asked for on an SM the compiler keeps all eight loads together
+// (without it, or with twelve, 12.4 us; eight warps a CTA 10.3).
 template <typename T, int D>
-__global__ void __launch_bounds__(kBoundWarps * 32) update_bounds_kernel(const BoundArgs a) {
+__global__ void __launch_bounds__(kBoundWarps * 32, 8) update_bounds_kernel(const BoundArgs a) {
   constexpr int kLanes = D / 8;             // lanes of a row
   constexpr int kRows = 32 / kLanes;        // rows of a load: 2 or 4
   constexpr int kLoads = kBlockSize / kRows;

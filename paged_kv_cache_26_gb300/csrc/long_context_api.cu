@@ -94,10 +94,12 @@ int rope_impl(const void* q, const void* k, const void* v, const int32_t* positi
   a.head_vecs = d->head_dim / 8;
   a.freqs = rope->rot_dim / 2;
   a.interleaved = rope->interleaved != 0;
-  // Tokens share the latency of their sines, as long as the CTAs fill the GPU four
-  // times over (1,237 tokens: two a CTA).
-  a.tokens_per_cta = pkv::kRopeTokens;
-  while (a.tokens_per_cta > 1 && num_tokens / a.tokens_per_cta < 4 * device_sms()) a.tokens_per_cta /= 2;
+  // Tokens share the latency of their sines: as few a CTA as make one round of CTAs, four
+  // on an SM, and four where there are more rounds (1,500 tokens, 32 + 8 + 8 heads: three
+  // 9.4 us, two 10.4; 2,000: four 11.4, two 12.7).
+  a.tokens_per_cta = 1;
+  while (a.tokens_per_cta < pkv::kRopeTokens && num_tokens > static_cast<int64_t>(a.tokens_per_cta) * 4 * device_sms())
+    ++a.tokens_per_cta;
   a.row_magic = static_cast<uint32_t>(((int64_t(1) << 32) + rows - 1) / rows);
   a.factor = rope->factor;
   a.axis_bits[0] = rope->axis_bits[0];

@@ -45,7 +45,7 @@ def bound(x, pos, inv, dtype, interleaved, factor, ref):
 @pytest.mark.parametrize("dtype", ["fp16", "bf16"])
 @pytest.mark.parametrize("d,rot", [(64, 64), (64, 16), (128, 128), (128, 32), (128, 112)])
 @pytest.mark.parametrize("tokens,hq,hk,axes,interleaved", [(1, 1, 1, 1, False), (1, 32, 8, 1, True), (3, 5, 5, 2, True),
-                                                           (67, 7, 1, 3, False), (700, 6, 2, 4, True),
+                                                           (67, 7, 1, 3, False), (700, 6, 2, 4, True), (1301, 3, 2, 2, False),
                                                            (5000, 8, 2, 1, False)])
 def test_rows(dtype, d, rot, tokens, hq, hk, axes, interleaved):
     dt = DT[dtype]
@@ -109,7 +109,7 @@ def test_strides_and_in_place(dtype, d):
 
 @pytest.mark.parametrize("dtype", ["fp16", "bf16"])
 @pytest.mark.parametrize("d", [64, 128])
-@pytest.mark.parametrize("tokens", [1, 41, 3000])
+@pytest.mark.parametrize("tokens", [1, 41, 610, 1300, 3000])
 @pytest.mark.parametrize("fp8", [False, True], ids=["16-bit", "e4m3"])
 def test_append_is_rope_then_append(dtype, d, tokens, fp8):
     dt, hq, hk = DT[dtype], 4, 2
