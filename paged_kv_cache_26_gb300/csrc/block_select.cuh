@@ -180,6 +180,7 @@ struct SelectArgs {
 
 constexpr int kScoreThreads = 128;  // of a CTA, a block each; of one that chooses too:
 constexpr int kWholeThreads = 256;
+constexpr int kScoreCtas = 4096;    // CTAs for the ranges of all tables, about
 constexpr int kWholeUnits = 2 * 152;  // two on each SM (64 KB of rows, at most 108 registers)
 
 // Unsigned numbers in the order of the floats (there is no -0 among them); NaN as
@@ -331,7 +332,8 @@ __device__ __forceinline__ void copy_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
-// A CTA scores 128 blocks of one (sequence, KV head) for its G >= group heads, a warp 32.
+// A CTA scores ranges of 128 blocks of one (sequence, KV head) for its G >= group heads, a
+// warp 32 of each.
 // The warp starts the copies of all its rows of bounds (2 D bytes each) at once, 8 KB at
 // D = 128, without a register for them; the query's codes are made while they come.
 // max(4, G) lanes share a row, 16 bytes at a time, upper bounds in its first half; they
@@ -362,11 +364,12 @@ __global__ void __launch_bounds__(kWhole ? kWholeThreads : kScoreThreads) score_
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // The heads of a range side by side, so that their pieces of a block, neighbours in
   // memory, are read at about the same time.
-  const int h = blockIdx.x % a.num_kv_heads, b = blockIdx.y, first = blockIdx.x / a.num_kv_heads * kThreads;
+  const int h = blockIdx.x % a.num_kv_heads, b = blockIdx.y;
+  int first = blockIdx.x / a.num_kv_heads * kThreads;  // of the CTA's blocks
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int block = first + threadIdx.x;             // this lane's
-  int phys = block < a.max_blocks ? __ldg(a.block_tables + static_cast<int64_t>(b) * a.max_blocks + block) : -1;
+  const int32_t* table = a.block_tables + static_cast<int64_t>(b) * a.max_blocks;
+  int phys = first + threadIdx.x < a.max_blocks ? __ldg(table + first + threadIdx.x) : -1;  // this lane's block
   constexpr int kVals = D / 32, kHeads = (G + kWarps - 1) / kWarps;  // values of a lane, heads of a warp
   float x[kHeads][kVals];
 #pragma unroll
@@ -385,25 +388,29 @@ __global__ void __launch_bounds__(kWhole ? kWholeThreads : kScoreThreads) score_
     return;
   }
   if (first >= nb) return;
-  if (block >= nb) {
-    phys = -1;
-  } else if (phys < 0 || phys >= a.num_blocks) {
-    if (h == 0) flag_error(kErrBlockId);
-    phys = -1;
-  }
-  // Without a block: a scale of 0, whatever lies in the row.
-  const float my_step = phys >= 0 ? __ldg(a.scales + static_cast<int64_t>(phys) * a.num_kv_heads + h) : 0.f;
   uint4* rows = s_rows + warp * 32 * kPieces;
   // In odd rows the halves of 64 bytes change places: four lanes a row meet all banks.
   auto place = [](int r, int piece) { return r * kPieces + (piece ^ ((r & 1) << 2)); };
+  float my_step;                                     // the scale of this lane's block
+  auto start_copies = [&]() {
+    if (first + static_cast<int>(threadIdx.x) >= nb) {
+      phys = -1;
+    } else if (phys < 0 || phys >= a.num_blocks) {
+      if (h == 0) flag_error(kErrBlockId);
+      phys = -1;
+    }
+    // Without a block: a scale of 0, whatever lies in the row.
+    my_step = phys >= 0 ? __ldg(a.scales + static_cast<int64_t>(phys) * a.num_kv_heads + h) : 0.f;
 #pragma unroll
-  for (int i = 0; i < kPieces; ++i) {
-    const int r = i * (32 / kPieces) + lane / kPieces, piece = lane % kPieces;
-    const int p = __shfl_sync(0xffffffffu, phys, r);
-    if (p >= 0)
-      copy_async16(smem_u32(rows + place(r, piece)),
-                   a.bounds + (static_cast<int64_t>(p) * a.num_kv_heads + h) * (2 * D) + 16 * piece);
-  }
+    for (int i = 0; i < kPieces; ++i) {
+      const int r = i * (32 / kPieces) + lane / kPieces, piece = lane % kPieces;
+      const int p = __shfl_sync(0xffffffffu, phys, r);
+      if (p >= 0)
+        copy_async16(smem_u32(rows + place(r, piece)),
+                     a.bounds + (static_cast<int64_t>(p) * a.num_kv_heads + h) * (2 * D) + 16 * piece);
+    }
+  };
+  start_copies();
 #pragma unroll
   for (int n = 0; n < kHeads; ++n) {
     const int g = warp + n * kWarps;
@@ -446,54 +453,60 @@ __global__ void __launch_bounds__(kWhole ? kWholeThreads : kScoreThreads) score_
   for (int n = G / 2, o = 1; n > 0; n /= 2, o *= 2)
     if (lane & o) head += n;
   const float head_scale = s_scale[head];
-  uint32_t* keys = kWhole ? s_keys + warp * 32
-                          : a.keys + (static_cast<int64_t>(b) * a.num_kv_heads + h) * a.max_blocks + first + warp * 32;
-  const int mine = nb - first - warp * 32;           // blocks of this warp, or more
-  asm volatile("cp.async.wait_all;" ::: "memory");
-  __syncwarp();
-  if (mine > 0) {
+  uint32_t* keys = kWhole ? s_keys : a.keys + (static_cast<int64_t>(b) * a.num_kv_heads + h) * a.max_blocks;
+  for (;;) {
+    const int mine = nb - first - warp * 32;         // blocks of this warp, or more
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncwarp();
+    if (mine > 0) {
 #pragma unroll
-    for (int r0 = 0; r0 < 32; r0 += kRows) {
-      const int r = r0 + grp;
-      int32_t dot[G];
+      for (int r0 = 0; r0 < 32; r0 += kRows) {
+        const int r = r0 + grp;
+        int32_t dot[G];
 #pragma unroll
-      for (int g = 0; g < G; ++g) dot[g] = 0;
+        for (int g = 0; g < G; ++g) dot[g] = 0;
 #pragma unroll
-      for (int t = 0; t < kTurns; ++t) {
-        const uint4 e = rows[place(r, t * kLanes + sub)];
+        for (int t = 0; t < kTurns; ++t) {
+          const uint4 e = rows[place(r, t * kLanes + sub)];
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
-          dot[g] = __dp4a(code[g][t][0], static_cast<int32_t>(e.x), dot[g]);
-          dot[g] = __dp4a(code[g][t][1], static_cast<int32_t>(e.y), dot[g]);
-          dot[g] = __dp4a(code[g][t][2], static_cast<int32_t>(e.z), dot[g]);
-          dot[g] = __dp4a(code[g][t][3], static_cast<int32_t>(e.w), dot[g]);
-        }
-      }
-      // Exchange halves while there are several sums, then add.
-#pragma unroll
-      for (int o = 1, n = G; o < kLanes; o *= 2, n = n > 1 ? n / 2 : 1) {
-        if (n > 1) {
-          const bool odd = lane & o;
-#pragma unroll
-          for (int g = 0; g < n / 2; ++g) {
-            const int32_t give = odd ? dot[g] : dot[g + n / 2];
-            const int32_t keep = odd ? dot[g + n / 2] : dot[g];
-            dot[g] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+          for (int g = 0; g < G; ++g) {
+            dot[g] = __dp4a(code[g][t][0], static_cast<int32_t>(e.x), dot[g]);
+            dot[g] = __dp4a(code[g][t][1], static_cast<int32_t>(e.y), dot[g]);
+            dot[g] = __dp4a(code[g][t][2], static_cast<int32_t>(e.z), dot[g]);
+            dot[g] = __dp4a(code[g][t][3], static_cast<int32_t>(e.w), dot[g]);
           }
-        } else {
-          dot[0] += __shfl_xor_sync(0xffffffffu, dot[0], o);
         }
-      }
-      // A NaN (0 times an infinite scale) is +infinity, as in ordered_key.
-      // Adding 0 makes a product that underflowed to -0 the equal of +0.
-      const float step = __shfl_sync(0xffffffffu, my_step, r);
-      float score = __fadd_rn(__fmul_rn(__fmul_rn(static_cast<float>(dot[0]), step), head_scale), 0.f);
-      if (head >= a.group) score = -INFINITY;
-      uint32_t key = ordered_key(score);
+        // Exchange halves while there are several sums, then add.
 #pragma unroll
-      for (int m = 1; m < G; m *= 2) key = max(key, __shfl_xor_sync(0xffffffffu, key, m));
-      if (sub == 0 && r < mine) keys[r] = key;
+        for (int o = 1, n = G; o < kLanes; o *= 2, n = n > 1 ? n / 2 : 1) {
+          if (n > 1) {
+            const bool odd = lane & o;
+#pragma unroll
+            for (int g = 0; g < n / 2; ++g) {
+              const int32_t give = odd ? dot[g] : dot[g + n / 2];
+              const int32_t keep = odd ? dot[g + n / 2] : dot[g];
+              dot[g] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+            }
+          } else {
+            dot[0] += __shfl_xor_sync(0xffffffffu, dot[0], o);
+          }
+        }
+        // A NaN (0 times an infinite scale) is +infinity, as in ordered_key.
+        // Adding 0 makes a product that underflowed to -0 the equal of +0.
+        const float step = __shfl_sync(0xffffffffu, my_step, r);
+        float score = __fadd_rn(__fmul_rn(__fmul_rn(static_cast<float>(dot[0]), step), head_scale), 0.f);
+        if (head >= a.group) score = -INFINITY;
+        uint32_t key = ordered_key(score);
+#pragma unroll
+        for (int m = 1; m < G; m *= 2) key = max(key, __shfl_xor_sync(0xffffffffu, key, m));
+        if (sub == 0 && r < mine) keys[first + warp * 32 + r] = key;
+      }
     }
+    first += gridDim.x / a.num_kv_heads * kThreads;
+    if (kWhole || first >= nb) break;
+    __syncwarp();                                    // the rows have been read
+    phys = first + threadIdx.x < a.max_blocks ? __ldg(table + first + threadIdx.x) : -1;
+    start_copies();
   }
   if constexpr (kWhole) {
     __syncthreads();

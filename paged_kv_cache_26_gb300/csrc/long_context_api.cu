@@ -319,9 +319,14 @@ int select_blocks_impl(const pkv::SelectArgs& args, void* workspace, size_t work
   const bool whole = scored && select_whole(d);
   if (scored) {
     const int threads = whole ? pkv::kWholeThreads : pkv::kScoreThreads;
-    const int64_t ctas = static_cast<int64_t>((a.max_blocks + threads - 1) / threads) * d->num_kv_heads;
-    if (ctas > INT32_MAX) return pkv_fail(PKV_ERR_UNSUPPORTED, "select_blocks: too many blocks x KV heads");
-    const dim3 grid(static_cast<unsigned>(ctas), d->num_seqs);
+    // CTAs side by side in a table, each of which takes every so manieth range of blocks:
+    // all ranges, but no more CTAs than kScoreCtas in the grid, as those behind a context's
+    // end cost time (32 sequences of 2,000 blocks in tables of 8,192, 8 KV heads: 40 us of
+    // 16,384 CTAs, 27 of 4,096).
+    const int64_t pairs = static_cast<int64_t>(d->num_kv_heads) * d->num_seqs;
+    const int64_t ranges = std::min<int64_t>((a.max_blocks + threads - 1) / threads,
+                                             std::max<int64_t>(1, pkv::kScoreCtas / pairs));
+    const dim3 grid(static_cast<unsigned>(ranges * d->num_kv_heads), d->num_seqs);
     with_type_and_dim(d, [&](auto t, auto dim) {
       using T = decltype(t);
       constexpr int D = decltype(dim)::value;

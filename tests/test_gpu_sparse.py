@@ -183,6 +183,31 @@ def test_selection_in_one_and_two_launches(dtype, d, hq, hk, seqs):
         assert np.array_equal(got.cpu().numpy(), ref), (num, sink, recent)
 
 
+@pytest.mark.parametrize("seqs,hq,hk,width,num", [(70, 16, 8, 1000, 100), (600, 8, 8, 300, 40), (64, 40, 8, 2500, 64)])
+def test_selection_of_many_long_tables(seqs, hq, hk, width, num):
+    """More ranges of blocks than CTAs."""
+    rng = np.random.default_rng(width)
+    lens = rng.integers(0, width * 16 + 1, seqs)
+    lens[:4] = (width * 16, 0, width * 16 - 15, 130 * 16)
+    nb = 300
+    tables = rng.integers(0, nb, (seqs, width)).astype(np.int32)
+    bounds = np.sort(rng.integers(-127, 128, (nb, hk, 2, 128)).astype(np.int8), axis=2)[:, :, ::-1].copy()
+    scales = rng.random((nb, hk)).astype(np.float32)
+    q = rand((seqs, hq, 128), torch.bfloat16, 6)
+    got = pkv.paged_select_blocks(q.to(DEV), torch.from_numpy(bounds).to(DEV), torch.from_numpy(scales).to(DEV),
+                                  i32(tables), i32(lens), num, 0, 1).cpu().numpy()
+    pkv.paged_kv_check_status()
+    g = hq // hk
+    for b, length in enumerate(lens):
+        n = -(-int(length) // 16)
+        for h in range(hk):
+            score = lc.block_scores(q[b, g * h:g * h + g].float().numpy(), bounds[:, h], scales[:, h])[tables[b, :n]]
+            best = np.lexsort((np.arange(n - 1), -score[:n - 1]))[:num - 1] if n else np.empty(0, int)
+            want = np.full(num, -1)
+            want[:min(n, num)] = np.sort(np.append(best, n - 1))[:n] if n else []
+            assert np.array_equal(got[b, h], want), (b, h)
+
+
 def test_selection_flags_and_buffers():
     lens = [400, 30]
     tables, nb = paged(lens, 0)
