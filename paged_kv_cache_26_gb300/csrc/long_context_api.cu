@@ -319,8 +319,8 @@ int select_blocks_impl(const pkv::SelectArgs& args, void* workspace, size_t work
   const bool whole = scored && select_whole(d);
   if (scored) {
     const int threads = whole ? pkv::kWholeThreads : pkv::kScoreThreads;
-    // CTAs side by side in a table, each of which takes every so manieth range of blocks:
-    // all ranges, but no more CTAs than kScoreCtas in the grid, as those behind a context's
+    // The CTAs of a table take its ranges of blocks in turn, a stride apart: one CTA for
+    // each, but no more than about kScoreCtas in the grid, as those behind a context's
     // end cost time (32 sequences of 2,000 blocks in tables of 8,192, 8 KV heads: 40 us of
     // 16,384 CTAs, 27 of 4,096).  A CTA of several ranges makes its codes once: 128 full tables
     // of 2,048, group of 8, 140 us against 152; with 2,432 CTAs 145, 1,216 148, and where
