@@ -605,7 +605,8 @@ int paged_kv_append_rope(const void* q, const void* k_new, const void* v_new, co
  * context_lens[b] = L counts the new tokens, which sit at positions L - n_b .. L - 1
  *               and are in the cache already (paged_kv_append_rope, paged_kv_append).
  * Row i of sequence b attends to positions [0, L - n_b + i]; a row whose position
- * would be negative (L < n_b) is zero.  Rows before q_offsets[0] and from
+ * would be negative (L < n_b) is zero, one whose visible logits are all -infinity
+ * NaN.  Rows before q_offsets[0] and from
  * q_offsets[num_seqs] on are left as they are.  Products run in T with fp32
  * accumulation; softmax weights (below 2^8 times the largest) are rounded to T for
  * their product with V, their sum is fp32.  Slots past a sequence's length, and for

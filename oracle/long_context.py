@@ -29,7 +29,8 @@ def gather(pool, table, n, kvh):
 def attend(q, k, v, seen, scale):
     """Rows q [n][D] over keys k, v [m][D]; seen [n][m] tells what a row attends to.
     Returns the outputs and the weighted means of |v| (what rounding a weight acts on).
-    A row that sees nothing is zero; values that no row sees do not matter."""
+    A row that sees nothing is zero, one whose logits are all -infinity NaN; values that
+    no row sees do not matter."""
     any_seen = seen.any(0)
     k = np.where(any_seen[:, None], k, 0.0)
     with np.errstate(invalid="ignore"):
@@ -39,7 +40,7 @@ def attend(q, k, v, seen, scale):
     with np.errstate(invalid="ignore"):
         p = np.where(seen, np.exp(s - np.where(np.isneginf(top), 0.0, top)), 0.0)
         total = p.sum(-1, keepdims=True)
-        p = np.divide(p, total, out=np.zeros_like(p), where=total != 0)
+        p = np.divide(p, total, out=np.zeros_like(p), where=seen.any(-1, keepdims=True))
     bad = ~np.isfinite(v) & any_seen[:, None]
     vf = np.where(np.isfinite(v), v, 0.0)
     out, mag = p @ vf, p @ np.abs(vf)

@@ -77,8 +77,8 @@ constexpr int kWholeKeys = 1024;
 // partial result 2 cta) and, `open`, ends inside it too.
 struct ChunkCut {
   int32_t cut, open;
-  int32_t row0, tokens, kvh;  // the unit's
-  int32_t unused[3];
+  int32_t row0, tokens, kvh, first;  // the unit's
+  int32_t unused[2];
 };
 
 struct ChunkArgs {
@@ -331,6 +331,11 @@ __device__ __forceinline__ void sum2(float& x, float& y, float a, float b) {
       : "f"(a), "f"(b));
 }
 
+// What takes the place of 1 / sum in a row without any weight, whose last visible
+// position is `limit`: it sees no key and is zero, or all its logits are -infinity and it
+// is NaN, as softmax is.
+__device__ __forceinline__ float no_weight(int limit) { return limit < 0 ? 0.f : __int_as_float(0x7fffffff); }
+
 // 3-D tiled TMA load (dims, heads, tokens) of a box of queries.
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, int32_t z,
                                             uint32_t bar) {
@@ -528,7 +533,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         if (last) p.b = -1;
         if (first && lane == 0) {
           ChunkCut c = {};
-          if (!last && p.t0 > 0) c = {1, p.t1 < p.tiles(), p.row0, p.tokens, p.kvh};
+          if (!last && p.t0 > 0) c = {1, p.t1 < p.tiles(), p.row0, p.tokens, p.kvh, p.first};
           a.cuts[cta] = c;
         }
         first = false;
@@ -869,7 +874,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         tc::fence_after_sync();
       }
       const int64_t orow = (static_cast<int64_t>(p.row0) + tok) * a.num_q_heads + p.kvh * a.group + r % a.group;
-      const float inv = l == 0.f ? 0.f : 1.0f / l;  // nothing attended to: a zero row (a NaN stays one)
+      const float inv = l == 0.f ? no_weight(limit) : 1.0f / l;  // (a NaN stays one)
       float* part = p.slot >= 0 ? a.part + p.slot * Shape::kPart : nullptr;
       // A lane holds a row, and 32 stores of 16 bytes to 32 rows are 32 accesses.  So the
       // output goes through exchanges within four lanes, after which each has the same
@@ -963,7 +968,7 @@ __global__ void __launch_bounds__(kChunkMergeThreads) merge_chunk_kernel(const C
   auto cut_of = [&](int x) {
     const int4* p = reinterpret_cast<const int4*>(a.cuts + x);
     const int4 u = __ldcg(p), v = __ldcg(p + 1);
-    return ChunkCut{u.x, u.y, u.z, u.w, v.x};
+    return ChunkCut{u.x, u.y, u.z, u.w, v.x, v.y};
   };
   const ChunkCut here = cut_of(c), prev = cut_of(c - 1);
   if (!here.cut || (prev.cut && prev.open)) return;
@@ -985,16 +990,16 @@ __global__ void __launch_bounds__(kChunkMergeThreads) merge_chunk_kernel(const C
     float4 v[kPer];
 #pragma unroll
     for (int k = 0; k < kPer; ++k) v[k] = __ldcg(reinterpret_cast<const float4*>(src) + ((lane >> 2) + 8 * k) * kChunkRows + pr);
-    if (!(m == -INFINITY && l == 0.f)) {  // (tile A may have no keys in the last piece)
-      const float top = fmaxf(M, m);
-      const float wo = M == -INFINITY && L == 0.f ? 0.f : exp2f(M - top), wn = exp2f(m - top);
-      L = L * wo + l * wn;
+    // A piece without any weight: tile A may have no keys in the last one, or their logits
+    // are all -infinity (its O is 0, or NaN by a V that is not finite).
+    const float top = fmaxf(M, m);
+    const float wo = M == -INFINITY && L == 0.f ? 0.f : exp2f(M - top), wn = m == -INFINITY && l == 0.f ? 0.f : exp2f(m - top);
+    L = L * wo + l * wn;
 #pragma unroll
-      for (int k = 0; k < kPer; ++k)
-        o[k] = make_float4(o[k].x * wo + v[k].x * wn, o[k].y * wo + v[k].y * wn, o[k].z * wo + v[k].z * wn,
-                           o[k].w * wo + v[k].w * wn);
-      M = top;
-    }
+    for (int k = 0; k < kPer; ++k)
+      o[k] = make_float4(o[k].x * wo + v[k].x * wn, o[k].y * wo + v[k].y * wn, o[k].z * wo + v[k].z * wn,
+                         o[k].w * wo + v[k].w * wn);
+    M = top;
     if (slot & 1) {
       slot = 2 * c;  // after the first piece, CTA c's
     } else {
@@ -1004,14 +1009,13 @@ __global__ void __launch_bounds__(kChunkMergeThreads) merge_chunk_kernel(const C
     }
   }
   if (rr >= rows) return;
-  const float inv = 1.0f / L;
+  const float inv = L == 0.f ? no_weight(here.first + rr / a.group) : 1.0f / L;
   const int64_t orow = (static_cast<int64_t>(here.row0) + rr / a.group) * a.num_q_heads + here.kvh * a.group + rr % a.group;
   T* dst = static_cast<T*>(a.out) + orow * D + 4 * (lane >> 2);
 #pragma unroll
   for (int k = 0; k < kPer; ++k)
     *reinterpret_cast<uint2*>(dst + 32 * k) =
-        L == 0.f ? make_uint2(0u, 0u)
-                 : make_uint2(pack2<T>(o[k].x * inv, o[k].y * inv), pack2<T>(o[k].z * inv, o[k].w * inv));
+        make_uint2(pack2<T>(o[k].x * inv, o[k].y * inv), pack2<T>(o[k].z * inv, o[k].w * inv));
 }
 
 }  // namespace pkv
