@@ -675,7 +675,7 @@ size_t paged_select_workspace_bytes(const pkv_dims* dims);
  * only: selected int32[num_seqs][Hkv][num_selected], logical blocks in any
  * order; negative entries are passed over, one at or behind ceil(L / 16) too, and
  * flagged (PKV_ERR_OUT_OF_RANGE).  A block listed twice counts twice.  No block: a zero
- * row.  16-bit pools; no workspace. */
+ * row; nothing but logits of -infinity: a row of NaN.  16-bit pools; no workspace. */
 int paged_decode_attention_sparse(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
                                   const int32_t* context_lens, const int32_t* selected, int32_t num_selected, float scale,
                                   void* out, const pkv_dims* dims, void* stream);

@@ -12,6 +12,8 @@
 // rounding of its own, and ties go to the lowest block.
 #pragma once
 
+#include <cfloat>
+
 #include "int4_cache.cuh"
 #include "paged_kv_kernels.cuh"
 
@@ -596,6 +598,9 @@ __global__ void __launch_bounds__(kSparseWarps * 32, 2)
 
   WarpAttn<T, D> at;
   at.reset();
+  // The smallest finite reference, so that logits of -infinity weigh 0 beside others
+  // instead of giving NaN; -infinity is left to partial results without a block.
+  at.m0 = at.m1 = -FLT_MAX;
   at.load_q(static_cast<const T*>(args.q) + (static_cast<int64_t>(b) * args.num_q_heads + kvh * g) * D, g, lane);
 
   // Windows of 32 entries: lane i holds the row and the valid tokens of one.
@@ -655,7 +660,7 @@ __global__ void __launch_bounds__(kSparseWarps * 32, 2)
     for (int e = 0; e < 2; ++e) {
       const int hd = 2 * c + e;
       if (gid == 0) {
-        red_m[warp * kMaxGroup + hd] = e ? at.m1 : at.m0;
+        red_m[warp * kMaxGroup + hd] = used == 0 ? -INFINITY : e ? at.m1 : at.m0;
         red_l[warp * kMaxGroup + hd] = e ? at.l1 : at.l0;
       }
       float* dst = red_o + (warp * kMaxGroup + hd) * D;
@@ -739,7 +744,8 @@ __global__ void __launch_bounds__(kSparseWarps * 32, 2)
       o.w += v.w * wt;
     }
     if (aborted) continue;
-    const float inv = L == 0.f ? 0.f : 1.0f / L;  // no block: a zero row (a NaN stays one)
+    // No block: a zero row; nothing but logits of -infinity: NaN, as softmax is (a NaN stays one).
+    const float inv = L != 0.f ? 1.0f / L : M == -INFINITY ? 0.f : __int_as_float(0x7fffffff);
     uint2 pk;
     pk.x = pack2<T>(o.x * inv, o.y * inv);
     pk.y = pack2<T>(o.z * inv, o.w * inv);

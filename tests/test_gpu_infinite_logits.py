@@ -64,15 +64,43 @@ def test_chunk(dtype, d, hq, hk, case, sign):
 
 
 @pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("d,hq,hk", [(64, 4, 2), (128, 8, 1)])
+@pytest.mark.parametrize("num", [3, 300])           # one CTA; a cluster of them
+def test_sparse(dtype, d, hq, hk, num):
+    """Blocks of nothing but -infinity, a last one of one token among them, alone and beside others."""
+    lens = [33, 33, 16, 4801, 4801, 0]
+    lost = [[32], range(33), range(16), list(range(16, 4000)) + [4800], range(4801), []]
+    q, kp, vp, tables = inputs(len(lens), lens, hq, hk, d, dtype, lost)
+    sel = np.full((len(lens), hk, num), -1, np.int32)
+    rng = np.random.default_rng(num)
+    for b, n in enumerate(lens):
+        some = rng.permutation(-(-n // 16))[:num]
+        sel[b, :, :len(some)] = some
+    sel[3, :, :3] = [300, 5, 0]
+    out = pkv.paged_decode_attention_sparse(q.to(DEV), kp.to(DEV), vp.to(DEV), i32(tables), i32(lens), i32(sel), 0.2)
+    pkv.paged_kv_check_status()
+    ref, mag = lc.sparse_attention(f64(q), f64(kp), f64(vp), tables, lens, sel, 0.2)
+    g = hq // hk
+    for b, nan in enumerate([False, True, True, False, True, False]):
+        assert np.isnan(ref[b, :g]).all() == nan and np.isfinite(ref[b, g:]).all()
+    assert not ref[5].any()
+    bits = 11 if dtype == "fp16" else 16
+    assert_within(f64(out), ref, tolerance(ref, mag, DT[dtype], f64(q), f64(kp), f64(vp), 0.2, 16 * num, bits))
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
 @pytest.mark.parametrize("length", [900, 3000])     # whole; cut between CTAs
 def test_infinite_values_at_weights_of_zero(dtype, length):
     """0 times infinity is NaN, in the piece of a unit that holds no weight as well."""
     q, kp, vp, tables = inputs(40, [length], 4, 2, 128, dtype, [range(800)])
     vp[tables[0, 0], 0, 5, 3] = float("inf")
     vp[tables[0, 40], 0, 7, 6] = float("nan")
-    off = np.array([0, 40])
-    out = pkv.paged_chunk_attention(q.to(DEV), kp.to(DEV), vp.to(DEV), i32(tables), i32([length]), i32(off), 0.2)
+    off, sel = np.array([0, 40]), np.arange(-(-length // 16), dtype=np.int32)[None, None].repeat(2, 1)
+    chunk = pkv.paged_chunk_attention(q.to(DEV), kp.to(DEV), vp.to(DEV), i32(tables), i32([length]), i32(off), 0.2)
+    sparse = pkv.paged_decode_attention_sparse(q[:1].to(DEV), kp.to(DEV), vp.to(DEV), i32(tables), i32([length]), i32(sel), 0.2)
     pkv.paged_kv_check_status()
-    ref, mag = lc.chunk_attention(f64(q), f64(kp), f64(vp), tables, [length], off, 0.2)
-    assert np.isnan(ref[:, :2, [3, 6]]).all() and np.isnan(ref).sum() == ref.shape[0] * 4
-    assert_within(f64(out), ref, tolerance(np.nan_to_num(ref), mag, DT[dtype], f64(q), f64(kp), f64(vp), 0.2, length))
+    for got, (ref, mag), x, bits in (
+            (chunk, lc.chunk_attention(f64(q), f64(kp), f64(vp), tables, [length], off, 0.2), q, None),
+            (sparse, lc.sparse_attention(f64(q[:1]), f64(kp), f64(vp), tables, [length], sel, 0.2), q[:1], 11 if dtype == "fp16" else 16)):
+        assert np.isnan(ref[:, :2, [3, 6]]).all() and np.isnan(ref).sum() == ref.shape[0] * 4
+        assert_within(f64(got), ref, tolerance(np.nan_to_num(ref), mag, DT[dtype], f64(x), f64(kp), f64(vp), 0.2, length, bits))
