@@ -642,8 +642,9 @@ size_t paged_chunk_workspace_bytes(const pkv_dims* dims);
  * Score of block j for KV head x, each query head h of its group having r =
  *   max |q_h| * float32(1/127), c[d] = round_half_even(q_h[d] / r) (0 where r is 0, or
  *   a query value is not finite): max over h of (S * scale) * r, two float32 products
- *   of the whole number S = sum_d max(c[d] upper[d], c[d] lower[d]); a NaN counts as
- *   +infinity.  The score does not depend on how it is computed.
+ *   of the whole number S = sum_d max(c[d] upper[d], c[d] lower[d]); a NaN (0 times an
+ *   infinite scale, or r of a query that is not finite) counts as +infinity.  The score
+ *   does not depend on how it is computed.
  * ---------------------------------------------------------------------- */
 
 /* Makes the bounds of every block that holds one of the new tokens (positions

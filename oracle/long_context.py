@@ -100,8 +100,8 @@ def block_scores(q, bounds, scales):
     best = np.full(len(bounds), -np.inf, np.float32)
     one = np.float32(1) / np.float32(127)
     for row in q:
-        r = np.float32(np.abs(row).max() * one) if np.isfinite(row).all() else np.float32(0)
-        c = np.rint(row / r).astype(np.int64) if r > 0 else np.zeros(q.shape[1], np.int64)
+        r = np.float32(np.abs(row).max() * one)      # an infinity or NaN where the row holds one: its scores are NaN
+        c = np.rint(row / r).astype(np.int64) if r > 0 and np.isfinite(r) else np.zeros(q.shape[1], np.int64)
         e = bounds.astype(np.int64)
         dot = np.maximum(c * e[:, 0], c * e[:, 1]).sum(-1)
         with np.errstate(invalid="ignore"):

@@ -427,10 +427,12 @@ __global__ void __launch_bounds__(kWhole ? kWholeThreads : kScoreThreads) score_
 #pragma unroll
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     finite = __all_sync(0xffffffffu, finite);
-    const float s = finite ? __fmul_rn(top, 1.f / 127.f) : 0.f;
+    // A query that is not finite has no codes and an infinite scale: 0 times that, a NaN,
+    // is a score of +infinity for every block.
+    const float s = finite ? __fmul_rn(top, 1.f / 127.f) : INFINITY;
 #pragma unroll
     for (int i = 0; i < kVals; ++i) {
-      const int c = s > 0.f ? static_cast<int>(rintf(__fdiv_rn(x[n][i], s))) : 0;
+      const int c = finite && s > 0.f ? static_cast<int>(rintf(__fdiv_rn(x[n][i], s))) : 0;
       s_code[g][lane * kVals + i] = static_cast<int8_t>(max(c, 0));
       s_code[g][D + lane * kVals + i] = static_cast<int8_t>(min(c, 0));
     }
@@ -493,7 +495,8 @@ __global__ void __launch_bounds__(kWhole ? kWholeThreads : kScoreThreads) score_
             dot[0] += __shfl_xor_sync(0xffffffffu, dot[0], o);
           }
         }
-        // A NaN (0 times an infinite scale) is +infinity, as in ordered_key.
+        // A NaN (0 times an infinite scale, of the bounds or the query) is +infinity, as in
+        // ordered_key.
         // Adding 0 makes a product that underflowed to -0 the equal of +0.
         const float step = __shfl_sync(0xffffffffu, my_step, r);
         float score = __fadd_rn(__fmul_rn(__fmul_rn(static_cast<float>(dot[0]), step), head_scale), 0.f);
