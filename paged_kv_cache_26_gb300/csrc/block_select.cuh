@@ -612,7 +612,7 @@ __global__ void __launch_bounds__(kSparseWarps * 32, 2)
   for (int base = me; base < num_selected && ok; base += 32 * stride) {
     const int e = base + lane * stride;
     int valid = 0, row = 0;
-    if (e < num_selected && ctx > 0) {
+    if (e < num_selected) {
       const int j = __ldg(list + e);
       if (j >= nblk) flag_error(kErrSelected);
       if (j >= 0 && j < nblk) {

@@ -1,4 +1,5 @@
-"""GPU: queries that are not finite in the selection of blocks."""
+"""GPU: queries that are not finite in the selection of blocks, and lists of empty sequences
+in the attention over them."""
 import numpy as np
 import pytest
 import torch
@@ -41,3 +42,26 @@ def test_queries_that_are_not_finite(dtype, d, hq, hk, width):
         for b in range(3):
             n = -(-lens[b] // 16)
             assert got[b, hk - 1].tolist() == [*range(num - recent), *range(n - recent, n)]
+
+
+def test_lists_of_empty_sequences_are_flagged():
+    """A listed block at or behind the context, of a sequence without tokens too."""
+    lens = [0, 40]
+    tables, nb = paged(lens, 1)
+    kp, vp, q = rand((nb, 2, 16, 64), torch.bfloat16, 1), rand((nb, 2, 16, 64), torch.bfloat16, 2), rand((2, 4, 64), torch.bfloat16, 3)
+
+    def attend(sel, tab=tables):
+        return pkv.paged_decode_attention_sparse(q.to(DEV), kp.to(DEV), vp.to(DEV), i32(tab), i32(lens), i32(sel), 0.125)
+
+    quiet = np.array([[[-1, -1]] * 2, [[0, 2]] * 2])
+    want = attend(quiet)
+    pkv.paged_kv_check_status()
+    assert not want[0].any()
+    for entry in (0, 1, 7, 2 ** 31 - 1):
+        sel = quiet.copy()
+        sel[0, 1, 1] = entry
+        got = attend(sel)
+        with pytest.raises(pkv.PagedKVError) as e:
+            pkv.paged_kv_check_status()
+        assert e.value.code == -6 and torch.equal(got, want)
+        pkv.paged_kv_check_status()
