@@ -445,8 +445,11 @@ int paged_kv_rope_init(pkv_rope* rope, const double* inv_freq, int32_t num_freqs
     const int axis = axes ? axes[f] : 0;
     if (axis < 0 || axis >= num_axes) return pkv_fail(PKV_ERR_INVALID_ARG, "rope_init: an axis is not among num_axes");
     r.axis_bits[f >> 5] |= static_cast<uint64_t>(axis) << (2 * (f & 31));
-    const double turns = inv_freq[f] * 0.15915494309189533577;  // 1 / (2 pi)
-    r.turns[f] = static_cast<uint64_t>(std::ldexp(turns - std::floor(turns), 64));
+    // The fraction of the magnitude, below 1, so that the conversion is defined; a negative
+    // frequency is its negative modulo 2^64.
+    const double turns = std::fabs(inv_freq[f]) * 0.15915494309189533577;  // 1 / (2 pi)
+    const uint64_t fraction = static_cast<uint64_t>(std::ldexp(turns - std::floor(turns), 64));
+    r.turns[f] = inv_freq[f] < 0 ? 0 - fraction : fraction;
   }
   *rope = r;
   return PKV_OK;
