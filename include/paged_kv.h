@@ -575,7 +575,8 @@ typedef struct pkv_rope_strides {
 
 /* Host: fills *rope.  inv_freq: num_freqs = rot_dim / 2 frequencies (radians per
  * position, finite; 8 to 64, a multiple of 8); axes: the axis of each, NULL for axis
- * 0; factor multiplies sines and cosines (1 but for some context extensions). */
+ * 0; factor, within float32, multiplies sines and cosines (1 but for some context
+ * extensions). */
 int paged_kv_rope_init(pkv_rope* rope, const double* inv_freq, int32_t num_freqs, const int32_t* axes, int32_t num_axes,
                        int32_t interleaved, double factor);
 

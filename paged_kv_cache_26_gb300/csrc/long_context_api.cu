@@ -434,7 +434,8 @@ int paged_kv_rope_init(pkv_rope* rope, const double* inv_freq, int32_t num_freqs
   if (num_freqs < 8 || num_freqs > pkv::kMaxFreqs || num_freqs % 8 != 0)
     return pkv_fail(PKV_ERR_INVALID_ARG, "rope_init: 8 to 64 frequencies, a multiple of 8");
   if (num_axes < 1 || num_axes > 4) return pkv_fail(PKV_ERR_INVALID_ARG, "rope_init: 1 to 4 position axes");
-  if (!std::isfinite(factor)) return pkv_fail(PKV_ERR_INVALID_ARG, "rope_init: factor is not finite");
+  if (!(std::fabs(factor) <= std::numeric_limits<float>::max()))
+    return pkv_fail(PKV_ERR_INVALID_ARG, "rope_init: factor is not finite in float32");
   pkv_rope r = {};
   r.rot_dim = 2 * num_freqs;
   r.num_axes = num_axes;

@@ -1,11 +1,13 @@
 """CPU: the frequencies of rotary positions as turns in units of 2^-64: negative ones are the
-negatives, whatever their size."""
+negatives, whatever their size, and factors that no float32 holds are refused."""
 import ctypes
 
 import pytest
 
 from paged_kv_cache_26_gb300 import build as pkv_build
 from paged_kv_cache_26_gb300._native import PkvRope, lib
+
+INVALID = -1
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -29,3 +31,9 @@ def test_negative_frequencies():
         assert down.turns[f] == -up.turns[f] % 2 ** 64, freqs[f]
     # the smallest ones are nothing at all, not half a turn or nearly a whole one beside nothing
     assert up.turns[5] == 0 and up.turns[4] == down.turns[4] == 0 and up.turns[12] == 0
+
+
+@pytest.mark.parametrize("factor,ok", [(1e39, False), (-1e300, False), (3.4e38, True), (-2.0, True), (0.0, True), (1e-50, True),
+                                       (float("inf"), False), (float("nan"), False)])
+def test_factors(factor, ok):
+    assert init([1.0] * 8, factor)[0] == (0 if ok else INVALID)
