@@ -617,7 +617,7 @@ int paged_kv_append_rope(const void* q, const void* k_new, const void* v_new, co
  * workspace (device): paged_chunk_workspace_bytes(dims) bytes, 256-byte aligned;
  * its contents need no initialisation.  Calls that share it must not overlap.
  * Limits: dims as paged_decode_attention; at most 8192 sequences, 2^26 blocks a table
- * and (num_tokens / 32 + num_seqs) (16 max_blocks + num_tokens + 256) Hkv below
+ * and num_seqs (num_tokens / 32 + 1) (16 max_blocks + num_tokens + 256) Hkv at most
  * 4 * 10^18.  Offsets that fall or leave [0, num_tokens] are flagged
  * (PKV_ERR_OUT_OF_RANGE from paged_kv_check_status) and limited.
  * ---------------------------------------------------------------------- */

@@ -198,8 +198,9 @@ int chunk_attention_impl(const void* q, const void* k_cache, const void* v_cache
                                              " bytes needed) or not 256-byte aligned");
   if (d->max_blocks_per_seq > (1 << 26))
     return pkv_fail(PKV_ERR_UNSUPPORTED, "chunk_attention: at most 2^26 blocks a table");
-  // The line of work is counted in 64 bits.
-  const double keys = (num_tokens / 32.0 + d->num_seqs) * (16.0 * d->max_blocks_per_seq + num_tokens + 256.0) * d->num_kv_heads;
+  // The line of work is counted in 64 bits.  (Offsets that fall may give many sequences
+  // all of the rows.)
+  const double keys = d->num_seqs * (num_tokens / 32.0 + 1) * (16.0 * d->max_blocks_per_seq + num_tokens + 256.0) * d->num_kv_heads;
   if (keys > 4e18) return pkv_fail(PKV_ERR_UNSUPPORTED, "chunk_attention: too many tokens, heads and keys");
   pkv::ChunkArgs a = {};
   a.out = out;
