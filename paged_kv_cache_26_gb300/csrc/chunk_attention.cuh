@@ -392,6 +392,7 @@ __device__ __noinline__ void chunk_row_product(uint32_t p, uint32_t o, const uin
 #pragma unroll 1
     for (int t0 = 0; t0 < kChunkKeys; t0 += 64) {
       uint32_t pk[32];
+      __syncwarp();  // (rows of other lengths: the lanes have parted below)
       tc::tmem_ld32(p + t0 / 2, pk);
       tc::tmem_wait_ld();
 #pragma unroll
