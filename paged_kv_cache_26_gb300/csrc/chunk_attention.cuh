@@ -45,6 +45,7 @@
 // the MMA warps included.  Waits give up after kWaitLimitNs.
 #pragma once
 
+#include <cfloat>
 #include <climits>
 
 #include "paged_kv_kernels.cuh"
@@ -72,13 +73,18 @@ constexpr int kLeastKeys = 512;
 // 16.5, 2 of 2,000 26.5 against 17.9.  (About 2 us more where only the GPU knows that they
 // are short.)
 constexpr int kWholeKeys = 1024;
+// A row's reference before its first weight: finite, so that logits of -infinity weigh 0
+// under it as under any other.  It tells rows without any weight apart, in partial results
+// too: one whose visible logits are all -infinity is NaN, as softmax is, one that sees no
+// key zero.
+constexpr float kLeastRef = -FLT_MAX, kNoKeysRef = -3e38f;
 
 // How a CTA's part begins, for the merge: inside a unit (its first piece is then
 // partial result 2 cta) and, `open`, ends inside it too.
 struct ChunkCut {
   int32_t cut, open;
-  int32_t row0, tokens, kvh, first;  // the unit's
-  int32_t unused[2];
+  int32_t row0, tokens, kvh;  // the unit's
+  int32_t unused[3];
 };
 
 struct ChunkArgs {
@@ -331,10 +337,10 @@ __device__ __forceinline__ void sum2(float& x, float& y, float a, float b) {
       : "f"(a), "f"(b));
 }
 
-// What takes the place of 1 / sum in a row without any weight, whose last visible
-// position is `limit`: it sees no key and is zero, or all its logits are -infinity and it
-// is NaN, as softmax is.
-__device__ __forceinline__ float no_weight(int limit) { return limit < 0 ? 0.f : __int_as_float(0x7fffffff); }
+// 1 / l of a row with reference m (a NaN stays one).
+__device__ __forceinline__ float sum_inverse(float m, float l) {
+  return l != 0.f ? 1.0f / l : m == kLeastRef ? __int_as_float(0x7fffffff) : 0.f;
+}
 
 // 3-D tiled TMA load (dims, heads, tokens) of a box of queries.
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, int32_t z,
@@ -534,7 +540,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         if (last) p.b = -1;
         if (first && lane == 0) {
           ChunkCut c = {};
-          if (!last && p.t0 > 0) c = {1, p.t1 < p.tiles(), p.row0, p.tokens, p.kvh, p.first};
+          if (!last && p.t0 > 0) c = {1, p.t1 < p.tiles(), p.row0, p.tokens, p.kvh};
           a.cuts[cta] = c;
         }
         first = false;
@@ -764,7 +770,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       const bool idle = !__any_sync(0xffffffffu, valid_row);
       const int seen = max(p.first + 1, 0);
       const int t0 = p.t0, t1 = p.t1, kt = p.kt[q];
-      float m = -INFINITY, l = 0.f;
+      float m = limit < 0 ? kNoKeysRef : kLeastRef, l = 0.f;
       for (int t = t0; t < t1 && ok; ++t) {
         if (t >= kt) break;  // the other tile's
         ok = mbar_wait(smem_u32(&s_full[q]), ns++ & 1);
@@ -812,7 +818,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         // The first weights are made with the reference there is while the maxima are
         // found, and made again if it has to move: when a score passes it by 2^8.
         l0 = l1 = l2 = l3 = 0.f;
-        float nr = m == -INFINITY ? 0.f : -m;
+        float nr = -m;
         if (t > t0) {
 #pragma unroll
           for (int j = 0; j < kEarly; ++j) weights(j, nr);
@@ -841,7 +847,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           }
           l *= al;
           if (up) m = top;
-          nr = m == -INFINITY ? 0.f : -m;
+          nr = -m;
           l0 = l1 = l2 = l3 = 0.f;
 #pragma unroll
           for (int j = 0; j < kEarly; ++j) weights(j, nr);
@@ -875,7 +881,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         tc::fence_after_sync();
       }
       const int64_t orow = (static_cast<int64_t>(p.row0) + tok) * a.num_q_heads + p.kvh * a.group + r % a.group;
-      const float inv = l == 0.f ? no_weight(limit) : 1.0f / l;  // (a NaN stays one)
+      const float inv = sum_inverse(m, l);
       float* part = p.slot >= 0 ? a.part + p.slot * Shape::kPart : nullptr;
       // A lane holds a row, and 32 stores of 16 bytes to 32 rows are 32 accesses.  So the
       // output goes through exchanges within four lanes, after which each has the same
@@ -969,7 +975,7 @@ __global__ void __launch_bounds__(kChunkMergeThreads) merge_chunk_kernel(const C
   auto cut_of = [&](int x) {
     const int4* p = reinterpret_cast<const int4*>(a.cuts + x);
     const int4 u = __ldcg(p), v = __ldcg(p + 1);
-    return ChunkCut{u.x, u.y, u.z, u.w, v.x, v.y};
+    return ChunkCut{u.x, u.y, u.z, u.w, v.x};
   };
   const ChunkCut here = cut_of(c), prev = cut_of(c - 1);
   if (!here.cut || (prev.cut && prev.open)) return;
@@ -979,7 +985,7 @@ __global__ void __launch_bounds__(kChunkMergeThreads) merge_chunk_kernel(const C
   // Lane: row r0 + lane % 4, dims 4 (lane / 4) + 32 k.
   const int rr = r0 + (lane & 3);
   const int pr = min(rr, rows - 1) < half ? min(rr, rows - 1) : 128 + min(rr, rows - 1) - half;  // its place in a partial result
-  float M = -INFINITY, L = 0.f;
+  float M = kLeastRef, L = 0.f;
   float4 o[kPer];
 #pragma unroll
   for (int k = 0; k < kPer; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -991,10 +997,9 @@ __global__ void __launch_bounds__(kChunkMergeThreads) merge_chunk_kernel(const C
     float4 v[kPer];
 #pragma unroll
     for (int k = 0; k < kPer; ++k) v[k] = __ldcg(reinterpret_cast<const float4*>(src) + ((lane >> 2) + 8 * k) * kChunkRows + pr);
-    // A piece without any weight: tile A may have no keys in the last one, or their logits
-    // are all -infinity (its O is 0, or NaN by a V that is not finite).
-    const float top = fmaxf(M, m);
-    const float wo = M == -INFINITY && L == 0.f ? 0.f : exp2f(M - top), wn = m == -INFINITY && l == 0.f ? 0.f : exp2f(m - top);
+    // (A piece without any weight, kLeastRef, counts 0; its O is 0, or NaN by a V that is not
+    // finite.)
+    const float top = fmaxf(M, m), wo = exp2f(M - top), wn = exp2f(m - top);
     L = L * wo + l * wn;
 #pragma unroll
     for (int k = 0; k < kPer; ++k)
@@ -1010,7 +1015,7 @@ __global__ void __launch_bounds__(kChunkMergeThreads) merge_chunk_kernel(const C
     }
   }
   if (rr >= rows) return;
-  const float inv = L == 0.f ? no_weight(here.first + rr / a.group) : 1.0f / L;
+  const float inv = sum_inverse(M, L);
   const int64_t orow = (static_cast<int64_t>(here.row0) + rr / a.group) * a.num_q_heads + here.kvh * a.group + rr % a.group;
   T* dst = static_cast<T*>(a.out) + orow * D + 4 * (lane >> 2);
 #pragma unroll
