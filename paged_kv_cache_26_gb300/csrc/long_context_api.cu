@@ -5,6 +5,7 @@
 #include "pkv_host.cuh"
 
 #include <algorithm>
+#include <atomic>
 #include <climits>
 #include <cmath>
 #include <limits>
@@ -15,6 +16,18 @@
 #include "rope_append.cuh"
 
 namespace {
+
+// Devices on which this unit has launched a kernel: elsewhere its error word is 0 and
+// paged_kv_check_status need not read it (a copy of its own, 23 us with both against 14).
+// A captured launch counts from its capture on.
+std::atomic<bool> g_launched[kMaxDevices];
+
+template <typename... Params, typename... Args>
+cudaError_t launch(void (*kern)(Params...), dim3 grid, unsigned cluster, unsigned threads, size_t smem,
+                   cudaStream_t stream, Args... args) {
+  g_launched[current_device()].store(true, std::memory_order_relaxed);
+  return launch_dependent(kern, grid, cluster, threads, smem, stream, args...);
+}
 
 // f(T) for the value type of d.
 template <typename F>
@@ -112,7 +125,7 @@ int rope_impl(const void* q, const void* k, const void* v, const int32_t* positi
     auto kern = dst == pkv::kRopeRows     ? pkv::rope_kernel<T, pkv::kRopeRows>
                 : dst == pkv::kRopePool16 ? pkv::rope_kernel<T, pkv::kRopePool16>
                                           : pkv::rope_kernel<T, pkv::kRopePoolE4M3>;
-    e = launch_dependent(kern, dim3(grid), 1, pkv::kRopeThreads, 0, stream, a);
+    e = launch(kern, dim3(grid), 1, pkv::kRopeThreads, 0, stream, a);
   });
   if (e != cudaSuccess) return cuda_fail(e, "rope_kernel launch");
   return PKV_OK;
@@ -234,10 +247,10 @@ int chunk_attention_impl(const void* q, const void* k_cache, const void* v_cache
     constexpr auto kern = pkv::chunk_attention_kernel<T, D>;
     e = configure_smem<kern>(pkv::ChunkShape<D>::kSmem);
     if (e == cudaSuccess)
-      e = launch_dependent(kern, dim3(a.grid), 1, pkv::kChunkThreads, pkv::ChunkShape<D>::kSmem, stream, mq, mk, mv, a);
+      e = launch(kern, dim3(a.grid), 1, pkv::kChunkThreads, pkv::ChunkShape<D>::kSmem, stream, mq, mk, mv, a);
     if (e == cudaSuccess && a.grid > 1 && a.whole_units != 2)
-      e = launch_dependent(pkv::merge_chunk_kernel<T, D>, dim3(a.grid - 1, pkv::kChunkRows / pkv::kChunkMergeRows), 1,
-                           pkv::kChunkMergeThreads, 0, stream, a);
+      e = launch(pkv::merge_chunk_kernel<T, D>, dim3(a.grid - 1, pkv::kChunkRows / pkv::kChunkMergeRows), 1,
+                 pkv::kChunkMergeThreads, 0, stream, a);
   });
   if (e != cudaSuccess) return cuda_fail(e, "chunk_attention_kernel launch");
   return PKV_OK;
@@ -265,8 +278,8 @@ int update_bounds_impl(const void* k_cache, const int32_t* block_tables, const i
   if (grid > INT_MAX) return pkv_fail(PKV_ERR_UNSUPPORTED, "update_bounds: too many blocks");
   cudaError_t e = cudaSuccess;
   with_type_and_dim(d, [&](auto t, auto dim) {
-    e = launch_dependent(pkv::update_bounds_kernel<decltype(t), decltype(dim)::value>, dim3(static_cast<unsigned>(grid)),
-                         1, pkv::kBoundWarps * 32, 0, stream, a);
+    e = launch(pkv::update_bounds_kernel<decltype(t), decltype(dim)::value>, dim3(static_cast<unsigned>(grid)), 1,
+               pkv::kBoundWarps * 32, 0, stream, a);
   });
   if (e != cudaSuccess) return cuda_fail(e, "update_bounds_kernel launch");
   return PKV_OK;
@@ -333,39 +346,39 @@ int select_blocks_impl(const pkv::SelectArgs& args, void* workspace, size_t work
     with_type_and_dim(d, [&](auto t, auto dim) {
       using T = decltype(t);
       constexpr int D = decltype(dim)::value;
-      auto launch = [&](auto group) {
+      auto launch_group = [&](auto group) {
         constexpr int G = decltype(group)::value;
         const int smem = threads * 2 * D;
         if (whole) {
           e = configure_smem<pkv::score_blocks_kernel<T, D, G, true>>(smem);
           if (e == cudaSuccess)
-            e = launch_dependent(pkv::score_blocks_kernel<T, D, G, true>, grid, 1, threads, smem, stream, a);
+            e = launch(pkv::score_blocks_kernel<T, D, G, true>, grid, 1, threads, smem, stream, a);
         } else {
-          e = launch_dependent(pkv::score_blocks_kernel<T, D, G, false>, grid, 1, threads, smem, stream, a);
+          e = launch(pkv::score_blocks_kernel<T, D, G, false>, grid, 1, threads, smem, stream, a);
         }
       };
       if (a.group == 1)
-        launch(std::integral_constant<int, 1>{});
+        launch_group(std::integral_constant<int, 1>{});
       else if (a.group == 2)
-        launch(std::integral_constant<int, 2>{});
+        launch_group(std::integral_constant<int, 2>{});
       else if (a.group <= 4)
-        launch(std::integral_constant<int, 4>{});
+        launch_group(std::integral_constant<int, 4>{});
       else
-        launch(std::integral_constant<int, 8>{});
+        launch_group(std::integral_constant<int, 8>{});
     });
     if (e != cudaSuccess) return cuda_fail(e, "score_blocks_kernel launch");
   }
   if (whole) return PKV_OK;
   const dim3 grid(d->num_kv_heads, d->num_seqs);
   if (!scored || a.max_blocks <= 256 * pkv::kSelectRun) {
-    e = launch_dependent(pkv::select_blocks_kernel<256>, grid, 1, 256, 0, stream, a);
+    e = launch(pkv::select_blocks_kernel<256>, grid, 1, 256, 0, stream, a);
   } else {
     const int most = pkv::select_place(pkv::kSelectCached) * 4 + 4;
     e = configure_smem<pkv::select_blocks_kernel<pkv::kSelectThreads>>(most);
     if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(select_blocks_kernel)");
     const size_t smem = a.max_blocks <= pkv::kSelectThreads * pkv::kSelectRun
                             ? 0 : pkv::select_place(std::min(a.max_blocks, pkv::kSelectCached)) * 4 + 4;
-    e = launch_dependent(pkv::select_blocks_kernel<pkv::kSelectThreads>, grid, 1, pkv::kSelectThreads, smem, stream, a);
+    e = launch(pkv::select_blocks_kernel<pkv::kSelectThreads>, grid, 1, pkv::kSelectThreads, smem, stream, a);
   }
   if (e != cudaSuccess) return cuda_fail(e, "select_blocks_kernel launch");
   return PKV_OK;
@@ -415,9 +428,8 @@ int decode_sparse_impl(const void* q, const void* k_cache, const void* v_cache, 
     constexpr auto kern = pkv::decode_sparse_kernel<decltype(t), D>;
     e = configure_smem<kern>(pkv::SparseShape<D>::kSmem, true);
     if (e == cudaSuccess)
-      e = launch_dependent(kern, dim3(cluster, d->num_kv_heads, d->num_seqs), cluster, pkv::kSparseWarps * 32,
-                           pkv::SparseShape<D>::kSmem, stream, mk, mv, a, selected, num_selected,
-                           static_cast<int32_t>(cluster));
+      e = launch(kern, dim3(cluster, d->num_kv_heads, d->num_seqs), cluster, pkv::kSparseWarps * 32,
+                 pkv::SparseShape<D>::kSmem, stream, mk, mv, a, selected, num_selected, static_cast<int32_t>(cluster));
   });
   if (e != cudaSuccess) return cuda_fail(e, "decode_sparse_kernel launch");
   return PKV_OK;
@@ -425,7 +437,10 @@ int decode_sparse_impl(const void* q, const void* k_cache, const void* v_cache, 
 
 }  // namespace
 
-int pkv_long_context_error_word(unsigned* word) { return take_error_word(word); }
+int pkv_long_context_error_word(unsigned* word) {
+  *word = 0;
+  return g_launched[current_device()].load(std::memory_order_relaxed) ? take_error_word(word) : cudaSuccess;
+}
 
 extern "C" {
 

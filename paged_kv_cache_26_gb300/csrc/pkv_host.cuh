@@ -21,11 +21,16 @@ namespace {
 
 constexpr int kMaxDevices = 64;
 
-int device_sms() {
-  static int sms[kMaxDevices] = {};
+// The current device as an index below kMaxDevices (the last stands for those past it).
+int current_device() {
   int dev = 0;
   cudaGetDevice(&dev);
-  if (dev >= kMaxDevices) dev = kMaxDevices - 1;
+  return dev < kMaxDevices ? dev : kMaxDevices - 1;
+}
+
+int device_sms() {
+  static int sms[kMaxDevices] = {};
+  const int dev = current_device();
   if (sms[dev] == 0) {
     int v = 0;
     cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev);
