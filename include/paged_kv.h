@@ -545,8 +545,9 @@ int paged_kv_resize_tables(int32_t* context_lens, const int32_t* new_lens, int32
  * (i, j) = (f, f + rot_dim/2), or (2f, 2f + 1) when interleaved.  Dims past
  * rot_dim stay as they are.  A token has num_axes positions (1 for text; time,
  * height and width for images and video), and frequency f takes that of axis
- * axes[f].  Positions are int32, negative ones allowed; the angle keeps its
- * precision at any of them (2^-32 of a turn plus the frequency's own 2^-53).
+ * axes[f].  Positions are int32, negative ones allowed.  The angle is off by 2^-26 of a
+ * turn at most (its float32 form), plus the position times 2^-52 of the frequency and
+ * 2^-64 of a turn (the frequency's 64-bit form).
  *
  * pkv_rope is a plain value, made once on the host by paged_kv_rope_init.
  * positions : int32[num_axes][num_tokens] (device)
@@ -609,11 +610,14 @@ int paged_kv_append_rope(const void* q, const void* k_new, const void* v_new, co
  * would be negative (L < n_b) is zero, one whose visible logits are all -infinity
  * NaN.  Rows before q_offsets[0] and from
  * q_offsets[num_seqs] on are left as they are.  Products run in T with fp32
- * accumulation; softmax weights (below 2^8 times the largest) are rounded to T for
- * their product with V, their sum is fp32.  Slots past a sequence's length, and for
- * each row the positions it does not attend to, may hold anything, NaN and
- * infinities too; an infinite V that a row does attend to gives it an infinity, or
- * NaN in fp16 where the weight, below 2^-25, rounds to 0.
+ * accumulation; softmax weights (below 2^8 times the largest) are rounded once to T for
+ * their product with V, their sum is fp32.  (The one-token decode calls hold a bf16
+ * weight as two terms: a single token attended to here is less exact than there, its
+ * error against exact arithmetic about 1.4 times as large.)  Slots past a sequence's
+ * length, and for each row the positions it does not attend to, may hold anything, NaN
+ * and infinities too; an infinite V that a row does attend to gives it an infinity, or
+ * NaN where the weight rounds to 0 (below 2^-25 in fp16, 2^-126 in bf16).  With scale 0 a
+ * logit of -infinity has weight 0.
  * workspace (device): paged_chunk_workspace_bytes(dims) bytes, 256-byte aligned;
  * its contents need no initialisation.  Calls that share it must not overlap.
  * Limits: dims as paged_decode_attention; at most 8192 sequences, 2^26 blocks a table

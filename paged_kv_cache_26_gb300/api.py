@@ -800,7 +800,7 @@ def make_rope(inv_freq: Sequence[float], head_dim: int, axes: Optional[Sequence[
     """Rotary positions of heads of head_dim dims whose first 2 * len(inv_freq) turn:
     frequency f (radians per position) turns dims f and f + len(inv_freq), or 2f and
     2f + 1 when interleaved.  axes: the position axis of every frequency (0 where not
-    given), from 0 to at most 3; factor multiplies sines and cosines."""
+    given), from 0 to at most 3; factor (within float32) multiplies sines and cosines."""
     freqs = [float(x) for x in inv_freq]
     n = len(freqs)
     if 2 * n > head_dim:
@@ -1004,7 +1004,8 @@ def paged_chunk_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
     q_offsets[b + 1] - 1 (int32 [num_seqs + 1] on the device), at positions
     context_lens[b] - n .. context_lens[b] - 1, and already in the caches.  Row i
     attends to positions 0 .. its own.  Rows outside the offsets keep what out
-    holds.  Returns out."""
+    holds.  Softmax weights are rounded once to q's type, where the one-token calls
+    hold bfloat16 ones as two terms and are closer to exact.  Returns out."""
     dev = _context_checks(q, k_cache, v_cache, block_tables, context_lens, None)
     if not (q_offsets.get_device() == dev and q_offsets.dtype is _i32 and q_offsets.is_contiguous() and
             q_offsets.shape == (block_tables.shape[0] + 1,)):
@@ -1067,7 +1068,8 @@ def paged_select_blocks(q: torch.Tensor, bounds: torch.Tensor, bound_scales: tor
     """The logical blocks that a decode step of q [B][Hq][D] should attend to, for
     every (sequence, KV head): the first sink_blocks, the last recent_blocks and
     those whose bounds promise the largest logits, num_selected in all, rising,
-    -1 behind them: int32 [B][Hkv][num_selected]."""
+    -1 behind them: int32 [B][Hkv][num_selected].  Where a head of q holds an
+    infinity or NaN, its group's blocks rank equal."""
     dev, dtype, qs, bs, bt = q.get_device(), q.dtype, q.shape, bounds.shape, block_tables.shape
     if not (dev >= 0 and dtype in _DTYPE_CODE and q.is_contiguous() and len(qs) == 3 and len(bs) == 4 and
             qs[2] == bs[3] and block_tables.get_device() == dev and context_lens.get_device() == dev and

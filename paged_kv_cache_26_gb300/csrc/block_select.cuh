@@ -183,7 +183,9 @@ struct SelectArgs {
 constexpr int kScoreThreads = 128;  // of a CTA, a block each; of one that chooses too:
 constexpr int kWholeThreads = 256;
 constexpr int kScoreCtas = 4096;    // CTAs for the ranges of all tables, about
-constexpr int kWholeUnits = 2 * 152;  // two on each SM (64 KB of rows, at most 108 registers)
+// Two on each SM (64 KB of rows, at most 107 registers).  A number, not the device's SMs, so
+// that the size of the workspace does not depend on which device is current.
+constexpr int kWholeUnits = 2 * 152;
 
 // Unsigned numbers in the order of the floats (there is no -0 among them); NaN as
 // +infinity.

@@ -16,12 +16,14 @@
 // queue it, and a barrier that is ready costs 100 to 200 cycles, which the pipe would
 // spend idle behind a single thread (438 us against 361, at the size below).
 //
-// Bound by the tensor pipe and the exponentials beside it.  2,048 new tokens after
-// 14,000, 32 query and 8 KV heads, bf16: D = 128 315 us (1.60 PFLOP/s of the measured
-// 1.92; the tensor pipe is busy for 75 % of the main kernel's 294 us), D = 64 258 us,
-// where a key costs half the products and the same exponentials.  2,048 tokens after
-// 63,001: 1.51 ms (1.43 PFLOP/s).  A step of 64 single tokens of 2,000 to 4,000 tokens
-// each 134 us: two of a tile's 128 rows hold a token's group, and K and V bound it.
+// Bound by the tensor pipe at D = 128: 2,048 new tokens after 14,000, 32 query and 8 KV
+// heads, bf16, 315 to 326 us (1.55 to 1.60 PFLOP/s of the measured 1.87; the tensor pipe is
+// busy for 75 % of the main kernel, the pipe of the exponentials for 37 %).  D = 64 258 us,
+// where a key costs half the products and the same exponentials: tensor pipe and
+// exponentials 41 % busy each, issue 47 %, so what bounds it is the chain scores,
+// softmax, product, which two tiles do not fill.  2,048 tokens after 63,001: 1.51 to 1.57 ms
+// (1.37 to 1.43 PFLOP/s).  A step of 64 single tokens of 2,000 to 4,000 tokens each 136 us:
+// four of a tile's 128 rows hold a token's group, and K and V bound it.
 //
 // Work is divided by keys, not by units: the units' keys (plus a fixed amount for
 // a unit's start and end) form one line which is cut into equal parts, one per

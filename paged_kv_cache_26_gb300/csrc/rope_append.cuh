@@ -10,18 +10,20 @@
 //
 // Angles.  Only the fraction of a turn matters, and float32 loses it at far
 // positions (position 10^6 at w = 1: a float32 product is good to 0.06 rad).  So a
-// frequency is held as turns per position in units of 2^-64, a 64-bit integer:
-// position * turns modulo 2^64 is the fraction, exact but for the 2^-65 the
-// frequency was rounded by, times the position.  Its upper 32 bits, signed, are
-// half turns in [-1, 1) for sincospif.  Three integer multiplications instead of
-// float64 arithmetic.
+// frequency is held as turns per position in units of 2^-64, a 64-bit integer made by
+// a float64 product (off by 2^-52 of itself and the 2^-64 cut off): position * turns
+// modulo 2^64 is the fraction, off by that times the position and by nothing else.
+// Its upper 32 bits, signed, are half turns in [-1, 1), and as a float32 for sincospif
+// right to 2^-26 of a turn.  Three integer multiplications instead of float64
+// arithmetic.
 //
 // Bound by the bytes of the rows: 16,384 tokens of 32 + 8 + 8 heads, D = 128, bf16 (403
 // MB in and out) take 68 us, 5.9 TB/s.  A CTA takes up to four tokens, makes their sines
 // and cosines once in shared memory (every head shares them), its first rows already
 // on their way, and then treats all rows alike, two 16-byte vectors a thread and step:
 // the eight pairs of eight neighbouring frequencies.  (Eight tokens a CTA 70 us, sixteen
-// 75, the next step's loads ahead of this one's stores 75: fewer threads fit.)
+// 75, the next step's loads ahead of this one's stores 75: fewer threads fit.)  The same
+// tokens into E4M3 pools (369 MB) 70 us, 5.3 TB/s; rows to rows (336 MB) 59 us, 5.7 TB/s.
 #pragma once
 
 #include "paged_kv_kernels.cuh"
